@@ -57,7 +57,8 @@ typedef enum {
   ATTN_ERR_NO_DEVICE = -5,      /* no usable sm_103 device / CUDA runtime error at setup */
   ATTN_ERR_LAUNCH = -6,         /* kernel launch or copy failed (message in attn_last_error) */
   ATTN_ERR_TIMEOUT = -7,        /* a bounded device-side wait ran out (see attn_status_sync) */
-  ATTN_ERR_BAD_ARG = -8         /* scale not finite or not > 0, or another bad scalar */
+  ATTN_ERR_BAD_ARG = -8,        /* scale not finite or not > 0, or another bad scalar */
+  ATTN_ERR_BAD_PAGE = -9        /* a cached position without a page (see attn_cache_check) */
 } attn_status;
 
 /*
@@ -304,6 +305,106 @@ int attn_splitkv_splits(int B, int H, int Nq, int Nk);
 attn_status attn_fwd_splitkv(const void* Q, const void* K, const void* V, void* O, float* LSE, int B, int H, int Nq,
                              int Nk, int d, float scale, int causal, const int32_t* key_padding_lens, int num_splits,
                              void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------------------
+ * Paged key/value cache, and attention over it.
+ * (Additions of this library; the pages treat one sequence whose K and V are at hand.)
+ *
+ * A cache is a pool of pages of page_size tokens: k and v are [num_pages, Hkv, page_size, d],
+ * row-major and contiguous.  A batch's sequences find their pages through a block table,
+ * device int32 [B, max_pages]: position p of sequence b is row p % page_size of page
+ * block_table[b, p / page_size].  Pages may be shared between sequences that only read them.
+ *
+ * Types.  ATTN_CACHE_BF16: rows as they are.  ATTN_CACHE_E4M3: 8-bit codes with one scale per
+ * (token, head) row, k_scale and v_scale uint8 [num_pages, Hkv, page_size]; a value is
+ * code * 2^(s - 127), s in 1 .. 254 (a code of 0 or 255 makes the row 0 or NaN).
+ *
+ * Bad pages.  A block-table entry outside [0, num_pages), or a position at or past
+ * max_pages * page_size, never leads outside the cache: a token without a page is not
+ * written, is read back as zeros, and is left out of the attention as a masked key is.  It is
+ * reported by attn_cache_check.  Positions that no call needs may have any entry.
+ * Lengths (cu_seqlens, start_lens, ctx_lens) are read on the device and clamped to what the
+ * buffers hold, so a captured call follows their contents at every replay.  Make one call on
+ * a device before a stream capture (the first sets up the device).
+ * ------------------------------------------------------------------------------------ */
+
+enum { ATTN_CACHE_BF16 = 0, ATTN_CACHE_E4M3 = 1 };
+
+typedef struct attn_cache {
+  size_t size;        /* sizeof(attn_cache) */
+  void* k;            /* device [num_pages, num_heads, page_size, d], 16-byte aligned */
+  void* v;
+  uint8_t* k_scale;   /* device [num_pages, num_heads, page_size], 16-byte aligned; e4m3 only */
+  uint8_t* v_scale;
+  int type;           /* ATTN_CACHE_* */
+  int num_pages;      /* >= 0 */
+  int page_size;      /* a multiple of 16 */
+  int num_heads;      /* K/V heads */
+  int d;              /* 64 or 128 */
+} attn_cache;
+
+/*
+ * attn_cache_write -- put the new tokens' K and V into the cache.
+ *   K, V  device bf16, `total` packed tokens of num_heads rows: element (t, h, x) of K is at
+ *         K + t * k_strides[0] + h * k_strides[1] + x, so slices of a joint projection need no
+ *         copy.  Host int64[2] strides in elements, multiples of 8.  16-byte aligned.
+ *   cu_seqlens  device int32 [B + 1]: sequence b's tokens are rows cu_seqlens[b] ..
+ *         cu_seqlens[b + 1] - 1; they go to positions start_lens[b], start_lens[b] + 1, ...
+ *         (start_lens: device int32 [B], or NULL for 0; negative counts as 0).  Rows outside
+ *         every sequence are not written.
+ *   The positions written must be distinct rows of the pool (two sequences that write share no
+ *   page there): with the same row named twice, which token it holds, or a mixture, is not
+ *   defined.
+ * e4m3: a row x gets e, the least integer >= -126 with max |x_i| <= 448 * 2^e over its finite
+ * values, s = e + 127 and codes x_i * 2^-e rounded to nearest even: infinities become
+ * +-448 * 2^e, NaN stays NaN.  At e = 120, the largest, magnitudes past 240 * 2^120 become
+ * that (2^128 would be no bf16).  Asynchronous.
+ */
+attn_status attn_cache_write(const attn_cache* cache, const void* K, const void* V, const int64_t* k_strides,
+                             const int64_t* v_strides, const int32_t* block_table, int max_pages,
+                             const int32_t* cu_seqlens, const int32_t* start_lens, int B, int total, void* stream);
+
+/*
+ * attn_cache_read -- cached positions back as packed bf16 K and V [total, num_heads, d] (what
+ *   attn_fwd_varlen takes, e.g. for a prompt over a cached prefix).  Row cu_seqlens[b] + i is
+ *   position start_lens[b] + i of sequence b.  Exact: every e4m3 value times its scale that
+ *   attn_cache_write makes is a bf16.  Rows outside every sequence are left as they were.
+ *   K, V 16-byte aligned.  Asynchronous.
+ */
+attn_status attn_cache_read(const attn_cache* cache, void* K, void* V, const int32_t* block_table, int max_pages,
+                            const int32_t* cu_seqlens, const int32_t* start_lens, int B, int total, void* stream);
+
+/*
+ * attn_fwd_tree -- attention of each sequence's new (drafted) tokens over its cache.
+ *   Sequence b has ctx_lens[b] cached tokens (device int32 [B], NULL: 0) and the T_b tokens of
+ *   rows cu_seqlens_q[b] .. cu_seqlens_q[b + 1] - 1 of Q, whose K and V are already in the
+ *   cache at positions ctx_lens[b] .. ctx_lens[b] + T_b - 1.  T_b = 1 is plain decoding.
+ *   Q, O  device bf16 [total_q, Hq, d], LSE fp32 [Hq, total_q].  Hq is a multiple of the
+ *         cache's heads: query head h reads K/V head h / (Hq / num_heads).
+ *   tree_mask  device int64 [total_q] or NULL.  Token i of a sequence sees every context key,
+ *         and its token u when bit u of tree_mask[row of i] is set (bits from T_b on are
+ *         ignored; a token sees itself only if its own bit is set).  NULL: a chain, u <= i.
+ *         A row that sees nothing gets O = 0 and LSE = -inf.  What K and V hold where a row
+ *         does not look, infinities and NaN among it, does not reach the row.
+ *   max_seqlen_q  in [0, 64], >= the most tokens of a sequence (rows past it are left as they
+ *         were, as are rows of Q outside every sequence).
+ *   workspace  device, attn_tree_workspace_bytes(...) bytes, 16-byte aligned, this call's own
+ *         until it has finished: calls that may run at the same time (other streams, graphs)
+ *         each need one.  Its contents mean nothing between calls.
+ *   Asynchronous, allocates nothing.  Errors: as attn_fwd, plus ATTN_ERR_BAD_SHAPE for
+ *   max_seqlen_q > 64 or Hq not a multiple, ATTN_ERR_BAD_ARG for a small workspace.
+ */
+attn_status attn_fwd_tree(const void* Q, const attn_cache* cache, void* O, float* LSE, const int32_t* block_table,
+                          int max_pages, const int32_t* cu_seqlens_q, const int32_t* ctx_lens,
+                          const int64_t* tree_mask, int B, int Hq, int max_seqlen_q, int total_q, float scale,
+                          void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace attn_fwd_tree needs (0 for invalid arguments). */
+size_t attn_tree_workspace_bytes(int Hq, int Hkv, int max_seqlen_q, int d);
+
+/* attn_status_sync, then ATTN_ERR_BAD_PAGE if a cache call on the current device has met a
+ * position without a page since the last check (read and cleared with plain copies). */
+attn_status attn_cache_check(void* stream);
 
 #ifdef __cplusplus
 }

@@ -16,11 +16,12 @@ LIB_PATH = os.path.join(_HERE, "libattn.so")
 
 EXPORTS = ("attn_fwd", "attn_fwd_ex", "attn_fwd_strided", "attn_fwd_varlen", "attn_fwd_host", "attn_release_workspace", "attn_status_sync", "attn_last_error",
            "attn_version", "attn_fwd_noalloc", "attn_fwd_states", "attn_merge_states",
-           "attn_splitkv_workspace_bytes", "attn_splitkv_splits", "attn_fwd_splitkv")
+           "attn_splitkv_workspace_bytes", "attn_splitkv_splits", "attn_fwd_splitkv",
+           "attn_cache_write", "attn_cache_read", "attn_cache_check", "attn_fwd_tree", "attn_tree_workspace_bytes")
 
 STATUS_NAMES = {0: "ATTN_OK", -1: "ATTN_ERR_NULLPTR", -2: "ATTN_ERR_BAD_SHAPE", -3: "ATTN_ERR_UNSUPPORTED_D",
                 -4: "ATTN_ERR_MISALIGNED", -5: "ATTN_ERR_NO_DEVICE", -6: "ATTN_ERR_LAUNCH", -7: "ATTN_ERR_TIMEOUT",
-                -8: "ATTN_ERR_BAD_ARG"}
+                -8: "ATTN_ERR_BAD_ARG", -9: "ATTN_ERR_BAD_PAGE"}
 
 
 EXP2_DEFAULT, EXP2_HARDWARE, EXP2_MIXED = 0, 1, 2
@@ -30,6 +31,17 @@ class AttnOptions(ctypes.Structure):
     """attn_options of include/attn.h."""
     _fields_ = [("size", ctypes.c_size_t), ("rescale_threshold", ctypes.c_float), ("exp2_mode", ctypes.c_int),
                 ("key_block", ctypes.c_int)]
+
+
+CACHE_BF16, CACHE_E4M3 = 0, 1
+
+
+class AttnCache(ctypes.Structure):
+    """attn_cache of include/attn.h."""
+    _fields_ = [("size", ctypes.c_size_t), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p), ("type", ctypes.c_int),
+                ("num_pages", ctypes.c_int), ("page_size", ctypes.c_int), ("num_heads", ctypes.c_int),
+                ("d", ctypes.c_int)]
 
 
 class AttnError(RuntimeError):
@@ -78,6 +90,17 @@ def load_library():
         lib.attn_splitkv_splits.restype = i
         lib.attn_fwd_splitkv.argtypes = [vp, vp, vp, vp, vp, i, i, i, i, i, f, i, vp, i, vp, ctypes.c_size_t, vp]
         lib.attn_fwd_splitkv.restype = i
+        cache = ctypes.POINTER(AttnCache)
+        lib.attn_cache_write.argtypes = [cache, vp, vp, i64p, i64p, vp, i, vp, vp, i, i, vp]
+        lib.attn_cache_write.restype = i
+        lib.attn_cache_read.argtypes = [cache, vp, vp, vp, i, vp, vp, i, i, vp]
+        lib.attn_cache_read.restype = i
+        lib.attn_cache_check.argtypes = [vp]
+        lib.attn_cache_check.restype = i
+        lib.attn_fwd_tree.argtypes = [vp, cache, vp, vp, vp, i, vp, vp, vp, i, i, i, i, f, vp, ctypes.c_size_t, vp]
+        lib.attn_fwd_tree.restype = i
+        lib.attn_tree_workspace_bytes.argtypes = [i, i, i, i]
+        lib.attn_tree_workspace_bytes.restype = ctypes.c_size_t
         _lib = lib
     return _lib
 
@@ -342,6 +365,186 @@ def attn_fwd_varlen(Q, K, V, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, O=None, L
                                         total_q, total_k, d, float(scale), int(causal), _stream_handle(stream))
     _check(rc)
     return O, LSE
+
+
+# --- paged cache, and attention over it ------------------------------------------
+
+def _cache_args(k_cache, v_cache, k_scale, v_scale):
+    """The attn_cache of these tensors (every check of their shapes, types and placement)."""
+    import torch
+    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
+        raise ValueError("k_cache and v_cache must be [num_pages, Hkv, page_size, d] of one type")
+    dev = k_cache.device
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        if not t.is_cuda or not t.is_contiguous() or t.device != dev:
+            raise ValueError(f"{name} must be a contiguous CUDA tensor on the cache's device")
+    P, H, page, d = k_cache.shape
+    if k_cache.dtype == torch.bfloat16:
+        if k_scale is not None or v_scale is not None:
+            raise ValueError("a bf16 cache takes no k_scale / v_scale")
+        return AttnCache(ctypes.sizeof(AttnCache), k_cache.data_ptr(), v_cache.data_ptr(), None, None, CACHE_BF16, P,
+                         page, H, d)
+    if k_cache.dtype != torch.float8_e4m3fn:
+        raise ValueError("the cache must be bf16 or float8_e4m3fn")
+    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+        if t is None or t.dtype != torch.uint8 or t.device != dev or t.shape != (P, H, page) or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous uint8 CUDA tensor [num_pages, Hkv, page_size]")
+    return AttnCache(ctypes.sizeof(AttnCache), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+                     v_scale.data_ptr(), CACHE_E4M3, P, page, H, d)
+
+
+def _batch_args(dev, block_table, cu_seqlens, cu_name, lens, lens_name):
+    """Checks the int32 arrays of a batch; returns (B, max_pages, lens_ptr)."""
+    import torch
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [B, max_pages]")
+    B, max_pages = block_table.shape
+    for name, t, n in (("block_table", block_table, None), (cu_name, cu_seqlens, B + 1), (lens_name, lens, B)):
+        if t is None:
+            continue
+        if t.dtype != torch.int32 or t.device != dev or not t.is_contiguous() or (n is not None and t.numel() != n):
+            raise ValueError(f"{name} must be a contiguous int32 tensor on the cache's device"
+                             + ("" if n is None else f" with {n} elements"))
+    return B, max_pages, None if lens is None else lens.data_ptr()
+
+
+class _On:
+    """The device of a call's tensors made current, and its stream for what is allocated."""
+
+    def __init__(self, dev, stream):
+        import torch
+        self.contexts = []
+        if torch.cuda.current_device() != dev.index:
+            self.contexts.append(torch.cuda.device(dev))
+        if stream is not None:  # buffers made here belong to the stream that uses them
+            if stream.device != dev:
+                raise ValueError("stream is on another device than the tensors")
+            self.contexts.append(torch.cuda.stream(stream))
+
+    def __enter__(self):
+        for c in self.contexts:
+            c.__enter__()
+
+    def __exit__(self, *exc):
+        for c in reversed(self.contexts):
+            c.__exit__(*exc)
+
+
+def attn_cache_write(K, V, k_cache, v_cache, block_table, cu_seqlens, *, start_lens=None, k_scale=None, v_scale=None,
+                     stream=None):
+    """Put packed new tokens into a paged cache, in place.
+
+    K, V [total, Hkv, d]: bf16 CUDA tensors with a contiguous last dimension (views of a joint
+    projection need no copy).  k_cache, v_cache [num_pages, Hkv, page_size, d]: bf16 or
+    float8_e4m3fn; an e4m3 cache comes with k_scale and v_scale, uint8 [num_pages, Hkv,
+    page_size] (value = code * 2^(s - 127)).  block_table int32 [B, max_pages]; cu_seqlens
+    int32 [B + 1]: sequence b's tokens are rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1 and go to
+    positions start_lens[b], ... (int32 [B]; None: 0).  Tokens without a page are left out and
+    reported by cache_check().
+    """
+    import torch
+    cache = _cache_args(k_cache, v_cache, k_scale, v_scale)
+    dev = k_cache.device
+    for name, t in (("K", K), ("V", V)):
+        if (t.dim() != 3 or t.dtype != torch.bfloat16 or t.device != dev or t.shape[1] != cache.num_heads
+                or t.shape[2] != cache.d or t.stride(2) != 1):
+            raise ValueError(f"{name} must be a bf16 tensor [total, Hkv, d] on the cache's device with a contiguous "
+                             "last dimension")
+    if V.shape[0] != K.shape[0]:
+        raise ValueError("K and V must have the same number of tokens")
+    B, max_pages, start_ptr = _batch_args(dev, block_table, cu_seqlens, "cu_seqlens", start_lens, "start_lens")
+    strides = ctypes.c_int64 * 2
+    with _On(dev, stream):
+        _check(load_library().attn_cache_write(ctypes.byref(cache), K.data_ptr(), V.data_ptr(),
+                                               strides(K.stride(0), K.stride(1)), strides(V.stride(0), V.stride(1)),
+                                               block_table.data_ptr(), max_pages, cu_seqlens.data_ptr(), start_ptr, B,
+                                               K.shape[0], _stream_handle(stream)))
+
+
+def attn_cache_read(k_cache, v_cache, block_table, cu_seqlens, total, K=None, V=None, *, start_lens=None, k_scale=None,
+                    v_scale=None, stream=None):
+    """Cached positions as packed bf16 K, V [total, Hkv, d] (allocated when not given), the
+    layout attn_fwd_varlen takes.  Row cu_seqlens[b] + i is position start_lens[b] + i of
+    sequence b; rows outside every sequence are left as they were, positions without a page are
+    zeros and reported by cache_check().  The cache's arguments: as attn_cache_write."""
+    import torch
+    cache = _cache_args(k_cache, v_cache, k_scale, v_scale)
+    dev = k_cache.device
+    B, max_pages, start_ptr = _batch_args(dev, block_table, cu_seqlens, "cu_seqlens", start_lens, "start_lens")
+    shape = (int(total), cache.num_heads, cache.d)
+    with _On(dev, stream):
+        if K is None:
+            K = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        if V is None:
+            V = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        for name, t in (("K", K), ("V", V)):
+            if t.shape != shape or t.dtype != torch.bfloat16 or t.device != dev or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous bf16 tensor [total, Hkv, d] on the cache's device")
+        _check(load_library().attn_cache_read(ctypes.byref(cache), K.data_ptr(), V.data_ptr(), block_table.data_ptr(),
+                                              max_pages, cu_seqlens.data_ptr(), start_ptr, B, shape[0],
+                                              _stream_handle(stream)))
+    return K, V
+
+
+def tree_workspace_bytes(Hq, Hkv, max_seqlen_q, d) -> int:
+    """Bytes of workspace attn_fwd_tree needs (0 for invalid arguments)."""
+    return load_library().attn_tree_workspace_bytes(Hq, Hkv, max_seqlen_q, d)
+
+
+def attn_fwd_tree(Q, k_cache, v_cache, block_table, ctx_lens, cu_seqlens_q, max_seqlen_q, O=None, LSE=None, *,
+                  tree_mask=None, k_scale=None, v_scale=None, scale=None, workspace=None, stream=None):
+    """Attention of each sequence's new (drafted) tokens over its paged cache.
+
+    Q [total_q, Hq, d]: contiguous bf16 CUDA tensor, sequence b's tokens at rows
+    cu_seqlens_q[b] .. cu_seqlens_q[b + 1] - 1 (int32 [B + 1]), at most max_seqlen_q <= 64 of
+    them; their K and V are already cached at positions ctx_lens[b], ... (int32 [B]; None: 0).
+    Hq is a multiple of the cache's heads.  tree_mask int64 [total_q]: bit u of a token's word
+    lets it see token u of its sequence (None: a chain, u <= i); every token sees the context.
+    One token per sequence is plain decoding.  Returns O [total_q, Hq, d] and LSE [Hq, total_q]
+    (allocated when not given).  workspace: a CUDA uint8 tensor of tree_workspace_bytes(...)
+    that no other call in flight uses, allocated here when not given.  The cache's arguments: as
+    attn_cache_write.
+    """
+    import torch
+    cache = _cache_args(k_cache, v_cache, k_scale, v_scale)
+    dev = k_cache.device
+    if Q.dim() != 3 or Q.dtype != torch.bfloat16 or Q.device != dev or not Q.is_contiguous() or Q.shape[2] != cache.d:
+        raise ValueError("Q must be a contiguous bf16 tensor [total_q, Hq, d] on the cache's device")
+    total_q, Hq, d = Q.shape
+    B, max_pages, ctx_ptr = _batch_args(dev, block_table, cu_seqlens_q, "cu_seqlens_q", ctx_lens, "ctx_lens")
+    mask_ptr = None
+    if tree_mask is not None:
+        if (tree_mask.dtype != torch.int64 or tree_mask.device != dev or tree_mask.numel() != total_q
+                or not tree_mask.is_contiguous()):
+            raise ValueError("tree_mask must be a contiguous int64 tensor [total_q] on the cache's device")
+        mask_ptr = tree_mask.data_ptr()
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    lib = load_library()
+    with _On(dev, stream):
+        if O is None:
+            O = torch.empty_like(Q)
+        if LSE is None:
+            LSE = torch.empty((Hq, total_q), dtype=torch.float32, device=dev)
+        if O.shape != Q.shape or O.dtype != torch.bfloat16 or O.device != dev or not O.is_contiguous():
+            raise ValueError("O must be a contiguous bf16 tensor shaped like Q")
+        if LSE.shape != (Hq, total_q) or LSE.dtype != torch.float32 or LSE.device != dev or not LSE.is_contiguous():
+            raise ValueError("LSE must be a contiguous fp32 tensor [Hq, total_q]")
+        if workspace is None:
+            need = lib.attn_tree_workspace_bytes(Hq, cache.num_heads, int(max_seqlen_q), d)
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        elif workspace.device != dev or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on the cache's device")
+        _check(lib.attn_fwd_tree(Q.data_ptr(), ctypes.byref(cache), O.data_ptr(), LSE.data_ptr(),
+                                 block_table.data_ptr(), max_pages, cu_seqlens_q.data_ptr(), ctx_ptr, mask_ptr, B, Hq,
+                                 int(max_seqlen_q), total_q, float(scale), workspace.data_ptr(),
+                                 workspace.numel() * workspace.element_size(), _stream_handle(stream)))
+    return O, LSE
+
+
+def cache_check(stream=None):
+    """Synchronise the stream; AttnError if a wait ran out or a cache call met a position without a page."""
+    _check(load_library().attn_cache_check(_stream_handle(stream)))
 
 
 # --- the CPU library (libattn_cpu.so, include/attn_cpu.h) ------------------------

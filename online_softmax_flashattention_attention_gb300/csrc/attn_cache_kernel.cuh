@@ -1,0 +1,280 @@
+// The paged key/value cache: writing packed new tokens into it and reading cached positions
+// back, sm_103a.
+//
+// Cache: k, v [num_pages, Hkv, page, d], bf16 or e4m3; e4m3 rows carry one scale code each,
+// uint8 [num_pages, Hkv, page], value = code * 2^(s - 127).  Position p of sequence b is row
+// p % page of page block_table[b, p / page].
+//
+// Quantisation of a row x: a = max |x_i| over its finite values, e the least integer >= -126
+// with a <= 448 * 2^e (448: the largest e4m3 value), s = e + 127, code_i = x_i * 2^-e to the
+// nearest e4m3 value, ties to even; infinities become +-448, NaN stays NaN.  With a power of
+// two for a scale both x * 2^-e and code * 2^e are exact, so the one rounding to e4m3 (half a
+// step: relative 2^-4, or 2^-10 * 2^e where the code is subnormal) is all that is lost, and a
+// value read back is exactly a bf16.  (At e = 120, the largest there is, magnitudes past
+// 240 * 2^120 are brought back to it: the next value up, 2^128, is no bf16.)  One byte a row is
+// 1/128 of the codes at d = 128.
+//
+// Both kernels only move bytes.  d / 8 lanes own one (token, head) row of K and of V: one
+// 16-byte bf16 access a lane, and for the row maximum a few shuffles.  A thread has the loads
+// of kCacheUnroll rows of K and V in flight; in the write they do not depend on where the
+// rows go, so they are issued before the sequence of a token is searched for.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "ptx.cuh"
+
+namespace attn {
+
+constexpr int kCacheThreads = 256;
+constexpr int kCacheUnroll = 4;  // rows of K and of V a lane group has in flight
+
+// What the entry points say about a cache and its block table.
+struct CacheParams {
+  void* k;                  // [num_pages, Hkv, page, d]
+  void* v;
+  uint8_t* ks;              // [num_pages, Hkv, page], e4m3 only
+  uint8_t* vs;
+  const int32_t* table;     // [B, max_pages]
+  const int32_t* cu;        // [B + 1] packed rows of the sequences
+  const int32_t* start;     // [B] first position of each sequence's rows, or null (0)
+  int B, Hkv, num_pages, page, max_pages;
+  int total;                // packed rows
+  const __nv_bfloat16* src_k;  // write: packed K and V, element (t, h, x) at t * st + h * sh + x
+  const __nv_bfloat16* src_v;
+  long long k_st, k_sh, v_st, v_sh;
+  __nv_bfloat16* dst_k;     // read: [total, Hkv, d]
+  __nv_bfloat16* dst_v;
+  uint32_t* page_word;      // bit 0: a position without a page, or a page outside the cache
+};
+
+// Row (of head 0) of packed token `tok` in the cache, in units of rows: page * Hkv * page_size
+// + row in the page; -1 when the token is in no sequence, -2 when its position has no page.
+// The sequence is the last one that starts at or before the token; a block table or a
+// cu_seqlens that holds anything at all leads to a row inside the cache or to none.
+__device__ __forceinline__ long long cache_row_of(const CacheParams& p, int tok) {
+  int lo = 0, hi = p.B;  // the sequence is in [lo, hi)
+  while (hi - lo > 1) {
+    const int mid = lo + (hi - lo) / 2;
+    if (__ldg(p.cu + mid) <= tok)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  const int first = max(__ldg(p.cu + lo), 0);
+  if (tok < first || tok >= __ldg(p.cu + lo + 1)) return -1;
+  const int start = p.start ? max(__ldg(p.start + lo), 0) : 0;
+  const long long pos = static_cast<long long>(start) + (tok - first);
+  const long long slot = pos / p.page;
+  if (slot >= p.max_pages) return -2;
+  const int pg = __ldg(p.table + static_cast<long long>(lo) * p.max_pages + slot);
+  if (static_cast<unsigned>(pg) >= static_cast<unsigned>(p.num_pages)) return -2;
+  return static_cast<long long>(pg) * p.Hkv * p.page + (pos - slot * p.page);
+}
+
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// Two floats to two e4m3 codes (low byte: the first), nearest even, +-448 past the range.
+__device__ __forceinline__ uint32_t pack_e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Two e4m3 codes to f16x2, exact.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t codes) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(codes)));
+  return r;
+}
+
+__device__ __forceinline__ float2 e4m3x2_to_f32(uint32_t codes) {
+  const uint32_t h = e4m3x2_to_f16x2(codes);
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
+// 2^(s - 127) for scale codes 1 .. 254.
+__device__ __forceinline__ float scale_of(uint32_t s) { return __uint_as_float(s << 23); }
+
+// Largest finite |x| of eight bf16 as its bits (they order as the values do).
+__device__ __forceinline__ uint32_t finite_max(const uint4& x) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t w = (&x.x)[i] & 0x7fff7fffu;
+    const uint32_t a = w & 0xffffu, b = w >> 16;
+    m = max(m, a < 0x7f80u ? a : 0u);
+    m = max(m, b < 0x7f80u ? b : 0u);
+  }
+  return m;
+}
+
+// Scale code of a row whose largest finite |x| has these bf16 bits: with a = (1 + mm / 128) *
+// 2^(ef - 127) and 448 = 1.75 * 2^8, e is ef - 135 while 1 + mm / 128 <= 1.75, else one more.
+__device__ __forceinline__ uint32_t scale_code(uint32_t bits) {
+  const int ef = static_cast<int>(bits >> 7), mm = static_cast<int>(bits & 127u);
+  const int s = ef - 8 + (mm > 96 ? 1 : 0);
+  return static_cast<uint32_t>(max(s, 1));  // zero and subnormal rows: 2^-126
+}
+
+constexpr uint32_t kTopScale = 247;  // e = 120
+
+// Magnitudes of two bf16 to at most 240 * 2^120 (bits 0x7f70), infinities too, NaN as it is.
+__device__ __forceinline__ uint32_t under_top(uint32_t w) {
+  const uint32_t a = w & 0x7fffu, b = (w >> 16) & 0x7fffu;
+  if (a > 0x7f70u && a <= 0x7f80u) w = (w & 0xffff8000u) | 0x7f70u;
+  if (b > 0x7f70u && b <= 0x7f80u) w = (w & 0x8000ffffu) | 0x7f700000u;
+  return w;
+}
+
+__device__ __forceinline__ uint2 quantise8(uint4 x, uint32_t s) {
+  if (s == kTopScale) x = make_uint4(under_top(x.x), under_top(x.y), under_top(x.z), under_top(x.w));
+  const float inv = scale_of(254u - s);
+  uint2 r;
+  r.x = pack_e4m3x2(bf16_lo(x.x) * inv, bf16_hi(x.x) * inv) | (pack_e4m3x2(bf16_lo(x.y) * inv, bf16_hi(x.y) * inv) << 16);
+  r.y = pack_e4m3x2(bf16_lo(x.z) * inv, bf16_hi(x.z) * inv) | (pack_e4m3x2(bf16_lo(x.w) * inv, bf16_hi(x.w) * inv) << 16);
+  return r;
+}
+
+__device__ __forceinline__ uint4 dequantise8(const uint2& c, float scale) {
+  uint4 r;
+  const float2 a = e4m3x2_to_f32(c.x & 0xffffu), b = e4m3x2_to_f32(c.x >> 16);
+  const float2 d = e4m3x2_to_f32(c.y & 0xffffu), e = e4m3x2_to_f32(c.y >> 16);
+  r.x = pack_bf16x2(a.x * scale, a.y * scale);
+  r.y = pack_bf16x2(b.x * scale, b.y * scale);
+  r.z = pack_bf16x2(d.x * scale, d.y * scale);
+  r.w = pack_bf16x2(e.x * scale, e.y * scale);
+  return r;
+}
+
+// A block owns (token, head) rows [blockIdx * kPerBlock, ...) in packed order.
+template <int D>
+struct CacheTile {
+  static constexpr int kLanes = D / 8;                                    // lanes of a row
+  static constexpr int kGroups = kCacheThreads / kLanes;                  // rows a block does at once
+  static constexpr int kPerBlock = kGroups * kCacheUnroll;
+};
+
+// Cache rows of the tokens this block touches, into shared memory.
+template <int D>
+__device__ __forceinline__ void cache_rows(const CacheParams& p, long long item0, long long items, long long* rows) {
+  const int tok0 = static_cast<int>(item0 / p.Hkv);
+  const long long last = min(item0 + CacheTile<D>::kPerBlock, items) - 1;
+  const int ntok = static_cast<int>(last / p.Hkv) - tok0 + 1;
+  for (int i = threadIdx.x; i < ntok; i += kCacheThreads) {
+    const long long r = cache_row_of(p, tok0 + i);
+    if (r == -2 && p.page_word) atomicOr(p.page_word, 1u);
+    rows[i] = r;
+  }
+  __syncthreads();
+}
+
+template <int D, bool kF8>
+__global__ void __launch_bounds__(kCacheThreads) attn_cache_write_kernel(const CacheParams p) {
+  using C = CacheTile<D>;
+  __shared__ long long rows[C::kPerBlock];
+  griddep_wait();
+  griddep_launch_dependents();
+  const long long items = static_cast<long long>(p.total) * p.Hkv;
+  const long long item0 = static_cast<long long>(blockIdx.x) * C::kPerBlock;
+  const int group = threadIdx.x / C::kLanes, lane = threadIdx.x % C::kLanes;
+  const int tok0 = static_cast<int>(item0 / p.Hkv);
+  uint4 xk[kCacheUnroll], xv[kCacheUnroll];
+  int tok[kCacheUnroll], head[kCacheUnroll];
+#pragma unroll
+  for (int u = 0; u < kCacheUnroll; ++u) {
+    const long long it = item0 + u * C::kGroups + group;
+    tok[u] = -1;
+    head[u] = 0;
+    xk[u] = xv[u] = make_uint4(0, 0, 0, 0);
+    if (it < items) {
+      const int t = static_cast<int>(it / p.Hkv);
+      tok[u] = t;
+      head[u] = static_cast<int>(it - static_cast<long long>(t) * p.Hkv);
+      xk[u] = __ldg(reinterpret_cast<const uint4*>(p.src_k + t * p.k_st + head[u] * p.k_sh) + lane);
+      xv[u] = __ldg(reinterpret_cast<const uint4*>(p.src_v + t * p.v_st + head[u] * p.v_sh) + lane);
+    }
+  }
+  cache_rows<D>(p, item0, items, rows);
+#pragma unroll
+  for (int u = 0; u < kCacheUnroll; ++u) {
+    const long long r0 = tok[u] >= 0 ? rows[tok[u] - tok0] : -1;
+    const long long r = r0 + static_cast<long long>(head[u]) * p.page;
+    if constexpr (kF8) {
+      uint32_t mk = finite_max(xk[u]), mv = finite_max(xv[u]);
+#pragma unroll
+      for (int o = C::kLanes / 2; o > 0; o >>= 1) {  // every lane of the warp, rows written or not
+        mk = max(mk, __shfl_xor_sync(0xffffffffu, mk, o));
+        mv = max(mv, __shfl_xor_sync(0xffffffffu, mv, o));
+      }
+      const uint32_t sk = scale_code(mk), sv = scale_code(mv);
+      if (r0 >= 0) {
+        reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.k) + r * D)[lane] = quantise8(xk[u], sk);
+        reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.v) + r * D)[lane] = quantise8(xv[u], sv);
+        if (lane == 0) {
+          p.ks[r] = static_cast<uint8_t>(sk);
+          p.vs[r] = static_cast<uint8_t>(sv);
+        }
+      }
+    } else if (r0 >= 0) {
+      reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.k) + r * D)[lane] = xk[u];
+      reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.v) + r * D)[lane] = xv[u];
+    }
+  }
+}
+
+template <int D, bool kF8>
+__global__ void __launch_bounds__(kCacheThreads) attn_cache_read_kernel(const CacheParams p) {
+  using C = CacheTile<D>;
+  __shared__ long long rows[C::kPerBlock];
+  griddep_wait();
+  griddep_launch_dependents();
+  const long long items = static_cast<long long>(p.total) * p.Hkv;
+  const long long item0 = static_cast<long long>(blockIdx.x) * C::kPerBlock;
+  const int group = threadIdx.x / C::kLanes, lane = threadIdx.x % C::kLanes;
+  const int tok0 = static_cast<int>(item0 / p.Hkv);
+  cache_rows<D>(p, item0, items, rows);
+  uint4 xk[kCacheUnroll], xv[kCacheUnroll];
+  long long src[kCacheUnroll];
+#pragma unroll
+  for (int u = 0; u < kCacheUnroll; ++u) {
+    const long long it = item0 + u * C::kGroups + group;
+    src[u] = -1;  // a row in no sequence: left as it was
+    xk[u] = xv[u] = make_uint4(0, 0, 0, 0);
+    if (it < items) {
+      const int t = static_cast<int>(it / p.Hkv);
+      const long long r0 = rows[t - tok0];
+      src[u] = r0;
+      if (r0 >= 0) {
+        const long long r = r0 + (it - static_cast<long long>(t) * p.Hkv) * p.page;
+        if constexpr (kF8) {
+          const uint2 ck = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.k) + r * D) + lane);
+          const uint2 cv = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.v) + r * D) + lane);
+          xk[u] = make_uint4(ck.x, ck.y, __ldg(p.ks + r), 0);
+          xv[u] = make_uint4(cv.x, cv.y, __ldg(p.vs + r), 0);
+        } else {
+          xk[u] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.k) + r * D) + lane);
+          xv[u] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.v) + r * D) + lane);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < kCacheUnroll; ++u) {
+    if (src[u] == -1) continue;  // -2 (no page): zeros
+    const long long it = item0 + u * C::kGroups + group;
+    if constexpr (kF8) {
+      xk[u] = dequantise8(make_uint2(xk[u].x, xk[u].y), scale_of(xk[u].z));
+      xv[u] = dequantise8(make_uint2(xv[u].x, xv[u].y), scale_of(xv[u].z));
+    }
+    reinterpret_cast<uint4*>(p.dst_k + it * D)[lane] = xk[u];
+    reinterpret_cast<uint4*>(p.dst_v + it * D)[lane] = xv[u];
+  }
+}
+
+}  // namespace attn

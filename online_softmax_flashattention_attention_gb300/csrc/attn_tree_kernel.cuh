@@ -1,0 +1,816 @@
+// Attention of drafted tokens over a paged cache, up to 16 rows a unit, sm_103a.
+//
+// Sequence b has ctx_b cached tokens and T_b <= 64 drafted ones at positions ctx_b ..
+// ctx_b + T_b - 1 of its pages.  Row (t, head) sees every context key, and drafted key u when
+// bit u of the token's mask word is set (without masks: u <= t).  A unit is (sequence, K/V
+// head, tile of kRows rows): the G = Hq / Hkv query heads of a group and the drafted tokens
+// share a unit's rows, row r = t * G + g, so every K/V row is read once for all of them.
+//
+// Bound: K and V are read once, 4 d (bf16) or 2 d + 2 (e4m3) bytes a key, for 4 d flops a row
+// and key; below 274 rows a unit memory is the limit.
+//
+// Work split: the keys of all units are laid end to end in chunks of 64 and cut into equal
+// ranges, one a CTA (two CTAs an SM), whatever the lengths are; every CTA finds its range from
+// a prefix sum over the sequences, so a captured launch follows the lengths on the device.  A
+// CTA's range covers a few whole units and at most two that it shares: its first piece may be
+// the rest of a unit begun by an earlier CTA, its last one the front of a unit that goes on in
+// the next.  Whole units leave as O and LSE; shared ones as the running state (m, l, o~) in
+// one of the CTA's two workspace slots, merged by attn_tree_merge_kernel.
+//
+// Inside a CTA each warp takes every fourth 16-key slice of the piece on its own: its own ring
+// of stages filled by TMA, its own (m, l, o~) in registers, no barrier in the loop.  The four
+// states are combined once a piece.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "attn_cache_kernel.cuh"
+#include "ptx.cuh"
+
+namespace attn {
+
+constexpr int kTreeMaxNodes = 64;    // bits of a mask word
+constexpr int kPlanGroups = 128;     // prefix-sum entries (each over ceil(B / 128) sequences)
+
+struct TreeParams {
+  const __nv_bfloat16* q;      // [total_q, Hq, d]
+  __nv_bfloat16* o;            // [total_q, Hq, d]
+  float* lse;                  // [Hq, total_q]
+  const int32_t* table;        // [B, max_pages]
+  const int32_t* cu;           // [B + 1]
+  const int32_t* ctx;          // [B] or null (no context)
+  const unsigned long long* mask;  // [total_q] or null (a chain)
+  const uint8_t* ks;           // [num_pages, Hkv, page] e4m3 only
+  const uint8_t* vs;
+  int B, Hq, Hkv, G;
+  int max_q, total_q;
+  int num_pages, page, max_pages;
+  int cap;                     // max_pages * page: positions the table has room for
+  float c;                     // scale * log2(e)
+  float* st_o;                 // [2 * CTAs, kRows, d] states of shared units
+  float* st_m;                 // [2 * CTAs, kRows] log2 units
+  float* st_l;
+  int4* meta;                  // [CTAs]: (sequence, head, tile, last CTA) of the unit whose front is CTA's slot 1; w < 0: none
+  uint32_t* status;            // bounded waits
+  uint32_t* page_word;         // bad pages
+  unsigned long long timeout_ns;
+};
+
+// One sequence as the kernels see it, every field clamped to what the buffers hold.
+struct TreeSeq {
+  int q0, T;    // first packed row, drafted tokens
+  int ctx, n;   // context keys, keys in all
+  int nch;      // chunks of keys (1 at least while there are rows)
+  int tiles;    // row tiles of one head
+};
+
+template <int kRows, int kChunk>
+__device__ __forceinline__ TreeSeq tree_seq(const TreeParams& p, int b) {
+  TreeSeq s;
+  s.q0 = min(max(__ldg(p.cu + b), 0), p.total_q);
+  const int q1 = min(max(__ldg(p.cu + b + 1), s.q0), p.total_q);
+  s.T = min(q1 - s.q0, p.max_q);
+  s.ctx = p.ctx ? min(max(__ldg(p.ctx + b), 0), p.cap) : 0;
+  s.n = static_cast<int>(min(static_cast<long long>(s.ctx) + s.T, static_cast<long long>(p.cap)));
+  s.nch = s.T > 0 ? max(1, s.n / kChunk + (s.n % kChunk != 0)) : 0;
+  s.tiles = (s.T * p.G + kRows - 1) / kRows;
+  return s;
+}
+
+// A run of chunks of one unit.
+struct TreePiece {
+  TreeSeq s;
+  int b, h, tile;
+  int ch0, ch1;       // chunks [ch0, ch1) of the unit's s.nch
+};
+
+// pre[i]: chunks of all units of the sequences before group i (groups of gs sequences).
+// CTA-wide (at least kPlanGroups threads).
+template <int kRows, int kChunk>
+__device__ __forceinline__ void tree_plan(const TreeParams& p, int gs, long long* pre, long long* warp_sums) {
+  const int t = threadIdx.x;
+  long long sum = 0;
+  if (t < kPlanGroups) {
+    const long long first = static_cast<long long>(t) * gs;
+    for (long long b = first; b < min(first + gs, static_cast<long long>(p.B)); ++b) {
+      const TreeSeq s = tree_seq<kRows, kChunk>(p, static_cast<int>(b));
+      sum += static_cast<long long>(s.nch) * s.tiles * p.Hkv;
+      if (blockIdx.x == 0 && s.T > 0 && p.page_word && static_cast<long long>(s.ctx) + s.T > p.cap)
+        atomicOr(p.page_word, 1u);
+    }
+    const int lane = t & 31;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += v;
+    }
+    if (lane == 31) warp_sums[t >> 5] = sum;
+  }
+  __syncthreads();
+  if (t < kPlanGroups) {
+    for (int w = 0; w < (t >> 5); ++w) sum += warp_sums[w];
+    pre[t + 1] = sum;
+    if (t == 0) pre[0] = 0;
+  }
+  __syncthreads();
+}
+
+// The piece that starts at chunk x of the whole list and ends with its unit or at x_end.
+template <int kRows, int kChunk>
+__device__ __forceinline__ TreePiece tree_piece(const TreeParams& p, int gs, const long long* pre, long long x,
+                                                long long x_end) {
+  int lo = 0, hi = kPlanGroups;  // pre[lo] <= x < pre[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (pre[mid] <= x)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  TreePiece pc;
+  pc.b = lo * gs;
+  long long base = pre[lo];
+  for (;; ++pc.b) {  // ends: x < pre[lo + 1], the chunks of this group's last sequence
+    pc.s = tree_seq<kRows, kChunk>(p, pc.b);
+    const long long w = static_cast<long long>(pc.s.nch) * pc.s.tiles * p.Hkv;
+    if (x < base + w || pc.b + 1 >= p.B) break;
+    base += w;
+  }
+  const long long y = x - base;
+  const long long unit = y / max(pc.s.nch, 1);
+  pc.h = static_cast<int>(unit / max(pc.s.tiles, 1));
+  pc.tile = static_cast<int>(unit - static_cast<long long>(pc.h) * pc.s.tiles);
+  pc.ch0 = static_cast<int>(y - unit * pc.s.nch);
+  pc.ch1 = static_cast<int>(min(static_cast<long long>(pc.s.nch), pc.ch0 + (x_end - x)));
+  return pc;
+}
+
+// Drafted nodes token t of a sequence sees, as bits.
+__device__ __forceinline__ unsigned long long tree_sees(const TreeParams& p, const TreeSeq& s, int t) {
+  const unsigned long long all = s.T >= 64 ? ~0ull : (1ull << s.T) - 1ull;
+  const unsigned long long w = p.mask ? __ldg(p.mask + s.q0 + t) : (t >= 63 ? ~0ull : (2ull << t) - 1ull);
+  return w & all;
+}
+
+// ------------------------------------------------------------------ warp-level products
+
+__device__ __forceinline__ void ldsm4(uint32_t* r, uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t* r, uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+// c[16 x 8] += a[16 x 16] b[16 x 8], fp32 accumulation.
+__device__ __forceinline__ void warp_mma_bf16(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void warp_mma_f16(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Plain bulk copy global -> shared (both addresses and the size multiples of 16 bytes).
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+      "r"(bytes), "r"(bar)
+      : "memory");
+}
+
+// e4m3 pair -> bf16 pair, exact (every e4m3 value is a bf16).
+__device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t codes) {
+  const float2 f = e4m3x2_to_f32(codes);
+  return pack_bf16x2(f.x, f.y);
+}
+
+// Whether either bf16 of a pair is infinite or NaN.
+__device__ __forceinline__ bool any_nonfinite(uint32_t w) {
+  return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+}
+
+constexpr int kTreeRows = 16;
+constexpr int kTreeChunk = 64;    // keys a CTA takes at a time: a 16-key slice a warp
+constexpr int kTreeSlice = 16;
+constexpr int kTreeWarps = 4;
+constexpr int kTreeThreads = 32 * kTreeWarps;
+
+template <int D, bool kF8>
+struct TreeCfg {
+  static constexpr int kRowBytes = kF8 ? D : 2 * D;
+  static constexpr int kHalf = kTreeSlice * kRowBytes;           // K (or V) of a slice
+  static constexpr int kStageBytes = 2 * kHalf;
+  static constexpr int kRingBytes = 24 * 1024;                   // of a warp
+  static constexpr int kStages = kRingBytes / kStageBytes;       // 3, 6, 6 or 12
+  static constexpr int kSub = kRowBytes > 128 ? kRowBytes / 128 : 1;  // 128-byte wide sub-tiles
+  static constexpr int kSubBytes = kHalf / kSub;
+  static constexpr int kScaleBytes = kF8 ? 32 : 0;               // 16 codes of K, 16 of V
+  static constexpr int kTxBytes = kStageBytes + kScaleBytes;
+  static constexpr int kOffScale = kTreeWarps * kRingBytes;
+  static constexpr int kOffBar = kOffScale + kTreeWarps * kStages * 32;
+  static constexpr int kOffMerge = kOffBar + kTreeWarps * kStages * 8;
+  static constexpr int kMergeStride = 36;                        // floats a row of 32 columns
+  static constexpr int kOffStat = kOffMerge + kTreeWarps * kTreeRows * kMergeStride * 4;
+  static constexpr int kOffPre = kOffStat + 2 * kTreeWarps * kTreeRows * 4;
+  static constexpr int kOffMisc = kOffPre + (kPlanGroups + 1 + 8) * 8;
+  static constexpr int kSmem = kOffMisc + 16 + 1024;             // slack to align the base
+  static_assert(kOffMerge % 16 == 0 && kOffPre % 8 == 0, "alignment");
+  static_assert(kSmem <= 113 * 1024, "two CTAs an SM");
+};
+
+template <int D, bool kF8>
+__global__ void __launch_bounds__(kTreeThreads, 2)
+    attn_tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                     const TreeParams p) {
+  using C = TreeCfg<D, kF8>;
+  constexpr int kTilesN = D / 8;   // 8-wide column tiles of o~
+  constexpr int kSteps = D / 16;   // 16-deep steps of q . k
+  constexpr float kTau = 8.f;      // o~ is rescaled when the max rises by more (log2 units)
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, t = lane & 3;  // fragment row and column pair
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t ring = sbase + warp * C::kRingBytes;
+  const uint32_t bars = sbase + C::kOffBar + warp * C::kStages * 8;
+  uint8_t* scales = smem + C::kOffScale + warp * C::kStages * 32;
+  float* merge = reinterpret_cast<float*>(smem + C::kOffMerge);
+  float* stat_m = reinterpret_cast<float*>(smem + C::kOffStat);
+  float* stat_l = stat_m + kTreeWarps * kTreeRows;
+  long long* pre = reinterpret_cast<long long*>(smem + C::kOffPre);
+  volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + C::kOffMisc);
+  const WaitCtx wc{abort_flag, p.status, p.timeout_ns};
+
+  if (lane == 0) {
+    for (int s = 0; s < C::kStages; ++s) mbar_init(bars + 8 * s, 1);
+    fence_mbar_init();
+    if (warp == 0) {
+      *abort_flag = 0u;
+      tma_prefetch_desc(&tmK);
+      tma_prefetch_desc(&tmV);
+    }
+  }
+  griddep_wait();
+  griddep_launch_dependents();
+  const int gs = (p.B + kPlanGroups - 1) / kPlanGroups;
+  tree_plan<kTreeRows, kTreeChunk>(p, gs, pre, pre + kPlanGroups + 1);  // its barriers also publish the mbarriers
+
+  const long long W = pre[kPlanGroups];
+  const int grid = static_cast<int>(gridDim.x), cta = static_cast<int>(blockIdx.x);
+  const long long per = W / grid, extra = W % grid;  // the first `extra` CTAs take one chunk more
+  const long long x0 = per * cta + min(static_cast<long long>(cta), extra);
+  const long long x1 = x0 + per + (cta < extra ? 1 : 0);
+  bool has_tail = false;
+
+  // ---- loads: an iterator over this warp's slices, kStages ahead of the products
+  const uint64_t pol = policy_evict_first();
+  long long px = x0;          // next chunk to make a piece of
+  int ps = 0, ps_end = 0;     // slices [ps, ps_end) step 4 of the piece in hand
+  int pbase = 0, pages = 0;   // lane i: the page of slice pbase + 4 i
+  int pb = 0, ph = 0;
+  uint32_t skip = 0;          // stages whose slice has no page: nothing was loaded
+  uint32_t live = 0;          // stages with a copy in flight
+  uint32_t phase = 0;         // parity each stage completes next
+  int ist = 0;                // stage of the next issue
+  auto fetch_pages = [&]() {
+    pbase = ps;
+    const long long s = ps + static_cast<long long>(kTreeWarps) * lane;
+    pages = s < ps_end ? __ldg(p.table + static_cast<long long>(pb) * p.max_pages + s * kTreeSlice / p.page) : -1;
+  };
+  auto issue = [&]() {
+    while (ps >= ps_end) {
+      if (px >= x1) return;
+      const TreePiece pc = tree_piece<kTreeRows, kTreeChunk>(p, gs, pre, px, x1);
+      px += pc.ch1 - pc.ch0;
+      pb = pc.b;
+      ph = pc.h;
+      ps = pc.ch0 * (kTreeChunk / kTreeSlice) + warp;
+      const long long end = min(static_cast<long long>(pc.ch1) * kTreeChunk, static_cast<long long>(pc.s.n));
+      ps_end = static_cast<int>((end + kTreeSlice - 1) / kTreeSlice);
+      fetch_pages();
+    }
+    if (ps - pbase >= 32 * kTreeWarps) fetch_pages();
+    const int pg = __shfl_sync(0xffffffffu, pages, (ps - pbase) / kTreeWarps);
+    const uint32_t bit = 1u << ist;
+    if (static_cast<unsigned>(pg) >= static_cast<unsigned>(p.num_pages)) {
+      skip |= bit;
+      if (lane == 0 && p.page_word) atomicOr(p.page_word, 1u);
+    } else {
+      skip &= ~bit;
+      live |= bit;
+      if (lane == 0) {
+        const int row = static_cast<int>(static_cast<unsigned>(ps * kTreeSlice) % static_cast<unsigned>(p.page));
+        const uint32_t bar = bars + 8 * ist, dst = ring + ist * C::kStageBytes;
+        mbar_arrive_expect_tx(bar, C::kTxBytes);
+#pragma unroll
+        for (int s = 0; s < C::kSub; ++s) tma_load_4d(dst + s * C::kSubBytes, &tmK, bar, s * 64, row, ph, pg, pol);
+#pragma unroll
+        for (int s = 0; s < C::kSub; ++s)
+          tma_load_4d(dst + C::kHalf + s * C::kSubBytes, &tmV, bar, s * 64, row, ph, pg, pol);
+        if constexpr (kF8) {
+          const long long r = (static_cast<long long>(pg) * p.Hkv + ph) * p.page + row;
+          const uint32_t sc = smem_u32(scales + ist * 32);
+          bulk_load(sc, p.ks + r, 16, bar);
+          bulk_load(sc + 16, p.vs + r, 16, bar);
+        }
+      }
+    }
+    ps += kTreeWarps;
+    ist = ist + 1 == C::kStages ? 0 : ist + 1;
+  };
+#pragma unroll 1
+  for (int s = 0; s < C::kStages; ++s) issue();
+
+  bool ok = true;
+  int cst = 0;  // stage of the next slice to take
+  for (long long x = x0; x < x1;) {
+    const TreePiece pc = tree_piece<kTreeRows, kTreeChunk>(p, gs, pre, x, x1);
+    x += pc.ch1 - pc.ch0;
+    // ---- this thread's two rows: g and g + 8
+    const int rows = pc.s.T * p.G;
+    float cr[2];                    // c, times the power of two the row was divided by (e4m3)
+    unsigned long long sees[2];
+    const __nv_bfloat16* qrow[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = pc.tile * kTreeRows + g + 8 * i;
+      cr[i] = p.c;
+      sees[i] = 0;
+      qrow[i] = nullptr;
+      if (r < rows) {
+        const int tok = r / p.G;
+        sees[i] = tree_sees(p, pc.s, tok);
+        qrow[i] = p.q + (static_cast<long long>(pc.s.q0 + tok) * p.Hq + pc.h * p.G + (r - tok * p.G)) * D;
+      }
+    }
+    uint32_t qf[kSteps][4];
+    if constexpr (!kF8) {
+#pragma unroll
+      for (int k = 0; k < kSteps; ++k)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)  // columns 16 k + 8 (j / 2) + 2 t
+          qf[k][j] = qrow[j & 1] ? __ldg(reinterpret_cast<const uint32_t*>(qrow[j & 1]) + k * 8 + (j >> 1) * 4 + t) : 0u;
+    } else {
+      // f16 operands: a row is divided by the power of two of its largest finite value, so its
+      // values lie in (-2, 2) and keep all 8 bits down to 2^-14 of the largest.  Columns are
+      // taken in the order the codes of K arrive in: 16 k + 4 t .. + 3.
+      uint2 w[kSteps][2];
+      uint32_t mx[2] = {0, 0};
+#pragma unroll
+      for (int k = 0; k < kSteps; ++k)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          w[k][i] = qrow[i] ? __ldg(reinterpret_cast<const uint2*>(qrow[i]) + k * 4 + t) : make_uint2(0u, 0u);
+          mx[i] = max(mx[i], finite_max(make_uint4(w[k][i].x, w[k][i].y, 0u, 0u)));
+        }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        mx[i] = max(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
+        mx[i] = max(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2));
+        const uint32_t ef = min(max(mx[i] >> 7, 1u), 253u);  // exponent field of the row's power of two
+        const float inv = __uint_as_float((254u - ef) << 23);
+        cr[i] = p.c * __uint_as_float(ef << 23);
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k) {
+          const __half2 lo = __floats2half2_rn(bf16_lo(w[k][i].x) * inv, bf16_hi(w[k][i].x) * inv);
+          const __half2 hi = __floats2half2_rn(bf16_lo(w[k][i].y) * inv, bf16_hi(w[k][i].y) * inv);
+          qf[k][i] = *reinterpret_cast<const uint32_t*>(&lo);
+          qf[k][2 + i] = *reinterpret_cast<const uint32_t*>(&hi);
+        }
+      }
+    }
+    float acc[kTilesN][4];
+#pragma unroll
+    for (int j = 0; j < kTilesN; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[j][i] = 0.f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};  // l: this thread's columns only
+
+    const long long end = min(static_cast<long long>(pc.ch1) * kTreeChunk, static_cast<long long>(pc.s.n));
+    const int s_end = static_cast<int>((end + kTreeSlice - 1) / kTreeSlice);
+    for (int s = pc.ch0 * (kTreeChunk / kTreeSlice) + warp; s < s_end; s += kTreeWarps) {
+      const int st = cst;
+      cst = cst + 1 == C::kStages ? 0 : cst + 1;
+      const uint32_t bit = 1u << st;
+      const bool absent = (skip & bit) != 0;
+      if (!absent) {
+        const bool got = mbar_wait(bars + 8 * st, (phase & bit) ? 1u : 0u, wc, 32);
+        if (!__all_sync(0xffffffffu, got)) ok = false;
+        if (ok) {  // a wait that ran out leaves its copy in flight
+          phase ^= bit;
+          live &= ~bit;
+        }
+      }
+      if (!ok) break;
+      if (!absent) {
+        const uint32_t sk = ring + st * C::kStageBytes, sv = sk + C::kHalf;
+        const int k0 = s * kTreeSlice;
+        // ---- scores of 16 keys: sc[n-tile][row g: 0, 1; row g + 8: 2, 3], keys 8 n + 2 t, + 1
+        float sc[2][4];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) (&sc[0][0])[i] = 0.f;
+        float pv[4];  // scales of V of this thread's keys (e4m3)
+        if constexpr (!kF8) {
+          const int key = (lane >> 4) * 8 + (lane & 7);
+#pragma unroll
+          for (int k = 0; k < kSteps; ++k) {
+            const int ch = (k & 3) * 2 + ((lane >> 3) & 1);  // 16-byte chunk of the 128-byte row
+            uint32_t b[4];
+            ldsm4(b, sk + (k >> 2) * C::kSubBytes + key * 128 + ((ch ^ (key & 7)) << 4));
+            warp_mma_bf16(sc[0], qf[k], b[0], b[1]);
+            warp_mma_bf16(sc[1], qf[k], b[2], b[3]);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            sc[0][i] *= p.c;
+            sc[1][i] *= p.c;
+            pv[i] = 1.f;
+          }
+        } else {
+          // chunk ch holds 16 columns; a register of it is 4 codes of a key, two f16 pairs
+          const int key = ((lane >> 3) & 1) * 8 + (lane & 7);
+#pragma unroll
+          for (int k = 0; k < kSteps; k += 2) {
+            const int ch = k + (lane >> 4);
+            const uint32_t at = D == 128 ? key * 128 + ((ch ^ (key & 7)) << 4) : key * 64 + ((ch ^ ((key >> 1) & 3)) << 4);
+            uint32_t b[4];
+            ldsm4(b, sk + at);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              warp_mma_f16(sc[0], qf[k + i], e4m3x2_to_f16x2(b[2 * i] & 0xffffu), e4m3x2_to_f16x2(b[2 * i] >> 16));
+              warp_mma_f16(sc[1], qf[k + i], e4m3x2_to_f16x2(b[2 * i + 1] & 0xffffu), e4m3x2_to_f16x2(b[2 * i + 1] >> 16));
+            }
+          }
+          const uint8_t* kc = scales + st * 32;
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            const uint32_t a = *reinterpret_cast<const uint16_t*>(kc + 8 * n + 2 * t);
+            const uint32_t b = *reinterpret_cast<const uint16_t*>(kc + 16 + 8 * n + 2 * t);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const float f = scale_of(i ? a >> 8 : a & 0xffu);
+              sc[n][i] *= cr[0] * f;
+              sc[n][2 + i] *= cr[1] * f;
+              // a key that does not exist may have any code: 0 keeps 0 * scale from being NaN
+              pv[2 * n + i] = k0 + 8 * n + 2 * t + i < pc.s.n ? scale_of(i ? b >> 8 : b & 0xffu) : 0.f;
+            }
+          }
+        }
+        // ---- masks: every row sees the context; drafted keys go by the row's bits
+        const bool draft = k0 + kTreeSlice > pc.s.ctx;
+        if (draft) {
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const int u = k0 + 8 * n + 2 * t + i - pc.s.ctx;
+              if (u >= 0) {
+                if (u >= 64 || !((sees[0] >> u) & 1ull)) sc[n][i] = -INFINITY;
+                if (u >= 64 || !((sees[1] >> u) & 1ull)) sc[n][2 + i] = -INFINITY;
+              }
+            }
+        }
+        // ---- running max (rows g, g + 8) and probabilities
+        uint32_t pf[4];
+        bool move = false;
+        float alpha[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float mx = fmaxf(fmaxf(sc[0][2 * i], sc[0][2 * i + 1]), fmaxf(sc[1][2 * i], sc[1][2 * i + 1]));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+          const float mn = mx > m[i] + kTau ? mx : m[i];
+          const float ref = mn == -INFINITY ? 0.f : mn;
+          alpha[i] = ex2_approx(m[i] - ref);
+          move |= mn != m[i];
+          m[i] = mn;
+          float sum = 0.f;
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const float e = ex2_approx(sc[n][2 * i + j] - ref);
+              sum += e;
+              sc[n][2 * i + j] = e;
+            }
+          l[i] = l[i] * alpha[i] + sum;
+        }
+        if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+          for (int j = 0; j < kTilesN; ++j) {
+            acc[j][0] *= alpha[0];
+            acc[j][1] *= alpha[0];
+            acc[j][2] *= alpha[1];
+            acc[j][3] *= alpha[1];
+          }
+        }
+        // P to bf16 for the product (relative 2^-9, unbiased; bf16 and not f16 for its range:
+        // many small probabilities next to a large one keep their relative precision)
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            pf[2 * n + i] = pack_bf16x2(sc[n][2 * i] * pv[2 * n], sc[n][2 * i + 1] * pv[2 * n + 1]);
+        // ---- o~ += P V.  Columns of tile j: bf16 8 j + 2 t, + 1; e4m3 16 (j / 2) + 4 t + (j & 1), + 2.
+        const int left = pc.s.n - k0;  // keys from `left` on do not exist: their rows may hold anything
+        uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
+        if (left < kTreeSlice) {
+          keep0 = (2 * t < left ? 0xffffu : 0u) | (2 * t + 1 < left ? 0xffff0000u : 0u);
+          keep1 = (2 * t + 8 < left ? 0xffffu : 0u) | (2 * t + 9 < left ? 0xffff0000u : 0u);
+        }
+        const int vkey = ((lane >> 3) & 1) * 8 + (lane & 7);
+        auto load_v = [&](int jj, uint32_t* b) {  // tiles 2 jj, 2 jj + 1: b[0..1], b[2..3]
+          if constexpr (!kF8) {
+            const int ch = (jj & 3) * 2 + (lane >> 4);
+            ldsm4_t(b, sv + (jj >> 2) * C::kSubBytes + vkey * 128 + ((ch ^ (vkey & 7)) << 4));
+          }
+        };
+        bool odd = false;  // a drafted key's value that is infinite or NaN
+        if (draft) {
+          // A masked probability of 0 times such a value would be NaN in rows that do not see
+          // the key: then this slice goes key by key and only to the rows that see it.
+          uint32_t bad = 0;
+          if constexpr (kF8) bad = lane < kTreeSlice && lane < left && scales[st * 32 + 16 + lane] == 255u;
+#pragma unroll 1
+          for (int i = lane; i < kTreeSlice * C::kRowBytes / 4; i += 32) {
+            if (i * 4 / C::kRowBytes >= left) break;
+            // every word of the slice once, wherever the swizzle put it inside its row
+            const int row = i / (C::kRowBytes / 4), wd = i % (C::kRowBytes / 4);
+            const uint32_t at = C::kSub == 1 ? row * C::kRowBytes + wd * 4
+                                             : (wd / 32) * C::kSubBytes + row * 128 + (wd % 32) * 4;
+            const uint32_t w = *reinterpret_cast<const uint32_t*>(smem + (sv - sbase) + at);
+            if constexpr (kF8) {
+              bad |= any_nonfinite(e4m3x2_to_bf16x2(w & 0xffffu)) || any_nonfinite(e4m3x2_to_bf16x2(w >> 16));
+            } else {
+              bad |= any_nonfinite(w);
+            }
+          }
+          odd = __any_sync(0xffffffffu, bad != 0);
+        }
+        if (!odd) {
+          if constexpr (!kF8) {
+#pragma unroll
+            for (int jj = 0; jj < kTilesN / 2; ++jj) {
+              uint32_t b[4];
+              load_v(jj, b);
+              warp_mma_bf16(acc[2 * jj], pf, b[0] & keep0, b[1] & keep1);
+              warp_mma_bf16(acc[2 * jj + 1], pf, b[2] & keep0, b[3] & keep1);
+            }
+          } else {
+#pragma unroll
+            for (int c0 = 0; c0 < kSteps; c0 += 2) {  // two 16-column chunks: four tiles
+              const int ch = c0 + (lane >> 4);
+              const uint32_t at =
+                  D == 128 ? vkey * 128 + ((ch ^ (vkey & 7)) << 4) : vkey * 64 + ((ch ^ ((vkey >> 1) & 3)) << 4);
+              uint32_t b[4];
+              ldsm4_t(b, sv + at);  // b[0], b[1]: keys 0-7, 8-15 of chunk c0; b[2], b[3]: of c0 + 1
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                // codes (key 2t, col 2g), (2t, 2g + 1), (2t + 1, 2g), (2t + 1, 2g + 1) -> pairs of keys
+                const uint32_t y0 = __byte_perm(b[2 * i], 0, 0x3120), y1 = __byte_perm(b[2 * i + 1], 0, 0x3120);
+                warp_mma_bf16(acc[2 * (c0 + i)], pf, e4m3x2_to_bf16x2(y0 & 0xffffu) & keep0,
+                              e4m3x2_to_bf16x2(y1 & 0xffffu) & keep1);
+                warp_mma_bf16(acc[2 * (c0 + i) + 1], pf, e4m3x2_to_bf16x2(y0 >> 16) & keep0,
+                              e4m3x2_to_bf16x2(y1 >> 16) & keep1);
+              }
+            }
+          }
+        } else {
+#pragma unroll 1
+          for (int key = 0; key < min(left, kTreeSlice); ++key) {
+            const int u = k0 + key - pc.s.ctx;
+            // the probabilities of this key sit in lane (key % 8) / 2 of each row's four
+            float e[2];
+            bool see[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const float a = (key & 8) ? sc[1][2 * i] * pv[2] : sc[0][2 * i] * pv[0];
+              const float b = (key & 8) ? sc[1][2 * i + 1] * pv[3] : sc[0][2 * i + 1] * pv[1];
+              e[i] = __shfl_sync(0xffffffffu, (key & 1) ? b : a, (lane & ~3) | ((key & 7) >> 1));
+              see[i] = u < 0 || (u < 64 && ((sees[i] >> u) & 1ull));
+            }
+#pragma unroll
+            for (int j = 0; j < kTilesN; ++j)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                float v;
+                if constexpr (!kF8) {
+                  const int col = 8 * j + 2 * t + i, ch = (col % 64) / 8;
+                  const uint32_t at = (col / 64) * C::kSubBytes + key * 128 + ((ch ^ (key & 7)) << 4) + (col & 7) * 2;
+                  v = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(smem + (sv - sbase) + at));
+                } else {
+                  const int col = 16 * (j / 2) + 4 * t + (j & 1) + 2 * i, ch = col / 16;
+                  const uint32_t at = (D == 128 ? key * 128 + ((ch ^ (key & 7)) << 4) : key * 64 + ((ch ^ ((key >> 1) & 3)) << 4)) + (col & 15);
+                  v = e4m3x2_to_f32(smem[(sv - sbase) + at]).x;
+                }
+                if (see[0]) acc[j][i] = fmaf(e[0], v, acc[j][i]);
+                if (see[1]) acc[j][2 + i] = fmaf(e[1], v, acc[j][2 + i]);
+              }
+          }
+        }
+      }
+      __syncwarp();  // every lane has read the stage
+      issue();
+    }
+
+    // ---- the four warps' states into one
+    if (!ok) *abort_flag = 1u;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+      if (t == 0) {
+        stat_m[warp * kTreeRows + g + 8 * i] = m[i];
+        stat_l[warp * kTreeRows + g + 8 * i] = l[i];
+      }
+    }
+    __syncthreads();
+    ok = *abort_flag == 0u;  // the same for every thread until the next piece's waits
+    float f[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float M = stat_m[g + 8 * i];
+#pragma unroll
+      for (int w = 1; w < kTreeWarps; ++w) M = fmaxf(M, stat_m[w * kTreeRows + g + 8 * i]);
+      f[i] = ex2_approx(m[i] - (M == -INFINITY ? 0.f : M));
+    }
+    const int orow = threadIdx.x >> 3, ocol = (threadIdx.x & 7) * 4;  // of the 16 x 32 quarter
+    float M = -INFINITY, L = 0.f;
+#pragma unroll
+    for (int w = 0; w < kTreeWarps; ++w) M = fmaxf(M, stat_m[w * kTreeRows + orow]);
+    const float ref = M == -INFINITY ? 0.f : M;
+#pragma unroll
+    for (int w = 0; w < kTreeWarps; ++w)
+      L = fmaf(stat_l[w * kTreeRows + orow], ex2_approx(stat_m[w * kTreeRows + orow] - ref), L);
+    const int r = pc.tile * kTreeRows + orow;
+    const bool whole = pc.ch0 == 0 && pc.ch1 == pc.s.nch;
+    const int slot = 2 * cta + (pc.ch0 == 0 ? 1 : 0);
+    const int tok = r / p.G;
+    const long long at = static_cast<long long>(pc.s.q0 + tok) * p.Hq + pc.h * p.G + (r - tok * p.G);
+    const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
+#pragma unroll
+    for (int q = 0; q < D / 32; ++q) {
+      if (q > 0) __syncthreads();  // the quarter before has been read
+      float* dst = merge + warp * kTreeRows * C::kMergeStride;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float* row = dst + (g + 8 * i) * C::kMergeStride;
+        if constexpr (!kF8) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<float2*>(row + 8 * j + 2 * t) =
+                make_float2(acc[4 * q + j][2 * i] * f[i], acc[4 * q + j][2 * i + 1] * f[i]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const float* e = acc[4 * q + 2 * j];
+            const float* o = acc[4 * q + 2 * j + 1];
+            *reinterpret_cast<float4*>(row + 16 * j + 4 * t) =
+                make_float4(e[2 * i] * f[i], o[2 * i] * f[i], e[2 * i + 1] * f[i], o[2 * i + 1] * f[i]);
+          }
+        }
+      }
+      __syncthreads();
+      float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kTreeWarps; ++w) {
+        const float4 v = *reinterpret_cast<const float4*>(merge + (w * kTreeRows + orow) * C::kMergeStride + ocol);
+        sum.x += v.x;
+        sum.y += v.y;
+        sum.z += v.z;
+        sum.w += v.w;
+      }
+      if (ok && r < rows) {
+        if (whole) {
+          *reinterpret_cast<uint2*>(p.o + at * D + 32 * q + ocol) =
+              make_uint2(pack_bf16x2(sum.x * inv, sum.y * inv), pack_bf16x2(sum.z * inv, sum.w * inv));
+        } else {
+          *reinterpret_cast<float4*>(p.st_o + (static_cast<long long>(slot) * kTreeRows + orow) * D + 32 * q + ocol) = sum;
+        }
+      }
+    }
+    if (ok && r < rows && ocol == 0) {
+      if (whole) {
+        p.lse[static_cast<long long>(pc.h * p.G + (r - tok * p.G)) * p.total_q + pc.s.q0 + tok] =
+            L > 0.f || L != L ? M * 0.69314718055994531f + logf(L) : -INFINITY;
+      } else {
+        p.st_m[slot * kTreeRows + orow] = M;
+        p.st_l[slot * kTreeRows + orow] = L;
+      }
+    }
+    if (pc.ch0 == 0 && pc.ch1 < pc.s.nch) {  // goes on in the next CTAs: the last piece of this one
+      has_tail = true;
+      if (threadIdx.x == 0) {
+        // the CTA that holds the unit's last chunk
+        const long long last = x + (pc.s.nch - pc.ch1) - 1;
+        const long long big = extra * (per + 1);
+        const long long owner = last < big ? last / (per + 1) : extra + (last - big) / max(per, 1ll);
+        p.meta[cta] = make_int4(pc.b, pc.h, pc.tile, ok ? static_cast<int>(owner) : -1);
+      }
+    }
+    __syncthreads();  // the statistics may be overwritten
+    if (!ok) break;
+  }
+  if (!has_tail && threadIdx.x == 0) p.meta[cta] = make_int4(0, 0, 0, -1);
+  // after a failed wait copies may still be in flight: let them land
+  if (live) {
+#pragma unroll 1
+    for (int s = 0; s < C::kStages; ++s)
+      if ((live >> s) & 1u) mbar_wait_drain(bars + 8 * s, (phase >> s) & 1u, p.timeout_ns);
+  }
+}
+
+// Units shared by several CTAs: CTA c's slot 1 holds the front of one, slot 0 of the CTAs after
+// it, up to meta[c].w, the rest.  A warp merges a row: every state is moved to the largest
+// reference, the sums add in CTA order (no atomics: the same bits every time), one division.
+template <int D, int kRows>
+__global__ void __launch_bounds__(128) attn_tree_merge_kernel(const TreeParams p) {
+  constexpr int kPer = D / 32;
+  constexpr int kBatch = 8;  // states loaded together
+  griddep_wait();
+  griddep_launch_dependents();
+  const int cta = static_cast<int>(blockIdx.x);
+  const int4 mt = p.meta[cta];
+  if (mt.w < 0) return;
+  const int row = blockIdx.y * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const TreeSeq s = tree_seq<kRows, 1>(p, mt.x);
+  const int r = mt.z * kRows + row;
+  if (r >= s.T * p.G) return;
+  const int count = mt.w - cta + 1;
+  float M = -INFINITY, L = 0.f;
+  float acc[kPer];
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) acc[k] = 0.f;
+  for (int c0 = 0; c0 < count; c0 += kBatch) {
+    float ms[kBatch], ls[kBatch], os[kBatch][kPer];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      ms[i] = -INFINITY;
+      ls[i] = 0.f;
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) os[i][k] = 0.f;
+      if (c0 + i < count) {
+        const long long at = static_cast<long long>(2 * (cta + c0 + i) + (c0 + i == 0 ? 1 : 0)) * kRows + row;
+        ms[i] = p.st_m[at];
+        ls[i] = p.st_l[at];
+        const float* src = p.st_o + at * D + lane * kPer;
+        if constexpr (kPer == 4) {
+          const float4 v = *reinterpret_cast<const float4*>(src);
+          os[i][0] = v.x;
+          os[i][1] = v.y;
+          os[i][2] = v.z;
+          os[i][3] = v.w;
+        } else {
+          const float2 v = *reinterpret_cast<const float2*>(src);
+          os[i][0] = v.x;
+          os[i][1] = v.y;
+        }
+      }
+    }
+    float mc = M;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) mc = fmaxf(mc, ms[i]);
+    const float ref = mc == -INFINITY ? 0.f : mc;
+    const float a = ex2_approx(M - ref);
+    L *= a;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) acc[k] *= a;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const float w = ex2_approx(ms[i] - ref);
+      L = fmaf(w, ls[i], L);
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) acc[k] = fmaf(w, os[i][k], acc[k]);
+    }
+    M = mc;
+  }
+  const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
+  const int tok = r / p.G, head = mt.y * p.G + (r - tok * p.G);
+  __nv_bfloat16* dst = p.o + (static_cast<long long>(s.q0 + tok) * p.Hq + head) * D + lane * kPer;
+  if constexpr (kPer == 4)
+    *reinterpret_cast<uint2*>(dst) =
+        make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
+  else
+    *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
+  if (lane == 0)
+    p.lse[static_cast<long long>(head) * p.total_q + s.q0 + tok] =
+        L > 0.f || L != L ? M * 0.69314718055994531f + logf(L) : -INFINITY;
+}
+
+}  // namespace attn
