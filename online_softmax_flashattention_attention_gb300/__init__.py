@@ -368,66 +368,68 @@ def attn_fwd_varlen(Q, K, V, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, O=None, L
 
 
 # --- paged cache, and attention over it ------------------------------------------
+# A decoding step calls these once a layer with little work on the GPU, so the host's time
+# counts: the checks are written out in a line each and nothing is looked up twice.
 
 def _cache_args(k_cache, v_cache, k_scale, v_scale):
     """The attn_cache of these tensors (every check of their shapes, types and placement)."""
     import torch
-    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
+    shape, dtype, dev = k_cache.shape, k_cache.dtype, k_cache.device
+    if len(shape) != 4 or v_cache.shape != shape or v_cache.dtype != dtype:
         raise ValueError("k_cache and v_cache must be [num_pages, Hkv, page_size, d] of one type")
-    dev = k_cache.device
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        if not t.is_cuda or not t.is_contiguous() or t.device != dev:
-            raise ValueError(f"{name} must be a contiguous CUDA tensor on the cache's device")
-    P, H, page, d = k_cache.shape
-    if k_cache.dtype == torch.bfloat16:
+    if not (k_cache.is_cuda and v_cache.device == dev and k_cache.is_contiguous() and v_cache.is_contiguous()):
+        raise ValueError("k_cache and v_cache must be contiguous CUDA tensors on one device")
+    P, H, page, d = shape
+    if dtype == torch.bfloat16:
         if k_scale is not None or v_scale is not None:
             raise ValueError("a bf16 cache takes no k_scale / v_scale")
-        return AttnCache(ctypes.sizeof(AttnCache), k_cache.data_ptr(), v_cache.data_ptr(), None, None, CACHE_BF16, P,
-                         page, H, d)
-    if k_cache.dtype != torch.float8_e4m3fn:
+        return AttnCache(_CACHE_SIZE, k_cache.data_ptr(), v_cache.data_ptr(), None, None, CACHE_BF16, P, page, H, d)
+    if dtype != torch.float8_e4m3fn:
         raise ValueError("the cache must be bf16 or float8_e4m3fn")
-    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-        if t is None or t.dtype != torch.uint8 or t.device != dev or t.shape != (P, H, page) or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous uint8 CUDA tensor [num_pages, Hkv, page_size]")
-    return AttnCache(ctypes.sizeof(AttnCache), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
-                     v_scale.data_ptr(), CACHE_E4M3, P, page, H, d)
+    if (k_scale is None or v_scale is None or k_scale.dtype != torch.uint8 or v_scale.dtype != torch.uint8
+            or k_scale.shape != shape[:3] or v_scale.shape != shape[:3] or k_scale.device != dev
+            or v_scale.device != dev or not k_scale.is_contiguous() or not v_scale.is_contiguous()):
+        raise ValueError("k_scale and v_scale must be contiguous uint8 tensors [num_pages, Hkv, page_size] on the "
+                         "cache's device")
+    return AttnCache(_CACHE_SIZE, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                     CACHE_E4M3, P, page, H, d)
 
 
-def _batch_args(dev, block_table, cu_seqlens, cu_name, lens, lens_name):
-    """Checks the int32 arrays of a batch; returns (B, max_pages, lens_ptr)."""
+_CACHE_SIZE = ctypes.sizeof(AttnCache)
+
+
+def _batch_args(dev, block_table, cu_seqlens, lens):
+    """Checks the int32 arrays of a batch; returns (B, max_pages, lens pointer)."""
     import torch
-    if block_table.dim() != 2:
-        raise ValueError("block_table must be [B, max_pages]")
+    i32 = torch.int32
+    if block_table.dim() != 2 or block_table.dtype != i32 or block_table.device != dev or not block_table.is_contiguous():
+        raise ValueError("block_table must be a contiguous int32 tensor [B, max_pages] on the cache's device")
     B, max_pages = block_table.shape
-    for name, t, n in (("block_table", block_table, None), (cu_name, cu_seqlens, B + 1), (lens_name, lens, B)):
-        if t is None:
-            continue
-        if t.dtype != torch.int32 or t.device != dev or not t.is_contiguous() or (n is not None and t.numel() != n):
-            raise ValueError(f"{name} must be a contiguous int32 tensor on the cache's device"
-                             + ("" if n is None else f" with {n} elements"))
-    return B, max_pages, None if lens is None else lens.data_ptr()
+    if cu_seqlens.numel() != B + 1 or cu_seqlens.dtype != i32 or cu_seqlens.device != dev or not cu_seqlens.is_contiguous():
+        raise ValueError("the cu_seqlens array must be a contiguous int32 tensor [B + 1] on the cache's device")
+    if lens is None:
+        return B, max_pages, None
+    if lens.numel() != B or lens.dtype != i32 or lens.device != dev or not lens.is_contiguous():
+        raise ValueError("start_lens / ctx_lens must be a contiguous int32 tensor [B] on the cache's device")
+    return B, max_pages, lens.data_ptr()
 
 
-class _On:
-    """The device of a call's tensors made current, and its stream for what is allocated."""
+def _elsewhere(dev, stream):
+    """Context that makes a call's device current, and its stream for what is allocated there
+    (so that buffers made here belong to the stream that uses them); None when both already are."""
+    import contextlib
 
-    def __init__(self, dev, stream):
-        import torch
-        self.contexts = []
-        if torch.cuda.current_device() != dev.index:
-            self.contexts.append(torch.cuda.device(dev))
-        if stream is not None:  # buffers made here belong to the stream that uses them
-            if stream.device != dev:
-                raise ValueError("stream is on another device than the tensors")
-            self.contexts.append(torch.cuda.stream(stream))
-
-    def __enter__(self):
-        for c in self.contexts:
-            c.__enter__()
-
-    def __exit__(self, *exc):
-        for c in reversed(self.contexts):
-            c.__exit__(*exc)
+    import torch
+    if dev.type != "cuda":
+        raise ValueError("the cache must be on a CUDA device")
+    if stream is None:
+        return None if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+    if stream.device != dev:
+        raise ValueError("stream is on another device than the tensors")
+    both = contextlib.ExitStack()
+    both.enter_context(torch.cuda.device(dev))
+    both.enter_context(torch.cuda.stream(stream))
+    return both
 
 
 def attn_cache_write(K, V, k_cache, v_cache, block_table, cu_seqlens, *, start_lens=None, k_scale=None, v_scale=None,
@@ -443,22 +445,30 @@ def attn_cache_write(K, V, k_cache, v_cache, block_table, cu_seqlens, *, start_l
     reported by cache_check().
     """
     import torch
-    cache = _cache_args(k_cache, v_cache, k_scale, v_scale)
     dev = k_cache.device
-    for name, t in (("K", K), ("V", V)):
-        if (t.dim() != 3 or t.dtype != torch.bfloat16 or t.device != dev or t.shape[1] != cache.num_heads
-                or t.shape[2] != cache.d or t.stride(2) != 1):
-            raise ValueError(f"{name} must be a bf16 tensor [total, Hkv, d] on the cache's device with a contiguous "
-                             "last dimension")
-    if V.shape[0] != K.shape[0]:
-        raise ValueError("K and V must have the same number of tokens")
-    B, max_pages, start_ptr = _batch_args(dev, block_table, cu_seqlens, "cu_seqlens", start_lens, "start_lens")
-    strides = ctypes.c_int64 * 2
-    with _On(dev, stream):
-        _check(load_library().attn_cache_write(ctypes.byref(cache), K.data_ptr(), V.data_ptr(),
-                                               strides(K.stride(0), K.stride(1)), strides(V.stride(0), V.stride(1)),
-                                               block_table.data_ptr(), max_pages, cu_seqlens.data_ptr(), start_ptr, B,
-                                               K.shape[0], _stream_handle(stream)))
+    away = _elsewhere(dev, stream)
+    if away is not None:
+        with away:
+            return attn_cache_write(K, V, k_cache, v_cache, block_table, cu_seqlens, start_lens=start_lens,
+                                    k_scale=k_scale, v_scale=v_scale)
+    cache = _cache_args(k_cache, v_cache, k_scale, v_scale)
+    shape = K.shape
+    if (len(shape) != 3 or shape[1] != cache.num_heads or shape[2] != cache.d or V.shape != shape
+            or K.dtype != torch.bfloat16 or V.dtype != torch.bfloat16 or K.device != dev or V.device != dev):
+        raise ValueError("K and V must be bf16 tensors [total, Hkv, d] on the cache's device")
+    ks, vs = K.stride(), V.stride()
+    if ks[2] != 1 or vs[2] != 1:
+        raise ValueError("K and V must have a contiguous last dimension")
+    B, max_pages, start_ptr = _batch_args(dev, block_table, cu_seqlens, start_lens)
+    rc = load_library().attn_cache_write(cache, K.data_ptr(), V.data_ptr(), _Strides(ks[0], ks[1]),
+                                         _Strides(vs[0], vs[1]), block_table.data_ptr(), max_pages,
+                                         cu_seqlens.data_ptr(), start_ptr, B, shape[0],
+                                         torch._C._cuda_getCurrentRawStream(dev.index))
+    if rc != 0:
+        _check(rc)
+
+
+_Strides = ctypes.c_int64 * 2
 
 
 def attn_cache_read(k_cache, v_cache, block_table, cu_seqlens, total, K=None, V=None, *, start_lens=None, k_scale=None,
@@ -468,21 +478,27 @@ def attn_cache_read(k_cache, v_cache, block_table, cu_seqlens, total, K=None, V=
     sequence b; rows outside every sequence are left as they were, positions without a page are
     zeros and reported by cache_check().  The cache's arguments: as attn_cache_write."""
     import torch
-    cache = _cache_args(k_cache, v_cache, k_scale, v_scale)
     dev = k_cache.device
-    B, max_pages, start_ptr = _batch_args(dev, block_table, cu_seqlens, "cu_seqlens", start_lens, "start_lens")
-    shape = (int(total), cache.num_heads, cache.d)
-    with _On(dev, stream):
-        if K is None:
-            K = torch.empty(shape, dtype=torch.bfloat16, device=dev)
-        if V is None:
-            V = torch.empty(shape, dtype=torch.bfloat16, device=dev)
-        for name, t in (("K", K), ("V", V)):
-            if t.shape != shape or t.dtype != torch.bfloat16 or t.device != dev or not t.is_contiguous():
-                raise ValueError(f"{name} must be a contiguous bf16 tensor [total, Hkv, d] on the cache's device")
-        _check(load_library().attn_cache_read(ctypes.byref(cache), K.data_ptr(), V.data_ptr(), block_table.data_ptr(),
-                                              max_pages, cu_seqlens.data_ptr(), start_ptr, B, shape[0],
-                                              _stream_handle(stream)))
+    away = _elsewhere(dev, stream)
+    if away is not None:
+        with away:
+            return attn_cache_read(k_cache, v_cache, block_table, cu_seqlens, total, K, V, start_lens=start_lens,
+                                   k_scale=k_scale, v_scale=v_scale)
+    cache = _cache_args(k_cache, v_cache, k_scale, v_scale)
+    B, max_pages, start_ptr = _batch_args(dev, block_table, cu_seqlens, start_lens)
+    shape = (total, cache.num_heads, cache.d)
+    if K is None:
+        K = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    if V is None:
+        V = torch.empty_like(K)
+    for t in (K, V):
+        if t.shape != shape or t.dtype != torch.bfloat16 or t.device != dev or not t.is_contiguous():
+            raise ValueError("K and V must be contiguous bf16 tensors [total, Hkv, d] on the cache's device")
+    rc = load_library().attn_cache_read(cache, K.data_ptr(), V.data_ptr(), block_table.data_ptr(), max_pages,
+                                        cu_seqlens.data_ptr(), start_ptr, B, total,
+                                        torch._C._cuda_getCurrentRawStream(dev.index))
+    if rc != 0:
+        _check(rc)
     return K, V
 
 
@@ -506,39 +522,48 @@ def attn_fwd_tree(Q, k_cache, v_cache, block_table, ctx_lens, cu_seqlens_q, max_
     attn_cache_write.
     """
     import torch
-    cache = _cache_args(k_cache, v_cache, k_scale, v_scale)
     dev = k_cache.device
-    if Q.dim() != 3 or Q.dtype != torch.bfloat16 or Q.device != dev or not Q.is_contiguous() or Q.shape[2] != cache.d:
+    away = _elsewhere(dev, stream)
+    if away is not None:
+        with away:
+            return attn_fwd_tree(Q, k_cache, v_cache, block_table, ctx_lens, cu_seqlens_q, max_seqlen_q, O, LSE,
+                                 tree_mask=tree_mask, k_scale=k_scale, v_scale=v_scale, scale=scale,
+                                 workspace=workspace)
+    cache = _cache_args(k_cache, v_cache, k_scale, v_scale)
+    shape = Q.shape
+    if (len(shape) != 3 or shape[2] != cache.d or Q.dtype != torch.bfloat16 or Q.device != dev
+            or not Q.is_contiguous()):
         raise ValueError("Q must be a contiguous bf16 tensor [total_q, Hq, d] on the cache's device")
-    total_q, Hq, d = Q.shape
-    B, max_pages, ctx_ptr = _batch_args(dev, block_table, cu_seqlens_q, "cu_seqlens_q", ctx_lens, "ctx_lens")
+    total_q, Hq, d = shape
+    B, max_pages, ctx_ptr = _batch_args(dev, block_table, cu_seqlens_q, ctx_lens)
     mask_ptr = None
     if tree_mask is not None:
         if (tree_mask.dtype != torch.int64 or tree_mask.device != dev or tree_mask.numel() != total_q
                 or not tree_mask.is_contiguous()):
             raise ValueError("tree_mask must be a contiguous int64 tensor [total_q] on the cache's device")
         mask_ptr = tree_mask.data_ptr()
-    if scale is None:
-        scale = 1.0 / math.sqrt(d)
     lib = load_library()
-    with _On(dev, stream):
-        if O is None:
-            O = torch.empty_like(Q)
-        if LSE is None:
-            LSE = torch.empty((Hq, total_q), dtype=torch.float32, device=dev)
-        if O.shape != Q.shape or O.dtype != torch.bfloat16 or O.device != dev or not O.is_contiguous():
-            raise ValueError("O must be a contiguous bf16 tensor shaped like Q")
-        if LSE.shape != (Hq, total_q) or LSE.dtype != torch.float32 or LSE.device != dev or not LSE.is_contiguous():
-            raise ValueError("LSE must be a contiguous fp32 tensor [Hq, total_q]")
-        if workspace is None:
-            need = lib.attn_tree_workspace_bytes(Hq, cache.num_heads, int(max_seqlen_q), d)
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        elif workspace.device != dev or not workspace.is_contiguous():
-            raise ValueError("workspace must be a contiguous tensor on the cache's device")
-        _check(lib.attn_fwd_tree(Q.data_ptr(), ctypes.byref(cache), O.data_ptr(), LSE.data_ptr(),
-                                 block_table.data_ptr(), max_pages, cu_seqlens_q.data_ptr(), ctx_ptr, mask_ptr, B, Hq,
-                                 int(max_seqlen_q), total_q, float(scale), workspace.data_ptr(),
-                                 workspace.numel() * workspace.element_size(), _stream_handle(stream)))
+    if O is None:
+        O = torch.empty_like(Q)
+    elif O.shape != shape or O.dtype != torch.bfloat16 or O.device != dev or not O.is_contiguous():
+        raise ValueError("O must be a contiguous bf16 tensor shaped like Q")
+    if LSE is None:
+        LSE = torch.empty((Hq, total_q), dtype=torch.float32, device=dev)
+    elif LSE.shape != (Hq, total_q) or LSE.dtype != torch.float32 or LSE.device != dev or not LSE.is_contiguous():
+        raise ValueError("LSE must be a contiguous fp32 tensor [Hq, total_q]")
+    if workspace is None:
+        nbytes = lib.attn_tree_workspace_bytes(Hq, cache.num_heads, max_seqlen_q, d)
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the cache's device")
+    else:
+        nbytes = workspace.numel() * workspace.element_size()
+    rc = lib.attn_fwd_tree(Q.data_ptr(), cache, O.data_ptr(), LSE.data_ptr(), block_table.data_ptr(), max_pages,
+                           cu_seqlens_q.data_ptr(), ctx_ptr, mask_ptr, B, Hq, max_seqlen_q, total_q,
+                           1.0 / math.sqrt(d) if scale is None else scale, workspace.data_ptr(), nbytes,
+                           torch._C._cuda_getCurrentRawStream(dev.index))
+    if rc != 0:
+        _check(rc)
     return O, LSE
 
 

@@ -9,8 +9,8 @@
 // Bound: K and V are read once, 4 d (bf16) or 2 d + 2 (e4m3) bytes a key, for 4 d flops a row
 // and key; below 274 rows a unit memory is the limit.
 //
-// Work split: the keys of all units are laid end to end in chunks of 64 and cut into equal
-// ranges, one a CTA (two CTAs an SM), whatever the lengths are; every CTA finds its range from
+// Work split: the keys of all units are laid end to end in chunks of 64 (and some places for
+// what a unit costs beside them, see tree_plan) and cut into equal ranges, one a CTA (two CTAs an SM), whatever the lengths are; every CTA finds its range from
 // a prefix sum over the sequences, so a captured launch follows the lengths on the device.  A
 // CTA's range covers a few whole units and at most two that it shares: its first piece may be
 // the rest of a unit begun by an earlier CTA, its last one the front of a unit that goes on in
@@ -34,7 +34,7 @@
 namespace attn {
 
 constexpr int kTreeMaxNodes = 64;    // bits of a mask word
-constexpr int kPlanGroups = 128;     // prefix-sum entries (each over ceil(B / 128) sequences)
+constexpr int kPlanGroups = 64;      // prefix-sum entries (each over ceil(B / 64) sequences)
 
 struct TreeParams {
   const __nv_bfloat16* q;      // [total_q, Hq, d]
@@ -44,12 +44,16 @@ struct TreeParams {
   const int32_t* cu;           // [B + 1]
   const int32_t* ctx;          // [B] or null (no context)
   const unsigned long long* mask;  // [total_q] or null (a chain)
+  const void* v;               // the cache's values
   const uint8_t* ks;           // [num_pages, Hkv, page] e4m3 only
   const uint8_t* vs;
   int B, Hq, Hkv, G;
   int max_q, total_q;
   int num_pages, page, max_pages;
   int cap;                     // max_pages * page: positions the table has room for
+  int box_rows;                // keys a copy takes (128-row tiles): 16 .. 128, divides the page
+  int tok_tile;                // tokens a 128-row tile holds (kRows = 128)
+  int unit_cost;               // what a unit costs beside its chunks, in chunks (see tree_plan)
   float c;                     // scale * log2(e)
   float* st_o;                 // [2 * CTAs, kRows, d] states of shared units
   float* st_m;                 // [2 * CTAs, kRows] log2 units
@@ -77,18 +81,34 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeParams& p, int b) {
   s.ctx = p.ctx ? min(max(__ldg(p.ctx + b), 0), p.cap) : 0;
   s.n = static_cast<int>(min(static_cast<long long>(s.ctx) + s.T, static_cast<long long>(p.cap)));
   s.nch = s.T > 0 ? max(1, s.n / kChunk + (s.n % kChunk != 0)) : 0;
-  s.tiles = (s.T * p.G + kRows - 1) / kRows;
+  s.tiles = kRows == 16 ? (s.T * p.G + kRows - 1) / kRows : (s.T + p.tok_tile - 1) / p.tok_tile;
   return s;
+}
+
+// Row r of a tile: token and head of the group; false when there is none.  16-row tiles are
+// cut from the rows t * G + g; a 128-row tile holds all heads of tok_tile tokens.
+template <int kRows>
+__device__ __forceinline__ bool tree_row(const TreeParams& p, const TreeSeq& s, int tile, int r, int* tok, int* g) {
+  const int rr = kRows == 16 ? tile * kRows + r : r;
+  const int t = rr / p.G;
+  *g = rr - t * p.G;
+  *tok = kRows == 16 ? t : tile * p.tok_tile + t;
+  return *tok < s.T && (kRows == 16 || t < p.tok_tile);
 }
 
 // A run of chunks of one unit.
 struct TreePiece {
   TreeSeq s;
   int b, h, tile;
-  int ch0, ch1;       // chunks [ch0, ch1) of the unit's s.nch
+  int ch0, ch1;       // chunks [ch0, ch1) of the unit's s.nch (none when ch1 <= ch0)
+  long long adv;      // places of the list it covers
 };
 
-// pre[i]: chunks of all units of the sequences before group i (groups of gs sequences).
+// The list of places the CTAs divide: every unit takes unit_cost places, then one for each of
+// its chunks.  The places at the front stand for what a unit costs whatever its length (its
+// rows, its start, its states' merge); without them a CTA that falls among many short
+// sequences gets as many units as another gets chunks.
+// pre[i]: places of all units of the sequences before group i (groups of gs sequences).
 // CTA-wide (at least kPlanGroups threads).
 template <int kRows, int kChunk>
 __device__ __forceinline__ void tree_plan(const TreeParams& p, int gs, long long* pre, long long* warp_sums) {
@@ -98,7 +118,7 @@ __device__ __forceinline__ void tree_plan(const TreeParams& p, int gs, long long
     const long long first = static_cast<long long>(t) * gs;
     for (long long b = first; b < min(first + gs, static_cast<long long>(p.B)); ++b) {
       const TreeSeq s = tree_seq<kRows, kChunk>(p, static_cast<int>(b));
-      sum += static_cast<long long>(s.nch) * s.tiles * p.Hkv;
+      sum += (s.nch > 0 ? static_cast<long long>(s.nch) + p.unit_cost : 0ll) * s.tiles * p.Hkv;
       if (blockIdx.x == 0 && s.T > 0 && p.page_word && static_cast<long long>(s.ctx) + s.T > p.cap)
         atomicOr(p.page_word, 1u);
     }
@@ -119,7 +139,7 @@ __device__ __forceinline__ void tree_plan(const TreeParams& p, int gs, long long
   __syncthreads();
 }
 
-// The piece that starts at chunk x of the whole list and ends with its unit or at x_end.
+// The piece that starts at place x of the list and ends with its unit or at x_end.
 template <int kRows, int kChunk>
 __device__ __forceinline__ TreePiece tree_piece(const TreeParams& p, int gs, const long long* pre, long long x,
                                                 long long x_end) {
@@ -134,19 +154,32 @@ __device__ __forceinline__ TreePiece tree_piece(const TreeParams& p, int gs, con
   TreePiece pc;
   pc.b = lo * gs;
   long long base = pre[lo];
-  for (;; ++pc.b) {  // ends: x < pre[lo + 1], the chunks of this group's last sequence
+  int len = 1;  // places of a unit of the sequence
+  for (;; ++pc.b) {  // ends: x < pre[lo + 1], the places of this group's last sequence
     pc.s = tree_seq<kRows, kChunk>(p, pc.b);
-    const long long w = static_cast<long long>(pc.s.nch) * pc.s.tiles * p.Hkv;
+    len = pc.s.nch + p.unit_cost;
+    const long long w = pc.s.nch > 0 ? static_cast<long long>(len) * pc.s.tiles * p.Hkv : 0;
     if (x < base + w || pc.b + 1 >= p.B) break;
     base += w;
   }
   const long long y = x - base;
-  const long long unit = y / max(pc.s.nch, 1);
-  pc.h = static_cast<int>(unit / max(pc.s.tiles, 1));
-  pc.tile = static_cast<int>(unit - static_cast<long long>(pc.h) * pc.s.tiles);
-  pc.ch0 = static_cast<int>(y - unit * pc.s.nch);
-  pc.ch1 = static_cast<int>(min(static_cast<long long>(pc.s.nch), pc.ch0 + (x_end - x)));
+  // 32-bit division where it fits (a 64-bit one costs about as much as a global load)
+  const int unit = y <= 0xffffffffll ? static_cast<int>(static_cast<uint32_t>(y) / static_cast<uint32_t>(len))
+                                     : static_cast<int>(y / len);
+  pc.h = unit / max(pc.s.tiles, 1);
+  pc.tile = unit - pc.h * pc.s.tiles;
+  const int off = static_cast<int>(y - static_cast<long long>(unit) * len);
+  const int end = static_cast<int>(min(static_cast<long long>(len), off + (x_end - x)));
+  pc.adv = end - off;
+  pc.ch0 = max(0, off - p.unit_cost);
+  pc.ch1 = max(0, end - p.unit_cost);
   return pc;
+}
+
+// The CTA whose range holds place x: the first `extra` CTAs have per + 1 places, the others per.
+__device__ __forceinline__ int tree_owner(long long x, long long per, long long extra) {
+  const long long big = extra * (per + 1);
+  return static_cast<int>(x < big ? x / (per + 1) : extra + (x - big) / max(per, 1ll));
 }
 
 // Drafted nodes token t of a sequence sees, as bits.
@@ -228,7 +261,7 @@ struct TreeCfg {
   static constexpr int kMergeStride = 36;                        // floats a row of 32 columns
   static constexpr int kOffStat = kOffMerge + kTreeWarps * kTreeRows * kMergeStride * 4;
   static constexpr int kOffPre = kOffStat + 2 * kTreeWarps * kTreeRows * 4;
-  static constexpr int kOffMisc = kOffPre + (kPlanGroups + 1 + 8) * 8;
+  static constexpr int kOffMisc = kOffPre + (kPlanGroups + 1 + 4) * 8;
   static constexpr int kSmem = kOffMisc + 16 + 1024;             // slack to align the base
   static_assert(kOffMerge % 16 == 0 && kOffPre % 8 == 0, "alignment");
   static_assert(kSmem <= 113 * 1024, "two CTAs an SM");
@@ -297,7 +330,8 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
     while (ps >= ps_end) {
       if (px >= x1) return;
       const TreePiece pc = tree_piece<kTreeRows, kTreeChunk>(p, gs, pre, px, x1);
-      px += pc.ch1 - pc.ch0;
+      px += pc.adv;
+      if (pc.ch1 <= pc.ch0) continue;
       pb = pc.b;
       ph = pc.h;
       ps = pc.ch0 * (kTreeChunk / kTreeSlice) + warp;
@@ -341,22 +375,21 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
   int cst = 0;  // stage of the next slice to take
   for (long long x = x0; x < x1;) {
     const TreePiece pc = tree_piece<kTreeRows, kTreeChunk>(p, gs, pre, x, x1);
-    x += pc.ch1 - pc.ch0;
+    x += pc.adv;
+    if (pc.ch1 <= pc.ch0) continue;
     // ---- this thread's two rows: g and g + 8
-    const int rows = pc.s.T * p.G;
     float cr[2];                    // c, times the power of two the row was divided by (e4m3)
     unsigned long long sees[2];
     const __nv_bfloat16* qrow[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int r = pc.tile * kTreeRows + g + 8 * i;
+      int tok, head;
       cr[i] = p.c;
-      sees[i] = 0;
+      sees[i] = ~0ull;  // a row that is none: anything
       qrow[i] = nullptr;
-      if (r < rows) {
-        const int tok = r / p.G;
+      if (tree_row<kTreeRows>(p, pc.s, pc.tile, g + 8 * i, &tok, &head)) {
         sees[i] = tree_sees(p, pc.s, tok);
-        qrow[i] = p.q + (static_cast<long long>(pc.s.q0 + tok) * p.Hq + pc.h * p.G + (r - tok * p.G)) * D;
+        qrow[i] = p.q + (static_cast<long long>(pc.s.q0 + tok) * p.Hq + pc.h * p.G + head) * D;
       }
     }
     uint32_t qf[kSteps][4];
@@ -542,7 +575,10 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
           }
         };
         bool odd = false;  // a drafted key's value that is infinite or NaN
-        if (draft) {
+        // drafted nodes of this slice, as bits; nothing is masked when every row sees them all
+        const int u0 = max(0, k0 - pc.s.ctx), u1 = min(pc.s.T, k0 + kTreeSlice - pc.s.ctx);
+        const unsigned long long here = u1 > u0 ? ((~0ull >> (64 - (u1 - u0))) << u0) : 0ull;
+        if (draft && __any_sync(0xffffffffu, ((sees[0] & sees[1]) & here) != here)) {
           // A masked probability of 0 times such a value would be NaN in rows that do not see
           // the key: then this slice goes key by key and only to the rows that see it.
           uint32_t bad = 0;
@@ -658,11 +694,11 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
 #pragma unroll
     for (int w = 0; w < kTreeWarps; ++w)
       L = fmaf(stat_l[w * kTreeRows + orow], ex2_approx(stat_m[w * kTreeRows + orow] - ref), L);
-    const int r = pc.tile * kTreeRows + orow;
+    int tok, head;
+    const bool row_here = tree_row<kTreeRows>(p, pc.s, pc.tile, orow, &tok, &head);
     const bool whole = pc.ch0 == 0 && pc.ch1 == pc.s.nch;
     const int slot = 2 * cta + (pc.ch0 == 0 ? 1 : 0);
-    const int tok = r / p.G;
-    const long long at = static_cast<long long>(pc.s.q0 + tok) * p.Hq + pc.h * p.G + (r - tok * p.G);
+    const long long at = static_cast<long long>(pc.s.q0 + tok) * p.Hq + pc.h * p.G + head;
     const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
 #pragma unroll
     for (int q = 0; q < D / 32; ++q) {
@@ -696,7 +732,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
         sum.z += v.z;
         sum.w += v.w;
       }
-      if (ok && r < rows) {
+      if (ok && row_here) {
         if (whole) {
           *reinterpret_cast<uint2*>(p.o + at * D + 32 * q + ocol) =
               make_uint2(pack_bf16x2(sum.x * inv, sum.y * inv), pack_bf16x2(sum.z * inv, sum.w * inv));
@@ -705,9 +741,9 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
         }
       }
     }
-    if (ok && r < rows && ocol == 0) {
+    if (ok && row_here && ocol == 0) {
       if (whole) {
-        p.lse[static_cast<long long>(pc.h * p.G + (r - tok * p.G)) * p.total_q + pc.s.q0 + tok] =
+        p.lse[static_cast<long long>(pc.h * p.G + head) * p.total_q + pc.s.q0 + tok] =
             L > 0.f || L != L ? M * 0.69314718055994531f + logf(L) : -INFINITY;
       } else {
         p.st_m[slot * kTreeRows + orow] = M;
@@ -718,10 +754,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
       has_tail = true;
       if (threadIdx.x == 0) {
         // the CTA that holds the unit's last chunk
-        const long long last = x + (pc.s.nch - pc.ch1) - 1;
-        const long long big = extra * (per + 1);
-        const long long owner = last < big ? last / (per + 1) : extra + (last - big) / max(per, 1ll);
-        p.meta[cta] = make_int4(pc.b, pc.h, pc.tile, ok ? static_cast<int>(owner) : -1);
+        p.meta[cta] = make_int4(pc.b, pc.h, pc.tile, ok ? tree_owner(x + (pc.s.nch - pc.ch1) - 1, per, extra) : -1);
       }
     }
     __syncthreads();  // the statistics may be overwritten
@@ -750,8 +783,8 @@ __global__ void __launch_bounds__(128) attn_tree_merge_kernel(const TreeParams p
   if (mt.w < 0) return;
   const int row = blockIdx.y * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   const TreeSeq s = tree_seq<kRows, 1>(p, mt.x);
-  const int r = mt.z * kRows + row;
-  if (r >= s.T * p.G) return;
+  int tok, g;
+  if (!tree_row<kRows>(p, s, mt.z, row, &tok, &g)) return;
   const int count = mt.w - cta + 1;
   float M = -INFINITY, L = 0.f;
   float acc[kPer];
@@ -801,7 +834,7 @@ __global__ void __launch_bounds__(128) attn_tree_merge_kernel(const TreeParams p
     M = mc;
   }
   const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
-  const int tok = r / p.G, head = mt.y * p.G + (r - tok * p.G);
+  const int head = mt.y * p.G + g;
   __nv_bfloat16* dst = p.o + (static_cast<long long>(s.q0 + tok) * p.Hq + head) * D + lane * kPer;
   if constexpr (kPer == 4)
     *reinterpret_cast<uint2*>(dst) =
