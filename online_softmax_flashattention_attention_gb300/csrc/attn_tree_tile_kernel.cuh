@@ -9,8 +9,16 @@
 // the list of chunks (128 keys each).
 //
 // Warps: 0-3 softmax, thread r owns row r (tensor-memory lane r); 4 producer (TMA); 5 issues
-// P V; 6 issues S; 7 (bf16) repairs V blocks at a sequence's end, see below; 8-11 (e4m3)
-// convert blocks to bf16 with their scales, 128 keys x d values a block, exact.
+// P V; 6 issues S; 7 (bf16) repairs V blocks at a sequence's end, see below, or (e4m3) turns
+// the scale codes of K into floats; 8-11 (e4m3) convert Q and V, thread r row r.
+//
+// e4m3: the codes of K go to the tensor cores as they are.  A query row, divided by the power
+// of two that brings its largest finite value into [128, 256), is split into two e4m3 terms,
+// q = hi + lo: 8 significant bits are 4 + 4, so the split is exact down to 2^-10 of the row's
+// largest and off by at most 2^-19 of it below, and S = hi K^T + lo K^T in fp32.  The row's
+// power of two and each key's scale multiply the scores afterwards.  V is widened to bf16 with
+// its scale, exact, because P needs bf16's range (two e4m3 terms would drop probabilities
+// under 2^-18 of the largest, which together can matter in a long context).
 //
 // K and V blocks are up to eight boxes of 16 keys, each from the page it lies in (larger boxes
 // when the page size allows: fewer copies).  A block that holds drafted keys, or keys past the
@@ -32,6 +40,19 @@ constexpr int kTileWarpFix = 7;
 constexpr uint32_t kTileRegsSoftmax = 232;  // of 3 x 168 (e4m3: 384 threads): 232 + 104 + 168 = 504
 constexpr uint32_t kTileRegsOther = 104;
 constexpr int kTileTags = 16;
+// Pieces announced in shared memory.  The producer is at most 7 blocks, so at most 8 pieces,
+// ahead of the softmax, and no role is behind it: a slot is never overwritten while in use.
+constexpr int kTilePieces = 16;
+
+// A piece as the producer announces it to the other roles.
+struct TileJob {
+  int q0, T, ctx, n;       // the sequence's first row, drafted tokens, context and keys
+  int b, h, tile, nch;
+  int ch0, ch1;            // blocks; ch1 <= ch0: the end of the list
+  int owner;               // the CTA with the unit's last block
+  int unused;
+};
+static_assert(sizeof(TileJob) == 48, "three 16-byte words");
 
 template <int D, bool kF8>
 struct TileCfg {
@@ -39,29 +60,53 @@ struct TileCfg {
   static constexpr int kSub = D / 64;                    // 64-column sub-tiles of a bf16 row
   static constexpr int kSubBytes = 128 * 128;            // 128 rows x 64 bf16
   static constexpr int kTileBytes = kSub * kSubBytes;    // a block of K, V or Q in bf16
-  static constexpr int kRawBytes = 128 * D;              // a block of K or V in e4m3
-  static constexpr int kStages = kF8 ? (D == 64 ? 3 : 2) : (D == 64 ? 4 : 3);
-  static constexpr int kRaw = kF8 ? 2 : 0;               // e4m3 stages
+  static constexpr int kRawBytes = 128 * D;              // a block in e4m3
+  // Rings: K and V blocks as they arrive, and (e4m3) V blocks in bf16
+  static constexpr int kRingK = kF8 ? 4 : (D == 64 ? 4 : 3);
+  static constexpr int kRingV = kF8 ? 3 : kRingK;
+  static constexpr int kWide = kF8 ? (D == 64 ? 3 : 2) : 0;
+  static constexpr int kStageK = kF8 ? kRawBytes : kTileBytes;
+  static constexpr int kStageV = kStageK;
   static constexpr int kSBufs = 3;
   static constexpr int kOffQ = 0;
-  static constexpr int kOffK = kTileBytes;
-  static constexpr int kOffV = kOffK + kStages * kTileBytes;
-  static constexpr int kOffRaw = kOffV + kStages * kTileBytes;          // K then V of each raw stage
-  static constexpr int kOffScale = kOffRaw + kRaw * 2 * kRawBytes;      // 128 codes of K, 128 of V a stage
-  static constexpr int kOffBar = kOffScale + kRaw * 256;
-  // q_full, q_free, {k_full, v_full, k_free, v_free, v_fixed}[S], {s_full, pv_done, p_full}[B],
-  // drain[2], {rk_full, rv_full, rk_free, rv_free}[R]
-  static constexpr int kNumBars = 2 + 5 * kStages + 3 * kSBufs + 2 + 4 * kRaw;
-  static constexpr int kOffPre = kOffBar + 8 * kNumBars;
-  static constexpr int kOffMisc = kOffPre + 8 * (kPlanGroups + 1 + 4);  // tmem base, abort, valid[8], tags[16]
-  static constexpr int kSmem = kOffMisc + 8 + 32 + 4 * kTileTags + 1024;
+  // e4m3: hi, then lo.  At d = 128 each row's two terms take the very bytes of its bf16 row
+  // (128 in each sub-tile), so a thread overwrites only what it has read; at d = 64 they lie beside.
+  static constexpr int kOffQ8 = kF8 && D == 64 ? kTileBytes : 0;
+  static constexpr int kOffK = kOffQ8 + kTileBytes;
+  static constexpr int kOffV = kOffK + kRingK * kStageK;
+  static constexpr int kOffWide = kOffV + kRingV * kStageV;
+  static constexpr int kOffCodeK = kOffWide + kWide * kTileBytes;       // scale codes, 128 a stage
+  static constexpr int kOffCodeV = kOffCodeK + (kF8 ? kRingK * 128 : 0);
+  static constexpr int kOffScaleK = kOffCodeV + (kF8 ? kRingV * 128 : 0);  // floats, block g % 8
+  static constexpr int kOffScaleQ = kOffScaleK + (kF8 ? 8 * 512 : 0);      // floats, piece u % 8
+  static constexpr int kOffBar = kOffScaleQ + (kF8 ? 8 * 512 : 0);
+  // q_full, q_free, q8_full, {k_full, k_free, k_ready}[RK], {v_full, v_free, v_fixed}[RV],
+  // {w_full, w_free}[W], {s_full, pv_done, p_full}[B], drain[2], piece[16]
+  static constexpr int kNumBars = 3 + 3 * kRingK + 3 * kRingV + 2 * kWide + 3 * kSBufs + 2 + kTilePieces;
+  static constexpr int kOffPieces = (kOffBar + 8 * kNumBars + 15) / 16 * 16;
+  static constexpr int kOffPre = kOffPieces + kTilePieces * 48;
+  static constexpr int kOffMisc = kOffPre + 8 * (kPlanGroups + 1 + 4);  // tmem base, abort, valid[16], tags[16]
+  static constexpr int kSmem = kOffMisc + 8 + 64 + 4 * kTileTags + 1024;
   static_assert(kSmem <= 232448, "shared memory per CTA");
   __host__ __device__ static constexpr uint32_t col_s(int b) { return 128u * b; }
   static constexpr uint32_t kColO = 128u * kSBufs;
   static constexpr uint32_t kIdescS = idesc_bf16_f32(kTileRows, kTileKeys, 0);
+  // kind::f8f6f4, e4m3 x e4m3 -> fp32 (the formats' codes are 0)
+  static constexpr uint32_t kIdescS8 = (1u << 4) | ((kTileKeys >> 3) << 17) | ((kTileRows >> 4) << 24);
   static constexpr uint32_t kIdescO = idesc_bf16_f32(kTileRows, D, 1);
   static_assert(kColO + D <= 512, "tensor memory");
 };
+
+// D[tmem] (+)= A[smem desc] * B[smem desc]^T, kind::f8f6f4 (e4m3 in, fp32 accumulate), k = 32.
+__device__ __forceinline__ void mma_ss_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
 
 // A bf16 pair with its infinite and NaN halves zeroed.
 __device__ __forceinline__ uint32_t finite_only(uint32_t w) {
@@ -85,36 +130,72 @@ __device__ __forceinline__ uint4 widen8(uint32_t lo, uint32_t hi, __nv_bfloat162
   return r;
 }
 
+// Infinities and NaN among the drafted values of a piece, which went into the product as zero,
+// to a row that sees their keys: columns col .. col + 31 of its o~ (a positive weight leaves
+// them what they are).
+template <bool kF8>
+__device__ __forceinline__ void tile_add_nonfinite(const TreeParams& p, const TileJob& t, unsigned long long sees, int col,
+                                                   int d, uint32_t* o) {
+#pragma unroll 1
+  for (; sees; sees &= sees - 1) {
+    const int pos = t.ctx + __ffsll(static_cast<long long>(sees)) - 1;
+    if (pos >= t.n || pos / kTileKeys < t.ch0 || pos / kTileKeys >= t.ch1) continue;
+    const int pg = __ldg(p.table + static_cast<long long>(t.b) * p.max_pages + pos / p.page);
+    if (static_cast<unsigned>(pg) >= static_cast<unsigned>(p.num_pages)) continue;
+    const long long at = (static_cast<long long>(pg) * p.Hkv + t.h) * p.page + pos % p.page;
+    uint32_t two = 0;
+    if constexpr (kF8) two = static_cast<uint32_t>(__ldg(p.vs + at)) * 0x00800080u;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      uint32_t w;
+      if constexpr (kF8) {
+        const uint32_t cw = e4m3x2_to_bf16x2(__ldg(reinterpret_cast<const uint16_t*>(static_cast<const uint8_t*>(p.v) + at * d + col) + k));
+        const __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&cw), *reinterpret_cast<const __nv_bfloat162*>(&two));
+        w = *reinterpret_cast<const uint32_t*>(&v);
+      } else {
+        w = __ldg(reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(p.v) + at * d + col) + k);
+      }
+      if (any_nonfinite(w & 0xffffu)) o[2 * k] = __float_as_uint(__uint_as_float(o[2 * k]) + bf16_lo(w));
+      if (any_nonfinite(w & 0xffff0000u)) o[2 * k + 1] = __float_as_uint(__uint_as_float(o[2 * k + 1]) + bf16_hi(w));
+    }
+  }
+}
+
 template <int D, bool kF8>
 __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
     attn_tree_tile_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                           const __grid_constant__ CUtensorMap tmV, const TreeParams p) {
   using C = TileCfg<D, kF8>;
-  constexpr int S = C::kStages, NB = C::kSBufs, R = C::kRaw > 0 ? C::kRaw : 1;
+  constexpr int RK = C::kRingK, RV = C::kRingV, NB = C::kSBufs, NW = C::kWide;
+  constexpr int NWm = NW > 0 ? NW : 1;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
   const uint32_t sQ = sbase + C::kOffQ, sK = sbase + C::kOffK, sV = sbase + C::kOffV;
   const uint32_t bar0 = sbase + C::kOffBar;
-  const uint32_t bar_q_full = bar0, bar_q_free = bar0 + 8u;
-  auto bar_k_full = [&](int s) { return bar0 + 8u * (2 + s); };
-  auto bar_v_full = [&](int s) { return bar0 + 8u * (2 + S + s); };
-  auto bar_k_free = [&](int s) { return bar0 + 8u * (2 + 2 * S + s); };
-  auto bar_v_free = [&](int s) { return bar0 + 8u * (2 + 3 * S + s); };
-  auto bar_v_fixed = [&](int s) { return bar0 + 8u * (2 + 4 * S + s); };
-  auto bar_s_full = [&](int b) { return bar0 + 8u * (2 + 5 * S + b); };
-  auto bar_pv_done = [&](int b) { return bar0 + 8u * (2 + 5 * S + NB + b); };
-  auto bar_p_full = [&](int b) { return bar0 + 8u * (2 + 5 * S + 2 * NB + b); };
-  auto bar_drain = [&](int i) { return bar0 + 8u * (2 + 5 * S + 3 * NB + i); };
-  auto bar_raw = [&](int kind, int s) { return bar0 + 8u * (4 + 5 * S + 3 * NB + kind * C::kRaw + s); };
+  const uint32_t bar_q_full = bar0, bar_q_free = bar0 + 8u, bar_q8_full = bar0 + 16u;
+  auto bar_k_full = [&](int s) { return bar0 + 8u * (3 + s); };
+  auto bar_k_free = [&](int s) { return bar0 + 8u * (3 + RK + s); };
+  auto bar_k_ready = [&](int s) { return bar0 + 8u * (3 + 2 * RK + s); };  // e4m3: its scales are out
+  auto bar_v_full = [&](int s) { return bar0 + 8u * (3 + 3 * RK + s); };
+  auto bar_v_free = [&](int s) { return bar0 + 8u * (3 + 3 * RK + RV + s); };
+  auto bar_v_fixed = [&](int s) { return bar0 + 8u * (3 + 3 * RK + 2 * RV + s); };
+  auto bar_w_full = [&](int s) { return bar0 + 8u * (3 + 3 * RK + 3 * RV + s); };
+  auto bar_w_free = [&](int s) { return bar0 + 8u * (3 + 3 * RK + 3 * RV + NW + s); };
+  constexpr int kB1 = 3 + 3 * RK + 3 * RV + 2 * NW;
+  auto bar_s_full = [&](int b) { return bar0 + 8u * (kB1 + b); };
+  auto bar_pv_done = [&](int b) { return bar0 + 8u * (kB1 + NB + b); };
+  auto bar_p_full = [&](int b) { return bar0 + 8u * (kB1 + 2 * NB + b); };
+  auto bar_drain = [&](int i) { return bar0 + 8u * (kB1 + 3 * NB + i); };
+  auto bar_piece = [&](int i) { return bar0 + 8u * (kB1 + 3 * NB + 2 + i); };
   long long* pre = reinterpret_cast<long long*>(smem + C::kOffPre);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + C::kOffMisc + 4);
-  // valid[g % 8]: which 16-key slices of block g exist (written before the block's copies are
-  // announced; a ring is at most four blocks deep)
+  // valid[g % 16]: which 16-key slices of block g exist (written before the block's copies are
+  // announced; the producer is at most 7 blocks ahead of the softmax)
   volatile uint32_t* valid = reinterpret_cast<volatile uint32_t*>(smem + C::kOffMisc + 8);
   // tag[u % 16] = u + 1 once unit u (of this CTA) has met an infinite or NaN drafted value
-  volatile uint32_t* tag = reinterpret_cast<volatile uint32_t*>(smem + C::kOffMisc + 40);
+  volatile uint32_t* tag = reinterpret_cast<volatile uint32_t*>(smem + C::kOffMisc + 72);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const WaitCtx wc{abort_flag, p.status, p.timeout_ns};
@@ -122,12 +203,20 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
   if (threadIdx.x == 0) {
     mbar_init(bar_q_full, 1);
     mbar_init(bar_q_free, 1);
-    for (int s = 0; s < S; ++s) {
-      mbar_init(bar_k_full(s), kF8 ? 4 : 1);
-      mbar_init(bar_v_full(s), kF8 ? 4 : 1);
+    mbar_init(bar_q8_full, 4);
+    for (int s = 0; s < RK; ++s) {
+      mbar_init(bar_k_full(s), 1);
       mbar_init(bar_k_free(s), 1);
-      mbar_init(bar_v_free(s), 1);
+      mbar_init(bar_k_ready(s), 1);
+    }
+    for (int s = 0; s < RV; ++s) {
+      mbar_init(bar_v_full(s), 1);
+      mbar_init(bar_v_free(s), kF8 ? 4 : 1);
       mbar_init(bar_v_fixed(s), 1);
+    }
+    for (int s = 0; s < NW; ++s) {
+      mbar_init(bar_w_full(s), 4);
+      mbar_init(bar_w_free(s), 1);
     }
     for (int b = 0; b < NB; ++b) {
       mbar_init(bar_s_full(b), 1);
@@ -136,12 +225,7 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
     }
     mbar_init(bar_drain(0), 1);
     mbar_init(bar_drain(1), 1);
-    for (int s = 0; s < C::kRaw; ++s) {
-      mbar_init(bar_raw(0, s), 1);
-      mbar_init(bar_raw(1, s), 1);
-      mbar_init(bar_raw(2, s), 4);
-      mbar_init(bar_raw(3, s), 4);
-    }
+    for (int i = 0; i < kTilePieces; ++i) mbar_init(bar_piece(i), 1);
     *abort_flag = 0u;
     for (int i = 0; i < kTileTags; ++i) tag[i] = 0u;
     fence_mbar_init();
@@ -165,12 +249,20 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
   const long long x0 = per * cta + min(static_cast<long long>(cta), extra);
   const long long x1 = x0 + per + (cta < extra ? 1 : 0);
 
-  // Every role walks the same pieces; g counts their blocks, u the pieces themselves.
+  // Every role walks the same pieces; g counts their blocks, u the pieces themselves.  The
+  // producer finds them (a search and a few global loads) and announces them to the others.
+  auto job_at = [&](int u) { return reinterpret_cast<TileJob*>(smem + C::kOffPieces + (u % kTilePieces) * 48); };
+  // Waits for piece u; false at the end of the list, or (ok = false too) when the wait ran out.
+  auto job = [&](int u, TileJob& t, bool& ok, uint32_t site) {
+    ok = mbar_wait(bar_piece(u % kTilePieces), (u / kTilePieces) & 1, wc, site);
+    if (!ok) return false;
+    t = *job_at(u);
+    return t.ch1 > t.ch0;
+  };
   if (warp == kTileWarpTma) {
     // ================================================================ producer
     if constexpr (kF8) setmaxnreg_dec<kTileRegsOther>();
     const uint64_t pol = policy_evict_first();
-    constexpr int kRing = kF8 ? R : S;
     const int box16 = p.box_rows / 16;  // slices a box holds
     int g = 0, u = 0;
     uint32_t k_live = 0, k_par = 0, v_live = 0, v_par = 0;
@@ -179,15 +271,22 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
       const TreePiece pc = tree_piece<kTileRows, kTileKeys>(p, gs, pre, x, x1);
       x += pc.adv;
       if (pc.ch1 <= pc.ch0) continue;
-      if (u > 0) ok = mbar_wait(bar_q_free, (u - 1) & 1, wc, 33);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
       if (lane == 0) {
-        mbar_arrive_expect_tx(bar_q_full, C::kSub * p.tok_tile * p.G * 128);
-        for (int s = 0; s < C::kSub; ++s)
-          tma_load_4d(sQ + s * C::kSubBytes, &tmQ, bar_q_full, s * 64, 0, pc.h, pc.s.q0 + pc.tile * p.tok_tile, pol);
+        TileJob t = {};
+        t.q0 = pc.s.q0;
+        t.T = pc.s.T;
+        t.ctx = pc.s.ctx;
+        t.n = pc.s.n;
+        t.b = pc.b;
+        t.h = pc.h;
+        t.tile = pc.tile;
+        t.nch = pc.s.nch;
+        t.ch0 = pc.ch0;
+        t.ch1 = pc.ch1;
+        t.owner = tree_owner(x + (pc.s.nch - pc.ch1) - 1, per, extra);
+        *job_at(u) = t;
+        mbar_arrive(bar_piece(u % kTilePieces));
       }
-      ++u;
       // lane i < 8 looks after slice i of a block; its page is fetched a block ahead
       auto page_of = [&](int j) {
         const long long pos = static_cast<long long>(j) * kTileKeys + 16 * lane;
@@ -205,33 +304,30 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
         const int row = static_cast<int>((static_cast<uint32_t>(j) * kTileKeys + 16u * lane) % static_cast<uint32_t>(p.page));
         const bool mine = have && lane < 8 && lane % box16 == 0;
         const int boxes = __popc(__ballot_sync(0xffffffffu, mine));
-        const int st = g % kRing;
-        const uint32_t ph = (g / kRing) & 1, bit = 1u << st;
-        const uint32_t kfree = kF8 ? bar_raw(2, st) : bar_k_free(st), vfree = kF8 ? bar_raw(3, st) : bar_v_free(st);
-        const uint32_t kfull = kF8 ? bar_raw(0, st) : bar_k_full(st), vfull = kF8 ? bar_raw(1, st) : bar_v_full(st);
         constexpr int kRowB = kF8 ? D : 128;                 // bytes of a row of a (sub-)tile
         constexpr int kSubs = kF8 ? 1 : C::kSub;
-        const uint32_t kdst = kF8 ? sbase + C::kOffRaw + st * 2 * C::kRawBytes : sK + st * C::kTileBytes;
-        const uint32_t vdst = kF8 ? kdst + C::kRawBytes : sV + st * C::kTileBytes;
         const uint32_t bytes = boxes * p.box_rows * (kSubs * kRowB + (kF8 ? 1 : 0));
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv) {
-          ok = __all_sync(0xffffffffu, mbar_wait(kv ? vfree : kfree, ph ^ 1, wc, 34 + kv));
+          const int st = kv ? g % RV : g % RK;
+          const uint32_t ph = ((kv ? g / RV : g / RK)) & 1, bit = 1u << st;
+          ok = __all_sync(0xffffffffu, mbar_wait(kv ? bar_v_free(st) : bar_k_free(st), ph ^ 1, wc, 34 + kv));
           if (!ok) break;
-          const uint32_t full = kv ? vfull : kfull;
+          const uint32_t full = kv ? bar_v_full(st) : bar_k_full(st);
           if (lane == 0) {
-            if (kv == 0) valid[g & 7] = vm;
+            if (kv == 0) valid[g & 15] = vm;
             mbar_arrive_expect_tx(full, bytes);
           }
           __syncwarp();
           if (mine) {
-            const uint32_t dst = (kv ? vdst : kdst) + 16 * lane * kRowB;
+            const uint32_t dst = (kv ? sV + st * C::kStageV : sK + st * C::kStageK) + 16 * lane * kRowB;
 #pragma unroll
             for (int s = 0; s < kSubs; ++s)
               tma_load_4d(dst + s * C::kSubBytes, kv ? &tmV : &tmK, full, s * 64, row, pc.h, pg, pol);
             if constexpr (kF8) {
               const long long r = (static_cast<long long>(pg) * p.Hkv + pc.h) * p.page + row;
-              bulk_load(sbase + C::kOffScale + st * 256 + kv * 128 + 16 * lane, (kv ? p.vs : p.ks) + r, p.box_rows, full);
+              bulk_load(sbase + (kv ? C::kOffCodeV : C::kOffCodeK) + st * 128 + 16 * lane, (kv ? p.vs : p.ks) + r,
+                        p.box_rows, full);
             }
           }
           if (kv == 0) {
@@ -242,16 +338,33 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
             v_par = (v_par & ~bit) | (ph << st);
           }
         }
+        // Q after the piece's first block, whose stages depend on earlier blocks only: its K and
+        // V are on their way while the last piece's products still read the old Q
+        if (ok && j == pc.ch0) {
+          if (u > 0) ok = __all_sync(0xffffffffu, mbar_wait(bar_q_free, (u - 1) & 1, wc, 33));
+          if (ok && lane == 0) {
+            mbar_arrive_expect_tx(bar_q_full, C::kSub * p.tok_tile * p.G * 128);
+            for (int s = 0; s < C::kSub; ++s)
+              tma_load_4d(sQ + s * C::kSubBytes, &tmQ, bar_q_full, s * 64, 0, pc.h, pc.s.q0 + pc.tile * p.tok_tile, pol);
+          }
+          if (ok) ++u;
+        }
         if (!ok) break;
       }
+    }
+    if (ok && lane == 0) {  // the end of the list
+      job_at(u)->ch0 = 0;
+      job_at(u)->ch1 = 0;
+      mbar_arrive(bar_piece(u % kTilePieces));
     }
     // let the copies in flight land before this warp leaves
     if (lane == 0) {
 #pragma unroll
-      for (int s = 0; s < kRing; ++s) {
-        if ((k_live >> s) & 1u) mbar_wait_drain(kF8 ? bar_raw(0, s) : bar_k_full(s), (k_par >> s) & 1u, p.timeout_ns);
-        if ((v_live >> s) & 1u) mbar_wait_drain(kF8 ? bar_raw(1, s) : bar_v_full(s), (v_par >> s) & 1u, p.timeout_ns);
-      }
+      for (int s = 0; s < RK; ++s)
+        if ((k_live >> s) & 1u) mbar_wait_drain(bar_k_full(s), (k_par >> s) & 1u, p.timeout_ns);
+#pragma unroll
+      for (int s = 0; s < RV; ++s)
+        if ((v_live >> s) & 1u) mbar_wait_drain(bar_v_full(s), (v_par >> s) & 1u, p.timeout_ns);
       if (u > 0) mbar_wait_drain(bar_q_full, (u - 1) & 1, p.timeout_ns);
     }
   } else if (warp == kTileWarpPv || warp == kTileWarpS) {
@@ -262,27 +375,37 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
       int g = 0, u = 0;
       bool ok = true;
       uint32_t fixed_par = 0;  // parity each v_fixed completes next
-      for (long long x = x0; ok && x < x1;) {
-        const TreePiece pc = tree_piece<kTileRows, kTileKeys>(p, gs, pre, x, x1);
-        x += pc.adv;
-        if (pc.ch1 <= pc.ch0) continue;
+      TileJob pc;
+      while (job(u, pc, ok, 50)) {
         if (warp == kTileWarpS) {
-          const uint32_t qlo = (sQ >> 4) | (1u << 16);
+          const uint32_t qlo = ((kF8 ? sbase + C::kOffQ8 : sQ) >> 4) | (1u << 16);
           const uint32_t klo = (sK >> 4) | (1u << 16);
-          ok = mbar_wait(bar_q_full, u & 1, wc, 36);
+          // e4m3 rows of 64 bytes: 64-byte swizzle, eight rows 512 bytes apart
+          const uint32_t dhi8 = D == 128 ? dhi : (512u >> 4) | (1u << 14) | (4u << 29);
+          ok = mbar_wait(kF8 ? bar_q8_full : bar_q_full, u & 1, wc, 36);
           for (int j = pc.ch0; ok && j < pc.ch1; ++j, ++g) {
-            const int st = g % S, bf = g % NB;
+            const int st = g % RK, bf = g % NB;
             if (g >= NB) ok = mbar_wait(bar_pv_done(bf), ((g - NB) / NB) & 1, wc, 37);
-            ok = ok && mbar_wait(bar_k_full(st), (g / S) & 1, wc, 38);
+            ok = ok && mbar_wait(kF8 ? bar_k_ready(st) : bar_k_full(st), (g / RK) & 1, wc, 38);
             if (!ok) break;
             tc_fence_after();
-            const uint32_t blo = klo + st * (C::kTileBytes >> 4);
+            const uint32_t blo = klo + st * (C::kStageK >> 4);
             const uint32_t dst = tmem + C::col_s(bf);
+            if constexpr (kF8) {
 #pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks) {
-              const uint32_t off = (ks / 4) * (C::kSubBytes >> 4) + (ks % 4) * 2;
-              mma_ss(dst, (static_cast<uint64_t>(dhi) << 32) | (qlo + off),
-                     (static_cast<uint64_t>(dhi) << 32) | (blo + off), C::kIdescS, ks > 0 ? 1u : 0u);
+              for (int part = 0; part < 2; ++part)  // hi, lo
+#pragma unroll
+                for (int ks = 0; ks < D / 32; ++ks)
+                  mma_ss_f8(dst, (static_cast<uint64_t>(dhi8) << 32) | (qlo + part * (C::kRawBytes >> 4) + ks * 2),
+                            (static_cast<uint64_t>(dhi8) << 32) | (blo + ks * 2), C::kIdescS8,
+                            part + ks > 0 ? 1u : 0u);
+            } else {
+#pragma unroll
+              for (int ks = 0; ks < D / 16; ++ks) {
+                const uint32_t off = (ks / 4) * (C::kSubBytes >> 4) + (ks % 4) * 2;
+                mma_ss(dst, (static_cast<uint64_t>(dhi) << 32) | (qlo + off),
+                       (static_cast<uint64_t>(dhi) << 32) | (blo + off), C::kIdescS, ks > 0 ? 1u : 0u);
+              }
             }
             mma_commit(bar_s_full(bf));
             mma_commit(bar_k_free(st));
@@ -290,11 +413,11 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
           if (!ok) break;
           mma_commit(bar_q_free);
         } else {
-          const uint32_t vlo = (sV >> 4) | (static_cast<uint32_t>(C::kSubBytes >> 4) << 16);
+          const uint32_t vlo = ((kF8 ? sbase + C::kOffWide : sV) >> 4) | (static_cast<uint32_t>(C::kSubBytes >> 4) << 16);
           for (int j = pc.ch0; ok && j < pc.ch1; ++j, ++g) {
-            const int st = g % S;
-            ok = mbar_wait(bar_v_full(st), (g / S) & 1, wc, 39);
-            if (!kF8 && ok && (static_cast<long long>(j + 1) * kTileKeys > pc.s.ctx || valid[g & 7] != 0xffu)) {
+            const int st = kF8 ? g % NWm : g % RV;
+            ok = kF8 ? mbar_wait(bar_w_full(st), (g / NWm) & 1, wc, 39) : mbar_wait(bar_v_full(st), (g / RV) & 1, wc, 39);
+            if (!kF8 && ok && (static_cast<long long>(j + 1) * kTileKeys > pc.ctx || valid[g & 15] != 0xffu)) {
               ok = mbar_wait(bar_v_fixed(st), (fixed_par >> st) & 1u, wc, 40);
               fixed_par ^= 1u << st;
             }
@@ -308,8 +431,9 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
               mma_ts(tmem + C::kColO, a + ks * 8, (static_cast<uint64_t>(dhi) << 32) | (blo + ks * (16 * 128 >> 4)),
                      C::kIdescO, (j > pc.ch0 || ks > 0) ? 1u : 0u);
             mma_commit(bar_pv_done(g % NB));
-            mma_commit(bar_v_free(st));
+            mma_commit(kF8 ? bar_w_free(st) : bar_v_free(st));
           }
+          if (!ok) break;
         }
         ++u;
       }
@@ -319,25 +443,44 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
   } else if (warp == kTileWarpFix) {
     // ================================================================ ragged blocks of V (bf16)
     if constexpr (kF8) {
-      setmaxnreg_dec<kTileRegsOther>();  // the warp without a role completes its warpgroup
+      // ---- scales of K's keys as floats, four a lane.  Entry g % 8: block g's stage was freed
+      // by S of block g - 4, which is at most 3 blocks ahead of the softmax.
+      setmaxnreg_dec<kTileRegsOther>();
+      int g = 0, u = 0;
+      bool ok = true;
+      TileJob pc;
+      while (job(u, pc, ok, 51)) {
+        ++u;
+        for (int j = pc.ch0; j < pc.ch1; ++j, ++g) {
+          const int st = g % RK;
+          ok = __all_sync(0xffffffffu, mbar_wait(bar_k_full(st), (g / RK) & 1, wc, 44));
+          if (!ok) break;
+          const uint32_t w = *reinterpret_cast<const volatile uint32_t*>(smem + C::kOffCodeK + st * 128 + lane * 4);
+          // at least 2^-126: a masked score, -inf, must stay that whatever the code beside it
+          reinterpret_cast<float4*>(smem + C::kOffScaleK)[(g & 7) * 32 + lane] =
+              make_float4(scale_of(max(w & 0xffu, 1u)), scale_of(max((w >> 8) & 0xffu, 1u)),
+                          scale_of(max((w >> 16) & 0xffu, 1u)), scale_of(max(w >> 24, 1u)));
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar_k_ready(st));
+        }
+        if (!ok) break;
+      }
     } else {
       int g = 0, u = 0;
       bool ok = true;
-      for (long long x = x0; ok && x < x1;) {
-        const TreePiece pc = tree_piece<kTileRows, kTileKeys>(p, gs, pre, x, x1);
-        x += pc.adv;
-        if (pc.ch1 <= pc.ch0) continue;
+      TileJob pc;
+      while (job(u, pc, ok, 52)) {
         for (int j = pc.ch0; j < pc.ch1; ++j, ++g) {
-          const int st = g % S, kb = j * kTileKeys;
-          ok = __all_sync(0xffffffffu, mbar_wait(bar_v_full(st), (g / S) & 1, wc, 42));
+          const int st = g % RV, kb = j * kTileKeys;
+          ok = __all_sync(0xffffffffu, mbar_wait(bar_v_full(st), (g / RV) & 1, wc, 42));
           if (!ok) break;
-          const uint32_t vm = valid[g & 7];
-          if (static_cast<long long>(kb) + kTileKeys <= pc.s.ctx && vm == 0xffu) continue;
+          const uint32_t vm = valid[g & 15];
+          if (static_cast<long long>(kb) + kTileKeys <= pc.ctx && vm == 0xffu) continue;
           bool odd = false;
           for (int i = lane; i < kTileKeys * (D / 8); i += 32) {
             const int r = i / (D / 8), ch = i % (D / 8);
-            const bool here = ((vm >> (r / 16)) & 1u) && kb + r < pc.s.n;
-            if (here && kb + r < pc.s.ctx) continue;
+            const bool here = ((vm >> (r / 16)) & 1u) && kb + r < pc.n;
+            if (here && kb + r < pc.ctx) continue;
             uint4* at = reinterpret_cast<uint4*>(smem + C::kOffV + st * C::kTileBytes + (ch / 8) * C::kSubBytes + r * 128 +
                                                  (((ch & 7) ^ (r & 7)) << 4));
             if (!here) {
@@ -355,67 +498,112 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(bar_v_fixed(st));
         }
+        if (!ok) break;
         ++u;
       }
     }
   } else if (kF8 && warp >= 8) {
     // ================================================================ e4m3 -> bf16
     if constexpr (kF8) {
-      const int r = threadIdx.x - 256;  // key of the block
+      // Loops over a row's chunks stay rolled: this role's code next to the softmax's overflows
+      // the instruction cache when unrolled (measured on GB300, one sequence of 131072 tokens,
+      // d = 128: 144 us with 8 chunks unrolled, a third of the stalls for want of instructions).
+      const int r = threadIdx.x - 256;  // row of Q, key of a block
       int g = 0, u = 0;
       bool ok = true;
-      for (long long x = x0; ok && x < x1;) {
-        const TreePiece pc = tree_piece<kTileRows, kTileKeys>(p, gs, pre, x, x1);
-        x += pc.adv;
-        if (pc.ch1 <= pc.ch0) continue;
-        for (int j = pc.ch0; ok && j < pc.ch1; ++j, ++g) {
-          const int st = g % S, rs = g % R, kb = j * kTileKeys;
+      TileJob pc;
+      while (job(u, pc, ok, 53)) {
+        // ---- Q: a row's largest value, then hi and lo over it
+        ok = __all_sync(0xffffffffu, mbar_wait(bar_q_full, u & 1, wc, 43));
+        if (!ok) break;
+        auto q_at = [&](int c) {
+          return *reinterpret_cast<const uint4*>(smem + C::kOffQ + (c / 8) * C::kSubBytes + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+        };
+        uint32_t mx = 0;
+        bool fine = true;
+#pragma unroll 2
+        for (int c = 0; c < D / 8; ++c) {
+          const uint4 q = q_at(c);
+          mx = max(mx, finite_max(q));
+          fine = fine && !any_nonfinite(q.x) && !any_nonfinite(q.y) && !any_nonfinite(q.z) && !any_nonfinite(q.w);
+        }
+        const uint32_t ef = min(max(mx >> 7, 8u), 253u);  // exponent field of the row's largest value
+        const float up = __uint_as_float((261u - ef) << 23);  // 2^(7 - (ef - 127))
+        // a row that is not finite has scores that are not
+        reinterpret_cast<float*>(smem + C::kOffScaleQ)[(u & 7) * 128 + r] =
+            fine ? p.c * __uint_as_float((ef - 7u) << 23) : __uint_as_float(0x7fffffffu);
+        // Chunk c of hi and of lo (16 columns) from chunks 2 c, 2 c + 1 of bf16.  At d = 128 the
+        // terms lie over the row itself, hi over its columns 0 - 63, lo over 64 - 127, each in
+        // the order its chunks are swizzled, so all of it is read before any is written.
+        uint4 q[D / 8];
 #pragma unroll
-          for (int kv = 0; kv < 2; ++kv) {
-            ok = mbar_wait(bar_raw(kv, rs), (g / R) & 1, wc, 43 + kv) &&
-                 mbar_wait(kv ? bar_v_free(st) : bar_k_free(st), ((g / S) & 1) ^ 1, wc, 45 + kv);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            const uint32_t vm = valid[g & 7];
-            const bool here = ((vm >> (r / 16)) & 1u) && kb + r < pc.s.n;
-            const bool scan = kv && kb + r >= pc.s.ctx;
-            const uint8_t* src = smem + C::kOffRaw + rs * 2 * C::kRawBytes + kv * C::kRawBytes + r * D;
-            uint8_t* dst = smem + (kv ? C::kOffV : C::kOffK) + st * C::kTileBytes + r * 128;
-            const uint32_t code = smem[C::kOffScale + rs * 256 + kv * 128 + r];
-            const uint32_t two = (code << 7) | (code << 23);  // 2^(code - 127) twice, as bf16
-            const __nv_bfloat162 scale = *reinterpret_cast<const __nv_bfloat162*>(&two);
-            bool odd = false;
+        for (int c = 0; c < D / 8; ++c) q[c] = q_at(c);
 #pragma unroll
-            for (int c = 0; c < D / 16; ++c) {
-              const int sw = D == 128 ? c ^ (r & 7) : c ^ ((r >> 1) & 3);
-              const uint4 raw = *reinterpret_cast<const uint4*>(src + (sw << 4));
-              uint4 a = widen8(raw.x, raw.y, scale), b = widen8(raw.z, raw.w, scale);
-              if (!here) {
-                a = make_uint4(0, 0, 0, 0);
-                b = make_uint4(0, 0, 0, 0);
-              } else if (scan) {
-                if (any_nonfinite(a.x) || any_nonfinite(a.y) || any_nonfinite(a.z) || any_nonfinite(a.w) ||
-                    any_nonfinite(b.x) || any_nonfinite(b.y) || any_nonfinite(b.z) || any_nonfinite(b.w)) {
-                  odd = true;
-                  a = make_uint4(finite_only(a.x), finite_only(a.y), finite_only(a.z), finite_only(a.w));
-                  b = make_uint4(finite_only(b.x), finite_only(b.y), finite_only(b.z), finite_only(b.w));
-                }
+        for (int c = 0; c < D / 16; ++c) {
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {  // four values each
+            const uint32_t w0 = (&q[2 * c + i / 2].x)[(i & 1) * 2], w1 = (&q[2 * c + i / 2].x)[(i & 1) * 2 + 1];
+            const float f0 = bf16_lo(w0) * up, f1 = bf16_hi(w0) * up, f2 = bf16_lo(w1) * up, f3 = bf16_hi(w1) * up;
+            const uint32_t h0 = pack_e4m3x2(f0, f1), h1 = pack_e4m3x2(f2, f3);
+            const float2 b0 = e4m3x2_to_f32(h0), b1 = e4m3x2_to_f32(h1);
+            hi[i] = h0 | (h1 << 16);
+            lo[i] = pack_e4m3x2(f0 - b0.x, f1 - b0.y) | (pack_e4m3x2(f2 - b1.x, f3 - b1.y) << 16);
+          }
+          const int sw = D == 128 ? c ^ (r & 7) : c ^ ((r >> 1) & 3);
+          uint8_t* to = smem + C::kOffQ8 + r * D + (sw << 4);
+          *reinterpret_cast<uint4*>(to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *reinterpret_cast<uint4*>(to + C::kRawBytes) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_q8_full);
+        for (int j = pc.ch0; j < pc.ch1; ++j, ++g) {
+          const int sv = g % RV, sw = g % NWm, kb = j * kTileKeys;
+          // ---- V: codes times scale as bf16
+          ok = mbar_wait(bar_v_full(sv), (g / RV) & 1, wc, 45) && mbar_wait(bar_w_free(sw), ((g / NWm) & 1) ^ 1, wc, 46);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          const uint32_t vm = valid[g & 15];
+          const bool here = ((vm >> (r / 16)) & 1u) && kb + r < pc.n;
+          const bool scan = kb + r >= pc.ctx;
+          const uint8_t* src = smem + C::kOffV + sv * C::kStageV + r * D;
+          uint8_t* dst = smem + C::kOffWide + sw * C::kTileBytes + r * 128;
+          const uint32_t code = here ? smem[C::kOffCodeV + sv * 128 + r] : 0u;
+          const uint32_t two = (code << 7) | (code << 23);  // 2^(code - 127) twice, as bf16
+          const __nv_bfloat162 scale = *reinterpret_cast<const __nv_bfloat162*>(&two);
+          const bool ragged = __any_sync(0xffffffffu, !here || scan);
+          bool odd = false;
+#pragma unroll 2
+          for (int c = 0; c < D / 16; ++c) {
+            const uint4 raw = *reinterpret_cast<const uint4*>(src + ((D == 128 ? c ^ (r & 7) : c ^ ((r >> 1) & 3)) << 4));
+            uint4 a = widen8(raw.x, raw.y, scale), b = widen8(raw.z, raw.w, scale);
+            if (ragged) {
+              // rows that do not exist, and (remembered) what is not finite among the drafted, become 0
+              uint32_t* w[2] = {&a.x, &b.x};
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                uint32_t& e = w[i >> 2][i & 3];
+                if (here && scan && any_nonfinite(e)) odd = true;
+                if (!here) e = 0u;
+                if (scan) e = finite_only(e);
               }
-              // 16 columns = chunks 2 c, 2 c + 1 of the bf16 row, in sub-tile c / 4
-              uint8_t* to = dst + (c / 4) * C::kSubBytes;
-              const int ch = (2 * c) & 7;
-              *reinterpret_cast<uint4*>(to + ((ch ^ (r & 7)) << 4)) = a;
-              *reinterpret_cast<uint4*>(to + (((ch + 1) ^ (r & 7)) << 4)) = b;
             }
-            if (odd) tag[u % kTileTags] = u + 1;
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              mbar_arrive(kv ? bar_v_full(st) : bar_k_full(st));
-              mbar_arrive(bar_raw(2 + kv, rs));
-            }
+            // 16 columns = chunks 2 c, 2 c + 1 of the bf16 row, in sub-tile c / 4
+            uint8_t* to = dst + (c / 4) * C::kSubBytes;
+            const int ch = (2 * c) & 7;
+            *reinterpret_cast<uint4*>(to + ((ch ^ (r & 7)) << 4)) = a;
+            *reinterpret_cast<uint4*>(to + (((ch + 1) ^ (r & 7)) << 4)) = b;
+          }
+          if (odd) tag[u % kTileTags] = u + 1;
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(bar_w_full(sw));
+            mbar_arrive(bar_v_free(sv));
           }
         }
+        if (!ok) break;
         ++u;
       }
     }
@@ -424,28 +612,68 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
     if constexpr (kF8) setmaxnreg_inc<kTileRegsSoftmax>();
     const int r = threadIdx.x;
     const uint32_t tl = tmem + (static_cast<uint32_t>(warp * 32) << 16);
-    const float c = p.c;
+    float c = p.c;  // e4m3: times the row's power of two, piece by piece
     constexpr float kTau = 8.f;  // o~ is rescaled when the max rises by more (log2 units)
     int g = 0, u = 0;
     bool ok = true, has_tail = false;
-    for (long long x = x0; ok && x < x1;) {
-      const TreePiece pc = tree_piece<kTileRows, kTileKeys>(p, gs, pre, x, x1);
-      x += pc.adv;
-      if (pc.ch1 <= pc.ch0) continue;
-      int tok, head;
-      const bool row_here = tree_row<kTileRows>(p, pc.s, pc.tile, r, &tok, &head);
-      const unsigned long long sees = row_here ? tree_sees(p, pc.s, tok) : 0ull;
+    // The next piece and this thread's row of it are looked up while the last product of the
+    // piece in hand runs.
+    TileJob pc;
+    int tok = 0, head = 0;
+    bool row_here = false;
+    unsigned long long sees = 0;
+    auto look = [&](int v) {
+      if (!job(v, pc, ok, 54)) return false;
+      const int t = r / p.G;
+      head = r - t * p.G;
+      tok = pc.tile * p.tok_tile + t;
+      row_here = tok < pc.T && t < p.tok_tile;
+      TreeSeq sq;
+      sq.q0 = pc.q0;
+      sq.T = pc.T;
+      sees = row_here ? tree_sees(p, sq, tok) : 0ull;
+      return true;
+    };
+    bool more = look(0);
+    while (__all_sync(0xffffffffu, ok && more)) {
       const bool idle = !__any_sync(0xffffffffu, row_here);  // no row of this warp exists
+      bool s_seen = false, pv_seen = false;  // barriers of the next block, and of the last one, tested early
       float m = -INFINITY, l = 0.f;
       for (int j = pc.ch0; j < pc.ch1; ++j, ++g) {
         const uint32_t colS = C::col_s(g % NB);
-        ok = __all_sync(0xffffffffu, mbar_wait(bar_s_full(g % NB), (g / NB) & 1, wc, 47));
+        if (!__all_sync(0xffffffffu, s_seen))
+          ok = __all_sync(0xffffffffu, mbar_wait(bar_s_full(g % NB), (g / NB) & 1, wc, 47));
         if (!ok) break;
+        s_seen = false;
+        const float4* ks = reinterpret_cast<const float4*>(smem + C::kOffScaleK + (g & 7) * 512);
+        if (kF8 && j == pc.ch0) c = reinterpret_cast<const volatile float*>(smem + C::kOffScaleQ)[(u & 7) * 128 + r];
         if (idle) {  // its lanes of P hold scores: rows nobody reads
           if (lane == 0) mbar_arrive(bar_p_full(g % NB));
           continue;
         }
         tc_fence_after();
+        const int kb = j * kTileKeys;
+        const uint32_t vm = valid[g & 15];
+        if (static_cast<long long>(kb) + kTileKeys > pc.ctx || vm != 0xffu) {
+          // a ragged block: the scores of keys this row does not see become -inf where they lie
+          const int off = pc.ctx - kb;  // context keys of the block; the drafted ones follow
+#pragma unroll 1
+          for (int w = 0; w < 4; ++w) {
+            const int o = off - 32 * w;
+            uint32_t see = o >= 32 ? 0xffffffffu : o <= 0 ? 0u : (1u << o) - 1u;
+            if (o < 32 && o > -64) see |= static_cast<uint32_t>(o >= 0 ? sees << o : sees >> -o);
+            if (!((vm >> (2 * w)) & 1u)) see &= 0xffff0000u;
+            if (!((vm >> (2 * w + 1)) & 1u)) see &= 0x0000ffffu;
+            uint32_t e[32];
+            tmem_ld32(tl + colS + 32 * w, e);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              if (!((see >> k) & 1u)) e[k] = 0xff800000u;
+            tmem_st32(tl + colS + 32 * w, e);
+          }
+          tmem_wait_st();
+        }
         float s[kTileKeys];
         {
           uint32_t sr[kTileKeys];
@@ -455,20 +683,16 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
 #pragma unroll
           for (int k = 0; k < kTileKeys; ++k) s[k] = __uint_as_float(sr[k]);
         }
-        const int kb = j * kTileKeys;
-        const uint32_t vm = valid[g & 7];
-        if (static_cast<long long>(kb) + kTileKeys > pc.s.ctx || vm != 0xffu) {
-          const int off = pc.s.ctx - kb;  // context keys of the block; the drafted ones follow
+        if constexpr (kF8) {  // times the keys' scales (a key that is masked may have any: -inf stays)
 #pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            const int o = off - 32 * w;
-            uint32_t see = o >= 32 ? 0xffffffffu : o <= 0 ? 0u : (1u << o) - 1u;
-            if (o < 32 && o > -64) see |= static_cast<uint32_t>(o >= 0 ? sees << o : sees >> -o);
-            if (!((vm >> (2 * w)) & 1u)) see &= 0xffff0000u;
-            if (!((vm >> (2 * w + 1)) & 1u)) see &= 0x0000ffffu;
-#pragma unroll
-            for (int k = 0; k < 32; ++k)
-              if (!((see >> k) & 1u)) s[32 * w + k] = -INFINITY;
+          for (int k = 0; k < kTileKeys / 4; ++k) {
+            const float4 f = ks[k];
+            const float2 a = __fmul2_rn(make_float2(s[4 * k], s[4 * k + 1]), make_float2(f.x, f.y));
+            const float2 b = __fmul2_rn(make_float2(s[4 * k + 2], s[4 * k + 3]), make_float2(f.z, f.w));
+            s[4 * k] = a.x;
+            s[4 * k + 1] = a.y;
+            s[4 * k + 2] = b.x;
+            s[4 * k + 3] = b.y;
           }
         }
         float a[8];
@@ -486,6 +710,10 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
         float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
 #pragma unroll
         for (int q = 0; q < kTileKeys / 32; ++q) {
+          if (q == kTileKeys / 32 - 1) {
+            s_seen = j + 1 < pc.ch1 && mbar_test_wait(bar_s_full((g + 1) % NB), ((g + 1) / NB) & 1);
+            pv_seen = j > pc.ch0 && mbar_test_wait(bar_pv_done((g - 1) % NB), ((g - 1) / NB) & 1);
+          }
           uint32_t pk[16];
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
@@ -506,11 +734,12 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
         const bool moved = m_new != m;
         m = m_new;
         if (j > pc.ch0 && __any_sync(0xffffffffu, moved)) {
-          ok = __all_sync(0xffffffffu, mbar_wait(bar_pv_done((g - 1) % NB), ((g - 1) / NB) & 1, wc, 48));
+          if (!__all_sync(0xffffffffu, pv_seen))
+            ok = __all_sync(0xffffffffu, mbar_wait(bar_pv_done((g - 1) % NB), ((g - 1) / NB) & 1, wc, 48));
           if (!ok) break;
           tc_fence_after();
           const float2 al2 = make_float2(alpha, alpha);
-#pragma unroll
+#pragma unroll 1
           for (int q = 0; q < D / 32; ++q) {
             uint32_t o[32];
             tmem_ld32(tl + C::kColO + q * 32, o);
@@ -530,74 +759,58 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
         if (lane == 0) mbar_arrive(bar_p_full(g % NB));
       }
       if (!ok) break;
+      const bool whole = pc.ch0 == 0 && pc.ch1 == pc.nch;
+      const bool front = pc.ch0 == 0 && !whole;  // goes on in the next CTAs
+      const int hq = pc.h * p.G + head;
+      const long long orow = static_cast<long long>(pc.q0 + tok) * p.Hq + hq;
+      const long long lrow = static_cast<long long>(hq) * p.total_q + pc.q0 + tok;
+      const long long at = static_cast<long long>(2 * cta + (pc.ch0 == 0 ? 1 : 0)) * kTileRows + r;
+      const TileJob done = pc;
+      const bool row_done = row_here;
+      const unsigned long long saw = sees;
+      more = look(u + 1);
       // ---- o~ out: the piece's last P V (and so all of them) has landed
-      ok = __all_sync(0xffffffffu, mbar_wait(bar_pv_done((g - 1) % NB), ((g - 1) / NB) & 1, wc, 49));
+      if (!mbar_wait(bar_pv_done((g - 1) % NB), ((g - 1) / NB) & 1, wc, 49)) ok = false;
+      ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
-      const bool whole = pc.ch0 == 0 && pc.ch1 == pc.s.nch;
       if (!idle) {
-        uint32_t o[D];
+        const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+        const bool odd = tag[u % kTileTags] == static_cast<uint32_t>(u + 1);
+#pragma unroll 1
+        for (int q = 0; q < D / 32; ++q) {
+          uint32_t o[32];
+          tmem_ld32(tl + C::kColO + q * 32, o);
+          tmem_wait_ld();
+          if (odd) tile_add_nonfinite<kF8>(p, done, saw, q * 32, D, o);
+          if (row_done && whole) {
+            uint4* dst = reinterpret_cast<uint4*>(p.o + orow * D + q * 32);
 #pragma unroll
-        for (int q = 0; q < D / 32; ++q) tmem_ld32(tl + C::kColO + q * 32, o + q * 32);
-        tmem_wait_ld();
-        if (tag[u % kTileTags] == static_cast<uint32_t>(u + 1)) {
-          // infinities and NaN among the drafted values of this piece, zero in the product: to
-          // the rows that see them (a positive weight leaves them what they are)
-          for (unsigned long long left = sees; left; left &= left - 1) {
-            const int pos = pc.s.ctx + __ffsll(static_cast<long long>(left)) - 1;
-            if (pos >= pc.s.n || pos < pc.ch0 * kTileKeys || pos - kTileKeys >= (pc.ch1 - 1) * kTileKeys) continue;
-            const int pg = __ldg(p.table + static_cast<long long>(pc.b) * p.max_pages + pos / p.page);
-            if (static_cast<unsigned>(pg) >= static_cast<unsigned>(p.num_pages)) continue;
-            const long long at = (static_cast<long long>(pg) * p.Hkv + pc.h) * p.page + pos % p.page;
-#pragma unroll
-            for (int k = 0; k < D / 2; ++k) {
-              uint32_t w;
-              if constexpr (kF8) {
-                const uint32_t two = (static_cast<uint32_t>(__ldg(p.vs + at)) << 7) | (static_cast<uint32_t>(__ldg(p.vs + at)) << 23);
-                const uint32_t cw = e4m3x2_to_bf16x2(__ldg(reinterpret_cast<const uint16_t*>(static_cast<const uint8_t*>(p.v) + at * D) + k));
-                const __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&cw), *reinterpret_cast<const __nv_bfloat162*>(&two));
-                w = *reinterpret_cast<const uint32_t*>(&v);
-              } else {
-                w = __ldg(reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(p.v) + at * D) + k);
-              }
-              if (!isfinite(bf16_lo(w))) o[2 * k] = __float_as_uint(__uint_as_float(o[2 * k]) + bf16_lo(w));
-              if (!isfinite(bf16_hi(w))) o[2 * k + 1] = __float_as_uint(__uint_as_float(o[2 * k + 1]) + bf16_hi(w));
-            }
-          }
-        }
-        if (row_here) {
-          if (whole) {
-            const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-            const int hq = pc.h * p.G + head;
-            uint4* dst = reinterpret_cast<uint4*>(p.o + (static_cast<long long>(pc.s.q0 + tok) * p.Hq + hq) * D);
-#pragma unroll
-            for (int k = 0; k < D / 8; ++k) {
+            for (int k = 0; k < 4; ++k) {
               uint32_t w[4];
 #pragma unroll
               for (int i = 0; i < 4; ++i)
                 w[i] = pack_bf16x2(__uint_as_float(o[8 * k + 2 * i]) * inv, __uint_as_float(o[8 * k + 2 * i + 1]) * inv);
               dst[k] = make_uint4(w[0], w[1], w[2], w[3]);
             }
-            p.lse[static_cast<long long>(hq) * p.total_q + pc.s.q0 + tok] =
-                l > 0.f || l != l ? m * 0.69314718055994531f + logf(l) : -INFINITY;
-          } else {
-            const long long at = static_cast<long long>(2 * cta + (pc.ch0 == 0 ? 1 : 0)) * kTileRows + r;
-            float4* dst = reinterpret_cast<float4*>(p.st_o + at * D);
+          } else if (row_done) {
+            uint4* dst = reinterpret_cast<uint4*>(p.st_o + at * D + q * 32);
 #pragma unroll
-            for (int k = 0; k < D / 4; ++k)
-              dst[k] = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
-                                   __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
-            p.st_m[at] = m;
-            p.st_l[at] = l;
+            for (int k = 0; k < 8; ++k) dst[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
           }
+        }
+        if (row_done && whole) {
+          p.lse[lrow] = l > 0.f || l != l ? m * 0.69314718055994531f + logf(l) : -INFINITY;
+        } else if (row_done) {
+          p.st_m[at] = m;
+          p.st_l[at] = l;
         }
       }
       // o~ has been read out: the next piece's first P V comes after this thread's next arrival
       tc_fence_before();
-      if (pc.ch0 == 0 && pc.ch1 < pc.s.nch) {
+      if (front) {
         has_tail = true;
-        if (r == 0)
-          p.meta[cta] = make_int4(pc.b, pc.h, pc.tile, tree_owner(x + (pc.s.nch - pc.ch1) - 1, per, extra));
+        if (r == 0) p.meta[cta] = make_int4(done.b, done.h, done.tile, done.owner);
       }
       ++u;
     }
