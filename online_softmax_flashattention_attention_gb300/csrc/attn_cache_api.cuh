@@ -126,7 +126,7 @@ attn_status cache_map(CUtensorMap* map, const void* ptr, const attn_cache* c, in
 
 // Workspace of attn_fwd_tree: room for this many CTAs (two an SM, SMs up to this), whatever
 // the device has, so that its size follows from the arguments alone.
-constexpr int kTreeMaxCtas = 320;
+constexpr int kTreeMaxCtas = 480;
 constexpr int kTileMaxCtas = 160;
 
 // Whether a call takes the 128-row tiles.
@@ -173,10 +173,10 @@ attn_status launch_tree(const attn_cache* c, attn::TreeParams p, void* ws, cudaS
   if ((st = set_smem_attr(kernel, C::kSmem, dev, attr_set)) != ATTN_OK) return st;
   CUtensorMap mk = {}, mv = {};
   if (c->num_pages > 0) {  // without pages nothing is loaded
-    if ((st = cache_map(&mk, c->k, c, attn::kTreeSlice)) != ATTN_OK) return st;
-    if ((st = cache_map(&mv, c->v, c, attn::kTreeSlice)) != ATTN_OK) return st;
+    if ((st = cache_map(&mk, c->k, c, 16)) != ATTN_OK) return st;
+    if ((st = cache_map(&mv, c->v, c, 16)) != ATTN_OK) return st;
   }
-  const unsigned grid = static_cast<unsigned>(std::min(kTreeMaxCtas, 2 * sm_count(dev)));
+  const unsigned grid = static_cast<unsigned>(std::min(kTreeMaxCtas, C::kCtas * sm_count(dev)));
   const TreeSpace sp = tree_space(attn::kTreeRows, kTreeMaxCtas, D);
   uint8_t* w = static_cast<uint8_t*>(ws);
   p.st_o = reinterpret_cast<float*>(w + sp.o);

@@ -9,15 +9,23 @@
 // Bound: K and V are read once, 4 d (bf16) or 2 d + 2 (e4m3) bytes a key, for 4 d flops a row
 // and key; below 274 rows a unit memory is the limit.
 //
-// Work split: the keys of all units are laid end to end in chunks of 64 (and some places for
-// what a unit costs beside them, see tree_plan) and cut into equal ranges, one a CTA (two CTAs an SM), whatever the lengths are; every CTA finds its range from
+// Work split: the keys of all units are laid end to end in chunks of 64 or 128 (and some places
+// for what a unit costs beside them, see tree_plan) and cut into equal ranges, one a CTA (two CTAs an SM), whatever the lengths are; every CTA finds its range from
 // a prefix sum over the sequences, so a captured launch follows the lengths on the device.  A
 // CTA's range covers a few whole units and at most two that it shares: its first piece may be
 // the rest of a unit begun by an earlier CTA, its last one the front of a unit that goes on in
 // the next.  Whole units leave as O and LSE; shared ones as the running state (m, l, o~) in
 // one of the CTA's two workspace slots, merged by attn_tree_merge_kernel.
 //
-// Inside a CTA each warp takes every fourth 16-key slice of the piece on its own: its own ring
+// e4m3.  The codes become f16 pairs (exact, one instruction a pair), and so do the other
+// operands.  Q: a row is divided by the power of two of its largest finite value.  P: a
+// probability times its key's scale over the largest scale met so far (2^X, per warp) times
+// 2^15, with the reference m never more than 0.9 (log2) under the running maximum: at most
+// 2^15.9, full 11 bits down to 2^-29 of the largest, steps of 2^-39 below.  That is finer than
+// a bf16 P (8 bits) wherever a key can matter: N keys below 2^-29 weigh at most N 2^-29 together
+// and are off by N 2^-40.  bf16 operands would cost three more conversions a pair of V.
+//
+// Inside a CTA each warp takes every fourth slice of 16 or 32 keys of the piece on its own: its own ring
 // of stages filled by TMA, its own (m, l, o~) in registers, no barrier in the loop.  The four
 // states are combined once a piece.
 #pragma once
@@ -227,6 +235,17 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
       : "memory");
 }
 
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// 2^x for any integer x, 0 or infinity past fp32's range.
+__device__ __forceinline__ float two_to(int x) {
+  return x > 127 ? INFINITY : x >= -126 ? __uint_as_float(static_cast<uint32_t>(x + 127) << 23) : x >= -149 ? __uint_as_float(1u << (x + 149)) : 0.f;
+}
+
 // e4m3 pair -> bf16 pair, exact (every e4m3 value is a bf16).
 __device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t codes) {
   const float2 f = e4m3x2_to_f32(codes);
@@ -239,42 +258,52 @@ __device__ __forceinline__ bool any_nonfinite(uint32_t w) {
 }
 
 constexpr int kTreeRows = 16;
-constexpr int kTreeChunk = 64;    // keys a CTA takes at a time: a 16-key slice a warp
-constexpr int kTreeSlice = 16;
 constexpr int kTreeWarps = 4;
 constexpr int kTreeThreads = 32 * kTreeWarps;
 
 template <int D, bool kF8>
 struct TreeCfg {
   static constexpr int kRowBytes = kF8 ? D : 2 * D;
-  static constexpr int kHalf = kTreeSlice * kRowBytes;           // K (or V) of a slice
+  // Keys a warp takes at a time.  Every slice pays for its wait, its copies' issue and the
+  // maximum's shuffles, so rows of 128 bytes and less go 32 at a time; 256-byte rows at 32 would
+  // leave too few stages.
+  static constexpr int kSlice = kRowBytes > 128 ? 16 : 32;
+  static constexpr int kSubs = kSlice / 16;                      // 16-key boxes of a slice
+  static constexpr int kChunk = kTreeWarps * kSlice;             // keys a CTA takes at a time
+  static constexpr int kHalf = kSlice * kRowBytes;               // K (or V) of a slice
   static constexpr int kStageBytes = 2 * kHalf;
-  static constexpr int kRingBytes = 24 * 1024;                   // of a warp
-  static constexpr int kStages = kRingBytes / kStageBytes;       // 3, 6, 6 or 12
+  static constexpr int kCtas = kF8 && D == 64 ? 3 : 2;                      // an SM
+  static constexpr int kRingBytes = (kCtas == 3 ? 12 : 24) * 1024 / kStageBytes * kStageBytes;  // of a warp
+  static constexpr int kStages = kRingBytes / kStageBytes;
   static constexpr int kSub = kRowBytes > 128 ? kRowBytes / 128 : 1;  // 128-byte wide sub-tiles
   static constexpr int kSubBytes = kHalf / kSub;
-  static constexpr int kScaleBytes = kF8 ? 32 : 0;               // 16 codes of K, 16 of V
-  static constexpr int kTxBytes = kStageBytes + kScaleBytes;
+  static constexpr int kCodes = 2 * kSlice;                      // e4m3: scale codes of K, then of V
+  static constexpr int kBoxBytes = 2 * 16 * kRowBytes + (kF8 ? 32 : 0);  // what a 16-key box brings
   static constexpr int kOffScale = kTreeWarps * kRingBytes;
-  static constexpr int kOffBar = kOffScale + kTreeWarps * kStages * 32;
-  static constexpr int kOffMerge = kOffBar + kTreeWarps * kStages * 8;
+  static constexpr int kOffBar = kOffScale + (kF8 ? kTreeWarps * kStages * kCodes : 0);
+  static constexpr int kOffMerge = (kOffBar + kTreeWarps * kStages * 8 + 15) / 16 * 16;
   static constexpr int kMergeStride = 36;                        // floats a row of 32 columns
   static constexpr int kOffStat = kOffMerge + kTreeWarps * kTreeRows * kMergeStride * 4;
   static constexpr int kOffPre = kOffStat + 2 * kTreeWarps * kTreeRows * 4;
   static constexpr int kOffMisc = kOffPre + (kPlanGroups + 1 + 4) * 8;
   static constexpr int kSmem = kOffMisc + 16 + 1024;             // slack to align the base
-  static_assert(kOffMerge % 16 == 0 && kOffPre % 8 == 0, "alignment");
-  static_assert(kSmem <= 113 * 1024, "two CTAs an SM");
+  static_assert(kSub == 1 || kSubs == 1, "a slice is one box, or its rows lie one after the other");
+  static_assert(kStages >= 2 && kStages * kSubs <= 32, "bits");
+  static_assert(kSmem <= 228 * 1024 / kCtas - 1024, "CTAs an SM");
 };
 
 template <int D, bool kF8>
-__global__ void __launch_bounds__(kTreeThreads, 2)
+__global__ void __launch_bounds__(kTreeThreads, TreeCfg<D, kF8>::kCtas)
     attn_tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                      const TreeParams p) {
   using C = TreeCfg<D, kF8>;
+  constexpr int kSlice = C::kSlice, kSubs = C::kSubs, kChunk = C::kChunk;
+  constexpr int kKeyTiles = kSlice / 8;
   constexpr int kTilesN = D / 8;   // 8-wide column tiles of o~
   constexpr int kSteps = D / 16;   // 16-deep steps of q . k
-  constexpr float kTau = 8.f;      // o~ is rescaled when the max rises by more (log2 units)
+  // o~ is rescaled when the max rises by more than this (log2 units); P is 2^kUp times larger
+  constexpr float kTau = kF8 ? 0.9f : 8.f;
+  constexpr float kUp = kF8 ? 15.f : 0.f;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -282,7 +311,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
   const uint32_t sbase = smem_u32(smem);
   const uint32_t ring = sbase + warp * C::kRingBytes;
   const uint32_t bars = sbase + C::kOffBar + warp * C::kStages * 8;
-  uint8_t* scales = smem + C::kOffScale + warp * C::kStages * 32;
+  uint8_t* scales = smem + C::kOffScale + warp * C::kStages * C::kCodes;
   float* merge = reinterpret_cast<float*>(smem + C::kOffMerge);
   float* stat_m = reinterpret_cast<float*>(smem + C::kOffStat);
   float* stat_l = stat_m + kTreeWarps * kTreeRows;
@@ -302,7 +331,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
   griddep_wait();
   griddep_launch_dependents();
   const int gs = (p.B + kPlanGroups - 1) / kPlanGroups;
-  tree_plan<kTreeRows, kTreeChunk>(p, gs, pre, pre + kPlanGroups + 1);  // its barriers also publish the mbarriers
+  tree_plan<kTreeRows, kChunk>(p, gs, pre, pre + kPlanGroups + 1);  // its barriers also publish the mbarriers
 
   const long long W = pre[kPlanGroups];
   const int grid = static_cast<int>(gridDim.x), cta = static_cast<int>(blockIdx.x);
@@ -313,45 +342,52 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
 
   // ---- loads: an iterator over this warp's slices, kStages ahead of the products
   const uint64_t pol = policy_evict_first();
-  long long px = x0;          // next chunk to make a piece of
+  long long px = x0;          // next place to make a piece of
   int ps = 0, ps_end = 0;     // slices [ps, ps_end) step 4 of the piece in hand
-  int pbase = 0, pages = 0;   // lane i: the page of slice pbase + 4 i
-  int pb = 0, ph = 0;
-  uint32_t skip = 0;          // stages whose slice has no page: nothing was loaded
+  int pbase = 0, pages = 0;   // lane i: the page of box i % kSubs of slice pbase + 4 (i / kSubs)
+  int pb = 0, ph = 0, pn = 0;
+  uint32_t there = 0;         // bits kSubs * stage ..: boxes that exist and have been asked for
   uint32_t live = 0;          // stages with a copy in flight
   uint32_t phase = 0;         // parity each stage completes next
   int ist = 0;                // stage of the next issue
   auto fetch_pages = [&]() {
     pbase = ps;
-    const long long s = ps + static_cast<long long>(kTreeWarps) * lane;
-    pages = s < ps_end ? __ldg(p.table + static_cast<long long>(pb) * p.max_pages + s * kTreeSlice / p.page) : -1;
+    const int s = ps + kTreeWarps * (lane / kSubs);
+    const long long pos = static_cast<long long>(s) * kSlice + 16 * (lane % kSubs);
+    pages = s < ps_end && pos < pn ? __ldg(p.table + static_cast<long long>(pb) * p.max_pages +
+                                           static_cast<uint32_t>(pos) / static_cast<uint32_t>(p.page))
+                                   : -1;
   };
   auto issue = [&]() {
     while (ps >= ps_end) {
       if (px >= x1) return;
-      const TreePiece pc = tree_piece<kTreeRows, kTreeChunk>(p, gs, pre, px, x1);
+      const TreePiece pc = tree_piece<kTreeRows, kChunk>(p, gs, pre, px, x1);
       px += pc.adv;
       if (pc.ch1 <= pc.ch0) continue;
       pb = pc.b;
       ph = pc.h;
-      ps = pc.ch0 * (kTreeChunk / kTreeSlice) + warp;
-      const long long end = min(static_cast<long long>(pc.ch1) * kTreeChunk, static_cast<long long>(pc.s.n));
-      ps_end = static_cast<int>((end + kTreeSlice - 1) / kTreeSlice);
+      pn = pc.s.n;
+      ps = pc.ch0 * kTreeWarps + warp;
+      const long long end = min(static_cast<long long>(pc.ch1) * kChunk, static_cast<long long>(pc.s.n));
+      ps_end = static_cast<int>((end + kSlice - 1) / kSlice);
       fetch_pages();
     }
-    if (ps - pbase >= 32 * kTreeWarps) fetch_pages();
-    const int pg = __shfl_sync(0xffffffffu, pages, (ps - pbase) / kTreeWarps);
-    const uint32_t bit = 1u << ist;
-    if (static_cast<unsigned>(pg) >= static_cast<unsigned>(p.num_pages)) {
-      skip |= bit;
-      if (lane == 0 && p.page_word) atomicOr(p.page_word, 1u);
-    } else {
-      skip &= ~bit;
-      live |= bit;
-      if (lane == 0) {
-        const int row = static_cast<int>(static_cast<unsigned>(ps * kTreeSlice) % static_cast<unsigned>(p.page));
-        const uint32_t bar = bars + 8 * ist, dst = ring + ist * C::kStageBytes;
-        mbar_arrive_expect_tx(bar, C::kTxBytes);
+    if (ps - pbase >= (32 / kSubs) * kTreeWarps) fetch_pages();
+    // lane i < kSubs looks after box i
+    const int pg = __shfl_sync(0xffffffffu, pages, (ps - pbase) / kTreeWarps * kSubs + (lane % kSubs));
+    const bool need = lane < kSubs && static_cast<long long>(ps) * kSlice + 16 * lane < pn;
+    const bool have = need && static_cast<unsigned>(pg) < static_cast<unsigned>(p.num_pages);
+    if (need && !have && p.page_word) atomicOr(p.page_word, 1u);
+    const uint32_t boxes = __ballot_sync(0xffffffffu, have);
+    there = (there & ~(((1u << kSubs) - 1u) << (kSubs * ist))) | (boxes << (kSubs * ist));
+    if (boxes) {
+      const uint32_t bar = bars + 8 * ist;
+      live |= 1u << ist;
+      if (lane == 0) mbar_arrive_expect_tx(bar, __popc(boxes) * C::kBoxBytes);
+      __syncwarp();
+      if (have) {
+        const uint32_t dst = ring + ist * C::kStageBytes + 16 * lane * C::kRowBytes;  // lane 0 where kSub > 1
+        const int row = static_cast<int>((static_cast<uint32_t>(ps) * kSlice + 16u * lane) % static_cast<uint32_t>(p.page));
 #pragma unroll
         for (int s = 0; s < C::kSub; ++s) tma_load_4d(dst + s * C::kSubBytes, &tmK, bar, s * 64, row, ph, pg, pol);
 #pragma unroll
@@ -359,9 +395,9 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
           tma_load_4d(dst + C::kHalf + s * C::kSubBytes, &tmV, bar, s * 64, row, ph, pg, pol);
         if constexpr (kF8) {
           const long long r = (static_cast<long long>(pg) * p.Hkv + ph) * p.page + row;
-          const uint32_t sc = smem_u32(scales + ist * 32);
+          const uint32_t sc = smem_u32(scales + ist * C::kCodes) + 16 * lane;
           bulk_load(sc, p.ks + r, 16, bar);
-          bulk_load(sc + 16, p.vs + r, 16, bar);
+          bulk_load(sc + kSlice, p.vs + r, 16, bar);
         }
       }
     }
@@ -374,7 +410,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
   bool ok = true;
   int cst = 0;  // stage of the next slice to take
   for (long long x = x0; x < x1;) {
-    const TreePiece pc = tree_piece<kTreeRows, kTreeChunk>(p, gs, pre, x, x1);
+    const TreePiece pc = tree_piece<kTreeRows, kChunk>(p, gs, pre, x, x1);
     x += pc.adv;
     if (pc.ch1 <= pc.ch0) continue;
     // ---- this thread's two rows: g and g + 8
@@ -433,48 +469,50 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
     for (int j = 0; j < kTilesN; ++j)
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[j][i] = 0.f;
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};  // l: this thread's columns only
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};  // l: this thread's columns only, times 2^kUp
+    int X = -127;  // e4m3: o~ holds the sums times 2^(kUp - X)
 
-    const long long end = min(static_cast<long long>(pc.ch1) * kTreeChunk, static_cast<long long>(pc.s.n));
-    const int s_end = static_cast<int>((end + kTreeSlice - 1) / kTreeSlice);
-    for (int s = pc.ch0 * (kTreeChunk / kTreeSlice) + warp; s < s_end; s += kTreeWarps) {
+    const long long end = min(static_cast<long long>(pc.ch1) * kChunk, static_cast<long long>(pc.s.n));
+    const int s_end = static_cast<int>((end + kSlice - 1) / kSlice);
+#pragma unroll 1
+    for (int s = pc.ch0 * kTreeWarps + warp; s < s_end; s += kTreeWarps) {
       const int st = cst;
       cst = cst + 1 == C::kStages ? 0 : cst + 1;
-      const uint32_t bit = 1u << st;
-      const bool absent = (skip & bit) != 0;
-      if (!absent) {
+      const uint32_t boxes = (there >> (kSubs * st)) & ((1u << kSubs) - 1u);
+      if (boxes) {
+        const uint32_t bit = 1u << st;
         const bool got = mbar_wait(bars + 8 * st, (phase & bit) ? 1u : 0u, wc, 32);
-        if (!__all_sync(0xffffffffu, got)) ok = false;
-        if (ok) {  // a wait that ran out leaves its copy in flight
-          phase ^= bit;
-          live &= ~bit;
+        if (!__all_sync(0xffffffffu, got)) {
+          ok = false;  // the copy stays in flight
+          break;
         }
-      }
-      if (!ok) break;
-      if (!absent) {
+        phase ^= bit;
+        live &= ~bit;
         const uint32_t sk = ring + st * C::kStageBytes, sv = sk + C::kHalf;
-        const int k0 = s * kTreeSlice;
-        // ---- scores of 16 keys: sc[n-tile][row g: 0, 1; row g + 8: 2, 3], keys 8 n + 2 t, + 1
-        float sc[2][4];
+        const int k0 = s * kSlice;
+        const int left = pc.s.n - k0;  // keys from `left` on do not exist: their rows may hold anything
+        const bool part = left < kSlice || boxes != (1u << kSubs) - 1u;
+        // ---- scores: sc[key tile][row g: 0, 1; row g + 8: 2, 3], keys 8 n + 2 t, + 1
+        float sc[kKeyTiles][4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) (&sc[0][0])[i] = 0.f;
-        float pv[4];  // scales of V of this thread's keys (e4m3)
+        for (int i = 0; i < 4 * kKeyTiles; ++i) (&sc[0][0])[i] = 0.f;
+        float pv[2 * kKeyTiles];  // e4m3: scales of V of this thread's keys, over 2^X
+        float drop = 1.f;         // what a rise of X takes o~ down by
         if constexpr (!kF8) {
           const int key = (lane >> 4) * 8 + (lane & 7);
 #pragma unroll
           for (int k = 0; k < kSteps; ++k) {
             const int ch = (k & 3) * 2 + ((lane >> 3) & 1);  // 16-byte chunk of the 128-byte row
-            uint32_t b[4];
-            ldsm4(b, sk + (k >> 2) * C::kSubBytes + key * 128 + ((ch ^ (key & 7)) << 4));
-            warp_mma_bf16(sc[0], qf[k], b[0], b[1]);
-            warp_mma_bf16(sc[1], qf[k], b[2], b[3]);
+#pragma unroll
+            for (int b = 0; b < kSubs; ++b) {
+              uint32_t w[4];
+              ldsm4(w, sk + (k >> 2) * C::kSubBytes + (16 * b + key) * 128 + ((ch ^ (key & 7)) << 4));
+              warp_mma_bf16(sc[2 * b], qf[k], w[0], w[1]);
+              warp_mma_bf16(sc[2 * b + 1], qf[k], w[2], w[3]);
+            }
           }
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            sc[0][i] *= p.c;
-            sc[1][i] *= p.c;
-            pv[i] = 1.f;
-          }
+          for (int i = 0; i < 4 * kKeyTiles; ++i) (&sc[0][0])[i] *= p.c;
         } else {
           // chunk ch holds 16 columns; a register of it is 4 codes of a key, two f16 pairs
           const int key = ((lane >> 3) & 1) * 8 + (lane & 7);
@@ -482,50 +520,73 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
           for (int k = 0; k < kSteps; k += 2) {
             const int ch = k + (lane >> 4);
             const uint32_t at = D == 128 ? key * 128 + ((ch ^ (key & 7)) << 4) : key * 64 + ((ch ^ ((key >> 1) & 3)) << 4);
-            uint32_t b[4];
-            ldsm4(b, sk + at);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              warp_mma_f16(sc[0], qf[k + i], e4m3x2_to_f16x2(b[2 * i] & 0xffffu), e4m3x2_to_f16x2(b[2 * i] >> 16));
-              warp_mma_f16(sc[1], qf[k + i], e4m3x2_to_f16x2(b[2 * i + 1] & 0xffffu), e4m3x2_to_f16x2(b[2 * i + 1] >> 16));
+            for (int b = 0; b < kSubs; ++b) {
+              uint32_t w[4];
+              ldsm4(w, sk + 16 * b * C::kRowBytes + at);
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                warp_mma_f16(sc[2 * b], qf[k + i], e4m3x2_to_f16x2(w[2 * i] & 0xffffu), e4m3x2_to_f16x2(w[2 * i] >> 16));
+                warp_mma_f16(sc[2 * b + 1], qf[k + i], e4m3x2_to_f16x2(w[2 * i + 1] & 0xffffu),
+                             e4m3x2_to_f16x2(w[2 * i + 1] >> 16));
+              }
             }
           }
-          const uint8_t* kc = scales + st * 32;
+          const uint8_t* kc = scales + st * C::kCodes;
+          uint32_t vc[kKeyTiles];  // codes of V's scales, keys 8 n + 2 t, + 1; 1 for a key that does not exist
+          uint32_t top = 1;
 #pragma unroll
-          for (int n = 0; n < 2; ++n) {
+          for (int n = 0; n < kKeyTiles; ++n) {
             const uint32_t a = *reinterpret_cast<const uint16_t*>(kc + 8 * n + 2 * t);
-            const uint32_t b = *reinterpret_cast<const uint16_t*>(kc + 16 + 8 * n + 2 * t);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const float f = scale_of(i ? a >> 8 : a & 0xffu);
-              sc[n][i] *= cr[0] * f;
-              sc[n][2 + i] *= cr[1] * f;
-              // a key that does not exist may have any code: 0 keeps 0 * scale from being NaN
-              pv[2 * n + i] = k0 + 8 * n + 2 * t + i < pc.s.n ? scale_of(i ? b >> 8 : b & 0xffu) : 0.f;
+            vc[n] = *reinterpret_cast<const uint16_t*>(kc + kSlice + 8 * n + 2 * t);
+            if (part) {
+              const bool out = !((boxes >> (n / 2)) & 1u);
+              if (out || 8 * n + 2 * t >= left) vc[n] = (vc[n] & 0xff00u) | 1u;
+              if (out || 8 * n + 2 * t + 1 >= left) vc[n] = (vc[n] & 0x00ffu) | 0x100u;
             }
+            const uint32_t c0 = vc[n] & 0xffu, c1 = vc[n] >> 8;
+            top = max(top, max(c0 == 255u ? 1u : c0, c1 == 255u ? 1u : c1));
+            const float f0 = scale_of(a & 0xffu), f1 = scale_of(a >> 8);
+            sc[n][0] *= cr[0] * f0;
+            sc[n][1] *= cr[0] * f1;
+            sc[n][2] *= cr[1] * f0;
+            sc[n][3] *= cr[1] * f1;
           }
+          top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));  // the same in every lane
+          if (static_cast<int>(top) - 127 > X) {
+            drop = two_to(max(X - (static_cast<int>(top) - 127), -200));
+            X = static_cast<int>(top) - 127;
+          }
+#pragma unroll
+          for (int n = 0; n < kKeyTiles; ++n)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {  // 2^(code - 127 - X): 0 once it is too small; 255 is NaN
+              const int code = static_cast<int>(i ? vc[n] >> 8 : vc[n] & 0xffu);
+              pv[2 * n + i] = code == 255 ? __int_as_float(0x7fffffff) : __int_as_float(max(code - X, 0) << 23);
+            }
         }
         // ---- masks: every row sees the context; drafted keys go by the row's bits
-        const bool draft = k0 + kTreeSlice > pc.s.ctx;
-        if (draft) {
+        const bool draft = k0 + kSlice > pc.s.ctx;
+        if (draft || part) {
 #pragma unroll
-          for (int n = 0; n < 2; ++n)
+          for (int n = 0; n < kKeyTiles; ++n)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               const int u = k0 + 8 * n + 2 * t + i - pc.s.ctx;
-              if (u >= 0) {
-                if (u >= 64 || !((sees[0] >> u) & 1ull)) sc[n][i] = -INFINITY;
-                if (u >= 64 || !((sees[1] >> u) & 1ull)) sc[n][2 + i] = -INFINITY;
-              }
+              const bool out = !((boxes >> (n / 2)) & 1u) || u >= 64;
+              if (out || (u >= 0 && !((sees[0] >> u) & 1ull))) sc[n][i] = -INFINITY;
+              if (out || (u >= 0 && !((sees[1] >> u) & 1ull))) sc[n][2 + i] = -INFINITY;
             }
         }
         // ---- running max (rows g, g + 8) and probabilities
-        uint32_t pf[4];
         bool move = false;
         float alpha[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          float mx = fmaxf(fmaxf(sc[0][2 * i], sc[0][2 * i + 1]), fmaxf(sc[1][2 * i], sc[1][2 * i + 1]));
+          float mx = fmaxf(sc[0][2 * i], sc[0][2 * i + 1]);
+#pragma unroll
+          for (int n = 1; n < kKeyTiles; ++n) mx = fmaxf(mx, fmaxf(sc[n][2 * i], sc[n][2 * i + 1]));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
           const float mn = mx > m[i] + kTau ? mx : m[i];
@@ -533,16 +594,22 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
           alpha[i] = ex2_approx(m[i] - ref);
           move |= mn != m[i];
           m[i] = mn;
+          const float refu = ref - kUp;
           float sum = 0.f;
 #pragma unroll
-          for (int n = 0; n < 2; ++n)
+          for (int n = 0; n < kKeyTiles; ++n)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              const float e = ex2_approx(sc[n][2 * i + j] - ref);
+              const float e = ex2_approx(sc[n][2 * i + j] - refu);
               sum += e;
               sc[n][2 * i + j] = e;
             }
           l[i] = l[i] * alpha[i] + sum;
+        }
+        if constexpr (kF8) {
+          move |= drop != 1.f;
+          alpha[0] *= drop;  // l has had its alpha
+          alpha[1] *= drop;
         }
         if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
@@ -553,93 +620,95 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
             acc[j][3] *= alpha[1];
           }
         }
-        // P to bf16 for the product (relative 2^-9, unbiased; bf16 and not f16 for its range:
-        // many small probabilities next to a large one keep their relative precision)
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-            pf[2 * n + i] = pack_bf16x2(sc[n][2 * i] * pv[2 * n], sc[n][2 * i + 1] * pv[2 * n + 1]);
-        // ---- o~ += P V.  Columns of tile j: bf16 8 j + 2 t, + 1; e4m3 16 (j / 2) + 4 t + (j & 1), + 2.
-        const int left = pc.s.n - k0;  // keys from `left` on do not exist: their rows may hold anything
-        uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
-        if (left < kTreeSlice) {
-          keep0 = (2 * t < left ? 0xffffu : 0u) | (2 * t + 1 < left ? 0xffff0000u : 0u);
-          keep1 = (2 * t + 8 < left ? 0xffffu : 0u) | (2 * t + 9 < left ? 0xffff0000u : 0u);
-        }
-        const int vkey = ((lane >> 3) & 1) * 8 + (lane & 7);
-        auto load_v = [&](int jj, uint32_t* b) {  // tiles 2 jj, 2 jj + 1: b[0..1], b[2..3]
-          if constexpr (!kF8) {
-            const int ch = (jj & 3) * 2 + (lane >> 4);
-            ldsm4_t(b, sv + (jj >> 2) * C::kSubBytes + vkey * 128 + ((ch ^ (vkey & 7)) << 4));
-          }
-        };
+        uint8_t* vat = smem + (sv - sbase);
         bool odd = false;  // a drafted key's value that is infinite or NaN
-        // drafted nodes of this slice, as bits; nothing is masked when every row sees them all
-        const int u0 = max(0, k0 - pc.s.ctx), u1 = min(pc.s.T, k0 + kTreeSlice - pc.s.ctx);
-        const unsigned long long here = u1 > u0 ? ((~0ull >> (64 - (u1 - u0))) << u0) : 0ull;
-        if (draft && __any_sync(0xffffffffu, ((sees[0] & sees[1]) & here) != here)) {
-          // A masked probability of 0 times such a value would be NaN in rows that do not see
-          // the key: then this slice goes key by key and only to the rows that see it.
-          uint32_t bad = 0;
-          if constexpr (kF8) bad = lane < kTreeSlice && lane < left && scales[st * 32 + 16 + lane] == 255u;
+        if (draft || part) {
+          if (part) {
+            // rows of V that do not exist: 0 instead of what is there (0 * NaN is NaN).  Their
+            // copies have landed, so plain stores to them stay.
 #pragma unroll 1
-          for (int i = lane; i < kTreeSlice * C::kRowBytes / 4; i += 32) {
-            if (i * 4 / C::kRowBytes >= left) break;
-            // every word of the slice once, wherever the swizzle put it inside its row
-            const int row = i / (C::kRowBytes / 4), wd = i % (C::kRowBytes / 4);
-            const uint32_t at = C::kSub == 1 ? row * C::kRowBytes + wd * 4
-                                             : (wd / 32) * C::kSubBytes + row * 128 + (wd % 32) * 4;
-            const uint32_t w = *reinterpret_cast<const uint32_t*>(smem + (sv - sbase) + at);
-            if constexpr (kF8) {
-              bad |= any_nonfinite(e4m3x2_to_bf16x2(w & 0xffffu)) || any_nonfinite(e4m3x2_to_bf16x2(w >> 16));
-            } else {
-              bad |= any_nonfinite(w);
+            for (int i = lane; i < C::kHalf / 16; i += 32) {
+              const int key = i % (C::kSubBytes / 16) / (C::kRowBytes / C::kSub / 16);
+              if (key >= left || !((boxes >> (key / 16)) & 1u)) reinterpret_cast<uint4*>(vat)[i] = make_uint4(0, 0, 0, 0);
             }
+            __syncwarp();
           }
-          odd = __any_sync(0xffffffffu, bad != 0);
-        }
-        if (!odd) {
-          if constexpr (!kF8) {
-#pragma unroll
-            for (int jj = 0; jj < kTilesN / 2; ++jj) {
-              uint32_t b[4];
-              load_v(jj, b);
-              warp_mma_bf16(acc[2 * jj], pf, b[0] & keep0, b[1] & keep1);
-              warp_mma_bf16(acc[2 * jj + 1], pf, b[2] & keep0, b[3] & keep1);
+          // drafted nodes of this slice, as bits; nothing is masked when every row sees them all
+          const int u0 = max(0, k0 - pc.s.ctx), u1 = min(pc.s.T, k0 + kSlice - pc.s.ctx);
+          const unsigned long long here = u1 > u0 ? ((~0ull >> (64 - (u1 - u0))) << u0) : 0ull;
+          if (__any_sync(0xffffffffu, ((sees[0] & sees[1]) & here) != here)) {
+            // A masked probability of 0 times such a value would be NaN in rows that do not see
+            // the key: then this slice goes key by key and only to the rows that see it.
+            bool bad = false;
+            if constexpr (kF8) bad = lane < kSlice && lane < left && scales[st * C::kCodes + kSlice + lane] == 255u;
+#pragma unroll 1
+            for (int i = lane; i < C::kHalf / 4; i += 32) {  // words, wherever the swizzle put them
+              const uint32_t w = reinterpret_cast<const uint32_t*>(vat)[i];
+              if constexpr (kF8)
+                bad |= any_nonfinite(e4m3x2_to_bf16x2(w & 0xffffu)) || any_nonfinite(e4m3x2_to_bf16x2(w >> 16));
+              else
+                bad |= any_nonfinite(w);
             }
-          } else {
+            odd = __any_sync(0xffffffffu, bad);
+          }
+        }
+        // ---- o~ += P V.  Columns of tile j: bf16 8 j + 2 t, + 1; e4m3 16 (j / 2) + 4 t + (j & 1), + 2.
+        const int vkey = ((lane >> 3) & 1) * 8 + (lane & 7);
+        if (!odd) {
 #pragma unroll
-            for (int c0 = 0; c0 < kSteps; c0 += 2) {  // two 16-column chunks: four tiles
-              const int ch = c0 + (lane >> 4);
-              const uint32_t at =
-                  D == 128 ? vkey * 128 + ((ch ^ (vkey & 7)) << 4) : vkey * 64 + ((ch ^ ((vkey >> 1) & 3)) << 4);
-              uint32_t b[4];
-              ldsm4_t(b, sv + at);  // b[0], b[1]: keys 0-7, 8-15 of chunk c0; b[2], b[3]: of c0 + 1
+          for (int b = 0; b < kSubs; ++b) {
+            // P rounds once for the product: to bf16 (relative 2^-8 at most; its range keeps small
+            // probabilities next to a large one as precise), or to f16 with e4m3 (see the top)
+            uint32_t pf[4];
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
 #pragma unroll
               for (int i = 0; i < 2; ++i) {
-                // codes (key 2t, col 2g), (2t, 2g + 1), (2t + 1, 2g), (2t + 1, 2g + 1) -> pairs of keys
-                const uint32_t y0 = __byte_perm(b[2 * i], 0, 0x3120), y1 = __byte_perm(b[2 * i + 1], 0, 0x3120);
-                warp_mma_bf16(acc[2 * (c0 + i)], pf, e4m3x2_to_bf16x2(y0 & 0xffffu) & keep0,
-                              e4m3x2_to_bf16x2(y1 & 0xffffu) & keep1);
-                warp_mma_bf16(acc[2 * (c0 + i) + 1], pf, e4m3x2_to_bf16x2(y0 >> 16) & keep0,
-                              e4m3x2_to_bf16x2(y1 >> 16) & keep1);
+                const float a = sc[2 * b + n][2 * i], e = sc[2 * b + n][2 * i + 1];
+                pf[2 * n + i] = kF8 ? pack_f16x2(a * pv[4 * b + 2 * n], e * pv[4 * b + 2 * n + 1]) : pack_bf16x2(a, e);
+              }
+            if constexpr (!kF8) {
+#pragma unroll
+              for (int jj = 0; jj < kTilesN / 2; ++jj) {
+                const int ch = (jj & 3) * 2 + (lane >> 4);
+                uint32_t w[4];
+                ldsm4_t(w, sv + (jj >> 2) * C::kSubBytes + (16 * b + vkey) * 128 + ((ch ^ (vkey & 7)) << 4));
+                warp_mma_bf16(acc[2 * jj], pf, w[0], w[1]);
+                warp_mma_bf16(acc[2 * jj + 1], pf, w[2], w[3]);
+              }
+            } else {
+#pragma unroll
+              for (int c0 = 0; c0 < kSteps; c0 += 2) {  // two 16-column chunks: four tiles
+                const int ch = c0 + (lane >> 4);
+                const uint32_t at =
+                    D == 128 ? vkey * 128 + ((ch ^ (vkey & 7)) << 4) : vkey * 64 + ((ch ^ ((vkey >> 1) & 3)) << 4);
+                uint32_t w[4];
+                ldsm4_t(w, sv + 16 * b * C::kRowBytes + at);  // keys 0-7, 8-15 of chunk c0, then of c0 + 1
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                  // codes (key 2t, col 2g), (2t, 2g + 1), (2t + 1, 2g), (2t + 1, 2g + 1) -> pairs of keys
+                  const uint32_t y0 = __byte_perm(w[2 * i], 0, 0x3120), y1 = __byte_perm(w[2 * i + 1], 0, 0x3120);
+                  warp_mma_f16(acc[2 * (c0 + i)], pf, e4m3x2_to_f16x2(y0 & 0xffffu), e4m3x2_to_f16x2(y1 & 0xffffu));
+                  warp_mma_f16(acc[2 * (c0 + i) + 1], pf, e4m3x2_to_f16x2(y0 >> 16), e4m3x2_to_f16x2(y1 >> 16));
+                }
               }
             }
           }
         } else {
 #pragma unroll 1
-          for (int key = 0; key < min(left, kTreeSlice); ++key) {
+          for (int key = 0; key < min(left, kSlice); ++key) {
             const int u = k0 + key - pc.s.ctx;
             // the probabilities of this key sit in lane (key % 8) / 2 of each row's four
             float e[2];
             bool see[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              const float a = (key & 8) ? sc[1][2 * i] * pv[2] : sc[0][2 * i] * pv[0];
-              const float b = (key & 8) ? sc[1][2 * i + 1] * pv[3] : sc[0][2 * i + 1] * pv[1];
-              e[i] = __shfl_sync(0xffffffffu, (key & 1) ? b : a, (lane & ~3) | ((key & 7) >> 1));
-              see[i] = u < 0 || (u < 64 && ((sees[i] >> u) & 1ull));
+              float a = 0.f;
+#pragma unroll
+              for (int n = 0; n < 2 * kKeyTiles; ++n)
+                if ((key >> 3) == n / 2 && (key & 1) == (n & 1)) a = sc[n / 2][2 * i + (n & 1)] * (kF8 ? pv[n] : 1.f);
+              e[i] = __shfl_sync(0xffffffffu, a, (lane & ~3) | ((key & 7) >> 1));
+              see[i] = ((boxes >> (key / 16)) & 1u) && (u < 0 || (u < 64 && ((sees[i] >> u) & 1ull)));
             }
 #pragma unroll
             for (int j = 0; j < kTilesN; ++j)
@@ -649,17 +718,18 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
                 if constexpr (!kF8) {
                   const int col = 8 * j + 2 * t + i, ch = (col % 64) / 8;
                   const uint32_t at = (col / 64) * C::kSubBytes + key * 128 + ((ch ^ (key & 7)) << 4) + (col & 7) * 2;
-                  v = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(smem + (sv - sbase) + at));
+                  v = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(vat + at));
                 } else {
                   const int col = 16 * (j / 2) + 4 * t + (j & 1) + 2 * i, ch = col / 16;
                   const uint32_t at = (D == 128 ? key * 128 + ((ch ^ (key & 7)) << 4) : key * 64 + ((ch ^ ((key >> 1) & 3)) << 4)) + (col & 15);
-                  v = e4m3x2_to_f32(smem[(sv - sbase) + at]).x;
+                  v = e4m3x2_to_f32(vat[at]).x;
                 }
                 if (see[0]) acc[j][i] = fmaf(e[0], v, acc[j][i]);
                 if (see[1]) acc[j][2 + i] = fmaf(e[1], v, acc[j][2 + i]);
               }
           }
         }
+        if (part) fence_proxy_async_smem();  // the plain stores before the next copy into the stage
       }
       __syncwarp();  // every lane has read the stage
       issue();
@@ -673,7 +743,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
       l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
       if (t == 0) {
         stat_m[warp * kTreeRows + g + 8 * i] = m[i];
-        stat_l[warp * kTreeRows + g + 8 * i] = l[i];
+        stat_l[warp * kTreeRows + g + 8 * i] = kF8 ? l[i] * 0x1p-15f : l[i];
       }
     }
     __syncthreads();
@@ -685,6 +755,13 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
 #pragma unroll
       for (int w = 1; w < kTreeWarps; ++w) M = fmaxf(M, stat_m[w * kTreeRows + g + 8 * i]);
       f[i] = ex2_approx(m[i] - (M == -INFINITY ? 0.f : M));
+    }
+    if constexpr (kF8) {  // to plain units: o~ 2^(X - kUp), in two steps that stay in range
+      const float a = two_to((X - 15) >> 1), b = two_to((X - 15) - ((X - 15) >> 1));
+#pragma unroll
+      for (int j = 0; j < kTilesN; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[j][i] = acc[j][i] * a * b;
     }
     const int orow = threadIdx.x >> 3, ocol = (threadIdx.x & 7) * 4;  // of the 16 x 32 quarter
     float M = -INFINITY, L = 0.f;
