@@ -20,10 +20,12 @@
 // e4m3.  The codes become f16 pairs (exact, one instruction a pair), and so do the other
 // operands.  Q: a row is divided by the power of two of its largest finite value.  P: a
 // probability times its key's scale over the largest scale met so far (2^X, per warp) times
-// 2^15, with the reference m never more than 0.9 (log2) under the running maximum: at most
-// 2^15.9, full 11 bits down to 2^-29 of the largest, steps of 2^-39 below.  That is finer than
-// a bf16 P (8 bits) wherever a key can matter: N keys below 2^-29 weigh at most N 2^-29 together
-// and are off by N 2^-40.  bf16 operands would cost three more conversions a pair of V.
+// 2^10, with the reference m never more than 5 (log2) under the running maximum: at most 2^15,
+// full 11 bits down to 2^-24 of the reference, steps of 2^-34 below.  That is finer than a bf16
+// P (8 bits) wherever a key can matter: below 2^-24, N keys weigh at most N 2^-24 together and
+// are off by N 2^-35.  bf16 operands would cost three more conversions a pair of V; a closer
+// reference (0.9, with 2^15) moves o~ so often that the softmax of a block in
+// attn_tree_tile_kernel took 3050 cycles instead of 2100.
 //
 // Inside a CTA each warp takes every fourth slice of 16 or 32 keys of the piece on its own: its own ring
 // of stages filled by TMA, its own (m, l, o~) in registers, no barrier in the loop.  The four
@@ -258,6 +260,9 @@ __device__ __forceinline__ bool any_nonfinite(uint32_t w) {
 }
 
 constexpr int kTreeRows = 16;
+// e4m3: how far the reference may lag (log2), and the power of two P goes in with
+constexpr float kTreeTau8 = 5.f;
+constexpr int kTreeUp8 = 10;
 constexpr int kTreeWarps = 4;
 constexpr int kTreeThreads = 32 * kTreeWarps;
 
@@ -302,8 +307,8 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<D, kF8>::kCtas)
   constexpr int kTilesN = D / 8;   // 8-wide column tiles of o~
   constexpr int kSteps = D / 16;   // 16-deep steps of q . k
   // o~ is rescaled when the max rises by more than this (log2 units); P is 2^kUp times larger
-  constexpr float kTau = kF8 ? 0.9f : 8.f;
-  constexpr float kUp = kF8 ? 15.f : 0.f;
+  constexpr float kTau = kF8 ? kTreeTau8 : 8.f;
+  constexpr float kUp = kF8 ? kTreeUp8 : 0.f;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -743,7 +748,7 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<D, kF8>::kCtas)
       l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
       if (t == 0) {
         stat_m[warp * kTreeRows + g + 8 * i] = m[i];
-        stat_l[warp * kTreeRows + g + 8 * i] = kF8 ? l[i] * 0x1p-15f : l[i];
+        stat_l[warp * kTreeRows + g + 8 * i] = kF8 ? l[i] * two_to(-kTreeUp8) : l[i];
       }
     }
     __syncthreads();
@@ -757,7 +762,7 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<D, kF8>::kCtas)
       f[i] = ex2_approx(m[i] - (M == -INFINITY ? 0.f : M));
     }
     if constexpr (kF8) {  // to plain units: o~ 2^(X - kUp), in two steps that stay in range
-      const float a = two_to((X - 15) >> 1), b = two_to((X - 15) - ((X - 15) >> 1));
+      const float a = two_to((X - kTreeUp8) >> 1), b = two_to((X - kTreeUp8) - ((X - kTreeUp8) >> 1));
 #pragma unroll
       for (int j = 0; j < kTilesN; ++j)
 #pragma unroll

@@ -4,21 +4,26 @@
 // and grouped heads make more rows than one 16-row tile: there every further tile reads the
 // keys again and its warp-level products become the limit.  Here a tile holds the G heads of
 // 128 / G tokens as the 128 lanes of tensor memory, and the products are tcgen05.mma: per
-// block of 128 keys S = Q K^T (128 x 128 x d, into one of three score buffers) and
+// block of 128 keys S = Q K^T (128 x 128 x d, into one of two score buffers) and
 // o~ += P V, with P written back over S as bf16.  One CTA an SM, persistent over its range of
 // the list of chunks (128 keys each).
 //
-// Warps: 0-3 softmax, thread r owns row r (tensor-memory lane r); 4 producer (TMA); 5 issues
-// P V; 6 issues S; 7 (bf16) repairs V blocks at a sequence's end, see below, or (e4m3) turns
-// the scale codes of K into floats; 8-11 (e4m3) convert Q and V, thread r row r.
+// Two streams: blocks of even number go to one group of four softmax warps and accumulator o~,
+// odd ones to the other, so that one group's softmax covers the other's products
+// and loads; each stream keeps its own (m, l, o~), combined once a piece.
+//
+// Warps: 0-3 and 8-11 softmax, thread r of a group owns row r (tensor-memory lane r); 4 producer
+// (TMA); 5 issues P V; 6 issues S; 7 (bf16) repairs V blocks at a sequence's end, see below, or
+// (e4m3) turns the scale codes of K into floats; 12-15 (e4m3) convert Q and V, thread r row r.
 //
 // e4m3: the codes of K go to the tensor cores as they are.  A query row, divided by the power
 // of two that brings its largest finite value into [128, 256), is split into two e4m3 terms,
 // q = hi + lo: 8 significant bits are 4 + 4, so the split is exact down to 2^-10 of the row's
 // largest and off by at most 2^-19 of it below, and S = hi K^T + lo K^T in fp32.  The row's
-// power of two and each key's scale multiply the scores afterwards.  V is widened to bf16 with
-// its scale, exact, because P needs bf16's range (two e4m3 terms would drop probabilities
-// under 2^-18 of the largest, which together can matter in a long context).
+// power of two and each key's scale multiply the scores afterwards.  V is widened to f16 times
+// its scale over 2^X, X a running exponent of the piece (raised when a block's largest scale
+// passes it by more than 2^7, o~ then scaled down with it), and P goes in as f16 times 2^10,
+// as in attn_tree_kernel.
 //
 // K and V blocks are up to eight boxes of 16 keys, each from the page it lies in (larger boxes
 // when the page size allows: fewer copies).  A block that holds drafted keys, or keys past the
@@ -37,8 +42,6 @@ constexpr int kTileWarpTma = 4;
 constexpr int kTileWarpPv = 5;
 constexpr int kTileWarpS = 6;
 constexpr int kTileWarpFix = 7;
-constexpr uint32_t kTileRegsSoftmax = 232;  // of 3 x 168 (e4m3: 384 threads): 232 + 104 + 168 = 504
-constexpr uint32_t kTileRegsOther = 104;
 constexpr int kTileTags = 16;
 // Pieces announced in shared memory.  The producer is at most 7 blocks, so at most 8 pieces,
 // ahead of the softmax, and no role is behind it: a slot is never overwritten while in use.
@@ -56,7 +59,10 @@ static_assert(sizeof(TileJob) == 48, "three 16-byte words");
 
 template <int D, bool kF8>
 struct TileCfg {
-  static constexpr int kThreads = kF8 ? 384 : 256;
+  // (bf16 at d = 128 has no shared memory left for the second stream's statistics, and reaches
+  // the memory's rate with one.)
+  static constexpr int kStreams = !kF8 && D == 128 ? 1 : 2;
+  static constexpr int kThreads = kF8 ? 512 : kStreams == 2 ? 384 : 256;
   static constexpr int kSub = D / 64;                    // 64-column sub-tiles of a bf16 row
   static constexpr int kSubBytes = 128 * 128;            // 128 rows x 64 bf16
   static constexpr int kTileBytes = kSub * kSubBytes;    // a block of K, V or Q in bf16
@@ -67,7 +73,7 @@ struct TileCfg {
   static constexpr int kWide = kF8 ? (D == 64 ? 3 : 2) : 0;
   static constexpr int kStageK = kF8 ? kRawBytes : kTileBytes;
   static constexpr int kStageV = kStageK;
-  static constexpr int kSBufs = 3;
+  static constexpr int kSBufs = kStreams * D + 3 * 128 <= 512 ? 3 : 2;  // what tensor memory has room for
   static constexpr int kOffQ = 0;
   // e4m3: hi, then lo.  At d = 128 each row's two terms take the very bytes of its bf16 row
   // (128 in each sub-tile), so a thread overwrites only what it has read; at d = 64 they lie beside.
@@ -79,22 +85,25 @@ struct TileCfg {
   static constexpr int kOffCodeV = kOffCodeK + (kF8 ? kRingK * 128 : 0);
   static constexpr int kOffScaleK = kOffCodeV + (kF8 ? kRingV * 128 : 0);  // floats, block g % 8
   static constexpr int kOffScaleQ = kOffScaleK + (kF8 ? 8 * 512 : 0);      // floats, piece u % 8
-  static constexpr int kOffBar = kOffScaleQ + (kF8 ? 8 * 512 : 0);
+  static constexpr int kOffX = kOffScaleQ + (kF8 ? 8 * 512 : 0);           // X of block g % 8
+  static constexpr int kOffStat = kOffX + (kF8 ? 32 : 0);   // m, l of each stream, piece u % 2
+  static constexpr int kOffBar = kOffStat + (kStreams == 2 ? 2 * 4 * 512 : 0);
   // q_full, q_free, q8_full, {k_full, k_free, k_ready}[RK], {v_full, v_free, v_fixed}[RV],
-  // {w_full, w_free}[W], {s_full, pv_done, p_full}[B], drain[2], piece[16]
-  static constexpr int kNumBars = 3 + 3 * kRingK + 3 * kRingV + 2 * kWide + 3 * kSBufs + 2 + kTilePieces;
+  // {w_full, w_free}[W], {s_full, pv_done, p_full}[B], drain[2], o_free, piece[16]
+  static constexpr int kNumBars = 3 + 3 * kRingK + 3 * kRingV + 2 * kWide + 3 * kSBufs + 3 + kTilePieces;
   static constexpr int kOffPieces = (kOffBar + 8 * kNumBars + 15) / 16 * 16;
   static constexpr int kOffPre = kOffPieces + kTilePieces * 48;
   static constexpr int kOffMisc = kOffPre + 8 * (kPlanGroups + 1 + 4);  // tmem base, abort, valid[16], tags[16]
   static constexpr int kSmem = kOffMisc + 8 + 64 + 4 * kTileTags + 1024;
   static_assert(kSmem <= 232448, "shared memory per CTA");
   __host__ __device__ static constexpr uint32_t col_s(int b) { return 128u * b; }
-  static constexpr uint32_t kColO = 128u * kSBufs;
+  __host__ __device__ static constexpr uint32_t col_o(int b) { return 128u * kSBufs + static_cast<uint32_t>(D) * b; }
   static constexpr uint32_t kIdescS = idesc_bf16_f32(kTileRows, kTileKeys, 0);
   // kind::f8f6f4, e4m3 x e4m3 -> fp32 (the formats' codes are 0)
   static constexpr uint32_t kIdescS8 = (1u << 4) | ((kTileKeys >> 3) << 17) | ((kTileRows >> 4) << 24);
-  static constexpr uint32_t kIdescO = idesc_bf16_f32(kTileRows, D, 1);
-  static_assert(kColO + D <= 512, "tensor memory");
+  // e4m3: f16 x f16 (the formats' codes are 0)
+  static constexpr uint32_t kIdescO = idesc_bf16_f32(kTileRows, D, 1) & ~(kF8 ? (1u << 7) | (1u << 10) : 0u);
+  static_assert(128 * kSBufs + kStreams * D <= 512, "tensor memory");
 };
 
 // D[tmem] (+)= A[smem desc] * B[smem desc]^T, kind::f8f6f4 (e4m3 in, fp32 accumulate), k = 32.
@@ -115,12 +124,12 @@ __device__ __forceinline__ uint32_t finite_only(uint32_t w) {
   return w;
 }
 
-// Eight e4m3 codes times the scale (a bf16 pair of it) as four bf16 pairs, exact.
-__device__ __forceinline__ uint4 widen8(uint32_t lo, uint32_t hi, __nv_bfloat162 scale) {
+// Eight e4m3 codes times the scale (an f16 pair of it) as four f16 pairs.
+__device__ __forceinline__ uint4 widen8(uint32_t lo, uint32_t hi, __half2 scale) {
   uint4 r;
   auto one = [&](uint32_t c) {
-    const uint32_t w = e4m3x2_to_bf16x2(c);
-    const __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w), scale);
+    const uint32_t w = e4m3x2_to_f16x2(c);
+    const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&w), scale);
     return *reinterpret_cast<const uint32_t*>(&v);
   };
   r.x = one(lo & 0xffffu);
@@ -128,6 +137,38 @@ __device__ __forceinline__ uint4 widen8(uint32_t lo, uint32_t hi, __nv_bfloat162
   r.z = one(hi & 0xffffu);
   r.w = one(hi >> 16);
   return r;
+}
+
+// f16 counterparts of any_nonfinite and finite_only.
+__device__ __forceinline__ bool any_nonfinite16(uint32_t w) {
+  return (w & 0x7c00u) == 0x7c00u || (w & 0x7c000000u) == 0x7c000000u;
+}
+__device__ __forceinline__ uint32_t finite_only16(uint32_t w) {
+  if ((w & 0x7c00u) == 0x7c00u) w &= 0xffff0000u;
+  if ((w & 0x7c000000u) == 0x7c000000u) w &= 0x0000ffffu;
+  return w;
+}
+
+// 2^k twice as f16, 0 below its range (k <= 7 here).
+__device__ __forceinline__ uint32_t two_to_f16x2(int k) {
+  const uint32_t h = k >= -14 ? static_cast<uint32_t>(k + 15) << 10 : k >= -24 ? 1u << (k + 24) : 0u;
+  return h | (h << 16);
+}
+
+// X after a block of V whose 128 scale codes are at `codes` (a warp's work, the same in all of
+// its lanes and in every warp that does it): the first block's largest scale, then raised when
+// a block's passes it by more than 2^7 (448 * 2^7 is an f16).  Keys that do not exist, and
+// codes of 255, do not count.
+__device__ __forceinline__ int tile_next_x(int x, bool first, const uint8_t* codes, uint32_t vm, int left, int lane) {
+  const uint32_t w = *reinterpret_cast<const volatile uint32_t*>(codes + 4 * lane);
+  uint32_t top = 1;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t c = (w >> (8 * i)) & 0xffu;
+    if (((vm >> (lane / 4)) & 1u) && 4 * lane + i < left && c != 255u) top = max(top, c);
+  }
+  const int t = static_cast<int>(__reduce_max_sync(0xffffffffu, top)) - 127;
+  return first || t > x + 7 ? t : x;
 }
 
 // Infinities and NaN among the drafted values of a piece, which went into the product as zero,
@@ -168,6 +209,7 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
   using C = TileCfg<D, kF8>;
   constexpr int RK = C::kRingK, RV = C::kRingV, NB = C::kSBufs, NW = C::kWide;
   constexpr int NWm = NW > 0 ? NW : 1;
+  constexpr int ST = C::kStreams;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
@@ -187,12 +229,13 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
   auto bar_pv_done = [&](int b) { return bar0 + 8u * (kB1 + NB + b); };
   auto bar_p_full = [&](int b) { return bar0 + 8u * (kB1 + 2 * NB + b); };
   auto bar_drain = [&](int i) { return bar0 + 8u * (kB1 + 3 * NB + i); };
-  auto bar_piece = [&](int i) { return bar0 + 8u * (kB1 + 3 * NB + 2 + i); };
+  const uint32_t bar_o_free = bar0 + 8u * (kB1 + 3 * NB + 2);  // both groups have read a piece's o~
+  auto bar_piece = [&](int i) { return bar0 + 8u * (kB1 + 3 * NB + 3 + i); };
   long long* pre = reinterpret_cast<long long*>(smem + C::kOffPre);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + C::kOffMisc + 4);
   // valid[g % 16]: which 16-key slices of block g exist (written before the block's copies are
-  // announced; the producer is at most 7 blocks ahead of the softmax)
+  // announced; the producer is at most 7 blocks ahead of either stream)
   volatile uint32_t* valid = reinterpret_cast<volatile uint32_t*>(smem + C::kOffMisc + 8);
   // tag[u % 16] = u + 1 once unit u (of this CTA) has met an infinite or NaN drafted value
   volatile uint32_t* tag = reinterpret_cast<volatile uint32_t*>(smem + C::kOffMisc + 72);
@@ -225,6 +268,7 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
     }
     mbar_init(bar_drain(0), 1);
     mbar_init(bar_drain(1), 1);
+    mbar_init(bar_o_free, 4 * ST);
     for (int i = 0; i < kTilePieces; ++i) mbar_init(bar_piece(i), 1);
     *abort_flag = 0u;
     for (int i = 0; i < kTileTags; ++i) tag[i] = 0u;
@@ -261,7 +305,6 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
   };
   if (warp == kTileWarpTma) {
     // ================================================================ producer
-    if constexpr (kF8) setmaxnreg_dec<kTileRegsOther>();
     const uint64_t pol = policy_evict_first();
     const int box16 = p.box_rows / 16;  // slices a box holds
     int g = 0, u = 0;
@@ -369,7 +412,6 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
     }
   } else if (warp == kTileWarpPv || warp == kTileWarpS) {
     // ================================================================ products
-    if constexpr (kF8) setmaxnreg_dec<kTileRegsOther>();
     if (lane == 0) {
       const uint32_t dhi = (1024u >> 4) | (1u << 14) | (2u << 29);
       int g = 0, u = 0;
@@ -414,6 +456,7 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
           mma_commit(bar_q_free);
         } else {
           const uint32_t vlo = ((kF8 ? sbase + C::kOffWide : sV) >> 4) | (static_cast<uint32_t>(C::kSubBytes >> 4) << 16);
+          if (u > 0) ok = mbar_wait(bar_o_free, (u - 1) & 1, wc, 56);
           for (int j = pc.ch0; ok && j < pc.ch1; ++j, ++g) {
             const int st = kF8 ? g % NWm : g % RV;
             ok = kF8 ? mbar_wait(bar_w_full(st), (g / NWm) & 1, wc, 39) : mbar_wait(bar_v_full(st), (g / RV) & 1, wc, 39);
@@ -428,8 +471,8 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
             const uint32_t a = tmem + C::col_s(g % NB);
 #pragma unroll
             for (int ks = 0; ks < kTileKeys / 16; ++ks)
-              mma_ts(tmem + C::kColO, a + ks * 8, (static_cast<uint64_t>(dhi) << 32) | (blo + ks * (16 * 128 >> 4)),
-                     C::kIdescO, (j > pc.ch0 || ks > 0) ? 1u : 0u);
+              mma_ts(tmem + C::col_o(g % ST), a + ks * 8, (static_cast<uint64_t>(dhi) << 32) | (blo + ks * (16 * 128 >> 4)),
+                     C::kIdescO, (j >= pc.ch0 + ST || ks > 0) ? 1u : 0u);
             mma_commit(bar_pv_done(g % NB));
             mma_commit(kF8 ? bar_w_free(st) : bar_v_free(st));
           }
@@ -445,8 +488,7 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
     if constexpr (kF8) {
       // ---- scales of K's keys as floats, four a lane.  Entry g % 8: block g's stage was freed
       // by S of block g - 4, which is at most 3 blocks ahead of the softmax.
-      setmaxnreg_dec<kTileRegsOther>();
-      int g = 0, u = 0;
+      int g = 0, u = 0, x = 0;
       bool ok = true;
       TileJob pc;
       while (job(u, pc, ok, 51)) {
@@ -460,6 +502,11 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
           reinterpret_cast<float4*>(smem + C::kOffScaleK)[(g & 7) * 32 + lane] =
               make_float4(scale_of(max(w & 0xffu, 1u)), scale_of(max((w >> 8) & 0xffu, 1u)),
                           scale_of(max((w >> 16) & 0xffu, 1u)), scale_of(max(w >> 24, 1u)));
+          // X, which the softmax needs before the block's P V (the converters find the same)
+          ok = __all_sync(0xffffffffu, mbar_wait(bar_v_full(g % RV), (g / RV) & 1, wc, 55));
+          if (!ok) break;
+          x = tile_next_x(x, j == pc.ch0, smem + C::kOffCodeV + (g % RV) * 128, valid[g & 15], pc.n - j * kTileKeys, lane);
+          if (lane == 0) reinterpret_cast<volatile int*>(smem + C::kOffX)[g & 7] = x;
           __syncwarp();
           if (lane == 0) mbar_arrive(bar_k_ready(st));
         }
@@ -502,14 +549,14 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
         ++u;
       }
     }
-  } else if (kF8 && warp >= 8) {
+  } else if (kF8 && warp >= 12) {
     // ================================================================ e4m3 -> bf16
     if constexpr (kF8) {
       // Loops over a row's chunks stay rolled: this role's code next to the softmax's overflows
       // the instruction cache when unrolled (measured on GB300, one sequence of 131072 tokens,
       // d = 128: 144 us with 8 chunks unrolled, a third of the stalls for want of instructions).
-      const int r = threadIdx.x - 256;  // row of Q, key of a block
-      int g = 0, u = 0;
+      const int r = threadIdx.x - 384;  // row of Q, key of a block
+      int g = 0, u = 0, vx = 0;
       bool ok = true;
       TileJob pc;
       while (job(u, pc, ok, 53)) {
@@ -560,7 +607,7 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
         if (lane == 0) mbar_arrive(bar_q8_full);
         for (int j = pc.ch0; j < pc.ch1; ++j, ++g) {
           const int sv = g % RV, sw = g % NWm, kb = j * kTileKeys;
-          // ---- V: codes times scale as bf16
+          // ---- V: codes times scale over 2^X as f16
           ok = mbar_wait(bar_v_full(sv), (g / RV) & 1, wc, 45) && mbar_wait(bar_w_free(sw), ((g / NWm) & 1) ^ 1, wc, 46);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
@@ -569,9 +616,10 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
           const bool scan = kb + r >= pc.ctx;
           const uint8_t* src = smem + C::kOffV + sv * C::kStageV + r * D;
           uint8_t* dst = smem + C::kOffWide + sw * C::kTileBytes + r * 128;
-          const uint32_t code = here ? smem[C::kOffCodeV + sv * 128 + r] : 0u;
-          const uint32_t two = (code << 7) | (code << 23);  // 2^(code - 127) twice, as bf16
-          const __nv_bfloat162 scale = *reinterpret_cast<const __nv_bfloat162*>(&two);
+          vx = tile_next_x(vx, j == pc.ch0, smem + C::kOffCodeV + sv * 128, vm, pc.n - kb, lane);
+          const int code = here ? smem[C::kOffCodeV + sv * 128 + r] : 0;
+          const uint32_t two = code == 255 ? 0x7e007e00u : two_to_f16x2(code - 127 - vx);  // 255: NaN
+          const __half2 scale = *reinterpret_cast<const __half2*>(&two);
           const bool ragged = __any_sync(0xffffffffu, !here || scan);
           bool odd = false;
 #pragma unroll 2
@@ -584,12 +632,12 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
                 uint32_t& e = w[i >> 2][i & 3];
-                if (here && scan && any_nonfinite(e)) odd = true;
+                if (here && scan && any_nonfinite16(e)) odd = true;
                 if (!here) e = 0u;
-                if (scan) e = finite_only(e);
+                if (scan) e = finite_only16(e);
               }
             }
-            // 16 columns = chunks 2 c, 2 c + 1 of the bf16 row, in sub-tile c / 4
+            // 16 columns = chunks 2 c, 2 c + 1 of the wide row, in sub-tile c / 4
             uint8_t* to = dst + (c / 4) * C::kSubBytes;
             const int ch = (2 * c) & 7;
             *reinterpret_cast<uint4*>(to + ((ch ^ (r & 7)) << 4)) = a;
@@ -609,11 +657,14 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
     }
   } else {
     // ================================================================ softmax
-    if constexpr (kF8) setmaxnreg_inc<kTileRegsSoftmax>();
-    const int r = threadIdx.x;
-    const uint32_t tl = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+    const int wg = warp >= 8 ? 1 : 0;           // stream: blocks g with g % ST == wg
+    const int r = (warp & 3) * 32 + lane;
+    const uint32_t tl = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     float c = p.c;  // e4m3: times the row's power of two, piece by piece
-    constexpr float kTau = 8.f;  // o~ is rescaled when the max rises by more (log2 units)
+    // o~ is rescaled when the max rises by more than this (log2 units); P and l are 2^kUp larger
+    constexpr float kTau = kF8 ? kTreeTau8 : 8.f;
+    constexpr float kUp = kF8 ? kTreeUp8 : 0.f;
+    int vx = 0;  // e4m3: o~ holds the sums times 2^(kUp - X)
     int g = 0, u = 0;
     bool ok = true, has_tail = false;
     // The next piece and this thread's row of it are looked up while the last product of the
@@ -635,20 +686,24 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
       return true;
     };
     bool more = look(0);
+    // warps that gave up here would be missing at the streams' barrier below
+    if (ST == 2 && bar_sync_or(1, 256, !ok)) ok = false;
     while (__all_sync(0xffffffffu, ok && more)) {
       const bool idle = !__any_sync(0xffffffffu, row_here);  // no row of this warp exists
-      bool s_seen = false, pv_seen = false;  // barriers of the next block, and of the last one, tested early
+      bool any = false;  // this stream has had a block of the piece
       float m = -INFINITY, l = 0.f;
+      if (kF8) vx = -126;
       for (int j = pc.ch0; j < pc.ch1; ++j, ++g) {
-        const uint32_t colS = C::col_s(g % NB);
-        if (!__all_sync(0xffffffffu, s_seen))
-          ok = __all_sync(0xffffffffu, mbar_wait(bar_s_full(g % NB), (g / NB) & 1, wc, 47));
+        if (g % ST != wg) continue;
+        const int bf = g % NB;
+        const uint32_t colS = C::col_s(bf), colO = C::col_o(wg);
+        ok = __all_sync(0xffffffffu, mbar_wait(bar_s_full(bf), (g / NB) & 1, wc, 47));
         if (!ok) break;
-        s_seen = false;
-        const float4* ks = reinterpret_cast<const float4*>(smem + C::kOffScaleK + (g & 7) * 512);
-        if (kF8 && j == pc.ch0) c = reinterpret_cast<const volatile float*>(smem + C::kOffScaleQ)[(u & 7) * 128 + r];
+        const bool first = !any;
+        any = true;
+        if (kF8 && first) c = reinterpret_cast<const volatile float*>(smem + C::kOffScaleQ)[(u & 7) * 128 + r];
         if (idle) {  // its lanes of P hold scores: rows nobody reads
-          if (lane == 0) mbar_arrive(bar_p_full(g % NB));
+          if (lane == 0) mbar_arrive(bar_p_full(bf));
           continue;
         }
         tc_fence_after();
@@ -674,75 +729,101 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
           }
           tmem_wait_st();
         }
-        float s[kTileKeys];
-        {
-          uint32_t sr[kTileKeys];
+        const float4* ks = reinterpret_cast<const float4*>(smem + C::kOffScaleK + (g & 7) * 512);
+        // 32 columns at a time, loaded twice (maximum, then exponentials) in rolled loops: a row's
+        // 128 columns unrolled are code enough for the instruction cache to be the limit, cold at
+        // a launch's start and beside the converters' code.
+        auto scores = [&](int q, float* s) {  // 32 scores (e4m3: times their keys' scales)
+          uint32_t e[32];
+          tmem_ld32(tl + colS + q * 32, e);
+          if constexpr (kF8) {
+            float4 f[8];
 #pragma unroll
-          for (int q = 0; q < kTileKeys / 32; ++q) tmem_ld32(tl + colS + q * 32, sr + q * 32);
-          tmem_wait_ld();
+            for (int k = 0; k < 8; ++k) f[k] = ks[q * 8 + k];
+            tmem_wait_ld();
 #pragma unroll
-          for (int k = 0; k < kTileKeys; ++k) s[k] = __uint_as_float(sr[k]);
-        }
-        if constexpr (kF8) {  // times the keys' scales (a key that is masked may have any: -inf stays)
+            for (int k = 0; k < 8; ++k) {
+              const float2 a = __fmul2_rn(make_float2(__uint_as_float(e[4 * k]), __uint_as_float(e[4 * k + 1])),
+                                          make_float2(f[k].x, f[k].y));
+              const float2 b = __fmul2_rn(make_float2(__uint_as_float(e[4 * k + 2]), __uint_as_float(e[4 * k + 3])),
+                                          make_float2(f[k].z, f[k].w));
+              s[4 * k] = a.x;
+              s[4 * k + 1] = a.y;
+              s[4 * k + 2] = b.x;
+              s[4 * k + 3] = b.y;
+            }
+          } else {
+            tmem_wait_ld();
 #pragma unroll
-          for (int k = 0; k < kTileKeys / 4; ++k) {
-            const float4 f = ks[k];
-            const float2 a = __fmul2_rn(make_float2(s[4 * k], s[4 * k + 1]), make_float2(f.x, f.y));
-            const float2 b = __fmul2_rn(make_float2(s[4 * k + 2], s[4 * k + 3]), make_float2(f.z, f.w));
-            s[4 * k] = a.x;
-            s[4 * k + 1] = a.y;
-            s[4 * k + 2] = b.x;
-            s[4 * k + 3] = b.y;
+            for (int k = 0; k < 32; ++k) s[k] = __uint_as_float(e[k]);
           }
+        };
+        float mx = -INFINITY;
+#pragma unroll 1
+        for (int q = 0; q < kTileKeys / 32; ++q) {
+          float s[32];
+          scores(q, s);
+          float a[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) a[i] = fmax3(s[2 * i], s[2 * i + 1], s[8 + 2 * i]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) a[i] = fmax3(a[i], s[9 + 2 * i], s[16 + 2 * i]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) a[i] = fmax3(a[i], s[17 + 2 * i], s[24 + 2 * i]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) a[i] = fmaxf(a[i], s[25 + 2 * i]);
+          mx = fmax3(mx, fmaxf(a[0], a[1]), fmaxf(a[2], a[3]));
         }
-        float a[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) a[i] = fmaxf(s[2 * i], s[2 * i + 1]);
-#pragma unroll
-        for (int k = 16; k < kTileKeys; k += 16)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) a[i] = fmax3(a[i], s[k + 2 * i], s[k + 2 * i + 1]);
-        const float mx = fmaxf(fmaxf(fmax3(a[0], a[1], a[2]), fmax3(a[3], a[4], a[5])), fmaxf(a[6], a[7])) * c;
+        mx *= c;
         const float m_new = mx > m + kTau ? mx : m;
         const float ref = m_new == -INFINITY ? 0.f : m_new;
-        const float alpha = ex2_approx(m - ref);
-        const float2 c2 = make_float2(c, c), nm2 = make_float2(-ref, -ref);
-        float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int q = 0; q < kTileKeys / 32; ++q) {
-          if (q == kTileKeys / 32 - 1) {
-            s_seen = j + 1 < pc.ch1 && mbar_test_wait(bar_s_full((g + 1) % NB), ((g + 1) / NB) & 1);
-            pv_seen = j > pc.ch0 && mbar_test_wait(bar_pv_done((g - 1) % NB), ((g - 1) / NB) & 1);
+        float alpha = ex2_approx(m - ref);
+        l *= alpha;
+        bool moved = m_new != m;
+        m = m_new;
+        if constexpr (kF8) {
+          const int nx = reinterpret_cast<volatile const int*>(smem + C::kOffX)[g & 7];
+          if (!first && nx != vx) {  // rises: o~ comes down with it
+            alpha *= two_to(max(vx - nx, -200));
+            moved = true;
           }
+          vx = nx;
+        }
+        const float2 c2 = make_float2(c, c), nm2 = make_float2(kUp - ref, kUp - ref);
+        float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
+#pragma unroll 1
+        for (int q = 0; q < kTileKeys / 32; ++q) {
+          float s[32];
+          scores(q, s);
           uint32_t pk[16];
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
-            float2 e = __ffma2_rn(make_float2(s[q * 32 + 2 * k], s[q * 32 + 2 * k + 1]), c2, nm2);
+            float2 e = __ffma2_rn(make_float2(s[2 * k], s[2 * k + 1]), c2, nm2);
             e.x = ex2_approx(e.x);
             e.y = ex2_approx(e.y);
             if (k & 1)
               acc1 = __fadd2_rn(acc1, e);
             else
               acc0 = __fadd2_rn(acc0, e);
-            // P to bf16 (relative 2^-8 at most), as in attn_tree_kernel
-            pk[k] = pack_bf16x2(e.x, e.y);
+            // P rounds once: to bf16 (relative 2^-8 at most) or f16, as in attn_tree_kernel
+            pk[k] = kF8 ? pack_f16x2(e.x, e.y) : pack_bf16x2(e.x, e.y);
           }
+          // over S: columns 16 q .. of the buffer held scores of chunk q / 2, which are used
           tmem_st16(tl + colS + q * 16, pk);
         }
         const float2 acc = __fadd2_rn(acc0, acc1);
-        l = l * alpha + (acc.x + acc.y);
-        const bool moved = m_new != m;
-        m = m_new;
-        if (j > pc.ch0 && __any_sync(0xffffffffu, moved)) {
-          if (!__all_sync(0xffffffffu, pv_seen))
-            ok = __all_sync(0xffffffffu, mbar_wait(bar_pv_done((g - 1) % NB), ((g - 1) / NB) & 1, wc, 48));
+        l += acc.x + acc.y;
+        if (!first && __any_sync(0xffffffffu, moved)) {
+          // o~ may be touched once the stream's last P V, of block g - ST, is in it.  With as many
+          // score buffers as streams it is: S of this block came after it.
+          if (NB > ST) ok = __all_sync(0xffffffffu, mbar_wait(bar_pv_done((g - ST) % NB), ((g - ST) / NB) & 1, wc, 48));
           if (!ok) break;
-          tc_fence_after();
+          if (NB > ST) tc_fence_after();
           const float2 al2 = make_float2(alpha, alpha);
 #pragma unroll 1
           for (int q = 0; q < D / 32; ++q) {
             uint32_t o[32];
-            tmem_ld32(tl + C::kColO + q * 32, o);
+            tmem_ld32(tl + colO + q * 32, o);
             tmem_wait_ld();
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
@@ -750,15 +831,14 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
               o[2 * k] = __float_as_uint(v.x);
               o[2 * k + 1] = __float_as_uint(v.y);
             }
-            tmem_st32(tl + C::kColO + q * 32, o);
+            tmem_st32(tl + colO + q * 32, o);
           }
         }
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar_p_full(g % NB));
+        if (lane == 0) mbar_arrive(bar_p_full(bf));
       }
-      if (!ok) break;
       const bool whole = pc.ch0 == 0 && pc.ch1 == pc.nch;
       const bool front = pc.ch0 == 0 && !whole;  // goes on in the next CTAs
       const int hq = pc.h * p.G + head;
@@ -768,30 +848,78 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
       const TileJob done = pc;
       const bool row_done = row_here;
       const unsigned long long saw = sees;
-      more = look(u + 1);
-      // ---- o~ out: the piece's last P V (and so all of them) has landed
-      if (!mbar_wait(bar_pv_done((g - 1) % NB), ((g - 1) / NB) & 1, wc, 49)) ok = false;
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
+      const int count = pc.ch1 - pc.ch0, g_end = g;
+      if (ok) more = look(u + 1);
+      // ---- o~ out: this stream's last P V of the piece has landed
+      if (ok && any) {
+        const int gl = (g_end - 1) % ST == wg ? g_end - 1 : g_end - 2;
+        ok = __all_sync(0xffffffffu, mbar_wait(bar_pv_done(gl % NB), (gl / NB) & 1, wc, 49));
+      }
+      // Both streams' statistics, then every thread has half the columns of its row.  Each of the
+      // eight warps comes here once a piece, also after a failed wait, and they leave together.
+      float mo = -INFINITY, lo = 0.f;             // the other stream's
+      if (kF8) l *= two_to(-kTreeUp8);            // units of states: l 2^-kUp, o~ 2^(X - kUp)
+      if constexpr (ST == 2) {
+        float* stat = reinterpret_cast<float*>(smem + C::kOffStat) + (u & 1) * 512;
+        stat[wg * 256 + r] = m;
+        stat[wg * 256 + 128 + r] = l;
+        if (bar_sync_or(1, 256, !ok || *abort_flag != 0u)) {
+          ok = false;
+          break;
+        }
+        mo = stat[(wg ^ 1) * 256 + r];
+        lo = stat[(wg ^ 1) * 256 + 128 + r];
+      } else if (!ok) {
+        break;
+      }
       tc_fence_after();
+      const float M = fmaxf(m, mo);
+      const float refM = M == -INFINITY ? 0.f : M;
+      const float fown = ex2_approx(m - refM), foth = ex2_approx(mo - refM);
+      const float L = l * fown + lo * foth;
       if (!idle) {
-        const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+        const float inv = whole ? (L > 0.f || L != L ? 1.f / L : 0.f) : 1.f;
+        // factors of the two accumulators, in two steps where 2^(X - kUp) needs it
+        float f0 = (wg == 0 ? fown : foth) * inv, f1 = (wg == 0 ? foth : fown) * inv, e0 = 1.f, e1 = 1.f;
+        if constexpr (kF8) {
+          const int x1 = reinterpret_cast<volatile const int*>(smem + C::kOffX)[(g_end - 1) & 7] - kTreeUp8;
+          const int x2 = count > 1 ? reinterpret_cast<volatile const int*>(smem + C::kOffX)[(g_end - 2) & 7] - kTreeUp8 : x1;
+          const int xa = ((g_end - 1) & 1) == 0 ? x1 : x2, xb = ((g_end - 1) & 1) == 0 ? x2 : x1;
+          f0 *= two_to(xa >> 1);
+          e0 = two_to(xa - (xa >> 1));
+          f1 *= two_to(xb >> 1);
+          e1 = two_to(xb - (xb >> 1));
+        }
+        // an accumulator no block has written holds anything
+        const bool has0 = count >= ST || (g_end - 1) % ST == 0, has1 = ST == 2 && (count > 1 || ((g_end - 1) & 1) == 1);
         const bool odd = tag[u % kTileTags] == static_cast<uint32_t>(u + 1);
 #pragma unroll 1
-        for (int q = 0; q < D / 32; ++q) {
-          uint32_t o[32];
-          tmem_ld32(tl + C::kColO + q * 32, o);
+        for (int q = wg * (D / 32 / ST); q < (wg + 1) * (D / 32 / ST); ++q) {
+          uint32_t o[32], w[32];
+          tmem_ld32(tl + C::col_o(0) + q * 32, o);
+          if constexpr (ST == 2) tmem_ld32(tl + C::col_o(1) + q * 32, w);
           tmem_wait_ld();
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            float v = has0 ? __uint_as_float(o[k]) * f0 : 0.f;
+            if (kF8) v *= e0;
+            if constexpr (ST == 2) {
+              float v1 = has1 ? __uint_as_float(w[k]) * f1 : 0.f;
+              if (kF8) v1 *= e1;
+              v += v1;
+            }
+            o[k] = __float_as_uint(v);
+          }
           if (odd) tile_add_nonfinite<kF8>(p, done, saw, q * 32, D, o);
           if (row_done && whole) {
             uint4* dst = reinterpret_cast<uint4*>(p.o + orow * D + q * 32);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              uint32_t w[4];
+              uint32_t v[4];
 #pragma unroll
               for (int i = 0; i < 4; ++i)
-                w[i] = pack_bf16x2(__uint_as_float(o[8 * k + 2 * i]) * inv, __uint_as_float(o[8 * k + 2 * i + 1]) * inv);
-              dst[k] = make_uint4(w[0], w[1], w[2], w[3]);
+                v[i] = pack_bf16x2(__uint_as_float(o[8 * k + 2 * i]), __uint_as_float(o[8 * k + 2 * i + 1]));
+              dst[k] = make_uint4(v[0], v[1], v[2], v[3]);
             }
           } else if (row_done) {
             uint4* dst = reinterpret_cast<uint4*>(p.st_o + at * D + q * 32);
@@ -799,22 +927,26 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
             for (int k = 0; k < 8; ++k) dst[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
           }
         }
-        if (row_done && whole) {
-          p.lse[lrow] = l > 0.f || l != l ? m * 0.69314718055994531f + logf(l) : -INFINITY;
-        } else if (row_done) {
-          p.st_m[at] = m;
-          p.st_l[at] = l;
+        if (row_done && wg == 0) {
+          if (whole) {
+            p.lse[lrow] = L > 0.f || L != L ? M * 0.69314718055994531f + logf(L) : -INFINITY;
+          } else {
+            p.st_m[at] = M;
+            p.st_l[at] = L;
+          }
         }
       }
-      // o~ has been read out: the next piece's first P V comes after this thread's next arrival
+      // both accumulators have been read by this warp: the next piece's products may write them
       tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_o_free);
       if (front) {
         has_tail = true;
-        if (r == 0) p.meta[cta] = make_int4(done.b, done.h, done.tile, done.owner);
+        if (wg == 0 && r == 0) p.meta[cta] = make_int4(done.b, done.h, done.tile, done.owner);
       }
       ++u;
     }
-    if (!has_tail && r == 0) p.meta[cta] = make_int4(0, 0, 0, -1);
+    if (!has_tail && wg == 0 && r == 0) p.meta[cta] = make_int4(0, 0, 0, -1);
   }
 
   tc_fence_before();
