@@ -222,6 +222,8 @@ def status_sync(stream=None):
 
 
 def release_workspace():
+    """Free the workspaces kept for attn_fwd_host and attn_fwd_tree."""
+    _tree_workspaces.clear()
     _check(load_library().attn_release_workspace())
 
 
@@ -423,7 +425,7 @@ def _elsewhere(dev, stream):
     if dev.type != "cuda":
         raise ValueError("the cache must be on a CUDA device")
     if stream is None:
-        return None if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+        return None if torch._C._cuda_getDevice() == dev.index else torch.cuda.device(dev)
     if stream.device != dev:
         raise ValueError("stream is on another device than the tensors")
     both = contextlib.ExitStack()
@@ -487,10 +489,12 @@ def attn_cache_read(k_cache, v_cache, block_table, cu_seqlens, total, K=None, V=
     cache = _cache_args(k_cache, v_cache, k_scale, v_scale)
     B, max_pages, start_ptr = _batch_args(dev, block_table, cu_seqlens, start_lens)
     shape = (total, cache.num_heads, cache.d)
-    if K is None:
+    if K is None and V is None:
+        K, V = torch.empty((2,) + shape, dtype=torch.bfloat16, device=dev).unbind(0)  # one allocation
+    elif K is None:
         K = torch.empty(shape, dtype=torch.bfloat16, device=dev)
-    if V is None:
-        V = torch.empty_like(K)
+    elif V is None:
+        V = torch.empty(shape, dtype=torch.bfloat16, device=dev)
     for t in (K, V):
         if t.shape != shape or t.dtype != torch.bfloat16 or t.device != dev or not t.is_contiguous():
             raise ValueError("K and V must be contiguous bf16 tensors [total, Hkv, d] on the cache's device")
@@ -507,6 +511,21 @@ def tree_workspace_bytes(Hq, Hkv, max_seqlen_q, d) -> int:
     return load_library().attn_tree_workspace_bytes(Hq, Hkv, max_seqlen_q, d)
 
 
+_tree_workspaces = {}  # (device index, stream) -> uint8 tensor
+
+
+def _tree_workspace(nbytes, dev, raw):
+    """attn_fwd_tree's default workspace: one kept for each stream, whose calls run one after the
+    other; a captured call gets its own, which belongs to the graph (graphs may run at once)."""
+    import torch
+    if torch._C._cuda_isCurrentStreamCapturing():
+        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    ws = _tree_workspaces.get((dev.index, raw))
+    if ws is None or ws.numel() < nbytes:
+        ws = _tree_workspaces[dev.index, raw] = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    return ws
+
+
 def attn_fwd_tree(Q, k_cache, v_cache, block_table, ctx_lens, cu_seqlens_q, max_seqlen_q, O=None, LSE=None, *,
                   tree_mask=None, k_scale=None, v_scale=None, scale=None, workspace=None, stream=None):
     """Attention of each sequence's new (drafted) tokens over its paged cache.
@@ -518,8 +537,8 @@ def attn_fwd_tree(Q, k_cache, v_cache, block_table, ctx_lens, cu_seqlens_q, max_
     lets it see token u of its sequence (None: a chain, u <= i); every token sees the context.
     One token per sequence is plain decoding.  Returns O [total_q, Hq, d] and LSE [Hq, total_q]
     (allocated when not given).  workspace: a CUDA uint8 tensor of tree_workspace_bytes(...)
-    that no other call in flight uses, allocated here when not given.  The cache's arguments: as
-    attn_cache_write.
+    that no other call in flight uses; when not given, one kept for the stream (a captured call
+    gets its own; release_workspace() lets them go).  The cache's arguments: as attn_cache_write.
     """
     import torch
     dev = k_cache.device
@@ -551,17 +570,17 @@ def attn_fwd_tree(Q, k_cache, v_cache, block_table, ctx_lens, cu_seqlens_q, max_
         LSE = torch.empty((Hq, total_q), dtype=torch.float32, device=dev)
     elif LSE.shape != (Hq, total_q) or LSE.dtype != torch.float32 or LSE.device != dev or not LSE.is_contiguous():
         raise ValueError("LSE must be a contiguous fp32 tensor [Hq, total_q]")
+    raw = torch._C._cuda_getCurrentRawStream(dev.index)
     if workspace is None:
         nbytes = lib.attn_tree_workspace_bytes(Hq, cache.num_heads, max_seqlen_q, d)
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        workspace = _tree_workspace(nbytes, dev, raw)
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the cache's device")
     else:
         nbytes = workspace.numel() * workspace.element_size()
     rc = lib.attn_fwd_tree(Q.data_ptr(), cache, O.data_ptr(), LSE.data_ptr(), block_table.data_ptr(), max_pages,
                            cu_seqlens_q.data_ptr(), ctx_ptr, mask_ptr, B, Hq, max_seqlen_q, total_q,
-                           1.0 / math.sqrt(d) if scale is None else scale, workspace.data_ptr(), nbytes,
-                           torch._C._cuda_getCurrentRawStream(dev.index))
+                           1.0 / math.sqrt(d) if scale is None else scale, workspace.data_ptr(), nbytes, raw)
     if rc != 0:
         _check(rc)
     return O, LSE

@@ -143,7 +143,7 @@ TreeSpace tree_space(int rows, int ctas, int d) {
   s.m = up(n * d * 4);
   s.l = s.m + up(n * 4);
   s.meta = s.l + up(n * 4);
-  s.total = s.meta + up(static_cast<size_t>(ctas) * sizeof(int4));
+  s.total = s.meta + up(static_cast<size_t>(2 * ctas) * sizeof(int4));
   return s;
 }
 
@@ -185,6 +185,7 @@ attn_status launch_tree(const attn_cache* c, attn::TreeParams p, void* ws, cudaS
   p.meta = reinterpret_cast<int4*>(w + sp.meta);
   // Measured on GB300 (0, 2, 4, 8, 14 tried): 7 chains over contexts of 0 to 5000 tokens at d = 64
   // 94, 36, 29, 28, 32 us; 64 sequences of 1000 to 16384 e4m3 tokens 227, 209, 198, 204, 215 us.
+  p.fan = 1;
   p.unit_cost = D == 128 ? 4 : 6;
   cudaError_t e = launch_pdl(kernel, grid, attn::kTreeThreads, C::kSmem, stream, mk, mv, p);
   if (e == cudaSuccess)
@@ -226,7 +227,12 @@ attn_status launch_tile(const attn_cache* c, attn::TreeParams p, void* ws, cudaS
     if ((st = cache_map(&mk, c->k, c, p.box_rows)) != ATTN_OK) return st;
     if ((st = cache_map(&mv, c->v, c, p.box_rows)) != ATTN_OK) return st;
   }
-  const unsigned grid = static_cast<unsigned>(std::min(kTileMaxCtas, sm_count(dev)));
+  // Two CTAs walk the same keys with a tile each, so that the second reads them from L2, where
+  // the keys' bandwidth is the limit (256-byte rows) and sequences have more than a tile of
+  // tokens on average.  Measured on GB300 against a unit a tile: 131072 tokens, 64 drafts, 4 heads
+  // a group 166 -> 132 us; 32 sequences with 1 to 64 drafts, a tile or less on average, 79 -> 107.
+  p.fan = !kF8 && D == 128 && p.total_q > static_cast<long long>(p.tok_tile) * p.B ? 2 : 1;
+  const unsigned grid = static_cast<unsigned>(std::min(kTileMaxCtas, std::max(sm_count(dev), p.fan)) / p.fan * p.fan);
   const TreeSpace sp = tree_space(attn::kTileRows, kTileMaxCtas, D);
   uint8_t* w = static_cast<uint8_t*>(ws);
   p.st_o = reinterpret_cast<float*>(w + sp.o);
@@ -276,6 +282,9 @@ attn_status attn_cache_write(const attn_cache* cache, const void* K, const void*
   p.k_sh = k_strides[1];
   p.v_st = v_strides[0];
   p.v_sh = v_strides[1];
+  const int groups = cache->d == 128 ? attn::CacheTile<128>::kGroups : attn::CacheTile<64>::kGroups;
+  p.step_t = groups / cache->num_heads;
+  p.step_h = groups % cache->num_heads;
   int dev;
   uint32_t* status;
   if ((st = cache_device(&dev, &status, &p.page_word)) != ATTN_OK) return st;

@@ -44,6 +44,7 @@ struct CacheParams {
   const int32_t* start;     // [B] first position of each sequence's rows, or null (0)
   int B, Hkv, num_pages, page, max_pages;
   int total;                // packed rows
+  int step_t, step_h;       // write: a block's row groups, in tokens and heads
   const __nv_bfloat16* src_k;  // write: packed K and V, element (t, h, x) at t * st + h * sh + x
   const __nv_bfloat16* src_v;
   long long k_st, k_sh, v_st, v_sh;
@@ -69,11 +70,11 @@ __device__ __forceinline__ long long cache_row_of(const CacheParams& p, int tok)
   if (tok < first || tok >= __ldg(p.cu + lo + 1)) return -1;
   const int start = p.start ? max(__ldg(p.start + lo), 0) : 0;
   const long long pos = static_cast<long long>(start) + (tok - first);
-  const long long slot = pos / p.page;
-  if (slot >= p.max_pages) return -2;
+  if (pos >= static_cast<long long>(p.max_pages) * p.page) return -2;
+  const int slot = static_cast<int>(static_cast<uint32_t>(pos) / static_cast<uint32_t>(p.page));  // pos < 2^31
   const int pg = __ldg(p.table + static_cast<long long>(lo) * p.max_pages + slot);
   if (static_cast<unsigned>(pg) >= static_cast<unsigned>(p.num_pages)) return -2;
-  return static_cast<long long>(pg) * p.Hkv * p.page + (pos - slot * p.page);
+  return static_cast<long long>(pg) * p.Hkv * p.page + (pos - static_cast<long long>(slot) * p.page);
 }
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
@@ -114,6 +115,20 @@ __device__ __forceinline__ uint32_t finite_max(const uint4& x) {
   return m;
 }
 
+// Elementwise maximum of two bf16 pairs; a NaN yields to the other operand.
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// Largest |x| of eight bf16 that is no NaN, as its bits; 0 if all are.
+__device__ __forceinline__ uint32_t number_max(const uint4& x) {
+  uint32_t m = max_bf16x2(max_bf16x2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu), max_bf16x2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu));
+  m = max_bf16x2(m, 0u);
+  return max(m & 0xffffu, m >> 16);
+}
+
 // Scale code of a row whose largest finite |x| has these bf16 bits: with a = (1 + mm / 128) *
 // 2^(ef - 127) and 448 = 1.75 * 2^8, e is ef - 135 while 1 + mm / 128 <= 1.75, else one more.
 __device__ __forceinline__ uint32_t scale_code(uint32_t bits) {
@@ -134,11 +149,12 @@ __device__ __forceinline__ uint32_t under_top(uint32_t w) {
 
 __device__ __forceinline__ uint2 quantise8(uint4 x, uint32_t s) {
   if (s == kTopScale) x = make_uint4(under_top(x.x), under_top(x.y), under_top(x.z), under_top(x.w));
-  const float inv = scale_of(254u - s);
-  uint2 r;
-  r.x = pack_e4m3x2(bf16_lo(x.x) * inv, bf16_hi(x.x) * inv) | (pack_e4m3x2(bf16_lo(x.y) * inv, bf16_hi(x.y) * inv) << 16);
-  r.y = pack_e4m3x2(bf16_lo(x.z) * inv, bf16_hi(x.z) * inv) | (pack_e4m3x2(bf16_lo(x.w) * inv, bf16_hi(x.w) * inv) << 16);
-  return r;
+  const float2 inv = make_float2(scale_of(254u - s), scale_of(254u - s));
+  auto two = [&](uint32_t w) {
+    const float2 v = __fmul2_rn(make_float2(bf16_lo(w), bf16_hi(w)), inv);
+    return pack_e4m3x2(v.x, v.y);
+  };
+  return make_uint2(two(x.x) | (two(x.y) << 16), two(x.z) | (two(x.w) << 16));
 }
 
 __device__ __forceinline__ uint4 dequantise8(const uint2& c, float scale) {
@@ -152,6 +168,13 @@ __device__ __forceinline__ uint4 dequantise8(const uint2& c, float scale) {
   return r;
 }
 
+// 16 bytes that are read once: past L1, which keeps cu_seqlens and the block table.
+__device__ __forceinline__ uint4 ld_stream(const uint4* p) {
+  uint4 r;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+  return r;
+}
+
 // A block owns (token, head) rows [blockIdx * kPerBlock, ...) in packed order.
 template <int D>
 struct CacheTile {
@@ -160,22 +183,27 @@ struct CacheTile {
   static constexpr int kPerBlock = kGroups * kCacheUnroll;
 };
 
-// Cache rows of the tokens this block touches, into shared memory.
+// Token of a (token, head) row; the 64-bit division only where it is needed.
+__device__ __forceinline__ int cache_token(long long item, int heads) {
+  if ((item >> 32) == 0) return static_cast<int>(static_cast<uint32_t>(item) / static_cast<uint32_t>(heads));
+  return static_cast<int>(item / heads);
+}
+
+// Cache rows of the tokens of the kPerBlock rows from item0 on, into shared memory.
 template <int D>
 __device__ __forceinline__ void cache_rows(const CacheParams& p, long long item0, long long items, long long* rows) {
-  const int tok0 = static_cast<int>(item0 / p.Hkv);
+  const int tok0 = cache_token(item0, p.Hkv);
   const long long last = min(item0 + CacheTile<D>::kPerBlock, items) - 1;
-  const int ntok = static_cast<int>(last / p.Hkv) - tok0 + 1;
+  const int ntok = cache_token(last, p.Hkv) - tok0 + 1;
   for (int i = threadIdx.x; i < ntok; i += kCacheThreads) {
     const long long r = cache_row_of(p, tok0 + i);
     if (r == -2 && p.page_word) atomicOr(p.page_word, 1u);
     rows[i] = r;
   }
-  __syncthreads();
 }
 
 template <int D, bool kF8>
-__global__ void __launch_bounds__(kCacheThreads) attn_cache_write_kernel(const CacheParams p) {
+__global__ void __launch_bounds__(kCacheThreads, 4) attn_cache_write_kernel(const CacheParams p) {
   using C = CacheTile<D>;
   __shared__ long long rows[C::kPerBlock];
   griddep_wait();
@@ -183,34 +211,50 @@ __global__ void __launch_bounds__(kCacheThreads) attn_cache_write_kernel(const C
   const long long items = static_cast<long long>(p.total) * p.Hkv;
   const long long item0 = static_cast<long long>(blockIdx.x) * C::kPerBlock;
   const int group = threadIdx.x / C::kLanes, lane = threadIdx.x % C::kLanes;
-  const int tok0 = static_cast<int>(item0 / p.Hkv);
+  const int tok0 = cache_token(item0, p.Hkv);
   uint4 xk[kCacheUnroll], xv[kCacheUnroll];
   int tok[kCacheUnroll], head[kCacheUnroll];
+  int t = cache_token(min(item0 + group, items - 1), p.Hkv);
+  int h = static_cast<int>(min(item0 + group, items - 1) - static_cast<long long>(t) * p.Hkv);
 #pragma unroll
   for (int u = 0; u < kCacheUnroll; ++u) {
-    const long long it = item0 + u * C::kGroups + group;
-    tok[u] = -1;
-    head[u] = 0;
+    tok[u] = item0 + u * C::kGroups + group < items ? t : -1;
+    head[u] = h;
     xk[u] = xv[u] = make_uint4(0, 0, 0, 0);
-    if (it < items) {
-      const int t = static_cast<int>(it / p.Hkv);
-      tok[u] = t;
-      head[u] = static_cast<int>(it - static_cast<long long>(t) * p.Hkv);
-      xk[u] = __ldg(reinterpret_cast<const uint4*>(p.src_k + t * p.k_st + head[u] * p.k_sh) + lane);
-      xv[u] = __ldg(reinterpret_cast<const uint4*>(p.src_v + t * p.v_st + head[u] * p.v_sh) + lane);
+    if (tok[u] >= 0) {
+      xk[u] = ld_stream(reinterpret_cast<const uint4*>(p.src_k + t * p.k_st + h * p.k_sh) + lane);
+      xv[u] = ld_stream(reinterpret_cast<const uint4*>(p.src_v + t * p.v_st + h * p.v_sh) + lane);
+    }
+    // kGroups rows further: p.step_t tokens and p.step_h heads
+    t += p.step_t;
+    h += p.step_h;
+    if (h >= p.Hkv) {
+      h -= p.Hkv;
+      ++t;
     }
   }
   cache_rows<D>(p, item0, items, rows);
+  __syncthreads();
 #pragma unroll
   for (int u = 0; u < kCacheUnroll; ++u) {
     const long long r0 = tok[u] >= 0 ? rows[tok[u] - tok0] : -1;
     const long long r = r0 + static_cast<long long>(head[u]) * p.page;
     if constexpr (kF8) {
-      uint32_t mk = finite_max(xk[u]), mv = finite_max(xv[u]);
+      // both maxima in one word for the shuffles; an infinity (the maximum of finite values is
+      // wanted) sends the row the long way
+      uint32_t m = number_max(xk[u]) | (number_max(xv[u]) << 16);
 #pragma unroll
-      for (int o = C::kLanes / 2; o > 0; o >>= 1) {  // every lane of the warp, rows written or not
-        mk = max(mk, __shfl_xor_sync(0xffffffffu, mk, o));
-        mv = max(mv, __shfl_xor_sync(0xffffffffu, mv, o));
+      for (int o = C::kLanes / 2; o > 0; o >>= 1)  // every lane of the warp, rows written or not
+        m = max_bf16x2(m, __shfl_xor_sync(0xffffffffu, m, o));
+      uint32_t mk = m & 0xffffu, mv = m >> 16;
+      if (__any_sync(0xffffffffu, mk >= 0x7f80u || mv >= 0x7f80u)) {
+        mk = finite_max(xk[u]);
+        mv = finite_max(xv[u]);
+#pragma unroll 1
+        for (int o = C::kLanes / 2; o > 0; o >>= 1) {
+          mk = max(mk, __shfl_xor_sync(0xffffffffu, mk, o));
+          mv = max(mv, __shfl_xor_sync(0xffffffffu, mv, o));
+        }
       }
       const uint32_t sk = scale_code(mk), sv = scale_code(mv);
       if (r0 >= 0) {
@@ -237,8 +281,9 @@ __global__ void __launch_bounds__(kCacheThreads) attn_cache_read_kernel(const Ca
   const long long items = static_cast<long long>(p.total) * p.Hkv;
   const long long item0 = static_cast<long long>(blockIdx.x) * C::kPerBlock;
   const int group = threadIdx.x / C::kLanes, lane = threadIdx.x % C::kLanes;
-  const int tok0 = static_cast<int>(item0 / p.Hkv);
+  const int tok0 = cache_token(item0, p.Hkv);
   cache_rows<D>(p, item0, items, rows);
+  __syncthreads();
   uint4 xk[kCacheUnroll], xv[kCacheUnroll];
   long long src[kCacheUnroll];
 #pragma unroll
@@ -247,7 +292,7 @@ __global__ void __launch_bounds__(kCacheThreads) attn_cache_read_kernel(const Ca
     src[u] = -1;  // a row in no sequence: left as it was
     xk[u] = xv[u] = make_uint4(0, 0, 0, 0);
     if (it < items) {
-      const int t = static_cast<int>(it / p.Hkv);
+      const int t = cache_token(it, p.Hkv);
       const long long r0 = rows[t - tok0];
       src[u] = r0;
       if (r0 >= 0) {

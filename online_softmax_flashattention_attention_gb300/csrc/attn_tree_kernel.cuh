@@ -63,12 +63,14 @@ struct TreeParams {
   int cap;                     // max_pages * page: positions the table has room for
   int box_rows;                // keys a copy takes (128-row tiles): 16 .. 128, divides the page
   int tok_tile;                // tokens a 128-row tile holds (kRows = 128)
+  int fan;                     // CTAs that walk a list of units together, a tile each (1: every tile its own unit)
   int unit_cost;               // what a unit costs beside its chunks, in chunks (see tree_plan)
   float c;                     // scale * log2(e)
   float* st_o;                 // [2 * CTAs, kRows, d] states of shared units
   float* st_m;                 // [2 * CTAs, kRows] log2 units
   float* st_l;
-  int4* meta;                  // [CTAs]: (sequence, head, tile, last CTA) of the unit whose front is CTA's slot 1; w < 0: none
+  int4* meta;                  // [2 * CTAs]: (first row, drafted tokens, head, tile), (last CTA, ..) of the unit
+                               // whose front is the CTA's slot 1; last CTA < 0: none
   uint32_t* status;            // bounded waits
   uint32_t* page_word;         // bad pages
   unsigned long long timeout_ns;
@@ -79,7 +81,7 @@ struct TreeSeq {
   int q0, T;    // first packed row, drafted tokens
   int ctx, n;   // context keys, keys in all
   int nch;      // chunks of keys (1 at least while there are rows)
-  int tiles;    // row tiles of one head
+  int tiles;    // row tiles of one head (of fan tiles each)
 };
 
 template <int kRows, int kChunk>
@@ -91,7 +93,7 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeParams& p, int b) {
   s.ctx = p.ctx ? min(max(__ldg(p.ctx + b), 0), p.cap) : 0;
   s.n = static_cast<int>(min(static_cast<long long>(s.ctx) + s.T, static_cast<long long>(p.cap)));
   s.nch = s.T > 0 ? max(1, s.n / kChunk + (s.n % kChunk != 0)) : 0;
-  s.tiles = kRows == 16 ? (s.T * p.G + kRows - 1) / kRows : (s.T + p.tok_tile - 1) / p.tok_tile;
+  s.tiles = kRows == 16 ? (s.T * p.G + kRows - 1) / kRows : (s.T + p.tok_tile * p.fan - 1) / (p.tok_tile * p.fan);
   return s;
 }
 
@@ -149,6 +151,31 @@ __device__ __forceinline__ void tree_plan(const TreeParams& p, int gs, long long
   __syncthreads();
 }
 
+// x / y for 0 <= x, 0 < y: 32 bits wide where both fit (a 64-bit division costs about as much
+// as a global load).
+__device__ __forceinline__ long long tree_div(long long x, long long y) {
+  if (((x | y) >> 32) == 0) return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
+  return x / y;
+}
+
+// The places [x0, x1) of CTA `cta` of `grid`: the first `extra` CTAs have per + 1, the others per.
+struct TreeRange {
+  long long per, extra, x0, x1;
+};
+__device__ __forceinline__ TreeRange tree_range(long long W, long long cta, long long grid) {
+  TreeRange r;
+  r.per = tree_div(W, grid);
+  r.extra = W - r.per * grid;
+  r.x0 = r.per * cta + min(cta, r.extra);
+  r.x1 = r.x0 + r.per + (cta < r.extra ? 1 : 0);
+  return r;
+}
+// The CTA whose range holds place x.
+__device__ __forceinline__ int tree_owner(const TreeRange& r, long long x) {
+  const long long big = r.extra * (r.per + 1);
+  return static_cast<int>(x < big ? tree_div(x, r.per + 1) : r.extra + tree_div(x - big, max(r.per, 1ll)));
+}
+
 // The piece that starts at place x of the list and ends with its unit or at x_end.
 template <int kRows, int kChunk>
 __device__ __forceinline__ TreePiece tree_piece(const TreeParams& p, int gs, const long long* pre, long long x,
@@ -173,9 +200,7 @@ __device__ __forceinline__ TreePiece tree_piece(const TreeParams& p, int gs, con
     base += w;
   }
   const long long y = x - base;
-  // 32-bit division where it fits (a 64-bit one costs about as much as a global load)
-  const int unit = y <= 0xffffffffll ? static_cast<int>(static_cast<uint32_t>(y) / static_cast<uint32_t>(len))
-                                     : static_cast<int>(y / len);
+  const int unit = static_cast<int>(tree_div(y, len));
   pc.h = unit / max(pc.s.tiles, 1);
   pc.tile = unit - pc.h * pc.s.tiles;
   const int off = static_cast<int>(y - static_cast<long long>(unit) * len);
@@ -184,12 +209,6 @@ __device__ __forceinline__ TreePiece tree_piece(const TreeParams& p, int gs, con
   pc.ch0 = max(0, off - p.unit_cost);
   pc.ch1 = max(0, end - p.unit_cost);
   return pc;
-}
-
-// The CTA whose range holds place x: the first `extra` CTAs have per + 1 places, the others per.
-__device__ __forceinline__ int tree_owner(long long x, long long per, long long extra) {
-  const long long big = extra * (per + 1);
-  return static_cast<int>(x < big ? x / (per + 1) : extra + (x - big) / max(per, 1ll));
 }
 
 // Drafted nodes token t of a sequence sees, as bits.
@@ -339,10 +358,9 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<D, kF8>::kCtas)
   tree_plan<kTreeRows, kChunk>(p, gs, pre, pre + kPlanGroups + 1);  // its barriers also publish the mbarriers
 
   const long long W = pre[kPlanGroups];
-  const int grid = static_cast<int>(gridDim.x), cta = static_cast<int>(blockIdx.x);
-  const long long per = W / grid, extra = W % grid;  // the first `extra` CTAs take one chunk more
-  const long long x0 = per * cta + min(static_cast<long long>(cta), extra);
-  const long long x1 = x0 + per + (cta < extra ? 1 : 0);
+  const int cta = static_cast<int>(blockIdx.x);
+  const TreeRange range = tree_range(W, cta, gridDim.x);
+  const long long x0 = range.x0, x1 = range.x1;
   bool has_tail = false;
 
   // ---- loads: an iterator over this warp's slices, kStages ahead of the products
@@ -836,13 +854,14 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<D, kF8>::kCtas)
       has_tail = true;
       if (threadIdx.x == 0) {
         // the CTA that holds the unit's last chunk
-        p.meta[cta] = make_int4(pc.b, pc.h, pc.tile, ok ? tree_owner(x + (pc.s.nch - pc.ch1) - 1, per, extra) : -1);
+        p.meta[2 * cta] = make_int4(pc.s.q0, pc.s.T, pc.h, pc.tile);
+        p.meta[2 * cta + 1] = make_int4(ok ? tree_owner(range, x + (pc.s.nch - pc.ch1) - 1) : -1, 0, 0, 0);
       }
     }
     __syncthreads();  // the statistics may be overwritten
     if (!ok) break;
   }
-  if (!has_tail && threadIdx.x == 0) p.meta[cta] = make_int4(0, 0, 0, -1);
+  if (!has_tail && threadIdx.x == 0) p.meta[2 * cta + 1] = make_int4(-1, 0, 0, 0);
   // after a failed wait copies may still be in flight: let them land
   if (live) {
 #pragma unroll 1
@@ -852,7 +871,7 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<D, kF8>::kCtas)
 }
 
 // Units shared by several CTAs: CTA c's slot 1 holds the front of one, slot 0 of the CTAs after
-// it, up to meta[c].w, the rest.  A warp merges a row: every state is moved to the largest
+// it (every fan-th), up to the one in meta, the rest.  A warp merges a row: every state is moved to the largest
 // reference, the sums add in CTA order (no atomics: the same bits every time), one division.
 template <int D, int kRows>
 __global__ void __launch_bounds__(128) attn_tree_merge_kernel(const TreeParams p) {
@@ -861,13 +880,15 @@ __global__ void __launch_bounds__(128) attn_tree_merge_kernel(const TreeParams p
   griddep_wait();
   griddep_launch_dependents();
   const int cta = static_cast<int>(blockIdx.x);
-  const int4 mt = p.meta[cta];
-  if (mt.w < 0) return;
+  const int4 unit = p.meta[2 * cta], last = p.meta[2 * cta + 1];
+  if (last.x < 0) return;
   const int row = blockIdx.y * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  const TreeSeq s = tree_seq<kRows, 1>(p, mt.x);
+  TreeSeq s;
+  s.q0 = unit.x;
+  s.T = unit.y;
   int tok, g;
-  if (!tree_row<kRows>(p, s, mt.z, row, &tok, &g)) return;
-  const int count = mt.w - cta + 1;
+  if (!tree_row<kRows>(p, s, unit.w, row, &tok, &g)) return;
+  const int count = (last.x - cta) / p.fan + 1;
   float M = -INFINITY, L = 0.f;
   float acc[kPer];
 #pragma unroll
@@ -881,7 +902,7 @@ __global__ void __launch_bounds__(128) attn_tree_merge_kernel(const TreeParams p
 #pragma unroll
       for (int k = 0; k < kPer; ++k) os[i][k] = 0.f;
       if (c0 + i < count) {
-        const long long at = static_cast<long long>(2 * (cta + c0 + i) + (c0 + i == 0 ? 1 : 0)) * kRows + row;
+        const long long at = static_cast<long long>(2 * (cta + (c0 + i) * p.fan) + (c0 + i == 0 ? 1 : 0)) * kRows + row;
         ms[i] = p.st_m[at];
         ls[i] = p.st_l[at];
         const float* src = p.st_o + at * D + lane * kPer;
@@ -916,7 +937,7 @@ __global__ void __launch_bounds__(128) attn_tree_merge_kernel(const TreeParams p
     M = mc;
   }
   const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
-  const int head = mt.y * p.G + g;
+  const int head = unit.z * p.G + g;
   __nv_bfloat16* dst = p.o + (static_cast<long long>(s.q0 + tok) * p.Hq + head) * D + lane * kPer;
   if constexpr (kPer == 4)
     *reinterpret_cast<uint2*>(dst) =

@@ -171,6 +171,12 @@ __device__ __forceinline__ int tile_next_x(int x, bool first, const uint8_t* cod
   return first || t > x + 7 ? t : x;
 }
 
+__device__ __forceinline__ uint64_t policy_evict_normal() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+
 // Infinities and NaN among the drafted values of a piece, which went into the product as zero,
 // to a row that sees their keys: columns col .. col + 31 of its o~ (a positive weight leaves
 // them what they are).
@@ -288,10 +294,10 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const long long W = pre[kPlanGroups];
-  const int grid = static_cast<int>(gridDim.x), cta = static_cast<int>(blockIdx.x);
-  const long long per = W / grid, extra = W % grid;
-  const long long x0 = per * cta + min(static_cast<long long>(cta), extra);
-  const long long x1 = x0 + per + (cta < extra ? 1 : 0);
+  const int cta = static_cast<int>(blockIdx.x);
+  // fan > 1: neighbouring CTAs walk the same places, each with its tile of every unit
+  const TreeRange range = tree_range(W, cta / p.fan, gridDim.x / p.fan);
+  const long long x0 = range.x0, x1 = range.x1;
 
   // Every role walks the same pieces; g counts their blocks, u the pieces themselves.  The
   // producer finds them (a search and a few global loads) and announces them to the others.
@@ -305,15 +311,17 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
   };
   if (warp == kTileWarpTma) {
     // ================================================================ producer
-    const uint64_t pol = policy_evict_first();
+    // with several tiles a neighbour reads the same keys a little later, or earlier
+    const uint64_t pol = p.fan > 1 ? policy_evict_normal() : policy_evict_first();
     const int box16 = p.box_rows / 16;  // slices a box holds
     int g = 0, u = 0;
     uint32_t k_live = 0, k_par = 0, v_live = 0, v_par = 0;
     bool ok = true;
     for (long long x = x0; ok && x < x1;) {
-      const TreePiece pc = tree_piece<kTileRows, kTileKeys>(p, gs, pre, x, x1);
+      TreePiece pc = tree_piece<kTileRows, kTileKeys>(p, gs, pre, x, x1);
       x += pc.adv;
-      if (pc.ch1 <= pc.ch0) continue;
+      pc.tile = pc.tile * p.fan + cta % p.fan;
+      if (pc.ch1 <= pc.ch0 || pc.tile * p.tok_tile >= pc.s.T) continue;
       if (lane == 0) {
         TileJob t = {};
         t.q0 = pc.s.q0;
@@ -326,7 +334,7 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
         t.nch = pc.s.nch;
         t.ch0 = pc.ch0;
         t.ch1 = pc.ch1;
-        t.owner = tree_owner(x + (pc.s.nch - pc.ch1) - 1, per, extra);
+        t.owner = tree_owner(range, x + (pc.s.nch - pc.ch1) - 1) * p.fan + cta % p.fan;
         *job_at(u) = t;
         mbar_arrive(bar_piece(u % kTilePieces));
       }
@@ -730,19 +738,22 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
           tmem_wait_st();
         }
         const float4* ks = reinterpret_cast<const float4*>(smem + C::kOffScaleK + (g & 7) * 512);
-        // 32 columns at a time, loaded twice (maximum, then exponentials) in rolled loops: a row's
-        // 128 columns unrolled are code enough for the instruction cache to be the limit, cold at
-        // a launch's start and beside the converters' code.
-        auto scores = [&](int q, float* s) {  // 32 scores (e4m3: times their keys' scales)
-          uint32_t e[32];
-          tmem_ld32(tl + colS + q * 32, e);
-          if constexpr (kF8) {
-            float4 f[8];
+        // A row's 128 scores go 32 at a time (64 with one stream, where nothing else covers the
+        // loads), loaded twice, for the maximum and for the exponentials, in rolled loops: unrolled
+        // they are code enough for the instruction cache to be the limit, cold at a launch's start
+        // and beside the converters' code.
+        constexpr int CW = ST == 1 ? 64 : 32;
+        auto scores = [&](int q, float* s) {  // CW scores (e4m3: times their keys' scales)
+          uint32_t e[CW];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) f[k] = ks[q * 8 + k];
+          for (int i = 0; i < CW / 32; ++i) tmem_ld32(tl + colS + q * CW + 32 * i, e + 32 * i);
+          if constexpr (kF8) {
+            float4 f[CW / 4];
+#pragma unroll
+            for (int k = 0; k < CW / 4; ++k) f[k] = ks[q * (CW / 4) + k];
             tmem_wait_ld();
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
+            for (int k = 0; k < CW / 4; ++k) {
               const float2 a = __fmul2_rn(make_float2(__uint_as_float(e[4 * k]), __uint_as_float(e[4 * k + 1])),
                                           make_float2(f[k].x, f[k].y));
               const float2 b = __fmul2_rn(make_float2(__uint_as_float(e[4 * k + 2]), __uint_as_float(e[4 * k + 3])),
@@ -755,23 +766,21 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
           } else {
             tmem_wait_ld();
 #pragma unroll
-            for (int k = 0; k < 32; ++k) s[k] = __uint_as_float(e[k]);
+            for (int k = 0; k < CW; ++k) s[k] = __uint_as_float(e[k]);
           }
         };
         float mx = -INFINITY;
+        float s[CW];
 #pragma unroll 1
-        for (int q = 0; q < kTileKeys / 32; ++q) {
-          float s[32];
+        for (int q = 0; q < kTileKeys / CW; ++q) {
           scores(q, s);
           float a[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) a[i] = fmax3(s[2 * i], s[2 * i + 1], s[8 + 2 * i]);
+          for (int i = 0; i < 4; ++i) a[i] = fmaxf(s[2 * i], s[2 * i + 1]);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) a[i] = fmax3(a[i], s[9 + 2 * i], s[16 + 2 * i]);
+          for (int k = 8; k < CW; k += 8)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) a[i] = fmax3(a[i], s[17 + 2 * i], s[24 + 2 * i]);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) a[i] = fmaxf(a[i], s[25 + 2 * i]);
+            for (int i = 0; i < 4; ++i) a[i] = fmax3(a[i], s[k + 2 * i], s[k + 2 * i + 1]);
           mx = fmax3(mx, fmaxf(a[0], a[1]), fmaxf(a[2], a[3]));
         }
         mx *= c;
@@ -792,24 +801,26 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
         const float2 c2 = make_float2(c, c), nm2 = make_float2(kUp - ref, kUp - ref);
         float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
 #pragma unroll 1
-        for (int q = 0; q < kTileKeys / 32; ++q) {
-          float s[32];
+        for (int q = 0; q < kTileKeys / CW; ++q) {
           scores(q, s);
-          uint32_t pk[16];
 #pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            float2 e = __ffma2_rn(make_float2(s[2 * k], s[2 * k + 1]), c2, nm2);
-            e.x = ex2_approx(e.x);
-            e.y = ex2_approx(e.y);
-            if (k & 1)
-              acc1 = __fadd2_rn(acc1, e);
-            else
-              acc0 = __fadd2_rn(acc0, e);
-            // P rounds once: to bf16 (relative 2^-8 at most) or f16, as in attn_tree_kernel
-            pk[k] = kF8 ? pack_f16x2(e.x, e.y) : pack_bf16x2(e.x, e.y);
+          for (int i = 0; i < CW / 32; ++i) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              float2 e = __ffma2_rn(make_float2(s[32 * i + 2 * k], s[32 * i + 2 * k + 1]), c2, nm2);
+              e.x = ex2_approx(e.x);
+              e.y = ex2_approx(e.y);
+              if (k & 1)
+                acc1 = __fadd2_rn(acc1, e);
+              else
+                acc0 = __fadd2_rn(acc0, e);
+              // P rounds once: to bf16 (relative 2^-8 at most) or f16, as in attn_tree_kernel
+              pk[k] = kF8 ? pack_f16x2(e.x, e.y) : pack_bf16x2(e.x, e.y);
+            }
+            // over S: columns CW / 2 q .. of the buffer held scores that are used by now
+            tmem_st16(tl + colS + q * (CW / 2) + 16 * i, pk);
           }
-          // over S: columns 16 q .. of the buffer held scores of chunk q / 2, which are used
-          tmem_st16(tl + colS + q * 16, pk);
         }
         const float2 acc = __fadd2_rn(acc0, acc1);
         l += acc.x + acc.y;
@@ -942,11 +953,14 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
       if (lane == 0) mbar_arrive(bar_o_free);
       if (front) {
         has_tail = true;
-        if (wg == 0 && r == 0) p.meta[cta] = make_int4(done.b, done.h, done.tile, done.owner);
+        if (wg == 0 && r == 0) {
+          p.meta[2 * cta] = make_int4(done.q0, done.T, done.h, done.tile);
+          p.meta[2 * cta + 1] = make_int4(done.owner, 0, 0, 0);
+        }
       }
       ++u;
     }
-    if (!has_tail && wg == 0 && r == 0) p.meta[cta] = make_int4(0, 0, 0, -1);
+    if (!has_tail && wg == 0 && r == 0) p.meta[2 * cta + 1] = make_int4(-1, 0, 0, 0);
   }
 
   tc_fence_before();
