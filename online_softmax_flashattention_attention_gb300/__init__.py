@@ -489,12 +489,10 @@ def attn_cache_read(k_cache, v_cache, block_table, cu_seqlens, total, K=None, V=
     cache = _cache_args(k_cache, v_cache, k_scale, v_scale)
     B, max_pages, start_ptr = _batch_args(dev, block_table, cu_seqlens, start_lens)
     shape = (total, cache.num_heads, cache.d)
-    if K is None and V is None:
-        K, V = torch.empty((2,) + shape, dtype=torch.bfloat16, device=dev).unbind(0)  # one allocation
-    elif K is None:
+    if K is None:
         K = torch.empty(shape, dtype=torch.bfloat16, device=dev)
-    elif V is None:
-        V = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    if V is None:
+        V = torch.empty_like(K)
     for t in (K, V):
         if t.shape != shape or t.dtype != torch.bfloat16 or t.device != dev or not t.is_contiguous():
             raise ValueError("K and V must be contiguous bf16 tensors [total, Hkv, d] on the cache's device")

@@ -32,6 +32,8 @@
 // rows that see them get them added in the epilogue, rows that do not never meet them.
 #pragma once
 
+#include <type_traits>
+
 #include "attn_tree_kernel.cuh"
 
 namespace attn {
@@ -68,16 +70,14 @@ struct TileCfg {
   static constexpr int kTileBytes = kSub * kSubBytes;    // a block of K, V or Q in bf16
   static constexpr int kRawBytes = 128 * D;              // a block in e4m3
   // Rings: K and V blocks as they arrive, and (e4m3) V blocks in bf16
-  static constexpr int kRingK = kF8 ? 4 : (D == 64 ? 4 : 3);
-  static constexpr int kRingV = kF8 ? 3 : kRingK;
+  static constexpr int kRingK = D == 64 ? 4 : 3;
+  static constexpr int kRingV = kF8 ? kRingK - 1 : kRingK;
   static constexpr int kWide = kF8 ? (D == 64 ? 3 : 2) : 0;
   static constexpr int kStageK = kF8 ? kRawBytes : kTileBytes;
   static constexpr int kStageV = kStageK;
   static constexpr int kSBufs = kStreams * D + 3 * 128 <= 512 ? 3 : 2;  // what tensor memory has room for
   static constexpr int kOffQ = 0;
-  // e4m3: hi, then lo.  At d = 128 each row's two terms take the very bytes of its bf16 row
-  // (128 in each sub-tile), so a thread overwrites only what it has read; at d = 64 they lie beside.
-  static constexpr int kOffQ8 = kF8 && D == 64 ? kTileBytes : 0;
+  static constexpr int kOffQ8 = kF8 ? kTileBytes : 0;    // e4m3: hi, then lo
   static constexpr int kOffK = kOffQ8 + kTileBytes;
   static constexpr int kOffV = kOffK + kRingK * kStageK;
   static constexpr int kOffWide = kOffV + kRingV * kStageV;
@@ -89,8 +89,8 @@ struct TileCfg {
   static constexpr int kOffStat = kOffX + (kF8 ? 32 : 0);   // m, l of each stream, piece u % 2
   static constexpr int kOffBar = kOffStat + (kStreams == 2 ? 2 * 4 * 512 : 0);
   // q_full, q_free, q8_full, {k_full, k_free, k_ready}[RK], {v_full, v_free, v_fixed}[RV],
-  // {w_full, w_free}[W], {s_full, pv_done, p_full}[B], drain[2], o_free, piece[16]
-  static constexpr int kNumBars = 3 + 3 * kRingK + 3 * kRingV + 2 * kWide + 3 * kSBufs + 3 + kTilePieces;
+  // {w_full, w_free}[W], {s_full, pv_done, p_full}[B], drain[2], o_free, q8_free, piece[16]
+  static constexpr int kNumBars = 3 + 3 * kRingK + 3 * kRingV + 2 * kWide + 3 * kSBufs + 4 + kTilePieces;
   static constexpr int kOffPieces = (kOffBar + 8 * kNumBars + 15) / 16 * 16;
   static constexpr int kOffPre = kOffPieces + kTilePieces * 48;
   static constexpr int kOffMisc = kOffPre + 8 * (kPlanGroups + 1 + 4);  // tmem base, abort, valid[16], tags[16]
@@ -236,7 +236,8 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
   auto bar_p_full = [&](int b) { return bar0 + 8u * (kB1 + 2 * NB + b); };
   auto bar_drain = [&](int i) { return bar0 + 8u * (kB1 + 3 * NB + i); };
   const uint32_t bar_o_free = bar0 + 8u * (kB1 + 3 * NB + 2);  // both groups have read a piece's o~
-  auto bar_piece = [&](int i) { return bar0 + 8u * (kB1 + 3 * NB + 3 + i); };
+  const uint32_t bar_q8_free = bar0 + 8u * (kB1 + 3 * NB + 3);  // e4m3: hi and lo have been read
+  auto bar_piece = [&](int i) { return bar0 + 8u * (kB1 + 3 * NB + 4 + i); };
   long long* pre = reinterpret_cast<long long*>(smem + C::kOffPre);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + C::kOffMisc + 4);
@@ -251,8 +252,9 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
 
   if (threadIdx.x == 0) {
     mbar_init(bar_q_full, 1);
-    mbar_init(bar_q_free, 1);
+    mbar_init(bar_q_free, kF8 ? 4 : 1);
     mbar_init(bar_q8_full, 4);
+    mbar_init(bar_q8_free, 1);
     for (int s = 0; s < RK; ++s) {
       mbar_init(bar_k_full(s), 1);
       mbar_init(bar_k_free(s), 1);
@@ -461,7 +463,7 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
             mma_commit(bar_k_free(st));
           }
           if (!ok) break;
-          mma_commit(bar_q_free);
+          mma_commit(kF8 ? bar_q8_free : bar_q_free);
         } else {
           const uint32_t vlo = ((kF8 ? sbase + C::kOffWide : sV) >> 4) | (static_cast<uint32_t>(C::kSubBytes >> 4) << 16);
           if (u > 0) ok = mbar_wait(bar_o_free, (u - 1) & 1, wc, 56);
@@ -568,8 +570,9 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
       bool ok = true;
       TileJob pc;
       while (job(u, pc, ok, 53)) {
-        // ---- Q: a row's largest value, then hi and lo over it
-        ok = __all_sync(0xffffffffu, mbar_wait(bar_q_full, u & 1, wc, 43));
+        // ---- Q: a row's largest value, then its two terms
+        ok = mbar_wait(bar_q_full, u & 1, wc, 43) && (u == 0 || mbar_wait(bar_q8_free, (u - 1) & 1, wc, 57));
+        ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         auto q_at = [&](int c) {
           return *reinterpret_cast<const uint4*>(smem + C::kOffQ + (c / 8) * C::kSubBytes + r * 128 + (((c & 7) ^ (r & 7)) << 4));
@@ -587,19 +590,15 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
         // a row that is not finite has scores that are not
         reinterpret_cast<float*>(smem + C::kOffScaleQ)[(u & 7) * 128 + r] =
             fine ? p.c * __uint_as_float((ef - 7u) << 23) : __uint_as_float(0x7fffffffu);
-        // Chunk c of hi and of lo (16 columns) from chunks 2 c, 2 c + 1 of bf16.  At d = 128 the
-        // terms lie over the row itself, hi over its columns 0 - 63, lo over 64 - 127, each in
-        // the order its chunks are swizzled, so all of it is read before any is written.
-        uint4 q[D / 8];
-#pragma unroll
-        for (int c = 0; c < D / 8; ++c) q[c] = q_at(c);
-#pragma unroll
-        for (int c = 0; c < D / 16; ++c) {
+#pragma unroll 1
+        for (int c = 0; c < D / 16; ++c) {  // 16 columns: chunks 2 c, 2 c + 1 of bf16, chunk c of hi and of lo
+          const uint4 q0 = q_at(2 * c), q1 = q_at(2 * c + 1);
+          const uint32_t w[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
           uint32_t hi[4], lo[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {  // four values each
-            const uint32_t w0 = (&q[2 * c + i / 2].x)[(i & 1) * 2], w1 = (&q[2 * c + i / 2].x)[(i & 1) * 2 + 1];
-            const float f0 = bf16_lo(w0) * up, f1 = bf16_hi(w0) * up, f2 = bf16_lo(w1) * up, f3 = bf16_hi(w1) * up;
+            const float f0 = bf16_lo(w[2 * i]) * up, f1 = bf16_hi(w[2 * i]) * up;
+            const float f2 = bf16_lo(w[2 * i + 1]) * up, f3 = bf16_hi(w[2 * i + 1]) * up;
             const uint32_t h0 = pack_e4m3x2(f0, f1), h1 = pack_e4m3x2(f2, f3);
             const float2 b0 = e4m3x2_to_f32(h0), b1 = e4m3x2_to_f32(h1);
             hi[i] = h0 | (h1 << 16);
@@ -612,7 +611,10 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar_q8_full);
+        if (lane == 0) {
+          mbar_arrive(bar_q8_full);
+          mbar_arrive(bar_q_free);
+        }
         for (int j = pc.ch0; j < pc.ch1; ++j, ++g) {
           const int sv = g % RV, sw = g % NWm, kb = j * kTileKeys;
           // ---- V: codes times scale over 2^X as f16
@@ -743,11 +745,11 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
         // they are code enough for the instruction cache to be the limit, cold at a launch's start
         // and beside the converters' code.
         constexpr int CW = ST == 1 ? 64 : 32;
-        auto scores = [&](int q, float* s) {  // CW scores (e4m3: times their keys' scales)
+        auto scores = [&](int q, float* s, auto raw) {  // CW scores (raw, e4m3: times their keys' scales)
           uint32_t e[CW];
 #pragma unroll
           for (int i = 0; i < CW / 32; ++i) tmem_ld32(tl + colS + q * CW + 32 * i, e + 32 * i);
-          if constexpr (kF8) {
+          if constexpr (kF8 && decltype(raw)::value) {
             float4 f[CW / 4];
 #pragma unroll
             for (int k = 0; k < CW / 4; ++k) f[k] = ks[q * (CW / 4) + k];
@@ -773,7 +775,14 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
         float s[CW];
 #pragma unroll 1
         for (int q = 0; q < kTileKeys / CW; ++q) {
-          scores(q, s);
+          scores(q, s, std::true_type{});
+          if constexpr (kF8) {  // scaled, for the second pass
+            uint32_t e[CW];
+#pragma unroll
+            for (int k = 0; k < CW; ++k) e[k] = __float_as_uint(s[k]);
+#pragma unroll
+            for (int i = 0; i < CW / 32; ++i) tmem_st32(tl + colS + q * CW + 32 * i, e + 32 * i);
+          }
           float a[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) a[i] = fmaxf(s[2 * i], s[2 * i + 1]);
@@ -783,6 +792,7 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
             for (int i = 0; i < 4; ++i) a[i] = fmax3(a[i], s[k + 2 * i], s[k + 2 * i + 1]);
           mx = fmax3(mx, fmaxf(a[0], a[1]), fmaxf(a[2], a[3]));
         }
+        if constexpr (kF8) tmem_wait_st();
         mx *= c;
         const float m_new = mx > m + kTau ? mx : m;
         const float ref = m_new == -INFINITY ? 0.f : m_new;
@@ -802,7 +812,7 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
         float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
 #pragma unroll 1
         for (int q = 0; q < kTileKeys / CW; ++q) {
-          scores(q, s);
+          scores(q, s, std::false_type{});
 #pragma unroll
           for (int i = 0; i < CW / 32; ++i) {
             uint32_t pk[16];
