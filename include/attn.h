@@ -317,7 +317,8 @@ attn_status attn_fwd_splitkv(const void* Q, const void* K, const void* V, void* 
  *
  * Types.  ATTN_CACHE_BF16: rows as they are.  ATTN_CACHE_E4M3: 8-bit codes with one scale per
  * (token, head) row, k_scale and v_scale uint8 [num_pages, Hkv, page_size]; a value is
- * code * 2^(s - 127), s in 1 .. 254 (a code of 0 or 255 makes the row 0 or NaN).
+ * code * 2^(s - 127), s in 1 .. 254 (attn_cache_write makes 1 .. 247).  A scale code of 0
+ * stands for a factor of 2^-126 or less, one of 255 for one that is not finite.
  *
  * Bad pages.  A block-table entry outside [0, num_pages), or a position at or past
  * max_pages * page_size, never leads outside the cache: a token without a page is not
@@ -386,12 +387,16 @@ attn_status attn_cache_read(const attn_cache* cache, void* K, void* V, const int
  *         ignored; a token sees itself only if its own bit is set).  NULL: a chain, u <= i.
  *         A row that sees nothing gets O = 0 and LSE = -inf.  What K and V hold where a row
  *         does not look, infinities and NaN among it, does not reach the row.
+ *   The running maximum may trail by a factor of 2^8 (as attn_options.rescale_threshold
+ *   describes), so sums must stay in range with that: keys * 2^8 * max|V| < 3.4e38.
  *   max_seqlen_q  in [0, 64], >= the most tokens of a sequence (rows past it are left as they
  *         were, as are rows of Q outside every sequence).
  *   workspace  device, attn_tree_workspace_bytes(...) bytes, 16-byte aligned, this call's own
  *         until it has finished: calls that may run at the same time (other streams, graphs)
  *         each need one.  Its contents mean nothing between calls.
- *   Asynchronous, allocates nothing.  Errors: as attn_fwd, plus ATTN_ERR_BAD_SHAPE for
+ *   Asynchronous, allocates nothing; device-side timeouts through attn_status_sync or
+ *   attn_cache_check (the environment variables of attn_fwd hold here too, key blocks of 128).
+ *   Errors: as attn_fwd, plus ATTN_ERR_BAD_SHAPE for
  *   max_seqlen_q > 64 or Hq not a multiple, ATTN_ERR_BAD_ARG for a small workspace.
  */
 attn_status attn_fwd_tree(const void* Q, const attn_cache* cache, void* O, float* LSE, const int32_t* block_table,

@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import threading
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libattn.so")
@@ -488,6 +489,7 @@ def attn_cache_read(k_cache, v_cache, block_table, cu_seqlens, total, K=None, V=
                                    k_scale=k_scale, v_scale=v_scale)
     cache = _cache_args(k_cache, v_cache, k_scale, v_scale)
     B, max_pages, start_ptr = _batch_args(dev, block_table, cu_seqlens, start_lens)
+    total = int(total)
     shape = (total, cache.num_heads, cache.d)
     if K is None:
         K = torch.empty(shape, dtype=torch.bfloat16, device=dev)
@@ -509,18 +511,20 @@ def tree_workspace_bytes(Hq, Hkv, max_seqlen_q, d) -> int:
     return load_library().attn_tree_workspace_bytes(Hq, Hkv, max_seqlen_q, d)
 
 
-_tree_workspaces = {}  # (device index, stream) -> uint8 tensor
+_tree_workspaces = {}  # (device index, stream, thread) -> uint8 tensor
 
 
 def _tree_workspace(nbytes, dev, raw):
-    """attn_fwd_tree's default workspace: one kept for each stream, whose calls run one after the
-    other; a captured call gets its own, which belongs to the graph (graphs may run at once)."""
+    """attn_fwd_tree's default workspace: one kept for each stream and host thread, whose calls run
+    one after the other (two threads may interleave their launches on a stream); a captured call
+    gets its own, which belongs to the graph (graphs may run at once)."""
     import torch
     if torch._C._cuda_isCurrentStreamCapturing():
         return torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    ws = _tree_workspaces.get((dev.index, raw))
+    key = (dev.index, raw, threading.get_ident())
+    ws = _tree_workspaces.get(key)
     if ws is None or ws.numel() < nbytes:
-        ws = _tree_workspaces[dev.index, raw] = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        ws = _tree_workspaces[key] = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     return ws
 
 
@@ -535,8 +539,8 @@ def attn_fwd_tree(Q, k_cache, v_cache, block_table, ctx_lens, cu_seqlens_q, max_
     lets it see token u of its sequence (None: a chain, u <= i); every token sees the context.
     One token per sequence is plain decoding.  Returns O [total_q, Hq, d] and LSE [Hq, total_q]
     (allocated when not given).  workspace: a CUDA uint8 tensor of tree_workspace_bytes(...)
-    that no other call in flight uses; when not given, one kept for the stream (a captured call
-    gets its own; release_workspace() lets them go).  The cache's arguments: as attn_cache_write.
+    that no other call in flight uses; when not given, one kept for the stream and host thread (a
+    captured call gets its own; release_workspace() lets them go).  The cache's arguments: as attn_cache_write.
     """
     import torch
     dev = k_cache.device
@@ -552,6 +556,7 @@ def attn_fwd_tree(Q, k_cache, v_cache, block_table, ctx_lens, cu_seqlens_q, max_
             or not Q.is_contiguous()):
         raise ValueError("Q must be a contiguous bf16 tensor [total_q, Hq, d] on the cache's device")
     total_q, Hq, d = shape
+    max_seqlen_q = int(max_seqlen_q)
     B, max_pages, ctx_ptr = _batch_args(dev, block_table, cu_seqlens_q, ctx_lens)
     mask_ptr = None
     if tree_mask is not None:

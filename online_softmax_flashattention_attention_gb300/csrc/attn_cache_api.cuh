@@ -377,6 +377,7 @@ attn_status attn_fwd_tree(const void* Q, const attn_cache* cache, void* O, float
   p.cap = max_pages * cache->page_size;
   p.c = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
   p.timeout_ns = wait_limit_ns();
+  p.fault_block = fault_block();
   const bool f8 = cache->type == ATTN_CACHE_E4M3;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (cache->d == 128)

@@ -17,15 +17,10 @@
 // the next.  Whole units leave as O and LSE; shared ones as the running state (m, l, o~) in
 // one of the CTA's two workspace slots, merged by attn_tree_merge_kernel.
 //
-// e4m3.  The codes become f16 pairs (exact, one instruction a pair), and so do the other
-// operands.  Q: a row is divided by the power of two of its largest finite value.  P: a
-// probability times its key's scale over the largest scale met so far (2^X, per warp) times
-// 2^10, with the reference m never more than 5 (log2) under the running maximum: at most 2^15,
-// full 11 bits down to 2^-24 of the reference, steps of 2^-34 below.  That is finer than a bf16
-// P (8 bits) wherever a key can matter: below 2^-24, N keys weigh at most N 2^-24 together and
-// are off by N 2^-35.  bf16 operands would cost three more conversions a pair of V; a closer
-// reference (0.9, with 2^15) moves o~ so often that the softmax of a block in
-// attn_tree_tile_kernel took 3050 cycles instead of 2100.
+// e4m3.  K's codes become f16 pairs (exact, one instruction a pair) against a query row divided by
+// the power of two of its largest finite value.  V's become bf16 pairs, exact, and its keys' scales
+// go into P, which therefore is bf16: with f16 (three conversions a pair of V less) a key's scale,
+// seen by a row or not, would decide how small a weight the other keys may have.
 //
 // Inside a CTA each warp takes every fourth slice of 16 or 32 keys of the piece on its own: its own ring
 // of stages filled by TMA, its own (m, l, o~) in registers, no barrier in the loop.  The four
@@ -74,6 +69,7 @@ struct TreeParams {
   uint32_t* status;            // bounded waits
   uint32_t* page_word;         // bad pages
   unsigned long long timeout_ns;
+  int fault_block;             // test hook: the block of 128 keys that is never loaded (-1: none)
 };
 
 // One sequence as the kernels see it, every field clamped to what the buffers hold.
@@ -262,11 +258,6 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return r;
 }
 
-// 2^x for any integer x, 0 or infinity past fp32's range.
-__device__ __forceinline__ float two_to(int x) {
-  return x > 127 ? INFINITY : x >= -126 ? __uint_as_float(static_cast<uint32_t>(x + 127) << 23) : x >= -149 ? __uint_as_float(1u << (x + 149)) : 0.f;
-}
-
 // e4m3 pair -> bf16 pair, exact (every e4m3 value is a bf16).
 __device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t codes) {
   const float2 f = e4m3x2_to_f32(codes);
@@ -279,9 +270,6 @@ __device__ __forceinline__ bool any_nonfinite(uint32_t w) {
 }
 
 constexpr int kTreeRows = 16;
-// e4m3: how far the reference may lag (log2), and the power of two P goes in with
-constexpr float kTreeTau8 = 5.f;
-constexpr int kTreeUp8 = 10;
 constexpr int kTreeWarps = 4;
 constexpr int kTreeThreads = 32 * kTreeWarps;
 
@@ -325,9 +313,7 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<D, kF8>::kCtas)
   constexpr int kKeyTiles = kSlice / 8;
   constexpr int kTilesN = D / 8;   // 8-wide column tiles of o~
   constexpr int kSteps = D / 16;   // 16-deep steps of q . k
-  // o~ is rescaled when the max rises by more than this (log2 units); P is 2^kUp times larger
-  constexpr float kTau = kF8 ? kTreeTau8 : 8.f;
-  constexpr float kUp = kF8 ? kTreeUp8 : 0.f;
+  constexpr float kTau = 8.f;      // o~ is rescaled when the max rises by more (log2 units)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -405,10 +391,11 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<D, kF8>::kCtas)
     there = (there & ~(((1u << kSubs) - 1u) << (kSubs * ist))) | (boxes << (kSubs * ist));
     if (boxes) {
       const uint32_t bar = bars + 8 * ist;
-      live |= 1u << ist;
-      if (lane == 0) mbar_arrive_expect_tx(bar, __popc(boxes) * C::kBoxBytes);
+      const bool withheld = ps * kSlice / 128 == p.fault_block;
+      if (!withheld) live |= 1u << ist;
+      if (lane == 0 && !withheld) mbar_arrive_expect_tx(bar, __popc(boxes) * C::kBoxBytes);
       __syncwarp();
-      if (have) {
+      if (have && !withheld) {
         const uint32_t dst = ring + ist * C::kStageBytes + 16 * lane * C::kRowBytes;  // lane 0 where kSub > 1
         const int row = static_cast<int>((static_cast<uint32_t>(ps) * kSlice + 16u * lane) % static_cast<uint32_t>(p.page));
 #pragma unroll
@@ -492,8 +479,7 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<D, kF8>::kCtas)
     for (int j = 0; j < kTilesN; ++j)
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[j][i] = 0.f;
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};  // l: this thread's columns only, times 2^kUp
-    int X = -127;  // e4m3: o~ holds the sums times 2^(kUp - X)
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};  // l: this thread's columns only
 
     const long long end = min(static_cast<long long>(pc.ch1) * kChunk, static_cast<long long>(pc.s.n));
     const int s_end = static_cast<int>((end + kSlice - 1) / kSlice);
@@ -519,8 +505,7 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<D, kF8>::kCtas)
         float sc[kKeyTiles][4];
 #pragma unroll
         for (int i = 0; i < 4 * kKeyTiles; ++i) (&sc[0][0])[i] = 0.f;
-        float pv[2 * kKeyTiles];  // e4m3: scales of V of this thread's keys, over 2^X
-        float drop = 1.f;         // what a rise of X takes o~ down by
+        float pv[2 * kKeyTiles];  // e4m3: scales of V of this thread's keys
         if constexpr (!kF8) {
           const int key = (lane >> 4) * 8 + (lane & 7);
 #pragma unroll
@@ -556,38 +541,23 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<D, kF8>::kCtas)
             }
           }
           const uint8_t* kc = scales + st * C::kCodes;
-          uint32_t vc[kKeyTiles];  // codes of V's scales, keys 8 n + 2 t, + 1; 1 for a key that does not exist
-          uint32_t top = 1;
 #pragma unroll
           for (int n = 0; n < kKeyTiles; ++n) {
             const uint32_t a = *reinterpret_cast<const uint16_t*>(kc + 8 * n + 2 * t);
-            vc[n] = *reinterpret_cast<const uint16_t*>(kc + kSlice + 8 * n + 2 * t);
-            if (part) {
-              const bool out = !((boxes >> (n / 2)) & 1u);
-              if (out || 8 * n + 2 * t >= left) vc[n] = (vc[n] & 0xff00u) | 1u;
-              if (out || 8 * n + 2 * t + 1 >= left) vc[n] = (vc[n] & 0x00ffu) | 0x100u;
-            }
-            const uint32_t c0 = vc[n] & 0xffu, c1 = vc[n] >> 8;
-            top = max(top, max(c0 == 255u ? 1u : c0, c1 == 255u ? 1u : c1));
+            const uint32_t b = *reinterpret_cast<const uint16_t*>(kc + kSlice + 8 * n + 2 * t);
             const float f0 = scale_of(a & 0xffu), f1 = scale_of(a >> 8);
             sc[n][0] *= cr[0] * f0;
             sc[n][1] *= cr[0] * f1;
             sc[n][2] *= cr[1] * f0;
             sc[n][3] *= cr[1] * f1;
-          }
-          top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-          top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));  // the same in every lane
-          if (static_cast<int>(top) - 127 > X) {
-            drop = two_to(max(X - (static_cast<int>(top) - 127), -200));
-            X = static_cast<int>(top) - 127;
-          }
-#pragma unroll
-          for (int n = 0; n < kKeyTiles; ++n)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {  // 2^(code - 127 - X): 0 once it is too small; 255 is NaN
-              const int code = static_cast<int>(i ? vc[n] >> 8 : vc[n] & 0xffu);
-              pv[2 * n + i] = code == 255 ? __int_as_float(0x7fffffff) : __int_as_float(max(code - X, 0) << 23);
+            pv[2 * n] = scale_of(b & 0xffu);
+            pv[2 * n + 1] = scale_of(b >> 8);
+            if (part) {  // a key that does not exist may have any code: 0 keeps 0 * scale from being NaN
+              const bool out = !((boxes >> (n / 2)) & 1u);
+              if (out || 8 * n + 2 * t >= left) pv[2 * n] = 0.f;
+              if (out || 8 * n + 2 * t + 1 >= left) pv[2 * n + 1] = 0.f;
             }
+          }
         }
         // ---- masks: every row sees the context; drafted keys go by the row's bits
         const bool draft = k0 + kSlice > pc.s.ctx;
@@ -617,22 +587,16 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<D, kF8>::kCtas)
           alpha[i] = ex2_approx(m[i] - ref);
           move |= mn != m[i];
           m[i] = mn;
-          const float refu = ref - kUp;
           float sum = 0.f;
 #pragma unroll
           for (int n = 0; n < kKeyTiles; ++n)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              const float e = ex2_approx(sc[n][2 * i + j] - refu);
+              const float e = ex2_approx(sc[n][2 * i + j] - ref);
               sum += e;
               sc[n][2 * i + j] = e;
             }
           l[i] = l[i] * alpha[i] + sum;
-        }
-        if constexpr (kF8) {
-          move |= drop != 1.f;
-          alpha[0] *= drop;  // l has had its alpha
-          alpha[1] *= drop;
         }
         if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
@@ -680,15 +644,15 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<D, kF8>::kCtas)
         if (!odd) {
 #pragma unroll
           for (int b = 0; b < kSubs; ++b) {
-            // P rounds once for the product: to bf16 (relative 2^-8 at most; its range keeps small
-            // probabilities next to a large one as precise), or to f16 with e4m3 (see the top)
+            // P rounds to bf16 for the product (relative 2^-8 at most; its range keeps small
+            // probabilities next to a large one as precise)
             uint32_t pf[4];
 #pragma unroll
             for (int n = 0; n < 2; ++n)
 #pragma unroll
               for (int i = 0; i < 2; ++i) {
                 const float a = sc[2 * b + n][2 * i], e = sc[2 * b + n][2 * i + 1];
-                pf[2 * n + i] = kF8 ? pack_f16x2(a * pv[4 * b + 2 * n], e * pv[4 * b + 2 * n + 1]) : pack_bf16x2(a, e);
+                pf[2 * n + i] = kF8 ? pack_bf16x2(a * pv[4 * b + 2 * n], e * pv[4 * b + 2 * n + 1]) : pack_bf16x2(a, e);
               }
             if constexpr (!kF8) {
 #pragma unroll
@@ -711,8 +675,8 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<D, kF8>::kCtas)
                 for (int i = 0; i < 2; ++i) {
                   // codes (key 2t, col 2g), (2t, 2g + 1), (2t + 1, 2g), (2t + 1, 2g + 1) -> pairs of keys
                   const uint32_t y0 = __byte_perm(w[2 * i], 0, 0x3120), y1 = __byte_perm(w[2 * i + 1], 0, 0x3120);
-                  warp_mma_f16(acc[2 * (c0 + i)], pf, e4m3x2_to_f16x2(y0 & 0xffffu), e4m3x2_to_f16x2(y1 & 0xffffu));
-                  warp_mma_f16(acc[2 * (c0 + i) + 1], pf, e4m3x2_to_f16x2(y0 >> 16), e4m3x2_to_f16x2(y1 >> 16));
+                  warp_mma_bf16(acc[2 * (c0 + i)], pf, e4m3x2_to_bf16x2(y0 & 0xffffu), e4m3x2_to_bf16x2(y1 & 0xffffu));
+                  warp_mma_bf16(acc[2 * (c0 + i) + 1], pf, e4m3x2_to_bf16x2(y0 >> 16), e4m3x2_to_bf16x2(y1 >> 16));
                 }
               }
             }
@@ -766,7 +730,7 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<D, kF8>::kCtas)
       l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
       if (t == 0) {
         stat_m[warp * kTreeRows + g + 8 * i] = m[i];
-        stat_l[warp * kTreeRows + g + 8 * i] = kF8 ? l[i] * two_to(-kTreeUp8) : l[i];
+        stat_l[warp * kTreeRows + g + 8 * i] = l[i];
       }
     }
     __syncthreads();
@@ -778,13 +742,6 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<D, kF8>::kCtas)
 #pragma unroll
       for (int w = 1; w < kTreeWarps; ++w) M = fmaxf(M, stat_m[w * kTreeRows + g + 8 * i]);
       f[i] = ex2_approx(m[i] - (M == -INFINITY ? 0.f : M));
-    }
-    if constexpr (kF8) {  // to plain units: o~ 2^(X - kUp), in two steps that stay in range
-      const float a = two_to((X - kTreeUp8) >> 1), b = two_to((X - kTreeUp8) - ((X - kTreeUp8) >> 1));
-#pragma unroll
-      for (int j = 0; j < kTilesN; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[j][i] = acc[j][i] * a * b;
     }
     const int orow = threadIdx.x >> 3, ocol = (threadIdx.x & 7) * 4;  // of the 16 x 32 quarter
     float M = -INFINITY, L = 0.f;

@@ -18,12 +18,12 @@
 //
 // e4m3: the codes of K go to the tensor cores as they are.  A query row, divided by the power
 // of two that brings its largest finite value into [128, 256), is split into two e4m3 terms,
-// q = hi + lo: 8 significant bits are 4 + 4, so the split is exact down to 2^-10 of the row's
-// largest and off by at most 2^-19 of it below, and S = hi K^T + lo K^T in fp32.  The row's
-// power of two and each key's scale multiply the scores afterwards.  V is widened to f16 times
-// its scale over 2^X, X a running exponent of the piece (raised when a block's largest scale
-// passes it by more than 2^7, o~ then scaled down with it), and P goes in as f16 times 2^10,
-// as in attn_tree_kernel.
+// q = hi + lo: 8 significant bits are 4 + 4, so the split is exact for values of 2^-9 of the row's
+// largest and more, and off by at most 2^-17 of it below; S = hi K^T + lo K^T in fp32.  The row's
+// power of two and each key's scale multiply the scores afterwards.  V is widened to bf16 with
+// its scale, exact, and P goes in as bf16.  (V as f16 over a running exponent is two conversions
+// a pair less; but a key's scale, seen by a row or not, would then decide how small a value the
+// other keys may hold.)
 //
 // K and V blocks are up to eight boxes of 16 keys, each from the page it lies in (larger boxes
 // when the page size allows: fewer copies).  A block that holds drafted keys, or keys past the
@@ -85,8 +85,7 @@ struct TileCfg {
   static constexpr int kOffCodeV = kOffCodeK + (kF8 ? kRingK * 128 : 0);
   static constexpr int kOffScaleK = kOffCodeV + (kF8 ? kRingV * 128 : 0);  // floats, block g % 8
   static constexpr int kOffScaleQ = kOffScaleK + (kF8 ? 8 * 512 : 0);      // floats, piece u % 8
-  static constexpr int kOffX = kOffScaleQ + (kF8 ? 8 * 512 : 0);           // X of block g % 8
-  static constexpr int kOffStat = kOffX + (kF8 ? 32 : 0);   // m, l of each stream, piece u % 2
+  static constexpr int kOffStat = kOffScaleQ + (kF8 ? 8 * 512 : 0);   // m, l of each stream, piece u % 2
   static constexpr int kOffBar = kOffStat + (kStreams == 2 ? 2 * 4 * 512 : 0);
   // q_full, q_free, q8_full, {k_full, k_free, k_ready}[RK], {v_full, v_free, v_fixed}[RV],
   // {w_full, w_free}[W], {s_full, pv_done, p_full}[B], drain[2], o_free, q8_free, piece[16]
@@ -101,8 +100,7 @@ struct TileCfg {
   static constexpr uint32_t kIdescS = idesc_bf16_f32(kTileRows, kTileKeys, 0);
   // kind::f8f6f4, e4m3 x e4m3 -> fp32 (the formats' codes are 0)
   static constexpr uint32_t kIdescS8 = (1u << 4) | ((kTileKeys >> 3) << 17) | ((kTileRows >> 4) << 24);
-  // e4m3: f16 x f16 (the formats' codes are 0)
-  static constexpr uint32_t kIdescO = idesc_bf16_f32(kTileRows, D, 1) & ~(kF8 ? (1u << 7) | (1u << 10) : 0u);
+  static constexpr uint32_t kIdescO = idesc_bf16_f32(kTileRows, D, 1);
   static_assert(128 * kSBufs + kStreams * D <= 512, "tensor memory");
 };
 
@@ -124,12 +122,12 @@ __device__ __forceinline__ uint32_t finite_only(uint32_t w) {
   return w;
 }
 
-// Eight e4m3 codes times the scale (an f16 pair of it) as four f16 pairs.
-__device__ __forceinline__ uint4 widen8(uint32_t lo, uint32_t hi, __half2 scale) {
+// Eight e4m3 codes times the scale (a bf16 pair of it) as four bf16 pairs, exact.
+__device__ __forceinline__ uint4 widen8(uint32_t lo, uint32_t hi, __nv_bfloat162 scale) {
   uint4 r;
   auto one = [&](uint32_t c) {
-    const uint32_t w = e4m3x2_to_f16x2(c);
-    const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&w), scale);
+    const uint32_t w = e4m3x2_to_bf16x2(c);
+    const __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w), scale);
     return *reinterpret_cast<const uint32_t*>(&v);
   };
   r.x = one(lo & 0xffffu);
@@ -137,38 +135,6 @@ __device__ __forceinline__ uint4 widen8(uint32_t lo, uint32_t hi, __half2 scale)
   r.z = one(hi & 0xffffu);
   r.w = one(hi >> 16);
   return r;
-}
-
-// f16 counterparts of any_nonfinite and finite_only.
-__device__ __forceinline__ bool any_nonfinite16(uint32_t w) {
-  return (w & 0x7c00u) == 0x7c00u || (w & 0x7c000000u) == 0x7c000000u;
-}
-__device__ __forceinline__ uint32_t finite_only16(uint32_t w) {
-  if ((w & 0x7c00u) == 0x7c00u) w &= 0xffff0000u;
-  if ((w & 0x7c000000u) == 0x7c000000u) w &= 0x0000ffffu;
-  return w;
-}
-
-// 2^k twice as f16, 0 below its range (k <= 7 here).
-__device__ __forceinline__ uint32_t two_to_f16x2(int k) {
-  const uint32_t h = k >= -14 ? static_cast<uint32_t>(k + 15) << 10 : k >= -24 ? 1u << (k + 24) : 0u;
-  return h | (h << 16);
-}
-
-// X after a block of V whose 128 scale codes are at `codes` (a warp's work, the same in all of
-// its lanes and in every warp that does it): the first block's largest scale, then raised when
-// a block's passes it by more than 2^7 (448 * 2^7 is an f16).  Keys that do not exist, and
-// codes of 255, do not count.
-__device__ __forceinline__ int tile_next_x(int x, bool first, const uint8_t* codes, uint32_t vm, int left, int lane) {
-  const uint32_t w = *reinterpret_cast<const volatile uint32_t*>(codes + 4 * lane);
-  uint32_t top = 1;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t c = (w >> (8 * i)) & 0xffu;
-    if (((vm >> (lane / 4)) & 1u) && 4 * lane + i < left && c != 255u) top = max(top, c);
-  }
-  const int t = static_cast<int>(__reduce_max_sync(0xffffffffu, top)) - 127;
-  return first || t > x + 7 ? t : x;
 }
 
 __device__ __forceinline__ uint64_t policy_evict_normal() {
@@ -367,10 +333,10 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
           ok = __all_sync(0xffffffffu, mbar_wait(kv ? bar_v_free(st) : bar_k_free(st), ph ^ 1, wc, 34 + kv));
           if (!ok) break;
           const uint32_t full = kv ? bar_v_full(st) : bar_k_full(st);
-          if (lane == 0) {
-            if (kv == 0) valid[g & 15] = vm;
-            mbar_arrive_expect_tx(full, bytes);
-          }
+          if (lane == 0 && kv == 0) valid[g & 15] = vm;
+          __syncwarp();
+          if (kv == 0 && j == p.fault_block) continue;  // withheld: the waits on it run out
+          if (lane == 0) mbar_arrive_expect_tx(full, bytes);
           __syncwarp();
           if (mine) {
             const uint32_t dst = (kv ? sV + st * C::kStageV : sK + st * C::kStageK) + 16 * lane * kRowB;
@@ -498,7 +464,7 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
     if constexpr (kF8) {
       // ---- scales of K's keys as floats, four a lane.  Entry g % 8: block g's stage was freed
       // by S of block g - 4, which is at most 3 blocks ahead of the softmax.
-      int g = 0, u = 0, x = 0;
+      int g = 0, u = 0;
       bool ok = true;
       TileJob pc;
       while (job(u, pc, ok, 51)) {
@@ -512,11 +478,6 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
           reinterpret_cast<float4*>(smem + C::kOffScaleK)[(g & 7) * 32 + lane] =
               make_float4(scale_of(max(w & 0xffu, 1u)), scale_of(max((w >> 8) & 0xffu, 1u)),
                           scale_of(max((w >> 16) & 0xffu, 1u)), scale_of(max(w >> 24, 1u)));
-          // X, which the softmax needs before the block's P V (the converters find the same)
-          ok = __all_sync(0xffffffffu, mbar_wait(bar_v_full(g % RV), (g / RV) & 1, wc, 55));
-          if (!ok) break;
-          x = tile_next_x(x, j == pc.ch0, smem + C::kOffCodeV + (g % RV) * 128, valid[g & 15], pc.n - j * kTileKeys, lane);
-          if (lane == 0) reinterpret_cast<volatile int*>(smem + C::kOffX)[g & 7] = x;
           __syncwarp();
           if (lane == 0) mbar_arrive(bar_k_ready(st));
         }
@@ -566,7 +527,7 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
       // the instruction cache when unrolled (measured on GB300, one sequence of 131072 tokens,
       // d = 128: 144 us with 8 chunks unrolled, a third of the stalls for want of instructions).
       const int r = threadIdx.x - 384;  // row of Q, key of a block
-      int g = 0, u = 0, vx = 0;
+      int g = 0, u = 0;
       bool ok = true;
       TileJob pc;
       while (job(u, pc, ok, 53)) {
@@ -617,7 +578,7 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
         }
         for (int j = pc.ch0; j < pc.ch1; ++j, ++g) {
           const int sv = g % RV, sw = g % NWm, kb = j * kTileKeys;
-          // ---- V: codes times scale over 2^X as f16
+          // ---- V: codes times scale as bf16
           ok = mbar_wait(bar_v_full(sv), (g / RV) & 1, wc, 45) && mbar_wait(bar_w_free(sw), ((g / NWm) & 1) ^ 1, wc, 46);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
@@ -626,10 +587,9 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
           const bool scan = kb + r >= pc.ctx;
           const uint8_t* src = smem + C::kOffV + sv * C::kStageV + r * D;
           uint8_t* dst = smem + C::kOffWide + sw * C::kTileBytes + r * 128;
-          vx = tile_next_x(vx, j == pc.ch0, smem + C::kOffCodeV + sv * 128, vm, pc.n - kb, lane);
-          const int code = here ? smem[C::kOffCodeV + sv * 128 + r] : 0;
-          const uint32_t two = code == 255 ? 0x7e007e00u : two_to_f16x2(code - 127 - vx);  // 255: NaN
-          const __half2 scale = *reinterpret_cast<const __half2*>(&two);
+          const uint32_t code = smem[C::kOffCodeV + sv * 128 + r];
+          const uint32_t two = (code << 7) | (code << 23);  // 2^(code - 127) twice, as bf16
+          const __nv_bfloat162 scale = *reinterpret_cast<const __nv_bfloat162*>(&two);
           const bool ragged = __any_sync(0xffffffffu, !here || scan);
           bool odd = false;
 #pragma unroll 2
@@ -642,9 +602,9 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
                 uint32_t& e = w[i >> 2][i & 3];
-                if (here && scan && any_nonfinite16(e)) odd = true;
+                if (here && scan && any_nonfinite(e)) odd = true;
                 if (!here) e = 0u;
-                if (scan) e = finite_only16(e);
+                if (scan) e = finite_only(e);
               }
             }
             // 16 columns = chunks 2 c, 2 c + 1 of the wide row, in sub-tile c / 4
@@ -671,10 +631,7 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
     const int r = (warp & 3) * 32 + lane;
     const uint32_t tl = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     float c = p.c;  // e4m3: times the row's power of two, piece by piece
-    // o~ is rescaled when the max rises by more than this (log2 units); P and l are 2^kUp larger
-    constexpr float kTau = kF8 ? kTreeTau8 : 8.f;
-    constexpr float kUp = kF8 ? kTreeUp8 : 0.f;
-    int vx = 0;  // e4m3: o~ holds the sums times 2^(kUp - X)
+    constexpr float kTau = 8.f;  // o~ is rescaled when the max rises by more (log2 units)
     int g = 0, u = 0;
     bool ok = true, has_tail = false;
     // The next piece and this thread's row of it are looked up while the last product of the
@@ -702,7 +659,6 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
       const bool idle = !__any_sync(0xffffffffu, row_here);  // no row of this warp exists
       bool any = false;  // this stream has had a block of the piece
       float m = -INFINITY, l = 0.f;
-      if (kF8) vx = -126;
       for (int j = pc.ch0; j < pc.ch1; ++j, ++g) {
         if (g % ST != wg) continue;
         const int bf = g % NB;
@@ -796,19 +752,11 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
         mx *= c;
         const float m_new = mx > m + kTau ? mx : m;
         const float ref = m_new == -INFINITY ? 0.f : m_new;
-        float alpha = ex2_approx(m - ref);
+        const float alpha = ex2_approx(m - ref);
         l *= alpha;
-        bool moved = m_new != m;
+        const bool moved = m_new != m;
         m = m_new;
-        if constexpr (kF8) {
-          const int nx = reinterpret_cast<volatile const int*>(smem + C::kOffX)[g & 7];
-          if (!first && nx != vx) {  // rises: o~ comes down with it
-            alpha *= two_to(max(vx - nx, -200));
-            moved = true;
-          }
-          vx = nx;
-        }
-        const float2 c2 = make_float2(c, c), nm2 = make_float2(kUp - ref, kUp - ref);
+        const float2 c2 = make_float2(c, c), nm2 = make_float2(-ref, -ref);
         float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
 #pragma unroll 1
         for (int q = 0; q < kTileKeys / CW; ++q) {
@@ -825,8 +773,7 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
                 acc1 = __fadd2_rn(acc1, e);
               else
                 acc0 = __fadd2_rn(acc0, e);
-              // P rounds once: to bf16 (relative 2^-8 at most) or f16, as in attn_tree_kernel
-              pk[k] = kF8 ? pack_f16x2(e.x, e.y) : pack_bf16x2(e.x, e.y);
+              pk[k] = pack_bf16x2(e.x, e.y);  // P rounds once, relative 2^-8 at most
             }
             // over S: columns CW / 2 q .. of the buffer held scores that are used by now
             tmem_st16(tl + colS + q * (CW / 2) + 16 * i, pk);
@@ -879,7 +826,6 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
       // Both streams' statistics, then every thread has half the columns of its row.  Each of the
       // eight warps comes here once a piece, also after a failed wait, and they leave together.
       float mo = -INFINITY, lo = 0.f;             // the other stream's
-      if (kF8) l *= two_to(-kTreeUp8);            // units of states: l 2^-kUp, o~ 2^(X - kUp)
       if constexpr (ST == 2) {
         float* stat = reinterpret_cast<float*>(smem + C::kOffStat) + (u & 1) * 512;
         stat[wg * 256 + r] = m;
@@ -900,17 +846,7 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
       const float L = l * fown + lo * foth;
       if (!idle) {
         const float inv = whole ? (L > 0.f || L != L ? 1.f / L : 0.f) : 1.f;
-        // factors of the two accumulators, in two steps where 2^(X - kUp) needs it
-        float f0 = (wg == 0 ? fown : foth) * inv, f1 = (wg == 0 ? foth : fown) * inv, e0 = 1.f, e1 = 1.f;
-        if constexpr (kF8) {
-          const int x1 = reinterpret_cast<volatile const int*>(smem + C::kOffX)[(g_end - 1) & 7] - kTreeUp8;
-          const int x2 = count > 1 ? reinterpret_cast<volatile const int*>(smem + C::kOffX)[(g_end - 2) & 7] - kTreeUp8 : x1;
-          const int xa = ((g_end - 1) & 1) == 0 ? x1 : x2, xb = ((g_end - 1) & 1) == 0 ? x2 : x1;
-          f0 *= two_to(xa >> 1);
-          e0 = two_to(xa - (xa >> 1));
-          f1 *= two_to(xb >> 1);
-          e1 = two_to(xb - (xb >> 1));
-        }
+        const float f0 = (wg == 0 ? fown : foth) * inv, f1 = (wg == 0 ? foth : fown) * inv;
         // an accumulator no block has written holds anything
         const bool has0 = count >= ST || (g_end - 1) % ST == 0, has1 = ST == 2 && (count > 1 || ((g_end - 1) & 1) == 1);
         const bool odd = tag[u % kTileTags] == static_cast<uint32_t>(u + 1);
@@ -923,12 +859,7 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
 #pragma unroll
           for (int k = 0; k < 32; ++k) {
             float v = has0 ? __uint_as_float(o[k]) * f0 : 0.f;
-            if (kF8) v *= e0;
-            if constexpr (ST == 2) {
-              float v1 = has1 ? __uint_as_float(w[k]) * f1 : 0.f;
-              if (kF8) v1 *= e1;
-              v += v1;
-            }
+            if (ST == 2 && has1) v = fmaf(__uint_as_float(w[k]), f1, v);
             o[k] = __float_as_uint(v);
           }
           if (odd) tile_add_nonfinite<kF8>(p, done, saw, q * 32, D, o);

@@ -3,8 +3,10 @@ token at a time, and the bounds the GPU's results are held to.
 
 Bounds (u = 2^-24, the half step of fp32; 2^-8 that of bf16; L = the row's keys):
 * a score's error is at most ds = d u B + 2 u |s|, B = scale * sum_i |q_i k_i| (fp32 sum of d
-  exact products in any order, then the scaling), for an e4m3 cache also
-  scale * d * 2^-25 max|q| max|k| (query values far under the row's largest, held in f16);
+  exact products in any order, then the scaling); for an e4m3 cache also scale * sum_i e_i |k_i|
+  with e_i what a query value's form may lose: with the row's largest in [1, 2) 2^E, either two
+  e4m3 terms of q 2^(7 - E), off by half their least step 2^-9 where |q 2^(7 - E)| < 1/4 and
+  exact above, or one f16 of q 2^-E, off by 2^-25 where |q 2^-E| < 2^-14;
 * a probability is off by a factor exp(+-2 ds) (its score and the reference) and 4 u (exp2 and
   products), and rounds to bf16 once, 2^-8;
 * l sums L terms in fp32 over 16 partial sums or more: (L / 16 + 64) u;
@@ -75,6 +77,16 @@ def rows_of(c, sc, table, b, n, page):
     return np.stack(out) if out else np.zeros((0,) + c.shape[1:2] + c.shape[3:])
 
 
+def query_loss(q):
+    """What a query row's values may lose in the form an e4m3 cache's kernels give them."""
+    top = np.abs(q).max()
+    if top == 0:
+        return np.zeros_like(q)
+    one = 2.0 ** math.floor(math.log2(top))
+    rel = np.abs(q) / one
+    return one * np.maximum(np.where(rel < 2.0 ** -9, 2.0 ** -17, 0.0), np.where(rel < 2.0 ** -14, 2.0 ** -25, 0.0))
+
+
 def ref_tree(Q, k, v, ks, vs, table, ctx, cu, masks, page, scale):
     """O, LSE and their bounds (fp64): Q [total, Hq, d], caches as fp64."""
     total, Hq, d = Q.shape
@@ -106,7 +118,7 @@ def ref_tree(Q, k, v, ks, vs, table, ctx, cu, masks, page, scale):
                 big = scale * (np.abs(Kh) @ np.abs(q)).max()
                 ds = d * U * big + 2 * U * np.abs(s).max()
                 if ks is not None:
-                    ds += scale * d * 2.0 ** -25 * np.abs(q).max() * np.abs(Kh).max()
+                    ds += scale * (np.abs(Kh) @ query_loss(q)).max()
                 sums = (len(see) / 16 + 64) * U
                 tolL[h, cu[b] + i] = ds + sums + 8 * U * (1 + abs(LSE[h, cu[b] + i]))
                 rel[cu[b] + i, h] = HALF_BF16 + 2 * (2 * ds) + 2 * sums + 8 * U

@@ -43,6 +43,9 @@ CASES = [
     (2, 2, 16, [0, 20], [3, 2], "none"),      # no drafted key visible: the first sequence's rows are empty
     (4, 32, 16, [31, 90], [1, 4], "tree"),
     (1, 1, 16, [1500], [1], "chain"),
+    (1, 160, 16, [40], [2], "tree"),          # more heads a group than a tile has rows
+    (1, 16, 32, [700, 90], [64, 41], "tree"),  # several tiles of one head, side by side
+    (2, 9, 64, [300, 5, 0], [50, 29, 33], "random"),
 ]
 
 
@@ -159,7 +162,7 @@ def test_lengths_that_make_no_sense_are_clamped():
 
 @pytest.mark.parametrize("f8", [False, True])
 @pytest.mark.parametrize("d", [64, 128])
-@pytest.mark.parametrize("B,hkv,G,T", [(300, 1, 2, 1), (3, 2, 4, 1), (9, 2, 2, 12), (1, 1, 1, 1)])
+@pytest.mark.parametrize("B,hkv,G,T", [(300, 1, 2, 1), (3, 2, 4, 1), (9, 2, 2, 12), (1, 1, 1, 1), (2, 2, 8, 40), (150, 2, 4, 9)])
 def test_long_ragged_batches_against_dense(B, hkv, G, T, d, f8):
     """Many CTAs a sequence and many sequences a CTA: all rows against a dense fp64 softmax over
     the rows read back from the cache (those are exact), under the same bounds."""
@@ -205,6 +208,10 @@ def test_long_ragged_batches_against_dense(B, hkv, G, T, d, f8):
         A = torch.einsum("thgn,nhd->thgd", p, Vb.abs()).reshape(T, hkv * G, d)
         big = torch.einsum("thgd,nhd->thgn", q.abs(), Kb.abs()).amax() / d ** 0.5
         ds = d * 2.0 ** -24 * big + 2.0 ** -20
+        if f8:  # query values under 2^-9 of the row's largest, as in cache_ref
+            one = torch.exp2(torch.floor(torch.log2(q.abs().amax(-1, keepdim=True))))
+            loss = torch.where(q.abs() < one * 2.0 ** -9, one * 2.0 ** -17, torch.zeros_like(q))
+            ds = ds + torch.einsum("thgd,nhd->thgn", loss, Kb.abs()).amax() / d ** 0.5
         sums = (n[b] / 16 + 64) * 2.0 ** -24
         tol = HALF_BF16 * want.abs() + (HALF_BF16 + 4 * ds + 2 * sums) * 1.01 * A
         err = (O[b * T:(b + 1) * T].double() - want).abs()
@@ -234,6 +241,86 @@ def test_attention_sinks_and_far_scores(f8):
                 b.k[pg, 0, row] = 0
                 b.k[pg, 0, row, 0] = x
         hold(*_run(b), b.reference())
+
+
+@pytest.mark.parametrize("f8", [False, True])
+@pytest.mark.parametrize("G,T", [(2, 5), (8, 20)])
+def test_scales_far_apart(f8, G, T):
+    """Keys whose values are 2^40 and more apart: a huge value that a row does not see, or sees with a
+    weight of 2^-60, leaves the others what they are."""
+    for kind in ("unseen", "weightless"):
+        b = Batch(17, 1, G, 64, 16, f8, [90], [T], scale=1.0)
+        if kind == "unseen":
+            u = T - 1
+            b.masks[: T - 1] &= np.uint64((1 << (T - 1)) - 1)
+            b.masks[T - 1] = np.uint64((1 << (T - 1)) - 1)  # nobody sees the last token
+            pos = 90 + u
+        else:
+            pos = 3
+            b.Q[:, :, 0] = 1.0
+        pg, row = int(b.table[0][pos // 16]), pos % 16
+        if f8:
+            b.vs[pg, :, row] = 230  # 2^103
+            if kind == "weightless":
+                c = torch.zeros(64)
+                c[0] = -60.0
+                b.k[pg, 0, row] = c.to(torch.float8_e4m3fn)
+                b.ks[pg, :, row] = 127
+        else:
+            b.v[pg, :, row] = 2.0 ** 100
+            if kind == "weightless":
+                b.k[pg, 0, row] = 0
+                b.k[pg, 0, row, 0] = -60.0
+        hold(*_run(b), b.reference())
+
+
+def test_two_threads_on_one_stream():
+    """Calls of two host threads with the default workspace, launches interleaved."""
+    import threading
+    pkg = _pkg()
+    a, b = Batch(31, 2, 4, 128, 16, True, [900, 30], [1, 1]), Batch(32, 2, 4, 128, 16, True, [12, 1500], [1, 1])
+    calls = [x.dev() for x in (a, b)]
+    wants = [pkg.attn_fwd_tree(*args, **kw) for args, kw in calls]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(i):
+        args, kw = calls[i]
+        for _ in range(200):
+            O, LSE = pkg.attn_fwd_tree(*args, **kw)
+            if not (torch.equal(O, wants[i][0]) and torch.equal(LSE, wants[i][1])):
+                bad.append(i)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    pkg.cache_check()
+    assert not bad
+
+
+@pytest.mark.parametrize("f8", [False, True])
+@pytest.mark.parametrize("G,T,d", [(1, 1, 64), (4, 1, 128), (8, 9, 64), (8, 9, 128)])
+def test_a_wait_that_runs_out_is_reported(f8, G, T, d, monkeypatch):
+    """A key block that is never loaded: every wait on it ends, the call reports a timeout, and the
+    next call is right again."""
+    pkg = _pkg()
+    b = Batch(51, 2, G, d, 32, f8, [600, 200], [T, T])
+    args, kw = b.dev()
+    want = pkg.attn_fwd_tree(*args, **kw)
+    pkg.cache_check()
+    monkeypatch.setenv("ATTN_WAIT_LIMIT_MS", "20")
+    monkeypatch.setenv("ATTN_ENABLE_TEST_HOOKS", "1")
+    monkeypatch.setenv("ATTN_TEST_WITHHOLD_K_BLOCK", "1")
+    pkg.attn_fwd_tree(*args, **kw)
+    with pytest.raises(pkg.AttnError) as e:
+        pkg.cache_check()
+    assert e.value.status == -7
+    monkeypatch.undo()
+    got = pkg.attn_fwd_tree(*args, **kw)
+    pkg.cache_check()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
 def test_capture_follows_the_lengths():
