@@ -463,9 +463,10 @@ def attn_cache_write(K, V, k_cache, v_cache, block_table, cu_seqlens, *, start_l
     if ks[2] != 1 or vs[2] != 1:
         raise ValueError("K and V must have a contiguous last dimension")
     B, max_pages, start_ptr = _batch_args(dev, block_table, cu_seqlens, start_lens)
-    rc = load_library().attn_cache_write(cache, K.data_ptr(), V.data_ptr(), _Strides(ks[0], ks[1]),
-                                         _Strides(vs[0], vs[1]), block_table.data_ptr(), max_pages,
-                                         cu_seqlens.data_ptr(), start_ptr, B, shape[0],
+    kst = _Strides(ks[0], ks[1])
+    rc = load_library().attn_cache_write(cache, K.data_ptr(), V.data_ptr(), kst,
+                                         kst if vs == ks else _Strides(vs[0], vs[1]), block_table.data_ptr(),
+                                         max_pages, cu_seqlens.data_ptr(), start_ptr, B, shape[0],
                                          torch._C._cuda_getCurrentRawStream(dev.index))
     if rc != 0:
         _check(rc)

@@ -284,8 +284,8 @@ struct TreeCfg {
   static constexpr int kChunk = kTreeWarps * kSlice;             // keys a CTA takes at a time
   static constexpr int kHalf = kSlice * kRowBytes;               // K (or V) of a slice
   static constexpr int kStageBytes = 2 * kHalf;
-  static constexpr int kCtas = kF8 && D == 64 ? 3 : 2;                      // an SM
-  static constexpr int kRingBytes = (kCtas == 3 ? 12 : 24) * 1024 / kStageBytes * kStageBytes;  // of a warp
+  static constexpr int kCtas = kF8 ? 3 : 2;                      // an SM
+  static constexpr int kRingBytes = (kCtas == 3 ? (D == 64 ? 12 : 16) : 24) * 1024 / kStageBytes * kStageBytes;  // of a warp
   static constexpr int kStages = kRingBytes / kStageBytes;
   static constexpr int kSub = kRowBytes > 128 ? kRowBytes / 128 : 1;  // 128-byte wide sub-tiles
   static constexpr int kSubBytes = kHalf / kSub;
@@ -294,8 +294,8 @@ struct TreeCfg {
   static constexpr int kOffScale = kTreeWarps * kRingBytes;
   static constexpr int kOffBar = kOffScale + (kF8 ? kTreeWarps * kStages * kCodes : 0);
   static constexpr int kOffMerge = (kOffBar + kTreeWarps * kStages * 8 + 15) / 16 * 16;
-  static constexpr int kMergeStride = 36;                        // floats a row of 32 columns
-  static constexpr int kOffStat = kOffMerge + kTreeWarps * kTreeRows * kMergeStride * 4;
+  // the warps' states on their way into one, 32 columns at a time; e4m3: the query's fragments before
+  static constexpr int kOffStat = kOffMerge + kTreeWarps * kTreeRows * 32 * 4;
   static constexpr int kOffPre = kOffStat + 2 * kTreeWarps * kTreeRows * 4;
   static constexpr int kOffMisc = kOffPre + (kPlanGroups + 1 + 4) * 8;
   static constexpr int kSmem = kOffMisc + 16 + 1024;             // slack to align the base
@@ -438,7 +438,10 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<D, kF8>::kCtas)
         qrow[i] = p.q + (static_cast<long long>(pc.s.q0 + tok) * p.Hq + pc.h * p.G + head) * D;
       }
     }
-    uint32_t qf[kSteps][4];
+    // The query's fragments: bf16 in registers; e4m3 in shared memory, the same for all four warps,
+    // which leaves registers for a third CTA an SM (measured: NOTE)
+    uint32_t qf[kF8 ? 1 : kSteps][4];
+    uint4* qs = reinterpret_cast<uint4*>(merge);
     if constexpr (!kF8) {
 #pragma unroll
       for (int k = 0; k < kSteps; ++k)
@@ -467,12 +470,14 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<D, kF8>::kCtas)
         cr[i] = p.c * __uint_as_float(ef << 23);
 #pragma unroll
         for (int k = 0; k < kSteps; ++k) {
-          const __half2 lo = __floats2half2_rn(bf16_lo(w[k][i].x) * inv, bf16_hi(w[k][i].x) * inv);
-          const __half2 hi = __floats2half2_rn(bf16_lo(w[k][i].y) * inv, bf16_hi(w[k][i].y) * inv);
-          qf[k][i] = *reinterpret_cast<const uint32_t*>(&lo);
-          qf[k][2 + i] = *reinterpret_cast<const uint32_t*>(&hi);
+          w[k][i].x = pack_f16x2(bf16_lo(w[k][i].x) * inv, bf16_hi(w[k][i].x) * inv);
+          w[k][i].y = pack_f16x2(bf16_lo(w[k][i].y) * inv, bf16_hi(w[k][i].y) * inv);
         }
       }
+#pragma unroll
+      for (int k = 0; k < kSteps; ++k)  // every warp has them all; each stores its share
+        if (k % kTreeWarps == warp) qs[k * 32 + lane] = make_uint4(w[k][0].x, w[k][1].x, w[k][0].y, w[k][1].y);
+      __syncthreads();
     }
     float acc[kTilesN][4];
 #pragma unroll
@@ -528,14 +533,15 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<D, kF8>::kCtas)
           for (int k = 0; k < kSteps; k += 2) {
             const int ch = k + (lane >> 4);
             const uint32_t at = D == 128 ? key * 128 + ((ch ^ (key & 7)) << 4) : key * 64 + ((ch ^ ((key >> 1) & 3)) << 4);
+            const uint4 q[2] = {qs[k * 32 + lane], qs[(k + 1) * 32 + lane]};
 #pragma unroll
             for (int b = 0; b < kSubs; ++b) {
               uint32_t w[4];
               ldsm4(w, sk + 16 * b * C::kRowBytes + at);
 #pragma unroll
               for (int i = 0; i < 2; ++i) {
-                warp_mma_f16(sc[2 * b], qf[k + i], e4m3x2_to_f16x2(w[2 * i] & 0xffffu), e4m3x2_to_f16x2(w[2 * i] >> 16));
-                warp_mma_f16(sc[2 * b + 1], qf[k + i], e4m3x2_to_f16x2(w[2 * i + 1] & 0xffffu),
+                warp_mma_f16(sc[2 * b], &q[i].x, e4m3x2_to_f16x2(w[2 * i] & 0xffffu), e4m3x2_to_f16x2(w[2 * i] >> 16));
+                warp_mma_f16(sc[2 * b + 1], &q[i].x, e4m3x2_to_f16x2(w[2 * i + 1] & 0xffffu),
                              e4m3x2_to_f16x2(w[2 * i + 1] >> 16));
               }
             }
@@ -760,21 +766,21 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<D, kF8>::kCtas)
 #pragma unroll
     for (int q = 0; q < D / 32; ++q) {
       if (q > 0) __syncthreads();  // the quarter before has been read
-      float* dst = merge + warp * kTreeRows * C::kMergeStride;
+      float* dst = merge + warp * kTreeRows * 32;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        float* row = dst + (g + 8 * i) * C::kMergeStride;
+        float* row = dst + (g + 8 * i) * 32;  // its 4-column groups in the order ^ (row & 7): no bank twice
         if constexpr (!kF8) {
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            *reinterpret_cast<float2*>(row + 8 * j + 2 * t) =
+            *reinterpret_cast<float2*>(row + ((2 * j + t / 2) ^ g) * 4 + 2 * (t & 1)) =
                 make_float2(acc[4 * q + j][2 * i] * f[i], acc[4 * q + j][2 * i + 1] * f[i]);
         } else {
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             const float* e = acc[4 * q + 2 * j];
             const float* o = acc[4 * q + 2 * j + 1];
-            *reinterpret_cast<float4*>(row + 16 * j + 4 * t) =
+            *reinterpret_cast<float4*>(row + ((4 * j + t) ^ g) * 4) =
                 make_float4(e[2 * i] * f[i], o[2 * i] * f[i], e[2 * i + 1] * f[i], o[2 * i + 1] * f[i]);
           }
         }
@@ -783,7 +789,7 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<D, kF8>::kCtas)
       float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < kTreeWarps; ++w) {
-        const float4 v = *reinterpret_cast<const float4*>(merge + (w * kTreeRows + orow) * C::kMergeStride + ocol);
+        const float4 v = *reinterpret_cast<const float4*>(merge + (w * kTreeRows + orow) * 32 + (ocol ^ ((orow & 7) * 4)));
         sum.x += v.x;
         sum.y += v.y;
         sum.z += v.z;
