@@ -124,8 +124,8 @@ attn_status cache_map(CUtensorMap* map, const void* ptr, const attn_cache* c, in
   return ATTN_OK;
 }
 
-// Workspace of attn_fwd_tree: room for this many CTAs (two an SM, SMs up to this), whatever
-// the device has, so that its size follows from the arguments alone.
+// Workspace of attn_fwd_tree: room for this many CTAs (up to three an SM, or one), whatever the
+// device has, so that its size follows from the arguments alone.
 constexpr int kTreeMaxCtas = 480;
 constexpr int kTileMaxCtas = 160;
 

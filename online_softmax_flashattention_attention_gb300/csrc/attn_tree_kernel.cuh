@@ -10,8 +10,9 @@
 // and key; below 274 rows a unit memory is the limit.
 //
 // Work split: the keys of all units are laid end to end in chunks of 64 or 128 (and some places
-// for what a unit costs beside them, see tree_plan) and cut into equal ranges, one a CTA (two CTAs an SM), whatever the lengths are; every CTA finds its range from
-// a prefix sum over the sequences, so a captured launch follows the lengths on the device.  A
+// for what a unit costs beside them, see tree_plan) and cut into equal ranges, one a CTA (two
+// CTAs an SM, three with e4m3), whatever the lengths are; every CTA finds its range from a
+// prefix sum over the sequences, so a captured launch follows the lengths on the device.  A
 // CTA's range covers a few whole units and at most two that it shares: its first piece may be
 // the rest of a unit begun by an earlier CTA, its last one the front of a unit that goes on in
 // the next.  Whole units leave as O and LSE; shared ones as the running state (m, l, o~) in
@@ -334,8 +335,10 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<D, kF8>::kCtas)
     fence_mbar_init();
     if (warp == 0) {
       *abort_flag = 0u;
-      tma_prefetch_desc(&tmK);
-      tma_prefetch_desc(&tmV);
+      if (p.num_pages > 0) {  // without pages there are no maps
+        tma_prefetch_desc(&tmK);
+        tma_prefetch_desc(&tmV);
+      }
     }
   }
   griddep_wait();
@@ -439,7 +442,8 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<D, kF8>::kCtas)
       }
     }
     // The query's fragments: bf16 in registers; e4m3 in shared memory, the same for all four warps,
-    // which leaves registers for a third CTA an SM (measured: NOTE)
+    // which leaves registers for a third CTA an SM (64 sequences of 1000 to 16384 tokens, d = 128,
+    // on GB300: 165 -> 145 us)
     uint32_t qf[kF8 ? 1 : kSteps][4];
     uint4* qs = reinterpret_cast<uint4*>(merge);
     if constexpr (!kF8) {

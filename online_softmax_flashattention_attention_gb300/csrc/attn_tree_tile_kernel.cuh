@@ -4,9 +4,15 @@
 // and grouped heads make more rows than one 16-row tile: there every further tile reads the
 // keys again and its warp-level products become the limit.  Here a tile holds the G heads of
 // 128 / G tokens as the 128 lanes of tensor memory, and the products are tcgen05.mma: per
-// block of 128 keys S = Q K^T (128 x 128 x d, into one of two score buffers) and
+// block of 128 keys S = Q K^T (128 x 128 x d, into one of two or three score buffers) and
 // o~ += P V, with P written back over S as bf16.  One CTA an SM, persistent over its range of
 // the list of chunks (128 keys each).
+//
+// Bound: the keys, read once a unit; P V alone is 128 x 128 x d x 2 flops a block whatever the
+// rows, so half-empty tiles make the tensor cores wait longer than the memory.  Measured on
+// GB300: one sequence of 131072 tokens and 64 drafts, 8 K/V heads with 4 query heads each
+// (two tiles a head), d = 128: bf16 123 us, 4.4 TB/s of keys and 4.5 TB/s more from L2 for the
+// second tile; 32 sequences of 1 to 64 drafts over 121 MB of e4m3 keys 64 us.
 //
 // Two streams: blocks of even number go to one group of four softmax warps and accumulator o~,
 // odd ones to the other, so that one group's softmax covers the other's products
@@ -251,15 +257,19 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
   if (warp == kTileWarpPv) tmem_alloc<512>(smem_u32(tmem_slot));
   if (warp == kTileWarpTma && lane == 0) {
     tma_prefetch_desc(&tmQ);
-    tma_prefetch_desc(&tmK);
-    tma_prefetch_desc(&tmV);
+    if (p.num_pages > 0) {  // without pages there are no maps
+      tma_prefetch_desc(&tmK);
+      tma_prefetch_desc(&tmV);
+    }
   }
   griddep_wait();
-  griddep_launch_dependents();
   const int gs = (p.B + kPlanGroups - 1) / kPlanGroups;
   tc_fence_before();
   tree_plan<kTileRows, kTileKeys>(p, gs, pre, pre + kPlanGroups + 1);  // ends with a barrier of the CTA
   tc_fence_after();
+  // not before this CTA has its tensor memory: a later launch that got there first would hold it
+  // until this one ends
+  griddep_launch_dependents();
   const uint32_t tmem = *tmem_slot;
   const long long W = pre[kPlanGroups];
   const int cta = static_cast<int>(blockIdx.x);
@@ -276,6 +286,13 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
     if (!ok) return false;
     t = *job_at(u);
     return t.ch1 > t.ch0;
+  };
+  // The same for a whole warp: one that gives up gives up with all its lanes, whichever of them
+  // the wait ran out for, so that none of them waits for another in a vote.
+  auto job_warp = [&](int u, TileJob& t, bool& ok, uint32_t site) {
+    const bool more = job(u, t, ok, site);
+    ok = __all_sync(0xffffffffu, ok);
+    return ok && more;
   };
   if (warp == kTileWarpTma) {
     // ================================================================ producer
@@ -467,7 +484,7 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
       int g = 0, u = 0;
       bool ok = true;
       TileJob pc;
-      while (job(u, pc, ok, 51)) {
+      while (job_warp(u, pc, ok, 51)) {
         ++u;
         for (int j = pc.ch0; j < pc.ch1; ++j, ++g) {
           const int st = g % RK;
@@ -487,7 +504,7 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
       int g = 0, u = 0;
       bool ok = true;
       TileJob pc;
-      while (job(u, pc, ok, 52)) {
+      while (job_warp(u, pc, ok, 52)) {
         for (int j = pc.ch0; j < pc.ch1; ++j, ++g) {
           const int st = g % RV, kb = j * kTileKeys;
           ok = __all_sync(0xffffffffu, mbar_wait(bar_v_full(st), (g / RV) & 1, wc, 42));
@@ -530,7 +547,7 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
       int g = 0, u = 0;
       bool ok = true;
       TileJob pc;
-      while (job(u, pc, ok, 53)) {
+      while (job_warp(u, pc, ok, 53)) {
         // ---- Q: a row's largest value, then its two terms
         ok = mbar_wait(bar_q_full, u & 1, wc, 43) && (u == 0 || mbar_wait(bar_q8_free, (u - 1) & 1, wc, 57));
         ok = __all_sync(0xffffffffu, ok);
@@ -641,7 +658,7 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
     bool row_here = false;
     unsigned long long sees = 0;
     auto look = [&](int v) {
-      if (!job(v, pc, ok, 54)) return false;
+      if (!job_warp(v, pc, ok, 54)) return false;
       const int t = r / p.G;
       head = r - t * p.G;
       tok = pc.tile * p.tok_tile + t;

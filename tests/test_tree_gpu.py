@@ -368,6 +368,37 @@ def test_other_stream():
 
 
 @pytest.mark.parametrize("f8", [False, True])
+@pytest.mark.parametrize("G,T", [(2, 3), (4, 20)])
+def test_a_pool_without_pages(f8, G, T):
+    """Nothing is cached and nothing can be: rows see nothing, and that is reported."""
+    pkg = _pkg()
+    k = torch.zeros((0, 2, 16, 64), dtype=torch.uint8 if f8 else torch.bfloat16, device="cuda")
+    sc = {}
+    if f8:
+        k = k.view(torch.float8_e4m3fn)
+        s = torch.zeros((0, 2, 16), dtype=torch.uint8, device="cuda")
+        sc = dict(k_scale=s, v_scale=s)
+    Q = torch.ones((2 * T, 2 * G, 64), dtype=torch.bfloat16, device="cuda")
+    cu, ctx = _i32([0, T, 2 * T]), _i32([0, 70])
+    for table in (_i32([[0, 1, 2], [3, -1, 7]]), torch.zeros((2, 0), dtype=torch.int32, device="cuda")):
+        O, LSE = pkg.attn_fwd_tree(Q, k, k, table, ctx, cu, T, **sc)
+        with pytest.raises(pkg.AttnError, match="no page"):
+            pkg.cache_check()
+        assert bool((O == 0).all()) and bool(torch.isneginf(LSE).all())
+    pkg.cache_check()  # told once
+
+
+@pytest.mark.parametrize("f8", [False, True])
+@pytest.mark.parametrize("T", [1, 40])
+def test_output_in_the_query(f8, T):
+    b = Batch(43, 2, 4, 128, 32, f8, [3000, 17, 0], [T, T, 1])
+    args, kw = b.dev()
+    want = _pkg().attn_fwd_tree(*args, **kw)
+    O, _ = _pkg().attn_fwd_tree(*args, args[0], **kw)
+    assert O is args[0] and torch.equal(O, want[0])
+
+
+@pytest.mark.parametrize("f8", [False, True])
 def test_decoding_run(f8):
     """As a program uses them: a prompt through the packed forward and into the cache, drafted
     trees appended and attended to, the prefix read back for a second prompt.  The forward over
