@@ -129,7 +129,11 @@ attn_status cache_map(CUtensorMap* map, const void* ptr, const attn_cache* c, in
 constexpr int kTreeMaxCtas = 480;
 constexpr int kTileMaxCtas = 160;
 
-// Whether a call takes the 128-row tiles.
+// Whether a call takes the 128-row tiles: when a sequence may have more rows than one 16-row
+// tile, whose second tile would read the keys again.  Measured on GB300, 8 K/V heads, d = 128, page
+// 64, 16 rows in the 16-row kernel and 20 in the other: one sequence of 131072 tokens bf16 95 and
+// 90 us, e4m3 66 and 95; 64 sequences of 500 tokens bf16 31 and 40, e4m3
+// 31 and 59.  So up to 16 rows stay with the first.
 bool use_tile_kernel(int G, int max_seqlen_q) { return G <= attn::kTileRows && G * max_seqlen_q > attn::kTreeRows; }
 
 struct TreeSpace {

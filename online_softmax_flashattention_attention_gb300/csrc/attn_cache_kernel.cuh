@@ -18,6 +18,11 @@
 // 16-byte bf16 access a lane, and for the row maximum a few shuffles.  A thread has the loads
 // of kCacheUnroll rows of K and V in flight; in the write they do not depend on where the
 // rows go, so they are issued before the sequence of a token is searched for.
+//
+// Bound: DRAM; the e4m3 write also by instructions (two thirds of the issue slots: the row
+// maximum, eight products and four conversions a lane).  Measured on GB300, 8 heads, d = 128:
+// 9 prompts of 900 to 16384 tokens into an e4m3 cache, 262 MB in 48.4 us, 5.4 TB/s; 6 prefixes of
+// 3000 to 32768 tokens out of one, 772 MB in 126 us, 6.1 TB/s; one token 2.8 us, a launch.
 #pragma once
 
 #include <cuda_bf16.h>
