@@ -130,10 +130,10 @@ constexpr int kTreeMaxCtas = 480;
 constexpr int kTileMaxCtas = 160;
 
 // Whether a call takes the 128-row tiles: when a sequence may have more rows than one 16-row
-// tile, whose second tile would read the keys again.  Measured on GB300, 8 K/V heads, d = 128, page
-// 64, 16 rows in the 16-row kernel and 20 in the other: one sequence of 131072 tokens bf16 95 and
-// 90 us, e4m3 66 and 95; 64 sequences of 500 tokens bf16 31 and 40, e4m3
-// 31 and 59.  So up to 16 rows stay with the first.
+// tile, whose second tile would read the keys again.  Measured on GB300, 32 query and 8 K/V heads,
+// d = 128, page 64, 16 rows in the 16-row kernel and 20 in the other: one sequence of 131072 tokens
+// bf16 94 and 88 us, e4m3 66 and 95; 64 sequences of 500 tokens bf16 36 and 38, e4m3 37 and 52.
+// The other way round, 32 rows: 119 and 89, 106 and 96; 60 and 40, 59 and 52.
 bool use_tile_kernel(int G, int max_seqlen_q) { return G <= attn::kTileRows && G * max_seqlen_q > attn::kTreeRows; }
 
 struct TreeSpace {
@@ -222,7 +222,7 @@ attn_status launch_tile(const attn_cache* c, attn::TreeParams p, void* ws, cudaS
   attn_status st;
   if ((st = set_smem_attr(kernel, C::kSmem, dev, attr_set)) != ATTN_OK) return st;
   p.tok_tile = attn::kTileRows / p.G;
-  p.unit_cost = 6;  // measured: 4, 6 and 8 within 5 %, 8 better for many short sequences, 4 for few long ones
+  p.unit_cost = 4;  // measured (2, 3, 4, 6): within 5 % of the best of them in 18 batches, the others within 10 to 15
   p.box_rows = 128;  // the most keys that no page border cuts
   while (p.page % p.box_rows != 0) p.box_rows /= 2;
   CUtensorMap mq, mk = {}, mv = {};

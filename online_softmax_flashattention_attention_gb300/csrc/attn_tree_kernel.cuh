@@ -152,10 +152,11 @@ __device__ __forceinline__ void tree_plan(const TreeParams& p, int gs, long long
 }
 
 // x / y for 0 <= x, 0 < y: 32 bits wide where both fit (a 64-bit division costs about as much
-// as a global load).
+// as a global load; out of line, since what runs rarely should not fill the instruction cache).
+__device__ __noinline__ long long tree_div_wide(long long x, long long y) { return x / y; }
 __device__ __forceinline__ long long tree_div(long long x, long long y) {
   if (((x | y) >> 32) == 0) return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
-  return x / y;
+  return tree_div_wide(x, y);
 }
 
 // The places [x0, x1) of CTA `cta` of `grid`: the first `extra` CTAs have per + 1, the others per.

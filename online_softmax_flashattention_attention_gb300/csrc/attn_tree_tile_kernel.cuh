@@ -12,7 +12,7 @@
 // rows, so half-empty tiles make the tensor cores wait longer than the memory.  Measured on
 // GB300: one sequence of 131072 tokens and 64 drafts, 8 K/V heads with 4 query heads each
 // (two tiles a head), d = 128: bf16 123 us, 4.4 TB/s of keys and 4.5 TB/s more from L2 for the
-// second tile; 32 sequences of 1 to 64 drafts over 121 MB of e4m3 keys 64 us.
+// second tile; 24 sequences of 500 to 8192 tokens and up to 24 drafts, 122 MB of e4m3 keys, 62 us.
 //
 // Two streams: blocks of even number go to one group of four softmax warps and accumulator o~,
 // odd ones to the other, so that one group's softmax covers the other's products
@@ -109,6 +109,16 @@ struct TileCfg {
   static constexpr uint32_t kIdescO = idesc_bf16_f32(kTileRows, D, 1);
   static_assert(128 * kSBufs + kStreams * D <= 512, "tensor memory");
 };
+
+// mbar_wait with the part that counts time out of line: inlined at some thirty places it fills the
+// instruction cache (64 sequences of 500 e4m3 tokens, 8 drafts, d = 128: 64 -> 50 us with this).
+__device__ __noinline__ bool tile_wait_on(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag, uint32_t* status,
+                                          unsigned long long limit_ns, uint32_t site) {
+  return mbar_wait(bar, parity, WaitCtx{abort_flag, status, limit_ns}, site);
+}
+__device__ __forceinline__ bool tile_wait(uint32_t bar, uint32_t parity, const WaitCtx& w, uint32_t site) {
+  return mbar_try_wait(bar, parity) || mbar_try_wait(bar, parity) || tile_wait_on(bar, parity, w.abort_flag, w.status, w.limit_ns, site);
+}
 
 // D[tmem] (+)= A[smem desc] * B[smem desc]^T, kind::f8f6f4 (e4m3 in, fp32 accumulate), k = 32.
 __device__ __forceinline__ void mma_ss_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
@@ -282,7 +292,7 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
   auto job_at = [&](int u) { return reinterpret_cast<TileJob*>(smem + C::kOffPieces + (u % kTilePieces) * 48); };
   // Waits for piece u; false at the end of the list, or (ok = false too) when the wait ran out.
   auto job = [&](int u, TileJob& t, bool& ok, uint32_t site) {
-    ok = mbar_wait(bar_piece(u % kTilePieces), (u / kTilePieces) & 1, wc, site);
+    ok = tile_wait(bar_piece(u % kTilePieces), (u / kTilePieces) & 1, wc, site);
     if (!ok) return false;
     t = *job_at(u);
     return t.ch1 > t.ch0;
@@ -302,11 +312,31 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
     int g = 0, u = 0;
     uint32_t k_live = 0, k_par = 0, v_live = 0, v_par = 0;
     bool ok = true;
-    for (long long x = x0; ok && x < x1;) {
-      TreePiece pc = tree_piece<kTileRows, kTileKeys>(p, gs, pre, x, x1);
-      x += pc.adv;
-      pc.tile = pc.tile * p.fan + cta % p.fan;
-      if (pc.ch1 <= pc.ch0 || pc.tile * p.tok_tile >= pc.s.T) continue;
+    // The next piece this CTA has rows and keys of, from place x on; lane i < 8 looks after slice i
+    // of a block, and has the page of its slice of the piece's first one.  Pages are fetched a block
+    // ahead, a piece while the one before is in flight.
+    long long x = x0;
+    auto page_of = [&](const TreePiece& t, int j) {
+      const long long pos = static_cast<long long>(j) * kTileKeys + 16 * lane;
+      const bool need = lane < 8 && j < t.ch1 && pos < t.s.n;
+      return need ? __ldg(p.table + static_cast<long long>(t.b) * p.max_pages + static_cast<uint32_t>(pos) / static_cast<uint32_t>(p.page)) : -1;
+    };
+    auto find = [&](TreePiece& t, int& owner, int& page) {
+      while (x < x1) {
+        t = tree_piece<kTileRows, kTileKeys>(p, gs, pre, x, x1);
+        x += t.adv;
+        t.tile = t.tile * p.fan + cta % p.fan;
+        if (t.ch1 <= t.ch0 || t.tile * p.tok_tile >= t.s.T) continue;
+        owner = tree_owner(range, x + (t.s.nch - t.ch1) - 1) * p.fan + cta % p.fan;
+        page = page_of(t, t.ch0);
+        return true;
+      }
+      return false;
+    };
+    TreePiece pc, nx;
+    int owner = 0, nx_owner = 0, next = -1, nx_page = -1;
+    bool more = find(pc, owner, next);
+    while (ok && more) {
       if (lane == 0) {
         TileJob t = {};
         t.q0 = pc.s.q0;
@@ -319,20 +349,13 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
         t.nch = pc.s.nch;
         t.ch0 = pc.ch0;
         t.ch1 = pc.ch1;
-        t.owner = tree_owner(range, x + (pc.s.nch - pc.ch1) - 1) * p.fan + cta % p.fan;
+        t.owner = owner;
         *job_at(u) = t;
         mbar_arrive(bar_piece(u % kTilePieces));
       }
-      // lane i < 8 looks after slice i of a block; its page is fetched a block ahead
-      auto page_of = [&](int j) {
-        const long long pos = static_cast<long long>(j) * kTileKeys + 16 * lane;
-        const bool need = lane < 8 && j < pc.ch1 && pos < pc.s.n;
-        return need ? __ldg(p.table + static_cast<long long>(pc.b) * p.max_pages + static_cast<uint32_t>(pos) / static_cast<uint32_t>(p.page)) : -1;
-      };
-      int next = page_of(pc.ch0);
       for (int j = pc.ch0; j < pc.ch1; ++j, ++g) {
         const int pg = next;
-        next = page_of(j + 1);
+        next = page_of(pc, j + 1);
         const bool have = static_cast<unsigned>(pg) < static_cast<unsigned>(p.num_pages);
         if (!have && lane < 8 && static_cast<long long>(j) * kTileKeys + 16 * lane < pc.s.n && p.page_word)
           atomicOr(p.page_word, 1u);
@@ -347,7 +370,7 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
         for (int kv = 0; kv < 2; ++kv) {
           const int st = kv ? g % RV : g % RK;
           const uint32_t ph = ((kv ? g / RV : g / RK)) & 1, bit = 1u << st;
-          ok = __all_sync(0xffffffffu, mbar_wait(kv ? bar_v_free(st) : bar_k_free(st), ph ^ 1, wc, 34 + kv));
+          ok = __all_sync(0xffffffffu, tile_wait(kv ? bar_v_free(st) : bar_k_free(st), ph ^ 1, wc, 34 + kv));
           if (!ok) break;
           const uint32_t full = kv ? bar_v_full(st) : bar_k_full(st);
           if (lane == 0 && kv == 0) valid[g & 15] = vm;
@@ -377,7 +400,7 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
         // Q after the piece's first block, whose stages depend on earlier blocks only: its K and
         // V are on their way while the last piece's products still read the old Q
         if (ok && j == pc.ch0) {
-          if (u > 0) ok = __all_sync(0xffffffffu, mbar_wait(bar_q_free, (u - 1) & 1, wc, 33));
+          if (u > 0) ok = __all_sync(0xffffffffu, tile_wait(bar_q_free, (u - 1) & 1, wc, 33));
           if (ok && lane == 0) {
             mbar_arrive_expect_tx(bar_q_full, C::kSub * p.tok_tile * p.G * 128);
             for (int s = 0; s < C::kSub; ++s)
@@ -386,7 +409,12 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
           if (ok) ++u;
         }
         if (!ok) break;
+        // once there is something to wait for
+        if (j == min(pc.ch0 + 2, pc.ch1 - 1)) more = find(nx, nx_owner, nx_page);
       }
+      pc = nx;
+      owner = nx_owner;
+      next = nx_page;
     }
     if (ok && lane == 0) {  // the end of the list
       job_at(u)->ch0 = 0;
@@ -417,11 +445,11 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
           const uint32_t klo = (sK >> 4) | (1u << 16);
           // e4m3 rows of 64 bytes: 64-byte swizzle, eight rows 512 bytes apart
           const uint32_t dhi8 = D == 128 ? dhi : (512u >> 4) | (1u << 14) | (4u << 29);
-          ok = mbar_wait(kF8 ? bar_q8_full : bar_q_full, u & 1, wc, 36);
+          ok = tile_wait(kF8 ? bar_q8_full : bar_q_full, u & 1, wc, 36);
           for (int j = pc.ch0; ok && j < pc.ch1; ++j, ++g) {
             const int st = g % RK, bf = g % NB;
-            if (g >= NB) ok = mbar_wait(bar_pv_done(bf), ((g - NB) / NB) & 1, wc, 37);
-            ok = ok && mbar_wait(kF8 ? bar_k_ready(st) : bar_k_full(st), (g / RK) & 1, wc, 38);
+            if (g >= NB) ok = tile_wait(bar_pv_done(bf), ((g - NB) / NB) & 1, wc, 37);
+            ok = ok && tile_wait(kF8 ? bar_k_ready(st) : bar_k_full(st), (g / RK) & 1, wc, 38);
             if (!ok) break;
             tc_fence_after();
             const uint32_t blo = klo + st * (C::kStageK >> 4);
@@ -449,12 +477,12 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
           mma_commit(kF8 ? bar_q8_free : bar_q_free);
         } else {
           const uint32_t vlo = ((kF8 ? sbase + C::kOffWide : sV) >> 4) | (static_cast<uint32_t>(C::kSubBytes >> 4) << 16);
-          if (u > 0) ok = mbar_wait(bar_o_free, (u - 1) & 1, wc, 56);
+          if (u > 0) ok = tile_wait(bar_o_free, (u - 1) & 1, wc, 56);
           for (int j = pc.ch0; ok && j < pc.ch1; ++j, ++g) {
             const int st = kF8 ? g % NWm : g % RV;
-            ok = kF8 ? mbar_wait(bar_w_full(st), (g / NWm) & 1, wc, 39) : mbar_wait(bar_v_full(st), (g / RV) & 1, wc, 39);
+            ok = kF8 ? tile_wait(bar_w_full(st), (g / NWm) & 1, wc, 39) : tile_wait(bar_v_full(st), (g / RV) & 1, wc, 39);
             if (!kF8 && ok && (static_cast<long long>(j + 1) * kTileKeys > pc.ctx || valid[g & 15] != 0xffu)) {
-              ok = mbar_wait(bar_v_fixed(st), (fixed_par >> st) & 1u, wc, 40);
+              ok = tile_wait(bar_v_fixed(st), (fixed_par >> st) & 1u, wc, 40);
               fixed_par ^= 1u << st;
             }
             ok = ok && mbar_wait_poll(bar_p_full(g % NB), (g / NB) & 1, wc, 41);
@@ -488,7 +516,7 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
         ++u;
         for (int j = pc.ch0; j < pc.ch1; ++j, ++g) {
           const int st = g % RK;
-          ok = __all_sync(0xffffffffu, mbar_wait(bar_k_full(st), (g / RK) & 1, wc, 44));
+          ok = __all_sync(0xffffffffu, tile_wait(bar_k_full(st), (g / RK) & 1, wc, 44));
           if (!ok) break;
           const uint32_t w = *reinterpret_cast<const volatile uint32_t*>(smem + C::kOffCodeK + st * 128 + lane * 4);
           // at least 2^-126: a masked score, -inf, must stay that whatever the code beside it
@@ -507,7 +535,7 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
       while (job_warp(u, pc, ok, 52)) {
         for (int j = pc.ch0; j < pc.ch1; ++j, ++g) {
           const int st = g % RV, kb = j * kTileKeys;
-          ok = __all_sync(0xffffffffu, mbar_wait(bar_v_full(st), (g / RV) & 1, wc, 42));
+          ok = __all_sync(0xffffffffu, tile_wait(bar_v_full(st), (g / RV) & 1, wc, 42));
           if (!ok) break;
           const uint32_t vm = valid[g & 15];
           if (static_cast<long long>(kb) + kTileKeys <= pc.ctx && vm == 0xffu) continue;
@@ -549,43 +577,52 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
       TileJob pc;
       while (job_warp(u, pc, ok, 53)) {
         // ---- Q: a row's largest value, then its two terms
-        ok = mbar_wait(bar_q_full, u & 1, wc, 43) && (u == 0 || mbar_wait(bar_q8_free, (u - 1) & 1, wc, 57));
+        ok = tile_wait(bar_q_full, u & 1, wc, 43) && (u == 0 || tile_wait(bar_q8_free, (u - 1) & 1, wc, 57));
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        auto q_at = [&](int c) {
-          return *reinterpret_cast<const uint4*>(smem + C::kOffQ + (c / 8) * C::kSubBytes + r * 128 + (((c & 7) ^ (r & 7)) << 4));
-        };
-        uint32_t mx = 0;
-        bool fine = true;
-#pragma unroll 2
-        for (int c = 0; c < D / 8; ++c) {
-          const uint4 q = q_at(c);
-          mx = max(mx, finite_max(q));
-          fine = fine && !any_nonfinite(q.x) && !any_nonfinite(q.y) && !any_nonfinite(q.z) && !any_nonfinite(q.w);
-        }
-        const uint32_t ef = min(max(mx >> 7, 8u), 253u);  // exponent field of the row's largest value
-        const float up = __uint_as_float((261u - ef) << 23);  // 2^(7 - (ef - 127))
-        // a row that is not finite has scores that are not
-        reinterpret_cast<float*>(smem + C::kOffScaleQ)[(u & 7) * 128 + r] =
-            fine ? p.c * __uint_as_float((ef - 7u) << 23) : __uint_as_float(0x7fffffffu);
+        // Four threads a row, 8 columns at a time, rows that exist only; rolled, as the code runs once a
+        // piece: unrolled, 8 KB, it took 7000 cycles, most of them waiting for instructions.
+        const int rows = min(pc.T - pc.tile * p.tok_tile, p.tok_tile) * p.G;
 #pragma unroll 1
-        for (int c = 0; c < D / 16; ++c) {  // 16 columns: chunks 2 c, 2 c + 1 of bf16, chunk c of hi and of lo
-          const uint4 q0 = q_at(2 * c), q1 = q_at(2 * c + 1);
-          const uint32_t w[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
-          uint32_t hi[4], lo[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {  // four values each
-            const float f0 = bf16_lo(w[2 * i]) * up, f1 = bf16_hi(w[2 * i]) * up;
-            const float f2 = bf16_lo(w[2 * i + 1]) * up, f3 = bf16_hi(w[2 * i + 1]) * up;
-            const uint32_t h0 = pack_e4m3x2(f0, f1), h1 = pack_e4m3x2(f2, f3);
-            const float2 b0 = e4m3x2_to_f32(h0), b1 = e4m3x2_to_f32(h1);
-            hi[i] = h0 | (h1 << 16);
-            lo[i] = pack_e4m3x2(f0 - b0.x, f1 - b0.y) | (pack_e4m3x2(f2 - b1.x, f3 - b1.y) << 16);
+        for (int r0 = 0; r0 < rows; r0 += 32) {
+          const int qr = r0 + 8 * (warp - 12) + (lane >> 2);
+          auto q_at = [&](int ch) {
+            return *reinterpret_cast<const uint4*>(smem + C::kOffQ + (ch / 8) * C::kSubBytes + qr * 128 + (((ch & 7) ^ (qr & 7)) << 4));
+          };
+          uint32_t mx = 0;  // largest finite magnitude; bit 31: one is not
+#pragma unroll 1
+          for (int ch = lane & 3; ch < D / 8; ch += 4) {
+            const uint4 q = q_at(ch);
+            mx = max(mx, finite_max(q));
+            if (any_nonfinite(q.x) || any_nonfinite(q.y) || any_nonfinite(q.z) || any_nonfinite(q.w)) mx |= 0x80000000u;
           }
-          const int sw = D == 128 ? c ^ (r & 7) : c ^ ((r >> 1) & 3);
-          uint8_t* to = smem + C::kOffQ8 + r * D + (sw << 4);
-          *reinterpret_cast<uint4*>(to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          *reinterpret_cast<uint4*>(to + C::kRawBytes) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+          mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+          const uint32_t ef = min(max((mx & 0x7fffffffu) >> 7, 8u), 253u);  // exponent field of the row's largest value
+          const float up = __uint_as_float((261u - ef) << 23);  // 2^(7 - (ef - 127))
+          // a row that is not finite has scores that are not
+          if ((lane & 3) == 0)
+            reinterpret_cast<float*>(smem + C::kOffScaleQ)[(u & 7) * 128 + qr] =
+                (mx >> 31) == 0u ? p.c * __uint_as_float((ef - 7u) << 23) : __uint_as_float(0x7fffffffu);
+#pragma unroll 1
+          for (int ch = lane & 3; ch < D / 8; ch += 4) {
+            const uint4 q = q_at(ch);
+            const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+            uint32_t hi[2], lo[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {  // four values each
+              const float f0 = bf16_lo(w[2 * i]) * up, f1 = bf16_hi(w[2 * i]) * up;
+              const float f2 = bf16_lo(w[2 * i + 1]) * up, f3 = bf16_hi(w[2 * i + 1]) * up;
+              const uint32_t h0 = pack_e4m3x2(f0, f1), h1 = pack_e4m3x2(f2, f3);
+              const float2 b0 = e4m3x2_to_f32(h0), b1 = e4m3x2_to_f32(h1);
+              hi[i] = h0 | (h1 << 16);
+              lo[i] = pack_e4m3x2(f0 - b0.x, f1 - b0.y) | (pack_e4m3x2(f2 - b1.x, f3 - b1.y) << 16);
+            }
+            const int sw = D == 128 ? (ch >> 1) ^ (qr & 7) : (ch >> 1) ^ ((qr >> 1) & 3);
+            uint8_t* to = smem + C::kOffQ8 + qr * D + (sw << 4) + (ch & 1) * 8;
+            *reinterpret_cast<uint2*>(to) = make_uint2(hi[0], hi[1]);
+            *reinterpret_cast<uint2*>(to + C::kRawBytes) = make_uint2(lo[0], lo[1]);
+          }
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -596,7 +633,7 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
         for (int j = pc.ch0; j < pc.ch1; ++j, ++g) {
           const int sv = g % RV, sw = g % NWm, kb = j * kTileKeys;
           // ---- V: codes times scale as bf16
-          ok = mbar_wait(bar_v_full(sv), (g / RV) & 1, wc, 45) && mbar_wait(bar_w_free(sw), ((g / NWm) & 1) ^ 1, wc, 46);
+          ok = tile_wait(bar_v_full(sv), (g / RV) & 1, wc, 45) && tile_wait(bar_w_free(sw), ((g / NWm) & 1) ^ 1, wc, 46);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           const uint32_t vm = valid[g & 15];
@@ -680,7 +717,7 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
         if (g % ST != wg) continue;
         const int bf = g % NB;
         const uint32_t colS = C::col_s(bf), colO = C::col_o(wg);
-        ok = __all_sync(0xffffffffu, mbar_wait(bar_s_full(bf), (g / NB) & 1, wc, 47));
+        ok = __all_sync(0xffffffffu, tile_wait(bar_s_full(bf), (g / NB) & 1, wc, 47));
         if (!ok) break;
         const bool first = !any;
         any = true;
@@ -801,7 +838,7 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
         if (!first && __any_sync(0xffffffffu, moved)) {
           // o~ may be touched once the stream's last P V, of block g - ST, is in it.  With as many
           // score buffers as streams it is: S of this block came after it.
-          if (NB > ST) ok = __all_sync(0xffffffffu, mbar_wait(bar_pv_done((g - ST) % NB), ((g - ST) / NB) & 1, wc, 48));
+          if (NB > ST) ok = __all_sync(0xffffffffu, tile_wait(bar_pv_done((g - ST) % NB), ((g - ST) / NB) & 1, wc, 48));
           if (!ok) break;
           if (NB > ST) tc_fence_after();
           const float2 al2 = make_float2(alpha, alpha);
@@ -838,7 +875,7 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
       // ---- o~ out: this stream's last P V of the piece has landed
       if (ok && any) {
         const int gl = (g_end - 1) % ST == wg ? g_end - 1 : g_end - 2;
-        ok = __all_sync(0xffffffffu, mbar_wait(bar_pv_done(gl % NB), (gl / NB) & 1, wc, 49));
+        ok = __all_sync(0xffffffffu, tile_wait(bar_pv_done(gl % NB), (gl / NB) & 1, wc, 49));
       }
       // Both streams' statistics, then every thread has half the columns of its row.  Each of the
       // eight warps comes here once a piece, also after a failed wait, and they leave together.
