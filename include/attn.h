@@ -314,6 +314,7 @@ attn_status attn_fwd_splitkv(const void* Q, const void* K, const void* V, void* 
  * row-major and contiguous.  A batch's sequences find their pages through a block table,
  * device int32 [B, max_pages]: position p of sequence b is row p % page_size of page
  * block_table[b, p / page_size].  Pages may be shared between sequences that only read them.
+ * max_pages * page_size <= 2^31 - 256.
  *
  * Types.  ATTN_CACHE_BF16: rows as they are.  ATTN_CACHE_E4M3: 8-bit codes with one scale per
  * (token, head) row, k_scale and v_scale uint8 [num_pages, Hkv, page_size]; a value is

@@ -40,8 +40,9 @@ attn_status check_cache(const attn_cache* c, int max_pages) {
     return fail(ATTN_ERR_BAD_SHAPE, "page_size=%d; must be a multiple of 16 in [16, 65536]", c->page_size);
   if (c->num_pages < 0 || c->num_heads < 1 || c->num_heads > 65536)
     return fail(ATTN_ERR_BAD_SHAPE, "num_pages=%d num_heads=%d", c->num_pages, c->num_heads);
-  if (max_pages < 0 || static_cast<long long>(max_pages) * c->page_size > INT32_MAX)
-    return fail(ATTN_ERR_BAD_SHAPE, "max_pages=%d: a sequence has at most 2^31 - 1 positions", max_pages);
+  // the kernels round positions up to a block of keys in 32 bits
+  if (max_pages < 0 || static_cast<long long>(max_pages) * c->page_size > INT32_MAX - 255)
+    return fail(ATTN_ERR_BAD_SHAPE, "max_pages=%d: a sequence has at most 2^31 - 256 positions", max_pages);
   if (c->num_pages > 0) {
     if (!c->k || !c->v) return fail(ATTN_ERR_NULLPTR, "the cache's k and v must not be NULL");
     if (odd16(c->k) || odd16(c->v)) return fail(ATTN_ERR_MISALIGNED, "the cache's k and v must be 16-byte aligned");

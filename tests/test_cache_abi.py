@@ -81,6 +81,12 @@ def test_common_faults(lib, call):
     assert call(lib, _cache(), total=0, cu=0, table=0) == 0
 
 
+@pytest.mark.parametrize("call", [_write, _read, _tree])
+def test_positions_that_round_past_32_bits(lib, call):
+    for page in (16, 32, 64, 128):  # 2^31 - page positions
+        assert call(lib, _cache(page_size=page), max_pages=2 ** 31 // page - 1) == -2
+
+
 @pytest.mark.parametrize("call", [_write, _read])
 def test_row_pointers(lib, call):
     assert call(lib, _cache(), K=0) == -1
