@@ -8,11 +8,12 @@
 // o~ += P V, with P written back over S as bf16.  One CTA an SM, persistent over its range of
 // the list of chunks (128 keys each).
 //
-// Bound: the keys, read once a unit; P V alone is 128 x 128 x d x 2 flops a block whatever the
-// rows, so half-empty tiles make the tensor cores wait longer than the memory.  Measured on
-// GB300: one sequence of 131072 tokens and 64 drafts, 8 K/V heads with 4 query heads each
-// (two tiles a head), d = 128: bf16 123 us, 4.4 TB/s of keys and 4.5 TB/s more from L2 for the
-// second tile; 24 sequences of 500 to 8192 tokens and up to 24 drafts, 122 MB of e4m3 keys, 62 us.
+// Bound: with one tile a head the keys, read once a unit (one sequence of 131072 tokens, 8 K/V
+// heads with 4 query heads each, d = 128, 8 drafts, on GB300: bf16 88 us, 6.1 TB/s); with two the
+// softmax, 1670 cycles for 128 x 128 scores (64 drafts: 123 us, 4.4 TB/s of keys and as much again
+// from L2 for the second tile).  e4m3 is bound by latency, 2840 cycles a block in two streams
+// beside the widening of V: 95 us with 8 drafts; 24 sequences of 500 to 8192 tokens and up to 24
+// drafts, 122 MB of keys, 62 us.
 //
 // Two streams: blocks of even number go to one group of four softmax warps and accumulator o~,
 // odd ones to the other, so that one group's softmax covers the other's products
@@ -67,8 +68,9 @@ static_assert(sizeof(TileJob) == 48, "three 16-byte words");
 
 template <int D, bool kF8>
 struct TileCfg {
-  // (bf16 at d = 128 has no shared memory left for the second stream's statistics, and reaches
-  // the memory's rate with one.)
+  // (bf16 at d = 128 has no shared memory left for the second stream's statistics, and tensor
+  // memory for two score buffers then; through the workspace two streams were slower, 137 us
+  // against 124 for 131072 tokens and 64 drafts.)
   static constexpr int kStreams = !kF8 && D == 128 ? 1 : 2;
   static constexpr int kThreads = kF8 ? 512 : kStreams == 2 ? 384 : 256;
   static constexpr int kSub = D / 64;                    // 64-column sub-tiles of a bf16 row
