@@ -150,7 +150,7 @@ attn_status attn_fwd_strided(const void* Q, const void* K, const void* V, void* 
  * attn_fwd_varlen -- attention over B packed sequences of different lengths (an addition
  * of this library; the pages treat one sequence).
  *   Q, O  device bf16 [total_q, H, d]: sequence b is rows cu_seqlens_q[b] ..
- *         cu_seqlens_q[b+1] - 1.  K, V device bf16 [total_k, H, d], rows cu_seqlens_k[b] ..
+ *         cu_seqlens_q[b+1] - 1.  K, V device bf16 [total_k, H, d] (Q's H), rows cu_seqlens_k[b] ..
  *   cu_seqlens_q, cu_seqlens_k  device int32[B + 1], non-decreasing from 0 to total_q /
  *         total_k (values are clamped to [0, total] on the device, so a bad array cannot
  *         make the kernel write outside O and LSE).
@@ -367,9 +367,11 @@ attn_status attn_cache_write(const attn_cache* cache, const void* K, const void*
                              const int32_t* cu_seqlens, const int32_t* start_lens, int B, int total, void* stream);
 
 /*
- * attn_cache_read -- cached positions back as packed bf16 K and V [total, num_heads, d] (what
- *   attn_fwd_varlen takes, e.g. for a prompt over a cached prefix).  Row cu_seqlens[b] + i is
- *   position start_lens[b] + i of sequence b.  Exact: every e4m3 value times its scale that
+ * attn_cache_read -- cached positions back as packed bf16 K and V [total, num_heads, d], e.g.
+ *   for a prompt over a cached prefix through attn_fwd_varlen.  That call has one head count:
+ *   where a group of query heads shares a K/V head, repeat the rows read here for each of them
+ *   first (passing them as they are with Q's H would read past their end).
+ *   Row cu_seqlens[b] + i is position start_lens[b] + i of sequence b.  Exact: every e4m3 value times its scale that
  *   attn_cache_write makes is a bf16.  Rows outside every sequence are left as they were.
  *   K, V 16-byte aligned.  Asynchronous.
  */

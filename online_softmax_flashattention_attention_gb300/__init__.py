@@ -347,10 +347,17 @@ def attn_fwd_varlen(Q, K, V, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, O=None, L
                     stream=None):
     """Packed sequences: Q [total_q, H, d], K/V [total_k, H, d] contiguous bf16 CUDA tensors,
     cu_seqlens_q / cu_seqlens_k int32 CUDA tensors [B + 1].  Returns O [total_q, H, d] and
-    LSE [H, total_q]."""
+    LSE [H, total_q].  K and V have Q's heads: where a group of query heads shares one, repeat it
+    (``K.repeat_interleave(Hq // Hkv, 1)``)."""
     import torch
     total_q, H, d = Q.shape
     total_k = K.shape[0]
+    # the library takes one head count, Q's: fewer K/V heads would be read past their end
+    if K.shape != (total_k, H, d) or V.shape != (total_k, H, d):
+        raise ValueError("K and V must be [total_k, H, d] with Q's H and d (repeat K/V heads that query heads share)")
+    for name, t in (("Q", Q), ("K", K), ("V", V)):
+        if t.dtype != torch.bfloat16 or not t.is_cuda or t.device != Q.device or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous bf16 CUDA tensor on Q's device")
     B = cu_seqlens_q.numel() - 1
     if cu_seqlens_k.numel() != B + 1:
         raise ValueError("cu_seqlens_q and cu_seqlens_k must have the same length")
@@ -363,6 +370,10 @@ def attn_fwd_varlen(Q, K, V, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, O=None, L
         O = torch.empty_like(Q)
     if LSE is None:
         LSE = torch.empty((H, total_q), dtype=torch.float32, device=Q.device)
+    if O.shape != Q.shape or O.dtype != torch.bfloat16 or O.device != Q.device or not O.is_contiguous():
+        raise ValueError("O must be a contiguous bf16 tensor shaped like Q")
+    if LSE.shape != (H, total_q) or LSE.dtype != torch.float32 or LSE.device != Q.device or not LSE.is_contiguous():
+        raise ValueError("LSE must be a contiguous fp32 tensor [H, total_q]")
     rc = load_library().attn_fwd_varlen(Q.data_ptr(), K.data_ptr(), V.data_ptr(), O.data_ptr(), LSE.data_ptr(),
                                         cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), B, H, int(max_seqlen_q),
                                         total_q, total_k, d, float(scale), int(causal), _stream_handle(stream))
@@ -478,7 +489,8 @@ _Strides = ctypes.c_int64 * 2
 def attn_cache_read(k_cache, v_cache, block_table, cu_seqlens, total, K=None, V=None, *, start_lens=None, k_scale=None,
                     v_scale=None, stream=None):
     """Cached positions as packed bf16 K, V [total, Hkv, d] (allocated when not given), the
-    layout attn_fwd_varlen takes.  Row cu_seqlens[b] + i is position start_lens[b] + i of
+    layout attn_fwd_varlen takes where every query head has its own K/V head; for grouped heads
+    repeat them (``K.repeat_interleave(Hq // Hkv, 1)``).  Row cu_seqlens[b] + i is position start_lens[b] + i of
     sequence b; rows outside every sequence are left as they were, positions without a page are
     zeros and reported by cache_check().  The cache's arguments: as attn_cache_write."""
     import torch
