@@ -602,10 +602,13 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
           mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
           const uint32_t ef = min(max((mx & 0x7fffffffu) >> 7, 8u), 253u);  // exponent field of the row's largest value
           const float up = __uint_as_float((261u - ef) << 23);  // 2^(7 - (ef - 127))
-          // a row that is not finite has scores that are not
-          if ((lane & 3) == 0)
-            reinterpret_cast<float*>(smem + C::kOffScaleQ)[(u & 7) * 128 + qr] =
-                (mx >> 31) == 0u ? p.c * __uint_as_float((ef - 7u) << 23) : __uint_as_float(0x7fffffffu);
+          // The row's factor, finite and more than 0, since a masked score is -inf before it is
+          // multiplied: where the product leaves fp32, its least number, off by 2^-149 of a score
+          // under 2^128.  Its sign says that the row holds an infinity or NaN.
+          if ((lane & 3) == 0) {
+            const float f = fmaxf(p.c * __uint_as_float((ef - 7u) << 23), __uint_as_float(1u));
+            reinterpret_cast<float*>(smem + C::kOffScaleQ)[(u & 7) * 128 + qr] = (mx >> 31) == 0u ? f : -f;
+          }
 #pragma unroll 1
           for (int ch = lane & 3; ch < D / 8; ch += 4) {
             const uint4 q = q_at(ch);
@@ -687,6 +690,7 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
     const int r = (warp & 3) * 32 + lane;
     const uint32_t tl = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     float c = p.c;  // e4m3: times the row's power of two, piece by piece
+    bool odd_q = false;  // e4m3: the row's query is not finite
     constexpr float kTau = 8.f;  // o~ is rescaled when the max rises by more (log2 units)
     int g = 0, u = 0;
     bool ok = true, has_tail = false;
@@ -723,7 +727,11 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
         if (!ok) break;
         const bool first = !any;
         any = true;
-        if (kF8 && first) c = reinterpret_cast<const volatile float*>(smem + C::kOffScaleQ)[(u & 7) * 128 + r];
+        if (kF8 && first) {
+          c = reinterpret_cast<const volatile float*>(smem + C::kOffScaleQ)[(u & 7) * 128 + r];
+          odd_q = c < 0.f;
+          c = fabsf(c);
+        }
         if (idle) {  // its lanes of P hold scores: rows nobody reads
           if (lane == 0) mbar_arrive(bar_p_full(bf));
           continue;
@@ -863,6 +871,8 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(bar_p_full(bf));
       }
+      // such a row is NaN once it has seen a key (its two terms, saturated, made finite scores)
+      if (kF8 && odd_q && m != -INFINITY) l = __uint_as_float(0x7fffffffu);
       const bool whole = pc.ch0 == 0 && pc.ch1 == pc.nch;
       const bool front = pc.ch0 == 0 && !whole;  // goes on in the next CTAs
       const int hq = pc.h * p.G + head;
