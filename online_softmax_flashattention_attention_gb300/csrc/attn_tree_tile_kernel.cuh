@@ -52,8 +52,10 @@ constexpr int kTileWarpPv = 5;
 constexpr int kTileWarpS = 6;
 constexpr int kTileWarpFix = 7;
 constexpr int kTileTags = 16;
-// Pieces announced in shared memory.  The producer is at most 7 blocks, so at most 8 pieces,
-// ahead of the softmax, and no role is behind it: a slot is never overwritten while in use.
+// Pieces announced in shared memory.  The producer is at most 7 blocks, so at most 8 pieces, ahead
+// of any role, as each is counted in what frees a stage: S in k_free (and through k_ready the
+// scales' warp), P V and the repair of V or the converters in v_free, the softmax through P V.  So
+// a slot is never overwritten while in use.
 constexpr int kTilePieces = 16;
 
 // A piece as the producer announces it to the other roles.
@@ -226,7 +228,7 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + C::kOffMisc + 4);
   // valid[g % 16]: which 16-key slices of block g exist (written before the block's copies are
-  // announced; the producer is at most 7 blocks ahead of either stream)
+  // announced; the producer is at most 7 blocks ahead of any role)
   volatile uint32_t* valid = reinterpret_cast<volatile uint32_t*>(smem + C::kOffMisc + 8);
   // tag[u % 16] = u + 1 once unit u (of this CTA) has met an infinite or NaN drafted value
   volatile uint32_t* tag = reinterpret_cast<volatile uint32_t*>(smem + C::kOffMisc + 72);
@@ -246,7 +248,9 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
     }
     for (int s = 0; s < RV; ++s) {
       mbar_init(bar_v_full(s), 1);
-      mbar_init(bar_v_free(s), kF8 ? 4 : 1);
+      // bf16: P V, and the repair on every block, ragged or not: a warp that waits by parity must not
+      // be passed by two turns of the ring
+      mbar_init(bar_v_free(s), kF8 ? 4 : 2);
       mbar_init(bar_v_fixed(s), 1);
     }
     for (int s = 0; s < NW; ++s) {
@@ -540,7 +544,10 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
           ok = __all_sync(0xffffffffu, tile_wait(bar_v_full(st), (g / RV) & 1, wc, 42));
           if (!ok) break;
           const uint32_t vm = valid[g & 15];
-          if (static_cast<long long>(kb) + kTileKeys <= pc.ctx && vm == 0xffu) continue;
+          if (static_cast<long long>(kb) + kTileKeys <= pc.ctx && vm == 0xffu) {
+            if (lane == 0) mbar_arrive(bar_v_free(st));
+            continue;
+          }
           bool odd = false;
           for (int i = lane; i < kTileKeys * (D / 8); i += 32) {
             const int r = i / (D / 8), ch = i % (D / 8);
@@ -561,7 +568,10 @@ __global__ void __launch_bounds__(TileCfg<D, kF8>::kThreads, 1)
           if (odd) tag[u % kTileTags] = u + 1;
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(bar_v_fixed(st));
+          if (lane == 0) {
+            mbar_arrive(bar_v_fixed(st));
+            mbar_arrive(bar_v_free(st));
+          }
         }
         if (!ok) break;
         ++u;
