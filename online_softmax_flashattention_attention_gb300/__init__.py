@@ -11,6 +11,7 @@ import ctypes
 import math
 import os
 import threading
+import weakref
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libattn.so")
@@ -223,8 +224,10 @@ def status_sync(stream=None):
 
 
 def release_workspace():
-    """Free the workspaces kept for attn_fwd_host and attn_fwd_tree."""
-    _tree_workspaces.clear()
+    """Free the workspaces kept for attn_fwd_host and (by every thread) for attn_fwd_tree."""
+    with _kept_lock:
+        for kept in list(_kept_by_threads):
+            kept.by_stream.clear()
     _check(load_library().attn_release_workspace())
 
 
@@ -524,20 +527,34 @@ def tree_workspace_bytes(Hq, Hkv, max_seqlen_q, d) -> int:
     return load_library().attn_tree_workspace_bytes(Hq, Hkv, max_seqlen_q, d)
 
 
-_tree_workspaces = {}  # (device index, stream, thread) -> uint8 tensor
+class _Kept:
+    """A host thread's workspaces: (device index, stream) -> uint8 tensor.  They go with the thread."""
+    __slots__ = ("by_stream", "__weakref__")
+
+    def __init__(self):
+        self.by_stream = {}
+
+
+_thread = threading.local()
+_kept_by_threads = weakref.WeakSet()  # for release_workspace
+_kept_lock = threading.Lock()
 
 
 def _tree_workspace(nbytes, dev, raw):
     """attn_fwd_tree's default workspace: one kept for each stream and host thread, whose calls run
-    one after the other (two threads may interleave their launches on a stream); a captured call
-    gets its own, which belongs to the graph (graphs may run at once)."""
+    one after the other (two threads may interleave their launches on a stream), until the thread
+    ends; a captured call gets its own, which belongs to the graph (graphs may run at once)."""
     import torch
     if torch._C._cuda_isCurrentStreamCapturing():
         return torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    key = (dev.index, raw, threading.get_ident())
-    ws = _tree_workspaces.get(key)
+    kept = getattr(_thread, "kept", None)
+    if kept is None:
+        kept = _thread.kept = _Kept()
+        with _kept_lock:
+            _kept_by_threads.add(kept)
+    ws = kept.by_stream.get((dev.index, raw))
     if ws is None or ws.numel() < nbytes:
-        ws = _tree_workspaces[key] = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        ws = kept.by_stream[dev.index, raw] = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     return ws
 
 

@@ -41,3 +41,47 @@ def test_a_prompt_over_a_prefix_read_back_with_grouped_heads(hkv, G, d, f8):
     # scores: d 2^-24 |q| |k| / sqrt(d) each, |q| |k| under 250 here, and 2^-17 of the query row's largest where
     # a value is 2^-9 of it and less
     assert bool(((LSE - LSE2).abs() <= 4e-4).all())
+
+
+def test_workspaces_go_with_their_threads():
+    """The workspaces kept for threads that have ended, and all of them after release_workspace(), no
+    longer take device memory."""
+    import gc
+    import threading
+    pkg = _pkg()
+    b = Batch(62, 2, 4, 128, 16, False, [300], [9])  # tiles: 21 MB a workspace
+    args, kw = b.dev()
+    O, LSE = torch.empty_like(args[0]), torch.empty((8, 9), device="cuda")
+    pkg.release_workspace()
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    one = pkg.tree_workspace_bytes(8, 2, 9, 128)
+    ready, go = threading.Barrier(5), threading.Event()
+
+    def work():
+        pkg.attn_fwd_tree(*args, O, LSE, **kw)
+        ready.wait()
+        go.wait()
+
+    threads = [threading.Thread(target=work) for _ in range(4)]
+    for t in threads:
+        t.start()
+    ready.wait()
+    torch.cuda.synchronize()
+    assert torch.cuda.memory_allocated() - before >= 4 * one
+    go.set()
+    for t in threads:
+        t.join()
+    gc.collect()
+    assert torch.cuda.memory_allocated() - before < one
+    pkg.attn_fwd_tree(*args, O, LSE, **kw)
+    ready, go = threading.Barrier(2), threading.Event()
+    t = threading.Thread(target=work)
+    t.start()
+    ready.wait()
+    assert torch.cuda.memory_allocated() - before >= 2 * one
+    pkg.release_workspace()
+    assert torch.cuda.memory_allocated() - before < one
+    go.set()
+    t.join()
+    pkg.cache_check()
