@@ -340,8 +340,8 @@ typedef struct attn_cache {
   uint8_t* v_scale;
   int type;           /* ATTN_CACHE_* */
   int num_pages;      /* >= 0 */
-  int page_size;      /* a multiple of 16 */
-  int num_heads;      /* K/V heads */
+  int page_size;      /* a multiple of 16, at most 65536 */
+  int num_heads;      /* K/V heads, 1 .. 65536 */
   int d;              /* 64 or 128 */
 } attn_cache;
 
@@ -384,7 +384,8 @@ attn_status attn_cache_read(const attn_cache* cache, void* K, void* V, const int
  *   rows cu_seqlens_q[b] .. cu_seqlens_q[b + 1] - 1 of Q, whose K and V are already in the
  *   cache at positions ctx_lens[b] .. ctx_lens[b] + T_b - 1.  T_b = 1 is plain decoding.
  *   Q, O  device bf16 [total_q, Hq, d], LSE fp32 [Hq, total_q].  Hq is a multiple of the
- *         cache's heads: query head h reads K/V head h / (Hq / num_heads).
+ *         cache's heads and at most 65536: query head h reads K/V head h / (Hq / num_heads).
+ *         O may be Q itself (not another part of it).
  *   tree_mask  device int64 [total_q] or NULL.  Token i of a sequence sees every context key,
  *         and its token u when bit u of tree_mask[row of i] is set (bits from T_b on are
  *         ignored; a token sees itself only if its own bit is set).  NULL: a chain, u <= i.
@@ -399,8 +400,8 @@ attn_status attn_cache_read(const attn_cache* cache, void* K, void* V, const int
  *         each need one.  Its contents mean nothing between calls.
  *   Asynchronous, allocates nothing; device-side timeouts through attn_status_sync or
  *   attn_cache_check (the environment variables of attn_fwd hold here too, key blocks of 128).
- *   Errors: as attn_fwd, plus ATTN_ERR_BAD_SHAPE for
- *   max_seqlen_q > 64 or Hq not a multiple, ATTN_ERR_BAD_ARG for a small workspace.
+ *   Errors: as attn_fwd, plus ATTN_ERR_BAD_SHAPE for max_seqlen_q > 64 or an Hq that is no
+ *   multiple or too large, ATTN_ERR_BAD_ARG for a small workspace.
  */
 attn_status attn_fwd_tree(const void* Q, const attn_cache* cache, void* O, float* LSE, const int32_t* block_table,
                           int max_pages, const int32_t* cu_seqlens_q, const int32_t* ctx_lens,

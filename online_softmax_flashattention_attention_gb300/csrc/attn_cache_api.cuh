@@ -26,6 +26,8 @@ attn_status page_word(int dev, uint32_t** out) {
   return ATTN_OK;
 }
 
+constexpr int kMaxPage = 65536, kMaxHeads = 65536;
+
 bool odd16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
 bool odd_to(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) != 0; }
 
@@ -36,10 +38,11 @@ attn_status check_cache(const attn_cache* c, int max_pages) {
   if (c->d != 64 && c->d != 128) return fail(ATTN_ERR_UNSUPPORTED_D, "d=%d; supported: 64, 128", c->d);
   if (c->type != ATTN_CACHE_BF16 && c->type != ATTN_CACHE_E4M3)
     return fail(ATTN_ERR_BAD_ARG, "cache type %d; ATTN_CACHE_BF16 or ATTN_CACHE_E4M3", c->type);
-  if (c->page_size < 16 || c->page_size % 16 != 0 || c->page_size > 65536)
-    return fail(ATTN_ERR_BAD_SHAPE, "page_size=%d; must be a multiple of 16 in [16, 65536]", c->page_size);
-  if (c->num_pages < 0 || c->num_heads < 1 || c->num_heads > 65536)
-    return fail(ATTN_ERR_BAD_SHAPE, "num_pages=%d num_heads=%d", c->num_pages, c->num_heads);
+  if (c->page_size < 16 || c->page_size % 16 != 0 || c->page_size > kMaxPage)
+    return fail(ATTN_ERR_BAD_SHAPE, "page_size=%d; must be a multiple of 16 in [16, %d]", c->page_size, kMaxPage);
+  if (c->num_pages < 0 || c->num_heads < 1 || c->num_heads > kMaxHeads)
+    return fail(ATTN_ERR_BAD_SHAPE, "num_pages=%d num_heads=%d; num_pages >= 0, num_heads in [1, %d]", c->num_pages,
+                c->num_heads, kMaxHeads);
   // the kernels round positions up to a block of keys in 32 bits
   if (max_pages < 0 || static_cast<long long>(max_pages) * c->page_size > INT32_MAX - 255)
     return fail(ATTN_ERR_BAD_SHAPE, "max_pages=%d: a sequence has at most 2^31 - 256 positions", max_pages);
@@ -343,7 +346,8 @@ attn_status attn_fwd_tree(const void* Q, const attn_cache* cache, void* O, float
   if (B < 0 || Hq < 0 || total_q < 0 || max_seqlen_q < 0 || max_seqlen_q > attn::kTreeMaxNodes)
     return fail(ATTN_ERR_BAD_SHAPE, "B=%d Hq=%d total_q=%d max_seqlen_q=%d; max_seqlen_q must be in [0, %d]", B, Hq,
                 total_q, max_seqlen_q, attn::kTreeMaxNodes);
-  if (Hq % cache->num_heads != 0 || Hq > 65536)
+  if (Hq > kMaxHeads) return fail(ATTN_ERR_BAD_SHAPE, "Hq=%d; at most %d", Hq, kMaxHeads);
+  if (Hq % cache->num_heads != 0)
     return fail(ATTN_ERR_BAD_SHAPE, "Hq=%d must be a multiple of the cache's %d heads", Hq, cache->num_heads);
   if (!std::isfinite(scale) || !(scale > 0.f)) return fail(ATTN_ERR_BAD_ARG, "scale must be finite and > 0");
   if (B == 0 || Hq == 0 || total_q == 0 || max_seqlen_q == 0) return ATTN_OK;
