@@ -392,7 +392,9 @@ attn_status attn_cache_read(const attn_cache* cache, void* K, void* V, const int
  *         A row that sees nothing gets O = 0 and LSE = -inf.  What K and V hold where a row
  *         does not look, infinities and NaN among it, does not reach the row.
  *   The running maximum may trail by a factor of 2^8 (as attn_options.rescale_threshold
- *   describes), so sums must stay in range with that: keys * 2^8 * max|V| < 3.4e38.
+ *   describes), so sums must stay in range with that: keys * 2^8 * max|V| < 3.4e38; and, for an
+ *   e4m3 cache, 2^8 * d * max|K| < 3.4e38.  Values of an e4m3 cache near the least normal number
+ *   lose digits: what a key adds to O may be off by 2^-125 more.
  *   max_seqlen_q  in [0, 64], >= the most tokens of a sequence (rows past it are left as they
  *         were, as are rows of Q outside every sequence).
  *   workspace  device, attn_tree_workspace_bytes(...) bytes, 16-byte aligned, this call's own
