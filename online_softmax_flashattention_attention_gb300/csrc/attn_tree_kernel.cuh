@@ -9,8 +9,9 @@
 // Bound: K and V are read once, 4 d (bf16) or 2 d + 2 (e4m3) bytes a key, for 4 d flops a row
 // and key; below 274 rows a unit memory is the limit.  Measured on GB300, one token a sequence,
 // 32 query and 8 K/V heads, d = 128, sequences of 900 to 16384 tokens: 48 of them in bf16, 1.14 GB
-// in 180 us, 6.3 TB/s; 64 in e4m3, 770 MB in 146 us, 5.2 TB/s (there the conversions of K and V
-// take half the issue slots, and the latency between them much of the rest).
+// in 180 us, 6.3 TB/s; 64 in e4m3, 770 MB in 147 us, 5.2 TB/s (there the conversions of K and V
+// take half the issue slots, and the latency between dependent steps is the limit: more conversions
+// cost little, a third CTA an SM gave an eighth).
 //
 // Work split: the keys of all units are laid end to end in chunks of 64 or 128 (and some places
 // for what a unit costs beside them, see tree_plan) and cut into equal ranges, one a CTA (two

@@ -10,8 +10,9 @@
 //
 // Bound: with one tile a head the keys, read once a unit (one sequence of 131072 tokens, 8 K/V
 // heads with 4 query heads each, d = 128, 8 drafts, on GB300: bf16 88 us, 6.1 TB/s); with two the
-// softmax, 1670 cycles for 128 x 128 scores (64 drafts: 123 us, 4.4 TB/s of keys and as much again
-// from L2 for the second tile).  e4m3 is bound by latency, 2840 cycles a block in two streams
+// softmax, 1670 cycles for 128 x 128 scores (64 drafts: 124 us at 2070 MHz, 4.3 TB/s of keys and as
+// much again from L2 for the second tile; 130 when calls go on and power holds the clock to 1730 to
+// 1910).  e4m3 is bound by latency, 2840 cycles a block in two streams
 // beside the widening of V: 95 us with 8 drafts; 24 sequences of 500 to 8192 tokens and up to 24
 // drafts, 122 MB of keys, 62 us.
 //
