@@ -455,11 +455,11 @@ def attn_cache_write(K, V, k_cache, v_cache, block_table, cu_seqlens, *, start_l
 
     K, V [total, Hkv, d]: bf16 CUDA tensors with a contiguous last dimension (views of a joint
     projection need no copy).  k_cache, v_cache [num_pages, Hkv, page_size, d] (page_size a
-    multiple of 16 up to 65536): bf16 or float8_e4m3fn; an e4m3 cache comes with k_scale and v_scale, uint8 [num_pages, Hkv,
-    page_size] (value = code * 2^(s - 127)).  block_table int32 [B, max_pages]; cu_seqlens
-    int32 [B + 1]: sequence b's tokens are rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1 and go to
-    positions start_lens[b], ... (int32 [B]; None: 0).  Tokens without a page are left out and
-    reported by cache_check().
+    multiple of 16 up to 65536): bf16 or float8_e4m3fn; an e4m3 cache comes with k_scale and
+    v_scale, uint8 [num_pages, Hkv, page_size] (value = code * 2^(s - 127)).  block_table int32
+    [B, max_pages]; cu_seqlens int32 [B + 1]: sequence b's tokens are rows cu_seqlens[b] ..
+    cu_seqlens[b + 1] - 1 and go to positions start_lens[b], ... (int32 [B]; None: 0).  Tokens
+    without a page are left out and reported by cache_check().
     """
     import torch
     dev = k_cache.device
@@ -493,8 +493,8 @@ def attn_cache_read(k_cache, v_cache, block_table, cu_seqlens, total, K=None, V=
                     v_scale=None, stream=None):
     """Cached positions as packed bf16 K, V [total, Hkv, d] (allocated when not given), the
     layout attn_fwd_varlen takes where every query head has its own K/V head; for grouped heads
-    repeat them (``K.repeat_interleave(Hq // Hkv, 1)``).  Row cu_seqlens[b] + i is position start_lens[b] + i of
-    sequence b; rows outside every sequence are left as they were, positions without a page are
+    repeat them (``K.repeat_interleave(Hq // Hkv, 1)``).  Row cu_seqlens[b] + i is position
+    start_lens[b] + i of sequence b; rows outside every sequence are left as they were, positions without a page are
     zeros and reported by cache_check().  The cache's arguments: as attn_cache_write."""
     import torch
     dev = k_cache.device
@@ -565,12 +565,13 @@ def attn_fwd_tree(Q, k_cache, v_cache, block_table, ctx_lens, cu_seqlens_q, max_
     Q [total_q, Hq, d]: contiguous bf16 CUDA tensor, sequence b's tokens at rows
     cu_seqlens_q[b] .. cu_seqlens_q[b + 1] - 1 (int32 [B + 1]), at most max_seqlen_q <= 64 of
     them; their K and V are already cached at positions ctx_lens[b], ... (int32 [B]; None: 0).
-    Hq is a multiple of the cache's heads, at most 65536; O may be Q.  tree_mask int64 [total_q]: bit u of a token's word
-    lets it see token u of its sequence (None: a chain, u <= i); every token sees the context.
-    One token per sequence is plain decoding.  Returns O [total_q, Hq, d] and LSE [Hq, total_q]
-    (allocated when not given).  workspace: a CUDA uint8 tensor of tree_workspace_bytes(...)
-    that no other call in flight uses; when not given, one kept for the stream and host thread (a
-    captured call gets its own; release_workspace() lets them go).  The cache's arguments: as attn_cache_write.
+    Hq is a multiple of the cache's heads, at most 65536; O may be Q.  tree_mask int64 [total_q]:
+    bit u of a token's word lets it see token u of its sequence (None: a chain, u <= i); every
+    token sees the context.  One token per sequence is plain decoding.  Returns O
+    [total_q, Hq, d] and LSE [Hq, total_q] (allocated when not given).  workspace: a CUDA uint8
+    tensor of tree_workspace_bytes(...) that no other call in flight uses; when not given, one
+    kept for the stream and host thread until the thread ends (a captured call gets its own;
+    release_workspace() lets them go).  The cache's arguments: as attn_cache_write.
     """
     import torch
     dev = k_cache.device

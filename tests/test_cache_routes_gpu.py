@@ -85,3 +85,16 @@ def test_workspaces_go_with_their_threads():
     go.set()
     t.join()
     pkg.cache_check()
+
+
+def test_packed_forward_refuses_outputs_that_do_not_fit():
+    pkg = _pkg()
+    z = lambda *s, dt=torch.bfloat16: torch.zeros(s, dtype=dt, device="cuda")  # noqa: E731
+    Q, cu = z(5, 8, 64), _i32([0, 5])
+    for O, LSE in ((z(5, 2, 64), None), (z(5, 8, 64, dt=torch.float32), None), (z(5, 8, 128)[:, :, ::2], None),
+                   (None, z(5, 8, dt=torch.float32)), (None, z(8, 5)), (z(5, 8, 64).cpu(), None)):
+        with pytest.raises(ValueError):
+            pkg.attn_fwd_varlen(Q, Q, Q, cu, cu, 5, O, LSE)
+    with pytest.raises(ValueError, match="K must be"):
+        pkg.attn_fwd_varlen(Q, z(5, 8, 128)[:, :, ::2], Q, cu, cu, 5)
+    assert bool((pkg.attn_fwd_varlen(Q, Q, Q, cu, cu, 5)[0] == 0).all())

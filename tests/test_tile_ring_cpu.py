@@ -30,7 +30,8 @@ class Bar:
 def roles(n, rk, rv, nb, ragged, v_free_count):
     """Generators that yield what they wait for, as functions."""
     k_full, k_free = [Bar(1) for _ in range(rk)], [Bar(1) for _ in range(rk)]
-    v_full, v_free, v_fixed = [Bar(1) for _ in range(rv)], [Bar(v_free_count) for _ in range(rv)], [Bar(1) for _ in range(rv)]
+    v_full, v_fixed = ([Bar(1) for _ in range(rv)] for _ in range(2))
+    v_free = [Bar(v_free_count) for _ in range(rv)]
     s_full, p_full, pv_done = ([Bar(1) for _ in range(nb)] for _ in range(3))
     in_k, in_v = [None] * rk, [None] * rv
 
@@ -95,17 +96,16 @@ def run(parts, starved, patience, seed):
         ready = [n for n, w in waits.items() if w()]
         assert ready, f"nobody can go on: {sorted(waits)}"
         others = [n for n in ready if n != starved]
-        name = r.choice(others) if others and (starved not in ready or step % patience) else (starved if starved in ready else r.choice(ready))
+        name = r.choice(others) if others and (starved not in ready or step % patience) else starved
         try:
             waits[name] = next(parts[name])
         except StopIteration:
             del waits[name]
 
 
-def counts():
-    src = open(SOURCE).read()
-    free = int(re.search(r"mbar_init\(bar_v_free\(s\), kF8 \? 4 : (\d)\)", src).group(1))
-    return free
+def counted():
+    with open(SOURCE) as f:
+        return int(re.search(r"mbar_init\(bar_v_free\(s\), kF8 \? 4 : (\d)\)", f.read()).group(1))
 
 
 @pytest.mark.parametrize("starved", ["producer", "scores", "softmax", "values", "repair"])
@@ -114,7 +114,7 @@ def counts():
 def test_no_role_is_passed_by_the_ring(starved, rk, rv, nb, ragged):
     for seed in range(20):
         for patience in (7, 61, 10 ** 9):
-            run(roles(200, rk, rv, nb, ragged, counts()), starved, patience, seed)
+            run(roles(200, rk, rv, nb, ragged, counted()), starved, patience, seed)
 
 
 def test_the_model_finds_a_repair_that_is_not_counted():
