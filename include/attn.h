@@ -413,6 +413,103 @@ attn_status attn_fwd_tree(const void* Q, const attn_cache* cache, void* O, float
 /* Bytes of workspace attn_fwd_tree needs (0 for invalid arguments). */
 size_t attn_tree_workspace_bytes(int Hq, int Hkv, int max_seqlen_q, int d);
 
+/* ------------------------------------------------------------------------------------
+ * Prompts of grouped heads, and a cache of bounded length.
+ * (Additions of this library, as the paged cache is.)
+ * ------------------------------------------------------------------------------------ */
+
+enum { ATTN_WEIGHT_BF16 = 0, ATTN_WEIGHT_FP32 = 1 };
+
+/*
+ * attn_qk_rotate -- norms of query and key heads and their rotation by position, in one pass.
+ *   Q [total, Hq, d], K [total, Hkv, d]: device bf16, element (t, h, x) at t * strides[0] + h *
+ *         strides[1] + x (host int64[2] in elements, multiples of 8), so slices of a joint
+ *         projection need no copy.  Q_out and K_out the same with strides of their own; they may be
+ *         Q and K themselves (same strides), not other parts of them.  16-byte aligned.  Hq or Hkv
+ *         may be 0 (its pointers are not used).
+ *   q_weight, k_weight  device [d] of weight_type, or NULL: no norm.  With one, a row becomes
+ *         x_i * w_i / sqrt(mean(x^2) + eps).
+ *   inv_freq  device fp32 [num_freq], num_freq a multiple of 8 up to d / 2 (0: no rotation).
+ *         Then column i of the first num_freq and column i + num_freq (interleaved != 0: columns
+ *         2 i and 2 i + 1) turn by position * inv_freq[i]: (a, b) -> (a cos - b sin, b cos + a sin).
+ *         Columns from 2 * num_freq on keep their places.  The angle's error is 2^-52 of it, and
+ *         2^-23 rad.  A frequency that is not finite makes its columns NaN.
+ *   Positions.  cu_seqlens (device int32 [B + 1]): row cu_seqlens[b] + i is at position
+ *         start_lens[b] + i (device int32 [B] or NULL for 0, negative counts as 0); rows outside
+ *         every sequence are left as they were.  NULL: all rows are one sequence (B = 1).
+ *         positions (device int32 [total] or NULL) replaces these positions: drafted trees, or
+ *         caches whose rows have moved (attn_cache_evict).
+ *   All in fp32, rounded to bf16 once; |x| must stay below 2^60 for its square.  Asynchronous.
+ */
+attn_status attn_qk_rotate(const void* Q, const void* K, void* Q_out, void* K_out, const int64_t* q_strides,
+                           const int64_t* k_strides, const int64_t* q_out_strides, const int64_t* k_out_strides,
+                           const int32_t* cu_seqlens, const int32_t* start_lens, const int32_t* positions,
+                           const float* inv_freq, int num_freq, int interleaved, const void* q_weight,
+                           const void* k_weight, int weight_type, float eps, int B, int Hq, int Hkv, int d, int total,
+                           void* stream);
+
+/*
+ * attn_fwd_prompt -- attn_fwd over packed sequences whose query heads share K/V heads.
+ *   Q, O [total_q, Hq, d], K, V [total_k, Hkv, d]: device bf16 with strides (token, head) as in
+ *         attn_qk_rotate, positive here.  Hq is a multiple of Hkv: query head h reads K/V head
+ *         h / (Hq / Hkv).  LSE fp32 [Hq, total_q].
+ *   cu_seqlens_q, cu_seqlens_k, max_seqlen_q: as attn_fwd_varlen (rows past max_seqlen_q and rows
+ *         outside every sequence are left as they were; a sequence's keys are rows
+ *         cu_seqlens_k[b] .. cu_seqlens_k[b + 1] - 1).  causal: bottom-right aligned, so a sequence
+ *         with more keys than queries is a prompt over its prefix.
+ *   What K and V hold where a row does not look, infinities and NaN among it, does not reach the row.
+ *   Asynchronous, allocates nothing.  Errors as attn_fwd.
+ */
+attn_status attn_fwd_prompt(const void* Q, const void* K, const void* V, void* O, float* LSE, const int64_t* q_strides,
+                            const int64_t* k_strides, const int64_t* v_strides, const int64_t* o_strides,
+                            const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k, int B, int Hq, int Hkv,
+                            int max_seqlen_q, int total_q, int total_k, int d, float scale, int causal, void* stream);
+
+/*
+ * attn_cache_weigh -- the attention weight that cached keys receive from a call's queries.
+ *   Q, cu_seqlens_q, ctx_lens, block_table: as attn_fwd_tree without a mask (token i of a sequence
+ *         sees positions up to ctx_lens[b] + i), with any number of tokens a sequence, whose K are in
+ *         the cache already; e.g. a prompt's last tokens, or all of them.  LSE fp32 [Hq, total_q]:
+ *         what the attention of these queries returned (attn_fwd_tree, attn_fwd_prompt,
+ *         attn_fwd_varlen), with the same scale.  The cache's values are not used (v and v_scale may
+ *         be NULL).
+ *   weights, out  device fp32 [num_pages, num_heads, page_size]:
+ *           out[p] = decay * weights[p] + sum exp(scale * q . k_p - LSE)
+ *         over the rows of the key's head (all tokens that see p, all heads of the group).  Positions
+ *         from ctx_lens[b] on, which the call's tokens brought, start from 0, and with decay = 0
+ *         weights is not read (may be NULL).  out may be weights itself, or another pool of the same
+ *         layout (drafts that may be taken back).  Only positions of sequences with tokens in the
+ *         call are written, and no page may be theirs twice.  A row that saw nothing (LSE = -inf)
+ *         adds nothing.
+ *   Each sum is made in one order whatever the batch around it: the same bits every time.
+ *   Asynchronous, allocates nothing.
+ */
+attn_status attn_cache_weigh(const void* Q, const float* LSE, const attn_cache* cache, const float* weights, float* out,
+                             const int32_t* block_table, int max_pages, const int32_t* cu_seqlens_q,
+                             const int32_t* ctx_lens, int B, int Hq, int total_q, float scale, float decay,
+                             void* stream);
+
+/*
+ * attn_cache_evict -- cut sequences to `keep` tokens a head by their weights.
+ *   lens  device int32 [B]: the sequences' tokens (clamped to [0, max_pages * page_size]).
+ *   weights  device fp32 [num_pages, num_heads, page_size] (attn_cache_weigh).  Every (sequence, head)
+ *         with more than `keep` tokens keeps its first `sink`, its last `recent` (together at most
+ *         keep) and, of those between, the ones with the largest weights; of equal ones the first,
+ *         NaN counts as -inf.  Heads choose for themselves.
+ *   The rows kept (K, V, scale codes, weights) move, in order, to places 0, 1, ... of the pages that
+ *         out_table (device int32 [B, out_max_pages]) names, which must be pages that no sequence
+ *         of the call reads and no place names twice; or, out_table NULL, of the sequence's own
+ *         pages, which then must be no other sequence's of the call.
+ *   kept  device int32 [B, num_heads, keep]: the positions kept, increasing; -1 past the sequence's
+ *         tokens.  out_lens device int32 [B]: min(lens, keep); not lens itself.
+ *   Positions without a page count as weight -inf and are packed as zeros of weight 0, places without
+ *         one are not written; both are reported by attn_cache_check.
+ *   Asynchronous, allocates nothing.
+ */
+attn_status attn_cache_evict(const attn_cache* cache, float* weights, const int32_t* block_table, int max_pages,
+                             const int32_t* out_table, int out_max_pages, const int32_t* lens, int32_t* kept,
+                             int32_t* out_lens, int B, int keep, int sink, int recent, void* stream);
+
 /* attn_status_sync, then ATTN_ERR_BAD_PAGE if a cache call on the current device has met a
  * position without a page since the last check (read and cleared with plain copies). */
 attn_status attn_cache_check(void* stream);

@@ -19,7 +19,8 @@ LIB_PATH = os.path.join(_HERE, "libattn.so")
 EXPORTS = ("attn_fwd", "attn_fwd_ex", "attn_fwd_strided", "attn_fwd_varlen", "attn_fwd_host", "attn_release_workspace", "attn_status_sync", "attn_last_error",
            "attn_version", "attn_fwd_noalloc", "attn_fwd_states", "attn_merge_states",
            "attn_splitkv_workspace_bytes", "attn_splitkv_splits", "attn_fwd_splitkv",
-           "attn_cache_write", "attn_cache_read", "attn_cache_check", "attn_fwd_tree", "attn_tree_workspace_bytes")
+           "attn_cache_write", "attn_cache_read", "attn_cache_check", "attn_fwd_tree", "attn_tree_workspace_bytes",
+           "attn_qk_rotate", "attn_fwd_prompt", "attn_cache_weigh", "attn_cache_evict")
 
 STATUS_NAMES = {0: "ATTN_OK", -1: "ATTN_ERR_NULLPTR", -2: "ATTN_ERR_BAD_SHAPE", -3: "ATTN_ERR_UNSUPPORTED_D",
                 -4: "ATTN_ERR_MISALIGNED", -5: "ATTN_ERR_NO_DEVICE", -6: "ATTN_ERR_LAUNCH", -7: "ATTN_ERR_TIMEOUT",
@@ -103,6 +104,15 @@ def load_library():
         lib.attn_fwd_tree.restype = i
         lib.attn_tree_workspace_bytes.argtypes = [i, i, i, i]
         lib.attn_tree_workspace_bytes.restype = ctypes.c_size_t
+        lib.attn_qk_rotate.argtypes = [vp, vp, vp, vp, i64p, i64p, i64p, i64p, vp, vp, vp, vp, i, i, vp, vp, i, f, i, i,
+                                       i, i, i, vp]
+        lib.attn_qk_rotate.restype = i
+        lib.attn_fwd_prompt.argtypes = [vp, vp, vp, vp, vp, i64p, i64p, i64p, i64p, vp, vp, i, i, i, i, i, i, i, f, i, vp]
+        lib.attn_fwd_prompt.restype = i
+        lib.attn_cache_weigh.argtypes = [vp, vp, cache, vp, vp, vp, i, vp, vp, i, i, i, f, f, vp]
+        lib.attn_cache_weigh.restype = i
+        lib.attn_cache_evict.argtypes = [cache, vp, vp, i, vp, i, vp, vp, vp, i, i, i, i, vp]
+        lib.attn_cache_evict.restype = i
         _lib = lib
     return _lib
 
@@ -618,6 +628,242 @@ def attn_fwd_tree(Q, k_cache, v_cache, block_table, ctx_lens, cu_seqlens_q, max_
     if rc != 0:
         _check(rc)
     return O, LSE
+
+
+# --- prompts of grouped heads, and a cache of bounded length -----------------------
+
+WEIGHT_BF16, WEIGHT_FP32 = 0, 1
+
+
+def _packed(name, t, dev, heads=None, d=None):
+    """Checks a packed bf16 tensor [total, heads, d] with a contiguous last dimension; returns its strides."""
+    import torch
+    shape = t.shape
+    if (len(shape) != 3 or t.dtype != torch.bfloat16 or t.device != dev or (heads is not None and shape[1] != heads)
+            or (d is not None and shape[2] != d)):
+        raise ValueError(f"{name} must be a bf16 tensor [total, heads, d] with the call's heads and d, on its device")
+    st = t.stride()
+    if st[2] != 1 and t.numel():
+        raise ValueError(f"{name} must have a contiguous last dimension")
+    return _Strides(st[0], st[1])
+
+
+def attn_qk_rotate(Q, K, cu_seqlens=None, inv_freq=None, Q_out=None, K_out=None, *, start_lens=None, positions=None,
+                   q_weight=None, k_weight=None, eps=1e-6, interleaved=False, stream=None):
+    """Norms of query and key heads and their rotation by position, in one pass.
+
+    Q [total, Hq, d], K [total, Hkv, d]: bf16 CUDA tensors with a contiguous last dimension (views of a
+    joint projection need no copy).  q_weight, k_weight [d] (bf16 or fp32, both alike; None: no norm):
+    x * w / sqrt(mean(x^2) + eps).  inv_freq fp32 [r], r a multiple of 8 up to d / 2 (None: no
+    rotation): column i turns with column i + r (interleaved: 2 i with 2 i + 1) by position *
+    inv_freq[i].  cu_seqlens int32 [B + 1] (None: all rows are one sequence): row cu_seqlens[b] + i is at
+    start_lens[b] + i (int32 [B]; None: 0), rows outside every sequence are left as they were;
+    positions int32 [total] replaces these.  Returns Q_out and K_out (allocated contiguous when not
+    given; they may be Q and K).
+    """
+    import torch
+    dev = Q.device
+    away = _elsewhere(dev, stream)
+    if away is not None:
+        with away:
+            return attn_qk_rotate(Q, K, cu_seqlens, inv_freq, Q_out, K_out, start_lens=start_lens, positions=positions,
+                                  q_weight=q_weight, k_weight=k_weight, eps=eps, interleaved=interleaved)
+    qs = _packed("Q", Q, dev)
+    total, Hq, d = Q.shape
+    ks = _packed("K", K, dev, None, d)
+    Hkv = K.shape[1]
+    if K.shape[0] != total:
+        raise ValueError("Q and K must have the same tokens")
+    i32 = torch.int32
+    B, cu_ptr, start_ptr, pos_ptr, freq_ptr, r = 1, None, None, None, None, 0
+    if cu_seqlens is not None:
+        B = cu_seqlens.numel() - 1
+        if B < 0 or cu_seqlens.dtype != i32 or cu_seqlens.device != dev or not cu_seqlens.is_contiguous():
+            raise ValueError("cu_seqlens must be a contiguous int32 tensor [B + 1] on Q's device")
+        cu_ptr = cu_seqlens.data_ptr()
+    if start_lens is not None:
+        if start_lens.numel() != B or start_lens.dtype != i32 or start_lens.device != dev or not start_lens.is_contiguous():
+            raise ValueError("start_lens must be a contiguous int32 tensor [B] on Q's device")
+        start_ptr = start_lens.data_ptr()
+    if positions is not None:
+        if positions.numel() != total or positions.dtype != i32 or positions.device != dev or not positions.is_contiguous():
+            raise ValueError("positions must be a contiguous int32 tensor [total] on Q's device")
+        pos_ptr = positions.data_ptr()
+    if inv_freq is not None:
+        if inv_freq.dim() != 1 or inv_freq.dtype != torch.float32 or inv_freq.device != dev or not inv_freq.is_contiguous():
+            raise ValueError("inv_freq must be a contiguous fp32 tensor [r] on Q's device")
+        freq_ptr, r = inv_freq.data_ptr(), inv_freq.numel()
+    wtype, wptr = WEIGHT_BF16, [None, None]
+    for i, w in enumerate((q_weight, k_weight)):
+        if w is None:
+            continue
+        if (w.numel() != d or w.dtype not in (torch.bfloat16, torch.float32) or w.device != dev or not w.is_contiguous()
+                or (i == 1 and q_weight is not None and w.dtype != q_weight.dtype)):
+            raise ValueError("q_weight and k_weight must be contiguous tensors [d] of one type, bf16 or fp32, on Q's device")
+        wtype = WEIGHT_FP32 if w.dtype == torch.float32 else WEIGHT_BF16
+        wptr[i] = w.data_ptr()
+    if Q_out is None:
+        Q_out = torch.empty((total, Hq, d), dtype=torch.bfloat16, device=dev)
+    if K_out is None:
+        K_out = torch.empty((total, Hkv, d), dtype=torch.bfloat16, device=dev)
+    if Q_out.shape != Q.shape or K_out.shape != K.shape:
+        raise ValueError("Q_out and K_out must be shaped like Q and K")
+    qos, kos = _packed("Q_out", Q_out, dev), _packed("K_out", K_out, dev)
+    rc = load_library().attn_qk_rotate(Q.data_ptr(), K.data_ptr(), Q_out.data_ptr(), K_out.data_ptr(), qs, ks, qos, kos,
+                                       cu_ptr, start_ptr, pos_ptr, freq_ptr, r, 1 if interleaved else 0, wptr[0], wptr[1],
+                                       wtype, eps, B, Hq, Hkv, d, total, torch._C._cuda_getCurrentRawStream(dev.index))
+    if rc != 0:
+        _check(rc)
+    return Q_out, K_out
+
+
+def attn_fwd_prompt(Q, K, V, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, O=None, LSE=None, *, scale=None, causal=True,
+                    stream=None):
+    """Attention of packed prompts whose query heads share K/V heads.
+
+    Q [total_q, Hq, d], K, V [total_k, Hkv, d]: bf16 CUDA tensors with a contiguous last dimension
+    (views of a joint projection need no copy), Hq a multiple of Hkv; cu_seqlens_q / cu_seqlens_k int32
+    [B + 1]; max_seqlen_q >= the longest sequence's queries.  causal: bottom-right aligned, so more keys
+    than queries are a prompt over its prefix.  Returns O [total_q, Hq, d] and LSE [Hq, total_q]
+    (allocated when not given; rows outside every sequence are left as they were).  What K and V hold
+    where a row does not look does not reach it.
+    """
+    import torch
+    dev = Q.device
+    away = _elsewhere(dev, stream)
+    if away is not None:
+        with away:
+            return attn_fwd_prompt(Q, K, V, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, O, LSE, scale=scale, causal=causal)
+    qs = _packed("Q", Q, dev)
+    total_q, Hq, d = Q.shape
+    ks = _packed("K", K, dev, None, d)
+    total_k, Hkv = K.shape[:2]
+    vs = _packed("V", V, dev, Hkv, d)
+    if V.shape[0] != total_k:
+        raise ValueError("K and V must have the same tokens")
+    B = cu_seqlens_q.numel() - 1
+    for t in (cu_seqlens_q, cu_seqlens_k):
+        if B < 0 or t.numel() != B + 1 or t.dtype != torch.int32 or t.device != dev or not t.is_contiguous():
+            raise ValueError("cu_seqlens_q and cu_seqlens_k must be contiguous int32 tensors [B + 1] on Q's device")
+    if O is None:
+        O = torch.empty((total_q, Hq, d), dtype=torch.bfloat16, device=dev)
+    elif O.shape != Q.shape:
+        raise ValueError("O must be shaped like Q")
+    os_ = _packed("O", O, dev)
+    if LSE is None:
+        LSE = torch.empty((Hq, total_q), dtype=torch.float32, device=dev)
+    elif LSE.shape != (Hq, total_q) or LSE.dtype != torch.float32 or LSE.device != dev or not LSE.is_contiguous():
+        raise ValueError("LSE must be a contiguous fp32 tensor [Hq, total_q]")
+    rc = load_library().attn_fwd_prompt(Q.data_ptr(), K.data_ptr(), V.data_ptr(), O.data_ptr(), LSE.data_ptr(), qs, ks, vs,
+                                        os_, cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), B, Hq, Hkv,
+                                        int(max_seqlen_q), total_q, total_k, d,
+                                        1.0 / math.sqrt(d) if scale is None else scale, 1 if causal else 0,
+                                        torch._C._cuda_getCurrentRawStream(dev.index))
+    if rc != 0:
+        _check(rc)
+    return O, LSE
+
+
+def _pool_weights(name, w, shape, dev):
+    import torch
+    if w.dtype != torch.float32 or w.shape != shape or w.device != dev or not w.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous fp32 tensor [num_pages, Hkv, page_size] on the cache's device")
+
+
+def attn_cache_weigh(Q, LSE, k_cache, weights, block_table, ctx_lens, cu_seqlens_q, out=None, *, decay=1.0, k_scale=None,
+                     scale=None, stream=None):
+    """The attention weight that cached keys receive from these queries, added to what they had.
+
+    Q [total_q, Hq, d] and LSE [Hq, total_q]: queries and what their attention returned (attn_fwd_tree,
+    attn_fwd_prompt, attn_fwd_varlen; same scale); cu_seqlens_q int32 [B + 1], any number of tokens a
+    sequence, whose keys are cached at positions ctx_lens[b], ... (int32 [B]; None: 0); token i sees
+    positions up to ctx_lens[b] + i.  weights, out fp32 [num_pages, Hkv, page_size]:
+    out = decay * weights + sum over the rows that see a key of exp(scale * q . k - LSE), where positions
+    that the call brought start from 0; decay = 0 reads no weights (they may be None).  Only positions of
+    sequences with tokens are written.  Returns out (None: weights, in place).  The cache's other
+    arguments: as attn_cache_write; its values are not needed.
+    """
+    import torch
+    dev = k_cache.device
+    away = _elsewhere(dev, stream)
+    if away is not None:
+        with away:
+            return attn_cache_weigh(Q, LSE, k_cache, weights, block_table, ctx_lens, cu_seqlens_q, out, decay=decay,
+                                    k_scale=k_scale, scale=scale)
+    cache = _cache_args(k_cache, k_cache, k_scale, k_scale)
+    shape = Q.shape
+    if (len(shape) != 3 or shape[2] != cache.d or Q.dtype != torch.bfloat16 or Q.device != dev or not Q.is_contiguous()):
+        raise ValueError("Q must be a contiguous bf16 tensor [total_q, Hq, d] on the cache's device")
+    total_q, Hq, d = shape
+    if LSE.shape != (Hq, total_q) or LSE.dtype != torch.float32 or LSE.device != dev or not LSE.is_contiguous():
+        raise ValueError("LSE must be a contiguous fp32 tensor [Hq, total_q] on the cache's device")
+    B, max_pages, ctx_ptr = _batch_args(dev, block_table, cu_seqlens_q, ctx_lens)
+    if out is None:
+        out = weights
+    if out is None or (weights is None and decay != 0):
+        raise ValueError("weights may be None only with decay = 0 and an out")
+    pool = k_cache.shape[:3]
+    _pool_weights("out", out, pool, dev)
+    if weights is not None and weights is not out:
+        _pool_weights("weights", weights, pool, dev)
+    rc = load_library().attn_cache_weigh(Q.data_ptr(), LSE.data_ptr(), cache, None if weights is None else weights.data_ptr(),
+                                         out.data_ptr(), block_table.data_ptr(), max_pages, cu_seqlens_q.data_ptr(), ctx_ptr,
+                                         B, Hq, total_q, 1.0 / math.sqrt(d) if scale is None else scale, decay,
+                                         torch._C._cuda_getCurrentRawStream(dev.index))
+    if rc != 0:
+        _check(rc)
+    return out
+
+
+def attn_cache_evict(k_cache, v_cache, weights, block_table, lens, keep, *, sink=0, recent=0, out_table=None, kept=None,
+                     out_lens=None, k_scale=None, v_scale=None, stream=None):
+    """Cut sequences to ``keep`` tokens a head by their weights; their rows are packed in order.
+
+    lens int32 [B]: the sequences' tokens; weights fp32 [num_pages, Hkv, page_size] (attn_cache_weigh).  A
+    longer sequence keeps, in each head, its first ``sink`` tokens, its last ``recent`` ones and the
+    largest weights between (the first of equal ones).  K, V, scales and weights of what is kept move to
+    positions 0, 1, ... of the pages of out_table (int32 [B, out_max_pages], pages that no sequence of the
+    call reads) or, without one, of the sequence's own.  Returns kept int32 [B, Hkv, keep] (the positions,
+    increasing; -1 past the sequence's tokens) and out_lens int32 [B] = min(lens, keep), allocated when not
+    given.  Positions without a page are reported by cache_check().  The cache's arguments: as
+    attn_cache_write.
+    """
+    import torch
+    dev = k_cache.device
+    away = _elsewhere(dev, stream)
+    if away is not None:
+        with away:
+            return attn_cache_evict(k_cache, v_cache, weights, block_table, lens, keep, sink=sink, recent=recent,
+                                    out_table=out_table, kept=kept, out_lens=out_lens, k_scale=k_scale, v_scale=v_scale)
+    cache = _cache_args(k_cache, v_cache, k_scale, v_scale)
+    _pool_weights("weights", weights, k_cache.shape[:3], dev)
+    i32 = torch.int32
+    if block_table.dim() != 2 or block_table.dtype != i32 or block_table.device != dev or not block_table.is_contiguous():
+        raise ValueError("block_table must be a contiguous int32 tensor [B, max_pages] on the cache's device")
+    B, max_pages = block_table.shape
+    if lens.numel() != B or lens.dtype != i32 or lens.device != dev or not lens.is_contiguous():
+        raise ValueError("lens must be a contiguous int32 tensor [B] on the cache's device")
+    to_ptr, to_pages = None, 0
+    if out_table is not None:
+        if (out_table.dim() != 2 or out_table.shape[0] != B or out_table.dtype != i32 or out_table.device != dev
+                or not out_table.is_contiguous()):
+            raise ValueError("out_table must be a contiguous int32 tensor [B, out_max_pages] on the cache's device")
+        to_ptr, to_pages = out_table.data_ptr(), out_table.shape[1]
+    keep = int(keep)
+    if kept is None:
+        kept = torch.empty((B, cache.num_heads, max(keep, 0)), dtype=i32, device=dev)
+    elif kept.shape != (B, cache.num_heads, keep) or kept.dtype != i32 or kept.device != dev or not kept.is_contiguous():
+        raise ValueError("kept must be a contiguous int32 tensor [B, Hkv, keep] on the cache's device")
+    if out_lens is None:
+        out_lens = torch.empty(B, dtype=i32, device=dev)
+    elif out_lens.numel() != B or out_lens.dtype != i32 or out_lens.device != dev or not out_lens.is_contiguous():
+        raise ValueError("out_lens must be a contiguous int32 tensor [B] on the cache's device")
+    rc = load_library().attn_cache_evict(cache, weights.data_ptr(), block_table.data_ptr(), max_pages, to_ptr, to_pages,
+                                         lens.data_ptr(), kept.data_ptr(), out_lens.data_ptr(), B, keep, int(sink),
+                                         int(recent), torch._C._cuda_getCurrentRawStream(dev.index))
+    if rc != 0:
+        _check(rc)
+    return kept, out_lens
 
 
 def cache_check(stream=None):

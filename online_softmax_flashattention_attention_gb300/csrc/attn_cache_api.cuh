@@ -31,7 +31,8 @@ constexpr int kMaxPage = 65536, kMaxHeads = 65536;
 bool odd16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
 bool odd_to(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) != 0; }
 
-attn_status check_cache(const attn_cache* c, int max_pages) {
+// need_v: whether the call touches the values (their pointers may be NULL otherwise).
+attn_status check_cache(const attn_cache* c, int max_pages, bool need_v = true) {
   if (!c) return fail(ATTN_ERR_NULLPTR, "cache must not be NULL");
   if (c->size < sizeof(attn_cache))
     return fail(ATTN_ERR_BAD_ARG, "attn_cache.size=%zu; expected at least %zu", c->size, sizeof(attn_cache));
@@ -47,10 +48,10 @@ attn_status check_cache(const attn_cache* c, int max_pages) {
   if (max_pages < 0 || static_cast<long long>(max_pages) * c->page_size > INT32_MAX - 255)
     return fail(ATTN_ERR_BAD_SHAPE, "max_pages=%d: a sequence has at most 2^31 - 256 positions", max_pages);
   if (c->num_pages > 0) {
-    if (!c->k || !c->v) return fail(ATTN_ERR_NULLPTR, "the cache's k and v must not be NULL");
+    if (!c->k || (need_v && !c->v)) return fail(ATTN_ERR_NULLPTR, "the cache's k and v must not be NULL");
     if (odd16(c->k) || odd16(c->v)) return fail(ATTN_ERR_MISALIGNED, "the cache's k and v must be 16-byte aligned");
     if (c->type == ATTN_CACHE_E4M3) {
-      if (!c->k_scale || !c->v_scale) return fail(ATTN_ERR_NULLPTR, "an e4m3 cache needs k_scale and v_scale");
+      if (!c->k_scale || (need_v && !c->v_scale)) return fail(ATTN_ERR_NULLPTR, "an e4m3 cache needs k_scale and v_scale");
       if (odd16(c->k_scale) || odd16(c->v_scale))
         return fail(ATTN_ERR_MISALIGNED, "k_scale and v_scale must be 16-byte aligned");
     }

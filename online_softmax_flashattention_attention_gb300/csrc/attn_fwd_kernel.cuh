@@ -53,6 +53,8 @@ constexpr int kWarpTma = 4;
 constexpr int kWarpPv = 5;
 constexpr int kWarpS = 6;
 constexpr int kThreads = 224;      // 4 softmax warps + producer + two MMA issuers
+constexpr int kWarpFix = 7;        // prompts (attn_fwd_prompt): an eighth warp repairs ragged V blocks
+constexpr int kPromptThreads = 256;
 constexpr uint32_t kTmemCols = 512;
 
 struct FwdParams {
@@ -94,6 +96,11 @@ struct FwdParams {
   // integer division, the same on long tiles.  (The two-tile kernel keeps the division: the
   // same change measured 0.955x there.)
   uint32_t dm_split, ds_split, dm_order, ds_order, dm_h, ds_h;
+  // prompts only: query heads that share a K/V head, as a divisor, and V in global memory (element
+  // (row, head, x) at v + row * vs_r + head * vs_h + x)
+  uint32_t dm_g, ds_g;
+  const __nv_bfloat16* v;
+  long long vs_r, vs_h;
 };
 
 __device__ __forceinline__ int fast_div(int n, uint32_t m, uint32_t s) {
@@ -113,7 +120,7 @@ constexpr int kMaxSortedSeqs = 512;
 // the softmax warps waiting for scores, 64 because every block's hand-offs and rescale now
 // cover half the keys.  They stay as options because they are the same recurrence over other
 // blocks, which the tests compare with the 128-key build.
-template <int D, int BN = kBN>
+template <int D, int BN = kBN, bool kPrompt = false>
 struct FwdCfg {
   static constexpr int kBNc = BN;
   static constexpr int kSub = D / 64;                   // 64-column swizzle sub-tiles per row tile
@@ -137,9 +144,9 @@ struct FwdCfg {
   static constexpr int kOffV = kOffK + kStages * kKVBytes;
   static constexpr int kOffBar = kOffV + kStages * kKVBytes;
   // barriers: q_full, q_free, (one unused slot), k_full[S], v_full[S], k_free[S],
-  // v_free[S], s_full[B], pv_done[B], p_full[B], drain[2]
-  static constexpr int kNumBars = 3 + 4 * kStages + 3 * kSBufs + 2;
-  static constexpr int kOffMisc = kOffBar + 8 * kNumBars;  // tmem base, abort flag
+  // v_free[S], s_full[B], pv_done[B], p_full[B], drain[2]; prompts: v_fixed[S]
+  static constexpr int kNumBars = 3 + 4 * kStages + 3 * kSBufs + 2 + (kPrompt ? kStages : 0);
+  static constexpr int kOffMisc = kOffBar + 8 * kNumBars;  // tmem base, abort flag, prompts: 8 tags
   static constexpr int kOffPerm = kOffMisc + 16;           // uint16 order of packed sequences
   static constexpr int kSmemBytes = kOffPerm + 2 * kMaxSortedSeqs;
   static constexpr int kSmemAlloc = kSmemBytes + 1024;     // slack to align the base to 1024 B
@@ -299,6 +306,36 @@ __device__ __forceinline__ Item decode(const FwdParams& p, int item, const uint1
 // front of each head spread evenly over the CTAs.
 __device__ __forceinline__ int item_of(int r, int c, int G) { return r * G + ((r & 1) ? G - 1 - c : c); }
 
+// Whether either bf16 of a pair is infinite or NaN.
+__device__ __forceinline__ bool any_nonfinite(uint32_t w) {
+  return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+}
+// A bf16 pair with its infinite and NaN halves zeroed.
+__device__ __forceinline__ uint32_t finite_only(uint32_t w) {
+  if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
+  if ((w & 0x7f800000u) == 0x7f800000u) w &= 0x0000ffffu;
+  return w;
+}
+
+// Prompts: the infinities and NaN of values that went into the product as zero, to a row that sees
+// keys [k0, k1) of them: columns col .. col + 31 of its o~ (a positive weight leaves them what they are).
+__device__ __noinline__ void prompt_add_nonfinite_row(const __nv_bfloat16* v, long long stride, int keys, float* o) {
+  for (int k = 0; k < keys; ++k)
+    for (int i = 0; i < 32; ++i) {
+      const float x = __bfloat162float(v[k * stride + i]);
+      if (!(fabsf(x) < INFINITY)) o[i] += x;
+    }
+}
+__device__ __forceinline__ void prompt_add_nonfinite(const FwdParams& p, const Item& it, int k0, int k1, int col, uint32_t* o) {
+  float f[32];
+#pragma unroll
+  for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(o[i]);
+  prompt_add_nonfinite_row(p.v + static_cast<long long>(it.k_base + k0) * p.vs_r +
+                               fast_div(it.hh, p.dm_g, p.ds_g) * p.vs_h + col, p.vs_r, k1 - k0, f);
+#pragma unroll
+  for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(f[i]);
+}
+
 // kSoftPairs: of every 16 pairs of scores in a block with no masked key, this many take
 // their exponential from exp2_poly2 instead of ex2.approx, to relieve the MUFU unit.
 //
@@ -311,12 +348,18 @@ __device__ __forceinline__ int item_of(int r, int c, int G) { return r * G + ((r
 // P V product has finished, and leaves by one TMA store; the softmax warps then hand that
 // stage back to the producer (v_free) instead of the P V issuer.  At d = 128 each thread
 // stores its row of O straight from registers.
-template <int D, bool kStates, int kSoftPairs, bool kPacked, int BN = kBN>
-__global__ void __launch_bounds__(kThreads, 1)
+//
+// kPrompt (attn_fwd_prompt): K and V have fewer heads, each shared by a group of query heads, and what
+// a row does not see must not reach it, whatever it holds.  Scores are masked; but 0 * NaN is NaN, so
+// in every block that some row of the tile sees in part (a sequence's end, the diagonal) an eighth
+// warp zeroes V's rows past the end, which belong to somebody else, and the infinities and NaN among
+// the others; rows that do see those get them added in the epilogue.
+template <int D, bool kStates, int kSoftPairs, bool kPacked, int BN = kBN, bool kPrompt = false>
+__global__ void __launch_bounds__(kPrompt ? kPromptThreads : kThreads, 1)
     attn_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
                     const FwdParams p) {
-  using C = FwdCfg<D, BN>;
+  using C = FwdCfg<D, BN, kPrompt>;
   constexpr int kBN = BN;           // keys per block of this instantiation
   constexpr int kSBufs = C::kSBufs;
   extern __shared__ uint8_t smem_raw[];
@@ -338,6 +381,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   // p_full[b]: the softmax warps have written P_g (and rescaled o~) for g % 3 == b
   auto bar_p_full = [&](int b) { return bar0 + 8u * (3 + 4 * C::kStages + 2 * kSBufs + b); };
   auto bar_drain = [&](int i) { return bar0 + 8u * (3 + 4 * C::kStages + 3 * kSBufs + i); };
+  // prompts: a V block that some row sees in part has been repaired
+  auto bar_v_fixed = [&](int s) { return bar0 + 8u * (3 + 4 * C::kStages + 3 * kSBufs + 2 + s); };
+  // prompts: tag[u % 8] = u + 1 (a byte) once tile u of this CTA has met an infinity or NaN in such a
+  // block; the repair is at most kStages tiles ahead of the epilogue that asks.  (A tag left from 256
+  // tiles ago makes the epilogue look once more, and find nothing.)
+  volatile uint8_t* tag = smem + C::kOffMisc + 8;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + C::kOffMisc + 4);
 
@@ -354,7 +403,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar_k_full(s), 1);
       mbar_init(bar_v_full(s), 1);
       mbar_init(bar_k_free(s), 1);
-      mbar_init(bar_v_free(s), 1);
+      // prompts: the repair hands every V block back too, ragged or not, so that a warp that waits by
+      // parity is never passed by two turns of the ring
+      mbar_init(bar_v_free(s), kPrompt ? 2 : 1);
+      if constexpr (kPrompt) mbar_init(bar_v_fixed(s), 1);
     }
     for (int i = 0; i < kSBufs; ++i) {
       mbar_init(bar_s_full(i), 1);
@@ -364,6 +416,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(bar_drain(0), 1);
     mbar_init(bar_drain(1), 1);
     *abort_flag = 0u;
+    if constexpr (kPrompt) {
+      for (int i = 0; i < 8; ++i) tag[i] = 0;
+    }
     fence_mbar_init();
   }
   if (warp == kWarpPv) tmem_alloc<kTmemCols>(smem_u32(tmem_slot));
@@ -403,6 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (item >= p.num_items) break;
         const Item it = decode<kPacked, kBN>(p, item, seq_perm);
         if (it.nblk == 0) continue;
+        const int hkv = kPrompt ? fast_div(it.hh, p.dm_g, p.ds_g) : it.hh;
         // the previous tile's Q must have been read by its last S product
         if (kq > 0 && !mbar_wait(bar_q_free, (kq - 1) & 1, wc, 13)) break;
         mbar_arrive_expect_tx(bar_q_full, C::kQBytes);
@@ -422,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_arrive_expect_tx(bar_k_full(st), C::kKVBytes);
             for (int s = 0; s < C::kSub; ++s)
               tma_load_4d(sK + st * C::kKVBytes + s * C::kSubBytesKV, &tmK, bar_k_full(st), s * 64,
-                          it.k_base + (it.jb0 + j) * kBN, it.hh, it.bcoord, pol_kv);
+                          it.k_base + (it.jb0 + j) * kBN, hkv, it.bcoord, pol_kv);
             k_live |= bit;
             k_par = (k_par & ~bit) | (ph << st);
           }
@@ -433,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive_expect_tx(bar_v_full(st), C::kKVBytes);
           for (int s = 0; s < C::kSub; ++s)
             tma_load_4d(sV + st * C::kKVBytes + s * C::kSubBytesKV, &tmV, bar_v_full(st), s * 64,
-                        it.k_base + (it.jb0 + j) * kBN, it.hh, it.bcoord, pol_kv);
+                        it.k_base + (it.jb0 + j) * kBN, hkv, it.bcoord, pol_kv);
           v_live |= bit;
           v_par = (v_par & ~bit) | (ph << st);
         }
@@ -493,6 +549,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       } else {
         const uint32_t vlo = (sV >> 4) | (static_cast<uint32_t>(C::kSubBytesKV >> 4) << 16);
+        uint32_t fixed_par = 0;  // prompts: parity each v_fixed completes next
         for (int ri = 0; ok; ++ri) {
           const int item = item_of(ri, cta, G);
           if (item >= p.num_items) break;
@@ -504,8 +561,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int j = 0; ok && j < it.nblk; ++j, ++g) {
             const int st = g % C::kStages;
             // V_g has normally landed long before P_g is ready: check it first
-            ok = mbar_wait(bar_v_full(st), (g / C::kStages) & 1, wc, 7) &&
-                 mbar_wait_poll(bar_p_full(g % kSBufs), (g / kSBufs) & 1, wc, 6);
+            ok = mbar_wait(bar_v_full(st), (g / C::kStages) & 1, wc, 7);
+            if constexpr (kPrompt) {
+              if (ok && (it.jb0 + j + 1) * kBN > it.min_limit) {
+                ok = mbar_wait(bar_v_fixed(st), (fixed_par >> st) & 1u, wc, 14);
+                fixed_par ^= 1u << st;
+              }
+            }
+            ok = ok && mbar_wait_poll(bar_p_full(g % kSBufs), (g / kSBufs) & 1, wc, 6);
             if (!ok) break;
             tc_fence_after();
             // o~ += P_g V_g: 8 k-steps of 16 keys; A = P_g from tensor memory, B = V_g MN-major
@@ -529,12 +592,53 @@ __global__ void __launch_bounds__(kThreads, 1)
       mma_commit(bar_drain(warp == kWarpS));
       mbar_wait_drain(bar_drain(warp == kWarpS), 0, p.timeout_ns);
     }
+  } else if (kPrompt && warp == kWarpFix) {
+    // ================================================================ ragged blocks of V (prompts)
+    int g = 0, u = 0;  // key blocks over all items, items with work
+    bool ok = true;
+    for (int ri = 0; ok; ++ri) {
+      const int item = item_of(ri, cta, G);
+      if (item >= p.num_items) break;
+      const Item it = decode<kPacked, kBN>(p, item, seq_perm);
+      if (it.nblk == 0) continue;
+      for (int j = 0; j < it.nblk; ++j, ++g) {
+        const int st = g % C::kStages, kb = (it.jb0 + j) * kBN;
+        ok = __all_sync(0xffffffffu, mbar_wait(bar_v_full(st), (g / C::kStages) & 1, wc, 15));
+        if (!ok) break;
+        if (kb + kBN > it.min_limit) {
+          bool odd = false;
+          const int r0 = max(0, it.min_limit - kb);  // rows before it are seen by every row of the tile
+          for (int i = r0 * (D / 8) + lane; i < kBN * (D / 8); i += 32) {
+            const int r = i / (D / 8), ch = i % (D / 8);
+            uint4* at = reinterpret_cast<uint4*>(smem + C::kOffV + st * C::kKVBytes + (ch / 8) * C::kSubBytesKV + r * 128 +
+                                                 (((ch & 7) ^ (r & 7)) << 4));
+            if (kb + r >= it.kv_len) {
+              *at = make_uint4(0, 0, 0, 0);
+            } else {
+              const uint4 v = *at;
+              if (any_nonfinite(v.x) || any_nonfinite(v.y) || any_nonfinite(v.z) || any_nonfinite(v.w)) {
+                *at = make_uint4(finite_only(v.x), finite_only(v.y), finite_only(v.z), finite_only(v.w));
+                odd = true;
+              }
+            }
+          }
+          if (odd) tag[u & 7] = static_cast<uint8_t>(u + 1);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar_v_fixed(st));
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_v_free(st));
+      }
+      ++u;
+    }
   } else {
     // ================================================================ softmax / epilogue
     const int r = threadIdx.x;  // 0..127: row within the tile = tensor-memory lane
     const uint32_t tl = tmem + (static_cast<uint32_t>(warp * 32) << 16);
     const float c = p.c;
     int g = 0;  // key blocks over all items: score buffer g % 3
+    int u = 0;  // prompts: items with work
     bool ok = true;
     for (int ri = 0; ok; ++ri) {
       const int item = item_of(ri, cta, G);
@@ -670,6 +774,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       g += nblk;
       const bool store = row < it.Nq;
+      bool odd = false;  // prompts: zeroed infinities or NaN among the values of the tile's ragged blocks
+      if constexpr (kPrompt) {
+        if (nblk > 0) {
+          odd = tag[u & 7] == static_cast<uint8_t>(u + 1);
+          ++u;
+        }
+      }
+      const int odd0 = it.min_limit / kBN * kBN;  // the first key of those blocks
       if (!kStates && C::kStageO && nblk > 0) {
         // O through the V stage of the last block and one TMA store.  Every softmax warp
         // reaches this barrier once per tile with blocks, also after a failed wait (it left
@@ -693,6 +805,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t o[32];
           tmem_ld32(tl + C::kColO + q * 32, o);
           tmem_wait_ld();
+          if constexpr (kPrompt) {
+            if (odd && store) prompt_add_nonfinite(p, it, odd0, limit, q * 32, o);
+          }
 #pragma unroll
           for (int ch = 0; ch < 4; ++ch) {
             uint4 v;
@@ -711,7 +826,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (store) {
-          const float lse = l > 0.f ? (m + __log2f(l)) * 0.69314718055994531f : -INFINITY;
+          const float lse = l > 0.f || (kPrompt && l != l) ? (m + __log2f(l)) * 0.69314718055994531f : -INFINITY;
           const size_t li = p.cu_q ? static_cast<size_t>(it.hh) * p.total_q + it.q_base + row
                                    : static_cast<size_t>(it.bh) * p.Nq + row;
           p.lse[li] = lse;
@@ -776,6 +891,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int k = 0; k < D; ++k) o[k] = 0u;
         }
+        if constexpr (kPrompt) {
+          if (odd && store) {
+#pragma unroll
+            for (int q = 0; q < D / 32; ++q) prompt_add_nonfinite(p, it, odd0, limit, q * 32, o + q * 32);
+          }
+        }
 #pragma unroll
         for (int k = 0; k < D / 2; ++k)
           o[k] = pack_bf16x2(__uint_as_float(o[2 * k]) * inv, __uint_as_float(o[2 * k + 1]) * inv);
@@ -790,7 +911,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (store) {
-          const float lse = l > 0.f ? (m + __log2f(l)) * 0.69314718055994531f : -INFINITY;
+          const float lse = l > 0.f || (kPrompt && l != l) ? (m + __log2f(l)) * 0.69314718055994531f : -INFINITY;
           // [B, H, Nq], or [H, total_q] for packed sequences
           const size_t li = p.cu_q ? static_cast<size_t>(it.hh) * p.total_q + it.q_base + row
                                    : static_cast<size_t>(it.bh) * p.Nq + row;

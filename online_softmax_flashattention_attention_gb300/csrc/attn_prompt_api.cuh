@@ -1,0 +1,358 @@
+// Host side of the entry points of include/attn.h that serve prompts and caches of bounded length
+// (attn_qk_rotate, attn_fwd_prompt, attn_cache_weigh, attn_cache_evict).  Included by attn_lib.cu
+// after attn_api.cu and attn_cache_api.cuh, whose checks, device set-up and launches it shares.
+#pragma once
+
+#include "attn_evict_kernel.cuh"
+#include "attn_rotate_kernel.cuh"
+#include "attn_weigh_kernel.cuh"
+
+namespace {
+
+// Strides (token, head) in elements of packed [total, heads, d] tensors; may_repeat: an input whose
+// elements may be seen more than once.
+attn_status check_strides(const int64_t* s, const char* name, bool may_repeat) {
+  for (int i = 0; i < 2; ++i)
+    if (s[i] < (may_repeat ? 0 : 8) || (s[i] & 7) != 0 || s[i] >= (1ll << 38))
+      return fail(ATTN_ERR_BAD_ARG, "stride %lld of %s: must be a multiple of 8 elements (16 bytes) in [%d, 2^38)",
+                  static_cast<long long>(s[i]), name, may_repeat ? 0 : 8);
+  return ATTN_OK;
+}
+
+template <typename... Params, typename... Args>
+cudaError_t launch_pdl_cluster(void (*kernel)(Params...), unsigned grid, unsigned cluster, unsigned block, size_t smem,
+                               cudaStream_t stream, Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
+// Strides as the kernels take them: those of an axis of one element may be anything, and are not used.
+void fix_strides(const int64_t* s, int rows, int heads, int d, long long* row, long long* head) {
+  *head = heads > 1 ? s[1] : d;
+  *row = rows > 1 ? s[0] : static_cast<long long>(heads) * d;
+}
+
+template <int D>
+attn_status launch_prompt(const void* Q, const void* K, const void* V, void* O, float* LSE, int B, int Hq, int Hkv,
+                          int max_q, float scale, int causal, cudaStream_t stream, int dev, uint32_t* status,
+                          const Geometry& geo) {
+  static bool attr_set[kMaxDevices] = {};
+  using C = attn::FwdCfg<D, attn::kBN, true>;
+  auto kernel = attn::attn_fwd_kernel<D, false, 0, true, attn::kBN, true>;
+  attn_status st;
+  if ((st = set_smem_attr(kernel, C::kSmemAlloc, dev, attr_set)) != ATTN_OK) return st;
+  CUtensorMap mq, mk, mv, mo;
+  attn::FwdParams p;
+  Geometry no_keys = geo;
+  no_keys.k_rows = 0;
+  if ((st = make_launch<D, false>(Q, K, V, O, LSE, B, Hq, max_q, 0, scale, causal, nullptr, status, StateOut{},
+                                  Variant{}, no_keys, &mq, &mk, &mv, &mo, &p)) != ATTN_OK)
+    return st;
+  if (geo.k_rows > 0) {  // K and V have heads of their own
+    if ((st = make_map(&mk, K, D, geo.k_rows, Hkv, 1, geo.ks)) != ATTN_OK) return st;
+    if ((st = make_map(&mv, V, D, geo.k_rows, Hkv, 1, geo.vs)) != ATTN_OK) return st;
+  }
+  p.total_k = static_cast<int>(geo.k_rows);
+  p.v = static_cast<const __nv_bfloat16*>(V);
+  p.vs_r = geo.vs[2];
+  p.vs_h = geo.vs[1];
+  divisor(Hq / Hkv, &p.dm_g, &p.ds_g);
+  set_divisors(&p);
+  const unsigned grid = static_cast<unsigned>(std::min(p.num_items, sm_count(dev)));
+  const int smem = p.seq_sort ? C::kSmemAlloc : C::kSmemAllocNoPerm;
+  cudaError_t e = launch_pdl(kernel, grid, attn::kPromptThreads, smem, stream, mq, mk, mv, mo, p);
+  if (e != cudaSuccess) return fail(ATTN_ERR_LAUNCH, "kernel launch: %s", cudaGetErrorString(e));
+  return ATTN_OK;
+}
+
+template <int D, bool kF8>
+attn_status launch_weigh(const attn::WeighParams& p, int dev, cudaStream_t stream) {
+  cudaError_t e = launch_pdl(attn::attn_weigh_kernel<D, kF8>, static_cast<unsigned>(4 * sm_count(dev)),
+                             attn::kWeighThreads, 0, stream, p);
+  if (e != cudaSuccess) return fail(ATTN_ERR_LAUNCH, "weigh kernel launch: %s", cudaGetErrorString(e));
+  return ATTN_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+attn_status attn_qk_rotate(const void* Q, const void* K, void* Q_out, void* K_out, const int64_t* q_strides,
+                           const int64_t* k_strides, const int64_t* q_out_strides, const int64_t* k_out_strides,
+                           const int32_t* cu_seqlens, const int32_t* start_lens, const int32_t* positions,
+                           const float* inv_freq, int num_freq, int interleaved, const void* q_weight,
+                           const void* k_weight, int weight_type, float eps, int B, int Hq, int Hkv, int d, int total,
+                           void* stream) {
+  g_err[0] = '\0';
+  attn_status st;
+  if (d != 64 && d != 128) return fail(ATTN_ERR_UNSUPPORTED_D, "d=%d; supported: 64, 128", d);
+  if (B < 0 || total < 0 || Hq < 0 || Hkv < 0 || Hq > kMaxHeads || Hkv > kMaxHeads)
+    return fail(ATTN_ERR_BAD_SHAPE, "B=%d total=%d Hq=%d Hkv=%d; sizes must not be negative, heads at most %d", B, total,
+                Hq, Hkv, kMaxHeads);
+  if (num_freq < 0 || num_freq % 8 != 0 || 2 * static_cast<long long>(num_freq) > d)
+    return fail(ATTN_ERR_BAD_SHAPE, "num_freq=%d; must be a multiple of 8 in [0, d / 2]", num_freq);
+  if (weight_type != ATTN_WEIGHT_BF16 && weight_type != ATTN_WEIGHT_FP32)
+    return fail(ATTN_ERR_BAD_ARG, "weight type %d; ATTN_WEIGHT_BF16 or ATTN_WEIGHT_FP32", weight_type);
+  if (!std::isfinite(eps) || eps < 0.f) return fail(ATTN_ERR_BAD_ARG, "eps must be finite and >= 0");
+  if (!cu_seqlens && B != 1) return fail(ATTN_ERR_BAD_SHAPE, "B=%d; without cu_seqlens all rows are one sequence (B = 1)", B);
+  if (B == 0 || total == 0 || Hq + Hkv == 0) return ATTN_OK;
+  const void* src[2] = {Q, K};
+  void* dst[2] = {Q_out, K_out};
+  const void* weight[2] = {q_weight, k_weight};
+  const int64_t* in[2] = {q_strides, k_strides};
+  const int64_t* out[2] = {q_out_strides, k_out_strides};
+  const int heads[2] = {Hq, Hkv};
+  const char* names[2] = {"Q", "K"};
+  const char* out_names[2] = {"Q_out", "K_out"};
+  attn::RotateParams p = {};
+  for (int i = 0; i < 2; ++i) {
+    if (heads[i] == 0) continue;
+    if (!src[i] || !dst[i]) return fail(ATTN_ERR_NULLPTR, "%s and %s must not be NULL", names[i], out_names[i]);
+    if (odd16(src[i]) || odd16(dst[i]))
+      return fail(ATTN_ERR_MISALIGNED, "%s and %s must be 16-byte aligned", names[i], out_names[i]);
+    if (!in[i] || !out[i]) return fail(ATTN_ERR_NULLPTR, "the strides of %s and %s must not be NULL", names[i], out_names[i]);
+    fix_strides(in[i], total, heads[i], d, &p.src_t[i], &p.src_h[i]);
+    fix_strides(out[i], total, heads[i], d, &p.dst_t[i], &p.dst_h[i]);
+    const int64_t used_in[2] = {p.src_t[i], p.src_h[i]}, used_out[2] = {p.dst_t[i], p.dst_h[i]};
+    if ((st = check_strides(used_in, names[i], true)) != ATTN_OK) return st;
+    if ((st = check_strides(used_out, out_names[i], false)) != ATTN_OK) return st;
+    if (odd_to(weight[i], weight_type == ATTN_WEIGHT_FP32 ? 4 : 2))
+      return fail(ATTN_ERR_MISALIGNED, "a weight must be aligned to its type");
+    p.src[i] = static_cast<const __nv_bfloat16*>(src[i]);
+    p.dst[i] = static_cast<__nv_bfloat16*>(dst[i]);
+    p.weight[i] = weight[i];
+  }
+  if (num_freq > 0 && !inv_freq) return fail(ATTN_ERR_NULLPTR, "inv_freq must not be NULL when num_freq > 0");
+  if (odd_to(inv_freq, 4) || odd_to(cu_seqlens, 4) || odd_to(start_lens, 4) || odd_to(positions, 4))
+    return fail(ATTN_ERR_MISALIGNED, "inv_freq, cu_seqlens, start_lens and positions must be 4-byte aligned");
+  p.cu = cu_seqlens;
+  p.start = start_lens;
+  p.positions = positions;
+  p.freq = inv_freq;
+  p.num_freq = num_freq;
+  p.interleaved = interleaved ? 1 : 0;
+  p.weight_f32 = weight_type == ATTN_WEIGHT_FP32;
+  p.eps = eps;
+  p.B = B;
+  p.Hq = Hq;
+  p.H = Hq + Hkv;
+  p.total = total;
+  int dev;
+  uint32_t* status;
+  if ((st = get_device(&dev)) != ATTN_OK || (st = setup(dev, &status)) != ATTN_OK) return st;
+  // A block takes all heads of its tokens, so that their angles are computed once, unless that
+  // leaves SMs idle; then as few as it has in flight.
+  const unsigned blocks = (static_cast<unsigned>(total) + attn::kRotTokens - 1) / attn::kRotTokens;
+  const int least = attn::kRotThreads / (d / 8) / attn::kRotTokens * attn::kRotUnroll;
+  p.heads_per_block = blocks >= static_cast<unsigned>(2 * sm_count(dev)) ? p.H : least;
+  const dim3 grid(blocks, static_cast<unsigned>((p.H + p.heads_per_block - 1) / p.heads_per_block));
+  cudaError_t e = launch_pdl2(d == 128 ? attn::attn_qk_rotate_kernel<128> : attn::attn_qk_rotate_kernel<64>, grid,
+                              attn::kRotThreads, 0, static_cast<cudaStream_t>(stream), p);
+  if (e != cudaSuccess) return fail(ATTN_ERR_LAUNCH, "rotate kernel launch: %s", cudaGetErrorString(e));
+  return ATTN_OK;
+}
+
+attn_status attn_fwd_prompt(const void* Q, const void* K, const void* V, void* O, float* LSE, const int64_t* q_strides,
+                            const int64_t* k_strides, const int64_t* v_strides, const int64_t* o_strides,
+                            const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k, int B, int Hq, int Hkv,
+                            int max_seqlen_q, int total_q, int total_k, int d, float scale, int causal, void* stream) {
+  g_err[0] = '\0';
+  attn_status st;
+  if (d != 64 && d != 128) return fail(ATTN_ERR_UNSUPPORTED_D, "d=%d; supported: 64, 128", d);
+  if (B < 0 || Hq < 0 || max_seqlen_q < 0 || total_q < 0 || total_k < 0)
+    return fail(ATTN_ERR_BAD_SHAPE, "negative size (B=%d Hq=%d max_seqlen_q=%d total_q=%d total_k=%d)", B, Hq,
+                max_seqlen_q, total_q, total_k);
+  if (Hkv < 1 || Hkv > kMaxHeads || Hq > kMaxHeads || Hq % Hkv != 0)
+    return fail(ATTN_ERR_BAD_SHAPE, "Hq=%d must be a multiple of Hkv=%d, both at most %d", Hq, Hkv, kMaxHeads);
+  // rows are counted in 32 bits, rounded up to a block of 128
+  if (max_seqlen_q > INT32_MAX - 255 || total_q > INT32_MAX - 255 || total_k > INT32_MAX - 255)
+    return fail(ATTN_ERR_BAD_SHAPE, "max_seqlen_q, total_q and total_k are at most 2^31 - 256");
+  if (!std::isfinite(scale) || !(scale > 0.f)) return fail(ATTN_ERR_BAD_ARG, "scale must be finite and > 0");
+  if (static_cast<long long>(B) * Hq == 0 || max_seqlen_q == 0 || total_q == 0) return ATTN_OK;
+  const long long tiles = static_cast<long long>(B) * Hq * ((max_seqlen_q + attn::kBM - 1) / attn::kBM);
+  if (tiles > INT32_MAX) return fail(ATTN_ERR_BAD_SHAPE, "problem too large (%lld tiles of 128 rows)", tiles);
+  if (!Q || !O || !LSE || !cu_seqlens_q || !cu_seqlens_k)
+    return fail(ATTN_ERR_NULLPTR, "Q, O, LSE and the cu_seqlens arrays must not be NULL");
+  if (total_k > 0 && (!K || !V)) return fail(ATTN_ERR_NULLPTR, "K and V must not be NULL when total_k > 0");
+  if (odd16(Q) || odd16(O) || (total_k > 0 && (odd16(K) || odd16(V))))
+    return fail(ATTN_ERR_MISALIGNED, "Q, K, V and O must be 16-byte aligned");
+  if (odd_to(LSE, 4) || odd_to(cu_seqlens_q, 4) || odd_to(cu_seqlens_k, 4))
+    return fail(ATTN_ERR_MISALIGNED, "LSE and the cu_seqlens arrays must be 4-byte aligned");
+  Geometry g;
+  const int64_t* in[4] = {q_strides, k_strides, v_strides, o_strides};
+  const char* names[4] = {"Q", "K", "V", "O"};
+  long long* out[4] = {g.qs, g.ks, g.vs, g.os};
+  for (int i = 0; i < 4; ++i) {
+    const bool kv = i == 1 || i == 2;
+    if (kv && total_k == 0) {
+      out[i][0] = out[i][1] = out[i][2] = d;
+      continue;
+    }
+    const int rows = kv ? total_k : total_q, heads = kv ? Hkv : Hq;
+    if (!in[i]) return fail(ATTN_ERR_NULLPTR, "%s's strides must not be NULL", names[i]);
+    fix_strides(in[i], rows, heads, d, &out[i][2], &out[i][1]);
+    const int64_t used[2] = {out[i][2], out[i][1]};
+    if ((st = check_strides(used, names[i], false)) != ATTN_OK) return st;
+    out[i][0] = 8;  // one batch
+  }
+  g.q_rows = total_q;
+  g.k_rows = total_k;
+  g.map_b = 1;
+  g.grid_q = max_seqlen_q;
+  g.cu_q = cu_seqlens_q;
+  g.cu_k = cu_seqlens_k;
+  int dev;
+  uint32_t* status = nullptr;
+  if ((st = get_device(&dev)) != ATTN_OK || (st = setup(dev, &status)) != ATTN_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return d == 128 ? launch_prompt<128>(Q, K, V, O, LSE, B, Hq, Hkv, max_seqlen_q, scale, causal, s, dev, status, g)
+                  : launch_prompt<64>(Q, K, V, O, LSE, B, Hq, Hkv, max_seqlen_q, scale, causal, s, dev, status, g);
+}
+
+attn_status attn_cache_weigh(const void* Q, const float* LSE, const attn_cache* cache, const float* weights, float* out,
+                             const int32_t* block_table, int max_pages, const int32_t* cu_seqlens_q,
+                             const int32_t* ctx_lens, int B, int Hq, int total_q, float scale, float decay,
+                             void* stream) {
+  g_err[0] = '\0';
+  attn_status st = check_cache(cache, max_pages, false);
+  if (st != ATTN_OK) return st;
+  if (B < 0 || Hq < 0 || total_q < 0)
+    return fail(ATTN_ERR_BAD_SHAPE, "negative size (B=%d Hq=%d total_q=%d)", B, Hq, total_q);
+  if (Hq > kMaxHeads) return fail(ATTN_ERR_BAD_SHAPE, "Hq=%d; at most %d", Hq, kMaxHeads);
+  if (Hq % cache->num_heads != 0)
+    return fail(ATTN_ERR_BAD_SHAPE, "Hq=%d must be a multiple of the cache's %d heads", Hq, cache->num_heads);
+  if (!std::isfinite(scale) || !(scale > 0.f)) return fail(ATTN_ERR_BAD_ARG, "scale must be finite and > 0");
+  if (!std::isfinite(decay)) return fail(ATTN_ERR_BAD_ARG, "decay must be finite");
+  if (B == 0 || Hq == 0 || total_q == 0) return ATTN_OK;
+  if (!Q || !LSE || !out) return fail(ATTN_ERR_NULLPTR, "Q, LSE and out must not be NULL");
+  if (decay != 0.f && !weights) return fail(ATTN_ERR_NULLPTR, "weights must not be NULL unless decay is 0");
+  if ((st = check_table(block_table, max_pages, cu_seqlens_q, ctx_lens)) != ATTN_OK) return st;
+  if (odd16(Q)) return fail(ATTN_ERR_MISALIGNED, "Q must be 16-byte aligned");
+  if (odd_to(LSE, 4) || odd_to(weights, 4) || odd_to(out, 4))
+    return fail(ATTN_ERR_MISALIGNED, "LSE, weights and out must be 4-byte aligned");
+  attn::WeighParams p = {};
+  int dev;
+  uint32_t* status;
+  if ((st = cache_device(&dev, &status, &p.page_word)) != ATTN_OK) return st;
+  p.q = static_cast<const __nv_bfloat16*>(Q);
+  p.lse = LSE;
+  p.k = cache->k;
+  p.ks = cache->k_scale;
+  p.w = weights;
+  p.out = out;
+  p.table = block_table;
+  p.cu = cu_seqlens_q;
+  p.ctx = ctx_lens;
+  p.B = B;
+  p.Hq = Hq;
+  p.Hkv = cache->num_heads;
+  p.G = Hq / cache->num_heads;
+  p.total_q = total_q;
+  p.num_pages = cache->num_pages;
+  p.page = cache->page_size;
+  p.max_pages = max_pages;
+  p.cap = max_pages * cache->page_size;
+  p.c = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+  p.decay = decay;
+  const bool f8 = cache->type == ATTN_CACHE_E4M3;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (cache->d == 128) return f8 ? launch_weigh<128, true>(p, dev, s) : launch_weigh<128, false>(p, dev, s);
+  return f8 ? launch_weigh<64, true>(p, dev, s) : launch_weigh<64, false>(p, dev, s);
+}
+
+attn_status attn_cache_evict(const attn_cache* cache, float* weights, const int32_t* block_table, int max_pages,
+                             const int32_t* out_table, int out_max_pages, const int32_t* lens, int32_t* kept,
+                             int32_t* out_lens, int B, int keep, int sink, int recent, void* stream) {
+  g_err[0] = '\0';
+  attn_status st = check_cache(cache, max_pages);
+  if (st != ATTN_OK) return st;
+  const bool in_place = !out_table || out_table == block_table;
+  if (B < 0 || keep < 0 || sink < 0 || recent < 0 || static_cast<long long>(sink) + recent > keep)
+    return fail(ATTN_ERR_BAD_SHAPE, "B=%d keep=%d sink=%d recent=%d; none negative, sink + recent at most keep", B, keep,
+                sink, recent);
+  const long long room = static_cast<long long>(max_pages) * cache->page_size;
+  if (!in_place) {
+    if (out_max_pages < 0 || static_cast<long long>(out_max_pages) * cache->page_size > INT32_MAX - 255)
+      return fail(ATTN_ERR_BAD_SHAPE, "out_max_pages=%d: a sequence has at most 2^31 - 256 positions", out_max_pages);
+    if (static_cast<long long>(out_max_pages) * cache->page_size < std::min<long long>(keep, room))
+      return fail(ATTN_ERR_BAD_SHAPE, "out_table has room for %lld positions of %lld kept",
+                  static_cast<long long>(out_max_pages) * cache->page_size, std::min<long long>(keep, room));
+  } else if (out_table && out_max_pages != max_pages) {
+    return fail(ATTN_ERR_BAD_SHAPE, "out_table is block_table: out_max_pages=%d must be max_pages=%d", out_max_pages, max_pages);
+  }
+  if (B == 0) return ATTN_OK;
+  if (!lens || !out_lens || (keep > 0 && !kept)) return fail(ATTN_ERR_NULLPTR, "lens, kept and out_lens must not be NULL");
+  if (lens == out_lens) return fail(ATTN_ERR_BAD_ARG, "out_lens must not be lens");
+  if (max_pages > 0 && !block_table) return fail(ATTN_ERR_NULLPTR, "block_table must not be NULL");
+  if (cache->num_pages > 0 && !weights) return fail(ATTN_ERR_NULLPTR, "weights must not be NULL");
+  if (odd_to(weights, 4) || odd_to(block_table, 4) || odd_to(out_table, 4) || odd_to(lens, 4) || odd_to(kept, 4) ||
+      odd_to(out_lens, 4))
+    return fail(ATTN_ERR_MISALIGNED, "weights, tables, lens, kept and out_lens must be 4-byte aligned");
+  attn::EvictParams p = {};
+  int dev;
+  uint32_t* status;
+  if ((st = cache_device(&dev, &status, &p.page_word)) != ATTN_OK) return st;
+  p.k = static_cast<uint8_t*>(cache->k);
+  p.v = static_cast<uint8_t*>(cache->v);
+  p.ks = cache->type == ATTN_CACHE_E4M3 ? cache->k_scale : nullptr;
+  p.vs = cache->type == ATTN_CACHE_E4M3 ? cache->v_scale : nullptr;
+  p.w = weights;
+  p.table = block_table;
+  p.to = in_place ? block_table : out_table;
+  p.lens = lens;
+  p.kept = kept;
+  p.out_lens = out_lens;
+  p.B = B;
+  p.Hkv = cache->num_heads;
+  p.num_pages = cache->num_pages;
+  p.page = cache->page_size;
+  p.max_pages = max_pages;
+  p.to_pages = in_place ? max_pages : out_max_pages;
+  p.keep = keep;
+  p.sink = sink;
+  p.recent = recent;
+  p.row_bytes = cache->d * (cache->type == ATTN_CACHE_E4M3 ? 1 : 2);
+  p.in_place = in_place ? 1 : 0;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  // A unit's weights are shared by as many CTAs as hold 8192 of them each, 8 at most.
+  unsigned cluster = 1;
+  while (cluster < 8 && room > 8192ll * cluster) cluster *= 2;
+  const long long units = static_cast<long long>(B) * p.Hkv;
+  p.key_cap = static_cast<int>(std::min<long long>((room + cluster - 1) / cluster, attn::kEvictMaxKeys));
+  static bool attr_set[kMaxDevices] = {};
+  if ((st = set_smem_attr(attn::attn_evict_select_kernel, attn::kEvictMaxKeys * 4, dev, attr_set)) != ATTN_OK) return st;
+  // Packing: in place a block walks all rows of some columns; else rows in runs of 256.
+  int slices = 1;
+  const long long most = std::min<long long>(keep, room);
+  p.rows_per_block = 256;
+  if (in_place) {
+    while (slices * 32 < p.row_bytes && 2 * units * slices < 2 * sm_count(dev)) slices *= 2;
+    p.rows_per_block = INT32_MAX;
+  }
+  p.slice = p.row_bytes / slices;
+  const long long blocks = in_place ? slices : (most + p.rows_per_block - 1) / p.rows_per_block;
+  if (units * cluster > INT32_MAX || units * (2 * blocks + 1) > INT32_MAX)
+    return fail(ATTN_ERR_BAD_SHAPE, "too many (sequence, head) units (%lld)", units);
+  cudaError_t e = launch_pdl_cluster(attn::attn_evict_select_kernel, static_cast<unsigned>(units * cluster), cluster,
+                                     attn::kEvictThreads, static_cast<size_t>(p.key_cap) * 4, s, p);
+  if (e == cudaSuccess && keep > 0)
+    e = launch_pdl(attn::attn_evict_move_kernel, static_cast<unsigned>(units * (2 * blocks + 1)), attn::kMoveThreads, 0,
+                   s, p, static_cast<int>(blocks));
+  if (e != cudaSuccess) return fail(ATTN_ERR_LAUNCH, "evict kernel launch: %s", cudaGetErrorString(e));
+  return ATTN_OK;
+}
+
+}  // extern "C"

@@ -270,11 +270,6 @@ __device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t codes) {
   return pack_bf16x2(f.x, f.y);
 }
 
-// Whether either bf16 of a pair is infinite or NaN.
-__device__ __forceinline__ bool any_nonfinite(uint32_t w) {
-  return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
-}
-
 constexpr int kTreeRows = 16;
 constexpr int kTreeWarps = 4;
 constexpr int kTreeThreads = 32 * kTreeWarps;

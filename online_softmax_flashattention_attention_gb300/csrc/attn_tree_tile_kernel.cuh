@@ -136,13 +136,6 @@ __device__ __forceinline__ void mma_ss_f8(uint32_t d_tmem, uint64_t a_desc, uint
       : "memory");
 }
 
-// A bf16 pair with its infinite and NaN halves zeroed.
-__device__ __forceinline__ uint32_t finite_only(uint32_t w) {
-  if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
-  if ((w & 0x7f800000u) == 0x7f800000u) w &= 0x0000ffffu;
-  return w;
-}
-
 // Eight e4m3 codes times the scale (a bf16 pair of it) as four bf16 pairs, exact.
 __device__ __forceinline__ uint4 widen8(uint32_t lo, uint32_t hi, __nv_bfloat162 scale) {
   uint4 r;
