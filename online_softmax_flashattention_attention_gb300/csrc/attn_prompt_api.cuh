@@ -78,10 +78,39 @@ attn_status launch_prompt(const void* Q, const void* K, const void* V, void* O, 
   return ATTN_OK;
 }
 
+// Q as (d, heads, tokens): a box holds `tokens` tokens of `heads` heads.
+attn_status weigh_q_map(CUtensorMap* map, const void* Q, int d, int Hq, int total, int heads, int tokens) {
+  const cuuint64_t row = static_cast<cuuint64_t>(d) * 2;
+  cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(Hq), static_cast<cuuint64_t>(total), 1};
+  cuuint64_t strides[3] = {row, row * Hq, row * Hq * total};
+  cuuint32_t box[4] = {64, static_cast<cuuint32_t>(heads), static_cast<cuuint32_t>(tokens), 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(Q), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(ATTN_ERR_LAUNCH, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
+  return ATTN_OK;
+}
+
 template <int D, bool kF8>
-attn_status launch_weigh(const attn::WeighParams& p, int dev, cudaStream_t stream) {
-  cudaError_t e = launch_pdl(attn::attn_weigh_kernel<D, kF8>, static_cast<unsigned>(4 * sm_count(dev)),
-                             attn::kWeighThreads, 0, stream, p);
+attn_status launch_weigh(const void* Q, int Hq, const attn_cache* c, attn::WeighParams p, int dev, cudaStream_t stream) {
+  static bool attr_set[kMaxDevices] = {};
+  using C = attn::WeighCfg<D, kF8>;
+  auto kernel = attn::attn_weigh_kernel<D, kF8>;
+  attn_status st;
+  if ((st = set_smem_attr(kernel, C::kSmem, dev, attr_set)) != ATTN_OK) return st;
+  p.heads = std::min(p.G, attn::kWeighCols);
+  p.tokens = attn::kWeighCols / p.heads;
+  // a small copy of Q: whole groups of 8 rows (of the swizzle), if two and more of them make a tile
+  p.small_tokens = p.heads % 8 == 0 ? 1 : p.heads % 4 == 0 ? 2 : p.heads % 2 == 0 ? 4 : 8;
+  if (2 * p.small_tokens > p.tokens) p.small_tokens = p.tokens;
+  p.box_rows = 128;  // the most keys that no page border cuts
+  while (p.page % p.box_rows != 0) p.box_rows /= 2;
+  CUtensorMap mq, ms, mk = {};
+  if ((st = weigh_q_map(&mq, Q, D, Hq, p.total_q, p.heads, p.tokens)) != ATTN_OK) return st;
+  if ((st = weigh_q_map(&ms, Q, D, Hq, p.total_q, p.heads, p.small_tokens)) != ATTN_OK) return st;
+  if (c->num_pages > 0 && (st = cache_map(&mk, c->k, c, p.box_rows)) != ATTN_OK) return st;
+  cudaError_t e = launch_pdl(kernel, static_cast<unsigned>(sm_count(dev)), C::kThreads, C::kSmem, stream, mq, ms, mk, p);
   if (e != cudaSuccess) return fail(ATTN_ERR_LAUNCH, "weigh kernel launch: %s", cudaGetErrorString(e));
   return ATTN_OK;
 }
@@ -243,13 +272,14 @@ attn_status attn_cache_weigh(const void* Q, const float* LSE, const attn_cache* 
   if (odd16(Q)) return fail(ATTN_ERR_MISALIGNED, "Q must be 16-byte aligned");
   if (odd_to(LSE, 4) || odd_to(weights, 4) || odd_to(out, 4))
     return fail(ATTN_ERR_MISALIGNED, "LSE, weights and out must be 4-byte aligned");
+  // tiles of query rows are counted in 32 bits
+  const int G = Hq / cache->num_heads;
+  if (static_cast<long long>(total_q) * ((G + attn::kWeighCols - 1) / attn::kWeighCols) > INT32_MAX - 255)
+    return fail(ATTN_ERR_BAD_SHAPE, "total_q=%d is too large for %d heads a group", total_q, G);
   attn::WeighParams p = {};
   int dev;
-  uint32_t* status;
-  if ((st = cache_device(&dev, &status, &p.page_word)) != ATTN_OK) return st;
-  p.q = static_cast<const __nv_bfloat16*>(Q);
+  if ((st = cache_device(&dev, &p.status, &p.page_word)) != ATTN_OK) return st;
   p.lse = LSE;
-  p.k = cache->k;
   p.ks = cache->k_scale;
   p.w = weights;
   p.out = out;
@@ -257,9 +287,8 @@ attn_status attn_cache_weigh(const void* Q, const float* LSE, const attn_cache* 
   p.cu = cu_seqlens_q;
   p.ctx = ctx_lens;
   p.B = B;
-  p.Hq = Hq;
   p.Hkv = cache->num_heads;
-  p.G = Hq / cache->num_heads;
+  p.G = G;
   p.total_q = total_q;
   p.num_pages = cache->num_pages;
   p.page = cache->page_size;
@@ -267,10 +296,12 @@ attn_status attn_cache_weigh(const void* Q, const float* LSE, const attn_cache* 
   p.cap = max_pages * cache->page_size;
   p.c = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
   p.decay = decay;
+  p.timeout_ns = wait_limit_ns();
   const bool f8 = cache->type == ATTN_CACHE_E4M3;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (cache->d == 128) return f8 ? launch_weigh<128, true>(p, dev, s) : launch_weigh<128, false>(p, dev, s);
-  return f8 ? launch_weigh<64, true>(p, dev, s) : launch_weigh<64, false>(p, dev, s);
+  if (cache->d == 128)
+    return f8 ? launch_weigh<128, true>(Q, Hq, cache, p, dev, s) : launch_weigh<128, false>(Q, Hq, cache, p, dev, s);
+  return f8 ? launch_weigh<64, true>(Q, Hq, cache, p, dev, s) : launch_weigh<64, false>(Q, Hq, cache, p, dev, s);
 }
 
 attn_status attn_cache_evict(const attn_cache* cache, float* weights, const int32_t* block_table, int max_pages,
