@@ -481,8 +481,9 @@ attn_status attn_fwd_prompt(const void* Q, const void* K, const void* V, void* O
  *         layout (drafts that may be taken back).  Only positions of sequences with tokens in the
  *         call are written, and no page may be theirs twice.  A row that saw nothing (LSE = -inf)
  *         adds nothing.
- *   Each sum is made in one order whatever the batch around it: the same bits every time.
- *   Asynchronous, allocates nothing.
+ *   scale must be at least 2^-100, and |LSE| / scale below 2^127.  Nothing is added atomically: the
+ *   same call gives the same bits.  Asynchronous, allocates nothing; device-side timeouts through
+ *   attn_status_sync or attn_cache_check.
  */
 attn_status attn_cache_weigh(const void* Q, const float* LSE, const attn_cache* cache, const float* weights, float* out,
                              const int32_t* block_table, int max_pages, const int32_t* cu_seqlens_q,

@@ -106,6 +106,11 @@ attn_status launch_weigh(const void* Q, int Hq, const attn_cache* c, attn::Weigh
   if (2 * p.small_tokens > p.tokens) p.small_tokens = p.tokens;
   p.box_rows = 128;  // the most keys that no page border cuts
   while (p.page % p.box_rows != 0) p.box_rows /= 2;
+  // The stages of shared memory go to K or to Q by the tiles of query rows that a sequence has on
+  // average: see WeighCfg.
+  const bool many = static_cast<long long>(p.total_q) * p.G > 4ll * attn::kWeighCols * p.B;
+  p.ring_k = many ? C::kManyK : C::kFewK;
+  p.ring_q = many ? C::kManyQ : C::kFewQ;
   CUtensorMap mq, ms, mk = {};
   if ((st = weigh_q_map(&mq, Q, D, Hq, p.total_q, p.heads, p.tokens)) != ATTN_OK) return st;
   if ((st = weigh_q_map(&ms, Q, D, Hq, p.total_q, p.heads, p.small_tokens)) != ATTN_OK) return st;
@@ -263,7 +268,7 @@ attn_status attn_cache_weigh(const void* Q, const float* LSE, const attn_cache* 
   if (Hq > kMaxHeads) return fail(ATTN_ERR_BAD_SHAPE, "Hq=%d; at most %d", Hq, kMaxHeads);
   if (Hq % cache->num_heads != 0)
     return fail(ATTN_ERR_BAD_SHAPE, "Hq=%d must be a multiple of the cache's %d heads", Hq, cache->num_heads);
-  if (!std::isfinite(scale) || !(scale > 0.f)) return fail(ATTN_ERR_BAD_ARG, "scale must be finite and > 0");
+  if (!std::isfinite(scale) || !(scale >= 0x1p-100f)) return fail(ATTN_ERR_BAD_ARG, "scale must be finite and at least 2^-100");
   if (!std::isfinite(decay)) return fail(ATTN_ERR_BAD_ARG, "decay must be finite");
   if (B == 0 || Hq == 0 || total_q == 0) return ATTN_OK;
   if (!Q || !LSE || !out) return fail(ATTN_ERR_NULLPTR, "Q, LSE and out must not be NULL");
@@ -295,6 +300,7 @@ attn_status attn_cache_weigh(const void* Q, const float* LSE, const attn_cache* 
   p.max_pages = max_pages;
   p.cap = max_pages * cache->page_size;
   p.c = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+  p.rscale = 1.f / scale;
   p.decay = decay;
   p.timeout_ns = wait_limit_ns();
   const bool f8 = cache->type == ATTN_CACHE_E4M3;

@@ -9,18 +9,32 @@
 // Scores are computed with keys as rows, S = K Q^T: 128 keys are the lanes of tensor memory, up to
 // 128 query rows its columns.  A thread then owns a key, and the sum it wants runs along its own
 // lane: no maximum, no exchange between threads, no second product.  A unit is (sequence, K/V head,
-// 128 keys); nobody else touches its keys, so nothing is added atomically.  Its keys are loaded once
-// and stay in shared memory while the queries stream by (a prompt), or the keys stream and the few
-// queries come along (decoding).
+// some blocks of 128 keys); nobody else touches its keys, so nothing is added atomically.  It goes in
+// steps of two blocks and one tile of query rows:
+//   one tile for the sequence's queries (decoding): the tile stays, 2 or 8 blocks of keys pass by;
+//   several (a prompt): two blocks of keys stay, the tiles pass by.  Two, as the tiles come from L2:
+//   with one block the copies alone were 7 TB/s.
 //
-// Units lie rank major, a sequence's tiles of keys by position and a tile's heads together: with
-// many queries the first keys are seen by most, so each sequence's units go from long to short, and
-// the CTAs (one an SM, persistent) take them in a snake.
+// Shared memory's bandwidth is what a prompt is bound by, before exponentials (1130 cycles for 256 x
+// 128 scores) and products (1090): both operands of a product come from there.  So the columns' LSE
+// does not: it enters the product as one more step of 16, K's side 1, 1, 1, 0 ..., Q's side -LSE /
+// scale as three bf16 terms (24 bits), and what a thread reads is ready for exp2.
 //
-// Warps: 0 finds units, looks their pages up (four units at a time, 8 slices of 16 keys each) and loads
-// K; 1 loads Q; 2 issues the products; 4-7 bring the columns' LSE, warp 4 + i for score buffer i;
-// 8-15 are two groups of four that take the tiles in turn, thread r of a group key r; 16-19 (e4m3)
-// widen K to bf16 with its scale, exact, so that the products are the same for both caches.
+// Units lie rank major, a sequence's runs of keys by position and a run's heads together: with many
+// queries the first keys are seen by most, so each sequence's units go from long to short, and the
+// CTAs (one an SM, persistent) take them in a snake.
+//
+// Warps: 0 loads K; 1 loads Q; 2 and 7 issue the products, a block of the step each (a warp beside busy
+// ones gets an instruction every ten cycles or so: one issuer took 3500 cycles a step); 3 and 6 find
+// units and look their pages up in turn (a unit is three dependent global loads away, some 3000
+// cycles); 4 and 5 bring the columns' LSE, of even and odd tiles; 8-23 are four groups of four, two for
+// the blocks of even steps and two for those of odd ones, thread r of a group key r of its block; 24-27
+// (e4m3) convert.
+//
+// e4m3.  A unit with several tiles of queries widens its keys to bf16 with their scales, exact, once.
+// One with a single tile would pay that for every key it sees: there the codes go to the tensor cores
+// as they are and the queries are split into two e4m3 terms, as attn_tree_tile_kernel.cuh describes;
+// the query row's power of two and the key's scale multiply the score afterwards.
 #pragma once
 
 #include <cuda.h>
@@ -33,16 +47,18 @@
 
 namespace attn {
 
-constexpr int kWeighKeys = 128;     // of a unit
+constexpr int kWeighStep = 256;     // keys of a step: two blocks of 128
+constexpr int kWeighSteps = 4;      // steps of a unit with one tile, at most
 constexpr int kWeighCols = 128;     // query rows of a tile, at most
 constexpr int kWeighGroups = 64;    // prefix-sum entries (each over ceil(B / 64) sequences)
-constexpr int kWeighBufs = 4;       // score buffers of tensor memory
-// Units announced in shared memory.  The first warp is at most kRingK + kWide <= 10 units ahead of the
-// products; these are at most three tiles, so three units, ahead of the tile that a summing or LSE warp
-// is at, and such a warp's last tile lies at most four before: 17 units, so that a slot is never
-// overwritten while in use.
-constexpr int kWeighJobs = 32;
-constexpr int kWeighParts = 8;      // sums on their way from one group to the other
+constexpr int kWeighJobs = 6;       // units announced in shared memory
+constexpr int kWeighFinders = 2;
+// e4m3: factors of query rows, unit u % 8, and scale codes of keys, block x % 16.  K is at most kRingK
+// <= 8 blocks ahead of the products and these two steps, four blocks, ahead of the sums.
+constexpr int kWeighFactors = 8;
+constexpr int kWeighCodes = 16;
+constexpr int kWeighParts = 4;      // sums on their way from one pair of groups to the other (three units apart at most)
+constexpr int kWeighSumWarp = 8, kWeighConvWarp = 24;
 
 struct WeighParams {
   const float* lse;          // [Hq, total_q]
@@ -58,7 +74,9 @@ struct WeighParams {
   int heads;                 // heads of the group in a tile of query rows (G, or 128 of more)
   int tokens;                // tokens of a full tile: 128 / heads
   int small_tokens;          // tokens of a small copy of Q (as many as make whole groups of 8 rows)
+  int ring_k, ring_q;        // stages of K's ring and of Q's
   float c;                   // scale * log2(e)
+  float rscale;              // 1 / scale
   float decay;
   uint32_t* status;
   uint32_t* page_word;
@@ -67,7 +85,7 @@ struct WeighParams {
 
 // A sequence, every field clamped to what the buffers hold.
 struct WeighSeq {
-  int q0, T, ctx, n, tiles;
+  int q0, T, ctx, n;
 };
 __device__ __forceinline__ WeighSeq weigh_seq(const WeighParams& p, int b) {
   WeighSeq s;
@@ -75,63 +93,113 @@ __device__ __forceinline__ WeighSeq weigh_seq(const WeighParams& p, int b) {
   s.T = min(max(__ldg(p.cu + b + 1), s.q0), p.total_q) - s.q0;
   s.ctx = p.ctx ? min(max(__ldg(p.ctx + b), 0), p.cap) : 0;
   s.n = static_cast<int>(min(static_cast<long long>(s.ctx) + s.T, static_cast<long long>(p.cap)));
-  s.tiles = s.T > 0 ? s.n / kWeighKeys + (s.n % kWeighKeys != 0) : 0;
   return s;
 }
+// Keys of a sequence's units, when those with one tile have `steps` steps, and their number for a head.
+__device__ __forceinline__ int weigh_unit_keys(const WeighParams& p, const WeighSeq& s, int steps) {
+  return p.heads == p.G && s.T <= p.tokens ? steps * kWeighStep : kWeighStep;
+}
+__device__ __forceinline__ int weigh_units(const WeighParams& p, const WeighSeq& s, int steps) {
+  const int keys = weigh_unit_keys(p, s, steps);
+  return s.T > 0 ? s.n / keys + (s.n % keys != 0) : 0;
+}
 
-// A unit as the first warp announces it.
-struct WeighJob {
+// A unit as its finder announces it.
+struct WeighUnit {
   int q0, T, ctx, n;
-  int h, tile;
-  int first;               // the first token that sees any key of the unit
+  int h, key0;             // its first key
   int nq;                  // tiles of query rows; < 0: the end
-  int pages[8];            // of the unit's slices of 16 keys, -1 without one
+  int steps;               // steps of its one tile (1 with several)
+  __device__ __forceinline__ int first() const { return max(0, key0 - ctx); }  // the first token that sees any of its keys
 };
-static_assert(sizeof(WeighJob) == 64, "four 16-byte words");
+struct WeighJob {
+  WeighUnit unit;
+  long long rows[16 * kWeighSteps];  // of the unit's slices of 16 keys in the pool, -1 without a page
+  int pages[16 * kWeighSteps];
+};
+
+// A place in a ring of stages and the parity of its turn.
+struct WeighRing {
+  int st = 0;
+  uint32_t ph = 0;
+  __device__ __forceinline__ void next(int n) {
+    if (++st == n) {
+      st = 0;
+      ph ^= 1u;
+    }
+  }
+};
 
 // Columns of tile j of a unit: tokens [tok, tok + n) with heads [head, head + p.heads) of the group.
 struct WeighCols {
   int tok, head, n;
 };
-__device__ __forceinline__ WeighCols weigh_cols(const WeighParams& p, const WeighJob& t, int j) {
+__device__ __forceinline__ WeighCols weigh_cols(const WeighParams& p, int first, int T, int j) {
   WeighCols c;
   if (p.heads == p.G) {
-    c.tok = t.first + j * p.tokens;
+    c.tok = first + j * p.tokens;
     c.head = 0;
-    c.n = min(p.tokens, t.T - c.tok) * p.heads;
+    c.n = min(p.tokens, T - c.tok) * p.heads;
   } else {  // more than 128 heads a group: a token, 128 heads at a time
     const int per = (p.G + p.heads - 1) / p.heads;
-    c.tok = t.first + j / per;
+    c.tok = first + j / per;
     c.head = (j % per) * p.heads;
     c.n = min(p.heads, p.G - c.head);
   }
   return c;
 }
 
+// 32 lanes x 8 columns of 32-bit.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+
+// A step of 16 in the product beside K and Q: 128 rows without swizzle, 8 x 16-byte blocks, the two of
+// a row's 32 bytes 128 apart, the next eight rows 256 further.
+constexpr int kWeighStepBytes = 128 * 32;
+__device__ __forceinline__ uint32_t weigh_step_row(int r) { return (r >> 3) * 256 + (r & 7) * 16; }
+__device__ __forceinline__ uint64_t weigh_step_desc(uint32_t saddr) {
+  return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(128 >> 4) << 16) |
+         (static_cast<uint64_t>(256 >> 4) << 32) | (static_cast<uint64_t>(1) << 46);
+}
+
 template <int D, bool kF8>
 struct WeighCfg {
-  static constexpr int kThreads = kF8 ? 640 : 512;
+  static constexpr int kThreads = 32 * (kWeighConvWarp + (kF8 ? 4 : 0));
   static constexpr int kSub = D / 64;
   static constexpr int kSubBytes = 128 * 128;            // 128 rows x 64 bf16
   static constexpr int kTileBytes = kSub * kSubBytes;    // 128 rows in bf16
-  static constexpr int kStageK = kF8 ? 128 * D : kTileBytes;
-  static constexpr int kRingK = kF8 ? (D == 128 ? 5 : 8) : (D == 128 ? 3 : 6);
-  static constexpr int kWide = kF8 ? 2 : 0;              // widened tiles of keys
-  static constexpr int kRingQ = kF8 ? (D == 128 ? 2 : 4) : (D == 128 ? 3 : 5);
-  static constexpr int kOffQ = 0;
-  static constexpr int kOffK = kOffQ + kRingQ * kTileBytes;
-  static constexpr int kOffWide = kOffK + kRingK * kStageK;
-  static constexpr int kOffCode = kOffWide + kWide * kTileBytes;            // scale codes, 128 a stage
-  static constexpr int kOffLse = kOffCode + (kF8 ? kRingK * 128 : 0);       // 128 floats a score buffer
-  static constexpr int kOffPart = kOffLse + kWeighBufs * 512;               // 128 floats a part
-  static constexpr int kOffJobs = kOffPart + kWeighParts * 512;
-  static constexpr int kOffPre = kOffJobs + kWeighJobs * 64;
-  static constexpr int kOffBar = kOffPre + 8 * (kWeighGroups + 1 + 3);
-  // job[J], {k_full, k_free}[RK], {w_full, w_free}[W], {q_full, q_free}[RQ], {s_full, s_free, lse_full}[4],
-  // part_full[P], drain
-  static constexpr int kNumBars = kWeighJobs + 2 * kRingK + 2 * kWide + 2 * kRingQ + 3 * kWeighBufs + kWeighParts + 1;
+  static constexpr int kStageK = kF8 ? 128 * D : kTileBytes;  // a block of keys
+  static constexpr int kWide = kF8 ? 2 : 0;              // operands in another form than they came
+  // What the rings of K and Q share: (one tile a unit, as in decoding) stages of K for the bytes in
+  // flight, or (several) of Q, whose way from L2 is 2000 to 3000 cycles with all SMs at it.
+  static constexpr int kFewK = D == 128 ? 4 : 8;
+  static constexpr int kFewQ = 2;
+  static constexpr int kManyK = kF8 ? (D == 128 ? 2 : 4) : 2;
+  static constexpr int kManyQ = kF8 ? (D == 128 ? 3 : 4) : (D == 128 ? 4 : 8);
+  static constexpr int kLse = kF8 ? 3 : 4;               // tiles whose LSE is at hand
+  static constexpr int kMaxK = kFewK > kManyK ? kFewK : kManyK, kMaxQ = kManyQ;
+  static constexpr int kPool = kFewK * kStageK + kFewQ * kTileBytes;
+  static_assert(kManyK * kStageK + kManyQ * kTileBytes <= kPool, "both divisions of the stages");
+  static constexpr int kOffWide = kPool;                                    // Q's stages, then K's, before it
+  static constexpr int kOffOnes = kOffWide + kWide * kTileBytes;            // the step of 16: K's side,
+  static constexpr int kOffStep = kOffOnes + kWeighStepBytes;               // Q's, tile by tile
+  static constexpr int kOffCode = kOffStep + kLse * kWeighStepBytes;        // scale codes, 128 a block
+  static constexpr int kOffLse = kOffCode + (kF8 ? kWeighCodes * 128 : 0);  // 128 floats a tile
+  static constexpr int kOffFactor = kOffLse + kLse * 512;                   // 128 floats, unit u % 8
+  static constexpr int kOffPart = kOffFactor + (kF8 ? kWeighFactors * 512 : 0);     // 256 floats, unit u % 4
+  static constexpr int kOffJobs = kOffPart + kWeighParts * 1024;
+  static constexpr int kOffPre = kOffJobs + kWeighJobs * static_cast<int>(sizeof(WeighJob));
+  static constexpr int kOffBar = kOffPre + 8 * (2 * (kWeighGroups + 1) + 2);
+  // {job, job_free}[J], {k_full, k_free}[K], {w_full, w_free}[W], {q_full, q_free}[Q], {s_full, s_free}[4],
+  // part[P][2], lse_free[L][4], lse_full[L], drain[2]
+  static constexpr int kNumBars = 2 * kWeighJobs + 2 * kMaxK + 2 * kWide + 2 * kMaxQ + 8 + 2 * kWeighParts + 5 * kLse + 2;
   static constexpr int kOffMisc = kOffBar + 8 * kNumBars;                   // tmem base, abort, odd[4]
   static constexpr int kSmem = kOffMisc + 24 + 1024;
+  // warps that read a unit: K, Q, products (2), LSE (2), sums (16), conversions (4)
+  static constexpr int kReaders = 22 + (kF8 ? 4 : 0);
   static_assert(kSmem <= 232448, "shared memory per CTA");
 };
 
@@ -140,57 +208,75 @@ __global__ void __launch_bounds__(WeighCfg<D, kF8>::kThreads, 1)
     attn_weigh_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmQs,
                       const __grid_constant__ CUtensorMap tmK, const WeighParams p) {
   using C = WeighCfg<D, kF8>;
-  constexpr int RK = C::kRingK, RQ = C::kRingQ, NW = C::kWide, NWm = NW > 0 ? NW : 1, NB = kWeighBufs;
+  constexpr int MK = C::kMaxK, MQ = C::kMaxQ, NW = C::kWide, NWm = NW > 0 ? NW : 1;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const uint32_t sbase = smem_u32(smem), sQ = sbase + C::kOffQ, sK = sbase + C::kOffK, bar0 = sbase + C::kOffBar;
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);  // (an offset: it stays a shared address)
+  const uint32_t sbase = smem_u32(smem), sQ = sbase, sK = sbase + p.ring_q * C::kTileBytes, bar0 = sbase + C::kOffBar;
   auto bar_job = [&](int i) { return bar0 + 8u * i; };
-  auto bar_k_full = [&](int s) { return bar0 + 8u * (kWeighJobs + s); };
-  auto bar_k_free = [&](int s) { return bar0 + 8u * (kWeighJobs + RK + s); };
-  constexpr int kB1 = kWeighJobs + 2 * RK;
+  auto bar_job_free = [&](int i) { return bar0 + 8u * (kWeighJobs + i); };
+  constexpr int kB0 = 2 * kWeighJobs;
+  auto bar_k_full = [&](int s) { return bar0 + 8u * (kB0 + s); };
+  auto bar_k_free = [&](int s) { return bar0 + 8u * (kB0 + MK + s); };
+  constexpr int kB1 = kB0 + 2 * MK;
   auto bar_w_full = [&](int s) { return bar0 + 8u * (kB1 + s); };
   auto bar_w_free = [&](int s) { return bar0 + 8u * (kB1 + NW + s); };
   constexpr int kB2 = kB1 + 2 * NW;
   auto bar_q_full = [&](int s) { return bar0 + 8u * (kB2 + s); };
-  auto bar_q_free = [&](int s) { return bar0 + 8u * (kB2 + RQ + s); };
-  constexpr int kB3 = kB2 + 2 * RQ;
+  auto bar_q_free = [&](int s) { return bar0 + 8u * (kB2 + MQ + s); };
+  constexpr int kB3 = kB2 + 2 * MQ;
+  // score buffers: block h of step g in buffer 2 (g % 2) + h
   auto bar_s_full = [&](int b) { return bar0 + 8u * (kB3 + b); };
-  auto bar_s_free = [&](int b) { return bar0 + 8u * (kB3 + NB + b); };
-  auto bar_lse = [&](int b) { return bar0 + 8u * (kB3 + 2 * NB + b); };
-  auto bar_part = [&](int i) { return bar0 + 8u * (kB3 + 3 * NB + i); };
-  const uint32_t bar_drain = bar0 + 8u * (kB3 + 3 * NB + kWeighParts);
+  auto bar_s_free = [&](int b) { return bar0 + 8u * (kB3 + 4 + b); };
+  // A barrier for each group of four warps, not one for several: a group's warps are never two of its
+  // steps apart, as they share a score buffer, while the blocks' groups may be a ring's length apart.
+  auto bar_part = [&](int i, int blk) { return bar0 + 8u * (kB3 + 8 + 2 * i + blk); };
+  auto bar_lse_free = [&](int i, int grp) { return bar0 + 8u * (kB3 + 8 + 2 * kWeighParts + 4 * i + grp); };
+  auto bar_lse_full = [&](int i) { return bar0 + 8u * (kB3 + 8 + 2 * kWeighParts + 4 * C::kLse + i); };
+  auto bar_drain = [&](int h) { return bar0 + 8u * (kB3 + 8 + 2 * kWeighParts + 5 * C::kLse + h); };
   long long* pre = reinterpret_cast<long long*>(smem + C::kOffPre);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + C::kOffMisc + 4);
-  // odd[b]: a column of score buffer b adds nothing whatever its scores are
+  // odd[i]: a column of the tile at place i adds nothing whatever its scores are
   volatile uint32_t* odd = reinterpret_cast<volatile uint32_t*>(smem + C::kOffMisc + 8);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const WaitCtx wc{abort_flag, p.status, p.timeout_ns};
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kWeighJobs; ++i) mbar_init(bar_job(i), 1);
-    for (int s = 0; s < RK; ++s) {
+    for (int i = 0; i < kWeighJobs; ++i) {
+      mbar_init(bar_job(i), 1);
+      mbar_init(bar_job_free(i), C::kReaders);
+    }
+    for (int s = 0; s < MK; ++s) {
       mbar_init(bar_k_full(s), 1);
-      mbar_init(bar_k_free(s), kF8 ? 4 : 1);
+      mbar_init(bar_k_free(s), 1);
     }
     for (int s = 0; s < NW; ++s) {
       mbar_init(bar_w_full(s), 4);
-      mbar_init(bar_w_free(s), 1);
+      mbar_init(bar_w_free(s), 2);
     }
-    for (int s = 0; s < RQ; ++s) {
-      mbar_init(bar_q_full(s), 1);
-      mbar_init(bar_q_free(s), 1);
+    for (int s = 0; s < MQ; ++s) {
+      mbar_init(bar_q_full(s), 2);  // its rows and their LSE
+      mbar_init(bar_q_free(s), 2);
     }
-    for (int b = 0; b < NB; ++b) {
+    for (int b = 0; b < 4; ++b) {
       mbar_init(bar_s_full(b), 1);
       mbar_init(bar_s_free(b), 4);
-      mbar_init(bar_lse(b), 1);
     }
-    for (int i = 0; i < kWeighParts; ++i) mbar_init(bar_part(i), 4);
-    mbar_init(bar_drain, 1);
+    for (int i = 0; i < 2 * kWeighParts; ++i) mbar_init(bar_part(0, i), 4);
+    for (int i = 0; i < 4 * C::kLse; ++i) mbar_init(bar_lse_free(0, i), 4);
+    for (int i = 0; i < C::kLse; ++i) mbar_init(bar_lse_full(i), 1);
+    mbar_init(bar_drain(0), 1);
+    mbar_init(bar_drain(1), 1);
     *abort_flag = 0u;
     fence_mbar_init();
   }
+  // the step of 16: K's side 1, 1, 1, 0 ..., Q's second half zeros (the first comes with the LSE)
+  for (int r = threadIdx.x; r < (1 + C::kLse) * 128; r += C::kThreads) {
+    uint4* row = reinterpret_cast<uint4*>(smem + C::kOffOnes + (r >> 7) * kWeighStepBytes + weigh_step_row(r & 127));
+    row[0] = r < 128 ? make_uint4(0x3f803f80u, 0x00003f80u, 0u, 0u) : make_uint4(0u, 0u, 0u, 0u);
+    row[8] = make_uint4(0u, 0u, 0u, 0u);
+  }
+  fence_proxy_async_smem();
   if (warp == 2) tmem_alloc<512>(smem_u32(tmem_slot));
   if (warp == 1 && lane == 0) {
     tma_prefetch_desc(&tmQ);
@@ -198,63 +284,82 @@ __global__ void __launch_bounds__(WeighCfg<D, kF8>::kThreads, 1)
     if (p.num_pages > 0) tma_prefetch_desc(&tmK);  // without pages there is no map
   }
   griddep_wait();
-  // units of the sequences before group i (groups of gs sequences)
+  // pre[0 / 1][i]: units of the sequences before group i (groups of gs sequences) with 1 or kWeighSteps
+  // steps where there is one tile.  The longer ones cost less a key and are taken when they still go
+  // round the CTAs four times.
   const int gs = (p.B + kWeighGroups - 1) / kWeighGroups;
   {
-    long long* warp_sums = pre + kWeighGroups + 1;
-    long long sum = 0;
+    long long* warp_sums = pre + 2 * (kWeighGroups + 1);
+    long long sum[2] = {0, 0};
     if (threadIdx.x < kWeighGroups) {
       const long long first = static_cast<long long>(threadIdx.x) * gs;
       for (long long b = first; b < min(first + gs, static_cast<long long>(p.B)); ++b) {
         const WeighSeq s = weigh_seq(p, static_cast<int>(b));
-        sum += static_cast<long long>(s.tiles) * p.Hkv;
+        sum[0] += static_cast<long long>(weigh_units(p, s, 1)) * p.Hkv;
+        sum[1] += static_cast<long long>(weigh_units(p, s, kWeighSteps)) * p.Hkv;
         if (blockIdx.x == 0 && s.T > 0 && p.page_word && static_cast<long long>(s.ctx) + s.T > p.cap) atomicOr(p.page_word, 1u);
       }
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long v = __shfl_up_sync(0xffffffffu, sum, o);
-        if (lane >= o) sum += v;
+      for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const long long v = __shfl_up_sync(0xffffffffu, sum[i], o);
+          if (lane >= o) sum[i] += v;
+        }
+      if (threadIdx.x == 31) {
+        warp_sums[0] = sum[0];
+        warp_sums[1] = sum[1];
       }
-      if (lane == 31) warp_sums[warp] = sum;
     }
     tc_fence_before();
     __syncthreads();
     if (threadIdx.x < kWeighGroups) {
-      if (warp == 1) sum += warp_sums[0];
-      pre[threadIdx.x + 1] = sum;
-      if (threadIdx.x == 0) pre[0] = 0;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        pre[i * (kWeighGroups + 1) + threadIdx.x + 1] = sum[i] + (warp == 1 ? warp_sums[i] : 0);
+        if (threadIdx.x == 0) pre[i * (kWeighGroups + 1)] = 0;
+      }
     }
     __syncthreads();
     tc_fence_after();
   }
+  const bool longer = pre[2 * kWeighGroups + 1] >= 4ll * gridDim.x;
+  if (longer) pre += kWeighGroups + 1;
   // not before this CTA has its tensor memory: a later launch that got there first would hold it
   griddep_launch_dependents();
   const uint32_t tmem = *tmem_slot;
-  auto job_at = [&](int u) { return reinterpret_cast<WeighJob*>(smem + C::kOffJobs + (u % kWeighJobs) * 64); };
-  // Unit u, for a whole warp (one that gives up gives up with all its lanes); false at the end of the
-  // list, or (ok = false too) when the wait ran out.
-  auto job = [&](int u, WeighJob& t, bool& ok, uint32_t site) {
-    ok = __all_sync(0xffffffffu, tile_wait(bar_job(u % kWeighJobs), (u / kWeighJobs) & 1, wc, site));
+  WeighJob* jobs = reinterpret_cast<WeighJob*>(smem + C::kOffJobs);
+  // The next unit, for a whole warp (one that gives up gives up with all its lanes); false at the end of
+  // the list, or (ok = false too) when the wait ran out.  rows: what of the slot the warp reads besides.
+  WeighRing jr;
+  auto job_more = [&](WeighUnit& t, bool& ok, uint32_t site, auto rows) {
+    ok = __all_sync(0xffffffffu, tile_wait(bar_job(jr.st), jr.ph, wc, site));
     if (!ok) return false;
-    t = *job_at(u);
+    const int4* at = reinterpret_cast<const int4*>(jobs + jr.st);
+    const int4 a = at[0], b = at[1];
+    t = WeighUnit{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    rows(jobs[jr.st], t);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar_job_free(jr.st));
+    jr.next(kWeighJobs);
     return t.nq >= 0;
   };
+  auto job = [&](WeighUnit& t, bool& ok, uint32_t site) { return job_more(t, ok, site, [](const WeighJob&, const WeighUnit&) {}); };
 
-  if (warp == 0) {
-    // ================================================================ units, K
-    const uint64_t pol = policy_evict_first();
+  if (warp == 3 || warp == 6) {
+    // ================================================================ units
     const long long U = pre[kWeighGroups];
-    const int box16 = p.box_rows / 16;
-    int u = 0;
-    uint32_t live = 0, par = 0;
+    const int steps = longer ? kWeighSteps : 1;
+    auto unit_of = [&](long long r) { return r * gridDim.x + ((r & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x); };
+    WeighRing slot;
+    if (warp == 6) slot.next(kWeighJobs);
     bool ok = true;
-    for (long long r0 = 0; ok; r0 += 4) {
-      // lane 8 i + s: unit r0 + i of this CTA, slice s
-      const long long r = r0 + lane / 8;
-      const long long unit = r * gridDim.x + ((r & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-      WeighJob t = {};
-      int page = -1, row = 0;
-      bool need = false;
+    for (long long r = warp == 3 ? 0 : 1; r == 0 || unit_of(r - 1) < U; r += kWeighFinders) {  // the end is announced once
+      const long long unit = unit_of(r);
+      WeighUnit t = {};
+      t.nq = -1;
+      long long rows[2] = {-1, -1};
+      int pages[2] = {-1, -1};
       if (unit < U) {
         int lo = 0, hi = kWeighGroups;  // pre[lo] <= unit < pre[hi]
         while (hi - lo > 1) {
@@ -267,166 +372,249 @@ __global__ void __launch_bounds__(WeighCfg<D, kF8>::kThreads, 1)
         long long y = unit - pre[lo];
         int b = lo * gs;
         WeighSeq s = weigh_seq(p, b);
-        while (y >= static_cast<long long>(s.tiles) * p.Hkv && b + 1 < p.B) {
-          y -= static_cast<long long>(s.tiles) * p.Hkv;
+        for (;;) {
+          const long long n = static_cast<long long>(weigh_units(p, s, steps)) * p.Hkv;
+          if (y < n || b + 1 >= p.B) break;
+          y -= n;
           s = weigh_seq(p, ++b);
         }
+        const int keys = weigh_unit_keys(p, s, steps), run = static_cast<int>(tree_div(y, p.Hkv));
         t.q0 = s.q0;
         t.T = s.T;
         t.ctx = s.ctx;
         t.n = s.n;
-        t.tile = static_cast<int>(y / p.Hkv);
-        t.h = static_cast<int>(y - static_cast<long long>(t.tile) * p.Hkv);
-        t.first = max(0, t.tile * kWeighKeys - s.ctx);
-        t.nq = p.heads == p.G ? (s.T - t.first + p.tokens - 1) / p.tokens : (s.T - t.first) * ((p.G + p.heads - 1) / p.heads);
-        const int pos = t.tile * kWeighKeys + 16 * (lane & 7);
-        need = pos < s.n;
-        if (need) {
-          const int slot = static_cast<uint32_t>(pos) / static_cast<uint32_t>(p.page);
-          page = __ldg(p.table + static_cast<long long>(b) * p.max_pages + slot);
-          row = pos - slot * p.page;
+        t.h = static_cast<int>(y - static_cast<long long>(run) * p.Hkv);
+        t.key0 = run * keys;
+        const int first = t.first();
+        t.nq = p.heads == p.G ? (s.T - first + p.tokens - 1) / p.tokens : (s.T - first) * ((p.G + p.heads - 1) / p.heads);
+        t.steps = (min(keys, s.n - t.key0) + kWeighStep - 1) / kWeighStep;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {  // lane i: slices i and i + 32
+          const int pos = min(t.key0 + 16 * (lane + 32 * i), s.n - 1);
+          const int in = static_cast<uint32_t>(pos) / static_cast<uint32_t>(p.page);
+          pages[i] = __ldg(p.table + static_cast<long long>(b) * p.max_pages + in);
+          rows[i] = pos - in * p.page;
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const bool need = 16 * (lane + 32 * i) < min(keys, s.n - t.key0);
+          const bool have = need && static_cast<unsigned>(pages[i]) < static_cast<unsigned>(p.num_pages);
+          if (need && !have && p.page_word) atomicOr(p.page_word, 1u);
+          rows[i] = have ? (static_cast<long long>(pages[i]) * p.Hkv + t.h) * p.page + rows[i] : -1;
         }
       }
-      const bool have = static_cast<unsigned>(page) < static_cast<unsigned>(p.num_pages);
-      if (need && !have && p.page_word) atomicOr(p.page_word, 1u);
-      const bool mine = have && (lane & 7) % box16 == 0;
-      const uint32_t boxes = __ballot_sync(0xffffffffu, mine);
-      const uint32_t units = __ballot_sync(0xffffffffu, unit < U && (lane & 7) == 0);
+      ok = __all_sync(0xffffffffu, tile_wait(bar_job_free(slot.st), slot.ph ^ 1u, wc, 60));
+      if (!ok) break;
+      WeighJob& at = jobs[slot.st];
+      if (lane == 0) {
+        reinterpret_cast<int4*>(&at)[0] = make_int4(t.q0, t.T, t.ctx, t.n);
+        reinterpret_cast<int4*>(&at)[1] = make_int4(t.h, t.key0, t.nq, t.steps);
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        at.rows[lane + 32 * i] = rows[i];
+        at.pages[lane + 32 * i] = pages[i];
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_job(slot.st));
+      for (int i = 0; i < kWeighFinders; ++i) slot.next(kWeighJobs);
+    }
+  } else if (warp == 0) {
+    // ================================================================ K
+    const uint64_t pol = policy_evict_first();
+    const int box16 = p.box_rows / 16;
+    WeighRing k;
+    uint32_t live = 0, par = 0, x = 0;  // x: blocks
+    bool ok = true;
+    WeighUnit t;
+    long long row[2] = {-1, -1};
+    int page[2] = {-1, -1};
+    while (job_more(t, ok, 61, [&](const WeighJob& at, const WeighUnit&) {  // lane i: slices i and i + 32
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        row[i] = at.rows[lane + 32 * i];
+        page[i] = at.pages[lane + 32 * i];
+      }
+    })) {
+      // (a row lies in its page's at row - (page * Hkv + h) * page_size)
 #pragma unroll 1
-      for (int i = 0; i < 4; ++i) {
-        if (!((units >> (8 * i)) & 1u)) break;
-        // the slot's last unit is done with: see kWeighJobs
-        if (u >= RK) ok = __all_sync(0xffffffffu, tile_wait(bar_k_free(u % RK), ((u - RK) / RK) & 1, wc, 60));
+      for (int blk = 0; blk < 2 * t.steps; ++blk, ++x, k.next(p.ring_k)) {  // a block without keys is a block of anything
+        const long long rw = blk < 4 ? row[0] : row[1];
+        const int pg = blk < 4 ? page[0] : page[1];
+        const bool mine = lane / 8 == (blk & 3) && rw >= 0 && (lane & 7) % box16 == 0;
+        const int boxes = __popc(__ballot_sync(0xffffffffu, mine));
+        ok = __all_sync(0xffffffffu, tile_wait(bar_k_free(k.st), k.ph ^ 1u, wc, 62));
         if (!ok) break;
-        if (lane == 8 * i) {
-          WeighJob* at = job_at(u);
-          at->q0 = t.q0;
-          at->T = t.T;
-          at->ctx = t.ctx;
-          at->n = t.n;
-          at->h = t.h;
-          at->tile = t.tile;
-          at->first = t.first;
-          at->nq = t.nq;
-        }
-        if (lane / 8 == i) job_at(u)->pages[lane & 7] = have ? page : -1;
-        __syncwarp();
-        const int st = u % RK;
         constexpr int kRowB = kF8 ? D : 128;
         constexpr int kSubs = kF8 ? 1 : C::kSub;
-        if (lane == 0) {
-          mbar_arrive(bar_job(u % kWeighJobs));
-          mbar_arrive_expect_tx(bar_k_full(st), __popc((boxes >> (8 * i)) & 0xffu) * p.box_rows * (kSubs * kRowB + (kF8 ? 1 : 0)));
-        }
+        if (lane == 0) mbar_arrive_expect_tx(bar_k_full(k.st), boxes * p.box_rows * (kSubs * kRowB + (kF8 ? 1 : 0)));
         __syncwarp();
-        if (mine && lane / 8 == i) {
-          const uint32_t dst = sK + st * C::kStageK + 16 * (lane & 7) * kRowB;
+        if (mine) {
+          const uint32_t dst = sK + k.st * C::kStageK + 16 * (lane & 7) * kRowB;
+          const int in_page = static_cast<int>(rw - (static_cast<long long>(pg) * p.Hkv + t.h) * p.page);
 #pragma unroll
-          for (int s = 0; s < kSubs; ++s)
-            tma_load_4d(dst + s * C::kSubBytes, &tmK, bar_k_full(st), s * 64, row, t.h, page, pol);
+          for (int s = 0; s < kSubs; ++s) tma_load_4d(dst + s * C::kSubBytes, &tmK, bar_k_full(k.st), s * 64, in_page, t.h, pg, pol);
           if constexpr (kF8)
-            bulk_load(sbase + C::kOffCode + st * 128 + 16 * (lane & 7),
-                      p.ks + (static_cast<long long>(page) * p.Hkv + t.h) * p.page + row, p.box_rows, bar_k_full(st));
+            bulk_load(sbase + C::kOffCode + (x % kWeighCodes) * 128 + 16 * (lane & 7), p.ks + rw, p.box_rows, bar_k_full(k.st));
         }
-        live |= 1u << st;
-        par = (par & ~(1u << st)) | (((u / RK) & 1u) << st);
-        ++u;
+        live |= 1u << k.st;
+        par = (par & ~(1u << k.st)) | (k.ph << k.st);
       }
-      if (__popc(units) < 4) break;
-    }
-    if (ok) {  // the end of the list: its slot too must be free
-      if (u >= RK) ok = __all_sync(0xffffffffu, tile_wait(bar_k_free(u % RK), ((u - RK) / RK) & 1, wc, 60));
-      if (ok && lane == 0) {
-        job_at(u)->nq = -1;
-        mbar_arrive(bar_job(u % kWeighJobs));
-      }
+      if (!ok) break;
     }
     // let the copies in flight land before this warp leaves
-    if (lane == 0) {
-#pragma unroll
-      for (int s = 0; s < RK; ++s)
+    if (lane == 0)
+      for (int s = 0; s < p.ring_k; ++s)
         if ((live >> s) & 1u) mbar_wait_drain(bar_k_full(s), (par >> s) & 1u, p.timeout_ns);
-    }
   } else if (warp == 1) {
     // ================================================================ Q
     const uint64_t pol = policy_evict_normal();
-    int g = 0;
+    WeighRing q;
     uint32_t live = 0, par = 0;
     bool ok = true;
-    WeighJob t;
-    for (int u = 0; job(u, t, ok, 61); ++u) {
-      for (int j = 0; j < t.nq; ++j, ++g) {
-        const int st = g % RQ;
-        if (g >= RQ) ok = __all_sync(0xffffffffu, tile_wait(bar_q_free(st), ((g - RQ) / RQ) & 1, wc, 62));
+    WeighUnit t;
+    while (job(t, ok, 63)) {
+      const int first = t.first();
+      for (int j = 0; j < t.nq; ++j, q.next(p.ring_q)) {
+        ok = __all_sync(0xffffffffu, tile_wait(bar_q_free(q.st), q.ph ^ 1u, wc, 64));
         if (!ok) break;
-        const WeighCols c = weigh_cols(p, t, j);
+        const WeighCols c = weigh_cols(p, first, t.T, j);
         // few tokens: only as many small copies as hold them
         const int toks = (c.n + p.heads - 1) / p.heads;
         const int small = (toks + p.small_tokens - 1) / p.small_tokens;
         const bool full = 4 * toks > p.tokens || small > 32;
         const int rows = full ? p.tokens * p.heads : p.small_tokens * p.heads;
-        if (lane == 0) mbar_arrive_expect_tx(bar_q_full(st), (full ? 1 : small) * rows * C::kSub * 128);
+        if (lane == 0) mbar_arrive_expect_tx(bar_q_full(q.st), (full ? 1 : small) * rows * C::kSub * 128);
         __syncwarp();
         if (lane < (full ? 1 : small)) {
 #pragma unroll
           for (int s = 0; s < C::kSub; ++s)
-            tma_load_4d(sQ + st * C::kTileBytes + s * C::kSubBytes + lane * rows * 128, full ? &tmQ : &tmQs, bar_q_full(st), s * 64,
+            tma_load_4d(sQ + q.st * C::kTileBytes + s * C::kSubBytes + lane * rows * 128, full ? &tmQ : &tmQs, bar_q_full(q.st), s * 64,
                         t.h * p.G + c.head, t.q0 + c.tok + lane * p.small_tokens, 0, pol);
         }
-        live |= 1u << st;
-        par = (par & ~(1u << st)) | (((g / RQ) & 1u) << st);
+        live |= 1u << q.st;
+        par = (par & ~(1u << q.st)) | (q.ph << q.st);
       }
       if (!ok) break;
     }
-    if (lane == 0) {
-#pragma unroll
-      for (int s = 0; s < RQ; ++s)
+    if (lane == 0)
+      for (int s = 0; s < p.ring_q; ++s)
         if ((live >> s) & 1u) mbar_wait_drain(bar_q_full(s), (par >> s) & 1u, p.timeout_ns);
-    }
-  } else if (warp == 2) {
+  } else if (warp == 2 || warp == 7) {
     // ================================================================ products
+    const int h = warp == 7 ? 1 : 0;  // the block
     const uint32_t dhi = (1024u >> 4) | (1u << 14) | (2u << 29);
-    const uint32_t klo = ((kF8 ? sbase + C::kOffWide : sK) >> 4) | (1u << 16);
+    const uint32_t dhi8 = D == 128 ? dhi : (512u >> 4) | (1u << 14) | (4u << 29);  // e4m3 rows of 64 bytes: 64-byte swizzle
+    const uint32_t klo = (sK >> 4) | (1u << 16), wlo = ((sbase + C::kOffWide) >> 4) | (1u << 16);
     const uint32_t qlo = (sQ >> 4) | (1u << 16);
-    int g = 0;
+    auto desc = [](uint32_t hi, uint32_t lo) { return (static_cast<uint64_t>(hi) << 32) | lo; };
+    WeighRing k, q, w;
+    if (h) k.next(p.ring_k);
+    WeighRing l;     // places of the tiles' LSE
+    uint32_t g = 0;  // steps
     bool ok = true;
-    WeighJob t;
-    for (int u = 0; job(u, t, ok, 63); ++u) {
-      const int sk = kF8 ? u % NWm : u % RK;
-      ok = __all_sync(0xffffffffu, kF8 ? tile_wait(bar_w_full(sk), (u / NWm) & 1, wc, 64) : tile_wait(bar_k_full(sk), (u / RK) & 1, wc, 64));
-      for (int j = 0; ok && j < t.nq; ++j, ++g) {
-        const int bf = g % NB, sq = g % RQ;
-        if (g >= NB) ok = tile_wait(bar_s_free(bf), ((g - NB) / NB) & 1, wc, 65);
-        ok = __all_sync(0xffffffffu, ok && tile_wait(bar_q_full(sq), (g / RQ) & 1, wc, 66));
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t idesc = idesc_bf16_f32(128, (weigh_cols(p, t, j).n + 15) / 16 * 16, 0);
-#pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          const uint32_t off = (ks / 4) * (C::kSubBytes >> 4) + (ks % 4) * 2;
-          mma_ss_elect(tmem + 128u * bf, (static_cast<uint64_t>(dhi) << 32) | (klo + sk * (C::kTileBytes >> 4) + off),
-                       (static_cast<uint64_t>(dhi) << 32) | (qlo + sq * (C::kTileBytes >> 4) + off), idesc, ks > 0 ? 1u : 0u);
+    WeighUnit t;
+    while (job(t, ok, 65)) {
+      const bool single = t.nq == 1, narrow = kF8 && single;
+      const int first = t.first();
+      if (lane == 0) {
+        uint32_t a = 0, wst = 0;
+        if (kF8 && !narrow) {  // widened keys: two stages, one for each issuer
+          if (h) w.next(NWm);
+          wst = w.st;
+          ok = tile_wait(bar_w_full(w.st), w.ph, wc, 66);
+          if (ok) mbar_arrive(bar_k_free(k.st));  // its codes have been read
+          a = wlo + w.st * (C::kTileBytes >> 4);
+          if (!h) w.next(NWm);
+          w.next(NWm);
         }
-        mma_commit_elect(bar_s_full(bf));
-        mma_commit_elect(bar_q_free(sq));
+        const int n = single ? t.steps : t.nq;
+        for (int j = 0; ok && j < n; ++j, ++g) {
+          const uint32_t bf = 2 * (g & 1) + h, dst = tmem + 128u * bf;
+          if (j == 0 || !single) ok = narrow ? tile_wait(bar_w_full(w.st), w.ph, wc, 68) : tile_wait(bar_q_full(q.st), q.ph, wc, 69);
+          if (narrow || (!kF8 && (single || j == 0))) {
+            ok = ok && tile_wait(bar_k_full(k.st), k.ph, wc, 66);
+            a = klo + k.st * (C::kStageK >> 4);
+          }
+          ok = ok && tile_wait(bar_s_free(bf), ((g >> 1) & 1) ^ 1, wc, 70);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t cols = (weigh_cols(p, first, t.T, single ? 0 : j).n + 15) / 16 * 16;
+          if (narrow) {
+            const uint32_t idesc = (1u << 4) | ((cols >> 3) << 17) | (8u << 24);  // e4m3 x e4m3 -> fp32
+            const uint32_t b = wlo + w.st * (C::kTileBytes >> 4);
+#pragma unroll
+            for (int part = 0; part < 2; ++part)  // hi, lo
+#pragma unroll
+              for (int ks = 0; ks < D / 32; ++ks)
+                mma_ss_f8(dst, desc(dhi8, a + ks * 2), desc(dhi8, b + part * (128 * D >> 4) + ks * 2), idesc, part + ks > 0 ? 1u : 0u);
+          } else {
+            const uint32_t idesc = idesc_bf16_f32(128, cols, 0);
+            const uint32_t b = qlo + q.st * (C::kTileBytes >> 4);
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks) {
+              const uint32_t off = (ks / 4) * (C::kSubBytes >> 4) + (ks % 4) * 2;
+              mma_ss(dst, desc(dhi, a + off), desc(dhi, b + off), idesc, ks > 0 ? 1u : 0u);
+            }
+            // the LSE last: everything before it is a sum of small terms
+            mma_ss(dst, weigh_step_desc(sbase + C::kOffOnes), weigh_step_desc(sbase + C::kOffStep + l.st * kWeighStepBytes), idesc, 1u);
+          }
+          mma_commit(bar_s_full(bf));
+          if (single) {
+            mma_commit(bar_k_free(k.st));
+            k.next(p.ring_k);
+            k.next(p.ring_k);
+          } else {
+            mma_commit(bar_q_free(q.st));
+            q.next(p.ring_q);
+            l.next(C::kLse);
+          }
+        }
+        if (ok) {
+          if (narrow) {
+            mbar_arrive(bar_q_free(q.st));  // its rows had been read when their two terms came
+            mma_commit(bar_w_free(w.st));
+            w.next(NWm);
+          } else if (single) {
+            mma_commit(bar_q_free(q.st));
+          } else if (kF8) {  // nobody but this issuer had the stage
+            mma_commit(bar_w_free(wst));
+            mma_commit(bar_w_free(wst));
+          } else {
+            mma_commit(bar_k_free(k.st));
+          }
+          if (single) {
+            q.next(p.ring_q);
+            l.next(C::kLse);
+          } else {
+            k.next(p.ring_k);
+            k.next(p.ring_k);
+          }
+        }
       }
+      ok = __shfl_sync(0xffffffffu, static_cast<int>(ok), 0) != 0;
       if (!ok) break;
-      mma_commit_elect(kF8 ? bar_w_free(sk) : bar_k_free(sk));
     }
     // every product issued must finish before tensor memory is released
-    mma_commit_elect(bar_drain);
-    mbar_wait_drain(bar_drain, 0, p.timeout_ns);
-  } else if (warp >= 4 && warp < 8) {
+    if (lane == 0) {
+      mma_commit(bar_drain(h));
+      mbar_wait_drain(bar_drain(h), 0, p.timeout_ns);
+    }
+  } else if (warp == 4 || warp == 5) {
     // ================================================================ LSE of the columns
-    const int bf = warp - 4;
-    float* to = reinterpret_cast<float*>(smem + C::kOffLse) + bf * 128;
-    int g = 0;
+    const int par = warp - 4;  // of the tiles
+    int g = 0;                 // tiles
     bool ok = true;
-    WeighJob t;
-    for (int u = 0; job(u, t, ok, 67); ++u) {
-      // tiles of this unit for this buffer
-      for (int j = (bf - g) & (NB - 1); j < t.nq; j += NB) {
-        const WeighCols c = weigh_cols(p, t, j);
+    WeighUnit t;
+    WeighRing q, l;
+    if (par) {
+      q.next(p.ring_q);
+      l.next(C::kLse);
+    }
+    while (job(t, ok, 71)) {
+      const int first = t.first();
+      for (int j = (par ^ g) & 1; j < t.nq; j += 2) {
+        const WeighCols c = weigh_cols(p, first, t.T, j);
         float v[4];
         bool none = false;
 #pragma unroll
@@ -440,80 +628,140 @@ __global__ void __launch_bounds__(WeighCfg<D, kF8>::kThreads, 1)
             none |= v[i] == -INFINITY;
           }
         }
-        const int gg = g + j;
-        if (gg >= NB) ok = __all_sync(0xffffffffu, tile_wait(bar_s_free(bf), ((gg - NB) / NB) & 1, wc, 68));
+        // every group is done with the tile that had this place (a lane looks after one), and the stage of
+        // its rows has been freed: what arrives there sooner would count for the tile before it
+        ok = __all_sync(0xffffffffu, tile_wait(bar_lse_free(l.st, lane & 3), l.ph ^ 1u, wc, 72) &&
+                                         tile_wait(bar_q_free(q.st), q.ph ^ 1u, wc, 72));
         if (!ok) break;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) to[32 * i + lane] = v[i];
+        for (int i = 0; i < 4; ++i) {
+          reinterpret_cast<float*>(smem + C::kOffLse)[l.st * 128 + 32 * i + lane] = v[i];
+          // three bf16 terms of -LSE / scale, each the rounding of what the ones before leave
+          const float x = v[i] == -INFINITY ? 0.f : v[i] * (p.rscale * 0.69314718055994531f);
+          const float t1 = __bfloat162float(__float2bfloat16_rn(x)), t2 = __bfloat162float(__float2bfloat16_rn(x - t1));
+          *reinterpret_cast<uint4*>(smem + C::kOffStep + l.st * kWeighStepBytes + weigh_step_row(32 * i + lane)) =
+              make_uint4(pack_bf16x2(t1, t2), pack_bf16x2(x - t1 - t2, 0.f), 0u, 0u);
+        }
         none = __any_sync(0xffffffffu, none);
-        if (lane == 0) odd[bf] = none;
+        if (lane == 0) odd[l.st] = none;
+        fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar_lse(bf));
+        if (lane == 0) {
+          mbar_arrive(bar_q_full(q.st));
+          mbar_arrive(bar_lse_full(l.st));
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          q.next(p.ring_q);
+          l.next(C::kLse);
+        }
       }
       if (!ok) break;
       g += t.nq;
     }
-  } else if (warp >= 8 && warp < 16) {
+  } else if (warp >= kWeighSumWarp && warp < kWeighConvWarp) {
     // ================================================================ exponentials and sums
-    const int grp = (warp - 8) >> 2, r = (warp & 3) * 32 + lane;
-    const uint32_t tl = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    float* parts = reinterpret_cast<float*>(smem + C::kOffPart);
-    int g = 0;
+    const int pair = (warp - kWeighSumWarp) >> 3, blk = ((warp - kWeighSumWarp) >> 2) & 1, r = (warp & 3) * 32 + lane;
+    const int bf = 2 * pair + blk;
+    const uint32_t ts = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + 128u * bf;
+    float* parts = reinterpret_cast<float*>(smem + C::kOffPart) + 128 * blk + r;
+    uint32_t g = 0, u = 0, x = 0;  // steps, units, blocks
     bool ok = true;
-    WeighJob t;
-    for (int u = 0; job(u, t, ok, 69); ++u) {
-      const bool last = ((g + t.nq - 1) & 1) == grp;  // this group has the unit's last tile and its result
-      const int pos = t.tile * kWeighKeys + r;
-      const int page = job_at(u)->pages[r / 16];
-      const bool here = page >= 0 && pos < t.n;
-      const long long at = here ? (static_cast<long long>(page) * p.Hkv + t.h) * p.page + static_cast<uint32_t>(pos) % static_cast<uint32_t>(p.page) : 0;
-      float old = 0.f;
-      if (last && here && pos < t.ctx && p.decay != 0.f) old = p.w[at];
-      const int sees = max(pos - t.ctx - t.first, 0);  // tokens from t.first + sees on see this key
-      float sum = 0.f;
-      for (int j = (g ^ grp) & 1; j < t.nq; j += 2) {
-        const int gg = g + j, bf = gg % NB;
-        const WeighCols c = weigh_cols(p, t, j);
-        ok = __all_sync(0xffffffffu, tile_wait(bar_lse(bf), (gg / NB) & 1, wc, 70) && tile_wait(bar_s_full(bf), (gg / NB) & 1, wc, 71));
+    WeighRing l;
+    WeighUnit t;
+    // The rows of this thread's keys: in a unit of one tile its steps are every other one, two at most.
+    long long row0[2] = {-1, -1};
+    auto rows = [&](const WeighJob& at, const WeighUnit& un) {
+      const int s0 = un.nq == 1 ? (g ^ pair) & 1 : 0;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) row0[i] = at.rows[16 * (s0 + 2 * i) + 8 * blk + r / 16];
+    };
+    static_assert(kWeighSteps <= 4, "two steps a group");
+    for (; job_more(t, ok, 73, rows); ++u) {
+      const bool single = t.nq == 1, narrow = kF8 && single;
+      const int first = t.first(), n = single ? t.steps : t.nq;
+      const int j0 = (g ^ pair) & 1;                    // this pair's first step
+      const bool last = single || ((n - 1) & 1) == j0;  // whether the result is this pair's to write
+      float old[2] = {0.f, 0.f}, sum = 0.f;
+      int sees = 0;      // tokens from first + sees on see this thread's key
+      long long at = -1;
+      auto key = [&](int i) {  // the thread's key of step i (its place in row0), if there is one
+        const int pos = t.key0 + (single ? kWeighStep * (j0 + 2 * i) : 0) + 128 * blk + r;
+        const long long row = i ? row0[1] : row0[0];
+        at = row >= 0 && pos < t.n && (!single || j0 + 2 * i < n) ? row + (r & 15) : -1;
+        sees = max(pos - t.ctx - first, 0);
+        return pos;
+      };
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int pos = key(i);
+        if (last && at >= 0 && pos < t.ctx && p.decay != 0.f && (i == 0 || single)) old[i] = p.w[at];
+      }
+      key(0);
+      // A tile that this group does not look at, handed back once its LSE has come: earlier it would be
+      // handed back for the tile before it at its place.
+      auto pass = [&]() {
+        if (!__all_sync(0xffffffffu, tile_wait(bar_lse_full(l.st), l.ph, wc, 80))) return false;
+        if (lane == 0) mbar_arrive(bar_lse_free(l.st, bf));
+        l.next(C::kLse);
+        return true;
+      };
+#pragma unroll 1
+      for (int j = 0; j < n; ++j) {
+        if ((j ^ j0) & 1) {  // the other pair's
+          if (single) continue;
+          ok = pass();
+          if (!ok) break;
+          continue;
+        }
+        const WeighCols c = weigh_cols(p, first, t.T, single ? 0 : j);
+        if (single) key((j - j0) >> 1);
+        const int c0 = max(sees - (c.tok - first), 0) * p.heads;  // the key's first column of the tile
+        ok = __all_sync(0xffffffffu, tile_wait(bar_s_full(bf), ((g + j) >> 1) & 1, wc, 74));
         if (!ok) break;
         tc_fence_after();
-        const float4* nl = reinterpret_cast<const float4*>(smem + C::kOffLse) + bf * 32;
-        const int c0 = max(sees - (c.tok - t.first), 0) * p.heads;  // the key's first column of the tile
-        const bool ragged = odd[bf] || __any_sync(0xffffffffu, c0 > 0) || (c.n & 31) != 0;
-        const float2 cc = make_float2(p.c, p.c);
         float2 a0 = make_float2(0.f, 0.f), a1 = make_float2(0.f, 0.f);
+        if (!(narrow || odd[l.st] || __any_sync(0xffffffffu, c0 > 0) || (c.n & 31) != 0)) {
+          const float2 cc = make_float2(p.c, p.c);
 #pragma unroll 1
-        for (int q = 0; 32 * q < c.n; ++q) {
-          uint32_t s[32];
-          tmem_ld32(tl + 128u * bf + 32 * q, s);
-          float4 n4[8];
+          for (int q = 0; q < c.n; q += 32) {
+            uint32_t s[32];
+            tmem_ld32(ts + q, s);
+            tmem_wait_ld();
 #pragma unroll
-          for (int k = 0; k < 8; ++k) n4[k] = nl[8 * q + k];
-          tmem_wait_ld();
-          if (!ragged) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              float2 x = __ffma2_rn(make_float2(__uint_as_float(s[4 * k]), __uint_as_float(s[4 * k + 1])), cc, make_float2(n4[k].x, n4[k].y));
-              float2 y = __ffma2_rn(make_float2(__uint_as_float(s[4 * k + 2]), __uint_as_float(s[4 * k + 3])), cc, make_float2(n4[k].z, n4[k].w));
-              x.x = ex2_approx(x.x);
-              x.y = ex2_approx(x.y);
-              y.x = ex2_approx(y.x);
-              y.y = ex2_approx(y.y);
-              a0 = __fadd2_rn(a0, x);
-              a1 = __fadd2_rn(a1, y);
+            for (int k = 0; k < 16; ++k) {
+              float2 e = __fmul2_rn(make_float2(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), cc);
+              e.x = ex2_approx(e.x);
+              e.y = ex2_approx(e.y);
+              if (k & 1)
+                a1 = __fadd2_rn(a1, e);
+              else
+                a0 = __fadd2_rn(a0, e);
             }
-          } else {
+          }
+        } else {
+          const float4* nl = reinterpret_cast<const float4*>(smem + C::kOffLse) + l.st * 32;
+          const float4* fac = reinterpret_cast<const float4*>(smem + C::kOffFactor) + (u % kWeighFactors) * 32;
+          float key_scale = 1.f;
+          if (narrow) key_scale = scale_of(max(static_cast<uint32_t>(smem[C::kOffCode + ((x + 2 * j + blk) % kWeighCodes) * 128 + r]), 1u));
+#pragma unroll 1
+          for (int q = 0; q < c.n; q += 8) {
+            uint32_t s[8];
+            tmem_ld8(ts + q, s);
+            tmem_wait_ld();
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const int col = 32 * q + 4 * k;
-              if (col < c.n) {
-                auto one = [&](int i, float n) {
-                  const float e = ex2_approx(fmaf(__uint_as_float(s[4 * k + i]), p.c, n));
-                  return col + i >= c0 && col + i < c.n && n != -INFINITY ? e : 0.f;
-                };
-                a0 = __fadd2_rn(a0, make_float2(one(0, n4[k].x), one(1, n4[k].y)));
-                a1 = __fadd2_rn(a1, make_float2(one(2, n4[k].z), one(3, n4[k].w)));
-              }
+            for (int k = 0; k < 2; ++k) {
+              const int col = q + 4 * k;
+              const float4 n4 = nl[col >> 2];
+              float4 f4 = make_float4(p.c, p.c, p.c, p.c);
+              if (narrow) f4 = fac[col >> 2];
+              auto one = [&](int i, float f, float nl1) {
+                const float y = __uint_as_float(s[4 * k + i]) * key_scale;
+                const float e = ex2_approx(narrow ? fmaf(y, f, nl1) : y * f);
+                return col + i >= c0 && col + i < c.n && nl1 != -INFINITY ? e : 0.f;
+              };
+              a0 = __fadd2_rn(a0, make_float2(one(0, f4.x, n4.x), one(1, f4.y, n4.y)));
+              a1 = __fadd2_rn(a1, make_float2(one(2, f4.z, n4.z), one(3, f4.w, n4.w)));
             }
           }
         }
@@ -521,54 +769,121 @@ __global__ void __launch_bounds__(WeighCfg<D, kF8>::kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(bar_s_free(bf));
         sum += (a0.x + a0.y) + (a1.x + a1.y);
+        if (single) {
+          if (at >= 0) p.out[at] = fmaf(p.decay, j == j0 ? old[0] : old[1], sum);
+          sum = 0.f;
+        } else {
+          if (lane == 0) mbar_arrive(bar_lse_free(l.st, bf));
+          l.next(C::kLse);
+        }
       }
       if (!ok) break;
-      // the sum of the even tiles and of the odd ones: the same two whichever group has which
-      const int slot = u % kWeighParts;
-      if (!last) {
-        parts[slot * 128 + r] = sum;
+      if (single) {
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar_part(slot));
-      } else {
-        if (t.nq > 1) {
-          ok = __all_sync(0xffffffffu, tile_wait(bar_part(slot), (u / kWeighParts) & 1, wc, 72));
-          if (!ok) break;
-          sum += parts[slot * 128 + r];
-        }
-        if (here) p.out[at] = fmaf(p.decay, old, sum);
-      }
-      g += t.nq;
-    }
-  } else if (kF8 && warp >= 16) {
-    // ================================================================ K: e4m3 -> bf16
-    if constexpr (kF8) {
-      const int r = threadIdx.x - 512;
-      bool ok = true;
-      WeighJob t;
-      for (int u = 0; job(u, t, ok, 73); ++u) {
-        const int st = u % RK, sw = u % NWm;
-        ok = tile_wait(bar_k_full(st), (u / RK) & 1, wc, 74) && (u < NWm || tile_wait(bar_w_free(sw), ((u - NWm) / NWm) & 1, wc, 75));
-        ok = __all_sync(0xffffffffu, ok);
+        ok = pass();
         if (!ok) break;
-        const uint8_t* src = smem + C::kOffK + st * C::kStageK + r * D;
-        uint8_t* dst = smem + C::kOffWide + sw * C::kTileBytes + r * 128;
-        const uint32_t code = smem[C::kOffCode + st * 128 + r];
-        const uint32_t two = (code << 7) | (code << 23);  // 2^(code - 127) twice, as bf16
-        const __nv_bfloat162 scale = *reinterpret_cast<const __nv_bfloat162*>(&two);
-#pragma unroll 2
-        for (int c = 0; c < D / 16; ++c) {
-          const uint4 raw = *reinterpret_cast<const uint4*>(src + ((D == 128 ? c ^ (r & 7) : c ^ ((r >> 1) & 3)) << 4));
-          uint8_t* to = dst + (c / 4) * C::kSubBytes;
-          const int ch = (2 * c) & 7;
-          *reinterpret_cast<uint4*>(to + ((ch ^ (r & 7)) << 4)) = widen8(raw.x, raw.y, scale);
-          *reinterpret_cast<uint4*>(to + (((ch + 1) ^ (r & 7)) << 4)) = widen8(raw.z, raw.w, scale);
+      } else {
+        // the sum of the even tiles and of the odd ones: the same two whichever pair has which
+        const int slot = u % kWeighParts;
+        if (!last) {
+          parts[slot * 256] = sum;
+        } else {
+          ok = __all_sync(0xffffffffu, tile_wait(bar_part(slot, blk), (u / kWeighParts) & 1, wc, 79));
+          if (!ok) break;
+          sum += parts[slot * 256];
+          if (at >= 0) p.out[at] = fmaf(p.decay, old[0], sum);
         }
-        fence_proxy_async_smem();
+      }
+      // (every unit, so that a slot's turns follow from u; in a unit of one tile by the pair that has its second step)
+      if (single ? j0 == 1 : !last) {
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(bar_w_full(sw));
-          mbar_arrive(bar_k_free(st));
+        if (lane == 0) mbar_arrive(bar_part(u % kWeighParts, blk));
+      }
+      g += n;
+      x += 2 * (single ? n : 1);
+    }
+  } else if (kF8 && warp >= kWeighConvWarp) {
+    // ================================================================ operands in another form (e4m3)
+    if constexpr (kF8) {
+      const int r = threadIdx.x - 32 * kWeighConvWarp;
+      WeighRing k, q, w;
+      uint32_t u = 0, x = 0;  // units, blocks
+      bool ok = true;
+      WeighUnit t;
+      for (; job(t, ok, 75); ++u) {
+        const int first = t.first();
+        if (t.nq == 1) {
+          // ---- the queries as two e4m3 terms, a lane 8 columns
+          constexpr int kL = D / 8;  // lanes of a row
+          ok = tile_wait(bar_q_full(q.st), q.ph, wc, 76) && tile_wait(bar_w_free(w.st), w.ph ^ 1u, wc, 77);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          const int rows = weigh_cols(p, first, t.T, 0).n, ch = lane % kL;
+          const uint8_t* src = smem + q.st * C::kTileBytes;
+          uint8_t* dst = smem + C::kOffWide + w.st * C::kTileBytes;
+          float* fac = reinterpret_cast<float*>(smem + C::kOffFactor) + (u % kWeighFactors) * 128;
+#pragma unroll 1
+          for (int r0 = (warp - kWeighConvWarp) * (32 / kL); r0 < rows; r0 += 4 * (32 / kL)) {
+            const int qr = r0 + lane / kL;
+            const uint4 x = *reinterpret_cast<const uint4*>(src + (ch / 8) * C::kSubBytes + qr * 128 + (((ch & 7) ^ (qr & 7)) << 4));
+            uint32_t mx = finite_max(x);  // largest finite magnitude; bit 31: one is not
+            if (any_nonfinite(x.x) || any_nonfinite(x.y) || any_nonfinite(x.z) || any_nonfinite(x.w)) mx |= 0x80000000u;
+#pragma unroll
+            for (int o = kL / 2; o > 0; o >>= 1) mx = max(mx & 0x7fffffffu, __shfl_xor_sync(0xffffffffu, mx, o) & 0x7fffffffu) |
+                                                    ((mx | __shfl_xor_sync(0xffffffffu, mx, o)) & 0x80000000u);
+            const uint32_t ef = min(max((mx & 0x7fffffffu) >> 7, 8u), 253u);  // exponent field of the row's largest value
+            const float up = __uint_as_float((261u - ef) << 23);              // brings it into [128, 256)
+            // a row that is not finite makes its keys' weights NaN
+            if (ch == 0) fac[qr] = (mx >> 31) == 0u ? p.c * __uint_as_float((ef - 7u) << 23) : NAN;
+            const uint32_t v[4] = {x.x, x.y, x.z, x.w};
+            uint32_t hi[2], lo[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {  // four values each
+              const float f0 = bf16_lo(v[2 * i]) * up, f1 = bf16_hi(v[2 * i]) * up;
+              const float f2 = bf16_lo(v[2 * i + 1]) * up, f3 = bf16_hi(v[2 * i + 1]) * up;
+              const uint32_t h0 = pack_e4m3x2(f0, f1), h1 = pack_e4m3x2(f2, f3);
+              const float2 b0 = e4m3x2_to_f32(h0), b1 = e4m3x2_to_f32(h1);
+              hi[i] = h0 | (h1 << 16);
+              lo[i] = pack_e4m3x2(f0 - b0.x, f1 - b0.y) | (pack_e4m3x2(f2 - b1.x, f3 - b1.y) << 16);
+            }
+            const int sx = D == 128 ? (ch >> 1) ^ (qr & 7) : (ch >> 1) ^ ((qr >> 1) & 3);
+            uint8_t* to = dst + qr * D + (sx << 4) + (ch & 1) * 8;
+            *reinterpret_cast<uint2*>(to) = make_uint2(hi[0], hi[1]);
+            *reinterpret_cast<uint2*>(to + 128 * D) = make_uint2(lo[0], lo[1]);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar_w_full(w.st));
+          w.next(NWm);
+          for (int i = 0; i < 2 * t.steps; ++i) k.next(p.ring_k);
+          x += 2 * t.steps;
+        } else {
+          // ---- both blocks of keys: codes times scale as bf16, a thread a key
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h, ++x, w.next(NWm), k.next(p.ring_k)) {
+            ok = tile_wait(bar_k_full(k.st), k.ph, wc, 78) && tile_wait(bar_w_free(w.st), w.ph ^ 1u, wc, 77);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            const uint8_t* src = smem + p.ring_q * C::kTileBytes + k.st * C::kStageK + r * D;
+            uint8_t* dst = smem + C::kOffWide + w.st * C::kTileBytes + r * 128;
+            const uint32_t code = smem[C::kOffCode + (x % kWeighCodes) * 128 + r];
+            const uint32_t two = (code << 7) | (code << 23);  // 2^(code - 127) twice, as bf16
+            const __nv_bfloat162 scale = *reinterpret_cast<const __nv_bfloat162*>(&two);
+#pragma unroll 2
+            for (int c = 0; c < D / 16; ++c) {
+              const uint4 raw = *reinterpret_cast<const uint4*>(src + ((D == 128 ? c ^ (r & 7) : c ^ ((r >> 1) & 3)) << 4));
+              uint8_t* to = dst + (c / 4) * C::kSubBytes;
+              const int ch = (2 * c) & 7;
+              *reinterpret_cast<uint4*>(to + ((ch ^ (r & 7)) << 4)) = widen8(raw.x, raw.y, scale);
+              *reinterpret_cast<uint4*>(to + (((ch + 1) ^ (r & 7)) << 4)) = widen8(raw.z, raw.w, scale);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar_w_full(w.st));
+          }
+          if (!ok) break;
         }
+        for (int j = 0; j < t.nq; ++j) q.next(p.ring_q);
       }
     }
   }

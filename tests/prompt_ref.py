@@ -6,8 +6,10 @@ Bounds (u = 2^-24, the half step of fp32; 2^-8 that of bf16):
   pi 2^-24, and the function's 2 units), and by position * frequency * 2^-51 for the product; the norm's
   sum of d squares, its root and three products are off by 32 u; the result rounds to bf16 once.
 * attention: as in cache_ref.
-* weights: a score is off by ds = d u B + 2 u |s| (B = scale * sum |q_i k_i|), the exponent's argument by
-  4 u (|s| + |LSE|) for its roundings, exp2 by 4 u; a sum of R rows is off by (R / 4 + 64) u at most.
+* weights: score - LSE is an fp32 sum of d products and three terms of LSE / scale, in any order, so off by
+  ds = (d + 16) u (B + |LSE|) with B = scale * sum |q_i k_i| (for an e4m3 cache also by what the query's two
+  e4m3 terms may lose, as in cache_ref); LSE's split, its conversions and the scaling are off by 8 u (|s| + |LSE|),
+  exp2 by 4 u; a sum of R rows is off by (R / 4 + 64) u at most.
 """
 from __future__ import annotations
 
@@ -16,7 +18,7 @@ import math
 import numpy as np
 import torch
 
-from cache_ref import HALF_BF16, U, place, rows_of
+from cache_ref import HALF_BF16, U, place, query_loss, rows_of
 
 
 def bf16(r, shape, scale=1.0):
@@ -121,9 +123,10 @@ def ref_weigh(Q, LSE, k, ks, table, ctx, cu, page, scale, decay, w, out):
                 q, L = Q[cu[b]:cu[b + 1], h * G + g], LSE[h * G + g, cu[b]:cu[b + 1]][:, None]
                 s = scale * (q @ K[:, h].T)
                 big = scale * (np.abs(q) @ np.abs(K[:, h]).T)
+                lost = 0.0 if ks is None else scale * (np.stack([query_loss(x) for x in q]) @ np.abs(K[:, h]).T)
                 with np.errstate(invalid="ignore", over="ignore"):
                     p = np.where(see & ~np.isneginf(L), np.exp(s - L), 0.0)
-                    e = p * (d * U * big + 2 * U * np.abs(s) + 4 * U * (np.abs(s) + np.abs(L)) + 4 * U)
+                    e = p * ((d + 16) * U * (big + np.abs(L)) + lost + 8 * U * (np.abs(s) + np.abs(L)) + 4 * U)
                 got += p.sum(0)
                 err += np.where(p > 0, e, 0.0).sum(0)
             out[pg, h, row] = old + got

@@ -182,6 +182,66 @@ def test_large_prompt_against_torch(f8):
         assert torch.equal(out, again) and torch.equal(out, two)
 
 
+@pytest.mark.parametrize("f8", [False, True])
+@pytest.mark.parametrize("hkv,G,d,page,B,ctx,T", [
+    (8, 4, 128, 64, 48, (2000, 5000), (1, 1)),      # long units, one step after the other
+    (8, 4, 64, 48, 60, (3000, 4500), (0, 3)),
+    (4, 5, 128, 16, 70, (0, 9000), (1, 20)),
+    (8, 1, 64, 128, 300, (0, 400), (1, 1)),          # many short ones
+    (2, 4, 128, 32, 40, (0, 2000), (1, 300)),        # one tile here, several there
+])
+def test_batches_against_torch(hkv, G, d, page, B, ctx, T, f8):
+    """Batches that go round the SMs several times, every key of them, in fp64 torch."""
+    pkg, r = _pkg(), np.random.default_rng(29)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(29)
+    ctxs, Ts = r.integers(ctx[0], ctx[1] + 1, B), r.integers(T[0], T[1] + 1, B)
+    need = [-(-int(c + t) // page) for c, t in zip(ctxs, Ts)]
+    P = sum(need) + 1
+    order = torch.randperm(P, generator=g, device="cuda").to(torch.int32)
+    table = torch.zeros((B, max(need)), dtype=torch.int32, device="cuda")
+    for b in range(B):
+        table[b, :need[b]] = order[sum(need[:b]):sum(need[:b + 1])]
+    k = torch.randn((P, hkv, page, d), generator=g, device="cuda").to(torch.bfloat16)
+    kw, kd = {}, k.double()
+    if f8:
+        codes = k.float().clamp(-4, 4).to(torch.float8_e4m3fn)
+        s = torch.randint(125, 130, (P, hkv, page), generator=g, device="cuda", dtype=torch.uint8)
+        kd = codes.double() * torch.exp2(s.double() - 127)[..., None]
+        k, kw = codes, {"k_scale": s}
+    cu = np.concatenate([[0], np.cumsum(Ts)])
+    total = int(cu[-1])
+    Q = torch.randn((total, hkv * G, d), generator=g, device="cuda").to(torch.bfloat16)
+    LSE = torch.full((hkv * G, total), -math.inf, device="cuda")
+    w = torch.rand((P, hkv, page), generator=g, device="cuda")
+    want, tol = torch.full((P, hkv, page), -5.0, dtype=torch.float64, device="cuda"), torch.zeros((P, hkv, page), device="cuda")
+    for b in range(B):
+        c, t = int(ctxs[b]), int(Ts[b])
+        if t == 0:
+            continue
+        p = torch.arange(c + t, device="cuda")
+        pg, row = table[b].long()[p // page], p % page
+        K = kd[pg, :, row].transpose(0, 1)
+        q = Q[cu[b]:cu[b + 1]].double().view(t, hkv, G, d).permute(1, 2, 0, 3).reshape(hkv, G * t, d)
+        z = q @ K.transpose(1, 2) / math.sqrt(d)
+        see = (p[None] <= c + torch.arange(t, device="cuda")[:, None]).repeat(G, 1)
+        z = z.masked_fill(~see, -math.inf)
+        lse = torch.logsumexp(z, -1).float()
+        LSE[:, cu[b]:cu[b + 1]] = lse.view(hkv * G, t)
+        prob = torch.exp(z - lse.double()[..., None])
+        old = torch.where(p < c, 0.5 * w[pg, :, row].double().t(), 0.0)
+        want[pg, :, row] = (old + prob.sum(1)).t()
+        # B of the module's bounds, and an e4m3 query's 2^-17 of its row's largest value
+        big = (q.abs() @ K.abs().transpose(1, 2)) / math.sqrt(d)
+        lost = (q.abs().amax(-1, keepdim=True) * 2.0 ** -17 * K.abs().sum(-1)[:, None]) / math.sqrt(d) if f8 else 0.0
+        e = prob * ((d + 16) * 2.0 ** -24 * (big + lse.abs()[..., None]) + lost + 2.0 ** -21 * (z.abs().nan_to_num(posinf=0.0) + lse.abs()[..., None] + 1))
+        tol[pg, :, row] = (e.sum(1) + (t * G / 4 + 64) * 2.0 ** -24 * prob.sum(1) + 2.0 ** -22 * old).t().float() + 1e-30
+    out = torch.full((P, hkv, page), -5.0, device="cuda")
+    pkg.attn_cache_weigh(Q, LSE, k, w, table, _i32(ctxs), _i32(cu), out, decay=0.5, **kw)
+    pkg.cache_check()
+    assert bool(((out.double() - want).abs() <= 1.01 * tol).all())
+
+
 def test_bad_pages_are_reported_and_left_out():
     pkg = _pkg()
     bt = Batch(26, 2, 2, 64, 16, False, [50], [4], masks="chain")
