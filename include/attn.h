@@ -424,8 +424,8 @@ enum { ATTN_WEIGHT_BF16 = 0, ATTN_WEIGHT_FP32 = 1 };
  * attn_qk_rotate -- norms of query and key heads and their rotation by position, in one pass.
  *   Q [total, Hq, d], K [total, Hkv, d]: device bf16, element (t, h, x) at t * strides[0] + h *
  *         strides[1] + x (host int64[2] in elements, multiples of 8), so slices of a joint
- *         projection need no copy.  Q_out and K_out the same with strides of their own; they may be
- *         Q and K themselves (same strides), not other parts of them.  16-byte aligned.  Hq or Hkv
+ *         projection need no copy.  Q_out and K_out the same with strides of their own; Q_out may
+ *         be Q itself and K_out K (same strides), an output overlaps no other input.  16-byte aligned.  Hq or Hkv
  *         may be 0 (its pointers are not used).
  *   q_weight, k_weight  device [d] of weight_type, or NULL: no norm.  With one, a row becomes
  *         x_i * w_i / sqrt(mean(x^2) + eps).

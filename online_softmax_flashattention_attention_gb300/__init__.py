@@ -659,7 +659,7 @@ def attn_qk_rotate(Q, K, cu_seqlens=None, inv_freq=None, Q_out=None, K_out=None,
     inv_freq[i].  cu_seqlens int32 [B + 1] (None: all rows are one sequence): row cu_seqlens[b] + i is at
     start_lens[b] + i (int32 [B]; None: 0), rows outside every sequence are left as they were;
     positions int32 [total] replaces these.  Returns Q_out and K_out (allocated contiguous when not
-    given; they may be Q and K).
+    given; Q_out may be Q and K_out K, an output overlaps no other input).
     """
     import torch
     dev = Q.device

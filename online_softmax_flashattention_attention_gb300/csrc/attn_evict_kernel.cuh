@@ -288,29 +288,41 @@ __global__ void __launch_bounds__(kMoveThreads) attn_evict_move_kernel(const Evi
   }
   uint8_t* pool = plane ? p.v : p.k;
   const int slices = p.row_bytes / p.slice;
-  const int lanes = p.slice / 16, col = (block % slices) * p.slice + (threadIdx.x % lanes) * 16;
+  const int lanes = p.slice / 16, col = (block % slices) * p.slice + (threadIdx.x % lanes) * 16;  // lanes: a power of two
   const int r0 = block / slices * p.rows_per_block, r1 = min(rows, r0 + p.rows_per_block);
-  const int step = kMoveThreads / lanes;
-  for (int i0 = r0; i0 < r1; i0 += step * kMoveUnroll) {
-    uint4 x[kMoveUnroll];
-    long long to[kMoveUnroll];
-#pragma unroll
-    for (int u = 0; u < kMoveUnroll; ++u) {
-      const int i = i0 + u * step + threadIdx.x / lanes;
-      to[u] = -1;
-      x[u] = make_uint4(0, 0, 0, 0);
-      if (i < r1) {
-        const int pos = kept[i];
-        if (p.in_place && pos == i) continue;
-        const long long from = evict_row(p, p.table, p.max_pages, b, h, pos);
-        to[u] = evict_row(p, p.to, p.to_pages, b, h, i);
-        if (from >= 0) x[u] = *reinterpret_cast<const uint4*>(pool + from * p.row_bytes + col);
+  const int step = kMoveThreads / lanes;  // rows a block moves at once
+  // The way of 256 rows, a thread each (two divisions and two loads), then the rows.
+  __shared__ long long from[kMoveThreads], to[kMoveThreads];
+  for (int i0 = r0; i0 < r1; i0 += kMoveThreads) {
+    const int i = i0 + threadIdx.x;
+    long long f = -1, t = -1;
+    if (i < r1) {
+      const int pos = kept[i];
+      if (!p.in_place || pos != i) {
+        f = evict_row(p, p.table, p.max_pages, b, h, pos);
+        t = evict_row(p, p.to, p.to_pages, b, h, i);
       }
     }
-    if (p.in_place) __syncthreads();  // a step's rows are read before any is written
+    from[threadIdx.x] = f;
+    to[threadIdx.x] = t;
+    __syncthreads();
+    for (int k0 = threadIdx.x / lanes; k0 < kMoveThreads; k0 += step * kMoveUnroll) {
+      uint4 x[kMoveUnroll];
+      long long dst[kMoveUnroll];
 #pragma unroll
-    for (int u = 0; u < kMoveUnroll; ++u)
-      if (to[u] >= 0) *reinterpret_cast<uint4*>(pool + to[u] * p.row_bytes + col) = x[u];
+      for (int u = 0; u < kMoveUnroll; ++u) {
+        const int k = k0 + u * step;
+        const long long src = k < kMoveThreads ? from[k] : -1;
+        dst[u] = k < kMoveThreads ? to[k] : -1;
+        x[u] = make_uint4(0, 0, 0, 0);
+        if (dst[u] >= 0 && src >= 0) x[u] = *reinterpret_cast<const uint4*>(pool + src * p.row_bytes + col);
+      }
+      if (p.in_place) __syncthreads();  // a step's rows are read before any is written
+#pragma unroll
+      for (int u = 0; u < kMoveUnroll; ++u)
+        if (dst[u] >= 0) *reinterpret_cast<uint4*>(pool + dst[u] * p.row_bytes + col) = x[u];
+    }
+    __syncthreads();
   }
 }
 

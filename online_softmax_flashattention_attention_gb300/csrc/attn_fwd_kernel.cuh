@@ -53,8 +53,6 @@ constexpr int kWarpTma = 4;
 constexpr int kWarpPv = 5;
 constexpr int kWarpS = 6;
 constexpr int kThreads = 224;      // 4 softmax warps + producer + two MMA issuers
-constexpr int kWarpFix = 7;        // prompts (attn_fwd_prompt): an eighth warp repairs ragged V blocks
-constexpr int kPromptThreads = 256;
 constexpr uint32_t kTmemCols = 512;
 
 struct FwdParams {
@@ -120,7 +118,7 @@ constexpr int kMaxSortedSeqs = 512;
 // the softmax warps waiting for scores, 64 because every block's hand-offs and rescale now
 // cover half the keys.  They stay as options because they are the same recurrence over other
 // blocks, which the tests compare with the 128-key build.
-template <int D, int BN = kBN, bool kPrompt = false>
+template <int D, int BN = kBN>
 struct FwdCfg {
   static constexpr int kBNc = BN;
   static constexpr int kSub = D / 64;                   // 64-column swizzle sub-tiles per row tile
@@ -144,8 +142,8 @@ struct FwdCfg {
   static constexpr int kOffV = kOffK + kStages * kKVBytes;
   static constexpr int kOffBar = kOffV + kStages * kKVBytes;
   // barriers: q_full, q_free, (one unused slot), k_full[S], v_full[S], k_free[S],
-  // v_free[S], s_full[B], pv_done[B], p_full[B], drain[2]; prompts: v_fixed[S]
-  static constexpr int kNumBars = 3 + 4 * kStages + 3 * kSBufs + 2 + (kPrompt ? kStages : 0);
+  // v_free[S], s_full[B], pv_done[B], p_full[B], drain[2]
+  static constexpr int kNumBars = 3 + 4 * kStages + 3 * kSBufs + 2;
   static constexpr int kOffMisc = kOffBar + 8 * kNumBars;  // tmem base, abort flag, prompts: 8 tags
   static constexpr int kOffPerm = kOffMisc + 16;           // uint16 order of packed sequences
   static constexpr int kSmemBytes = kOffPerm + 2 * kMaxSortedSeqs;
@@ -317,6 +315,38 @@ __device__ __forceinline__ uint32_t finite_only(uint32_t w) {
   return w;
 }
 
+// Row r of a V block in shared memory: zeros when it does not count, its infinities and NaN zeroed when
+// it does; whether there were any.
+template <int D, int kSubBytes>
+__device__ __forceinline__ bool repair_v_row(uint8_t* block, int r, bool past) {
+  uint4* at = reinterpret_cast<uint4*>(block + r * 128);
+  auto chunk = [&](int c) { return (c / 8) * (kSubBytes / 16) + ((c & 7) ^ (r & 7)); };
+  if (past) {
+#pragma unroll
+    for (int c = 0; c < D / 8; ++c) at[chunk(c)] = make_uint4(0, 0, 0, 0);
+    fence_proxy_async_smem();
+    return false;
+  }
+  // v * 0 is NaN for what is not finite, and nothing else
+  __nv_bfloat162 acc = __floats2bfloat162_rn(0.f, 0.f);
+#pragma unroll
+  for (int c = 0; c < D / 8; ++c) {
+    const uint4 v = at[chunk(c)];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      acc = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&(&v.x)[i]), __floats2bfloat162_rn(0.f, 0.f), acc);
+  }
+  const uint32_t bits = *reinterpret_cast<const uint32_t*>(&acc);
+  if (!any_nonfinite(bits)) return false;
+#pragma unroll 1
+  for (int c = 0; c < D / 8; ++c) {
+    const uint4 v = at[chunk(c)];
+    at[chunk(c)] = make_uint4(finite_only(v.x), finite_only(v.y), finite_only(v.z), finite_only(v.w));
+  }
+  fence_proxy_async_smem();
+  return true;
+}
+
 // Prompts: the infinities and NaN of values that went into the product as zero, to a row that sees
 // keys [k0, k1) of them: columns col .. col + 31 of its o~ (a positive weight leaves them what they are).
 __device__ __noinline__ void prompt_add_nonfinite_row(const __nv_bfloat16* v, long long stride, int keys, float* o) {
@@ -326,12 +356,12 @@ __device__ __noinline__ void prompt_add_nonfinite_row(const __nv_bfloat16* v, lo
       if (!(fabsf(x) < INFINITY)) o[i] += x;
     }
 }
-__device__ __forceinline__ void prompt_add_nonfinite(const FwdParams& p, const Item& it, int k0, int k1, int col, uint32_t* o) {
+__device__ __forceinline__ void prompt_add_nonfinite(const FwdParams& p, int k_base, int head, int k0, int k1, int col, uint32_t* o) {
   float f[32];
 #pragma unroll
   for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(o[i]);
-  prompt_add_nonfinite_row(p.v + static_cast<long long>(it.k_base + k0) * p.vs_r +
-                               fast_div(it.hh, p.dm_g, p.ds_g) * p.vs_h + col, p.vs_r, k1 - k0, f);
+  prompt_add_nonfinite_row(p.v + static_cast<long long>(k_base + k0) * p.vs_r + fast_div(head, p.dm_g, p.ds_g) * p.vs_h + col,
+                           p.vs_r, k1 - k0, f);
 #pragma unroll
   for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(f[i]);
 }
@@ -351,15 +381,16 @@ __device__ __forceinline__ void prompt_add_nonfinite(const FwdParams& p, const I
 //
 // kPrompt (attn_fwd_prompt): K and V have fewer heads, each shared by a group of query heads, and what
 // a row does not see must not reach it, whatever it holds.  Scores are masked; but 0 * NaN is NaN, so
-// in every block that some row of the tile sees in part (a sequence's end, the diagonal) an eighth
-// warp zeroes V's rows past the end, which belong to somebody else, and the infinities and NaN among
-// the others; rows that do see those get them added in the epilogue.
+// in every block that some row of the tile sees in part (a sequence's end, the diagonal) the softmax
+// warps, before they hand P over, zero V's rows past the end, which belong to somebody else, and the
+// infinities and NaN among the others; rows that do see those get them added in the epilogue.  (An
+// eighth warp for it took 15000 cycles a tile, beside busy warps: 2048 tokens 73 us against 46.)
 template <int D, bool kStates, int kSoftPairs, bool kPacked, int BN = kBN, bool kPrompt = false>
-__global__ void __launch_bounds__(kPrompt ? kPromptThreads : kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 1)
     attn_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
                     const FwdParams p) {
-  using C = FwdCfg<D, BN, kPrompt>;
+  using C = FwdCfg<D, BN>;
   constexpr int kBN = BN;           // keys per block of this instantiation
   constexpr int kSBufs = C::kSBufs;
   extern __shared__ uint8_t smem_raw[];
@@ -381,11 +412,9 @@ __global__ void __launch_bounds__(kPrompt ? kPromptThreads : kThreads, 1)
   // p_full[b]: the softmax warps have written P_g (and rescaled o~) for g % 3 == b
   auto bar_p_full = [&](int b) { return bar0 + 8u * (3 + 4 * C::kStages + 2 * kSBufs + b); };
   auto bar_drain = [&](int i) { return bar0 + 8u * (3 + 4 * C::kStages + 3 * kSBufs + i); };
-  // prompts: a V block that some row sees in part has been repaired
-  auto bar_v_fixed = [&](int s) { return bar0 + 8u * (3 + 4 * C::kStages + 3 * kSBufs + 2 + s); };
-  // prompts: tag[u % 8] = u + 1 (a byte) once tile u of this CTA has met an infinity or NaN in such a
-  // block; the repair is at most kStages tiles ahead of the epilogue that asks.  (A tag left from 256
-  // tiles ago makes the epilogue look once more, and find nothing.)
+  // prompts: tag[u % 8] = u + 1 (a byte) once tile u of this CTA has met an infinity or NaN in a block
+  // that some row sees in part.  (A tag left from 256 tiles ago makes the epilogue look once more, and
+  // find nothing.)
   volatile uint8_t* tag = smem + C::kOffMisc + 8;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + C::kOffMisc + 4);
@@ -403,10 +432,7 @@ __global__ void __launch_bounds__(kPrompt ? kPromptThreads : kThreads, 1)
       mbar_init(bar_k_full(s), 1);
       mbar_init(bar_v_full(s), 1);
       mbar_init(bar_k_free(s), 1);
-      // prompts: the repair hands every V block back too, ragged or not, so that a warp that waits by
-      // parity is never passed by two turns of the ring
-      mbar_init(bar_v_free(s), kPrompt ? 2 : 1);
-      if constexpr (kPrompt) mbar_init(bar_v_fixed(s), 1);
+      mbar_init(bar_v_free(s), 1);
     }
     for (int i = 0; i < kSBufs; ++i) {
       mbar_init(bar_s_full(i), 1);
@@ -549,7 +575,6 @@ __global__ void __launch_bounds__(kPrompt ? kPromptThreads : kThreads, 1)
         }
       } else {
         const uint32_t vlo = (sV >> 4) | (static_cast<uint32_t>(C::kSubBytesKV >> 4) << 16);
-        uint32_t fixed_par = 0;  // prompts: parity each v_fixed completes next
         for (int ri = 0; ok; ++ri) {
           const int item = item_of(ri, cta, G);
           if (item >= p.num_items) break;
@@ -561,14 +586,8 @@ __global__ void __launch_bounds__(kPrompt ? kPromptThreads : kThreads, 1)
           for (int j = 0; ok && j < it.nblk; ++j, ++g) {
             const int st = g % C::kStages;
             // V_g has normally landed long before P_g is ready: check it first
-            ok = mbar_wait(bar_v_full(st), (g / C::kStages) & 1, wc, 7);
-            if constexpr (kPrompt) {
-              if (ok && (it.jb0 + j + 1) * kBN > it.min_limit) {
-                ok = mbar_wait(bar_v_fixed(st), (fixed_par >> st) & 1u, wc, 14);
-                fixed_par ^= 1u << st;
-              }
-            }
-            ok = ok && mbar_wait_poll(bar_p_full(g % kSBufs), (g / kSBufs) & 1, wc, 6);
+            ok = mbar_wait(bar_v_full(st), (g / C::kStages) & 1, wc, 7) &&
+                 mbar_wait_poll(bar_p_full(g % kSBufs), (g / kSBufs) & 1, wc, 6);
             if (!ok) break;
             tc_fence_after();
             // o~ += P_g V_g: 8 k-steps of 16 keys; A = P_g from tensor memory, B = V_g MN-major
@@ -591,46 +610,6 @@ __global__ void __launch_bounds__(kPrompt ? kPromptThreads : kThreads, 1)
       // normal run they have: the softmax warps consumed them)
       mma_commit(bar_drain(warp == kWarpS));
       mbar_wait_drain(bar_drain(warp == kWarpS), 0, p.timeout_ns);
-    }
-  } else if (kPrompt && warp == kWarpFix) {
-    // ================================================================ ragged blocks of V (prompts)
-    int g = 0, u = 0;  // key blocks over all items, items with work
-    bool ok = true;
-    for (int ri = 0; ok; ++ri) {
-      const int item = item_of(ri, cta, G);
-      if (item >= p.num_items) break;
-      const Item it = decode<kPacked, kBN>(p, item, seq_perm);
-      if (it.nblk == 0) continue;
-      for (int j = 0; j < it.nblk; ++j, ++g) {
-        const int st = g % C::kStages, kb = (it.jb0 + j) * kBN;
-        ok = __all_sync(0xffffffffu, mbar_wait(bar_v_full(st), (g / C::kStages) & 1, wc, 15));
-        if (!ok) break;
-        if (kb + kBN > it.min_limit) {
-          bool odd = false;
-          const int r0 = max(0, it.min_limit - kb);  // rows before it are seen by every row of the tile
-          for (int i = r0 * (D / 8) + lane; i < kBN * (D / 8); i += 32) {
-            const int r = i / (D / 8), ch = i % (D / 8);
-            uint4* at = reinterpret_cast<uint4*>(smem + C::kOffV + st * C::kKVBytes + (ch / 8) * C::kSubBytesKV + r * 128 +
-                                                 (((ch & 7) ^ (r & 7)) << 4));
-            if (kb + r >= it.kv_len) {
-              *at = make_uint4(0, 0, 0, 0);
-            } else {
-              const uint4 v = *at;
-              if (any_nonfinite(v.x) || any_nonfinite(v.y) || any_nonfinite(v.z) || any_nonfinite(v.w)) {
-                *at = make_uint4(finite_only(v.x), finite_only(v.y), finite_only(v.z), finite_only(v.w));
-                odd = true;
-              }
-            }
-          }
-          if (odd) tag[u & 7] = static_cast<uint8_t>(u + 1);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar_v_fixed(st));
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar_v_free(st));
-      }
-      ++u;
     }
   } else {
     // ================================================================ softmax / epilogue
@@ -736,6 +715,14 @@ __global__ void __launch_bounds__(kPrompt ? kPromptThreads : kThreads, 1)
         const float2 acc = __fadd2_rn(acc0, acc1);
         l = l * alpha + (acc.x + acc.y);
         m = m_new;
+        if constexpr (kPrompt) {
+          if (kb + kBN > it.min_limit) {  // V's row r of this block
+            ok = __all_sync(0xffffffffu, mbar_wait(bar_v_full(gj % C::kStages), (gj / C::kStages) & 1, wc, 14));
+            if (!ok) break;
+            if (repair_v_row<D, C::kSubBytesKV>(smem + C::kOffV + (gj % C::kStages) * C::kKVBytes, r, kb + r >= it.kv_len))
+              tag[u & 7] = static_cast<uint8_t>(u + 1);
+          }
+        }
         if (j > 0 && !__all_sync(0xffffffffu, alpha == 1.f)) {
           // o~ may be touched only after the previous P V product has landed in it
           if (!__all_sync(0xffffffffu, pv_seen))
@@ -806,7 +793,7 @@ __global__ void __launch_bounds__(kPrompt ? kPromptThreads : kThreads, 1)
           tmem_ld32(tl + C::kColO + q * 32, o);
           tmem_wait_ld();
           if constexpr (kPrompt) {
-            if (odd && store) prompt_add_nonfinite(p, it, odd0, limit, q * 32, o);
+            if (odd && store) prompt_add_nonfinite(p, it.k_base, it.hh, odd0, limit, q * 32, o);
           }
 #pragma unroll
           for (int ch = 0; ch < 4; ++ch) {
@@ -894,7 +881,7 @@ __global__ void __launch_bounds__(kPrompt ? kPromptThreads : kThreads, 1)
         if constexpr (kPrompt) {
           if (odd && store) {
 #pragma unroll
-            for (int q = 0; q < D / 32; ++q) prompt_add_nonfinite(p, it, odd0, limit, q * 32, o + q * 32);
+            for (int q = 0; q < D / 32; ++q) prompt_add_nonfinite(p, it.k_base, it.hh, odd0, limit, q * 32, o + q * 32);
           }
         }
 #pragma unroll

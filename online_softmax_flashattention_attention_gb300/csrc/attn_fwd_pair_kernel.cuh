@@ -145,7 +145,11 @@ __device__ __forceinline__ PairItem decode_pair(const FwdParams& p, int item, co
 // completed (a tile's previous product is two places back, and tcgen05 commits of one
 // thread complete in order), and the phase after it needs an arrival that comes after the
 // wait.
-template <int kSoftPairs, bool kPacked>
+//
+// kPrompt: as in attn_fwd_kernel.  A block of V that tile 0 sees in part is repaired by tile 0's warps,
+// before its product, which comes before tile 1's with that block; tile 1's warps repair the blocks that
+// tile 0 lacks.  What tile 0 zeroed in a block that tile 1 sees whole is added to tile 1's rows too.
+template <int kSoftPairs, bool kPacked, bool kPrompt = false>
 __global__ void __launch_bounds__(kPairThreads, 1)
     attn_fwd_pair_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                          const __grid_constant__ CUtensorMap tmV, const FwdParams p) {
@@ -167,6 +171,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   auto bar_drain = [&](int i) { return bar0 + 8u * (4 + 2 * C::kSlots + 3 * kPairSBufs + i); };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + C::kOffMisc + 4);
+  volatile uint8_t* tag = smem + C::kOffMisc + 8;  // prompts: as in attn_fwd_kernel, for pairs of tiles
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -191,6 +196,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       mbar_init(bar_drain(t), 1);
     }
     *abort_flag = 0u;
+    if constexpr (kPrompt) {
+      for (int i = 0; i < 8; ++i) tag[i] = 0;
+    }
     fence_mbar_init();
   }
   if (warp == kPairWarpPv) tmem_alloc<kTmemCols>(smem_u32(tmem_slot));
@@ -229,6 +237,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         if (item >= p.num_items) break;
         const PairItem it = decode_pair<kPacked>(p, item, seq_perm);
         if (it.nmax == 0) continue;
+        const int hkv = kPrompt ? fast_div(it.hh, p.dm_g, p.ds_g) : it.hh;
         // the previous pair's Q tiles must have been read by its last S product
         if (kq > 0 && !__all_sync(0xffffffffu, mbar_wait(bar_q_free, (kq - 1) & 1, wc, 13))) break;
         mbar_arrive_expect_tx_elect(bar_q_full, ((it.nblk[0] > 0) + (it.nblk[1] > 0)) * C::kTileBytes);
@@ -251,7 +260,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             if (kv == 1 || j != p.fault_block) {
               mbar_arrive_expect_tx_elect(bar_full(slot), C::kTileBytes);
               tma_load_4d_elect(sRing + slot * C::kTileBytes, kv ? &tmV : &tmK, bar_full(slot), 0,
-                                it.k_base + j * kBN, it.hh, it.bcoord, pol_kv);
+                                it.k_base + j * kBN, hkv, it.bcoord, pol_kv);
               live |= bit;
               par = (par & ~bit) | (static_cast<uint32_t>((e / C::kSlots) & 1) << slot);
             }
@@ -365,6 +374,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     const float c = p.c;
     int qn = 0;  // products of the pairs before this one
     int nd = 0;  // pairs so far in which this tile had blocks: phase of o_done[t]
+    int u = 0;   // prompts: pairs with work
     bool ok = true;
     for (int ri = 0; ok; ++ri) {
       const int item = item_of(ri, cta, G);
@@ -472,6 +482,16 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         const float2 acc = __fadd2_rn(acc0, acc1);
         l = l * alpha + (acc.x + acc.y);
         m = m_new;
+        if constexpr (kPrompt) {
+          const bool other = t && j < it.nblk[0] && kb + kBN > it.min_limit[0];  // tile 0's to repair
+          if (kb + kBN > t_min_limit && !other) {
+            const int e = (qbase >> 1) * 2 + 2 * j + 1;  // V_j's ring entry: two entries and two products a block
+            ok = __all_sync(0xffffffffu, mbar_wait(bar_full(e % C::kSlots), (e / C::kSlots) & 1, wc, 14));
+            if (!ok) break;
+            if (repair_v_row<64, 0>(smem + C::kOffRing + (e % C::kSlots) * C::kTileBytes, r, kb + r >= it.kv_len))
+              tag[u & 7] = static_cast<uint8_t>(u + 1);
+          }
+        }
         if (j > 0 && !__all_sync(0xffffffffu, alpha == 1.f)) {
           // o~_t may be touched only after the tile's previous P V product has landed in it
           if (!__all_sync(0xffffffffu, pv_seen))
@@ -497,6 +517,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(bar_p_full(b));
       }
+      const int ui = u;
+      if (kPrompt && it.nmax > 0) ++u;
       if (!t_valid) continue;  // a tile past the end of its sequence: no rows
       // ---- epilogue: one division by l; O and LSE out, straight from registers
       if (ok && nblk > 0) {
@@ -507,6 +529,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       }
       if (!ok) break;
       const bool store = row < it.Nq;
+      const bool odd = kPrompt && nblk > 0 && tag[ui & 7] == static_cast<uint8_t>(ui + 1);
       const float inv = l > 0.f ? 1.f / l : 0.f;
       uint4* dst = reinterpret_cast<uint4*>(p.o + it.b * p.os_b + it.hh * p.os_h +
                                             (it.q_base + (store ? row : 0)) * p.os_r);
@@ -519,6 +542,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         } else {
 #pragma unroll
           for (int x = 0; x < 32; ++x) o[x] = 0u;
+        }
+        if constexpr (kPrompt) {
+          if (odd && store)
+            prompt_add_nonfinite(p, it.k_base, it.hh, (it.nblk[0] > 0 ? it.min_limit[0] : t_min_limit) / kBN * kBN, limit, x4 * 32, o);
         }
         if (store) {
 #pragma unroll
@@ -533,7 +560,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         }
       }
       if (store) {
-        const float lse = l > 0.f ? (m + __log2f(l)) * 0.69314718055994531f : -INFINITY;
+        const float lse = l > 0.f || (kPrompt && l != l) ? (m + __log2f(l)) * 0.69314718055994531f : -INFINITY;
         // [B, H, Nq], or [H, total_q] for packed sequences
         const size_t li = p.cu_q ? static_cast<size_t>(it.hh) * p.total_q + it.q_base + row
                                  : static_cast<size_t>(it.bh) * p.Nq + row;

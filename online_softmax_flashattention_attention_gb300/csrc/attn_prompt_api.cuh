@@ -45,15 +45,19 @@ void fix_strides(const int64_t* s, int rows, int heads, int d, long long* row, l
   *row = rows > 1 ? s[0] : static_cast<long long>(heads) * d;
 }
 
-template <int D>
+// kPair: d = 64, two query tiles a CTA (attn_fwd_pair_kernel).
+template <int D, bool kPair>
 attn_status launch_prompt(const void* Q, const void* K, const void* V, void* O, float* LSE, int B, int Hq, int Hkv,
                           int max_q, float scale, int causal, cudaStream_t stream, int dev, uint32_t* status,
                           const Geometry& geo) {
   static bool attr_set[kMaxDevices] = {};
-  using C = attn::FwdCfg<D, attn::kBN, true>;
-  auto kernel = attn::attn_fwd_kernel<D, false, 0, true, attn::kBN, true>;
+  using C = std::conditional_t<kPair, attn::PairCfg, attn::FwdCfg<D>>;
   attn_status st;
-  if ((st = set_smem_attr(kernel, C::kSmemAlloc, dev, attr_set)) != ATTN_OK) return st;
+  if constexpr (kPair)
+    st = set_smem_attr(attn::attn_fwd_pair_kernel<0, true, true>, C::kSmemAlloc, dev, attr_set);
+  else
+    st = set_smem_attr(attn::attn_fwd_kernel<D, false, 0, true, attn::kBN, true>, C::kSmemAlloc, dev, attr_set);
+  if (st != ATTN_OK) return st;
   CUtensorMap mq, mk, mv, mo;
   attn::FwdParams p;
   Geometry no_keys = geo;
@@ -70,10 +74,19 @@ attn_status launch_prompt(const void* Q, const void* K, const void* V, void* O, 
   p.vs_r = geo.vs[2];
   p.vs_h = geo.vs[1];
   divisor(Hq / Hkv, &p.dm_g, &p.ds_g);
+  if (kPair) {
+    p.num_items = static_cast<int>(static_cast<long long>((p.num_qtiles + 1) / 2) * p.BH);
+    p.order_div = (p.num_qtiles + 1) / 2;
+  }
   set_divisors(&p);
   const unsigned grid = static_cast<unsigned>(std::min(p.num_items, sm_count(dev)));
   const int smem = p.seq_sort ? C::kSmemAlloc : C::kSmemAllocNoPerm;
-  cudaError_t e = launch_pdl(kernel, grid, attn::kPromptThreads, smem, stream, mq, mk, mv, mo, p);
+  cudaError_t e;
+  if constexpr (kPair)
+    e = launch_pdl(attn::attn_fwd_pair_kernel<0, true, true>, grid, attn::kPairThreads, smem, stream, mq, mk, mv, p);
+  else
+    e = launch_pdl(attn::attn_fwd_kernel<D, false, 0, true, attn::kBN, true>, grid, attn::kThreads, smem, stream, mq, mk,
+                   mv, mo, p);
   if (e != cudaSuccess) return fail(ATTN_ERR_LAUNCH, "kernel launch: %s", cudaGetErrorString(e));
   return ATTN_OK;
 }
@@ -190,9 +203,11 @@ attn_status attn_qk_rotate(const void* Q, const void* K, void* Q_out, void* K_ou
   // A block takes all heads of its tokens, so that their angles are computed once, unless that
   // leaves SMs idle; then as few as it has in flight.
   const unsigned blocks = (static_cast<unsigned>(total) + attn::kRotTokens - 1) / attn::kRotTokens;
+  const unsigned full = 4u * static_cast<unsigned>(sm_count(dev));  // blocks that run at once
   const int least = attn::kRotThreads / (d / 8) / attn::kRotTokens * attn::kRotUnroll;
-  p.heads_per_block = blocks >= static_cast<unsigned>(2 * sm_count(dev)) ? p.H : least;
-  const dim3 grid(blocks, static_cast<unsigned>((p.H + p.heads_per_block - 1) / p.heads_per_block));
+  p.heads_per_block = 2 * blocks >= full ? p.H : least;
+  const unsigned parts = static_cast<unsigned>((p.H + p.heads_per_block - 1) / p.heads_per_block);
+  const dim3 grid(parts == 1 ? std::min(blocks, full) : blocks, parts);
   cudaError_t e = launch_pdl2(d == 128 ? attn::attn_qk_rotate_kernel<128> : attn::attn_qk_rotate_kernel<64>, grid,
                               attn::kRotThreads, 0, static_cast<cudaStream_t>(stream), p);
   if (e != cudaSuccess) return fail(ATTN_ERR_LAUNCH, "rotate kernel launch: %s", cudaGetErrorString(e));
@@ -252,8 +267,10 @@ attn_status attn_fwd_prompt(const void* Q, const void* K, const void* V, void* O
   uint32_t* status = nullptr;
   if ((st = get_device(&dev)) != ATTN_OK || (st = setup(dev, &status)) != ATTN_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return d == 128 ? launch_prompt<128>(Q, K, V, O, LSE, B, Hq, Hkv, max_seqlen_q, scale, causal, s, dev, status, g)
-                  : launch_prompt<64>(Q, K, V, O, LSE, B, Hq, Hkv, max_seqlen_q, scale, causal, s, dev, status, g);
+  auto launch = d == 128                                     ? launch_prompt<128, false>
+                : use_pair_kernel(dev, B, Hq, g, causal) ? launch_prompt<64, true>
+                                                             : launch_prompt<64, false>;
+  return launch(Q, K, V, O, LSE, B, Hq, Hkv, max_seqlen_q, scale, causal, s, dev, status, g);
 }
 
 attn_status attn_cache_weigh(const void* Q, const float* LSE, const attn_cache* cache, const float* weights, float* out,

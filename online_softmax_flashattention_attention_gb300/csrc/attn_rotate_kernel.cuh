@@ -11,12 +11,16 @@
 // fraction without another rounding, at any position: the error is position * inv_freq * 2^-52 rad
 // at most, as a product of 64-bit floats has, and 2^-24 of it for what follows in fp32.
 //
-// A row is d / 8 lanes of 16 bytes: both halves of a half-split pair lie at the same place in two
-// lanes, so a partner's eight values are four shuffles away.  Rows share their factors: with
-// A_i = w_i cos t and B_i = +-w_partner sin t a row costs two products a value and one for its
-// norm.  A block owns kRotTokens tokens: its threads look up the positions and compute each of the
-// tokens' angles once, in shared memory, while the first rows are on their way; then each group of
-// lanes keeps A and B of one token in registers and walks the token's heads.
+// A row is d / 8 lanes, each with two pieces of four columns: half-split, a piece of the first half and
+// the one it turns with; so no value changes lanes, and a norm's sum is all that crosses them.  Rows
+// share their factors: with A_i = w_i cos t and B_i = +-w_partner sin t a row costs two products a
+// value and one for its norm.  A block owns kRotTokens tokens at a time: its threads look up the
+// positions and compute each of the tokens' angles once, in shared memory, while the first rows are on
+// their way; then each group of lanes keeps A and B of one token in registers and walks the token's
+// heads, Q's, then K's.  Blocks are persistent, so that the frequencies (64-bit floats, slow here) and
+// weights are made once a block.
+//
+// Bound: DRAM.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -74,130 +78,138 @@ __device__ __forceinline__ unsigned long long rotate_step(float freq) {
   return __double2ull_rn((turns - floor(turns)) * 18446744073709551616.0);
 }
 
-// Eight weights from column c on, 1 without any.
-__device__ __forceinline__ void rotate_weights(const void* w, int f32, int c, float* out) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) out[i] = 1.f;
-  if (!w) return;
-  if (f32) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) out[i] = __ldg(static_cast<const float*>(w) + c + i);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) out[i] = __bfloat162float(static_cast<const __nv_bfloat16*>(w)[c + i]);
-  }
-}
+struct RotRow {
+  uint2 a, b;  // the lane's two pieces of four columns
+};
 
 template <int D>
 __global__ void __launch_bounds__(kRotThreads, 4) attn_qk_rotate_kernel(const RotateParams p) {
   constexpr int kLanes = D / 8;
   constexpr int kGroups = kRotThreads / kLanes;
   constexpr int kPerTok = kGroups / kRotTokens;  // groups that share a token
+  constexpr int kU = kRotUnroll;
   __shared__ float2 turn[kRotTokens][D / 2];     // cos, sin
+  __shared__ unsigned long long step[D / 2];
+  __shared__ float weight[2][D];
   __shared__ long long at[kRotTokens];
   __shared__ int in[kRotTokens];
   griddep_wait();
   griddep_launch_dependents();
   const int group = threadIdx.x / kLanes, lane = threadIdx.x % kLanes;
-  const int tk = group / kPerTok, tok = blockIdx.x * kRotTokens + tk;
-  const int h0 = blockIdx.y * p.heads_per_block + group % kPerTok;
-  const int h1 = min(p.H, static_cast<int>(blockIdx.y + 1) * p.heads_per_block);
-  const bool row_here = tok < p.total;
-  uint4 x[kRotUnroll];
-  auto load = [&](int h) {
-#pragma unroll
-    for (int u = 0; u < kRotUnroll; ++u) {
-      const int hh = h + u * kPerTok, k = hh >= p.Hq;
-      if (row_here && hh < h1)
-        x[u] = *(reinterpret_cast<const uint4*>(p.src[k] + tok * p.src_t[k] + (hh - (k ? p.Hq : 0)) * p.src_h[k]) + lane);
-    }
-  };
-  load(h0);
-  if (threadIdx.x < kRotTokens) {
-    const int t = blockIdx.x * kRotTokens + threadIdx.x;
-    long long pos = 0;
-    in[threadIdx.x] = t < p.total && rotate_position(p, t, &pos);
-    at[threadIdx.x] = pos;
+  const int tk = group / kPerTok, sub = group % kPerTok;
+  const int r = p.num_freq;
+  // the lane's pieces: columns ca .. + 3 and cb .. + 3; which frequency the first of ca has, if it turns
+  int ca = 8 * lane, cb = 8 * lane + 4, fa = 4 * lane;
+  bool turned = 8 * lane < 2 * r;
+  if (!p.interleaved) {
+    turned = 4 * lane < r;
+    ca = turned ? 4 * lane : 2 * r + 8 * (lane - r / 4);
+    cb = turned ? ca + r : ca + 4;
+    fa = ca;
   }
-  __syncthreads();
-  for (int i = threadIdx.x; i < kRotTokens * p.num_freq; i += kRotThreads) {
-    const int t = i / p.num_freq, f = i - t * p.num_freq;
-    const unsigned long long frac = static_cast<unsigned long long>(at[t]) * rotate_step(__ldg(p.freq + f));
-    // half turns in [-1, 1)
-    const float half = static_cast<float>(static_cast<int>(frac >> 32)) * 4.656612873077393e-10f;  // 2^-31
-    float s, c;
-    sincospif(half, &s, &c);
-    if (!(fabsf(__ldg(p.freq + f)) < INFINITY)) s = c = NAN;
-    turn[t][f] = make_float2(c, s);
-  }
-  __syncthreads();
-  if (!row_here || !in[tk]) return;  // a whole group of lanes: shuffles below are among a group's lanes
-
+  const int head0 = blockIdx.y * p.heads_per_block, head1 = min(p.H, head0 + p.heads_per_block);
   const uint32_t mask = kLanes == 32 ? 0xffffffffu : ((1u << kLanes) - 1u) << (threadIdx.x & 31 & ~(kLanes - 1));
-  const int r8 = p.num_freq / 8;  // lanes of a half
-  const bool turned = lane < 2 * r8;
-  const bool second = !p.interleaved && lane >= r8;
-  const int partner = !turned || p.interleaved ? lane : second ? lane - r8 : lane + r8;
-  float A[8], Bf[8];
-  int have = -1;  // whose factors A and B are
-  for (int h = h0; h < h1; h += kRotUnroll * kPerTok) {
-    if (h != h0) load(h);
+  for (int i = threadIdx.x; i < 2 * D; i += kRotThreads) {
+    const void* w = p.weight[i / D];
+    weight[i / D][i % D] = !w ? 1.f : p.weight_f32 ? static_cast<const float*>(w)[i % D]
+                                                   : __bfloat162float(static_cast<const __nv_bfloat16*>(w)[i % D]);
+  }
+  if (threadIdx.x < r) step[threadIdx.x] = rotate_step(__ldg(p.freq + threadIdx.x));
+  for (int t0 = blockIdx.x * kRotTokens; t0 < p.total; t0 += gridDim.x * kRotTokens) {
+    const int tok = t0 + tk;
+    __syncthreads();  // the last tokens' angles have been used
+    if (threadIdx.x < kRotTokens) {
+      const int t = t0 + threadIdx.x;
+      long long pos = 0;
+      in[threadIdx.x] = t < p.total && rotate_position(p, t, &pos);
+      at[threadIdx.x] = pos;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < kRotTokens * r; i += kRotThreads) {
+      const int t = i / r, f = i - t * r;
+      const unsigned long long frac = static_cast<unsigned long long>(at[t]) * step[f];
+      // half turns in [-1, 1)
+      const float half = static_cast<float>(static_cast<int>(frac >> 32)) * 4.656612873077393e-10f;  // 2^-31
+      float s, c;
+      sincospif(half, &s, &c);
+      if (!(fabsf(__ldg(p.freq + f)) < INFINITY)) s = c = NAN;
+      turn[t][f] = make_float2(c, s);
+    }
+    __syncthreads();
+    if (tok >= p.total || !in[tk]) continue;  // a whole group of lanes
+
 #pragma unroll
-    for (int u = 0; u < kRotUnroll; ++u) {
-      const int hh = h + u * kPerTok, k = hh >= p.Hq;
-      if (hh >= h1) break;
-      if (k != have) {
-        have = k;
-        float wo[8], wp[8];
-        rotate_weights(p.weight[k], p.weight_f32, 8 * lane, wo);
-        rotate_weights(p.weight[k], p.weight_f32, 8 * partner, wp);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          A[i] = wo[i];
-          Bf[i] = 0.f;
-          if (turned) {
-            const float2 cs = turn[tk][p.interleaved ? 4 * lane + i / 2 : 8 * lane + i - (second ? p.num_freq : 0)];
-            const bool plus = p.interleaved ? (i & 1) : second;
-            A[i] = wo[i] * cs.x;
-            Bf[i] = (plus ? cs.y : -cs.y) * (p.interleaved ? wo[i ^ 1] : wp[i]);
-          }
-        }
-      }
-      const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-      float v[8], o[8];
+    for (int k = 0; k < 2; ++k) {  // Q's heads, then K's
+      const int h0 = max(head0 - (k ? p.Hq : 0), 0) + sub, h1 = min(head1 - (k ? p.Hq : 0), k ? p.H - p.Hq : p.Hq);
+      if (h0 >= h1) continue;
+      // out_a = A va + Ba other, out_b = B vb + Bb other (other: the column it turns with)
+      float wa[4], wb[4], Ac[4], Bc[4], As[4], Bs[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        v[2 * i] = bf16_lo(w[i]);
-        v[2 * i + 1] = bf16_hi(w[i]);
+        wa[i] = weight[k][ca + i];
+        wb[i] = weight[k][cb + i];
       }
-      float inv = 1.f;
-      if (p.weight[k]) {
-        float ss = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(v[i], v[i], ss);
-#pragma unroll
-        for (int s = kLanes / 2; s > 0; s >>= 1) ss += __shfl_xor_sync(mask, ss, s);
-        inv = rsqrtf(ss * (1.f / D) + p.eps);
-      }
-      if (p.interleaved) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = turned ? fmaf(v[i ^ 1], Bf[i], v[i] * A[i]) : v[i] * A[i];
-      } else {
-        uint32_t q[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) q[i] = __shfl_sync(mask, w[i], partner, kLanes);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float other = (i & 1) ? bf16_hi(q[i / 2]) : bf16_lo(q[i / 2]);
-          o[i] = turned ? fmaf(other, Bf[i], v[i] * A[i]) : v[i] * A[i];
+      for (int i = 0; i < 4; ++i) {
+        Ac[i] = wa[i];
+        Bc[i] = wb[i];
+        As[i] = Bs[i] = 0.f;
+        if (turned) {
+          const float2 x = turn[tk][p.interleaved ? fa + i / 2 : fa + i], y = p.interleaved ? turn[tk][fa + 2 + i / 2] : x;
+          Ac[i] *= x.x;
+          Bc[i] *= y.x;
+          As[i] = p.interleaved ? ((i & 1) ? x.y : -x.y) * wa[i ^ 1] : -x.y * wb[i];
+          Bs[i] = p.interleaved ? ((i & 1) ? y.y : -y.y) * wb[i ^ 1] : x.y * wa[i];
         }
       }
-      uint4 r;
-      r.x = pack_bf16x2(o[0] * inv, o[1] * inv);
-      r.y = pack_bf16x2(o[2] * inv, o[3] * inv);
-      r.z = pack_bf16x2(o[4] * inv, o[5] * inv);
-      r.w = pack_bf16x2(o[6] * inv, o[7] * inv);
-      *(reinterpret_cast<uint4*>(p.dst[k] + tok * p.dst_t[k] + (hh - (k ? p.Hq : 0)) * p.dst_h[k]) + lane) = r;
+      const bool norm = p.weight[k] != nullptr;
+      const __nv_bfloat16* src = p.src[k] + tok * p.src_t[k];
+      __nv_bfloat16* dst = p.dst[k] + tok * p.dst_t[k];
+      const long long sh = p.src_h[k], dh = p.dst_h[k];
+      for (int h = h0; h < h1; h += kU * kPerTok) {
+        RotRow x[kU];
+#pragma unroll
+        for (int u = 0; u < kU; ++u)
+          if (h + u * kPerTok < h1) {
+            const __nv_bfloat16* row = src + (h + u * kPerTok) * sh;
+            x[u].a = *reinterpret_cast<const uint2*>(row + ca);
+            x[u].b = *reinterpret_cast<const uint2*>(row + cb);
+          }
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+          if (h + u * kPerTok >= h1) break;
+          float2 va[2] = {make_float2(bf16_lo(x[u].a.x), bf16_hi(x[u].a.x)), make_float2(bf16_lo(x[u].a.y), bf16_hi(x[u].a.y))};
+          float2 vb[2] = {make_float2(bf16_lo(x[u].b.x), bf16_hi(x[u].b.x)), make_float2(bf16_lo(x[u].b.y), bf16_hi(x[u].b.y))};
+          float inv = 1.f;
+          if (norm) {
+            float2 ss = __fmul2_rn(va[0], va[0]);
+            ss = __ffma2_rn(va[1], va[1], ss);
+            ss = __ffma2_rn(vb[0], vb[0], ss);
+            ss = __ffma2_rn(vb[1], vb[1], ss);
+            float sum = ss.x + ss.y;
+#pragma unroll
+            for (int o = kLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(mask, sum, o);
+            inv = rsqrtf(sum * (1.f / D) + p.eps);
+          }
+          float2 oa[2], ob[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            oa[i] = __fmul2_rn(va[i], make_float2(Ac[2 * i], Ac[2 * i + 1]));
+            ob[i] = __fmul2_rn(vb[i], make_float2(Bc[2 * i], Bc[2 * i + 1]));
+            if (turned) {
+              const float2 other_a = p.interleaved ? make_float2(va[i].y, va[i].x) : vb[i];
+              const float2 other_b = p.interleaved ? make_float2(vb[i].y, vb[i].x) : va[i];
+              oa[i] = __ffma2_rn(other_a, make_float2(As[2 * i], As[2 * i + 1]), oa[i]);
+              ob[i] = __ffma2_rn(other_b, make_float2(Bs[2 * i], Bs[2 * i + 1]), ob[i]);
+            }
+            oa[i] = __fmul2_rn(oa[i], make_float2(inv, inv));
+            ob[i] = __fmul2_rn(ob[i], make_float2(inv, inv));
+          }
+          __nv_bfloat16* row = dst + (h + u * kPerTok) * dh;
+          *reinterpret_cast<uint2*>(row + ca) = make_uint2(pack_bf16x2(oa[0].x, oa[0].y), pack_bf16x2(oa[1].x, oa[1].y));
+          *reinterpret_cast<uint2*>(row + cb) = make_uint2(pack_bf16x2(ob[0].x, ob[0].y), pack_bf16x2(ob[1].x, ob[1].y));
+        }
+      }
     }
   }
 }

@@ -50,6 +50,7 @@ namespace attn {
 constexpr int kWeighStep = 256;     // keys of a step: two blocks of 128
 constexpr int kWeighSteps = 4;      // steps of a unit with one tile, at most
 constexpr int kWeighCols = 128;     // query rows of a tile, at most
+constexpr int kWeighStacked = 64;   // e4m3, columns up to which a query's two terms are rows of one operand
 constexpr int kWeighGroups = 64;    // prefix-sum entries (each over ceil(B / 64) sequences)
 constexpr int kWeighJobs = 6;       // units announced in shared memory
 constexpr int kWeighFinders = 2;
@@ -528,68 +529,78 @@ __global__ void __launch_bounds__(WeighCfg<D, kF8>::kThreads, 1)
           if (!h) w.next(NWm);
           w.next(NWm);
         }
-        const int n = single ? t.steps : t.nq;
-        for (int j = 0; ok && j < n; ++j, ++g) {
-          const uint32_t bf = 2 * (g & 1) + h, dst = tmem + 128u * bf;
-          if (j == 0 || !single) ok = narrow ? tile_wait(bar_w_full(w.st), w.ph, wc, 68) : tile_wait(bar_q_full(q.st), q.ph, wc, 69);
-          if (narrow || (!kF8 && (single || j == 0))) {
-            ok = ok && tile_wait(bar_k_full(k.st), k.ph, wc, 66);
+        auto product = [&](uint32_t dst, uint32_t b, uint32_t idesc) {  // bf16
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks) {
+            const uint32_t off = (ks / 4) * (C::kSubBytes >> 4) + (ks % 4) * 2;
+            mma_ss(dst, desc(dhi, a + off), desc(dhi, b + off), idesc, ks > 0 ? 1u : 0u);
+          }
+          // the LSE last: everything before it is a sum of small terms
+          mma_ss(dst, weigh_step_desc(sbase + C::kOffOnes), weigh_step_desc(sbase + C::kOffStep + l.st * kWeighStepBytes), idesc, 1u);
+        };
+        const uint32_t cols = (weigh_cols(p, first, t.T, 0).n + 15) / 16 * 16;
+        if (single) {
+          ok = narrow ? tile_wait(bar_w_full(w.st), w.ph, wc, 68) : tile_wait(bar_q_full(q.st), q.ph, wc, 69);
+          const bool stacked = narrow && cols <= kWeighStacked;
+          const uint32_t idesc = narrow ? (1u << 4) | (((stacked ? 2 * cols : cols) >> 3) << 17) | (8u << 24)  // e4m3 x e4m3 -> fp32
+                                        : idesc_bf16_f32(128, cols, 0);
+          const uint32_t b = narrow ? wlo + w.st * (C::kTileBytes >> 4) : qlo + q.st * (C::kTileBytes >> 4);
+          for (int j = 0; ok && j < t.steps; ++j, ++g) {
+            const uint32_t bf = 2 * (g & 1) + h, dst = tmem + 128u * bf;
+            ok = tile_wait(bar_k_full(k.st), k.ph, wc, 66) && tile_wait(bar_s_free(bf), ((g >> 1) & 1) ^ 1, wc, 70);
+            if (!ok) break;
+            tc_fence_after();
             a = klo + k.st * (C::kStageK >> 4);
-          }
-          ok = ok && tile_wait(bar_s_free(bf), ((g >> 1) & 1) ^ 1, wc, 70);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t cols = (weigh_cols(p, first, t.T, single ? 0 : j).n + 15) / 16 * 16;
-          if (narrow) {
-            const uint32_t idesc = (1u << 4) | ((cols >> 3) << 17) | (8u << 24);  // e4m3 x e4m3 -> fp32
-            const uint32_t b = wlo + w.st * (C::kTileBytes >> 4);
+            if constexpr (kF8) {
 #pragma unroll
-            for (int part = 0; part < 2; ++part)  // hi, lo
+              for (int ks = 0; ks < D / 32; ++ks) mma_ss_f8(dst, desc(dhi8, a + ks * 2), desc(dhi8, b + ks * 2), idesc, ks > 0 ? 1u : 0u);
+              if (!stacked) {
 #pragma unroll
-              for (int ks = 0; ks < D / 32; ++ks)
-                mma_ss_f8(dst, desc(dhi8, a + ks * 2), desc(dhi8, b + part * (128 * D >> 4) + ks * 2), idesc, part + ks > 0 ? 1u : 0u);
-          } else {
-            const uint32_t idesc = idesc_bf16_f32(128, cols, 0);
-            const uint32_t b = qlo + q.st * (C::kTileBytes >> 4);
-#pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks) {
-              const uint32_t off = (ks / 4) * (C::kSubBytes >> 4) + (ks % 4) * 2;
-              mma_ss(dst, desc(dhi, a + off), desc(dhi, b + off), idesc, ks > 0 ? 1u : 0u);
+                for (int ks = 0; ks < D / 32; ++ks) mma_ss_f8(dst, desc(dhi8, a + ks * 2), desc(dhi8, b + (128 * D >> 4) + ks * 2), idesc, 1u);
+              }
+            } else {
+              product(dst, b, idesc);
             }
-            // the LSE last: everything before it is a sum of small terms
-            mma_ss(dst, weigh_step_desc(sbase + C::kOffOnes), weigh_step_desc(sbase + C::kOffStep + l.st * kWeighStepBytes), idesc, 1u);
-          }
-          mma_commit(bar_s_full(bf));
-          if (single) {
+            mma_commit(bar_s_full(bf));
             mma_commit(bar_k_free(k.st));
             k.next(p.ring_k);
             k.next(p.ring_k);
-          } else {
-            mma_commit(bar_q_free(q.st));
-            q.next(p.ring_q);
-            l.next(C::kLse);
           }
-        }
-        if (ok) {
           if (narrow) {
-            mbar_arrive(bar_q_free(q.st));  // its rows had been read when their two terms came
+            if (ok) mbar_arrive(bar_q_free(q.st));  // its rows had been read when their two terms came
             mma_commit(bar_w_free(w.st));
             w.next(NWm);
-          } else if (single) {
+          } else {
             mma_commit(bar_q_free(q.st));
-          } else if (kF8) {  // nobody but this issuer had the stage
+          }
+          q.next(p.ring_q);
+          l.next(C::kLse);
+        } else {
+          if constexpr (!kF8) {
+            ok = tile_wait(bar_k_full(k.st), k.ph, wc, 66);
+            a = klo + k.st * (C::kStageK >> 4);
+          }
+          for (int j = 0; ok && j < t.nq; ++j, ++g) {
+            const uint32_t bf = 2 * (g & 1) + h;
+            ok = tile_wait(bar_q_full(q.st), q.ph, wc, 69) && tile_wait(bar_s_free(bf), ((g >> 1) & 1) ^ 1, wc, 70);
+            if (!ok) break;
+            tc_fence_after();
+            // all tiles but the last have the first one's columns (a group of more than 128 heads aside)
+            const uint32_t n = j + 1 < t.nq && p.heads == p.G ? cols : (weigh_cols(p, first, t.T, j).n + 15) / 16 * 16;
+            product(tmem + 128u * bf, qlo + q.st * (C::kTileBytes >> 4), idesc_bf16_f32(128, n, 0));
+            mma_commit(bar_s_full(bf));
+            mma_commit(bar_q_free(q.st));
+            q.next(p.ring_q);
+            l.next(C::kLse);
+          }
+          if constexpr (kF8) {  // nobody but this issuer had the stage
             mma_commit(bar_w_free(wst));
             mma_commit(bar_w_free(wst));
           } else {
             mma_commit(bar_k_free(k.st));
           }
-          if (single) {
-            q.next(p.ring_q);
-            l.next(C::kLse);
-          } else {
-            k.next(p.ring_k);
-            k.next(p.ring_k);
-          }
+          k.next(p.ring_k);
+          k.next(p.ring_k);
         }
       }
       ok = __shfl_sync(0xffffffffu, static_cast<int>(ok), 0) != 0;
@@ -611,36 +622,47 @@ __global__ void __launch_bounds__(WeighCfg<D, kF8>::kThreads, 1)
       q.next(p.ring_q);
       l.next(C::kLse);
     }
+    // this lane's columns, four of them: token of the tile and the way to their head's LSE from the first's
+    int tok[4];
+    long long off[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      tok[i] = (32 * i + lane) / p.heads;
+      off[i] = static_cast<long long>(32 * i + lane - tok[i] * p.heads) * p.total_q + tok[i];
+    }
+    float next[4];
     while (job(t, ok, 71)) {
       const int first = t.first();
-      for (int j = (par ^ g) & 1; j < t.nq; j += 2) {
+      auto load = [&](int j) {
         const WeighCols c = weigh_cols(p, first, t.T, j);
-        float v[4];
-        bool none = false;
+        const float* from = p.lse + static_cast<long long>(t.h * p.G + c.head) * p.total_q + t.q0 + c.tok;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int col = 32 * i + lane;
-          v[i] = -INFINITY;
-          if (col < c.n) {
-            const int tok = col / p.heads, head = c.head + col - tok * p.heads;
-            v[i] = -1.4426950408889634f * __ldg(p.lse + static_cast<long long>(t.h * p.G + head) * p.total_q + t.q0 + c.tok + tok);
-            if (v[i] == INFINITY) v[i] = -INFINITY;  // a row that saw nothing: exp2(-inf)
-            none |= v[i] == -INFINITY;
-          }
-        }
+        for (int i = 0; i < 4; ++i) next[i] = 32 * i + lane < c.n ? __ldg(from + off[i]) : -INFINITY;
+      };
+      const int j0 = (par ^ g) & 1;
+      if (j0 < t.nq) load(j0);
+      for (int j = j0; j < t.nq; j += 2) {
+        float v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = next[i];
+        if (j + 2 < t.nq) load(j + 2);
         // every group is done with the tile that had this place (a lane looks after one), and the stage of
         // its rows has been freed: what arrives there sooner would count for the tile before it
         ok = __all_sync(0xffffffffu, tile_wait(bar_lse_free(l.st, lane & 3), l.ph ^ 1u, wc, 72) &&
                                          tile_wait(bar_q_free(q.st), q.ph ^ 1u, wc, 72));
         if (!ok) break;
+        bool none = false;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          reinterpret_cast<float*>(smem + C::kOffLse)[l.st * 128 + 32 * i + lane] = v[i];
-          // three bf16 terms of -LSE / scale, each the rounding of what the ones before leave
-          const float x = v[i] == -INFINITY ? 0.f : v[i] * (p.rscale * 0.69314718055994531f);
-          const float t1 = __bfloat162float(__float2bfloat16_rn(x)), t2 = __bfloat162float(__float2bfloat16_rn(x - t1));
+          const bool out = fabsf(v[i]) == INFINITY;  // a row that saw nothing, or none: exp2(-inf)
+          none |= out && (v[i] > 0.f || 32 * i + lane < p.tokens * p.heads);
+          reinterpret_cast<float*>(smem + C::kOffLse)[l.st * 128 + 32 * i + lane] = out ? -INFINITY : -1.4426950408889634f * v[i];
+          // -LSE / scale as three bf16 terms, exact: eight of its bits each
+          const float x = out ? 0.f : -p.rscale * v[i];
+          const float t1 = __uint_as_float(__float_as_uint(x) & 0xffff0000u), t23 = x - t1;
+          const float t2 = __uint_as_float(__float_as_uint(t23) & 0xffff0000u);
           *reinterpret_cast<uint4*>(smem + C::kOffStep + l.st * kWeighStepBytes + weigh_step_row(32 * i + lane)) =
-              make_uint4(pack_bf16x2(t1, t2), pack_bf16x2(x - t1 - t2, 0.f), 0u, 0u);
+              make_uint4(__byte_perm(__float_as_uint(t1), __float_as_uint(t2), 0x7632), __float_as_uint(t23 - t2) >> 16, 0u, 0u);
         }
         none = __any_sync(0xffffffffu, none);
         if (lane == 0) odd[l.st] = none;
@@ -742,13 +764,19 @@ __global__ void __launch_bounds__(WeighCfg<D, kF8>::kThreads, 1)
         } else {
           const float4* nl = reinterpret_cast<const float4*>(smem + C::kOffLse) + l.st * 32;
           const float4* fac = reinterpret_cast<const float4*>(smem + C::kOffFactor) + (u % kWeighFactors) * 32;
+          const int lo = narrow && c.n <= kWeighStacked ? (c.n + 15) / 16 * 16 : 0;  // where the second terms' products are
           float key_scale = 1.f;
           if (narrow) key_scale = scale_of(max(static_cast<uint32_t>(smem[C::kOffCode + ((x + 2 * j + blk) % kWeighCodes) * 128 + r]), 1u));
 #pragma unroll 1
           for (int q = 0; q < c.n; q += 8) {
-            uint32_t s[8];
+            uint32_t s[8], s2[8];
             tmem_ld8(ts + q, s);
+            if (lo) tmem_ld8(ts + lo + q, s2);
             tmem_wait_ld();
+            if (lo) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) s[i] = __float_as_uint(__uint_as_float(s[i]) + __uint_as_float(s2[i]));
+            }
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
               const int col = q + 4 * k;
@@ -819,6 +847,7 @@ __global__ void __launch_bounds__(WeighCfg<D, kF8>::kThreads, 1)
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           const int rows = weigh_cols(p, first, t.T, 0).n, ch = lane % kL;
+          const bool stacked = rows <= kWeighStacked;  // the second terms are rows after the first ones, or a tile
           const uint8_t* src = smem + q.st * C::kTileBytes;
           uint8_t* dst = smem + C::kOffWide + w.st * C::kTileBytes;
           float* fac = reinterpret_cast<float*>(smem + C::kOffFactor) + (u % kWeighFactors) * 128;
@@ -846,10 +875,10 @@ __global__ void __launch_bounds__(WeighCfg<D, kF8>::kThreads, 1)
               hi[i] = h0 | (h1 << 16);
               lo[i] = pack_e4m3x2(f0 - b0.x, f1 - b0.y) | (pack_e4m3x2(f2 - b1.x, f3 - b1.y) << 16);
             }
-            const int sx = D == 128 ? (ch >> 1) ^ (qr & 7) : (ch >> 1) ^ ((qr >> 1) & 3);
+            const int sx = D == 128 ? (ch >> 1) ^ (qr & 7) : (ch >> 1) ^ ((qr >> 1) & 3);  // (rows 16 apart alike)
             uint8_t* to = dst + qr * D + (sx << 4) + (ch & 1) * 8;
             *reinterpret_cast<uint2*>(to) = make_uint2(hi[0], hi[1]);
-            *reinterpret_cast<uint2*>(to + 128 * D) = make_uint2(lo[0], lo[1]);
+            *reinterpret_cast<uint2*>(to + (stacked ? (rows + 15) / 16 * 16 : 128) * D) = make_uint2(lo[0], lo[1]);
           }
           fence_proxy_async_smem();
           __syncwarp();

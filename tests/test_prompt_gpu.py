@@ -74,22 +74,25 @@ def test_against_definition(case, joint):
     hold_prompt(O, LSE, ref_prompt(f64(Q), f64(K), f64(V), cu_q, cu_k, scale, causal))
 
 
-@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("d,heads", [(64, 4), (128, 4), (64, 64)])  # the last: two query tiles a CTA
 @pytest.mark.parametrize("kind", ["nan", "inf", "both"])
-def test_values_that_are_not_finite_stay_with_who_sees_them(d, kind):
-    """Infinities and NaN in keys and values of later tokens and of other sequences."""
+@pytest.mark.parametrize("before", [0, 77])
+def test_values_that_are_not_finite_stay_with_who_sees_them(d, heads, kind, before):
+    """Infinities and NaN in keys and values of later tokens and of other sequences, diagonals in a block or across two."""
     rng = np.random.default_rng(12)
     nq = [260, 3, 129, 60]
     cu = _cu(nq)
-    Q, K, V = bf16(rng, (cu[-1], 4, d)), bf16(rng, (cu[-1], 2, d)), bf16(rng, (cu[-1], 2, d))
+    Q = bf16(rng, (cu[-1], heads, d))
+    cu_k = _cu([n + before for n in nq])
+    K, V = bf16(rng, (cu_k[-1], 2, d)), bf16(rng, (cu_k[-1], 2, d))
     bad = {"nan": [math.nan], "inf": [math.inf, -math.inf], "both": [math.nan, math.inf]}[kind]
     for i, row in enumerate((200, 259, 262, 263, 300, 390, 392, 440)):
         V[row, i % 2, 7 * i] = bad[i % len(bad)]
     K[255, 1] = math.nan
     K[391, 0] = math.nan
-    O, LSE = _run(Q, K, V, cu, cu, max(nq))
+    O, LSE = _run(Q, K, V, cu, cu_k, max(nq))
     with np.errstate(invalid="ignore"):
-        refs = ref_prompt(f64(Q), f64(K), f64(V), cu, cu, 1 / math.sqrt(d), True)
+        refs = ref_prompt(f64(Q), f64(K), f64(V), cu, cu_k, 1 / math.sqrt(d), True)
     hold_prompt(O, LSE, refs)
 
 

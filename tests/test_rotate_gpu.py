@@ -158,8 +158,10 @@ def test_offsets_past_32_bits():
     Q.copy_(src)
     f = torch.from_numpy(_freq(32)).cuda()
     want = pkg.attn_qk_rotate(src, src, None, f)
-    got = pkg.attn_qk_rotate(Q, Q, None, f, Q, None)
+    got = pkg.attn_qk_rotate(src, Q, None, f)  # read there
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    pkg.attn_qk_rotate(Q, src, None, f, Q, None)  # and written
+    assert torch.equal(Q, want[0])
 
 
 def test_streams():
