@@ -35,6 +35,7 @@ constexpr int kEvictWarps = kEvictThreads / 32;
 constexpr int kEvictBins = 2048;
 constexpr int kEvictBinBits = 11;
 constexpr int kEvictMaxKeys = 49152;  // keys a CTA holds in shared memory; further ones are read again
+constexpr int kEvictLoads = 8;        // weights a thread has in flight
 constexpr int kMoveThreads = 256;
 constexpr int kMoveUnroll = 4;
 
@@ -115,7 +116,6 @@ __global__ void __launch_bounds__(kEvictThreads) attn_evict_select_kernel(const 
   const int c0 = min(rank * seg, m), c1 = min(c0 + seg, m);
   auto read = [&](int c) {
     const long long r = evict_row(p, p.table, p.max_pages, b, h, p.sink + c);
-    if (r < 0 && p.page_word) atomicOr(p.page_word, 1u);
     return evict_key(r < 0 ? -INFINITY : p.w[r]);
   };
   auto key_at = [&](int c) { return c - c0 < p.key_cap ? keys[c - c0] : read(c); };
@@ -126,11 +126,26 @@ __global__ void __launch_bounds__(kEvictThreads) attn_evict_select_kernel(const 
   for (int i = tid; i < kEvictBins; i += kEvictThreads) hist[0][i] = hist[1][i] = 0;
   __syncthreads();
   uint32_t lo = 0xffffffffu, hi = 0u;
-  for (int c = c0 + tid; c < c1; c += kEvictThreads) {
-    const uint32_t key = read(c);
-    if (c - c0 < p.key_cap) keys[c - c0] = key;
-    lo = min(lo, key);
-    hi = max(hi, key);
+  // several at a time: a page is one load away, its weight another, some 2000 cycles together
+  for (int b0 = c0 + tid; b0 < c1; b0 += kEvictThreads * kEvictLoads) {
+    long long at[kEvictLoads];
+    uint32_t key[kEvictLoads];
+#pragma unroll
+    for (int i = 0; i < kEvictLoads; ++i) {
+      const int c = b0 + i * kEvictThreads;
+      at[i] = c < c1 ? evict_row(p, p.table, p.max_pages, b, h, p.sink + c) : -1;
+    }
+#pragma unroll
+    for (int i = 0; i < kEvictLoads; ++i) key[i] = evict_key(at[i] < 0 ? -INFINITY : p.w[at[i]]);
+#pragma unroll
+    for (int i = 0; i < kEvictLoads; ++i) {
+      const int c = b0 + i * kEvictThreads;
+      if (c >= c1) break;
+      if (at[i] < 0 && p.page_word) atomicOr(p.page_word, 1u);
+      if (c - c0 < p.key_cap) keys[c - c0] = key[i];
+      lo = min(lo, key[i]);
+      hi = max(hi, key[i]);
+    }
   }
   lo = __reduce_min_sync(0xffffffffu, lo);
   hi = __reduce_max_sync(0xffffffffu, hi);

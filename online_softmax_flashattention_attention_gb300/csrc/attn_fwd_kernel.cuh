@@ -321,20 +321,23 @@ template <int D, int kSubBytes>
 __device__ __forceinline__ bool repair_v_row(uint8_t* block, int r, bool past) {
   uint4* at = reinterpret_cast<uint4*>(block + r * 128);
   auto chunk = [&](int c) { return (c / 8) * (kSubBytes / 16) + ((c & 7) ^ (r & 7)); };
+  // (rolled: this runs once a tile, so its code is cold; unrolled it took thousands of cycles)
   if (past) {
-#pragma unroll
+#pragma unroll 1
     for (int c = 0; c < D / 8; ++c) at[chunk(c)] = make_uint4(0, 0, 0, 0);
     fence_proxy_async_smem();
     return false;
   }
   // v * 0 is NaN for what is not finite, and nothing else
-  __nv_bfloat162 acc = __floats2bfloat162_rn(0.f, 0.f);
+  const __nv_bfloat162 zero = __floats2bfloat162_rn(0.f, 0.f);
+  __nv_bfloat162 acc = zero;
+#pragma unroll 1
+  for (int c = 0; c < D / 8; c += 4) {
+    uint4 v[4];
 #pragma unroll
-  for (int c = 0; c < D / 8; ++c) {
-    const uint4 v = at[chunk(c)];
+    for (int i = 0; i < 4; ++i) v[i] = at[chunk(c + i)];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      acc = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&(&v.x)[i]), __floats2bfloat162_rn(0.f, 0.f), acc);
+    for (int i = 0; i < 16; ++i) acc = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&(&v[i / 4].x)[i % 4]), zero, acc);
   }
   const uint32_t bits = *reinterpret_cast<const uint32_t*>(&acc);
   if (!any_nonfinite(bits)) return false;
@@ -347,23 +350,27 @@ __device__ __forceinline__ bool repair_v_row(uint8_t* block, int r, bool past) {
   return true;
 }
 
-// Prompts: the infinities and NaN of values that went into the product as zero, to a row that sees
-// keys [k0, k1) of them: columns col .. col + 31 of its o~ (a positive weight leaves them what they are).
-__device__ __noinline__ void prompt_add_nonfinite_row(const __nv_bfloat16* v, long long stride, int keys, float* o) {
-  for (int k = 0; k < keys; ++k)
-    for (int i = 0; i < 32; ++i) {
-      const float x = __bfloat162float(v[k * stride + i]);
-      if (!(fabsf(x) < INFINITY)) o[i] += x;
-    }
+// Prompts: the infinities and NaN of values that went into the product as zero, to a row of o~ (d columns
+// of tensor memory from taddr on) that sees keys [0, keys) of the rows at v: a positive weight leaves
+// them what they are.  Warp-wide, rows without keys too.
+__device__ __noinline__ void prompt_add_nonfinite(uint32_t taddr, int d, const __nv_bfloat16* v, long long stride, int keys) {
+  for (int q = 0; q < d; q += 32) {
+    uint32_t o[32];
+    tmem_ld32(taddr + q, o);
+    tmem_wait_ld();
+    for (int k = 0; k < keys; ++k)
+#pragma unroll 1
+      for (int i = 0; i < 32; ++i) {
+        const float x = __bfloat162float(v[k * stride + q + i]);
+        if (!(fabsf(x) < INFINITY)) o[i] = __float_as_uint(__uint_as_float(o[i]) + x);
+      }
+    tmem_st32(taddr + q, o);
+  }
+  tmem_wait_st();
 }
-__device__ __forceinline__ void prompt_add_nonfinite(const FwdParams& p, int k_base, int head, int k0, int k1, int col, uint32_t* o) {
-  float f[32];
-#pragma unroll
-  for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(o[i]);
-  prompt_add_nonfinite_row(p.v + static_cast<long long>(k_base + k0) * p.vs_r + fast_div(head, p.dm_g, p.ds_g) * p.vs_h + col,
-                           p.vs_r, k1 - k0, f);
-#pragma unroll
-  for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(f[i]);
+// V's row of a prompt's key k for query head `head`.
+__device__ __forceinline__ const __nv_bfloat16* prompt_v_row(const FwdParams& p, int head, int k) {
+  return p.v + static_cast<long long>(k) * p.vs_r + fast_div(head, p.dm_g, p.ds_g) * p.vs_h;
 }
 
 // kSoftPairs: of every 16 pairs of scores in a block with no masked key, this many take
@@ -761,14 +768,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       g += nblk;
       const bool store = row < it.Nq;
-      bool odd = false;  // prompts: zeroed infinities or NaN among the values of the tile's ragged blocks
       if constexpr (kPrompt) {
         if (nblk > 0) {
-          odd = tag[u & 7] == static_cast<uint8_t>(u + 1);
+          const bool odd = tag[u & 7] == static_cast<uint8_t>(u + 1);  // the same for all its warps
           ++u;
+          const int k0 = it.min_limit / kBN * kBN;  // the first key of the blocks that were repaired
+          if (ok && odd)
+            prompt_add_nonfinite(tl + C::kColO, D, prompt_v_row(p, it.hh, it.k_base + k0), p.vs_r, store ? limit - k0 : 0);
         }
       }
-      const int odd0 = it.min_limit / kBN * kBN;  // the first key of those blocks
       if (!kStates && C::kStageO && nblk > 0) {
         // O through the V stage of the last block and one TMA store.  Every softmax warp
         // reaches this barrier once per tile with blocks, also after a failed wait (it left
@@ -792,9 +800,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t o[32];
           tmem_ld32(tl + C::kColO + q * 32, o);
           tmem_wait_ld();
-          if constexpr (kPrompt) {
-            if (odd && store) prompt_add_nonfinite(p, it.k_base, it.hh, odd0, limit, q * 32, o);
-          }
 #pragma unroll
           for (int ch = 0; ch < 4; ++ch) {
             uint4 v;
@@ -877,12 +882,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
 #pragma unroll
           for (int k = 0; k < D; ++k) o[k] = 0u;
-        }
-        if constexpr (kPrompt) {
-          if (odd && store) {
-#pragma unroll
-            for (int q = 0; q < D / 32; ++q) prompt_add_nonfinite(p, it.k_base, it.hh, odd0, limit, q * 32, o + q * 32);
-          }
         }
 #pragma unroll
         for (int k = 0; k < D / 2; ++k)

@@ -485,7 +485,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         if constexpr (kPrompt) {
           const bool other = t && j < it.nblk[0] && kb + kBN > it.min_limit[0];  // tile 0's to repair
           if (kb + kBN > t_min_limit && !other) {
-            const int e = (qbase >> 1) * 2 + 2 * j + 1;  // V_j's ring entry: two entries and two products a block
+            const int e = qbase + 2 * j + 1;  // V_j's ring entry: two entries and two products a block
             ok = __all_sync(0xffffffffu, mbar_wait(bar_full(e % C::kSlots), (e / C::kSlots) & 1, wc, 14));
             if (!ok) break;
             if (repair_v_row<64, 0>(smem + C::kOffRing + (e % C::kSlots) * C::kTileBytes, r, kb + r >= it.kv_len))
@@ -529,7 +529,12 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       }
       if (!ok) break;
       const bool store = row < it.Nq;
-      const bool odd = kPrompt && nblk > 0 && tag[ui & 7] == static_cast<uint8_t>(ui + 1);
+      if constexpr (kPrompt) {
+        if (nblk > 0 && tag[ui & 7] == static_cast<uint8_t>(ui + 1)) {
+          const int k0 = (it.nblk[0] > 0 ? it.min_limit[0] : t_min_limit) / kBN * kBN;  // the first key of the blocks that were repaired
+          prompt_add_nonfinite(tl + colO, C::D, prompt_v_row(p, it.hh, it.k_base + k0), p.vs_r, store ? limit - k0 : 0);
+        }
+      }
       const float inv = l > 0.f ? 1.f / l : 0.f;
       uint4* dst = reinterpret_cast<uint4*>(p.o + it.b * p.os_b + it.hh * p.os_h +
                                             (it.q_base + (store ? row : 0)) * p.os_r);
@@ -542,10 +547,6 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         } else {
 #pragma unroll
           for (int x = 0; x < 32; ++x) o[x] = 0u;
-        }
-        if constexpr (kPrompt) {
-          if (odd && store)
-            prompt_add_nonfinite(p, it.k_base, it.hh, (it.nblk[0] > 0 ? it.min_limit[0] : t_min_limit) / kBN * kBN, limit, x4 * 32, o);
         }
         if (store) {
 #pragma unroll
