@@ -651,6 +651,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!__all_sync(0xffffffffu, s_seen))
           ok = __all_sync(0xffffffffu, mbar_wait(bar_s_full(gj % kSBufs), (gj / kSBufs) & 1, wc, 9));
         if (!ok) break;
+        if constexpr (kPrompt) {
+          if ((it.jb0 + j + 1) * kBN > it.min_limit) {  // V's row r of this block
+            ok = __all_sync(0xffffffffu, mbar_wait(bar_v_full(gj % C::kStages), (gj / C::kStages) & 1, wc, 14));
+            if (!ok) break;
+            if (repair_v_row<D, C::kSubBytesKV>(smem + C::kOffV + (gj % C::kStages) * C::kKVBytes, r,
+                                                (it.jb0 + j) * kBN + r >= it.kv_len))
+              tag[u & 7] = static_cast<uint8_t>(u + 1);
+          }
+        }
         tc_fence_after();
         uint32_t sr[kBN];
 #pragma unroll
@@ -722,14 +731,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float2 acc = __fadd2_rn(acc0, acc1);
         l = l * alpha + (acc.x + acc.y);
         m = m_new;
-        if constexpr (kPrompt) {
-          if (kb + kBN > it.min_limit) {  // V's row r of this block
-            ok = __all_sync(0xffffffffu, mbar_wait(bar_v_full(gj % C::kStages), (gj / C::kStages) & 1, wc, 14));
-            if (!ok) break;
-            if (repair_v_row<D, C::kSubBytesKV>(smem + C::kOffV + (gj % C::kStages) * C::kKVBytes, r, kb + r >= it.kv_len))
-              tag[u & 7] = static_cast<uint8_t>(u + 1);
-          }
-        }
         if (j > 0 && !__all_sync(0xffffffffu, alpha == 1.f)) {
           // o~ may be touched only after the previous P V product has landed in it
           if (!__all_sync(0xffffffffu, pv_seen))

@@ -410,6 +410,16 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           if (lane == 0) mbar_arrive(bar_p_full(b));
           continue;
         }
+        if constexpr (kPrompt) {
+          const bool other = t && j < it.nblk[0] && (j + 1) * kBN > it.min_limit[0];  // tile 0's to repair
+          if ((j + 1) * kBN > t_min_limit && !other) {
+            const int e = qbase + 2 * j + 1;  // V_j's ring entry: two entries and two products a block
+            ok = __all_sync(0xffffffffu, mbar_wait(bar_full(e % C::kSlots), (e / C::kSlots) & 1, wc, 14));
+            if (!ok) break;
+            if (repair_v_row<64, 0>(smem + C::kOffRing + (e % C::kSlots) * C::kTileBytes, r, j * kBN + r >= it.kv_len))
+              tag[u & 7] = static_cast<uint8_t>(u + 1);
+          }
+        }
         tc_fence_after();
         uint32_t sr[kBN];
 #pragma unroll
@@ -482,16 +492,6 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         const float2 acc = __fadd2_rn(acc0, acc1);
         l = l * alpha + (acc.x + acc.y);
         m = m_new;
-        if constexpr (kPrompt) {
-          const bool other = t && j < it.nblk[0] && kb + kBN > it.min_limit[0];  // tile 0's to repair
-          if (kb + kBN > t_min_limit && !other) {
-            const int e = qbase + 2 * j + 1;  // V_j's ring entry: two entries and two products a block
-            ok = __all_sync(0xffffffffu, mbar_wait(bar_full(e % C::kSlots), (e / C::kSlots) & 1, wc, 14));
-            if (!ok) break;
-            if (repair_v_row<64, 0>(smem + C::kOffRing + (e % C::kSlots) * C::kTileBytes, r, kb + r >= it.kv_len))
-              tag[u & 7] = static_cast<uint8_t>(u + 1);
-          }
-        }
         if (j > 0 && !__all_sync(0xffffffffu, alpha == 1.f)) {
           // o~_t may be touched only after the tile's previous P V product has landed in it
           if (!__all_sync(0xffffffffu, pv_seen))
