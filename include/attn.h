@@ -453,8 +453,8 @@ attn_status attn_qk_rotate(const void* Q, const void* K, void* Q_out, void* K_ou
  *   Q, O [total_q, Hq, d], K, V [total_k, Hkv, d]: device bf16 with strides (token, head) as in
  *         attn_qk_rotate, positive here.  Hq is a multiple of Hkv: query head h reads K/V head
  *         h / (Hq / Hkv).  LSE fp32 [Hq, total_q].
- *   cu_seqlens_q, cu_seqlens_k, max_seqlen_q: as attn_fwd_varlen (rows past max_seqlen_q and rows
- *         outside every sequence are left as they were; a sequence's keys are rows
+ *   cu_seqlens_q, cu_seqlens_k, max_seqlen_q: as attn_fwd_varlen (rows outside every sequence are
+ *         left as they were, rows past max_seqlen_q may be; a sequence's keys are rows
  *         cu_seqlens_k[b] .. cu_seqlens_k[b + 1] - 1).  causal: bottom-right aligned, so a sequence
  *         with more keys than queries is a prompt over its prefix.
  *   What K and V hold where a row does not look, infinities and NaN among it, does not reach the row.

@@ -99,6 +99,7 @@ struct FwdParams {
   uint32_t dm_g, ds_g;
   const __nv_bfloat16* v;
   long long vs_r, vs_h;
+  int levels;              // prompts: take the tiles by their cost (PromptWalk)
 };
 
 __device__ __forceinline__ int fast_div(int n, uint32_t m, uint32_t s) {
@@ -239,6 +240,9 @@ __device__ __noinline__ void rank_sequences(const FwdParams& p, int B, float* sc
   __syncthreads();
 }
 
+template <bool kPacked, int BN>
+__device__ __forceinline__ void fill_item(const FwdParams& p, Item& it, int qtile, const uint16_t* seq_perm);
+
 // kPacked: a launch over packed sequences (cu_q set), which may take them in the order of
 // seq_perm; the other launches' code has no such step.
 template <bool kPacked, int BN>
@@ -258,6 +262,13 @@ __device__ __forceinline__ Item decode(const FwdParams& p, int item, const uint1
   if (p.causal) qtile = nqt - 1 - qtile;
   it.b = fast_div(it.bh, p.dm_h, p.ds_h);
   it.hh = it.bh - it.b * p.H;
+  fill_item<kPacked, BN>(p, it, qtile, seq_perm);
+  return it;
+}
+
+// The tile `qtile` of (it.b, it.hh); kPacked: it.b may be a rank in seq_perm.
+template <bool kPacked, int BN>
+__device__ __forceinline__ void fill_item(const FwdParams& p, Item& it, int qtile, const uint16_t* seq_perm) {
   it.q0 = qtile * kBM;
   it.q_base = 0;
   it.k_base = 0;
@@ -296,7 +307,115 @@ __device__ __forceinline__ Item decode(const FwdParams& p, int item, const uint1
   it.jb0 = it.split * p.split_blocks;
   const int nsplit = p.num_splits > 1 ? max(0, min(nvis, it.jb0 + p.split_blocks) - it.jb0) : nvis;
   it.nblk = it.valid ? nsplit : 0;
-  return it;
+}
+
+// Causal prompts whose K and V fit in L2 are taken by cost.  A tile's level is the number of its key
+// blocks, as it is for whole tiles: tile t of a sequence whose keys go `off` tiles past its queries is
+// on level t + off, and the sequence has levels up to tiles + off.  Levels go from the highest down, on
+// each the sequences that reach it, in rank order, with all their heads: every CTA's tiles go from long
+// to short, and the CTAs' work evens out whatever the lengths are.  A level below a sequence's first
+// tile is an empty item; where these are more than the others (short prompts over long prefixes: 45 us
+// by heads, 54 by cost) the order is by heads after all.  With ranks by levels, h_0 >= h_1 >= ..., levels h_k - 1 down to h_(k + 1)
+// have k + 1 sequences; an index only grows, so each role walks k along.
+constexpr int kLevelSeqs = 96;  // sequences taken by cost, at most
+struct PromptRanks {            // in the place of the order of packed sequences
+  uint16_t seq[kLevelSeqs];
+  int levels[kLevelSeqs];       // of the rank's sequence
+  int off[kLevelSeqs];          // its lowest level
+  int by_cost;                  // whether the items are taken so
+};
+static_assert(sizeof(PromptRanks) <= 2 * kMaxSortedSeqs, "room");
+
+// rank_sequences for these; scratch: two words a sequence.  rows: of a tile.
+__device__ __noinline__ void rank_prompts(const FwdParams& p, int B, int rows, int* scratch, PromptRanks* ranks) {
+  for (int b = threadIdx.x; b < B; b += blockDim.x) {
+    const int qs = min(max(__ldg(p.cu_q + b), 0), p.total_q), qe = min(max(__ldg(p.cu_q + b + 1), qs), p.total_q);
+    const int ks = min(max(__ldg(p.cu_k + b), 0), p.total_k), ke = min(max(__ldg(p.cu_k + b + 1), ks), p.total_k);
+    const int nq = qe - qs, off = max(ke - ks - nq, 0);
+    scratch[2 * b] = nq > 0 ? (nq + rows - 1) / rows + (off + rows - 1) / rows : 0;
+    scratch[2 * b + 1] = (off + rows - 1) / rows;
+  }
+  __syncthreads();
+  long long all = 0, empty = 0;
+  for (int b = 0; b < B; ++b) {
+    all += scratch[2 * b];
+    if (scratch[2 * b]) empty += scratch[2 * b + 1];
+  }
+  const bool by_cost = 2 * empty <= all;
+  if (threadIdx.x == 0) ranks->by_cost = by_cost;
+  // by heads, the order is that of rank_sequences: decreasing work
+  auto weight = [&](int b) {
+    const float levels = static_cast<float>(scratch[2 * b]);
+    return by_cost ? levels : levels * (levels - static_cast<float>(scratch[2 * b + 1]));
+  };
+  for (int b = threadIdx.x; b < B; b += blockDim.x) {
+    const float w = weight(b);
+    int r = 0;
+    for (int o = 0; o < B; ++o) r += weight(o) > w || (weight(o) == w && o < b);
+    ranks->seq[r] = static_cast<uint16_t>(b);
+    ranks->levels[r] = scratch[2 * b];
+    ranks->off[r] = scratch[2 * b + 1];
+  }
+  fence_proxy_async_smem();  // the scratch's accesses before the TMA copies that overwrite it
+  __syncthreads();
+}
+
+struct PromptWalk {
+  int k = -1, hk = 0, hn = 0;  // k + 1 sequences on a level now, levels [hn, hk)
+  long long before = 0;        // items above them
+
+  // Item n as (rank, head, tile); false past the last.
+  __device__ __forceinline__ bool at(const FwdParams& p, long long n, const PromptRanks* ranks, int* rank, int* head, int* tile) {
+    const int B = p.BH / p.H;
+    if (k < 0) {
+      k = 0;
+      hk = ranks->levels[0];
+      hn = B > 1 ? ranks->levels[1] : 0;
+    }
+    for (;;) {
+      if (k >= B) return false;
+      const long long size = static_cast<long long>(k + 1) * p.H * (hk - hn);
+      if (n < before + size) break;
+      before += size;
+      ++k;
+      hk = hn;
+      hn = k + 1 < B ? ranks->levels[k + 1] : 0;
+    }
+    const long long m = n - before;
+    const int per = (k + 1) * p.H;
+    const int down = (m >> 31) == 0 ? static_cast<int>(static_cast<uint32_t>(m) / static_cast<uint32_t>(per)) : static_cast<int>(m / per);
+    const int i = static_cast<int>(m - static_cast<long long>(down) * per);
+    *rank = fast_div(i, p.dm_h, p.ds_h);
+    *head = i - *rank * p.H;
+    *tile = hk - 1 - down - ranks->off[*rank];
+    return true;
+  }
+};
+
+// Item `ri` of this CTA for any of its roles; false past the last.  (The items of a CTA: item_of.)
+__device__ __forceinline__ int item_of(int r, int c, int G);
+template <bool kPacked, int BN, bool kPrompt>
+__device__ __forceinline__ bool next_item(const FwdParams& p, int ri, int cta, int G, const uint16_t* seq_perm, PromptWalk& walk,
+                                          Item& it) {
+  if constexpr (kPrompt) {
+    if (p.levels && reinterpret_cast<const PromptRanks*>(seq_perm)->by_cost) {
+      int tile;
+      const long long n = static_cast<long long>(ri) * G + ((ri & 1) ? G - 1 - cta : cta);
+      if (!walk.at(p, n, reinterpret_cast<const PromptRanks*>(seq_perm), &it.b, &it.hh, &tile)) return false;
+      it.split = 0;
+      it.bh = it.b * p.H + it.hh;
+      fill_item<kPacked, BN>(p, it, max(tile, 0), seq_perm);
+      if (tile < 0 || tile >= p.num_qtiles) {  // (past max_seqlen_q)
+        it.valid = false;
+        it.nblk = 0;
+      }
+      return true;
+    }
+  }
+  const int item = item_of(ri, cta, G);
+  if (item >= p.num_items) return false;
+  it = decode<kPacked, BN>(p, item, seq_perm);
+  return true;
 }
 
 // The items of CTA c, in order: round r takes items r G .. r G + G - 1 (G = number of
@@ -471,7 +590,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   griddep_launch_dependents();
   uint16_t* seq_perm = reinterpret_cast<uint16_t*>(smem + C::kOffPerm);
   if constexpr (kPacked) {
-    if (p.seq_sort) rank_sequences(p, p.BH / p.H, reinterpret_cast<float*>(smem + C::kOffQ), seq_perm);
+    if (kPrompt && p.levels)
+      rank_prompts(p, p.BH / p.H, kBM, reinterpret_cast<int*>(smem + C::kOffQ), reinterpret_cast<PromptRanks*>(seq_perm));
+    else if (p.seq_sort)
+      rank_sequences(p, p.BH / p.H, reinterpret_cast<float*>(smem + C::kOffQ), seq_perm);
   }
 
   if (warp == kWarpTma) {
@@ -486,10 +608,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       // indexed by the stage: a dynamically indexed array would live in local memory.
       uint32_t k_live = 0, k_par = 0, v_live = 0, v_par = 0;
       bool ok = true;
+      PromptWalk walk;
       for (int ri = 0; ok; ++ri) {
-        const int item = item_of(ri, cta, G);
-        if (item >= p.num_items) break;
-        const Item it = decode<kPacked, kBN>(p, item, seq_perm);
+        Item it;
+        if (!next_item<kPacked, kBN, kPrompt>(p, ri, cta, G, seq_perm, walk, it)) break;
         if (it.nblk == 0) continue;
         const int hkv = kPrompt ? fast_div(it.hh, p.dm_g, p.ds_g) : it.hh;
         // the previous tile's Q must have been read by its last S product
@@ -548,10 +670,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (warp == kWarpS) {
         const uint32_t qlo = (sQ >> 4) | (1u << 16);
         const uint32_t klo = (sK >> 4) | (1u << 16);
+        PromptWalk walk;
         for (int ri = 0; ok; ++ri) {
-          const int item = item_of(ri, cta, G);
-          if (item >= p.num_items) break;
-          const Item it = decode<kPacked, kBN>(p, item, seq_perm);
+          Item it;
+          if (!next_item<kPacked, kBN, kPrompt>(p, ri, cta, G, seq_perm, walk, it)) break;
           if (it.nblk == 0) continue;
           ok = mbar_wait(bar_q_full, kq & 1, wc, 3);
           for (int j = 0; ok && j < it.nblk; ++j, ++g) {
@@ -582,10 +704,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       } else {
         const uint32_t vlo = (sV >> 4) | (static_cast<uint32_t>(C::kSubBytesKV >> 4) << 16);
+        PromptWalk walk;
         for (int ri = 0; ok; ++ri) {
-          const int item = item_of(ri, cta, G);
-          if (item >= p.num_items) break;
-          const Item it = decode<kPacked, kBN>(p, item, seq_perm);
+          Item it;
+          if (!next_item<kPacked, kBN, kPrompt>(p, ri, cta, G, seq_perm, walk, it)) break;
           if (it.nblk == 0) continue;
           // The first product of a tile overwrites o~.  The softmax warps read the previous
           // tile's o~ out before they write this tile's first P, and P_0 is awaited below,
@@ -626,10 +748,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     int g = 0;  // key blocks over all items: score buffer g % 3
     int u = 0;  // prompts: items with work
     bool ok = true;
+    PromptWalk walk;
+    Item it, ahead;  // prompts: the next item is looked up while this one's last product runs
+    bool more = true;
+    if constexpr (kPrompt) more = next_item<kPacked, kBN, kPrompt>(p, 0, cta, G, seq_perm, walk, ahead);
     for (int ri = 0; ok; ++ri) {
-      const int item = item_of(ri, cta, G);
-      if (item >= p.num_items) break;
-      const Item it = decode<kPacked, kBN>(p, item, seq_perm);
+      if constexpr (kPrompt) {
+        if (!more) break;
+        it = ahead;
+        if (!it.valid) more = next_item<kPacked, kBN, kPrompt>(p, ri + 1, cta, G, seq_perm, walk, ahead);
+      } else {
+        if (!next_item<kPacked, kBN, kPrompt>(p, ri, cta, G, seq_perm, walk, it)) break;
+      }
       if (!it.valid) continue;  // a tile past the end of a shorter packed sequence
       const int row = it.q0 + r;
       const int limit = row_key_limit(row, it.kv_len, it.Nq, it.Nk, p.causal);
@@ -760,6 +890,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(bar_p_full(gj % kSBufs));
       }
+      if constexpr (kPrompt) more = next_item<kPacked, kBN, kPrompt>(p, ri + 1, cta, G, seq_perm, walk, ahead);
       // ---- epilogue: one division by l; O and LSE out
       const int gl = g + nblk - 1;  // the tile's last block
       if (ok && nblk > 0) {

@@ -82,6 +82,9 @@ struct PairItem {
   bool valid[2];           // the tile has rows in its sequence
 };
 
+template <bool kPacked>
+__device__ __forceinline__ void fill_pair(const FwdParams& p, PairItem& it, int pair, const uint16_t* seq_perm);
+
 template <bool kPacked>  // as in decode
 __device__ __forceinline__ PairItem decode_pair(const FwdParams& p, int item, const uint16_t* seq_perm) {
   PairItem it;
@@ -95,6 +98,13 @@ __device__ __forceinline__ PairItem decode_pair(const FwdParams& p, int item, co
   if (p.causal) pair = npairs - 1 - pair;
   it.b = it.bh / p.H;
   it.hh = it.bh - it.b * p.H;
+  fill_pair<kPacked>(p, it, pair, seq_perm);
+  return it;
+}
+
+// The pair `pair` of (it.b, it.hh), as fill_item.
+template <bool kPacked>
+__device__ __forceinline__ void fill_pair(const FwdParams& p, PairItem& it, int pair, const uint16_t* seq_perm) {
   it.q_base = 0;
   it.k_base = 0;
   it.Nq = p.Nq;
@@ -133,7 +143,34 @@ __device__ __forceinline__ PairItem decode_pair(const FwdParams& p, int item, co
     it.nblk[t] = it.valid[t] ? nvis : 0;
   }
   it.nmax = max(it.nblk[0], it.nblk[1]);
-  return it;
+}
+
+// As next_item, with pairs of tiles.
+template <bool kPacked, bool kPrompt>
+__device__ __forceinline__ bool next_pair(const FwdParams& p, int ri, int cta, int G, const uint16_t* seq_perm, PromptWalk& walk,
+                                          PairItem& it) {
+  if constexpr (kPrompt) {
+    if (p.levels && reinterpret_cast<const PromptRanks*>(seq_perm)->by_cost) {
+      int pair;
+      const long long n = static_cast<long long>(ri) * G + ((ri & 1) ? G - 1 - cta : cta);
+      if (!walk.at(p, n, reinterpret_cast<const PromptRanks*>(seq_perm), &it.b, &it.hh, &pair)) return false;
+      it.bh = it.b * p.H + it.hh;
+      fill_pair<kPacked>(p, it, max(pair, 0), seq_perm);
+      if (pair < 0 || 2 * pair >= p.num_qtiles) {  // (past max_seqlen_q)
+        it.nmax = 0;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          it.valid[t] = false;
+          it.nblk[t] = 0;
+        }
+      }
+      return true;
+    }
+  }
+  const int item = item_of(ri, cta, G);
+  if (item >= p.num_items) return false;
+  it = decode_pair<kPacked>(p, item, seq_perm);
+  return true;
 }
 
 // Persistent like attn_fwd_kernel: one CTA per SM walks its pairs in item_of() order; the
@@ -215,7 +252,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   griddep_launch_dependents();
   uint16_t* seq_perm = reinterpret_cast<uint16_t*>(smem + C::kOffPerm);
   if constexpr (kPacked) {
-    if (p.seq_sort) rank_sequences(p, p.BH / p.H, reinterpret_cast<float*>(smem + C::kOffQ), seq_perm);
+    if (kPrompt && p.levels)
+      rank_prompts(p, p.BH / p.H, 2 * kBM, reinterpret_cast<int*>(smem + C::kOffQ), reinterpret_cast<PromptRanks*>(seq_perm));
+    else if (p.seq_sort)
+      rank_sequences(p, p.BH / p.H, reinterpret_cast<float*>(smem + C::kOffQ), seq_perm);
   }
 
   if (warp == kPairWarpTma) {
@@ -232,10 +272,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       // local memory).
       uint32_t live = 0, par = 0;
       bool ok = true;
+      PromptWalk walk;
       for (int ri = 0; ok; ++ri) {
-        const int item = item_of(ri, cta, G);
-        if (item >= p.num_items) break;
-        const PairItem it = decode_pair<kPacked>(p, item, seq_perm);
+        PairItem it;
+        if (!next_pair<kPacked, kPrompt>(p, ri, cta, G, seq_perm, walk, it)) break;
         if (it.nmax == 0) continue;
         const int hkv = kPrompt ? fast_div(it.hh, p.dm_g, p.ds_g) : it.hh;
         // the previous pair's Q tiles must have been read by its last S product
@@ -286,10 +326,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       int qn = 0;                             // products of the pairs before this one
       int kq = 0;
       bool ok = true;
+      PromptWalk walk;
       for (int ri = 0; ok; ++ri) {
-        const int item = item_of(ri, cta, G);
-        if (item >= p.num_items) break;
-        const PairItem it = decode_pair<kPacked>(p, item, seq_perm);
+        PairItem it;
+        if (!next_pair<kPacked, kPrompt>(p, ri, cta, G, seq_perm, walk, it)) break;
         if (it.nmax == 0) continue;
         if (warp == kPairWarpS) {
           ok = __all_sync(0xffffffffu, mbar_wait(bar_q_full, kq & 1, wc, 3));
@@ -376,10 +416,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     int nd = 0;  // pairs so far in which this tile had blocks: phase of o_done[t]
     int u = 0;   // prompts: pairs with work
     bool ok = true;
+    PromptWalk walk;
     for (int ri = 0; ok; ++ri) {
-      const int item = item_of(ri, cta, G);
-      if (item >= p.num_items) break;
-      const PairItem it = decode_pair<kPacked>(p, item, seq_perm);
+      PairItem it;
+      if (!next_pair<kPacked, kPrompt>(p, ri, cta, G, seq_perm, walk, it)) break;
       const int qbase = qn;
       qn += 2 * it.nmax;
       // this tile's fields, chosen by value (an array indexed by t would go to local memory)

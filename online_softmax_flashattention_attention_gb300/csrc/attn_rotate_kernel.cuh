@@ -46,7 +46,7 @@ struct RotateParams {
   const int32_t* start;          // [B] or null (0)
   const int32_t* positions;      // [total] or null (start + place in the sequence)
   const float* freq;             // [num_freq]
-  int num_freq, interleaved, weight_f32;
+  int num_freq, weight_f32;
   float eps;
   int B, Hq, H, total;           // H: heads of Q and K together
   int heads_per_block;
@@ -82,8 +82,9 @@ struct RotRow {
   uint2 a, b;  // the lane's two pieces of four columns
 };
 
-template <int D>
-__global__ void __launch_bounds__(kRotThreads, 4) attn_qk_rotate_kernel(const RotateParams p) {
+// kPairs: interleaved.  kAll: every column turns.
+template <int D, bool kPairs, bool kAll>
+__global__ void __launch_bounds__(kRotThreads, 3) attn_qk_rotate_kernel(const RotateParams p) {
   constexpr int kLanes = D / 8;
   constexpr int kGroups = kRotThreads / kLanes;
   constexpr int kPerTok = kGroups / kRotTokens;  // groups that share a token
@@ -100,15 +101,14 @@ __global__ void __launch_bounds__(kRotThreads, 4) attn_qk_rotate_kernel(const Ro
   const int r = p.num_freq;
   // the lane's pieces: columns ca .. + 3 and cb .. + 3; which frequency the first of ca has, if it turns
   int ca = 8 * lane, cb = 8 * lane + 4, fa = 4 * lane;
-  bool turned = 8 * lane < 2 * r;
-  if (!p.interleaved) {
-    turned = 4 * lane < r;
+  bool turned = kAll || 8 * lane < 2 * r;
+  if (!kPairs) {
+    turned = kAll || 4 * lane < r;
     ca = turned ? 4 * lane : 2 * r + 8 * (lane - r / 4);
     cb = turned ? ca + r : ca + 4;
     fa = ca;
   }
   const int head0 = blockIdx.y * p.heads_per_block, head1 = min(p.H, head0 + p.heads_per_block);
-  const uint32_t mask = kLanes == 32 ? 0xffffffffu : ((1u << kLanes) - 1u) << (threadIdx.x & 31 & ~(kLanes - 1));
   for (int i = threadIdx.x; i < 2 * D; i += kRotThreads) {
     const void* w = p.weight[i / D];
     weight[i / D][i % D] = !w ? 1.f : p.weight_f32 ? static_cast<const float*>(w)[i % D]
@@ -136,12 +136,26 @@ __global__ void __launch_bounds__(kRotThreads, 4) attn_qk_rotate_kernel(const Ro
       turn[t][f] = make_float2(c, s);
     }
     __syncthreads();
-    if (tok >= p.total || !in[tk]) continue;  // a whole group of lanes
+    if (tok >= p.total || !in[tk]) continue;  // whole warps: a token's groups are
+    static_assert(kPerTok * kLanes % 32 == 0, "a warp has one token");
 
 #pragma unroll
     for (int k = 0; k < 2; ++k) {  // Q's heads, then K's
-      const int h0 = max(head0 - (k ? p.Hq : 0), 0) + sub, h1 = min(head1 - (k ? p.Hq : 0), k ? p.H - p.Hq : p.Hq);
+      const int h0 = max(head0 - (k ? p.Hq : 0), 0), h1 = min(head1 - (k ? p.Hq : 0), k ? p.H - p.Hq : p.Hq);
       if (h0 >= h1) continue;
+      const __nv_bfloat16* src = p.src[k] + tok * p.src_t[k] + (h0 + sub) * p.src_h[k];
+      __nv_bfloat16* dst = p.dst[k] + tok * p.dst_t[k] + (h0 + sub) * p.dst_h[k];
+      const long long sstep = kPerTok * p.src_h[k], dstep = kPerTok * p.dst_h[k];
+      RotRow x[kU];
+      auto load = [&](int h) {
+#pragma unroll
+        for (int u = 0; u < kU; ++u, src += sstep)
+          if (h + u * kPerTok < h1) {
+            x[u].a = *reinterpret_cast<const uint2*>(src + ca);
+            x[u].b = *reinterpret_cast<const uint2*>(src + cb);
+          }
+      };
+      load(h0 + sub);
       // out_a = A va + Ba other, out_b = B vb + Bb other (other: the column it turns with)
       float wa[4], wb[4], Ac[4], Bc[4], As[4], Bs[4];
 #pragma unroll
@@ -155,31 +169,25 @@ __global__ void __launch_bounds__(kRotThreads, 4) attn_qk_rotate_kernel(const Ro
         Bc[i] = wb[i];
         As[i] = Bs[i] = 0.f;
         if (turned) {
-          const float2 x = turn[tk][p.interleaved ? fa + i / 2 : fa + i], y = p.interleaved ? turn[tk][fa + 2 + i / 2] : x;
+          const float2 x = turn[tk][kPairs ? fa + i / 2 : fa + i], y = kPairs ? turn[tk][fa + 2 + i / 2] : x;
           Ac[i] *= x.x;
           Bc[i] *= y.x;
-          As[i] = p.interleaved ? ((i & 1) ? x.y : -x.y) * wa[i ^ 1] : -x.y * wb[i];
-          Bs[i] = p.interleaved ? ((i & 1) ? y.y : -y.y) * wb[i ^ 1] : x.y * wa[i];
+          As[i] = kPairs ? ((i & 1) ? x.y : -x.y) * wa[i ^ 1] : -x.y * wb[i];
+          Bs[i] = kPairs ? ((i & 1) ? y.y : -y.y) * wb[i ^ 1] : x.y * wa[i];
         }
       }
       const bool norm = p.weight[k] != nullptr;
-      const __nv_bfloat16* src = p.src[k] + tok * p.src_t[k];
-      __nv_bfloat16* dst = p.dst[k] + tok * p.dst_t[k];
-      const long long sh = p.src_h[k], dh = p.dst_h[k];
-      for (int h = h0; h < h1; h += kU * kPerTok) {
-        RotRow x[kU];
+#pragma unroll 1
+      for (int hb = h0; hb < h1; hb += kU * kPerTok) {  // (the same rounds for every lane of a warp)
+        const int h = hb + sub;
+        RotRow row[kU];
 #pragma unroll
-        for (int u = 0; u < kU; ++u)
-          if (h + u * kPerTok < h1) {
-            const __nv_bfloat16* row = src + (h + u * kPerTok) * sh;
-            x[u].a = *reinterpret_cast<const uint2*>(row + ca);
-            x[u].b = *reinterpret_cast<const uint2*>(row + cb);
-          }
+        for (int u = 0; u < kU; ++u) row[u] = x[u];
+        load(h + kU * kPerTok);  // the next rows, while these are in hand
 #pragma unroll
-        for (int u = 0; u < kU; ++u) {
-          if (h + u * kPerTok >= h1) break;
-          float2 va[2] = {make_float2(bf16_lo(x[u].a.x), bf16_hi(x[u].a.x)), make_float2(bf16_lo(x[u].a.y), bf16_hi(x[u].a.y))};
-          float2 vb[2] = {make_float2(bf16_lo(x[u].b.x), bf16_hi(x[u].b.x)), make_float2(bf16_lo(x[u].b.y), bf16_hi(x[u].b.y))};
+        for (int u = 0; u < kU; ++u, dst += dstep) {
+          float2 va[2] = {make_float2(bf16_lo(row[u].a.x), bf16_hi(row[u].a.x)), make_float2(bf16_lo(row[u].a.y), bf16_hi(row[u].a.y))};
+          float2 vb[2] = {make_float2(bf16_lo(row[u].b.x), bf16_hi(row[u].b.x)), make_float2(bf16_lo(row[u].b.y), bf16_hi(row[u].b.y))};
           float inv = 1.f;
           if (norm) {
             float2 ss = __fmul2_rn(va[0], va[0]);
@@ -188,7 +196,7 @@ __global__ void __launch_bounds__(kRotThreads, 4) attn_qk_rotate_kernel(const Ro
             ss = __ffma2_rn(vb[1], vb[1], ss);
             float sum = ss.x + ss.y;
 #pragma unroll
-            for (int o = kLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(mask, sum, o);
+            for (int o = kLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
             inv = rsqrtf(sum * (1.f / D) + p.eps);
           }
           float2 oa[2], ob[2];
@@ -196,18 +204,19 @@ __global__ void __launch_bounds__(kRotThreads, 4) attn_qk_rotate_kernel(const Ro
           for (int i = 0; i < 2; ++i) {
             oa[i] = __fmul2_rn(va[i], make_float2(Ac[2 * i], Ac[2 * i + 1]));
             ob[i] = __fmul2_rn(vb[i], make_float2(Bc[2 * i], Bc[2 * i + 1]));
-            if (turned) {
-              const float2 other_a = p.interleaved ? make_float2(va[i].y, va[i].x) : vb[i];
-              const float2 other_b = p.interleaved ? make_float2(vb[i].y, vb[i].x) : va[i];
+            if (kAll || turned) {
+              const float2 other_a = kPairs ? make_float2(va[i].y, va[i].x) : vb[i];
+              const float2 other_b = kPairs ? make_float2(vb[i].y, vb[i].x) : va[i];
               oa[i] = __ffma2_rn(other_a, make_float2(As[2 * i], As[2 * i + 1]), oa[i]);
               ob[i] = __ffma2_rn(other_b, make_float2(Bs[2 * i], Bs[2 * i + 1]), ob[i]);
             }
             oa[i] = __fmul2_rn(oa[i], make_float2(inv, inv));
             ob[i] = __fmul2_rn(ob[i], make_float2(inv, inv));
           }
-          __nv_bfloat16* row = dst + (h + u * kPerTok) * dh;
-          *reinterpret_cast<uint2*>(row + ca) = make_uint2(pack_bf16x2(oa[0].x, oa[0].y), pack_bf16x2(oa[1].x, oa[1].y));
-          *reinterpret_cast<uint2*>(row + cb) = make_uint2(pack_bf16x2(ob[0].x, ob[0].y), pack_bf16x2(ob[1].x, ob[1].y));
+          if (h + u * kPerTok < h1) {
+            *reinterpret_cast<uint2*>(dst + ca) = make_uint2(pack_bf16x2(oa[0].x, oa[0].y), pack_bf16x2(oa[1].x, oa[1].y));
+            *reinterpret_cast<uint2*>(dst + cb) = make_uint2(pack_bf16x2(ob[0].x, ob[0].y), pack_bf16x2(ob[1].x, ob[1].y));
+          }
         }
       }
     }
