@@ -99,7 +99,6 @@ struct FwdParams {
   uint32_t dm_g, ds_g;
   const __nv_bfloat16* v;
   long long vs_r, vs_h;
-  int levels;              // prompts: take the tiles by their cost (PromptWalk)
 };
 
 __device__ __forceinline__ int fast_div(int n, uint32_t m, uint32_t s) {
@@ -394,11 +393,11 @@ struct PromptWalk {
 
 // Item `ri` of this CTA for any of its roles; false past the last.  (The items of a CTA: item_of.)
 __device__ __forceinline__ int item_of(int r, int c, int G);
-template <bool kPacked, int BN, bool kPrompt>
+template <bool kPacked, int BN, bool kByCost>
 __device__ __forceinline__ bool next_item(const FwdParams& p, int ri, int cta, int G, const uint16_t* seq_perm, PromptWalk& walk,
                                           Item& it) {
-  if constexpr (kPrompt) {
-    if (p.levels && reinterpret_cast<const PromptRanks*>(seq_perm)->by_cost) {
+  if constexpr (kByCost) {
+    if (reinterpret_cast<const PromptRanks*>(seq_perm)->by_cost) {
       int tile;
       const long long n = static_cast<long long>(ri) * G + ((ri & 1) ? G - 1 - cta : cta);
       if (!walk.at(p, n, reinterpret_cast<const PromptRanks*>(seq_perm), &it.b, &it.hh, &tile)) return false;
@@ -511,7 +510,8 @@ __device__ __forceinline__ const __nv_bfloat16* prompt_v_row(const FwdParams& p,
 // warps, before they hand P over, zero V's rows past the end, which belong to somebody else, and the
 // infinities and NaN among the others; rows that do see those get them added in the epilogue.  (An
 // eighth warp for it took 15000 cycles a tile, beside busy warps: 2048 tokens 73 us against 46.)
-template <int D, bool kStates, int kSoftPairs, bool kPacked, int BN = kBN, bool kPrompt = false>
+// kByCost: its items by PromptWalk.
+template <int D, bool kStates, int kSoftPairs, bool kPacked, int BN = kBN, bool kPrompt = false, bool kByCost = false>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
@@ -590,7 +590,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   griddep_launch_dependents();
   uint16_t* seq_perm = reinterpret_cast<uint16_t*>(smem + C::kOffPerm);
   if constexpr (kPacked) {
-    if (kPrompt && p.levels)
+    if constexpr (kByCost)
       rank_prompts(p, p.BH / p.H, kBM, reinterpret_cast<int*>(smem + C::kOffQ), reinterpret_cast<PromptRanks*>(seq_perm));
     else if (p.seq_sort)
       rank_sequences(p, p.BH / p.H, reinterpret_cast<float*>(smem + C::kOffQ), seq_perm);
@@ -611,7 +611,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       PromptWalk walk;
       for (int ri = 0; ok; ++ri) {
         Item it;
-        if (!next_item<kPacked, kBN, kPrompt>(p, ri, cta, G, seq_perm, walk, it)) break;
+        if (!next_item<kPacked, kBN, kByCost>(p, ri, cta, G, seq_perm, walk, it)) break;
         if (it.nblk == 0) continue;
         const int hkv = kPrompt ? fast_div(it.hh, p.dm_g, p.ds_g) : it.hh;
         // the previous tile's Q must have been read by its last S product
@@ -673,7 +673,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         PromptWalk walk;
         for (int ri = 0; ok; ++ri) {
           Item it;
-          if (!next_item<kPacked, kBN, kPrompt>(p, ri, cta, G, seq_perm, walk, it)) break;
+          if (!next_item<kPacked, kBN, kByCost>(p, ri, cta, G, seq_perm, walk, it)) break;
           if (it.nblk == 0) continue;
           ok = mbar_wait(bar_q_full, kq & 1, wc, 3);
           for (int j = 0; ok && j < it.nblk; ++j, ++g) {
@@ -707,7 +707,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         PromptWalk walk;
         for (int ri = 0; ok; ++ri) {
           Item it;
-          if (!next_item<kPacked, kBN, kPrompt>(p, ri, cta, G, seq_perm, walk, it)) break;
+          if (!next_item<kPacked, kBN, kByCost>(p, ri, cta, G, seq_perm, walk, it)) break;
           if (it.nblk == 0) continue;
           // The first product of a tile overwrites o~.  The softmax warps read the previous
           // tile's o~ out before they write this tile's first P, and P_0 is awaited below,
@@ -749,16 +749,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     int u = 0;  // prompts: items with work
     bool ok = true;
     PromptWalk walk;
-    Item it, ahead;  // prompts: the next item is looked up while this one's last product runs
+    Item it, ahead;  // by cost, the next item is looked up while this one's last product runs
     bool more = true;
-    if constexpr (kPrompt) more = next_item<kPacked, kBN, kPrompt>(p, 0, cta, G, seq_perm, walk, ahead);
+    if constexpr (kByCost) more = next_item<kPacked, kBN, kByCost>(p, 0, cta, G, seq_perm, walk, ahead);
     for (int ri = 0; ok; ++ri) {
-      if constexpr (kPrompt) {
+      if constexpr (kByCost) {
         if (!more) break;
         it = ahead;
-        if (!it.valid) more = next_item<kPacked, kBN, kPrompt>(p, ri + 1, cta, G, seq_perm, walk, ahead);
+        if (!it.valid) more = next_item<kPacked, kBN, kByCost>(p, ri + 1, cta, G, seq_perm, walk, ahead);
       } else {
-        if (!next_item<kPacked, kBN, kPrompt>(p, ri, cta, G, seq_perm, walk, it)) break;
+        if (!next_item<kPacked, kBN, kByCost>(p, ri, cta, G, seq_perm, walk, it)) break;
       }
       if (!it.valid) continue;  // a tile past the end of a shorter packed sequence
       const int row = it.q0 + r;
@@ -890,7 +890,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(bar_p_full(gj % kSBufs));
       }
-      if constexpr (kPrompt) more = next_item<kPacked, kBN, kPrompt>(p, ri + 1, cta, G, seq_perm, walk, ahead);
+      if constexpr (kByCost) more = next_item<kPacked, kBN, kByCost>(p, ri + 1, cta, G, seq_perm, walk, ahead);
       // ---- epilogue: one division by l; O and LSE out
       const int gl = g + nblk - 1;  // the tile's last block
       if (ok && nblk > 0) {

@@ -146,11 +146,11 @@ __device__ __forceinline__ void fill_pair(const FwdParams& p, PairItem& it, int 
 }
 
 // As next_item, with pairs of tiles.
-template <bool kPacked, bool kPrompt>
+template <bool kPacked, bool kByCost>
 __device__ __forceinline__ bool next_pair(const FwdParams& p, int ri, int cta, int G, const uint16_t* seq_perm, PromptWalk& walk,
                                           PairItem& it) {
-  if constexpr (kPrompt) {
-    if (p.levels && reinterpret_cast<const PromptRanks*>(seq_perm)->by_cost) {
+  if constexpr (kByCost) {
+    if (reinterpret_cast<const PromptRanks*>(seq_perm)->by_cost) {
       int pair;
       const long long n = static_cast<long long>(ri) * G + ((ri & 1) ? G - 1 - cta : cta);
       if (!walk.at(p, n, reinterpret_cast<const PromptRanks*>(seq_perm), &it.b, &it.hh, &pair)) return false;
@@ -186,7 +186,7 @@ __device__ __forceinline__ bool next_pair(const FwdParams& p, int ri, int cta, i
 // kPrompt: as in attn_fwd_kernel.  A block of V that tile 0 sees in part is repaired by tile 0's warps,
 // before its product, which comes before tile 1's with that block; tile 1's warps repair the blocks that
 // tile 0 lacks.  What tile 0 zeroed in a block that tile 1 sees whole is added to tile 1's rows too.
-template <int kSoftPairs, bool kPacked, bool kPrompt = false>
+template <int kSoftPairs, bool kPacked, bool kPrompt = false, bool kByCost = false>
 __global__ void __launch_bounds__(kPairThreads, 1)
     attn_fwd_pair_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                          const __grid_constant__ CUtensorMap tmV, const FwdParams p) {
@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   griddep_launch_dependents();
   uint16_t* seq_perm = reinterpret_cast<uint16_t*>(smem + C::kOffPerm);
   if constexpr (kPacked) {
-    if (kPrompt && p.levels)
+    if constexpr (kByCost)
       rank_prompts(p, p.BH / p.H, 2 * kBM, reinterpret_cast<int*>(smem + C::kOffQ), reinterpret_cast<PromptRanks*>(seq_perm));
     else if (p.seq_sort)
       rank_sequences(p, p.BH / p.H, reinterpret_cast<float*>(smem + C::kOffQ), seq_perm);
@@ -275,7 +275,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       PromptWalk walk;
       for (int ri = 0; ok; ++ri) {
         PairItem it;
-        if (!next_pair<kPacked, kPrompt>(p, ri, cta, G, seq_perm, walk, it)) break;
+        if (!next_pair<kPacked, kByCost>(p, ri, cta, G, seq_perm, walk, it)) break;
         if (it.nmax == 0) continue;
         const int hkv = kPrompt ? fast_div(it.hh, p.dm_g, p.ds_g) : it.hh;
         // the previous pair's Q tiles must have been read by its last S product
@@ -329,7 +329,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       PromptWalk walk;
       for (int ri = 0; ok; ++ri) {
         PairItem it;
-        if (!next_pair<kPacked, kPrompt>(p, ri, cta, G, seq_perm, walk, it)) break;
+        if (!next_pair<kPacked, kByCost>(p, ri, cta, G, seq_perm, walk, it)) break;
         if (it.nmax == 0) continue;
         if (warp == kPairWarpS) {
           ok = __all_sync(0xffffffffu, mbar_wait(bar_q_full, kq & 1, wc, 3));
@@ -419,7 +419,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     PromptWalk walk;
     for (int ri = 0; ok; ++ri) {
       PairItem it;
-      if (!next_pair<kPacked, kPrompt>(p, ri, cta, G, seq_perm, walk, it)) break;
+      if (!next_pair<kPacked, kByCost>(p, ri, cta, G, seq_perm, walk, it)) break;
       const int qbase = qn;
       qn += 2 * it.nmax;
       // this tile's fields, chosen by value (an array indexed by t would go to local memory)

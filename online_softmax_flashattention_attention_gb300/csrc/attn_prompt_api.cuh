@@ -45,8 +45,18 @@ void fix_strides(const int64_t* s, int rows, int heads, int d, long long* row, l
   *row = rows > 1 ? s[0] : static_cast<long long>(heads) * d;
 }
 
+// Whether a prompt's tiles go by cost (PromptWalk): where sequences may have eight and more and all K and
+// V stay in L2 meanwhile; else head by head, as the packed forward has them.  Measured on GB300, 32 / 8
+// heads, d = 128: 8192 tokens 455 -> 423 us, 9 prompts of 900 to 8192 tokens 1885 -> 1860; d = 64: 8192
+// tokens 339 -> 307.  The other way round, for the ranks that the order needs: 77 tokens 6.2 -> 7.3 us; 7
+// prompts of 61 to 517 tokens over prefixes of up to 5000, 16 / 4 heads, d = 64: 45 -> 50.
+bool prompt_by_cost(int B, int Hkv, const Geometry& geo, int d, int causal) {
+  return causal && B <= attn::kLevelSeqs && geo.grid_q > 7 * attn::kBM &&
+         kv_footprint(1, Hkv, static_cast<int>(geo.k_rows), d) <= kRankMajorMaxKvBytes;
+}
+
 // kPair: d = 64, two query tiles a CTA (attn_fwd_pair_kernel).
-template <int D, bool kPair>
+template <int D, bool kPair, bool kByCost>
 attn_status launch_prompt(const void* Q, const void* K, const void* V, void* O, float* LSE, int B, int Hq, int Hkv,
                           int max_q, float scale, int causal, cudaStream_t stream, int dev, uint32_t* status,
                           const Geometry& geo) {
@@ -54,9 +64,9 @@ attn_status launch_prompt(const void* Q, const void* K, const void* V, void* O, 
   using C = std::conditional_t<kPair, attn::PairCfg, attn::FwdCfg<D>>;
   attn_status st;
   if constexpr (kPair)
-    st = set_smem_attr(attn::attn_fwd_pair_kernel<0, true, true>, C::kSmemAlloc, dev, attr_set);
+    st = set_smem_attr(attn::attn_fwd_pair_kernel<0, true, true, kByCost>, C::kSmemAlloc, dev, attr_set);
   else
-    st = set_smem_attr(attn::attn_fwd_kernel<D, false, 0, true, attn::kBN, true>, C::kSmemAlloc, dev, attr_set);
+    st = set_smem_attr(attn::attn_fwd_kernel<D, false, 0, true, attn::kBN, true, kByCost>, C::kSmemAlloc, dev, attr_set);
   if (st != ATTN_OK) return st;
   CUtensorMap mq, mk, mv, mo;
   attn::FwdParams p;
@@ -78,22 +88,15 @@ attn_status launch_prompt(const void* Q, const void* K, const void* V, void* O, 
     p.num_items = static_cast<int>(static_cast<long long>((p.num_qtiles + 1) / 2) * p.BH);
     p.order_div = (p.num_qtiles + 1) / 2;
   }
-  // Tiles go by cost (PromptWalk) where sequences may have eight and more and all K and V stay in L2
-  // meanwhile; else head by head, as the packed forward has them.  Measured on GB300, 32 / 8 heads,
-  // d = 128: 8192 tokens 455 -> 423 us, 9 prompts of 900 to 8192 tokens 1885 -> 1860; d = 64: 8192 tokens
-  // 339 -> 307.  The other way round, for the ranks that the order needs: 77 tokens 6.2 -> 7.3; 7 prompts
-  // of 61 to 517 tokens over prefixes of up to 5000, 16 / 4 heads, d = 64: 45 -> 50.
-  p.levels = causal && B <= attn::kLevelSeqs && p.num_qtiles >= 8 &&
-             kv_footprint(1, Hkv, static_cast<int>(geo.k_rows), D) <= kRankMajorMaxKvBytes;
-  if (p.levels) p.seq_sort = 1;
+  if (kByCost) p.seq_sort = 1;  // the ranks' place
   set_divisors(&p);
   const unsigned grid = static_cast<unsigned>(std::min(p.num_items, sm_count(dev)));
   const int smem = p.seq_sort ? C::kSmemAlloc : C::kSmemAllocNoPerm;
   cudaError_t e;
   if constexpr (kPair)
-    e = launch_pdl(attn::attn_fwd_pair_kernel<0, true, true>, grid, attn::kPairThreads, smem, stream, mq, mk, mv, p);
+    e = launch_pdl(attn::attn_fwd_pair_kernel<0, true, true, kByCost>, grid, attn::kPairThreads, smem, stream, mq, mk, mv, p);
   else
-    e = launch_pdl(attn::attn_fwd_kernel<D, false, 0, true, attn::kBN, true>, grid, attn::kThreads, smem, stream, mq, mk,
+    e = launch_pdl(attn::attn_fwd_kernel<D, false, 0, true, attn::kBN, true, kByCost>, grid, attn::kThreads, smem, stream, mq, mk,
                    mv, mo, p);
   if (e != cudaSuccess) return fail(ATTN_ERR_LAUNCH, "kernel launch: %s", cudaGetErrorString(e));
   return ATTN_OK;
@@ -282,9 +285,10 @@ attn_status attn_fwd_prompt(const void* Q, const void* K, const void* V, void* O
   uint32_t* status = nullptr;
   if ((st = get_device(&dev)) != ATTN_OK || (st = setup(dev, &status)) != ATTN_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  auto launch = d == 128                                     ? launch_prompt<128, false>
-                : use_pair_kernel(dev, B, Hq, g, causal) ? launch_prompt<64, true>
-                                                             : launch_prompt<64, false>;
+  const bool pair = d == 64 && use_pair_kernel(dev, B, Hq, g, causal), cost = prompt_by_cost(B, Hkv, g, d, causal);
+  auto launch = d == 128 ? (cost ? launch_prompt<128, false, true> : launch_prompt<128, false, false>)
+                : pair   ? (cost ? launch_prompt<64, true, true> : launch_prompt<64, true, false>)
+                         : (cost ? launch_prompt<64, false, true> : launch_prompt<64, false, false>);
   return launch(Q, K, V, O, LSE, B, Hq, Hkv, max_seqlen_q, scale, causal, s, dev, status, g);
 }
 
