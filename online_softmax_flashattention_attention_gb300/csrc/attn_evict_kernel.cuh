@@ -267,20 +267,17 @@ __global__ void __launch_bounds__(kEvictThreads) attn_evict_select_kernel(const 
   cluster.sync();  // nobody leaves while its counts may be read
 }
 
-// 2 * blocks + 1 blocks a unit: `blocks` for K's rows, `blocks` for V's, one for scale codes and weights.
+// blocks + 1 blocks a unit: `blocks` for K's and V's rows, one for scale codes and weights.
 __global__ void __launch_bounds__(kMoveThreads) attn_evict_move_kernel(const EvictParams p, int blocks) {
   griddep_wait();
   griddep_launch_dependents();
-  const int per_unit = 2 * blocks + 1;
-  const int unit = blockIdx.x / per_unit, rest = blockIdx.x - unit * per_unit;
+  const int unit = blockIdx.x / (blocks + 1), block = blockIdx.x - unit * (blocks + 1);
   const int b = unit / p.Hkv, h = unit - b * p.Hkv;
   const int n = evict_len(p, b), rows = min(n, p.keep);
   const int32_t* kept = p.kept + static_cast<long long>(unit) * p.keep;
-  const int plane = rest == 2 * blocks ? 2 : rest / blocks;
-  const int block = plane == 2 ? 0 : rest - plane * blocks;
   const bool here = p.in_place && n <= p.keep;  // every row is where it belongs
   if (here) return;
-  if (plane == 2) {
+  if (block == blocks) {
     // scale codes and weights: a thread a row
     for (int i0 = 0; i0 < rows; i0 += kMoveThreads) {
       const int i = i0 + threadIdx.x;
@@ -301,7 +298,6 @@ __global__ void __launch_bounds__(kMoveThreads) attn_evict_move_kernel(const Evi
     }
     return;
   }
-  uint8_t* pool = plane ? p.v : p.k;
   const int slices = p.row_bytes / p.slice;
   const int lanes = p.slice / 16, col = (block % slices) * p.slice + (threadIdx.x % lanes) * 16;  // lanes: a power of two
   const int r0 = block / slices * p.rows_per_block, r1 = min(rows, r0 + p.rows_per_block);
@@ -322,20 +318,26 @@ __global__ void __launch_bounds__(kMoveThreads) attn_evict_move_kernel(const Evi
     to[threadIdx.x] = t;
     __syncthreads();
     for (int k0 = threadIdx.x / lanes; k0 < kMoveThreads; k0 += step * kMoveUnroll) {
-      uint4 x[kMoveUnroll];
+      uint4 x[2][kMoveUnroll];
       long long dst[kMoveUnroll];
 #pragma unroll
       for (int u = 0; u < kMoveUnroll; ++u) {
         const int k = k0 + u * step;
         const long long src = k < kMoveThreads ? from[k] : -1;
         dst[u] = k < kMoveThreads ? to[k] : -1;
-        x[u] = make_uint4(0, 0, 0, 0);
-        if (dst[u] >= 0 && src >= 0) x[u] = *reinterpret_cast<const uint4*>(pool + src * p.row_bytes + col);
+        x[0][u] = x[1][u] = make_uint4(0, 0, 0, 0);
+        if (dst[u] >= 0 && src >= 0) {
+          x[0][u] = *reinterpret_cast<const uint4*>(p.k + src * p.row_bytes + col);
+          x[1][u] = *reinterpret_cast<const uint4*>(p.v + src * p.row_bytes + col);
+        }
       }
       if (p.in_place) __syncthreads();  // a step's rows are read before any is written
 #pragma unroll
       for (int u = 0; u < kMoveUnroll; ++u)
-        if (dst[u] >= 0) *reinterpret_cast<uint4*>(pool + dst[u] * p.row_bytes + col) = x[u];
+        if (dst[u] >= 0) {
+          *reinterpret_cast<uint4*>(p.k + dst[u] * p.row_bytes + col) = x[0][u];
+          *reinterpret_cast<uint4*>(p.v + dst[u] * p.row_bytes + col) = x[1][u];
+        }
     }
     __syncthreads();
   }

@@ -400,10 +400,10 @@ attn_status attn_cache_evict(const attn_cache* cache, float* weights, const int3
   p.row_bytes = cache->d * (cache->type == ATTN_CACHE_E4M3 ? 1 : 2);
   p.in_place = in_place ? 1 : 0;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  // A unit's weights are shared by as many CTAs as hold 8192 of them each, 8 at most.
-  unsigned cluster = 1;
-  while (cluster < 8 && room > 8192ll * cluster) cluster *= 2;
+  // A unit's weights are shared by as many CTAs as hold 8192 of them each, 8 at most, while SMs are idle.
   const long long units = static_cast<long long>(B) * p.Hkv;
+  unsigned cluster = 1;
+  while (cluster < 8 && room > 8192ll * cluster && units * cluster < sm_count(dev)) cluster *= 2;
   p.key_cap = static_cast<int>(std::min<long long>((room + cluster - 1) / cluster, attn::kEvictMaxKeys));
   static bool attr_set[kMaxDevices] = {};
   if ((st = set_smem_attr(attn::attn_evict_select_kernel, attn::kEvictMaxKeys * 4, dev, attr_set)) != ATTN_OK) return st;
@@ -412,17 +412,17 @@ attn_status attn_cache_evict(const attn_cache* cache, float* weights, const int3
   const long long most = std::min<long long>(keep, room);
   p.rows_per_block = 256;
   if (in_place) {
-    while (slices * 32 < p.row_bytes && 2 * units * slices < 2 * sm_count(dev)) slices *= 2;
+    while (slices * 32 < p.row_bytes && units * slices < 2 * sm_count(dev)) slices *= 2;
     p.rows_per_block = INT32_MAX;
   }
   p.slice = p.row_bytes / slices;
   const long long blocks = in_place ? slices : (most + p.rows_per_block - 1) / p.rows_per_block;
-  if (units * cluster > INT32_MAX || units * (2 * blocks + 1) > INT32_MAX)
+  if (units * cluster > INT32_MAX || units * (blocks + 1) > INT32_MAX)
     return fail(ATTN_ERR_BAD_SHAPE, "too many (sequence, head) units (%lld)", units);
   cudaError_t e = launch_pdl_cluster(attn::attn_evict_select_kernel, static_cast<unsigned>(units * cluster), cluster,
                                      attn::kEvictThreads, static_cast<size_t>(p.key_cap) * 4, s, p);
   if (e == cudaSuccess && keep > 0)
-    e = launch_pdl(attn::attn_evict_move_kernel, static_cast<unsigned>(units * (2 * blocks + 1)), attn::kMoveThreads, 0,
+    e = launch_pdl(attn::attn_evict_move_kernel, static_cast<unsigned>(units * (blocks + 1)), attn::kMoveThreads, 0,
                    s, p, static_cast<int>(blocks));
   if (e != cudaSuccess) return fail(ATTN_ERR_LAUNCH, "evict kernel launch: %s", cudaGetErrorString(e));
   return ATTN_OK;
