@@ -150,10 +150,10 @@ __device__ __forceinline__ WeighCols weigh_cols(const WeighParams& p, int first,
   return c;
 }
 
-// 32 lanes x 8 columns of 32-bit.
-__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t* r) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+// 32 lanes x 4 columns of 32-bit.
+__device__ __forceinline__ void tmem_ld4(uint32_t taddr, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(taddr));
 }
 
@@ -580,14 +580,14 @@ __global__ void __launch_bounds__(WeighCfg<D, kF8>::kThreads, 1)
             ok = tile_wait(bar_k_full(k.st), k.ph, wc, 66);
             a = klo + k.st * (C::kStageK >> 4);
           }
+          const uint32_t idesc = idesc_bf16_f32(128, cols, 0);
           for (int j = 0; ok && j < t.nq; ++j, ++g) {
             const uint32_t bf = 2 * (g & 1) + h;
             ok = tile_wait(bar_q_full(q.st), q.ph, wc, 69) && tile_wait(bar_s_free(bf), ((g >> 1) & 1) ^ 1, wc, 70);
             if (!ok) break;
             tc_fence_after();
-            // all tiles but the last have the first one's columns (a group of more than 128 heads aside)
-            const uint32_t n = j + 1 < t.nq && p.heads == p.G ? cols : (weigh_cols(p, first, t.T, j).n + 15) / 16 * 16;
-            product(tmem + 128u * bf, qlo + q.st * (C::kTileBytes >> 4), idesc_bf16_f32(128, n, 0));
+            // with the first tile's columns, which are never fewer (what lies past a tile's own is not looked at)
+            product(tmem + 128u * bf, qlo + q.st * (C::kTileBytes >> 4), idesc);
             mma_commit(bar_s_full(bf));
             mma_commit(bar_q_free(q.st));
             q.next(p.ring_q);
@@ -738,15 +738,21 @@ __global__ void __launch_bounds__(WeighCfg<D, kF8>::kThreads, 1)
         }
         const WeighCols c = weigh_cols(p, first, t.T, single ? 0 : j);
         if (single) key((j - j0) >> 1);
-        const int c0 = max(sees - (c.tok - first), 0) * p.heads;  // the key's first column of the tile
+        int c0 = 0;     // the key's first column of the tile
+        int plain = narrow ? 0 : c.n & ~31;  // columns that every key of the warp sees, 32 at a time
+        if (c.tok - first < kWeighStep) {
+          c0 = max(sees - (c.tok - first), 0) * p.heads;
+          if (__any_sync(0xffffffffu, c0 > 0)) plain = 0;
+        }
         ok = __all_sync(0xffffffffu, tile_wait(bar_s_full(bf), ((g + j) >> 1) & 1, wc, 74));
         if (!ok) break;
         tc_fence_after();
+        if (odd[l.st]) plain = 0;
         float2 a0 = make_float2(0.f, 0.f), a1 = make_float2(0.f, 0.f);
-        if (!(narrow || odd[l.st] || __any_sync(0xffffffffu, c0 > 0) || (c.n & 31) != 0)) {
+        {
           const float2 cc = make_float2(p.c, p.c);
 #pragma unroll 1
-          for (int q = 0; q < c.n; q += 32) {
+          for (int q = 0; q < plain; q += 32) {
             uint32_t s[32];
             tmem_ld32(ts + q, s);
             tmem_wait_ld();
@@ -761,35 +767,28 @@ __global__ void __launch_bounds__(WeighCfg<D, kF8>::kThreads, 1)
                 a0 = __fadd2_rn(a0, e);
             }
           }
-        } else {
+        }
+        if (plain < c.n) {
           const float4* nl = reinterpret_cast<const float4*>(smem + C::kOffLse) + l.st * 32;
           const float4* fac = reinterpret_cast<const float4*>(smem + C::kOffFactor) + (u % kWeighFactors) * 32;
           const int lo = narrow && c.n <= kWeighStacked ? (c.n + 15) / 16 * 16 : 0;  // where the second terms' products are
           float key_scale = 1.f;
           if (narrow) key_scale = scale_of(max(static_cast<uint32_t>(smem[C::kOffCode + ((x + 2 * j + blk) % kWeighCodes) * 128 + r]), 1u));
 #pragma unroll 1
-          for (int q = 0; q < c.n; q += 8) {
-            uint32_t s[8], s2[8];
-            tmem_ld8(ts + q, s);
-            if (lo) tmem_ld8(ts + lo + q, s2);
+          for (int q = plain; q < c.n; q += 4) {
+            uint32_t s[4], s2[4];
+            tmem_ld4(ts + q, s);
+            if (lo) tmem_ld4(ts + lo + q, s2);
             tmem_wait_ld();
-            if (lo) {
+            const float* n1 = reinterpret_cast<const float*>(nl) + q;
+            const float* f1 = reinterpret_cast<const float*>(fac) + q;
 #pragma unroll
-              for (int i = 0; i < 8; ++i) s[i] = __float_as_uint(__uint_as_float(s[i]) + __uint_as_float(s2[i]));
-            }
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const int col = q + 4 * k;
-              const float4 n4 = nl[col >> 2];
-              float4 f4 = make_float4(p.c, p.c, p.c, p.c);
-              if (narrow) f4 = fac[col >> 2];
-              auto one = [&](int i, float f, float nl1) {
-                const float y = __uint_as_float(s[4 * k + i]) * key_scale;
-                const float e = ex2_approx(narrow ? fmaf(y, f, nl1) : y * f);
-                return col + i >= c0 && col + i < c.n && nl1 != -INFINITY ? e : 0.f;
-              };
-              a0 = __fadd2_rn(a0, make_float2(one(0, f4.x, n4.x), one(1, f4.y, n4.y)));
-              a1 = __fadd2_rn(a1, make_float2(one(2, f4.z, n4.z), one(3, f4.w, n4.w)));
+            for (int i = 0; i < 4; ++i) {
+              float y = __uint_as_float(s[i]);
+              if (lo) y += __uint_as_float(s2[i]);
+              const float n0 = n1[i];
+              const float e = ex2_approx(narrow ? fmaf(y * key_scale, f1[i], n0) : y * p.c);
+              if (q + i >= c0 && q + i < c.n && n0 != -INFINITY) (i & 1 ? a0.y : a0.x) += e;
             }
           }
         }
