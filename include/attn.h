@@ -458,12 +458,17 @@ attn_status attn_qk_rotate(const void* Q, const void* K, void* Q_out, void* K_ou
  *         cu_seqlens_k[b] .. cu_seqlens_k[b + 1] - 1).  causal: bottom-right aligned, so a sequence
  *         with more keys than queries is a prompt over its prefix.
  *   What K and V hold where a row does not look, infinities and NaN among it, does not reach the row.
+ *   workspace  device, attn_prompt_workspace_bytes(...) bytes, 16-byte aligned, this call's own until
+ *         it is done: few query tiles over many keys are then split along the keys.  NULL: they are not.
  *   Asynchronous, allocates nothing.  Errors as attn_fwd.
  */
 attn_status attn_fwd_prompt(const void* Q, const void* K, const void* V, void* O, float* LSE, const int64_t* q_strides,
                             const int64_t* k_strides, const int64_t* v_strides, const int64_t* o_strides,
                             const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k, int B, int Hq, int Hkv,
-                            int max_seqlen_q, int total_q, int total_k, int d, float scale, int causal, void* stream);
+                            int max_seqlen_q, int total_q, int total_k, int d, float scale, int causal, void* workspace,
+                            size_t workspace_bytes, void* stream);
+/* Workspace with which attn_fwd_prompt splits keys, in bytes; 0: such a call would not (or bad sizes). */
+size_t attn_prompt_workspace_bytes(int B, int Hq, int max_seqlen_q, int total_q, int total_k, int d);
 
 /*
  * attn_cache_weigh -- the attention weight that cached keys receive from a call's queries.

@@ -20,7 +20,7 @@ EXPORTS = ("attn_fwd", "attn_fwd_ex", "attn_fwd_strided", "attn_fwd_varlen", "at
            "attn_version", "attn_fwd_noalloc", "attn_fwd_states", "attn_merge_states",
            "attn_splitkv_workspace_bytes", "attn_splitkv_splits", "attn_fwd_splitkv",
            "attn_cache_write", "attn_cache_read", "attn_cache_check", "attn_fwd_tree", "attn_tree_workspace_bytes",
-           "attn_qk_rotate", "attn_fwd_prompt", "attn_cache_weigh", "attn_cache_evict")
+           "attn_qk_rotate", "attn_fwd_prompt", "attn_prompt_workspace_bytes", "attn_cache_weigh", "attn_cache_evict")
 
 STATUS_NAMES = {0: "ATTN_OK", -1: "ATTN_ERR_NULLPTR", -2: "ATTN_ERR_BAD_SHAPE", -3: "ATTN_ERR_UNSUPPORTED_D",
                 -4: "ATTN_ERR_MISALIGNED", -5: "ATTN_ERR_NO_DEVICE", -6: "ATTN_ERR_LAUNCH", -7: "ATTN_ERR_TIMEOUT",
@@ -107,8 +107,11 @@ def load_library():
         lib.attn_qk_rotate.argtypes = [vp, vp, vp, vp, i64p, i64p, i64p, i64p, vp, vp, vp, vp, i, i, vp, vp, i, f, i, i,
                                        i, i, i, vp]
         lib.attn_qk_rotate.restype = i
-        lib.attn_fwd_prompt.argtypes = [vp, vp, vp, vp, vp, i64p, i64p, i64p, i64p, vp, vp, i, i, i, i, i, i, i, f, i, vp]
+        lib.attn_fwd_prompt.argtypes = [vp, vp, vp, vp, vp, i64p, i64p, i64p, i64p, vp, vp, i, i, i, i, i, i, i, f, i, vp,
+                                        ctypes.c_size_t, vp]
         lib.attn_fwd_prompt.restype = i
+        lib.attn_prompt_workspace_bytes.argtypes = [i, i, i, i, i, i]
+        lib.attn_prompt_workspace_bytes.restype = ctypes.c_size_t
         lib.attn_cache_weigh.argtypes = [vp, vp, cache, vp, vp, vp, i, vp, vp, i, i, i, f, f, vp]
         lib.attn_cache_weigh.restype = i
         lib.attn_cache_evict.argtypes = [cache, vp, vp, i, vp, i, vp, vp, vp, i, i, i, i, vp]
@@ -717,8 +720,13 @@ def attn_qk_rotate(Q, K, cu_seqlens=None, inv_freq=None, Q_out=None, K_out=None,
     return Q_out, K_out
 
 
-def attn_fwd_prompt(Q, K, V, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, O=None, LSE=None, *, scale=None, causal=True,
-                    stream=None):
+def prompt_workspace_bytes(B, Hq, max_seqlen_q, total_q, total_k, d) -> int:
+    """Bytes of workspace with which attn_fwd_prompt splits keys (0: it does not, or invalid arguments)."""
+    return load_library().attn_prompt_workspace_bytes(B, Hq, max_seqlen_q, total_q, total_k, d)
+
+
+def attn_fwd_prompt(Q, K, V, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, O=None, LSE=None, *, workspace=None, scale=None,
+                    causal=True, stream=None):
     """Attention of packed prompts whose query heads share K/V heads.
 
     Q [total_q, Hq, d], K, V [total_k, Hkv, d]: bf16 CUDA tensors with a contiguous last dimension
@@ -726,14 +734,17 @@ def attn_fwd_prompt(Q, K, V, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, O=None, L
     [B + 1]; max_seqlen_q >= the longest sequence's queries.  causal: bottom-right aligned, so more keys
     than queries are a prompt over its prefix.  Returns O [total_q, Hq, d] and LSE [Hq, total_q]
     (allocated when not given; rows outside every sequence are left as they were).  What K and V hold
-    where a row does not look does not reach it.
+    where a row does not look does not reach it.  Few tiles of 128 queries over many keys are split along
+    the keys, in a workspace: a uint8 tensor of prompt_workspace_bytes(...) that no other call in flight
+    uses; when not given, the stream's own is used, as in attn_fwd_tree.
     """
     import torch
     dev = Q.device
     away = _elsewhere(dev, stream)
     if away is not None:
         with away:
-            return attn_fwd_prompt(Q, K, V, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, O, LSE, scale=scale, causal=causal)
+            return attn_fwd_prompt(Q, K, V, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, O, LSE, workspace=workspace,
+                                   scale=scale, causal=causal)
     qs = _packed("Q", Q, dev)
     total_q, Hq, d = Q.shape
     ks = _packed("K", K, dev, None, d)
@@ -754,11 +765,18 @@ def attn_fwd_prompt(Q, K, V, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, O=None, L
         LSE = torch.empty((Hq, total_q), dtype=torch.float32, device=dev)
     elif LSE.shape != (Hq, total_q) or LSE.dtype != torch.float32 or LSE.device != dev or not LSE.is_contiguous():
         raise ValueError("LSE must be a contiguous fp32 tensor [Hq, total_q]")
-    rc = load_library().attn_fwd_prompt(Q.data_ptr(), K.data_ptr(), V.data_ptr(), O.data_ptr(), LSE.data_ptr(), qs, ks, vs,
-                                        os_, cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), B, Hq, Hkv,
-                                        int(max_seqlen_q), total_q, total_k, d,
-                                        1.0 / math.sqrt(d) if scale is None else scale, 1 if causal else 0,
-                                        torch._C._cuda_getCurrentRawStream(dev.index))
+    lib, raw, max_q = load_library(), torch._C._cuda_getCurrentRawStream(dev.index), int(max_seqlen_q)
+    if workspace is None:
+        nbytes = lib.attn_prompt_workspace_bytes(B, Hq, max_q, total_q, total_k, d)
+        if nbytes:
+            workspace = _tree_workspace(nbytes, dev, raw)
+    elif workspace.dtype != torch.uint8 or workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous uint8 tensor on Q's device")
+    rc = lib.attn_fwd_prompt(Q.data_ptr(), K.data_ptr(), V.data_ptr(), O.data_ptr(), LSE.data_ptr(), qs, ks, vs, os_,
+                             cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), B, Hq, Hkv, max_q, total_q, total_k, d,
+                             1.0 / math.sqrt(d) if scale is None else scale, 1 if causal else 0,
+                             None if workspace is None else workspace.data_ptr(),
+                             0 if workspace is None else workspace.numel(), raw)
     if rc != 0:
         _check(rc)
     return O, LSE

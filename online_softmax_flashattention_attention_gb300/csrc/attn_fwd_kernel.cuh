@@ -99,6 +99,9 @@ struct FwdParams {
   uint32_t dm_g, ds_g;
   const __nv_bfloat16* v;
   long long vs_r, vs_h;
+  // prompts whose keys may be split: where CTA 0 leaves the plan, and the states there is room for
+  struct PromptPlan* plan;
+  int slots;
 };
 
 __device__ __forceinline__ int fast_div(int n, uint32_t m, uint32_t s) {
@@ -209,6 +212,7 @@ struct Item {
   int min_limit;           // smallest key limit of the tile's rows
   int split, jb0, nblk;    // key blocks jb0 .. jb0 + nblk - 1 (nblk = 0: nothing to compute)
   bool valid;              // false: a tile past the end of a shorter packed sequence
+  int parts, slot;         // prompts with split keys: parts of the tile's keys, and where this one's state goes
 };
 
 // Packed sequences: perm[r] = the sequence of rank r in decreasing work Lq * Lk (ties by
@@ -391,11 +395,144 @@ struct PromptWalk {
   }
 };
 
+// Few tiles over many keys (short prompts over long prefixes) leave most SMs idle.  There a tile's key
+// blocks are split into parts that are items of their own: each leaves its state (m, l, o~), which
+// attn_prompt_merge_kernel joins.  How many parts a sequence's tiles have depends on all lengths, which
+// only the device knows, so every CTA works out the same plan.  Sequences that are split come first, the
+// others after them, each by an item's blocks, most first; an item is (sequence, tile, head, part), and
+// its state's place is its number.  Sequences that are not split store their rows as ever.
+struct PromptPlan {               // in the place of the order of packed sequences
+  int first[kLevelSeqs + 1];      // items before the rank's sequence
+  uint16_t seq[kLevelSeqs];
+  uint16_t parts[kLevelSeqs];     // of its tiles, 1: not split
+  int split;                      // ranks that are split
+};
+static_assert(sizeof(PromptPlan) <= 2 * kMaxSortedSeqs, "room");
+constexpr int kSplitLeast = 4;    // blocks of a part, about, at least
+constexpr float kSplitStart = 2.5f;  // an item's start and end, in blocks
+constexpr float kSplitJoin = 7;   // the states' way through memory and their join, in blocks
+
+// By all threads of the CTA, one for a sequence; scratch: four words a sequence and 16.  Warp w tries
+// parts of w + 4 quarters of the CTAs' share of all blocks, the last warp none.  The time is that of all
+// blocks and starts spread evenly, or that of the CTA with the most of the longer items.
+__device__ __noinline__ void plan_prompts(const FwdParams& p, int B, int* scratch, PromptPlan* plan) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, b = threadIdx.x;
+  constexpr int kNone = kThreads / 32 - 1;
+  int* tiles = scratch;                   // with all heads
+  int* blocks = scratch + kLevelSeqs;
+  int* parts = scratch + 2 * kLevelSeqs;
+  int* rank = scratch + 3 * kLevelSeqs;   // what the order goes by
+  float* est = reinterpret_cast<float*>(scratch + 4 * kLevelSeqs);
+  float* target = est + 8;
+  if (b < B) {
+    const int qs = min(max(__ldg(p.cu_q + b), 0), p.total_q), qe = min(max(__ldg(p.cu_q + b + 1), qs), p.total_q);
+    const int ks = min(max(__ldg(p.cu_k + b), 0), p.total_k), ke = min(max(__ldg(p.cu_k + b + 1), ks), p.total_k);
+    tiles[b] = min((qe - qs + kBM - 1) / kBM, p.num_qtiles) * p.H;
+    blocks[b] = (ke - ks + kBN - 1) / kBN;
+  }
+  __syncthreads();
+  auto parts_of = [](int k, float per) { return min(max(static_cast<int>(ceilf(static_cast<float>(k) * per)), 1), 1024); };
+  {
+    const float G = static_cast<float>(gridDim.x);
+    int work = 0, most = 0;
+    // (lengths of 2^16 blocks and more count as that, so that sums fit: a sequence has 2 tiles an SM at most)
+#pragma unroll 1
+    for (int o = lane; o < B; o += 32) {
+      work += tiles[o] * min(blocks[o], 1 << 16);
+      if (tiles[o] > 0) most = max(most, blocks[o]);
+    }
+    work = __reduce_add_sync(0xffffffffu, work);
+    most = __reduce_max_sync(0xffffffffu, most);
+    float len = fmaxf(static_cast<float>(work) / G, static_cast<float>(kSplitLeast)) * (1.f + 0.25f * static_cast<float>(warp));
+    if (warp == kNone) len = static_cast<float>(most);
+    const float per = warp == kNone ? 0.f : 1.f / len;
+    int items = 0, states = 0, many = 0, many_blocks = 0;
+#pragma unroll 1
+    for (int o = lane; o < B; o += 32) {
+      const int n = parts_of(blocks[o], per), k = min(blocks[o], 1 << 16);
+      items += tiles[o] * n;
+      if (n > 1) states += tiles[o] * n;
+      if (2.f * static_cast<float>(k) > len * static_cast<float>(n)) {
+        many += tiles[o] * n;
+        many_blocks += tiles[o] * k;
+      }
+    }
+    items = __reduce_add_sync(0xffffffffu, items);
+    states = __reduce_add_sync(0xffffffffu, states);
+    many = __reduce_add_sync(0xffffffffu, many);
+    many_blocks = __reduce_add_sync(0xffffffffu, many_blocks);
+    if (lane == 0) {
+      const float even = (static_cast<float>(work) + kSplitStart * static_cast<float>(items)) / G;
+      const float each = static_cast<float>(many_blocks) / static_cast<float>(max(many, 1)) + kSplitStart;
+      const float worst = fmaxf(even, ceilf(static_cast<float>(many) / G) * each);
+      est[warp] = states > p.slots ? INFINITY : states > 0 ? worst + kSplitJoin : worst;
+      target[warp] = per;
+    }
+  }
+  __syncthreads();
+  int best = kNone;
+#pragma unroll 1
+  for (int i = 0; i < kNone; ++i)
+    if (est[i] < est[best]) best = i;
+  // the order: split ones first, by blocks of an item
+  bool split = false;
+  if (b < B) {
+    const int n = parts_of(blocks[b], target[best]);
+    split = n > 1 && tiles[b] > 0;
+    parts[b] = n;
+    rank[b] = tiles[b] == 0 ? 0 : blocks[b] / n + 1 + (split ? 1 << 26 : 0);
+  }
+  const int splits = __syncthreads_count(split);
+  if (b < B) {
+    int r = 0, before = 0;
+#pragma unroll 1
+    for (int o = 0; o < B; ++o)
+      if (rank[o] > rank[b] || (rank[o] == rank[b] && o < b)) {
+        ++r;
+        before += tiles[o] * parts[o];
+      }
+    plan->seq[r] = static_cast<uint16_t>(b);
+    plan->parts[r] = static_cast<uint16_t>(parts[b]);
+    plan->first[r] = before;
+    if (r == B - 1) {
+      plan->first[B] = before + tiles[b] * parts[b];
+      plan->split = splits;
+    }
+  }
+  fence_proxy_async_smem();  // the scratch's accesses before the TMA copies that overwrite it
+  __syncthreads();
+  if (blockIdx.x == 0) {  // for the merge
+    if (b < static_cast<int>(sizeof(PromptPlan) / 4)) reinterpret_cast<int*>(p.plan)[b] = reinterpret_cast<const int*>(plan)[b];
+  }
+}
+static_assert(kLevelSeqs <= kThreads && sizeof(PromptPlan) / 4 <= kThreads, "a thread for each");
+
 // Item `ri` of this CTA for any of its roles; false past the last.  (The items of a CTA: item_of.)
 __device__ __forceinline__ int item_of(int r, int c, int G);
-template <bool kPacked, int BN, bool kByCost>
+template <bool kPacked, int BN, bool kByCost, bool kSplit = false>
 __device__ __forceinline__ bool next_item(const FwdParams& p, int ri, int cta, int G, const uint16_t* seq_perm, PromptWalk& walk,
                                           Item& it) {
+  if constexpr (kSplit) {
+    const PromptPlan* plan = reinterpret_cast<const PromptPlan*>(seq_perm);
+    const int B = p.BH / p.H, n = item_of(ri, cta, G);
+    if (n >= plan->first[B]) return false;
+    int r = max(walk.k, 0);
+    while (plan->first[r + 1] <= n) ++r;
+    walk.k = r;
+    it.parts = plan->parts[r];
+    it.slot = n;
+    const int i = n - plan->first[r], th = i / it.parts, part = i - th * it.parts;
+    const int tile = fast_div(th, p.dm_h, p.ds_h);
+    it.b = plan->seq[r];
+    it.hh = th - tile * p.H;
+    it.bh = it.b * p.H + it.hh;
+    it.split = 0;
+    fill_item<false, BN>(p, it, tile, nullptr);
+    const int each = it.nblk / it.parts, more = it.nblk - each * it.parts;  // `more` parts have one more
+    it.jb0 = each * part + min(part, more);
+    it.nblk = each + (part < more ? 1 : 0);
+    return true;
+  }
   if constexpr (kByCost) {
     if (reinterpret_cast<const PromptRanks*>(seq_perm)->by_cost) {
       int tile;
@@ -510,7 +647,7 @@ __device__ __forceinline__ const __nv_bfloat16* prompt_v_row(const FwdParams& p,
 // warps, before they hand P over, zero V's rows past the end, which belong to somebody else, and the
 // infinities and NaN among the others; rows that do see those get them added in the epilogue.  (An
 // eighth warp for it took 15000 cycles a tile, beside busy warps: 2048 tokens 73 us against 46.)
-// kByCost: its items by PromptWalk.
+// kByCost: its items by PromptWalk.  kStates too: by PromptPlan.
 template <int D, bool kStates, int kSoftPairs, bool kPacked, int BN = kBN, bool kPrompt = false, bool kByCost = false>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -519,6 +656,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   using C = FwdCfg<D, BN>;
   constexpr int kBN = BN;           // keys per block of this instantiation
   constexpr int kSBufs = C::kSBufs;
+  constexpr bool kSplit = kPrompt && kStates;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
@@ -590,7 +728,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   griddep_launch_dependents();
   uint16_t* seq_perm = reinterpret_cast<uint16_t*>(smem + C::kOffPerm);
   if constexpr (kPacked) {
-    if constexpr (kByCost)
+    if constexpr (kSplit)
+      plan_prompts(p, p.BH / p.H, reinterpret_cast<int*>(smem + C::kOffQ), reinterpret_cast<PromptPlan*>(seq_perm));
+    else if constexpr (kByCost)
       rank_prompts(p, p.BH / p.H, kBM, reinterpret_cast<int*>(smem + C::kOffQ), reinterpret_cast<PromptRanks*>(seq_perm));
     else if (p.seq_sort)
       rank_sequences(p, p.BH / p.H, reinterpret_cast<float*>(smem + C::kOffQ), seq_perm);
@@ -611,7 +751,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       PromptWalk walk;
       for (int ri = 0; ok; ++ri) {
         Item it;
-        if (!next_item<kPacked, kBN, kByCost>(p, ri, cta, G, seq_perm, walk, it)) break;
+        if (!next_item<kPacked, kBN, kByCost, kSplit>(p, ri, cta, G, seq_perm, walk, it)) break;
         if (it.nblk == 0) continue;
         const int hkv = kPrompt ? fast_div(it.hh, p.dm_g, p.ds_g) : it.hh;
         // the previous tile's Q must have been read by its last S product
@@ -673,7 +813,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         PromptWalk walk;
         for (int ri = 0; ok; ++ri) {
           Item it;
-          if (!next_item<kPacked, kBN, kByCost>(p, ri, cta, G, seq_perm, walk, it)) break;
+          if (!next_item<kPacked, kBN, kByCost, kSplit>(p, ri, cta, G, seq_perm, walk, it)) break;
           if (it.nblk == 0) continue;
           ok = mbar_wait(bar_q_full, kq & 1, wc, 3);
           for (int j = 0; ok && j < it.nblk; ++j, ++g) {
@@ -707,7 +847,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         PromptWalk walk;
         for (int ri = 0; ok; ++ri) {
           Item it;
-          if (!next_item<kPacked, kBN, kByCost>(p, ri, cta, G, seq_perm, walk, it)) break;
+          if (!next_item<kPacked, kBN, kByCost, kSplit>(p, ri, cta, G, seq_perm, walk, it)) break;
           if (it.nblk == 0) continue;
           // The first product of a tile overwrites o~.  The softmax warps read the previous
           // tile's o~ out before they write this tile's first P, and P_0 is awaited below,
@@ -751,14 +891,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     PromptWalk walk;
     Item it, ahead;  // by cost, the next item is looked up while this one's last product runs
     bool more = true;
-    if constexpr (kByCost) more = next_item<kPacked, kBN, kByCost>(p, 0, cta, G, seq_perm, walk, ahead);
+    if constexpr (kByCost) more = next_item<kPacked, kBN, kByCost, kSplit>(p, 0, cta, G, seq_perm, walk, ahead);
     for (int ri = 0; ok; ++ri) {
       if constexpr (kByCost) {
         if (!more) break;
         it = ahead;
-        if (!it.valid) more = next_item<kPacked, kBN, kByCost>(p, ri + 1, cta, G, seq_perm, walk, ahead);
+        if (!it.valid) more = next_item<kPacked, kBN, kByCost, kSplit>(p, ri + 1, cta, G, seq_perm, walk, ahead);
       } else {
-        if (!next_item<kPacked, kBN, kByCost>(p, ri, cta, G, seq_perm, walk, it)) break;
+        if (!next_item<kPacked, kBN, kByCost, kSplit>(p, ri, cta, G, seq_perm, walk, it)) break;
       }
       if (!it.valid) continue;  // a tile past the end of a shorter packed sequence
       const int row = it.q0 + r;
@@ -890,7 +1030,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(bar_p_full(gj % kSBufs));
       }
-      if constexpr (kByCost) more = next_item<kPacked, kBN, kByCost>(p, ri + 1, cta, G, seq_perm, walk, ahead);
+      if constexpr (kByCost) more = next_item<kPacked, kBN, kByCost, kSplit>(p, ri + 1, cta, G, seq_perm, walk, ahead);
       // ---- epilogue: one division by l; O and LSE out
       const int gl = g + nblk - 1;  // the tile's last block
       if (ok && nblk > 0) {
@@ -904,9 +1044,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (nblk > 0) {
           const bool odd = tag[u & 7] == static_cast<uint8_t>(u + 1);  // the same for all its warps
           ++u;
-          const int k0 = it.min_limit / kBN * kBN;  // the first key of the blocks that were repaired
+          int k0 = it.min_limit / kBN * kBN, k1 = limit;  // the first key of the blocks that were repaired, and past the row's last
+          if constexpr (kSplit) {
+            k0 = max(k0, it.jb0 * kBN);
+            k1 = min(k1, (it.jb0 + nblk) * kBN);
+          }
           if (ok && odd)
-            prompt_add_nonfinite(tl + C::kColO, D, prompt_v_row(p, it.hh, it.k_base + k0), p.vs_r, store ? limit - k0 : 0);
+            prompt_add_nonfinite(tl + C::kColO, D, prompt_v_row(p, it.hh, it.k_base + k0), p.vs_r, store ? k1 - k0 : 0);
         }
       }
       if (!kStates && C::kStageO && nblk > 0) {
@@ -972,10 +1116,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         continue;
       }
       if (!ok) break;
-      if constexpr (kStates) {
+      if (kStates && (!kSplit || it.parts > 1)) {
         // the state of this split, undivided: o~ and l as accumulated, m back in natural-log
-        // units of the scaled scores (m2 = c * max q.k, c = scale * log2 e, so m = m2 * ln 2)
-        const size_t ridx = (static_cast<size_t>(it.split) * p.BH + it.bh) * p.Nq + (store ? row : 0);
+        // units of the scaled scores (m2 = c * max q.k, c = scale * log2 e, so m = m2 * ln 2;
+        // prompts keep m2)
+        const size_t ridx = kSplit ? static_cast<size_t>(it.slot) * kBM + r
+                                   : (static_cast<size_t>(it.split) * p.BH + it.bh) * p.Nq + (store ? row : 0);
         float4* dst = reinterpret_cast<float4*>(p.st_o + ridx * D);
 #pragma unroll
         for (int q = 0; q < D / 32; ++q) {
@@ -995,7 +1141,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (store) {
-          p.st_m[ridx] = m * 0.69314718055994531f;  // -inf stays -inf for a row that saw no key
+          p.st_m[ridx] = kSplit ? m : m * 0.69314718055994531f;  // -inf stays -inf for a row that saw no key
           p.st_l[ridx] = l;
         }
       } else {  // straight from registers (d = 128, or a tile with no visible key)

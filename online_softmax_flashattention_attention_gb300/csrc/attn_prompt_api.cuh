@@ -4,6 +4,7 @@
 #pragma once
 
 #include "attn_evict_kernel.cuh"
+#include "attn_prompt_merge_kernel.cuh"
 #include "attn_rotate_kernel.cuh"
 #include "attn_weigh_kernel.cuh"
 
@@ -55,6 +56,30 @@ bool prompt_by_cost(int B, int Hkv, const Geometry& geo, int d, int causal) {
          kv_footprint(1, Hkv, static_cast<int>(geo.k_rows), d) <= kRankMajorMaxKvBytes;
 }
 
+template <int D>
+attn_status prompt_params(const void* Q, const void* K, const void* V, void* O, float* LSE, int B, int Hq, int Hkv, int max_q,
+                          float scale, int causal, uint32_t* status, const Geometry& geo, CUtensorMap* mq, CUtensorMap* mk,
+                          CUtensorMap* mv, CUtensorMap* mo, attn::FwdParams* p) {
+  attn_status st;
+  Geometry no_keys = geo;
+  no_keys.k_rows = 0;
+  if ((st = make_launch<D, false>(Q, K, V, O, LSE, B, Hq, max_q, 0, scale, causal, nullptr, status, StateOut{},
+                                  Variant{}, no_keys, mq, mk, mv, mo, p)) != ATTN_OK)
+    return st;
+  if (geo.k_rows > 0) {  // K and V have heads of their own
+    if ((st = make_map(mk, K, D, geo.k_rows, Hkv, 1, geo.ks)) != ATTN_OK) return st;
+    if ((st = make_map(mv, V, D, geo.k_rows, Hkv, 1, geo.vs)) != ATTN_OK) return st;
+  }
+  p->total_k = static_cast<int>(geo.k_rows);
+  p->v = static_cast<const __nv_bfloat16*>(V);
+  p->vs_r = geo.vs[2];
+  p->vs_h = geo.vs[1];
+  p->plan = nullptr;
+  p->slots = 0;
+  divisor(Hq / Hkv, &p->dm_g, &p->ds_g);
+  return ATTN_OK;
+}
+
 // kPair: d = 64, two query tiles a CTA (attn_fwd_pair_kernel).
 template <int D, bool kPair, bool kByCost>
 attn_status launch_prompt(const void* Q, const void* K, const void* V, void* O, float* LSE, int B, int Hq, int Hkv,
@@ -70,20 +95,8 @@ attn_status launch_prompt(const void* Q, const void* K, const void* V, void* O, 
   if (st != ATTN_OK) return st;
   CUtensorMap mq, mk, mv, mo;
   attn::FwdParams p;
-  Geometry no_keys = geo;
-  no_keys.k_rows = 0;
-  if ((st = make_launch<D, false>(Q, K, V, O, LSE, B, Hq, max_q, 0, scale, causal, nullptr, status, StateOut{},
-                                  Variant{}, no_keys, &mq, &mk, &mv, &mo, &p)) != ATTN_OK)
+  if ((st = prompt_params<D>(Q, K, V, O, LSE, B, Hq, Hkv, max_q, scale, causal, status, geo, &mq, &mk, &mv, &mo, &p)) != ATTN_OK)
     return st;
-  if (geo.k_rows > 0) {  // K and V have heads of their own
-    if ((st = make_map(&mk, K, D, geo.k_rows, Hkv, 1, geo.ks)) != ATTN_OK) return st;
-    if ((st = make_map(&mv, V, D, geo.k_rows, Hkv, 1, geo.vs)) != ATTN_OK) return st;
-  }
-  p.total_k = static_cast<int>(geo.k_rows);
-  p.v = static_cast<const __nv_bfloat16*>(V);
-  p.vs_r = geo.vs[2];
-  p.vs_h = geo.vs[1];
-  divisor(Hq / Hkv, &p.dm_g, &p.ds_g);
   if (kPair) {
     p.num_items = static_cast<int>(static_cast<long long>((p.num_qtiles + 1) / 2) * p.BH);
     p.order_div = (p.num_qtiles + 1) / 2;
@@ -98,6 +111,55 @@ attn_status launch_prompt(const void* Q, const void* K, const void* V, void* O, 
   else
     e = launch_pdl(attn::attn_fwd_kernel<D, false, 0, true, attn::kBN, true, kByCost>, grid, attn::kThreads, smem, stream, mq, mk,
                    mv, mo, p);
+  if (e != cudaSuccess) return fail(ATTN_ERR_LAUNCH, "kernel launch: %s", cudaGetErrorString(e));
+  return ATTN_OK;
+}
+
+// Whether a prompt's keys may be split (PromptPlan), by what the host knows: few tiles, and a sequence
+// with so many keys that its tiles would still run when the others are done.  With several sequences that
+// one is taken to have half of the prefixes' tokens.  Measured on GB300, split and not: 128 tokens over
+// 2048, 32 heads, d = 128 18.1 and 19.8 us, over 4096 22.1 and 32.7, over 16384 43.9 and 106.3; 512 over
+// 4096, 16 heads, d = 64 27.0 and 32.5; 7 prompts of 69 to 517 over prefixes up to 5000 20.3 and 44.6.
+// The other way round (two launches, the plan): 128 over 512, 32 heads, d = 128 14.2 and 9.9; 512 over
+// 4096 41.3 and 36.1; and, where sequences are as long as each other, 8 of 100 over 3000 61.8 and 57.0.
+bool prompt_splits(int B, int Hq, int max_q, int total_q, int total_k, int sms) {
+  if (B > attn::kLevelSeqs) return false;
+  const long long tiles = std::min(static_cast<long long>(total_q) / attn::kBM + B,
+                                   static_cast<long long>(B) * ((max_q + attn::kBM - 1) / attn::kBM)) * Hq;
+  if (tiles > 2ll * sms) return false;
+  const double before = std::max(total_k - total_q, 0) / (B > 1 ? 2.0 : 1.0);
+  const double blocks = (before + std::min(total_k, total_q) / static_cast<double>(B)) / attn::kBN;
+  return blocks * (1.0 - 1.5 * static_cast<double>(tiles) / B / sms) >= 11.0;
+}
+
+// Workspace of such a call: the plan, and 4 states an SM.
+constexpr size_t kPlanBytes = 1024;
+static_assert(sizeof(attn::PromptPlan) <= kPlanBytes, "room");
+size_t split_bytes(int sms, int d) { return kPlanBytes + static_cast<size_t>(4 * sms) * attn::kBM * (d + 2) * 4; }
+
+template <int D>
+attn_status launch_prompt_split(const void* Q, const void* K, const void* V, void* O, float* LSE, int B, int Hq, int Hkv,
+                                int max_q, float scale, int causal, cudaStream_t stream, int dev, uint32_t* status,
+                                const Geometry& geo, void* workspace) {
+  static bool attr_set[kMaxDevices] = {};
+  using C = attn::FwdCfg<D>;
+  auto kernel = attn::attn_fwd_kernel<D, true, 0, true, attn::kBN, true, false>;
+  attn_status st;
+  if ((st = set_smem_attr(kernel, C::kSmemAlloc, dev, attr_set)) != ATTN_OK) return st;
+  CUtensorMap mq, mk, mv, mo;
+  attn::FwdParams p;
+  if ((st = prompt_params<D>(Q, K, V, O, LSE, B, Hq, Hkv, max_q, scale, causal, status, geo, &mq, &mk, &mv, &mo, &p)) != ATTN_OK)
+    return st;
+  const int sms = sm_count(dev);
+  p.plan = static_cast<attn::PromptPlan*>(workspace);
+  p.slots = 4 * sms;
+  p.st_o = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kPlanBytes);
+  p.st_m = p.st_o + static_cast<size_t>(p.slots) * attn::kBM * D;
+  p.st_l = p.st_m + static_cast<size_t>(p.slots) * attn::kBM;
+  set_divisors(&p);
+  cudaError_t e = launch_pdl(kernel, static_cast<unsigned>(sms), attn::kThreads, C::kSmemAlloc, stream, mq, mk, mv, mo, p);
+  if (e == cudaSuccess)
+    e = launch_pdl(attn::attn_prompt_merge_kernel<D>, 4 * static_cast<unsigned>(sms), attn::kPromptMergeThreads, 0, stream, p);
   if (e != cudaSuccess) return fail(ATTN_ERR_LAUNCH, "kernel launch: %s", cudaGetErrorString(e));
   return ATTN_OK;
 }
@@ -232,10 +294,21 @@ attn_status attn_qk_rotate(const void* Q, const void* K, void* Q_out, void* K_ou
   return ATTN_OK;
 }
 
+size_t attn_prompt_workspace_bytes(int B, int Hq, int max_seqlen_q, int total_q, int total_k, int d) {
+  if (B < 1 || Hq < 1 || Hq > kMaxHeads || max_seqlen_q < 1 || total_q < 1 || total_k < 1 || (d != 64 && d != 128)) return 0;
+  if (max_seqlen_q > INT32_MAX - 255) return 0;
+  int dev;
+  uint32_t* status = nullptr;
+  if (get_device(&dev) != ATTN_OK || setup(dev, &status) != ATTN_OK) return 0;
+  const int sms = sm_count(dev);
+  return prompt_splits(B, Hq, max_seqlen_q, total_q, total_k, sms) ? split_bytes(sms, d) : 0;
+}
+
 attn_status attn_fwd_prompt(const void* Q, const void* K, const void* V, void* O, float* LSE, const int64_t* q_strides,
                             const int64_t* k_strides, const int64_t* v_strides, const int64_t* o_strides,
                             const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k, int B, int Hq, int Hkv,
-                            int max_seqlen_q, int total_q, int total_k, int d, float scale, int causal, void* stream) {
+                            int max_seqlen_q, int total_q, int total_k, int d, float scale, int causal, void* workspace,
+                            size_t workspace_bytes, void* stream) {
   g_err[0] = '\0';
   attn_status st;
   if (d != 64 && d != 128) return fail(ATTN_ERR_UNSUPPORTED_D, "d=%d; supported: 64, 128", d);
@@ -285,6 +358,14 @@ attn_status attn_fwd_prompt(const void* Q, const void* K, const void* V, void* O
   uint32_t* status = nullptr;
   if ((st = get_device(&dev)) != ATTN_OK || (st = setup(dev, &status)) != ATTN_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int sms = sm_count(dev);
+  if (workspace && prompt_splits(B, Hq, max_seqlen_q, total_q, total_k, sms)) {
+    if (odd16(workspace)) return fail(ATTN_ERR_MISALIGNED, "workspace must be 16-byte aligned");
+    if (workspace_bytes < split_bytes(sms, d))
+      return fail(ATTN_ERR_BAD_ARG, "workspace of %zu B is smaller than the %zu B needed", workspace_bytes, split_bytes(sms, d));
+    return (d == 128 ? launch_prompt_split<128> : launch_prompt_split<64>)(Q, K, V, O, LSE, B, Hq, Hkv, max_seqlen_q, scale, causal,
+                                                                           s, dev, status, g, workspace);
+  }
   const bool pair = d == 64 && use_pair_kernel(dev, B, Hq, g, causal), cost = prompt_by_cost(B, Hkv, g, d, causal);
   auto launch = d == 128 ? (cost ? launch_prompt<128, false, true> : launch_prompt<128, false, false>)
                 : pair   ? (cost ? launch_prompt<64, true, true> : launch_prompt<64, true, false>)

@@ -37,10 +37,10 @@ def _rotate(lib, **kw):
 
 def _prompt(lib, **kw):
     a = dict(Q=0x10000, K=0x20000, V=0x30000, O=0x40000, LSE=0x50000, qs=_st(4096, 128), ks=_st(1024, 128), vs=_st(1024, 128),
-             os=_st(4096, 128), cuq=0x60000, cuk=0x70000, B=2, Hq=32, Hkv=8, maxq=7, tq=7, tk=9, d=128, scale=0.1, causal=1)
+             os=_st(4096, 128), cuq=0x60000, cuk=0x70000, B=2, Hq=32, Hkv=8, maxq=7, tq=7, tk=9, d=128, scale=0.1, causal=1, ws=None, wsb=0)
     a.update(kw)
     return lib.attn_fwd_prompt(*[a[n] for n in ("Q", "K", "V", "O", "LSE", "qs", "ks", "vs", "os", "cuq", "cuk", "B", "Hq", "Hkv",
-                                                "maxq", "tq", "tk", "d", "scale", "causal")], None)
+                                                "maxq", "tq", "tk", "d", "scale", "causal", "ws", "wsb")], None)
 
 
 def _weigh(lib, cache=None, **kw):
