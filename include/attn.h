@@ -486,7 +486,8 @@ size_t attn_prompt_workspace_bytes(int B, int Hq, int max_seqlen_q, int total_q,
  *         layout (drafts that may be taken back).  Only positions of sequences with tokens in the
  *         call are written, and no page may be theirs twice.  A row that saw nothing (LSE = -inf)
  *         adds nothing.
- *   scale must be at least 2^-100, and |LSE| / scale below 2^127.  Nothing is added atomically: the
+ *   scale must be at least 2^-100, |LSE| / scale below 2^127, and max_pages * page_size at most 2^31 -
+ *   2^17.  Nothing is added atomically: the
  *   same call gives the same bits.  Asynchronous, allocates nothing; device-side timeouts through
  *   attn_status_sync or attn_cache_check.
  */
@@ -508,6 +509,7 @@ attn_status attn_cache_weigh(const void* Q, const float* LSE, const attn_cache* 
  *         pages, which then must be no other sequence's of the call.
  *   kept  device int32 [B, num_heads, keep]: the positions kept, increasing; -1 past the sequence's
  *         tokens.  out_lens device int32 [B]: min(lens, keep); not lens itself.
+ *   keep and max_pages * page_size are at most 2^31 - 2^17.
  *   Positions without a page count as weight -inf and are packed as zeros of weight 0, places without
  *         one are not written; both are reported by attn_cache_check.
  *   Asynchronous, allocates nothing.

@@ -10,6 +10,10 @@
 
 namespace {
 
+// Positions of a sequence that weights are added to or evicted by, at most: the kernels count them in 32
+// bits, by steps of up to 4096.
+constexpr long long kMostPositions = INT32_MAX - 0x1ffffll;
+
 // Strides (token, head) in elements of packed [total, heads, d] tensors; may_repeat: an input whose
 // elements may be seen more than once.
 attn_status check_strides(const int64_t* s, const char* name, bool may_repeat) {
@@ -380,6 +384,8 @@ attn_status attn_cache_weigh(const void* Q, const float* LSE, const attn_cache* 
   g_err[0] = '\0';
   attn_status st = check_cache(cache, max_pages, false);
   if (st != ATTN_OK) return st;
+  if (static_cast<long long>(max_pages) * cache->page_size > kMostPositions)
+    return fail(ATTN_ERR_BAD_SHAPE, "max_pages=%d: a sequence has at most %lld positions", max_pages, kMostPositions);
   if (B < 0 || Hq < 0 || total_q < 0)
     return fail(ATTN_ERR_BAD_SHAPE, "negative size (B=%d Hq=%d total_q=%d)", B, Hq, total_q);
   if (Hq > kMaxHeads) return fail(ATTN_ERR_BAD_SHAPE, "Hq=%d; at most %d", Hq, kMaxHeads);
@@ -438,6 +444,8 @@ attn_status attn_cache_evict(const attn_cache* cache, float* weights, const int3
     return fail(ATTN_ERR_BAD_SHAPE, "B=%d keep=%d sink=%d recent=%d; none negative, sink + recent at most keep", B, keep,
                 sink, recent);
   const long long room = static_cast<long long>(max_pages) * cache->page_size;
+  if (room > kMostPositions || keep > kMostPositions)
+    return fail(ATTN_ERR_BAD_SHAPE, "a sequence of %lld positions, keep=%d; at most %lld", room, keep, kMostPositions);
   if (!in_place) {
     if (out_max_pages < 0 || static_cast<long long>(out_max_pages) * cache->page_size > INT32_MAX - 255)
       return fail(ATTN_ERR_BAD_SHAPE, "out_max_pages=%d: a sequence has at most 2^31 - 256 positions", out_max_pages);

@@ -20,7 +20,9 @@
 // heads, Q's, then K's.  Blocks are persistent, so that the frequencies (64-bit floats, slow here) and
 // weights are made once a block.
 //
-// Bound: DRAM.
+// Bound: DRAM.  58327 tokens of 9 prompts, 32 / 8 heads, d = 128: 220 us, 5.4 TB/s, 0.80 of a plain
+// copy's rate; with partners a lane's exchange away 340, without the next rows ahead 230.  One token,
+// 3.4 us, is a launch and three loads that wait for each other.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -115,13 +117,14 @@ __global__ void __launch_bounds__(kRotThreads, 3) attn_qk_rotate_kernel(const Ro
                                                    : __bfloat162float(static_cast<const __nv_bfloat16*>(w)[i % D]);
   }
   if (threadIdx.x < r) step[threadIdx.x] = rotate_step(__ldg(p.freq + threadIdx.x));
-  for (int t0 = blockIdx.x * kRotTokens; t0 < p.total; t0 += gridDim.x * kRotTokens) {
-    const int tok = t0 + tk;
+  // (unsigned: the last step may pass 2^31)
+  for (unsigned t0 = blockIdx.x * kRotTokens; t0 < static_cast<unsigned>(p.total); t0 += gridDim.x * kRotTokens) {
+    const unsigned tok = t0 + tk;
     __syncthreads();  // the last tokens' angles have been used
     if (threadIdx.x < kRotTokens) {
-      const int t = t0 + threadIdx.x;
+      const unsigned t = t0 + threadIdx.x;
       long long pos = 0;
-      in[threadIdx.x] = t < p.total && rotate_position(p, t, &pos);
+      in[threadIdx.x] = t < static_cast<unsigned>(p.total) && rotate_position(p, static_cast<int>(t), &pos);
       at[threadIdx.x] = pos;
     }
     __syncthreads();
@@ -136,7 +139,7 @@ __global__ void __launch_bounds__(kRotThreads, 3) attn_qk_rotate_kernel(const Ro
       turn[t][f] = make_float2(c, s);
     }
     __syncthreads();
-    if (tok >= p.total || !in[tk]) continue;  // whole warps: a token's groups are
+    if (tok >= static_cast<unsigned>(p.total) || !in[tk]) continue;  // whole warps: a token's groups are
     static_assert(kPerTok * kLanes % 32 == 0, "a warp has one token");
 
 #pragma unroll

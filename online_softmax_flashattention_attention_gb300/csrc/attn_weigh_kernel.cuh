@@ -16,8 +16,8 @@
 //   with one block the copies alone were 7 TB/s.
 //
 // Shared memory's bandwidth is what a prompt is bound by, before exponentials (1130 cycles for 256 x
-// 128 scores) and products (1090): both operands of a product come from there.  So the columns' LSE
-// does not: it enters the product as one more step of 16, K's side 1, 1, 1, 0 ..., Q's side -LSE /
+// 128 scores) and the tensor pipe (1090): both operands of a product come from there.  So the columns'
+// LSE does not: it enters the product as one more step of 16, K's side 1, 1, 1, 0 ..., Q's side -LSE /
 // scale as three bf16 terms (24 bits), and what a thread reads is ready for exp2.
 //
 // Units lie rank major, a sequence's runs of keys by position and a run's heads together: with many
@@ -35,6 +35,15 @@
 // One with a single tile would pay that for every key it sees: there the codes go to the tensor cores
 // as they are and the queries are split into two e4m3 terms, as attn_tree_tile_kernel.cuh describes;
 // the query row's power of two and the key's scale multiply the score afterwards.
+//
+// Measured, 32 / 8 heads, d = 128.  A prompt of 8192 tokens in bf16 243 us, 0.60 of the measured product
+// rate: a step of 256 keys x 128 columns takes 2170 cycles, and shared memory feeds its products (18 of
+// 128 x 128 x 16, both operands from there) for some 1800 of them.  64 e4m3 contexts of 900 to 16384
+// tokens, a token each, 150 us where the keys alone take 69 at a copy's rate: a step of 256 keys is a
+// chain of copy, product, read and sum, some 2200 cycles at two blocks in hand, and CTAs with as many
+// steps as each other differ by a quarter in time (173000 to 262000 cycles).  One context of 517 tokens
+// 6.3 us: a launch, the units' list, three loads that wait for each other, a product.  (A thread a key
+// with scalar products: 23.6 ms, 1502 us and 10; one MMA warp and the LSE from shared memory: 312, 213.)
 #pragma once
 
 #include <cuda.h>

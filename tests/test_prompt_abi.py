@@ -160,3 +160,14 @@ def test_python_refusals():
         pkg.attn_cache_weigh(z(1, 4, 64), f(4, 1), z(2, 2, 16, 64), f(2, 2, 16), i(1, 2), None, i(2))
     with pytest.raises(ValueError):
         pkg.attn_cache_evict(z(2, 2, 16, 64), z(2, 2, 16, 64), f(2, 2, 16), i(1, 2), i(1), 4)
+
+
+def test_most_positions(lib):
+    """Steps of a kernel must not pass 2^31: a sequence of more than 2^31 - 2^17 positions is refused."""
+    most = (2 ** 31 - 2 ** 17) // 16
+    page = _cache(page_size=16)
+    for n, status in ((most + 1, -2), (2 ** 27 - 16, -2), (most, -1)):  # (then the missing pointer is found)
+        assert _weigh(lib, page, max_pages=n, Q=0) == status
+        assert _evict(lib, page, max_pages=n, lens=0) == status
+    for keep, status in ((2 ** 31 - 1, -2), (2 ** 31 - 2 ** 17 + 1, -2), (2 ** 31 - 2 ** 17, -1)):
+        assert _evict(lib, keep=keep, lens=0) == status
