@@ -8,6 +8,7 @@ raised.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 import threading
@@ -447,8 +448,6 @@ def _batch_args(dev, block_table, cu_seqlens, lens):
 def _elsewhere(dev, stream):
     """Context that makes a call's device current, and its stream for what is allocated there
     (so that buffers made here belong to the stream that uses them); None when both already are."""
-    import contextlib
-
     import torch
     if dev.type != "cuda":
         raise ValueError("the cache must be on a CUDA device")
@@ -456,6 +455,7 @@ def _elsewhere(dev, stream):
         return None if torch._C._cuda_getDevice() == dev.index else torch.cuda.device(dev)
     if stream.device != dev:
         raise ValueError("stream is on another device than the tensors")
+    import contextlib
     both = contextlib.ExitStack()
     both.enter_context(torch.cuda.device(dev))
     both.enter_context(torch.cuda.stream(stream))
@@ -638,6 +638,12 @@ def attn_fwd_tree(Q, k_cache, v_cache, block_table, ctx_lens, cu_seqlens_q, max_
 WEIGHT_BF16, WEIGHT_FP32 = 0, 1
 
 
+@functools.lru_cache(maxsize=256)
+def _strides(row, head):
+    """A pair of strides as the library takes them (never written to)."""
+    return _Strides(row, head)
+
+
 def _packed(name, t, dev, heads=None, d=None):
     """Checks a packed bf16 tensor [total, heads, d] with a contiguous last dimension; returns its strides."""
     import torch
@@ -648,7 +654,7 @@ def _packed(name, t, dev, heads=None, d=None):
     st = t.stride()
     if st[2] != 1 and t.numel():
         raise ValueError(f"{name} must have a contiguous last dimension")
-    return _Strides(st[0], st[1])
+    return _strides(st[0], st[1])
 
 
 def attn_qk_rotate(Q, K, cu_seqlens=None, inv_freq=None, Q_out=None, K_out=None, *, start_lens=None, positions=None,
@@ -706,12 +712,15 @@ def attn_qk_rotate(Q, K, cu_seqlens=None, inv_freq=None, Q_out=None, K_out=None,
         wtype = WEIGHT_FP32 if w.dtype == torch.float32 else WEIGHT_BF16
         wptr[i] = w.data_ptr()
     if Q_out is None:
-        Q_out = torch.empty((total, Hq, d), dtype=torch.bfloat16, device=dev)
+        Q_out, qos = torch.empty((total, Hq, d), dtype=torch.bfloat16, device=dev), _strides(Hq * d, d)
+    else:
+        qos = _packed("Q_out", Q_out, dev, Hq, d)
     if K_out is None:
-        K_out = torch.empty((total, Hkv, d), dtype=torch.bfloat16, device=dev)
-    if Q_out.shape != Q.shape or K_out.shape != K.shape:
+        K_out, kos = torch.empty((total, Hkv, d), dtype=torch.bfloat16, device=dev), _strides(Hkv * d, d)
+    else:
+        kos = _packed("K_out", K_out, dev, Hkv, d)
+    if Q_out.shape[0] != total or K_out.shape[0] != total:
         raise ValueError("Q_out and K_out must be shaped like Q and K")
-    qos, kos = _packed("Q_out", Q_out, dev), _packed("K_out", K_out, dev)
     rc = load_library().attn_qk_rotate(Q.data_ptr(), K.data_ptr(), Q_out.data_ptr(), K_out.data_ptr(), qs, ks, qos, kos,
                                        cu_ptr, start_ptr, pos_ptr, freq_ptr, r, 1 if interleaved else 0, wptr[0], wptr[1],
                                        wtype, eps, B, Hq, Hkv, d, total, torch._C._cuda_getCurrentRawStream(dev.index))
@@ -757,10 +766,11 @@ def attn_fwd_prompt(Q, K, V, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, O=None, L
         if B < 0 or t.numel() != B + 1 or t.dtype != torch.int32 or t.device != dev or not t.is_contiguous():
             raise ValueError("cu_seqlens_q and cu_seqlens_k must be contiguous int32 tensors [B + 1] on Q's device")
     if O is None:
-        O = torch.empty((total_q, Hq, d), dtype=torch.bfloat16, device=dev)
-    elif O.shape != Q.shape:
-        raise ValueError("O must be shaped like Q")
-    os_ = _packed("O", O, dev)
+        O, os_ = torch.empty((total_q, Hq, d), dtype=torch.bfloat16, device=dev), _strides(Hq * d, d)
+    else:
+        os_ = _packed("O", O, dev, Hq, d)
+        if O.shape[0] != total_q:
+            raise ValueError("O must be shaped like Q")
     if LSE is None:
         LSE = torch.empty((Hq, total_q), dtype=torch.float32, device=dev)
     elif LSE.shape != (Hq, total_q) or LSE.dtype != torch.float32 or LSE.device != dev or not LSE.is_contiguous():

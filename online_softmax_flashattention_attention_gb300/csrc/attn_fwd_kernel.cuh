@@ -83,7 +83,7 @@ struct FwdParams {
   // (split + 1) * split_blocks) and writes the state (m, l, o~) instead of O and LSE
   int num_splits;          // >= 1
   int split_blocks;        // key blocks per split, >= 1
-  int seq_sort;            // packed sequences: take them in decreasing work (rank_sequences)
+  int seq_sort;            // packed sequences: take them in decreasing work (rank_sequences); kByCost: see rank_prompts
   int o_v8;                // every O row starts on a 32-byte boundary: 32-byte stores
   float* st_o;             // [num_splits, BH, Nq, D] fp32 o~ (unnormalised)
   float* st_m;             // [num_splits, BH, Nq] running max of the scaled scores (natural log units)
@@ -312,7 +312,7 @@ __device__ __forceinline__ void fill_item(const FwdParams& p, Item& it, int qtil
   it.nblk = it.valid ? nsplit : 0;
 }
 
-// Causal prompts whose K and V fit in L2 are taken by cost.  A tile's level is the number of its key
+// Causal prompts are taken by cost (but see prompt_by_cost).  A tile's level is the number of its key
 // blocks, as it is for whole tiles: tile t of a sequence whose keys go `off` tiles past its queries is
 // on level t + off, and the sequence has levels up to tiles + off.  Levels go from the highest down, on
 // each the sequences that reach it, in rank order, with all their heads: every CTA's tiles go from long
@@ -340,11 +340,15 @@ __device__ __noinline__ void rank_prompts(const FwdParams& p, int B, int rows, i
   }
   __syncthreads();
   long long all = 0, empty = 0;
+  int most = 0, some = 0;
   for (int b = 0; b < B; ++b) {
     all += scratch[2 * b];
+    most = max(most, scratch[2 * b]);
+    some += scratch[2 * b] > 0;
     if (scratch[2 * b]) empty += scratch[2 * b + 1];
   }
-  const bool by_cost = 2 * empty <= all;
+  // seq_sort = 2: only where lengths differ, the longest being a quarter above the average
+  const bool by_cost = 2 * empty <= all && (p.seq_sort != 2 || 4ll * most * some > 5 * all);
   if (threadIdx.x == 0) ranks->by_cost = by_cost;
   // by heads, the order is that of rank_sequences: decreasing work
   auto weight = [&](int b) {

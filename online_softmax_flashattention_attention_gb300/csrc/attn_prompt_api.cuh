@@ -50,14 +50,21 @@ void fix_strides(const int64_t* s, int rows, int heads, int d, long long* row, l
   *row = rows > 1 ? s[0] : static_cast<long long>(heads) * d;
 }
 
-// Whether a prompt's tiles go by cost (PromptWalk): where sequences may have eight and more and all K and
-// V stay in L2 meanwhile; else head by head, as the packed forward has them.  Measured on GB300, 32 / 8
-// heads, d = 128: 8192 tokens 455 -> 423 us, 9 prompts of 900 to 8192 tokens 1885 -> 1860; d = 64: 8192
-// tokens 339 -> 307.  The other way round, for the ranks that the order needs: 77 tokens 6.2 -> 7.3 us; 7
-// prompts of 61 to 517 tokens over prefixes of up to 5000, 16 / 4 heads, d = 64: 45 -> 50.
-bool prompt_by_cost(int B, int Hkv, const Geometry& geo, int d, int causal) {
-  return causal && B <= attn::kLevelSeqs && geo.grid_q > 7 * attn::kBM &&
-         kv_footprint(1, Hkv, static_cast<int>(geo.k_rows), d) <= kRankMajorMaxKvBytes;
+// Whether a prompt's tiles go by cost (PromptWalk): 0 no, then head by head, as the packed forward has
+// them; 1 yes; 2 where the sequences' lengths differ.  By cost, all K and V are read side by side, so beside
+// sequences of eight tiles and more it takes that they stay in L2, or that a block read from DRAM serves
+// enough scores (four heads' tiles at d = 128, where sequences of 2048 tokens on average are wanted too, one
+// CTA's two tiles at d = 64).  Measured on GB300, by heads and by cost, us.  In L2, 32 / 8 heads: 8192
+// tokens 455 and 423, at d = 64 339 and 307.  Past it, 150 to 330 MB of K and V, d = 128: 9 prompts of 900 to
+// 8192 1893 and 1720, 24 of 500 to 4000 854 and 826, but 40 of 1000 549 and 593, 20 of 2048 722 and 752 (by
+// heads in the same kernel 716); the 9 with a K/V head for two query heads 1896 and 1917, for one 1910 and
+// 2159.  d = 64: 18 of 900 to 8192 2900 and 2420, 80 of 1000 864 and 737.  Too short for the ranks that the
+// order needs: 77 tokens 6.2 and 7.3; 7 of 61 to 517 over prefixes of up to 5000, 16 / 4 heads, 45 and 50.
+int prompt_by_cost(int B, int Hq, int Hkv, const Geometry& geo, int d, int causal, bool pair) {
+  if (!causal || B > attn::kLevelSeqs || geo.grid_q <= 7 * attn::kBM) return 0;
+  if (kv_footprint(1, Hkv, static_cast<int>(geo.k_rows), d) <= kRankMajorMaxKvBytes) return 1;
+  if (d == 128) return Hq / Hkv >= 4 && geo.k_rows >= 2048ll * B ? 2 : 0;
+  return pair || Hq / Hkv >= 2 ? 1 : 0;
 }
 
 template <int D>
@@ -88,7 +95,7 @@ attn_status prompt_params(const void* Q, const void* K, const void* V, void* O, 
 template <int D, bool kPair, bool kByCost>
 attn_status launch_prompt(const void* Q, const void* K, const void* V, void* O, float* LSE, int B, int Hq, int Hkv,
                           int max_q, float scale, int causal, cudaStream_t stream, int dev, uint32_t* status,
-                          const Geometry& geo) {
+                          const Geometry& geo, int cost) {
   static bool attr_set[kMaxDevices] = {};
   using C = std::conditional_t<kPair, attn::PairCfg, attn::FwdCfg<D>>;
   attn_status st;
@@ -105,7 +112,7 @@ attn_status launch_prompt(const void* Q, const void* K, const void* V, void* O, 
     p.num_items = static_cast<int>(static_cast<long long>((p.num_qtiles + 1) / 2) * p.BH);
     p.order_div = (p.num_qtiles + 1) / 2;
   }
-  if (kByCost) p.seq_sort = 1;  // the ranks' place
+  if (kByCost) p.seq_sort = cost;  // the ranks' place
   set_divisors(&p);
   const unsigned grid = static_cast<unsigned>(std::min(p.num_items, sm_count(dev)));
   const int smem = p.seq_sort ? C::kSmemAlloc : C::kSmemAllocNoPerm;
@@ -370,11 +377,12 @@ attn_status attn_fwd_prompt(const void* Q, const void* K, const void* V, void* O
     return (d == 128 ? launch_prompt_split<128> : launch_prompt_split<64>)(Q, K, V, O, LSE, B, Hq, Hkv, max_seqlen_q, scale, causal,
                                                                            s, dev, status, g, workspace);
   }
-  const bool pair = d == 64 && use_pair_kernel(dev, B, Hq, g, causal), cost = prompt_by_cost(B, Hkv, g, d, causal);
+  const bool pair = d == 64 && use_pair_kernel(dev, B, Hq, g, causal);
+  const int cost = prompt_by_cost(B, Hq, Hkv, g, d, causal, pair);
   auto launch = d == 128 ? (cost ? launch_prompt<128, false, true> : launch_prompt<128, false, false>)
                 : pair   ? (cost ? launch_prompt<64, true, true> : launch_prompt<64, true, false>)
                          : (cost ? launch_prompt<64, false, true> : launch_prompt<64, false, false>);
-  return launch(Q, K, V, O, LSE, B, Hq, Hkv, max_seqlen_q, scale, causal, s, dev, status, g);
+  return launch(Q, K, V, O, LSE, B, Hq, Hkv, max_seqlen_q, scale, causal, s, dev, status, g, cost);
 }
 
 attn_status attn_cache_weigh(const void* Q, const float* LSE, const attn_cache* cache, const float* weights, float* out,

@@ -78,6 +78,31 @@ def test_against_definition(case):
         _hold(Q, K, V, nq, nk, O, LSE, at)
 
 
+@pytest.mark.parametrize("d,heads,kv,nq", [
+    (128, 32, 8, [7000, 2100, 9000, 1500, 8000]),   # K and V past L2, by cost as lengths differ
+    (128, 32, 8, [4200] * 6),                       # by heads as they do not
+    (64, 32, 16, [7000, 2100, 9000, 1500, 8000]),
+    (128, 8, 8, [12000, 9000, 6000]),               # a K/V head each: by heads
+])
+def test_past_l2(d, heads, kv, nq):
+    """Whichever order the tiles go in: the rows of every sequence and head are those of the sequence alone."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(33)
+    pkg, cu = _pkg(), _cu(nq)
+    Q = torch.randn((sum(nq), heads, d), generator=g, device="cuda").to(torch.bfloat16)
+    K, V = (torch.randn((sum(nq), kv, d), generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+    assert 2 * K.numel() * K.element_size() > 96 << 20
+    O, LSE = pkg.attn_fwd_prompt(Q, K, V, cu, cu, max(nq))
+    pkg.status_sync()
+    q0 = 0
+    for n in nq:
+        at = slice(q0, q0 + n)
+        one = _cu([n])
+        want = pkg.attn_fwd_varlen(Q[at], *(x[at].repeat_interleave(heads // kv, 1) for x in (K, V)), one, one, n, causal=True)
+        assert torch.equal(O[at], want[0]) and torch.equal(LSE[:, at], want[1])
+        q0 += n
+
+
 @pytest.mark.parametrize("d", [64, 128])
 def test_without_causality_and_lies(d):
     """Not causal is not by cost; lengths past the rows, or fewer rows than max_seqlen_q, change nothing else."""
