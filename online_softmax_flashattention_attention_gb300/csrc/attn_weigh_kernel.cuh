@@ -159,6 +159,17 @@ __device__ __forceinline__ WeighCols weigh_cols(const WeighParams& p, int first,
   return c;
 }
 
+// mma_ss_f8 by one elected lane of a warp that agrees on everything.
+__device__ __forceinline__ void mma_ss_f8_elect(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
 // 32 lanes x 4 columns of 32-bit.
 __device__ __forceinline__ void tmem_ld4(uint32_t taddr, uint32_t* r) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
@@ -192,6 +203,7 @@ struct WeighCfg {
   static constexpr int kLse = kF8 ? 3 : 4;               // tiles whose LSE is at hand
   static constexpr int kMaxK = kFewK > kManyK ? kFewK : kManyK, kMaxQ = kManyQ;
   static constexpr int kPool = kFewK * kStageK + kFewQ * kTileBytes;
+  static_assert(kFewK % 2 == 0 && kManyK % 2 == 0, "a step's two blocks have neighbouring stages");
   static_assert(kManyK * kStageK + kManyQ * kTileBytes <= kPool, "both divisions of the stages");
   static constexpr int kOffWide = kPool;                                    // Q's stages, then K's, before it
   static constexpr int kOffOnes = kOffWide + kWide * kTileBytes;            // the step of 16: K's side,
@@ -446,29 +458,33 @@ __global__ void __launch_bounds__(WeighCfg<D, kF8>::kThreads, 1)
         page[i] = at.pages[lane + 32 * i];
       }
     })) {
-      // (a row lies in its page's at row - (page * Hkv + h) * page_size)
+      // A step's two blocks at a time, 16 lanes with a slice each (a warp beside busy ones gets an instruction
+      // every ten cycles: block by block this was as slow as the products).  The ring's stages are even.
+      // A row lies in its page's at row - (page * Hkv + h) * page_size.
 #pragma unroll 1
-      for (int blk = 0; blk < 2 * t.steps; ++blk, ++x, k.next(p.ring_k)) {  // a block without keys is a block of anything
-        const long long rw = blk < 4 ? row[0] : row[1];
-        const int pg = blk < 4 ? page[0] : page[1];
-        const bool mine = lane / 8 == (blk & 3) && rw >= 0 && (lane & 7) % box16 == 0;
-        const int boxes = __popc(__ballot_sync(0xffffffffu, mine));
-        ok = __all_sync(0xffffffffu, tile_wait(bar_k_free(k.st), k.ph ^ 1u, wc, 62));
+      for (int st = 0; st < t.steps; ++st, x += 2, k.next(p.ring_k), k.next(p.ring_k)) {  // a block without keys is a block of anything
+        const long long rw = st < 2 ? row[0] : row[1];
+        const int pg = st < 2 ? page[0] : page[1];
+        const bool mine = lane / 16 == (st & 1) && rw >= 0 && (lane & 7) % box16 == 0;
+        const uint32_t who = __ballot_sync(0xffffffffu, mine) >> (16 * (st & 1));
+        ok = __all_sync(0xffffffffu, tile_wait(bar_k_free(k.st), k.ph ^ 1u, wc, 62) && tile_wait(bar_k_free(k.st + 1), k.ph ^ 1u, wc, 62));
         if (!ok) break;
         constexpr int kRowB = kF8 ? D : 128;
         constexpr int kSubs = kF8 ? 1 : C::kSub;
-        if (lane == 0) mbar_arrive_expect_tx(bar_k_full(k.st), boxes * p.box_rows * (kSubs * kRowB + (kF8 ? 1 : 0)));
+        if (lane < 2)
+          mbar_arrive_expect_tx(bar_k_full(k.st + lane), __popc((who >> (8 * lane)) & 0xffu) * p.box_rows * (kSubs * kRowB + (kF8 ? 1 : 0)));
         __syncwarp();
         if (mine) {
-          const uint32_t dst = sK + k.st * C::kStageK + 16 * (lane & 7) * kRowB;
+          const int h = (lane >> 3) & 1;
+          const uint32_t dst = sK + (k.st + h) * C::kStageK + 16 * (lane & 7) * kRowB, bar = bar_k_full(k.st + h);
           const int in_page = static_cast<int>(rw - (static_cast<long long>(pg) * p.Hkv + t.h) * p.page);
 #pragma unroll
-          for (int s = 0; s < kSubs; ++s) tma_load_4d(dst + s * C::kSubBytes, &tmK, bar_k_full(k.st), s * 64, in_page, t.h, pg, pol);
+          for (int s = 0; s < kSubs; ++s) tma_load_4d(dst + s * C::kSubBytes, &tmK, bar, s * 64, in_page, t.h, pg, pol);
           if constexpr (kF8)
-            bulk_load(sbase + C::kOffCode + (x % kWeighCodes) * 128 + 16 * (lane & 7), p.ks + rw, p.box_rows, bar_k_full(k.st));
+            bulk_load(sbase + C::kOffCode + ((x + h) % kWeighCodes) * 128 + 16 * (lane & 7), p.ks + rw, p.box_rows, bar);
         }
-        live |= 1u << k.st;
-        par = (par & ~(1u << k.st)) | (k.ph << k.st);
+        live |= 3u << k.st;
+        par = (par & ~(3u << k.st)) | (k.ph ? 3u << k.st : 0u);
       }
       if (!ok) break;
     }
@@ -512,7 +528,10 @@ __global__ void __launch_bounds__(WeighCfg<D, kF8>::kThreads, 1)
         if ((live >> s) & 1u) mbar_wait_drain(bar_q_full(s), (par >> s) & 1u, p.timeout_ns);
   } else if (warp == 2 || warp == 7) {
     // ================================================================ products
+    // (all lanes go the same way and one elected issues, with what comes from memory made the warp's: as in
+    // attn_fwd_pair_kernel)
     const int h = warp == 7 ? 1 : 0;  // the block
+    auto wait = [&](uint32_t bar, uint32_t parity, uint32_t site) { return __all_sync(0xffffffffu, tile_wait(bar, parity, wc, site)) != 0; };
     const uint32_t dhi = (1024u >> 4) | (1u << 14) | (2u << 29);
     const uint32_t dhi8 = D == 128 ? dhi : (512u >> 4) | (1u << 14) | (4u << 29);  // e4m3 rows of 64 bytes: 64-byte swizzle
     const uint32_t klo = (sK >> 4) | (1u << 16), wlo = ((sbase + C::kOffWide) >> 4) | (1u << 16);
@@ -525,15 +544,17 @@ __global__ void __launch_bounds__(WeighCfg<D, kF8>::kThreads, 1)
     bool ok = true;
     WeighUnit t;
     while (job(t, ok, 65)) {
+      t.nq = __shfl_sync(0xffffffffu, t.nq, 0);
+      t.steps = __shfl_sync(0xffffffffu, t.steps, 0);
       const bool single = t.nq == 1, narrow = kF8 && single;
-      const int first = t.first();
-      if (lane == 0) {
+      const uint32_t cols = __shfl_sync(0xffffffffu, (weigh_cols(p, t.first(), t.T, 0).n + 15) / 16 * 16, 0);
+      {
         uint32_t a = 0, wst = 0;
         if (kF8 && !narrow) {  // widened keys: two stages, one for each issuer
           if (h) w.next(NWm);
           wst = w.st;
-          ok = tile_wait(bar_w_full(w.st), w.ph, wc, 66);
-          if (ok) mbar_arrive(bar_k_free(k.st));  // its codes have been read
+          ok = wait(bar_w_full(w.st), w.ph, 66);
+          if (ok && lane == 0) mbar_arrive(bar_k_free(k.st));  // its codes have been read
           a = wlo + w.st * (C::kTileBytes >> 4);
           if (!h) w.next(NWm);
           w.next(NWm);
@@ -542,77 +563,75 @@ __global__ void __launch_bounds__(WeighCfg<D, kF8>::kThreads, 1)
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks) {
             const uint32_t off = (ks / 4) * (C::kSubBytes >> 4) + (ks % 4) * 2;
-            mma_ss(dst, desc(dhi, a + off), desc(dhi, b + off), idesc, ks > 0 ? 1u : 0u);
+            mma_ss_elect(dst, desc(dhi, a + off), desc(dhi, b + off), idesc, ks > 0 ? 1u : 0u);
           }
           // the LSE last: everything before it is a sum of small terms
-          mma_ss(dst, weigh_step_desc(sbase + C::kOffOnes), weigh_step_desc(sbase + C::kOffStep + l.st * kWeighStepBytes), idesc, 1u);
+          mma_ss_elect(dst, weigh_step_desc(sbase + C::kOffOnes), weigh_step_desc(sbase + C::kOffStep + l.st * kWeighStepBytes), idesc, 1u);
         };
-        const uint32_t cols = (weigh_cols(p, first, t.T, 0).n + 15) / 16 * 16;
         if (single) {
-          ok = narrow ? tile_wait(bar_w_full(w.st), w.ph, wc, 68) : tile_wait(bar_q_full(q.st), q.ph, wc, 69);
+          ok = narrow ? wait(bar_w_full(w.st), w.ph, 68) : wait(bar_q_full(q.st), q.ph, 69);
           const bool stacked = narrow && cols <= kWeighStacked;
           const uint32_t idesc = narrow ? (1u << 4) | (((stacked ? 2 * cols : cols) >> 3) << 17) | (8u << 24)  // e4m3 x e4m3 -> fp32
                                         : idesc_bf16_f32(128, cols, 0);
           const uint32_t b = narrow ? wlo + w.st * (C::kTileBytes >> 4) : qlo + q.st * (C::kTileBytes >> 4);
           for (int j = 0; ok && j < t.steps; ++j, ++g) {
             const uint32_t bf = 2 * (g & 1) + h, dst = tmem + 128u * bf;
-            ok = tile_wait(bar_k_full(k.st), k.ph, wc, 66) && tile_wait(bar_s_free(bf), ((g >> 1) & 1) ^ 1, wc, 70);
+            ok = wait(bar_k_full(k.st), k.ph, 66) && wait(bar_s_free(bf), ((g >> 1) & 1) ^ 1, 70);
             if (!ok) break;
             tc_fence_after();
             a = klo + k.st * (C::kStageK >> 4);
             if constexpr (kF8) {
 #pragma unroll
-              for (int ks = 0; ks < D / 32; ++ks) mma_ss_f8(dst, desc(dhi8, a + ks * 2), desc(dhi8, b + ks * 2), idesc, ks > 0 ? 1u : 0u);
+              for (int ks = 0; ks < D / 32; ++ks) mma_ss_f8_elect(dst, desc(dhi8, a + ks * 2), desc(dhi8, b + ks * 2), idesc, ks > 0 ? 1u : 0u);
               if (!stacked) {
 #pragma unroll
-                for (int ks = 0; ks < D / 32; ++ks) mma_ss_f8(dst, desc(dhi8, a + ks * 2), desc(dhi8, b + (128 * D >> 4) + ks * 2), idesc, 1u);
+                for (int ks = 0; ks < D / 32; ++ks) mma_ss_f8_elect(dst, desc(dhi8, a + ks * 2), desc(dhi8, b + (128 * D >> 4) + ks * 2), idesc, 1u);
               }
             } else {
               product(dst, b, idesc);
             }
-            mma_commit(bar_s_full(bf));
-            mma_commit(bar_k_free(k.st));
+            mma_commit_elect(bar_s_full(bf));
+            mma_commit_elect(bar_k_free(k.st));
             k.next(p.ring_k);
             k.next(p.ring_k);
           }
           if (narrow) {
-            if (ok) mbar_arrive(bar_q_free(q.st));  // its rows had been read when their two terms came
-            mma_commit(bar_w_free(w.st));
+            if (ok && lane == 0) mbar_arrive(bar_q_free(q.st));  // its rows had been read when their two terms came
+            mma_commit_elect(bar_w_free(w.st));
             w.next(NWm);
           } else {
-            mma_commit(bar_q_free(q.st));
+            mma_commit_elect(bar_q_free(q.st));
           }
           q.next(p.ring_q);
           l.next(C::kLse);
         } else {
           if constexpr (!kF8) {
-            ok = tile_wait(bar_k_full(k.st), k.ph, wc, 66);
+            ok = wait(bar_k_full(k.st), k.ph, 66);
             a = klo + k.st * (C::kStageK >> 4);
           }
           const uint32_t idesc = idesc_bf16_f32(128, cols, 0);
           for (int j = 0; ok && j < t.nq; ++j, ++g) {
             const uint32_t bf = 2 * (g & 1) + h;
-            ok = tile_wait(bar_q_full(q.st), q.ph, wc, 69) && tile_wait(bar_s_free(bf), ((g >> 1) & 1) ^ 1, wc, 70);
+            ok = wait(bar_q_full(q.st), q.ph, 69) && wait(bar_s_free(bf), ((g >> 1) & 1) ^ 1, 70);
             if (!ok) break;
             tc_fence_after();
             // with the first tile's columns, which are never fewer (what lies past a tile's own is not looked at)
             product(tmem + 128u * bf, qlo + q.st * (C::kTileBytes >> 4), idesc);
-            mma_commit(bar_s_full(bf));
-            mma_commit(bar_q_free(q.st));
+            mma_commit_elect(bar_s_full(bf));
+            mma_commit_elect(bar_q_free(q.st));
             q.next(p.ring_q);
             l.next(C::kLse);
           }
           if constexpr (kF8) {  // nobody but this issuer had the stage
-            mma_commit(bar_w_free(wst));
-            mma_commit(bar_w_free(wst));
+            mma_commit_elect(bar_w_free(wst));
+            mma_commit_elect(bar_w_free(wst));
           } else {
-            mma_commit(bar_k_free(k.st));
+            mma_commit_elect(bar_k_free(k.st));
           }
           k.next(p.ring_k);
           k.next(p.ring_k);
         }
       }
-      ok = __shfl_sync(0xffffffffu, static_cast<int>(ok), 0) != 0;
       if (!ok) break;
     }
     // every product issued must finish before tensor memory is released
