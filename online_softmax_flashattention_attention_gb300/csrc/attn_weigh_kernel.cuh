@@ -723,12 +723,12 @@ __global__ void __launch_bounds__(WeighCfg<D, kF8>::kThreads, 1)
     bool ok = true;
     WeighRing l;
     WeighUnit t;
-    // The rows of this thread's keys: in a unit of one tile its steps are every other one, two at most.
-    long long row0[2] = {-1, -1};
-    auto rows = [&](const WeighJob& at, const WeighUnit& un) {
+    // Where this thread's keys are: in a unit of one tile its steps are every other one, two at most.
+    long long at[2] = {-1, -1};
+    auto rows = [&](const WeighJob& job, const WeighUnit& un) {
       const int s0 = un.nq == 1 ? (g ^ pair) & 1 : 0;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) row0[i] = at.rows[16 * (s0 + 2 * i) + 8 * blk + r / 16];
+      for (int i = 0; i < 2; ++i) at[i] = job.rows[16 * (s0 + 2 * i) + 8 * blk + r / 16];
     };
     static_assert(kWeighSteps <= 4, "two steps a group");
     for (; job_more(t, ok, 73, rows); ++u) {
@@ -737,21 +737,15 @@ __global__ void __launch_bounds__(WeighCfg<D, kF8>::kThreads, 1)
       const int j0 = (g ^ pair) & 1;                    // this pair's first step
       const bool last = single || ((n - 1) & 1) == j0;  // whether the result is this pair's to write
       float old[2] = {0.f, 0.f}, sum = 0.f, before = 0.f;  // before: the first step's sum
-      int sees = 0;      // tokens from first + sees on see this thread's key
-      long long at = -1;
-      auto key = [&](int i) {  // the thread's key of step i (its place in row0), if there is one
-        const int pos = t.key0 + (single ? kWeighStep * (j0 + 2 * i) : 0) + 128 * blk + r;
-        const long long row = i ? row0[1] : row0[0];
-        at = row >= 0 && pos < t.n && (!single || j0 + 2 * i < n) ? row + (r & 15) : -1;
-        sees = max(pos - t.ctx - first, 0);
-        return pos;
-      };
+      const int pos = t.key0 + (single ? kWeighStep * j0 : 0) + 128 * blk + r;  // of the first
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int pos = key(i);
-        if (last && at >= 0 && pos < t.ctx && p.decay != 0.f && (i == 0 || single)) old[i] = p.w[at];
+        const int here = pos + 2 * kWeighStep * i;
+        const bool is = at[i] >= 0 && here < t.n && (single ? j0 + 2 * i < n : i == 0 && last);
+        at[i] = is ? at[i] + (r & 15) : -1;
+        if (is && here < t.ctx && p.decay != 0.f) old[i] = p.w[at[i]];
       }
-      key(0);
+      int sees = max(pos - t.ctx - first, 0);  // tokens from first + sees on see this thread's key
       // A tile that this group does not look at, handed back once its LSE has come: earlier it would be
       // handed back for the tile before it at its place.
       auto pass = [&]() {
@@ -769,7 +763,7 @@ __global__ void __launch_bounds__(WeighCfg<D, kF8>::kThreads, 1)
           continue;
         }
         const WeighCols c = weigh_cols(p, first, t.T, single ? 0 : j);
-        if (single) key((j - j0) >> 1);
+        if (single) sees = max(pos + kWeighStep * (j - j0) - t.ctx - first, 0);
         int c0 = 0;     // the key's first column of the tile
         int plain = narrow ? 0 : c.n & ~31;  // columns that every key of the warp sees, 32 at a time
         if (c.tok - first < kWeighStep) {
@@ -845,10 +839,8 @@ __global__ void __launch_bounds__(WeighCfg<D, kF8>::kThreads, 1)
         if (!ok) break;
         // (the old weights have had both steps' time to come)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          key(i);
-          if (at >= 0) p.out[at] = fmaf(p.decay, old[i], i ? sum : before);
-        }
+        for (int i = 0; i < 2; ++i)
+          if (at[i] >= 0) p.out[at[i]] = fmaf(p.decay, old[i], i ? sum : before);
       } else {
         // the sum of the even tiles and of the odd ones: the same two whichever pair has which
         const int slot = u % kWeighParts;
@@ -858,7 +850,7 @@ __global__ void __launch_bounds__(WeighCfg<D, kF8>::kThreads, 1)
           ok = __all_sync(0xffffffffu, tile_wait(bar_part(slot, blk), (u / kWeighParts) & 1, wc, 79));
           if (!ok) break;
           sum += parts[slot * 256];
-          if (at >= 0) p.out[at] = fmaf(p.decay, old[0], sum);
+          if (at[0] >= 0) p.out[at[0]] = fmaf(p.decay, old[0], sum);
         }
       }
       // (every unit, so that a slot's turns follow from u; in a unit of one tile by the pair that has its second step)
