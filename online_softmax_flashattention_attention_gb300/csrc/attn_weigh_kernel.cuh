@@ -746,6 +746,7 @@ __global__ void __launch_bounds__(WeighCfg<D, kF8>::kThreads, 1)
         if (is && here < t.ctx && p.decay != 0.f) old[i] = p.w[at[i]];
       }
       int sees = max(pos - t.ctx - first, 0);  // tokens from first + sees on see this thread's key
+      WeighCols c = weigh_cols(p, first, t.T, 0);
       // A tile that this group does not look at, handed back once its LSE has come: earlier it would be
       // handed back for the tile before it at its place.
       auto pass = [&]() {
@@ -762,7 +763,7 @@ __global__ void __launch_bounds__(WeighCfg<D, kF8>::kThreads, 1)
           if (!ok) break;
           continue;
         }
-        const WeighCols c = weigh_cols(p, first, t.T, single ? 0 : j);
+        if (!single) c = weigh_cols(p, first, t.T, j);
         if (single) sees = max(pos + kWeighStep * (j - j0) - t.ctx - first, 0);
         int c0 = 0;     // the key's first column of the tile
         int plain = narrow ? 0 : c.n & ~31;  // columns that every key of the warp sees, 32 at a time
@@ -773,7 +774,7 @@ __global__ void __launch_bounds__(WeighCfg<D, kF8>::kThreads, 1)
         ok = __all_sync(0xffffffffu, tile_wait(bar_s_full(bf), ((g + j) >> 1) & 1, wc, 74));
         if (!ok) break;
         tc_fence_after();
-        if (odd[l.st]) plain = 0;
+        if (plain > 0 && odd[l.st]) plain = 0;
         float2 a0 = make_float2(0.f, 0.f), a1 = make_float2(0.f, 0.f);
         {
           const float2 cc = make_float2(p.c, p.c);
