@@ -807,15 +807,17 @@ __global__ void __launch_bounds__(WeighCfg<D, kF8>::kThreads, 1)
             tmem_ld4(ts + q, s);
             if (lo) tmem_ld4(ts + lo + q, s2);
             tmem_wait_ld();
-            const float* n1 = reinterpret_cast<const float*>(nl) + q;
-            const float* f1 = reinterpret_cast<const float*>(fac) + q;
+            const float4 n4 = nl[q >> 2];  // (-infinity past the tile's columns)
+            float4 f4 = make_float4(p.c, p.c, p.c, p.c);
+            if (narrow) f4 = fac[q >> 2];
+            const float n1[4] = {n4.x, n4.y, n4.z, n4.w}, f1[4] = {f4.x, f4.y, f4.z, f4.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               float y = __uint_as_float(s[i]);
               if (lo) y += __uint_as_float(s2[i]);
-              const float n0 = n1[i];
-              const float e = ex2_approx(narrow ? fmaf(y * key_scale, f1[i], n0) : y * p.c);
-              if (q + i >= c0 && q + i < c.n && n0 != -INFINITY) (i & 1 ? a0.y : a0.x) += e;
+              // (key_scale is 1 and the LSE in the product already where the operands are bf16)
+              const float e = ex2_approx(fmaf(y * key_scale, f1[i], narrow ? n1[i] : 0.f));
+              if (q + i >= c0 && n1[i] != -INFINITY) (i & 1 ? a0.y : a0.x) += e;
             }
           }
         }
