@@ -199,7 +199,7 @@ struct WeighCfg {
   // What the rings of K and Q share: (one tile a unit, as in decoding) stages of K for the bytes in
   // flight, or (several) of Q, whose way from L2 is 2000 to 3000 cycles with all SMs at it.
   static constexpr int kFewK = D == 128 ? 4 : 8;
-  static constexpr int kFewQ = 2;
+  static constexpr int kFewQ = 2;  // (not 1: the LSE's warps see every other turn of a single stage, and could not tell them apart)
   static constexpr int kManyK = kF8 ? (D == 128 ? 2 : 4) : 2;
   static constexpr int kManyQ = kF8 ? (D == 128 ? 3 : 4) : (D == 128 ? 4 : 8);
   static constexpr int kLse = kF8 ? 3 : 4;               // tiles whose LSE is at hand
@@ -574,6 +574,7 @@ __global__ void __launch_bounds__(WeighCfg<D, kF8>::kThreads, 1)
         };
         if (single) {
           ok = narrow ? wait(bar_w_full(w.st), w.ph, 68) : wait(bar_q_full(q.st), q.ph, 69);
+          if (narrow && ok && lane == 0) mbar_arrive(bar_q_free(q.st));  // its rows have been read: their two terms are there
           const bool stacked = narrow && cols <= kWeighStacked;
           const uint32_t idesc = narrow ? (1u << 4) | (((stacked ? 2 * cols : cols) >> 3) << 17) | (8u << 24)  // e4m3 x e4m3 -> fp32
                                         : idesc_bf16_f32(128, cols, 0);
@@ -600,7 +601,6 @@ __global__ void __launch_bounds__(WeighCfg<D, kF8>::kThreads, 1)
             k.next(p.ring_k);
           }
           if (narrow) {
-            if (ok && lane == 0) mbar_arrive(bar_q_free(q.st));  // its rows had been read when their two terms came
             mma_commit_elect(bar_w_free(w.st));
             w.next(NWm);
           } else {
