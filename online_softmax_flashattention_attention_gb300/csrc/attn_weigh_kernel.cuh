@@ -36,14 +36,15 @@
 // as they are and the queries are split into two e4m3 terms, as attn_tree_tile_kernel.cuh describes;
 // the query row's power of two and the key's scale multiply the score afterwards.
 //
-// Measured, 32 / 8 heads, d = 128.  A prompt of 8192 tokens in bf16 243 us, 0.60 of the measured product
-// rate: a step of 256 keys x 128 columns takes 2170 cycles, and shared memory feeds its products (18 of
-// 128 x 128 x 16, both operands from there) for some 1800 of them.  64 e4m3 contexts of 900 to 16384
-// tokens, a token each, 150 us where the keys alone take 69 at a copy's rate: a step of 256 keys is a
-// chain of copy, product, read and sum, some 2200 cycles at two blocks in hand, and CTAs with as many
-// steps as each other differ by a quarter in time (173000 to 262000 cycles).  One context of 517 tokens
-// 6.3 us: a launch, the units' list, three loads that wait for each other, a product.  (A thread a key
-// with scalar products: 23.6 ms, 1502 us and 10; one MMA warp and the LSE from shared memory: 312, 213.)
+// Measured, 32 / 8 heads, d = 128.  A prompt of 8192 tokens in bf16 230 us, 0.64 of the measured product
+// rate: a step of 256 keys x 128 columns takes some 2000 cycles, and shared memory feeds its products (18
+// of 128 x 128 x 16, both operands from there) for some 1800 of them.  64 e4m3 contexts of 900 to 16384
+// tokens, a token each, 115 us where the keys alone take 69 at a copy's rate: no unit is busy, but 28 warps
+// of eight roles share the instruction caches (2.2 of 7 warps a scheduler wait for instructions), so that
+// each instruction of a role's step counts: a key's place worked out three times a unit instead of once was
+// 134 us, all else alike.  One context of 517 tokens 6.1 us: a launch, the units' list, three loads that wait
+// for each other, a product.  (A thread a key with scalar products: 23.6 ms, 1502 us and 10; one MMA warp and
+// the LSE from shared memory: 312 and 213.)
 #pragma once
 
 #include <cuda.h>
