@@ -554,7 +554,7 @@ _kept_lock = threading.Lock()
 
 
 def _tree_workspace(nbytes, dev, raw):
-    """attn_fwd_tree's default workspace: one kept for each stream and host thread, whose calls run
+    """attn_fwd_tree's and attn_fwd_prompt's default workspace: one kept for each stream and host thread, whose calls run
     one after the other (two threads may interleave their launches on a stream), until the thread
     ends; a captured call gets its own, which belongs to the graph (graphs may run at once)."""
     import torch

@@ -40,8 +40,8 @@
 // rate: a step of 256 keys x 128 columns takes some 2000 cycles, and shared memory feeds its products (18
 // of 128 x 128 x 16, both operands from there) for some 1800 of them.  64 e4m3 contexts of 900 to 16384
 // tokens, a token each, 115 us where the keys alone take 69 at a copy's rate: no unit is busy, but 28 warps
-// of eight roles share the instruction caches (2.2 of 7 warps a scheduler wait for instructions), so that
-// each instruction of a role's step counts: a key's place worked out three times a unit instead of once was
+// of eight roles share the instruction caches (one of a scheduler's seven waits for instructions, another
+// issues every second cycle), so that each instruction of a role's step counts: a key's place worked out three times a unit instead of once was
 // 134 us, all else alike.  One context of 517 tokens 6.1 us: a launch, the units' list, three loads that wait
 // for each other, a product.  (A thread a key with scalar products: 23.6 ms, 1502 us and 10; one MMA warp and
 // the LSE from shared memory: 312 and 213.)

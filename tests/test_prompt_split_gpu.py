@@ -77,7 +77,7 @@ def test_values_that_are_not_finite_stay_with_who_sees_them(d, kind):
     cu, cu_k = _cu(nq), _cu([a + b for a, b in zip(nq, before)])
     Q, K, V = bf16(rng, (cu[-1], 2, d)), bf16(rng, (cu_k[-1], 2, d)), bf16(rng, (cu_k[-1], 2, d))
     bad = {"nan": [math.nan], "inf": [math.inf, -math.inf], "both": [math.nan, math.inf]}[kind]
-    for i, row in enumerate((3001, 3070, 3072, 3150, 3199, 3200 + 1760, 3200 + 1800, 3200 + 700)):
+    for i, row in enumerate((3001, 3070, 3073, 3150, 3199, 3200 + 1760, 3200 + 1800, 3200 + 700)):
         V[row, i % 2, 7 * i] = bad[i % len(bad)]
     K[3190, 1] = math.nan
     K[3200 + 1801, 0] = math.nan
