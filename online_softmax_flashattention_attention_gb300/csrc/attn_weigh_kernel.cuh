@@ -702,8 +702,8 @@ __global__ void __launch_bounds__(WeighCfg<D, kF8>::kThreads, 1)
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
+          mbar_arrive(bar_lse_full(l.st));  // before q_full: a group that looks at the tile does not wait for this
           mbar_arrive(bar_q_full(q.st));
-          mbar_arrive(bar_lse_full(l.st));
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -878,7 +878,9 @@ __global__ void __launch_bounds__(WeighCfg<D, kF8>::kThreads, 1)
         if (t.nq == 1) {
           // ---- the queries as two e4m3 terms, a lane 8 columns
           constexpr int kL = D / 8;  // lanes of a row
-          ok = tile_wait(bar_q_full(q.st), q.ph, wc, 76) && tile_wait(bar_w_free(w.st), w.ph ^ 1u, wc, 77);
+          // (w_free first: after several tiles, which this role does not wait for, it says that the last of them
+          // have come, and so that q_full is at this tile's turn)
+          ok = tile_wait(bar_w_free(w.st), w.ph ^ 1u, wc, 77) && tile_wait(bar_q_full(q.st), q.ph, wc, 76);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           const int rows = weigh_cols(p, first, t.T, 0).n, ch = lane % kL;
@@ -923,6 +925,16 @@ __global__ void __launch_bounds__(WeighCfg<D, kF8>::kThreads, 1)
           x += 2 * t.steps;
         } else {
           // ---- both blocks of keys: codes times scale as bf16, a thread a key
+          // This role does not wait for the keys of a unit with one tile.  Both stages free: its products are
+          // done, its keys have come, and k_full is at this unit's turn (a turn too early, the stage would be
+          // handed back before its copy has landed).
+          {
+            WeighRing other = w;
+            other.next(NWm);
+            ok = tile_wait(bar_w_free(w.st), w.ph ^ 1u, wc, 77) && tile_wait(bar_w_free(other.st), other.ph ^ 1u, wc, 77);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+          }
 #pragma unroll 1
           for (int h = 0; h < 2; ++h, ++x, w.next(NWm), k.next(p.ring_k)) {
             ok = tile_wait(bar_k_full(k.st), k.ph, wc, 78) && tile_wait(bar_w_free(w.st), w.ph ^ 1u, wc, 77);

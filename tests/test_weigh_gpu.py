@@ -329,3 +329,17 @@ def test_pools_past_32_bits():
     pkg.cache_check()
     assert torch.equal(out[P - 1], want[a[3][0, 0].long()])
     assert torch.equal(out[P - 2, :, :46], want[a[3][0, 1].long(), :, :46])
+
+
+@pytest.mark.parametrize("hkv,G,d,page,B,ctx,T", [
+    (16, 7, 128, 16, 28, (11, 22), (1, 401)),
+    (16, 7, 64, 16, 28, (11, 22), (1, 401)),
+    (8, 4, 128, 32, 100, (0, 700), (1, 80)),
+    (8, 8, 128, 16, 150, (200, 1500), (1, 33)),
+    (4, 16, 128, 64, 120, (0, 90), (0, 20)),
+    (2, 100, 128, 16, 60, (0, 3000), (1, 2)),
+])
+def test_one_tile_and_several_in_turn(hkv, G, d, page, B, ctx, T):
+    """e4m3 units whose codes go to the products as they are, next to ones that are widened: a role that sees only the
+    keys of some units must not take one turn of a stage for another."""
+    test_batches_against_torch(hkv, G, d, page, B, ctx, T, True)
