@@ -39,9 +39,10 @@
 // Measured, 32 / 8 heads, d = 128.  A prompt of 8192 tokens in bf16 230 us, 0.64 of the measured product
 // rate: a step of 256 keys x 128 columns takes some 2000 cycles, and shared memory feeds its products (18
 // of 128 x 128 x 16, both operands from there) for some 1800 of them.  64 e4m3 contexts of 900 to 16384
-// tokens, a token each, 115 us where the keys alone take 69 at a copy's rate: no unit is busy, but 28 warps
+// tokens, a token each, 114 us where the keys alone take 69 at a copy's rate: no unit is busy, but 28 warps
 // of eight roles share the instruction caches (one of a scheduler's seven waits for instructions, another
-// issues every second cycle), so that each instruction of a role's step counts: a key's place worked out three times a unit instead of once was
+// issues every second cycle; two waits more in the code of the widening warps, which do not run here, 122),
+// so that each instruction of a role's step counts: a key's place worked out three times a unit instead of once was
 // 134 us, all else alike.  One context of 517 tokens 6.1 us: a launch, the units' list, three loads that wait
 // for each other, a product.  (A thread a key with scalar products: 23.6 ms, 1502 us and 10; one MMA warp and
 // the LSE from shared memory: 312 and 213.)
@@ -929,16 +930,14 @@ __global__ void __launch_bounds__(WeighCfg<D, kF8>::kThreads, 1)
           // done, its keys have come, and k_full is at this unit's turn (a turn too early, the stage would be
           // handed back before its copy has landed).
           {
-            WeighRing other = w;
-            other.next(NWm);
-            ok = tile_wait(bar_w_free(w.st), w.ph ^ 1u, wc, 77) && tile_wait(bar_w_free(other.st), other.ph ^ 1u, wc, 77);
-            ok = __all_sync(0xffffffffu, ok);
+            WeighRing both = w;
+#pragma unroll 1
+            for (int h = 0; ok && h < 2; ++h, both.next(NWm)) ok = __all_sync(0xffffffffu, tile_wait(bar_w_free(both.st), both.ph ^ 1u, wc, 77));
             if (!ok) break;
           }
 #pragma unroll 1
           for (int h = 0; h < 2; ++h, ++x, w.next(NWm), k.next(p.ring_k)) {
-            ok = tile_wait(bar_k_full(k.st), k.ph, wc, 78) && tile_wait(bar_w_free(w.st), w.ph ^ 1u, wc, 77);
-            ok = __all_sync(0xffffffffu, ok);
+            ok = __all_sync(0xffffffffu, tile_wait(bar_k_full(k.st), k.ph, wc, 78));
             if (!ok) break;
             const uint8_t* src = smem + p.ring_q * C::kTileBytes + k.st * C::kStageK + r * D;
             uint8_t* dst = smem + C::kOffWide + w.st * C::kTileBytes + r * 128;
