@@ -42,10 +42,10 @@
 // tokens, a token each, 114 us where the keys alone take 69 at a copy's rate: no unit is busy, but 28 warps
 // of eight roles share the instruction caches (one of a scheduler's seven waits for instructions, another
 // issues every second cycle; two waits more in the code of the widening warps, which do not run here, 122),
-// so that each instruction of a role's step counts: a key's place worked out three times a unit instead of once was
-// 134 us, all else alike.  One context of 517 tokens 6.1 us: a launch, the units' list, three loads that wait
-// for each other, a product.  (A thread a key with scalar products: 23.6 ms, 1502 us and 10; one MMA warp and
-// the LSE from shared memory: 312 and 213.)
+// so that each instruction of a role's step counts: a key's place worked out three times a unit instead of
+// once was 134 us, all else alike.  One context of 517 tokens 6.1 us: a launch, the units' list, three loads
+// that wait for each other, a product.  (A thread a key with scalar products: 23.6 ms, 1502 us and 10; one
+// MMA warp and the LSE from shared memory: 312 and 213.)
 #pragma once
 
 #include <cuda.h>
