@@ -7,9 +7,10 @@
 // rounded to bf16 once.
 //
 // The angle.  Only its fraction of a turn counts, so it is kept as a fixed-point number: with
-// F = frac(inv_freq / 2 pi) * 2^64 (one product in 64-bit floats), position * F modulo 2^64 is that
-// fraction without another rounding, at any position: the error is position * inv_freq * 2^-52 rad
-// at most, as a product of 64-bit floats has, and 2^-24 of it for what follows in fp32.
+// F = frac(|inv_freq| / 2 pi) * 2^64 (one product in 64-bit floats; negated where inv_freq is negative),
+// position * F modulo 2^64 is that fraction without another rounding, at any position: the error is
+// position * inv_freq * 2^-52 rad at most, as a product of 64-bit floats has, and 2^-23 rad for what
+// follows in fp32 (of a half turn, 24 bits).
 //
 // A row is d / 8 lanes, each with two pieces of four columns: half-split, a piece of the first half and
 // the one it turns with; so no value changes lanes, and a norm's sum is all that crosses them.  Rows
@@ -74,10 +75,12 @@ __device__ __forceinline__ bool rotate_position(const RotateParams& p, int tok, 
   return true;
 }
 
-// Column i's turn a position, as a fraction of 2^64.
+// Column i's turn a position, as a fraction of 2^64.  A negative one is the other's modulo 2^64: the
+// fraction of a small negative number itself, 1 less that number, would have 53 bits of 1.
 __device__ __forceinline__ unsigned long long rotate_step(float freq) {
-  const double turns = static_cast<double>(freq) * 0.15915494309189533577;  // 1 / 2 pi
-  return __double2ull_rn((turns - floor(turns)) * 18446744073709551616.0);
+  const double turns = static_cast<double>(fabsf(freq)) * 0.15915494309189533577;  // 1 / 2 pi
+  const unsigned long long step = __double2ull_rn((turns - floor(turns)) * 18446744073709551616.0);
+  return freq < 0.f ? 0ull - step : step;
 }
 
 struct RotRow {
