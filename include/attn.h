@@ -155,7 +155,8 @@ attn_status attn_fwd_strided(const void* Q, const void* K, const void* V, void* 
  *         total_k (values are clamped to [0, total] on the device, so a bad array cannot
  *         make the kernel write outside O and LSE).
  *   max_seqlen_q  >= the longest query sequence (the grid covers that many rows; longer
- *         sequences are left partly unwritten).
+ *         sequences are left partly unwritten).  It, total_q and total_k are at most 2^31 - 256, and
+ *         B * H * ceil(max_seqlen_q / 128) at most 2^31 - 2^13 - 1.
  *   LSE   device fp32 [H, total_q].
  *   Masks per sequence: query i of sequence b (Nq_b rows, Nk_b keys) sees key j iff
  *   j < Nk_b and, when causal, j <= i + (Nk_b - Nq_b).  A sequence with no keys gets O = 0
@@ -453,7 +454,7 @@ attn_status attn_qk_rotate(const void* Q, const void* K, void* Q_out, void* K_ou
  *   Q, O [total_q, Hq, d], K, V [total_k, Hkv, d]: device bf16 with strides (token, head) as in
  *         attn_qk_rotate, positive here.  Hq is a multiple of Hkv: query head h reads K/V head
  *         h / (Hq / Hkv).  LSE fp32 [Hq, total_q].
- *   cu_seqlens_q, cu_seqlens_k, max_seqlen_q: as attn_fwd_varlen (rows outside every sequence are
+ *   cu_seqlens_q, cu_seqlens_k, max_seqlen_q, and the most rows and tiles: as attn_fwd_varlen (rows outside every sequence are
  *         left as they were, rows past max_seqlen_q may be; a sequence's keys are rows
  *         cu_seqlens_k[b] .. cu_seqlens_k[b + 1] - 1).  causal: bottom-right aligned, so a sequence
  *         with more keys than queries is a prompt over its prefix.

@@ -201,6 +201,12 @@ int fault_block() {
   return -1;
 }
 
+// Items of a launch, at most: the index a CTA looks at after its last item (item_of) lies up to two rounds
+// of CTAs further and has to stay in 32 bits.
+constexpr long long kMostItems = INT32_MAX - 2 * 4096;
+// Tiles of 128 rows.
+long long row_tiles(int rows) { return (static_cast<long long>(rows) + attn::kBM - 1) / attn::kBM; }
+
 bool misaligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
 
 attn_status check_args(const void* Q, const void* K, const void* V, void* O, float* LSE, int B, int H, int Nq,
@@ -209,8 +215,8 @@ attn_status check_args(const void* Q, const void* K, const void* V, void* O, flo
     return fail(ATTN_ERR_BAD_SHAPE, "negative size (B=%d H=%d Nq=%d Nk=%d)", B, H, Nq, Nk);
   if (d != 64 && d != 128) return fail(ATTN_ERR_UNSUPPORTED_D, "d=%d; supported: 64, 128", d);
   const long long BH = static_cast<long long>(B) * H;
-  const long long tiles = BH * ((Nq + attn::kBM - 1) / attn::kBM);
-  if (BH > INT32_MAX || tiles > INT32_MAX || static_cast<long long>(Nq) * BH > INT32_MAX * 64ll)
+  const long long tiles = BH * row_tiles(Nq);
+  if (BH > INT32_MAX || tiles > kMostItems || static_cast<long long>(Nq) * BH > INT32_MAX * 64ll)
     return fail(ATTN_ERR_BAD_SHAPE, "problem too large (B*H=%lld)", BH);
   if (!std::isfinite(scale) || !(scale > 0.f)) return fail(ATTN_ERR_BAD_ARG, "scale must be finite and > 0");
   if (BH == 0 || Nq == 0) return ATTN_OK;
@@ -290,7 +296,7 @@ attn_status make_launch(const void* Q, const void* K, const void* V, void* O, fl
   p.H = H;
   p.Nq = Nq;
   p.Nk = Nk;
-  p.num_qtiles = (geo.grid_q + attn::kBM - 1) / attn::kBM;
+  p.num_qtiles = static_cast<int>(row_tiles(geo.grid_q));
   p.causal = causal ? 1 : 0;
   p.rank_major = 0;
   p.order_div = p.num_qtiles;
@@ -441,7 +447,7 @@ attn_status launch_pair(const void* Q, const void* K, const void* V, void* O, fl
 // unequal causal tiles over more SMs); without one, as soon as the pairs fill more than
 // half the SMs (a single-tile grid would then need two rounds of equal tiles).
 bool use_pair_kernel(int dev, int B, int H, const Geometry& geo, int causal) {
-  const long long pairs = static_cast<long long>(B) * H * (((geo.grid_q + attn::kBM - 1) / attn::kBM + 1) / 2);
+  const long long pairs = static_cast<long long>(B) * H * ((row_tiles(geo.grid_q) + 1) / 2);
   return causal ? pairs >= sm_count(dev) : 2 * pairs > sm_count(dev);
 }
 
@@ -601,8 +607,11 @@ attn_status attn_fwd_varlen(const void* Q, const void* K, const void* V, void* O
                 max_seqlen_q, total_q, total_k);
   if (d != 64 && d != 128) return fail(ATTN_ERR_UNSUPPORTED_D, "d=%d; supported: 64, 128", d);
   if (!std::isfinite(scale) || !(scale > 0.f)) return fail(ATTN_ERR_BAD_ARG, "scale must be finite and > 0");
-  const long long tiles = static_cast<long long>(B) * H * ((max_seqlen_q + attn::kBM - 1) / attn::kBM);
-  if (tiles > INT32_MAX || static_cast<long long>(total_q) * H * d > (1ll << 40))
+  // rows are counted in 32 bits, rounded up to a block of 128
+  if (max_seqlen_q > INT32_MAX - 255 || total_q > INT32_MAX - 255 || total_k > INT32_MAX - 255)
+    return fail(ATTN_ERR_BAD_SHAPE, "max_seqlen_q, total_q and total_k are at most 2^31 - 256");
+  const long long BH = static_cast<long long>(B) * H;
+  if (BH > INT32_MAX || BH * row_tiles(max_seqlen_q) > kMostItems || static_cast<long long>(total_q) * H > (1ll << 40) / d)
     return fail(ATTN_ERR_BAD_SHAPE, "problem too large");
   if (static_cast<long long>(B) * H == 0 || max_seqlen_q == 0 || total_q == 0) return ATTN_OK;
   if (!Q || !O || !LSE || !cu_seqlens_q || !cu_seqlens_k)
@@ -908,8 +917,8 @@ attn_status attn_fwd_states(const void* Q, const void* K, const void* V, float* 
   if (static_cast<long long>(B) * H == 0 || Nq == 0) return ATTN_OK;
   if (!l_states) return fail(ATTN_ERR_NULLPTR, "l_states must not be NULL");
   if (misaligned(l_states)) return fail(ATTN_ERR_MISALIGNED, "pointers must be 16-byte aligned");
-  const long long units = static_cast<long long>(B) * H * ((Nq + attn::kBM - 1) / attn::kBM);
-  if (units * num_splits > INT32_MAX) return fail(ATTN_ERR_BAD_SHAPE, "too many (tile, split) units");
+  const long long units = static_cast<long long>(B) * H * row_tiles(Nq);
+  if (units * num_splits > kMostItems) return fail(ATTN_ERR_BAD_SHAPE, "too many (tile, split) units");
   int dev;
   if ((st = get_device(&dev)) != ATTN_OK) return st;
   uint32_t* status = nullptr;
@@ -960,7 +969,7 @@ int attn_splitkv_splits(int B, int H, int Nq, int Nk) {
   if (get_device(&dev) != ATTN_OK) return 1;
   uint32_t* status = nullptr;
   if (setup(dev, &status) != ATTN_OK) return 1;
-  const long long units = static_cast<long long>(B) * H * ((Nq + attn::kBM - 1) / attn::kBM);
+  const long long units = static_cast<long long>(B) * H * row_tiles(Nq);
   return auto_splits(units, (Nk + attn::kBN - 1) / attn::kBN, g_sms[dev]);
 }
 

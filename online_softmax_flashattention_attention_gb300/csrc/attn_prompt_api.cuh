@@ -333,8 +333,9 @@ attn_status attn_fwd_prompt(const void* Q, const void* K, const void* V, void* O
     return fail(ATTN_ERR_BAD_SHAPE, "max_seqlen_q, total_q and total_k are at most 2^31 - 256");
   if (!std::isfinite(scale) || !(scale > 0.f)) return fail(ATTN_ERR_BAD_ARG, "scale must be finite and > 0");
   if (static_cast<long long>(B) * Hq == 0 || max_seqlen_q == 0 || total_q == 0) return ATTN_OK;
-  const long long tiles = static_cast<long long>(B) * Hq * ((max_seqlen_q + attn::kBM - 1) / attn::kBM);
-  if (tiles > INT32_MAX) return fail(ATTN_ERR_BAD_SHAPE, "problem too large (%lld tiles of 128 rows)", tiles);
+  const long long seq_heads = static_cast<long long>(B) * Hq, tiles = row_tiles(max_seqlen_q);
+  if (seq_heads > kMostItems || seq_heads * tiles > kMostItems)
+    return fail(ATTN_ERR_BAD_SHAPE, "problem too large (%lld tiles of 128 rows for each of %lld sequences' heads)", tiles, seq_heads);
   if (!Q || !O || !LSE || !cu_seqlens_q || !cu_seqlens_k)
     return fail(ATTN_ERR_NULLPTR, "Q, O, LSE and the cu_seqlens arrays must not be NULL");
   if (total_k > 0 && (!K || !V)) return fail(ATTN_ERR_NULLPTR, "K and V must not be NULL when total_k > 0");
