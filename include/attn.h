@@ -509,7 +509,7 @@ attn_status attn_cache_weigh(const void* Q, const float* LSE, const attn_cache* 
  *         of the call reads and no place names twice; or, out_table NULL, of the sequence's own
  *         pages, which then must be no other sequence's of the call.
  *   kept  device int32 [B, num_heads, keep]: the positions kept, increasing; -1 past the sequence's
- *         tokens.  out_lens device int32 [B]: min(lens, keep); not lens itself.
+ *         tokens.  out_lens device int32 [B]: min(lens, keep); no part of lens.
  *   keep and max_pages * page_size are at most 2^31 - 2^17.
  *   Positions without a page count as weight -inf and are packed as zeros of weight 0, places without
  *         one are not written; both are reported by attn_cache_check.

@@ -852,8 +852,8 @@ def attn_cache_evict(k_cache, v_cache, weights, block_table, lens, keep, *, sink
     largest weights between (the first of equal ones).  K, V, scales and weights of what is kept move to
     positions 0, 1, ... of the pages of out_table (int32 [B, out_max_pages], pages that no sequence of the
     call reads) or, without one, of the sequence's own.  Returns kept int32 [B, Hkv, keep] (the positions,
-    increasing; -1 past the sequence's tokens) and out_lens int32 [B] = min(lens, keep), allocated when not
-    given.  Positions without a page are reported by cache_check().  The cache's arguments: as
+    increasing; -1 past the sequence's tokens) and out_lens int32 [B] = min(lens, keep; no part of lens),
+    allocated when not given.  Positions without a page are reported by cache_check().  The cache's arguments: as
     attn_cache_write.
     """
     import torch

@@ -466,7 +466,10 @@ attn_status attn_cache_evict(const attn_cache* cache, float* weights, const int3
   }
   if (B == 0) return ATTN_OK;
   if (!lens || !out_lens || (keep > 0 && !kept)) return fail(ATTN_ERR_NULLPTR, "lens, kept and out_lens must not be NULL");
-  if (lens == out_lens) return fail(ATTN_ERR_BAD_ARG, "out_lens must not be lens");
+  // (every CTA reads its sequence's length, at a time of its own)
+  const uintptr_t in0 = reinterpret_cast<uintptr_t>(lens), out0 = reinterpret_cast<uintptr_t>(out_lens);
+  if ((in0 > out0 ? in0 - out0 : out0 - in0) < static_cast<uintptr_t>(B) * sizeof(int32_t))
+    return fail(ATTN_ERR_BAD_ARG, "out_lens must not overlap lens");
   if (max_pages > 0 && !block_table) return fail(ATTN_ERR_NULLPTR, "block_table must not be NULL");
   if (cache->num_pages > 0 && !weights) return fail(ATTN_ERR_NULLPTR, "weights must not be NULL");
   if (odd_to(weights, 4) || odd_to(block_table, 4) || odd_to(out_table, 4) || odd_to(lens, 4) || odd_to(kept, 4) ||
