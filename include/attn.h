@@ -369,9 +369,9 @@ attn_status attn_cache_write(const attn_cache* cache, const void* K, const void*
 
 /*
  * attn_cache_read -- cached positions back as packed bf16 K and V [total, num_heads, d], e.g.
- *   for a prompt over a cached prefix through attn_fwd_varlen.  That call has one head count:
- *   where a group of query heads shares a K/V head, repeat the rows read here for each of them
- *   first (passing them as they are with Q's H would read past their end).
+ *   for a prompt over a cached prefix through attn_fwd_prompt, which takes them as they are.
+ *   (attn_fwd_varlen has one head count: for it, where a group of query heads shares a K/V head, repeat
+ *   the rows read here for each of them; passing them as they are with Q's H would read past their end.)
  *   Row cu_seqlens[b] + i is position start_lens[b] + i of sequence b.  Exact: every e4m3 value times its scale that
  *   attn_cache_write makes is a bf16.  Rows outside every sequence are left as they were.
  *   K, V 16-byte aligned.  Asynchronous.
@@ -454,10 +454,10 @@ attn_status attn_qk_rotate(const void* Q, const void* K, void* Q_out, void* K_ou
  *   Q, O [total_q, Hq, d], K, V [total_k, Hkv, d]: device bf16 with strides (token, head) as in
  *         attn_qk_rotate, positive here.  Hq is a multiple of Hkv: query head h reads K/V head
  *         h / (Hq / Hkv).  LSE fp32 [Hq, total_q].
- *   cu_seqlens_q, cu_seqlens_k, max_seqlen_q, and the most rows and tiles: as attn_fwd_varlen (rows outside every sequence are
- *         left as they were, rows past max_seqlen_q may be; a sequence's keys are rows
- *         cu_seqlens_k[b] .. cu_seqlens_k[b + 1] - 1).  causal: bottom-right aligned, so a sequence
- *         with more keys than queries is a prompt over its prefix.
+ *   cu_seqlens_q, cu_seqlens_k, max_seqlen_q, and the most rows and tiles: as attn_fwd_varlen (rows
+ *         outside every sequence are left as they were, rows past max_seqlen_q may be; a sequence's keys
+ *         are rows cu_seqlens_k[b] .. cu_seqlens_k[b + 1] - 1).  causal: bottom-right aligned, so a
+ *         sequence with more keys than queries is a prompt over its prefix.
  *   What K and V hold where a row does not look, infinities and NaN among it, does not reach the row.
  *   workspace  device, attn_prompt_workspace_bytes(...) bytes, 16-byte aligned, this call's own until
  *         it is done: few query tiles over many keys are then split along the keys.  NULL: they are not.

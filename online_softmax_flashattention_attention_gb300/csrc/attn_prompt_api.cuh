@@ -132,7 +132,9 @@ attn_status launch_prompt(const void* Q, const void* K, const void* V, void* O, 
 // 2048, 32 heads, d = 128 18.1 and 19.8 us, over 4096 22.1 and 32.7, over 16384 43.9 and 106.3; 512 over
 // 4096, 16 heads, d = 64 27.0 and 32.5; 7 prompts of 69 to 517 over prefixes up to 5000 20.3 and 44.6.
 // The other way round (two launches, the plan): 128 over 512, 32 heads, d = 128 14.2 and 9.9; 512 over
-// 4096 41.3 and 36.1; and, where sequences are as long as each other, 8 of 100 over 3000 61.8 and 57.0.
+// 4096 41.3 and 36.1.  Sequences as long as each other lose what an uneven batch would win, as the host knows
+// the sum of their keys alone: 8 of 100 over 3000, 32 / 8 heads, 62.5 and 56.5; 4 of them 33.7 and 28.8; 8
+// over 6000 102 and 95; 4 of 100 over 2000, 16 / 4 heads, 26.0 and 21.6.
 bool prompt_splits(int B, int Hq, int max_q, int total_q, int total_k, int sms) {
   if (B > attn::kLevelSeqs) return false;
   const long long tiles = std::min(static_cast<long long>(total_q) / attn::kBM + B,
@@ -501,7 +503,9 @@ attn_status attn_cache_evict(const attn_cache* cache, float* weights, const int3
   p.row_bytes = cache->d * (cache->type == ATTN_CACHE_E4M3 ? 1 : 2);
   p.in_place = in_place ? 1 : 0;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  // A unit's weights are shared by as many CTAs as hold 8192 of them each, 8 at most, while SMs are idle.
+  // A unit's weights are shared by as many CTAs as hold 8192 of them each, 8 at most, while SMs are idle.  How
+  // many keys a CTA has room for goes by the table, as the lengths are the device's: 48 sequences of up to 16384
+  // tokens with tables of as many positions (64 KB a CTA, two an SM) 151 us, of 131072 (192 KB, one) 193.
   const long long units = static_cast<long long>(B) * p.Hkv;
   unsigned cluster = 1;
   while (cluster < 8 && room > 8192ll * cluster && units * cluster < sm_count(dev)) cluster *= 2;

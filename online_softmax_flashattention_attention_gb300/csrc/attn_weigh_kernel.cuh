@@ -36,10 +36,24 @@
 // as they are and the queries are split into two e4m3 terms, as attn_tree_tile_kernel.cuh describes;
 // the query row's power of two and the key's scale multiply the score afterwards.
 //
+// Turns.  A parity tells a turn of a stage from the next one, not from the one after it: who skips a turn
+// of a barrier needs something else to say that it has ended before the next.
+//   LSE: a warp has every other tile.  For tile t it waits until all four groups are done with the tile kLse
+//   before t; the tile before that one at its place is done too, as the warp waited for a later tile's when it
+//   had tile t - 2, and groups go in order.  The query stage of that tile has been given back as well: a group is
+//   done with a tile after its scores have come, and an issuer gives stages back in order, before later scores.
+//   Products: an issuer has every turn of its own stages of K and of its score buffers.  Where it skips q_full
+//   or k_full it waits for w_full, which comes after them; a w_full that it skips (the other block's) comes before
+//   the next one that it waits for, as the converting warps go in order.
+//   Sums: lse_full is not waited for where scores are, which come after it.  part: arrived at in every unit;
+//   who waits for it in a unit of several tiles has seen scores for which the others had to be done with more
+//   tiles than lie behind the slot's last unit.
+//   Conversions: at their waits.
+//
 // Measured, 32 / 8 heads, d = 128.  A prompt of 8192 tokens in bf16 230 us, 0.64 of the measured product
 // rate: a step of 256 keys x 128 columns takes some 2000 cycles, and shared memory feeds its products (18
 // of 128 x 128 x 16, both operands from there) for some 1800 of them.  64 e4m3 contexts of 900 to 16384
-// tokens, a token each, 114 us where the keys alone take 69 at a copy's rate: no unit is busy, but 28 warps
+// tokens, a token each, 108 to 114 us where the keys alone take 69 at a copy's rate: no unit is busy, but 28 warps
 // of eight roles share the instruction caches (one of a scheduler's seven waits for instructions, another
 // issues every second cycle; two waits more in the code of the widening warps, which do not run here, 122),
 // so that each instruction of a role's step counts: a key's place worked out three times a unit instead of
