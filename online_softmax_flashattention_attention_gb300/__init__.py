@@ -238,7 +238,7 @@ def status_sync(stream=None):
 
 
 def release_workspace():
-    """Free the workspaces kept for attn_fwd_host and (by every thread) for attn_fwd_tree."""
+    """Free the workspaces kept for attn_fwd_host and (by every thread) for attn_fwd_tree and attn_fwd_prompt."""
     with _kept_lock:
         for kept in list(_kept_by_threads):
             kept.by_stream.clear()
